@@ -49,7 +49,7 @@
 extern "C" {
 #endif
 
-#define SSMSCAN_VERSION 15
+#define SSMSCAN_VERSION 16
 
 /* Bits of the `flags` argument of the scan entry points. */
 #define SSM_SCAN_SOFTPLUS 1     /* step size = softplus(delta + delta_bias) */
@@ -77,7 +77,8 @@ typedef enum {
     SSM_ERR_UNSUPPORTED_N = -5,   /* dstate is not 1, 2, 4, 8 or 16 */
     SSM_ERR_WORKSPACE = -6,       /* workspace missing or smaller than required */
     SSM_ERR_HIP = -7,             /* the HIP runtime refused a launch */
-    SSM_ERR_FLAGS = -8            /* unknown flag bits, or a flag the entry point does not take */
+    SSM_ERR_FLAGS = -8,           /* unknown flag bits, or a flag the entry point does not take */
+    SSM_ERR_VALUE = -9            /* a scalar argument is out of its range */
 } ssm_status;
 
 /* Problem sizes.
@@ -422,6 +423,114 @@ SSMSCAN_API int ssm_step(float *state, const void *u, const void *delta, const f
 SSMSCAN_API int ssm_step_act(float *state, const void *u, const void *delta, const float *A, const void *B,
              const void *C, const float *D, const void *z, const float *delta_bias, int flags, void *y,
              const ssm_dims *dims, void *stream);
+
+/* The gated linear recurrence: one state per channel, a decay and an input gate per token and
+ * channel, the input scaled so that the state keeps the input's variance.
+ *   log a_t = A[d] * sigmoid(r_t)
+ *   h_t     = a_t h_{t-1} + sqrt(1 - a_t^2) * sigmoid(g_t) * x_t
+ *   y_t     = h_t * silu(z_t)                       (z optional: without it y_t = h_t)
+ *   x, r, g, z, y : [batch][seqlen][dim] (io_dtype); z may be NULL (no gate)
+ *   A             : [dim] fp32, the logarithm of the decay at an open gate: A <= 0 (not checked;
+ *                   A > 0 gives NaN, A = 0 a state that ignores its input)
+ *   initial_state : [batch][dim] fp32, or NULL (= zero).  It may be the last_state buffer (the
+ *                   state advanced in place)
+ *   seq_lens      : [batch] int32 in device memory, or NULL: sequence b has seq_lens[b] tokens
+ *                   (values outside [0, seqlen] are taken as 0 or seqlen).  Inputs past a
+ *                   sequence's length are not read; y is zero there
+ *   y             : output, written completely
+ *   last_state    : [batch][dim] fp32 output, the state after each sequence's last token (the
+ *                   initial state for a length of 0), or NULL
+ *   workspace     : at least ssm_gated_scan_workspace_bytes(dims) bytes, 16-byte aligned (NULL
+ *                   when that is 0); its contents on entry do not matter.  After the call it
+ *                   holds the states that ssm_gated_scan_bwd takes as checkpoints
+ * Arithmetic and states are fp32; 1 - a^2 is formed without cancellation where a is near 1.
+ * dims->dstate and dims->chunk_len are ignored; seqlen is at most 2^30.  Returns SSM_OK or a
+ * negative ssm_status (nothing is launched on an error). */
+SSMSCAN_API int ssm_gated_scan_fwd(const void *x, const void *r, const void *g, const float *A, const void *z,
+                const float *initial_state, const int32_t *seq_lens, void *y, float *last_state,
+                const ssm_dims *dims, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Bytes of device workspace ssm_gated_scan_fwd needs for these sizes (0 for an invalid or empty
+ * problem, and for sequences that are scanned in one piece). */
+SSMSCAN_API size_t ssm_gated_scan_workspace_bytes(const ssm_dims *dims);
+
+/* Gradients of ssm_gated_scan_fwd given dy = dLoss/dy and dlast_state = dLoss/d(last_state).
+ * With dh_t = dy_t silu(z_t) and lambda_t = dh_t + a_{t+1} lambda_{t+1} (dlast_state added after
+ * the last token), s = sigmoid(r), i = sigmoid(g), beta = sqrt(1 - a^2):
+ *   dx = lambda beta i,   dg = lambda beta x i (1 - i),   dz = dy h silu'(z)
+ *   e  = lambda (a h_{t-1} - i x a^2 / beta)     (the second term is 0 where beta = 0)
+ *   dr = e A s (1 - s),   dA = sum over b, t of e s,   dinitial_state = a_0 lambda_0
+ *   x, r, g, A, z, initial_state, seq_lens : exactly those of the forward call
+ *   dy, dx, dr, dg : [batch][seqlen][dim] (io_dtype); the gradients are zero past a sequence's
+ *                    length, whatever dy holds there
+ *   dz             : as dx, required when z is given
+ *   dlast_state    : [batch][dim] fp32, or NULL (= 0)
+ *   checkpoints    : the workspace a forward call with the same inputs and dims left (contents
+ *                    not checked; of checkpoints_bytes bytes, at least
+ *                    ssm_gated_scan_workspace_bytes(dims)), or NULL: the states are then
+ *                    recomputed in a pass of their own
+ *   dA             : [dim] fp32 output;  dinitial_state : [batch][dim] fp32 output, or NULL
+ *   workspace      : at least ssm_gated_scan_bwd_workspace_bytes(dims) bytes, 16-byte aligned
+ * The sums behind dA have a fixed order: the results are the same from run to run.  Outputs must
+ * not overlap inputs or each other.  Returns SSM_OK or a negative ssm_status. */
+SSMSCAN_API int ssm_gated_scan_bwd(const void *x, const void *r, const void *g, const float *A, const void *z,
+                const float *initial_state, const int32_t *seq_lens, const void *dy, const float *dlast_state,
+                const void *checkpoints, size_t checkpoints_bytes, void *dx, void *dr, void *dg, float *dA,
+                void *dz, float *dinitial_state, const ssm_dims *dims, void *workspace, size_t workspace_bytes,
+                void *stream);
+
+/* Bytes of device workspace ssm_gated_scan_bwd needs (0 for an invalid or empty problem). */
+SSMSCAN_API size_t ssm_gated_scan_bwd_workspace_bytes(const ssm_dims *dims);
+
+/* One token of the gated linear recurrence for `batch` independent sequences.
+ *   state      : [batch][dim] fp32, read and overwritten with the new state
+ *   x, r, g, y : [batch][dim] (io_dtype); z likewise, or NULL
+ *   A          : [dim] fp32
+ * The state and y are formed with the scan's arithmetic.  dims->seqlen, dstate and chunk_len are
+ * ignored.  Returns SSM_OK or a negative ssm_status. */
+SSMSCAN_API int ssm_gated_step(float *state, const void *x, const void *r, const void *g, const float *A,
+                const void *z, void *y, const ssm_dims *dims, void *stream);
+
+/* Bits of the `flags` argument of the layer norm's entry points. */
+#define SSM_NORM_SUM_F32 1      /* residual, sum and their gradients are fp32 whatever the io_dtype */
+
+/* Layer norm over the last axis, with the residual sum in front of it: batch * seqlen rows of
+ * dim values,
+ *   s = x + residual,   y = (s - mean(s)) * rstd * weight + bias,
+ *   rstd = 1 / sqrt(mean((s - mean(s))^2) + eps)
+ * s is rounded to the type it is kept in before it is normalised, so that the call equals a sum
+ * followed by a norm; means and variances are fp32, the variance from the centred values.
+ *   x, y          : rows (io_dtype);   weight : [dim] fp32;   bias : [dim] fp32, or NULL (= 0)
+ *   residual      : rows, or NULL (s = x);   sum : rows, receives s, or NULL (not wanted); both of
+ *                   io_dtype, or fp32 with SSM_NORM_SUM_F32.  sum may be the residual buffer (the
+ *                   residual stream advanced in place)
+ *   mean, rstd    : [batch * seqlen] fp32 outputs for the backward pass, each may be NULL
+ *   eps           : >= 0 and finite (SSM_ERR_VALUE otherwise)
+ * dims->dstate and dims->chunk_len are ignored.  Returns SSM_OK or a negative ssm_status. */
+SSMSCAN_API int ssm_layernorm_fwd(const void *x, const void *residual, const float *weight, const float *bias,
+                float eps, int flags, void *y, void *sum, float *mean, float *rstd, const ssm_dims *dims,
+                void *stream);
+
+/* Gradients of ssm_layernorm_fwd given dy = dLoss/dy.  With n = (s - mean) * rstd:
+ *   ds      = rstd * (dy w - mean_row(dy w) - n mean_row(dy w n)) + dresidual
+ *   dweight = sum over rows of dy n,   dbias = sum over rows of dy
+ *   s             : the normalised rows (the forward's sum, or its x without a residual), of
+ *                   io_dtype, or fp32 with SSM_NORM_SUM_F32;   mean, rstd : the forward's
+ *   dresidual     : the gradient that reaches s past the norm (the residual stream's), of s's
+ *                   type, or NULL (= 0)
+ *   ds            : output of s's type: the gradient of the residual and of x (s = x + residual)
+ *   dx            : output of io_dtype, ds once more in x's type, or NULL (not wanted)
+ *   dweight, dbias: [dim] fp32 outputs, each may be NULL (not wanted)
+ *   workspace     : at least ssm_layernorm_bwd_workspace_bytes(dims) bytes, 16-byte aligned; may be
+ *                   NULL when neither dweight nor dbias is wanted
+ * ds may be the dresidual buffer.  The sums over rows have a fixed order: the results are the same
+ * from run to run.  Returns SSM_OK or a negative ssm_status. */
+SSMSCAN_API int ssm_layernorm_bwd(const void *dy, const void *s, const float *weight, const float *mean,
+                const float *rstd, const void *dresidual, int flags, void *ds, void *dx, float *dweight,
+                float *dbias, const ssm_dims *dims, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Bytes of device workspace ssm_layernorm_bwd needs (0 for an invalid or empty problem). */
+SSMSCAN_API size_t ssm_layernorm_bwd_workspace_bytes(const ssm_dims *dims);
 
 /* Message describing the last non-OK status returned on this thread ("" if none). */
 SSMSCAN_API const char *ssm_last_error(void);

@@ -8,10 +8,11 @@ machines without a GPU.
 """
 import importlib
 
-__all__ = ["scan_fwd", "step", "workspace_bytes"]
+__all__ = ["scan_fwd", "step", "workspace_bytes", "gated_scan_fwd", "gated_scan_bwd", "gated_step", "layernorm_fwd",
+           "layernorm_bwd"]
 
 
 def __getattr__(name):
-    if name in ("scan_fwd", "step", "workspace_bytes"):
+    if name in __all__:
         return getattr(importlib.import_module(__name__ + ".ssmscan"), name)
     raise AttributeError(name)

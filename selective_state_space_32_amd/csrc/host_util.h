@@ -1,0 +1,20 @@
+// What the entry points of every translation unit share on the host: the calling thread's
+// status and message, and alignment helpers.
+#pragma once
+
+#include <cstddef>
+#include <cstdint>
+
+#include "ssmscan.h"
+
+namespace ssmlib {
+
+// The status and message of the calling thread's last failure (ssm_last_error); defined in
+// ssmscan.hip.
+int fail(int code, const char *fmt, ...);
+int ok();
+
+inline size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
+inline bool aligned(const void *p, size_t a) { return ((uintptr_t)p % a) == 0; }
+
+}  // namespace ssmlib

@@ -21,7 +21,7 @@ SSM_IO_F32 = 0
 SSM_IO_BF16 = 1
 
 STATUS = {0: "SSM_OK", -1: "SSM_ERR_NULL", -2: "SSM_ERR_SHAPE", -3: "SSM_ERR_DTYPE", -4: "SSM_ERR_ALIGN",
-          -5: "SSM_ERR_UNSUPPORTED_N", -6: "SSM_ERR_WORKSPACE", -7: "SSM_ERR_HIP", -8: "SSM_ERR_FLAGS"}
+          -5: "SSM_ERR_UNSUPPORTED_N", -6: "SSM_ERR_WORKSPACE", -7: "SSM_ERR_HIP", -8: "SSM_ERR_FLAGS", -9: "SSM_ERR_VALUE"}
 
 
 class ssm_dims(ctypes.Structure):
@@ -91,6 +91,22 @@ def _load() -> ctypes.CDLL:
     lib.ssm_ssd_fwd.restype = ctypes.c_int
     lib.ssm_ssd_fwd_from.argtypes = [P] * 9 + [ctypes.c_int, P, P, ctypes.POINTER(ssm_ssd_dims), P]
     lib.ssm_ssd_fwd_from.restype = ctypes.c_int
+    lib.ssm_gated_scan_workspace_bytes.argtypes = [D]
+    lib.ssm_gated_scan_workspace_bytes.restype = ctypes.c_size_t
+    lib.ssm_gated_scan_bwd_workspace_bytes.argtypes = [D]
+    lib.ssm_gated_scan_bwd_workspace_bytes.restype = ctypes.c_size_t
+    lib.ssm_gated_scan_fwd.argtypes = [P] * 9 + [D, P, ctypes.c_size_t, P]
+    lib.ssm_gated_scan_fwd.restype = ctypes.c_int
+    lib.ssm_gated_scan_bwd.argtypes = [P] * 10 + [ctypes.c_size_t] + [P] * 6 + [D, P, ctypes.c_size_t, P]
+    lib.ssm_gated_scan_bwd.restype = ctypes.c_int
+    lib.ssm_gated_step.argtypes = [P] * 7 + [D, P]
+    lib.ssm_gated_step.restype = ctypes.c_int
+    lib.ssm_layernorm_fwd.argtypes = [P] * 4 + [ctypes.c_float, ctypes.c_int] + [P] * 4 + [D, P]
+    lib.ssm_layernorm_fwd.restype = ctypes.c_int
+    lib.ssm_layernorm_bwd_workspace_bytes.argtypes = [D]
+    lib.ssm_layernorm_bwd_workspace_bytes.restype = ctypes.c_size_t
+    lib.ssm_layernorm_bwd.argtypes = [P] * 6 + [ctypes.c_int] + [P] * 4 + [D, P, ctypes.c_size_t, P]
+    lib.ssm_layernorm_bwd.restype = ctypes.c_int
     return lib
 
 
@@ -699,3 +715,228 @@ def ssd_fwd(x: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B: torch.Tensor,
                                 _ptr(z), _ptr(dt_bias), 1 if softplus else 0, _ptr(y), _ptr(last_state),
                                 ctypes.byref(dims), _stream_handle(stream)))
     return y, last_state
+
+
+def _need_lens(seq_lens, bsz, dev):
+    if seq_lens.dtype != torch.int32 or seq_lens.dim() != 1 or seq_lens.shape[0] != bsz:
+        raise ValueError("seq_lens must be an int32 tensor of shape (batch,)")
+    if seq_lens.device != dev:
+        raise ValueError("seq_lens must be on the device of x")
+    if not seq_lens.is_contiguous():
+        raise ValueError("seq_lens: must be contiguous")
+
+
+def _gated_inputs(x, r, g, A, z, initial_state, seq_lens):
+    """Checks of the inputs that the gated recurrence's scan and its backward share; their sizes."""
+    if x.dim() != 3:
+        raise ValueError("x must be (batch, L, dim)")
+    bsz, L, dim = x.shape
+    dev, io = x.device, x.dtype
+    _io_code(io)
+    _need(x, "x", (bsz, L, dim), io, dev)
+    _need(r, "r", (bsz, L, dim), io, dev)
+    _need(g, "g", (bsz, L, dim), io, dev)
+    _need(A, "A", (dim,), torch.float32, dev)
+    if z is not None:
+        _need(z, "z", (bsz, L, dim), io, dev)
+    if initial_state is not None:
+        _need(initial_state, "initial_state", (bsz, dim), torch.float32, dev)
+    if seq_lens is not None:
+        _need_lens(seq_lens, bsz, dev)
+    return bsz, L, dim, dev, io
+
+
+def gated_scan_fwd(x: torch.Tensor, r: torch.Tensor, g: torch.Tensor, A: torch.Tensor,
+                   z: Optional[torch.Tensor] = None, *, initial_state: Optional[torch.Tensor] = None,
+                   seq_lens: Optional[torch.Tensor] = None, y: Optional[torch.Tensor] = None,
+                   last_state: Optional[torch.Tensor] = None, return_last_state: bool = True,
+                   workspace: Optional[torch.Tensor] = None, stream=None, save_checkpoints: bool = False):
+    """The gated linear recurrence over whole sequences (ssm_gated_scan_fwd):
+    h_t = a_t h_{t-1} + sqrt(1 - a_t^2) sigmoid(g_t) x_t with a_t = exp(A sigmoid(r_t)), and
+    y_t = h_t silu(z_t) (h_t without z).
+
+    x, r, g, z: (batch, L, dim) of one dtype (float32 or bfloat16); A: (dim,) float32, A <= 0;
+    initial_state: (batch, dim) float32 (may be last_state: advanced in place); seq_lens: (batch,)
+    int32 on the device, sequence b then has seq_lens[b] tokens and y is zero past them.
+    Returns (y, last_state) -- last_state (batch, dim) float32, or None if not asked for -- and
+    with save_checkpoints (a training forward) also the workspace, for gated_scan_bwd's
+    `checkpoints`."""
+    bsz, L, dim, dev, io = _gated_inputs(x, r, g, A, z, initial_state, seq_lens)
+    if y is None:
+        y = torch.empty_like(x)
+    else:
+        _need(y, "y", (bsz, L, dim), io, dev)
+    if last_state is not None:
+        _need(last_state, "last_state", (bsz, dim), torch.float32, dev)
+    elif return_last_state:
+        last_state = torch.empty((bsz, dim), dtype=torch.float32, device=dev)
+    dims = make_dims(bsz, L, dim, 1, io)
+    if workspace is None:
+        need = int(lib.ssm_gated_scan_workspace_bytes(ctypes.byref(dims)))
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    _check(lib.ssm_gated_scan_fwd(_ptr(x), _ptr(r), _ptr(g), _ptr(A), _ptr(z), _ptr(initial_state), _ptr(seq_lens),
+                                  _ptr(y), _ptr(last_state), ctypes.byref(dims), _ptr(workspace),
+                                  workspace.numel() * workspace.element_size(), _stream_handle(stream)))
+    return (y, last_state, workspace) if save_checkpoints else (y, last_state)
+
+
+def gated_scan_bwd(dy: torch.Tensor, x: torch.Tensor, r: torch.Tensor, g: torch.Tensor, A: torch.Tensor,
+                   z: Optional[torch.Tensor] = None, *, initial_state: Optional[torch.Tensor] = None,
+                   seq_lens: Optional[torch.Tensor] = None, dlast_state: Optional[torch.Tensor] = None,
+                   want_initial_state_grad: bool = False, checkpoints: Optional[torch.Tensor] = None,
+                   workspace: Optional[torch.Tensor] = None, stream=None) -> dict:
+    """Gradients of gated_scan_fwd (ssm_gated_scan_bwd) given dy (batch, L, dim) and optionally
+    dlast_state (batch, dim).  The forward inputs are passed as they were; `checkpoints`: the
+    workspace a gated_scan_fwd(..., save_checkpoints=True) call on them returned (without it the
+    states are recomputed).  Returns a dict: dx, dr, dg, dz (if z) of x's dtype, dA (dim,) float32,
+    dinitial_state (batch, dim) float32 (if asked for)."""
+    bsz, L, dim, dev, io = _gated_inputs(x, r, g, A, z, initial_state, seq_lens)
+    _need(dy, "dy", (bsz, L, dim), io, dev)
+    if dlast_state is not None:
+        _need(dlast_state, "dlast_state", (bsz, dim), torch.float32, dev)
+    if checkpoints is not None and (checkpoints.device != dev or not checkpoints.is_contiguous()):
+        raise ValueError("checkpoints: must be contiguous and on the device of x")
+    grads = dict(dx=torch.empty_like(x), dr=torch.empty_like(x), dg=torch.empty_like(x),
+                 dA=torch.empty((dim,), dtype=torch.float32, device=dev))
+    if z is not None:
+        grads["dz"] = torch.empty_like(x)
+    if want_initial_state_grad:
+        grads["dinitial_state"] = torch.empty((bsz, dim), dtype=torch.float32, device=dev)
+    dims = make_dims(bsz, L, dim, 1, io)
+    if workspace is None:
+        need = int(lib.ssm_gated_scan_bwd_workspace_bytes(ctypes.byref(dims)))
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    have = 0 if checkpoints is None else checkpoints.numel() * checkpoints.element_size()
+    # (a forward that needed no workspace left none to read: nothing is recomputed then either)
+    _check(lib.ssm_gated_scan_bwd(_ptr(x), _ptr(r), _ptr(g), _ptr(A), _ptr(z), _ptr(initial_state), _ptr(seq_lens),
+                                  _ptr(dy), _ptr(dlast_state), _ptr(checkpoints) if have else None, have,
+                                  _ptr(grads["dx"]), _ptr(grads["dr"]), _ptr(grads["dg"]), _ptr(grads["dA"]),
+                                  _ptr(grads.get("dz")), _ptr(grads.get("dinitial_state")), ctypes.byref(dims),
+                                  _ptr(workspace), workspace.numel() * workspace.element_size(),
+                                  _stream_handle(stream)))
+    return grads
+
+
+def gated_step(state: torch.Tensor, x: torch.Tensor, r: torch.Tensor, g: torch.Tensor, A: torch.Tensor,
+               z: Optional[torch.Tensor] = None, *, y: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """One token of the gated linear recurrence (ssm_gated_step); `state` (S, dim) float32 is
+    updated in place.  x, r, g, z: (S, dim) of one dtype; A: (dim,) float32.  Returns y (S, dim)."""
+    if x.dim() != 2:
+        raise ValueError("x must be (sequences, dim)")
+    S, dim = x.shape
+    dev, io = x.device, x.dtype
+    _io_code(io)
+    _need(state, "state", (S, dim), torch.float32, dev)
+    _need(x, "x", (S, dim), io, dev)
+    _need(r, "r", (S, dim), io, dev)
+    _need(g, "g", (S, dim), io, dev)
+    _need(A, "A", (dim,), torch.float32, dev)
+    if z is not None:
+        _need(z, "z", (S, dim), io, dev)
+    if y is None:
+        y = torch.empty_like(x)
+    else:
+        _need(y, "y", (S, dim), io, dev)
+    dims = make_dims(S, 1, dim, 1, io)
+    _check(lib.ssm_gated_step(_ptr(state), _ptr(x), _ptr(r), _ptr(g), _ptr(A), _ptr(z), _ptr(y), ctypes.byref(dims),
+                              _stream_handle(stream)))
+    return y
+
+
+NORM_SUM_F32 = 1   # flag bit of the layer norm's entry points (include/ssmscan.h)
+
+
+def _norm_shape(t, name):
+    if t.dim() < 1:
+        raise ValueError(f"{name} must have at least one axis")
+    dim = t.shape[-1]
+    rows = 1
+    for n in t.shape[:-1]:
+        rows *= n
+    return rows, dim
+
+
+def layernorm_fwd(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor] = None, eps: float = 1e-5, *,
+                  residual: Optional[torch.Tensor] = None, sum_f32: bool = False, y: Optional[torch.Tensor] = None,
+                  total: Optional[torch.Tensor] = None, stream=None):
+    """Layer norm over the last axis with the residual sum in front of it (ssm_layernorm_fwd):
+    total = x + residual, y = (total - mean) rstd weight + bias.
+
+    x: (..., dim) float32 or bfloat16; weight, bias: (dim,) float32; residual: as x, or float32.
+    total has the residual's dtype (it may be the residual tensor itself, updated in place); without a
+    residual it is x, or with sum_f32 x widened to float32 (the start of an fp32 residual stream).
+    Returns (y, total, mean, rstd): y in x's dtype, mean and rstd float32 of x's leading shape."""
+    rows, dim = _norm_shape(x, "x")
+    dev, io = x.device, x.dtype
+    _io_code(io)
+    shape = x.shape
+    _need(x, "x", shape, io, dev)
+    _need(weight, "weight", (dim,), torch.float32, dev)
+    if bias is not None:
+        _need(bias, "bias", (dim,), torch.float32, dev)
+    kept = torch.float32 if sum_f32 else io
+    if residual is not None:
+        kept = residual.dtype
+        if kept != io and kept != torch.float32:
+            raise TypeError(f"residual: dtype {kept} is neither x's nor float32")
+        if sum_f32 and kept != torch.float32:
+            raise TypeError("sum_f32 needs a float32 residual")
+        _need(residual, "residual", shape, kept, dev)
+    if y is None:
+        y = torch.empty_like(x)
+    else:
+        _need(y, "y", shape, io, dev)
+    if total is not None:
+        _need(total, "total", shape, kept, dev)
+    elif residual is not None or kept != io:
+        total = torch.empty(shape, dtype=kept, device=dev)
+    mean = torch.empty(shape[:-1], dtype=torch.float32, device=dev)
+    rstd = torch.empty(shape[:-1], dtype=torch.float32, device=dev)
+    dims = make_dims(1, rows, dim, 1, io)
+    _check(lib.ssm_layernorm_fwd(_ptr(x), _ptr(residual), _ptr(weight), _ptr(bias), float(eps),
+                                 NORM_SUM_F32 if kept != io else 0, _ptr(y), _ptr(total), _ptr(mean), _ptr(rstd),
+                                 ctypes.byref(dims), _stream_handle(stream)))
+    return y, x if total is None else total, mean, rstd
+
+
+def layernorm_bwd(dy: torch.Tensor, total: torch.Tensor, weight: torch.Tensor, mean: torch.Tensor,
+                  rstd: torch.Tensor, *, dresidual: Optional[torch.Tensor] = None, want_param_grads: bool = True,
+                  ds: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None, stream=None) -> dict:
+    """Gradients of layernorm_fwd (ssm_layernorm_bwd) given dy of x's dtype; total, mean, rstd: what
+    the forward returned.  dresidual: the gradient that reaches total past the norm, of its dtype.
+    Returns a dict: ds (total's dtype: the gradient of the residual and of x), dx (the same in dy's
+    dtype) when total is float32 and dy bfloat16, and with want_param_grads dweight, dbias (dim,)
+    float32.  ds may be the dresidual tensor itself (updated in place)."""
+    rows, dim = _norm_shape(dy, "dy")
+    dev, io = dy.device, dy.dtype
+    _io_code(io)
+    shape, kept = dy.shape, total.dtype
+    if kept != io and kept != torch.float32:
+        raise TypeError(f"total: dtype {kept} is neither dy's nor float32")
+    _need(dy, "dy", shape, io, dev)
+    _need(total, "total", shape, kept, dev)
+    _need(weight, "weight", (dim,), torch.float32, dev)
+    _need(mean, "mean", shape[:-1], torch.float32, dev)
+    _need(rstd, "rstd", shape[:-1], torch.float32, dev)
+    if dresidual is not None:
+        _need(dresidual, "dresidual", shape, kept, dev)
+    if ds is None:
+        ds = torch.empty_like(total)
+    else:
+        _need(ds, "ds", shape, kept, dev)
+    grads = dict(ds=ds)
+    if kept != io:
+        grads["dx"] = torch.empty_like(dy)
+    dims = make_dims(1, rows, dim, 1, io)
+    if want_param_grads:
+        grads["dweight"] = torch.empty((dim,), dtype=torch.float32, device=dev)
+        grads["dbias"] = torch.empty((dim,), dtype=torch.float32, device=dev)
+        if workspace is None:
+            need = int(lib.ssm_layernorm_bwd_workspace_bytes(ctypes.byref(dims)))
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    have = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(lib.ssm_layernorm_bwd(_ptr(dy), _ptr(total), _ptr(weight), _ptr(mean), _ptr(rstd), _ptr(dresidual),
+                                 NORM_SUM_F32 if kept != io else 0, _ptr(ds), _ptr(grads.get("dx")),
+                                 _ptr(grads.get("dweight")), _ptr(grads.get("dbias")), ctypes.byref(dims),
+                                 _ptr(workspace) if have else None, have, _stream_handle(stream)))
+    return grads
