@@ -14,7 +14,8 @@ using namespace ssmlib;
 constexpr int64_t kMaxRows = (int64_t(1) << 31) - 1;
 constexpr int64_t kMaxNormDim = int64_t(1) << 30;
 constexpr int64_t kMaxElems = int64_t(1) << 46;
-constexpr int64_t kParts = 256;   // row blocks of the parameters' gradients
+constexpr int64_t kBwdGroups = 512;   // workgroups of the backward, and so partial sums, at most
+constexpr int64_t kWideParts = 256;   // partial sums for rows wider than the registers hold
 
 // batch * seqlen rows of dim values; dstate and chunk_len do not apply.
 int check_norm_dims(const ssm_dims *dm) {
@@ -43,33 +44,76 @@ int launched() {
     return ok();
 }
 
-int64_t part_rows(int64_t rows) { return std::max<int64_t>((rows + kParts - 1) / kParts, 1); }
+// Workgroups of a launch: enough to fill the chip's CUs several times over; a workgroup takes
+// several rows, so that its weights and its sums are worth keeping.
+constexpr int64_t kFwdGroups = 1024;
 
+// Rows that a workgroup holds at a time, by the row's width (0: wider than the registers hold).
+int64_t norm_slots(int64_t D) { return D <= 1024 ? 4 : D <= 8192 ? 1 : 0; }
+
+// Partial sums of the parameters' gradients: one per workgroup of the backward.
+int64_t norm_parts(int64_t rows, int64_t D) {
+    const int64_t slots = norm_slots(D);
+    if (slots == 0) return std::min<int64_t>(rows, kWideParts);
+    return std::min<int64_t>((rows + slots - 1) / slots, kBwdGroups);
+}
+
+// The narrowest shape that holds a row of D values: lanes past the row's end do nothing.
 template <typename IO, typename S>
-void launch_norm(const void *x, const void *res, const float *w, const float *bias, float eps, void *y, void *sum,
+void launch_norm(const void *x_, const void *res_, const float *w, const float *bias, float eps, void *y_, void *sum_,
                  float *mean, float *rstd, int64_t rows, int64_t D, hipStream_t st) {
-    hipLaunchKernelGGL((ssm::layernorm_fwd_kernel<IO, S>), dim3((unsigned)rows), dim3(ssm::kNormThreads), 0, st,
-                       static_cast<const IO *>(x), static_cast<const S *>(res), w, bias, eps, static_cast<IO *>(y),
-                       static_cast<S *>(sum), mean, rstd, D);
+    const IO *x = static_cast<const IO *>(x_);
+    const S *res = static_cast<const S *>(res_);
+    IO *y = static_cast<IO *>(y_);
+    S *sum = static_cast<S *>(sum_);
+    if (norm_slots(D) == 0) {
+        hipLaunchKernelGGL((ssm::layernorm_fwd_wide_kernel<IO, S>), dim3((unsigned)rows), dim3(ssm::kNormWideThreads),
+                           0, st, x, res, w, bias, eps, y, sum, mean, rstd, D);
+        return;
+    }
+    auto kern = D <= 256    ? ssm::layernorm_fwd_kernel<IO, S, 64, 1>
+                : D <= 1024 ? ssm::layernorm_fwd_kernel<IO, S, 64, 4>
+                : D <= 2048 ? ssm::layernorm_fwd_kernel<IO, S, 256, 2>
+                : D <= 5120 ? ssm::layernorm_fwd_kernel<IO, S, 256, 5>
+                            : ssm::layernorm_fwd_kernel<IO, S, 256, 8>;
+    const int64_t slots = norm_slots(D), grid = std::min<int64_t>((rows + slots - 1) / slots, kFwdGroups);
+    hipLaunchKernelGGL(kern, dim3((unsigned)grid), dim3(256), 0, st, x, res, w, bias, eps, y, sum, mean, rstd, rows,
+                       D);
 }
 
 template <typename IO, typename S>
-void launch_norm_bwd(const void *dy, const void *s, const float *w, const float *mean, const float *rstd,
-                     const void *dres, void *ds, void *dx, float *dw, float *db, float *part, int64_t rows, int64_t D,
-                     hipStream_t st) {
-    if (rows > 0)
-        hipLaunchKernelGGL((ssm::layernorm_bwd_kernel<IO, S>), dim3((unsigned)rows), dim3(ssm::kNormThreads), 0, st,
-                           static_cast<const IO *>(dy), static_cast<const S *>(s), w, mean, rstd,
-                           static_cast<const S *>(dres), static_cast<S *>(ds), static_cast<IO *>(dx), D);
-    if (!dw && !db) return;
-    const int64_t per = part_rows(rows), n = (rows + per - 1) / per;
-    const unsigned cols = (unsigned)((D + 255) / 256);
-    if (n > 0)
-        hipLaunchKernelGGL((ssm::layernorm_wgrad_kernel<IO, S>), dim3(cols, (unsigned)n), dim3(256), 0, st,
-                           static_cast<const IO *>(dy), static_cast<const S *>(s), mean, rstd, part, part + n * D,
-                           rows, D, per);
-    hipLaunchKernelGGL(ssm::layernorm_wgrad_sum_kernel, dim3(cols), dim3(256), 0, st, part, part + n * D, dw, db, n,
-                       D);
+void launch_norm_bwd(const void *dy_, const void *s_, const float *w, const float *mean, const float *rstd,
+                     const void *dres_, void *ds_, void *dx_, float *dw, float *db, float *part, int64_t rows,
+                     int64_t D, hipStream_t st) {
+    const IO *dy = static_cast<const IO *>(dy_);
+    const S *s = static_cast<const S *>(s_), *dres = static_cast<const S *>(dres_);
+    S *ds = static_cast<S *>(ds_);
+    IO *dx = static_cast<IO *>(dx_);
+    const int64_t parts = norm_parts(rows, D);
+    const bool sums = dw || db;   // (without rows there are no parts: the sums are zero)
+    float *pw = sums ? part : nullptr, *pb = sums ? part + parts * D : nullptr;
+    if (rows > 0 && norm_slots(D) == 0) {
+        hipLaunchKernelGGL((ssm::layernorm_bwd_wide_kernel<IO, S>), dim3((unsigned)rows), dim3(ssm::kNormWideThreads),
+                           0, st, dy, s, w, mean, rstd, dres, ds, dx, D);
+    } else if (rows > 0) {
+        auto kern = D <= 256    ? ssm::layernorm_bwd_kernel<IO, S, 64, 1>
+                    : D <= 1024 ? ssm::layernorm_bwd_kernel<IO, S, 64, 4>
+                    : D <= 2048 ? ssm::layernorm_bwd_kernel<IO, S, 256, 2>
+                    : D <= 5120 ? ssm::layernorm_bwd_kernel<IO, S, 256, 5>
+                                : ssm::layernorm_bwd_kernel<IO, S, 512, 4>;
+        hipLaunchKernelGGL(kern, dim3((unsigned)parts), dim3(D <= 5120 ? 256 : 512), 0, st, dy, s, w, mean, rstd,
+                           dres, ds, dx, pw, pb, rows, D);
+    }
+    if (!sums) return;
+    if (rows > 0 && norm_slots(D) == 0) {
+        // ds may have replaced dresidual, but dy and s are still there
+        const int64_t per = (rows + parts - 1) / parts;
+        hipLaunchKernelGGL((ssm::layernorm_wgrad_wide_kernel<IO, S>),
+                           dim3((unsigned)((D + 255) / 256), (unsigned)parts), dim3(256), 0, st, dy, s, mean, rstd,
+                           pw, pb, rows, D, per);
+    }
+    hipLaunchKernelGGL(ssm::layernorm_wgrad_sum_kernel, dim3((unsigned)((D + 63) / 64)),
+                       dim3(64 * ssm::kNormSumWaves), 0, st, pw, pb, dw, db, parts, D);
 }
 
 }  // namespace
@@ -101,8 +145,7 @@ int ssm_layernorm_fwd(const void *x, const void *residual, const float *weight, 
 
 size_t ssm_layernorm_bwd_workspace_bytes(const ssm_dims *dims) {
     if (check_norm_dims(dims) != SSM_OK) return 0;
-    const int64_t rows = dims->batch * dims->seqlen, per = part_rows(rows), n = (rows + per - 1) / per;
-    return align256((size_t)(2 * n * dims->dim) * sizeof(float));
+    return align256((size_t)(2 * norm_parts(dims->batch * dims->seqlen, dims->dim) * dims->dim) * sizeof(float));
 }
 
 int ssm_layernorm_bwd(const void *dy, const void *s, const float *weight, const float *mean, const float *rstd,

@@ -2,37 +2,348 @@
 //
 //   s = x + residual (rounded to the type it is kept in),  mu = mean(s),
 //   rstd = 1 / sqrt(mean((s - mu)^2) + eps),  y = (s - mu) rstd w + b
-//   ds = rstd (dy w - mean(dy w) - xh mean(dy w xh)) + dresidual,  xh = (s - mu) rstd
-//   dw = sum over rows of dy xh,  db = sum over rows of dy
+//   ds = rstd (dy w - mean(dy w) - n mean(dy w n)) + dresidual,  n = (s - mu) rstd
+//   dw = sum over rows of dy n,  db = sum over rows of dy
+//
+// Bound: HBM (every row is read once and written once).  A row is held in the registers of TPR
+// threads (a wave for narrow rows, a workgroup for wide ones), NV vectors of kNormVec values each,
+// so that the variance is taken from centred values without a second pass over memory.  A thread
+// keeps its columns over all the rows that its workgroup takes: the weights stay in registers, and
+// so do the sums over rows behind dw and db.  The next row is requested before the current one is
+// reduced.  Rows wider than the registers hold take the kernels at the end, which pass over a row
+// several times (its later passes come from the cache).
 #pragma once
 
 #include "device_math.h"
 
 namespace ssm {
 
-constexpr int kNormThreads = 256;
+constexpr int kNormVec = 4;   // values per access
 
-// Sum over the workgroup, the same value in every thread.
-__device__ __forceinline__ float block_sum(float v, float *red) {
-#pragma unroll
-    for (int k = 32; k >= 1; k >>= 1) v += __shfl_xor(v, k);
-    __syncthreads();
-    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
-    __syncthreads();
-    float s = red[0];
-#pragma unroll
-    for (int k = 1; k < kNormThreads / 64; ++k) s += red[k];
-    return s;
+// Sum over the wave's lanes, in every lane (row shifts, then the two row broadcasts).
+__device__ __forceinline__ float wave_sum(float v) {
+    v += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x111, 0xf, 0xf, false));  // row_shr:1
+    v += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x112, 0xf, 0xf, false));  // row_shr:2
+    v += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x114, 0xf, 0xf, false));  // row_shr:4
+    v += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x118, 0xf, 0xf, false));  // row_shr:8
+    v += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x142, 0xa, 0xf, false));  // row_bcast:15
+    v += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x143, 0xc, 0xf, false));  // row_bcast:31
+    return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
 }
 
-// One workgroup per row, three passes over it.  S: the type of residual and sum.
-template <typename IO, typename S>
-__global__ void __launch_bounds__(kNormThreads)
+// Sums of two values over the TPR threads of a row, in every thread.  red: the row's LDS slots, one
+// pair per wave; the caller alternates between two sets, so that one barrier per sum is enough.
+template <int TPR>
+__device__ __forceinline__ void row_sum2(float &p, float &q, float (*red)[2]) {
+    p = wave_sum(p);
+    q = wave_sum(q);
+    if constexpr (TPR > 64) {
+        const int w = threadIdx.x >> 6;
+        if ((threadIdx.x & 63) == 0) {
+            red[w][0] = p;
+            red[w][1] = q;
+        }
+        __syncthreads();
+        p = red[0][0];
+        q = red[0][1];
+#pragma unroll
+        for (int k = 1; k < TPR / 64; ++k) {
+            p += red[k][0];
+            q += red[k][1];
+        }
+    }
+}
+template <int TPR>
+__device__ __forceinline__ float row_sum(float p, float *red) {
+    p = wave_sum(p);
+    if constexpr (TPR > 64) {
+        if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = p;
+        __syncthreads();
+        p = red[0];
+#pragma unroll
+        for (int k = 1; k < TPR / 64; ++k) p += red[k];
+    }
+    return p;
+}
+
+// kNormVec values of a row from column c on, as raw words; nothing is assumed about alignment
+// beyond the element's own (rows of an odd width start anywhere).  The vector that crosses the
+// row's end is read by elements, columns past it are zero.
+template <typename T> struct norm_vec {
+    static constexpr int W = kNormVec * (int)sizeof(T) / 4;
+    typedef uint32_t any_u32 __attribute__((ext_vector_type(W), aligned(sizeof(T))));
+    uint32_t w[W];
+    __device__ __forceinline__ void load(const T *row, int64_t c, int64_t D) {
+        if (c + kNormVec <= D) {
+            const any_u32 v = __builtin_nontemporal_load(reinterpret_cast<const any_u32 *>(row + c));
+            __builtin_memcpy(w, &v, sizeof w);
+        } else {
+#pragma unroll
+            for (int k = 0; k < W; ++k) w[k] = 0;
+#pragma unroll
+            for (int k = 0; k < kNormVec; ++k)
+                if (c + k < D) {
+                    if constexpr (sizeof(T) == 2) w[k >> 1] |= (uint32_t)row[c + k] << (16 * (k & 1));
+                    else w[k] = __float_as_uint(row[c + k]);
+                }
+        }
+    }
+    __device__ __forceinline__ float get(int k) const {
+        if constexpr (sizeof(T) == 4) return __uint_as_float(w[k]);
+        else return __uint_as_float((k & 1) ? (w[k >> 1] & 0xffff0000u) : (w[k >> 1] << 16));
+    }
+    __device__ __forceinline__ static void store(T *row, int64_t c, int64_t D, const float (&y)[kNormVec]) {
+        if (c + kNormVec <= D) {
+            uint32_t o[W];
+            if constexpr (sizeof(T) == 2) {
+#pragma unroll
+                for (int k = 0; k < W; ++k) o[k] = f32x2_to_bf16x2(y[2 * k], y[2 * k + 1]);
+            } else {
+#pragma unroll
+                for (int k = 0; k < W; ++k) o[k] = __float_as_uint(y[k]);
+            }
+            any_u32 v;
+            __builtin_memcpy(&v, o, sizeof o);
+            __builtin_nontemporal_store(v, reinterpret_cast<any_u32 *>(row + c));
+        } else {
+#pragma unroll
+            for (int k = 0; k < kNormVec; ++k)
+                if (c + k < D) io<T>::st(row, c + k, y[k]);
+        }
+    }
+};
+
+// fp32 parameters of the thread's columns (zero without the array or past the row).
+__device__ __forceinline__ void load_params(const float *p, int64_t c, int64_t D, float (&o)[kNormVec]) {
+    typedef float any_f32 __attribute__((ext_vector_type(kNormVec), aligned(sizeof(float))));
+    if (p && c + kNormVec <= D) {
+        const any_f32 v = *reinterpret_cast<const any_f32 *>(p + c);
+#pragma unroll
+        for (int k = 0; k < kNormVec; ++k) o[k] = v[k];
+    } else {
+#pragma unroll
+        for (int k = 0; k < kNormVec; ++k) o[k] = p && c + k < D ? p[c + k] : 0.0f;
+    }
+}
+
+// SLOTS = threads / TPR rows at a time.  S: the type of residual and sum.
+template <typename IO, typename S, int TPR, int NV>
+__global__ void __launch_bounds__(TPR > 64 ? TPR : 256)
 layernorm_fwd_kernel(const IO *__restrict__ x, const S *res, const float *__restrict__ w,
                      const float *__restrict__ bias, float eps, IO *__restrict__ y, S *sum,
-                     float *__restrict__ mean, float *__restrict__ rstd, int64_t D) {
-    __shared__ float red[kNormThreads / 64];
+                     float *__restrict__ mean, float *__restrict__ rstd, int64_t M, int64_t D) {
+    constexpr int SLOTS = TPR > 64 ? 1 : 256 / TPR;
+    __shared__ float red[2][TPR / 64];
+    const int tid = threadIdx.x % TPR;
+    const float inv_d = 1.0f / (float)D;
+    float wv[NV][kNormVec], bv[NV][kNormVec];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+        const int64_t c = (int64_t)(j * TPR + tid) * kNormVec;
+        load_params(w, c, D, wv[j]);
+        load_params(bias, c, D, bv[j]);
+    }
+    norm_vec<IO> rx[NV];
+    norm_vec<S> rr[NV];
+    auto fetch = [&](int64_t row) {
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int64_t c = (int64_t)(j * TPR + tid) * kNormVec;
+            rx[j].load(x + row * D, c, D);
+            if (res) rr[j].load(res + row * D, c, D);
+        }
+    };
+    const int64_t step = (int64_t)gridDim.x * SLOTS;
+    int64_t row = (int64_t)blockIdx.x * SLOTS + (SLOTS > 1 ? __builtin_amdgcn_readfirstlane(threadIdx.x / TPR) : 0);
+    if (row < M) fetch(row);
+    for (; row < M; row += step) {
+        float v[NV][kNormVec], m = 0.0f;
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+#pragma unroll
+            for (int k = 0; k < kNormVec; ++k) {
+                float t = rx[j].get(k);
+                if (res) t += rr[j].get(k);
+                if constexpr (sizeof(S) == 2) t = bf16_to_f32(f32_to_bf16(t));
+                v[j][k] = t;
+                m += t;
+            }
+        if (row + step < M) fetch(row + step);
+        m = row_sum<TPR>(m, red[0]) * inv_d;
+        float q = 0.0f;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int64_t c = (int64_t)(j * TPR + tid) * kNormVec;
+            if (sum && c < D) norm_vec<S>::store(sum + row * D, c, D, v[j]);
+#pragma unroll
+            for (int k = 0; k < kNormVec; ++k) {
+                v[j][k] = c + k < D ? v[j][k] - m : 0.0f;
+                q = fmaf(v[j][k], v[j][k], q);
+            }
+        }
+        const float rs = 1.0f / sqrtf(fmaf(row_sum<TPR>(q, red[1]), inv_d, eps));
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int64_t c = (int64_t)(j * TPR + tid) * kNormVec;
+            float o[kNormVec];
+#pragma unroll
+            for (int k = 0; k < kNormVec; ++k) o[k] = fmaf(v[j][k] * rs, wv[j][k], bv[j][k]);
+            if (c < D) norm_vec<IO>::store(y + row * D, c, D, o);
+        }
+        if (tid == 0) {
+            if (mean) mean[row] = m;
+            if (rstd) rstd[row] = rs;
+        }
+    }
+}
+
+// The gradients; the sums over this workgroup's rows go to row blockIdx.x of pw and pb (if given).
+template <typename IO, typename S, int TPR, int NV>
+__global__ void __launch_bounds__(TPR > 64 ? TPR : 256)
+layernorm_bwd_kernel(const IO *__restrict__ dy, const S *__restrict__ s, const float *__restrict__ w,
+                     const float *__restrict__ mean, const float *__restrict__ rstd, const S *dres, S *ds,
+                     IO *__restrict__ dx, float *__restrict__ pw, float *__restrict__ pb, int64_t M, int64_t D) {
+    constexpr int SLOTS = TPR > 64 ? 1 : 256 / TPR;
+    __shared__ float red[2][TPR / 64][2];
+    const int tid = threadIdx.x % TPR;
+    const int slot = SLOTS > 1 ? __builtin_amdgcn_readfirstlane(threadIdx.x / TPR) : 0;
+    const float inv_d = 1.0f / (float)D;
+    float wv[NV][kNormVec], aw[NV][kNormVec], ab[NV][kNormVec];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+        load_params(w, (int64_t)(j * TPR + tid) * kNormVec, D, wv[j]);
+#pragma unroll
+        for (int k = 0; k < kNormVec; ++k) aw[j][k] = ab[j][k] = 0.0f;
+    }
+    norm_vec<IO> rg[NV];
+    norm_vec<S> rs[NV], rd[NV];
+    float m = 0.0f, r = 0.0f;
+    auto fetch = [&](int64_t row) {
+        m = mean[row];
+        r = rstd[row];
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int64_t c = (int64_t)(j * TPR + tid) * kNormVec;
+            rg[j].load(dy + row * D, c, D);
+            rs[j].load(s + row * D, c, D);
+            if (dres) rd[j].load(dres + row * D, c, D);
+        }
+    };
+    const int64_t step = (int64_t)gridDim.x * SLOTS;
+    int64_t row = (int64_t)blockIdx.x * SLOTS + slot;
+    int turn = 0;
+    if (row < M) fetch(row);
+    for (; row < M; row += step, turn ^= 1) {
+        float t[NV][kNormVec], n[NV][kNormVec], p = 0.0f, q = 0.0f;
+        norm_vec<S> cd[NV];
+        const float rc = r;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int64_t c = (int64_t)(j * TPR + tid) * kNormVec;
+#pragma unroll
+            for (int k = 0; k < kNormVec; ++k) {
+                const float g = rg[j].get(k);
+                n[j][k] = c + k < D ? (rs[j].get(k) - m) * r : 0.0f;
+                aw[j][k] = fmaf(g, n[j][k], aw[j][k]);
+                ab[j][k] += g;
+                t[j][k] = g * wv[j][k];
+                p += t[j][k];
+                q = fmaf(t[j][k], n[j][k], q);
+            }
+            if (dres) cd[j] = rd[j];
+        }
+        if (row + step < M) fetch(row + step);
+        row_sum2<TPR>(p, q, red[turn]);
+        p *= inv_d;
+        q *= inv_d;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int64_t c = (int64_t)(j * TPR + tid) * kNormVec;
+            float o[kNormVec];
+#pragma unroll
+            for (int k = 0; k < kNormVec; ++k) {
+                o[k] = (t[j][k] - fmaf(n[j][k], q, p)) * rc;
+                if (dres) o[k] += cd[j].get(k);
+            }
+            if (c < D) {
+                norm_vec<S>::store(ds + row * D, c, D, o);
+                if (dx) norm_vec<IO>::store(dx + row * D, c, D, o);
+            }
+        }
+    }
+    if (!pw) return;
+    if constexpr (SLOTS > 1) {   // the slots' sums, in order
+        __shared__ float acc[2][NV * kNormVec][TPR];
+        for (int k = SLOTS - 1; k >= 0; --k) {
+            if (slot == k) {
+#pragma unroll
+                for (int j = 0; j < NV * kNormVec; ++j) {
+                    if (k < SLOTS - 1) {
+                        aw[j / kNormVec][j % kNormVec] += acc[0][j][tid];
+                        ab[j / kNormVec][j % kNormVec] += acc[1][j][tid];
+                    }
+                    acc[0][j][tid] = aw[j / kNormVec][j % kNormVec];
+                    acc[1][j][tid] = ab[j / kNormVec][j % kNormVec];
+                }
+            }
+            __syncthreads();
+        }
+    }
+    if (slot == 0) {
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int64_t c = (int64_t)(j * TPR + tid) * kNormVec;
+#pragma unroll
+            for (int k = 0; k < kNormVec; ++k)
+                if (c + k < D) {
+                    pw[(int64_t)blockIdx.x * D + c + k] = aw[j][k];
+                    pb[(int64_t)blockIdx.x * D + c + k] = ab[j][k];
+                }
+        }
+    }
+}
+
+// out[d] = sum of the n rows of each part, in an order of their own: 16 waves take every 16th row,
+// and their sums are added in order.
+constexpr int kNormSumWaves = 16;
+static __global__ void __launch_bounds__(64 * kNormSumWaves)
+layernorm_wgrad_sum_kernel(const float *__restrict__ pw, const float *__restrict__ pb, float *__restrict__ dw,
+                           float *__restrict__ db, int64_t n, int64_t D) {
+    __shared__ float red[2][kNormSumWaves][64];
+    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+    const int64_t d = (int64_t)blockIdx.x * 64 + lane;
+    float a = 0.0f, b = 0.0f;
+    if (d < D) {
+#pragma unroll 4
+        for (int64_t k = w; k < n; k += kNormSumWaves) {
+            a += pw[k * D + d];
+            b += pb[k * D + d];
+        }
+    }
+    red[0][w][lane] = a;
+    red[1][w][lane] = b;
+    __syncthreads();
+    if (w < 2 && d < D) {
+        float t = red[w][0][lane];
+#pragma unroll
+        for (int k = 1; k < kNormSumWaves; ++k) t += red[w][k][lane];
+        float *o = w == 0 ? dw : db;
+        if (o) o[d] = t;
+    }
+}
+
+// ---- rows wider than the registers hold: one workgroup per row, several passes over it ----------
+
+constexpr int kNormWideThreads = 1024;
+
+template <typename IO, typename S>
+__global__ void __launch_bounds__(kNormWideThreads)
+layernorm_fwd_wide_kernel(const IO *__restrict__ x, const S *res, const float *__restrict__ w,
+                          const float *__restrict__ bias, float eps, IO *__restrict__ y, S *sum,
+                          float *__restrict__ mean, float *__restrict__ rstd, int64_t D) {
+    __shared__ float red[2][kNormWideThreads / 64];
     const int64_t row = blockIdx.x, o = row * D;
+    const float inv_d = 1.0f / (float)D;
     auto value = [&](int64_t k) {
         float v = io<IO>::ld(x, o + k);
         if (res) v += io<S>::ld(res, o + k);
@@ -40,18 +351,18 @@ layernorm_fwd_kernel(const IO *__restrict__ x, const S *res, const float *__rest
         return v;
     };
     float m = 0.0f;
-    for (int64_t k = threadIdx.x; k < D; k += kNormThreads) m += value(k);
-    m = block_sum(m, red) / (float)D;
+    for (int64_t k = threadIdx.x; k < D; k += kNormWideThreads) m += value(k);
+    m = row_sum<kNormWideThreads>(m, red[0]) * inv_d;
     float q = 0.0f;
-    for (int64_t k = threadIdx.x; k < D; k += kNormThreads) {
+    for (int64_t k = threadIdx.x; k < D; k += kNormWideThreads) {
         const float c = value(k) - m;
         q = fmaf(c, c, q);
     }
-    const float rs = 1.0f / sqrtf(block_sum(q, red) / (float)D + eps);
-    for (int64_t k = threadIdx.x; k < D; k += kNormThreads) {
+    const float rs = 1.0f / sqrtf(fmaf(row_sum<kNormWideThreads>(q, red[1]), inv_d, eps));
+    for (int64_t k = threadIdx.x; k < D; k += kNormWideThreads) {
         const float v = value(k), n = (v - m) * rs;
         if (sum) io<S>::st(sum, o + k, v);
-        io<IO>::st(y, o + k, bias ? fmaf(n, w[k], bias[k]) : n * w[k]);
+        io<IO>::st(y, o + k, fmaf(n, w[k], bias ? bias[k] : 0.0f));
     }
     if (threadIdx.x == 0) {
         if (mean) mean[row] = m;
@@ -60,24 +371,25 @@ layernorm_fwd_kernel(const IO *__restrict__ x, const S *res, const float *__rest
 }
 
 template <typename IO, typename S>
-__global__ void __launch_bounds__(kNormThreads)
-layernorm_bwd_kernel(const IO *__restrict__ dy, const S *__restrict__ s, const float *__restrict__ w,
-                     const float *__restrict__ mean, const float *__restrict__ rstd, const S *dres, S *ds,
-                     IO *__restrict__ dx, int64_t D) {
-    __shared__ float red[kNormThreads / 64];
+__global__ void __launch_bounds__(kNormWideThreads)
+layernorm_bwd_wide_kernel(const IO *__restrict__ dy, const S *__restrict__ s, const float *__restrict__ w,
+                          const float *__restrict__ mean, const float *__restrict__ rstd, const S *dres, S *ds,
+                          IO *__restrict__ dx, int64_t D) {
+    __shared__ float red[kNormWideThreads / 64][2];
     const int64_t row = blockIdx.x, o = row * D;
-    const float m = mean[row], rs = rstd[row];
+    const float m = mean[row], rs = rstd[row], inv_d = 1.0f / (float)D;
     float p = 0.0f, q = 0.0f;
-    for (int64_t k = threadIdx.x; k < D; k += kNormThreads) {
+    for (int64_t k = threadIdx.x; k < D; k += kNormWideThreads) {
         const float t = io<IO>::ld(dy, o + k) * w[k];
         p += t;
         q = fmaf(t, (io<S>::ld(s, o + k) - m) * rs, q);
     }
-    p = block_sum(p, red) / (float)D;
-    q = block_sum(q, red) / (float)D;
-    for (int64_t k = threadIdx.x; k < D; k += kNormThreads) {
-        const float xh = (io<S>::ld(s, o + k) - m) * rs;
-        float v = (io<IO>::ld(dy, o + k) * w[k] - p - xh * q) * rs;
+    row_sum2<kNormWideThreads>(p, q, red);
+    p *= inv_d;
+    q *= inv_d;
+    for (int64_t k = threadIdx.x; k < D; k += kNormWideThreads) {
+        const float n = (io<S>::ld(s, o + k) - m) * rs;
+        float v = (io<IO>::ld(dy, o + k) * w[k] - fmaf(n, q, p)) * rs;
         if (dres) v += io<S>::ld(dres, o + k);
         io<S>::st(ds, o + k, v);
         if (dx) io<IO>::st(dx, o + k, v);
@@ -87,9 +399,9 @@ layernorm_bwd_kernel(const IO *__restrict__ dy, const S *__restrict__ s, const f
 // The parameters' gradients over rows [blockIdx.y * rows_per, ...), one column per thread.
 template <typename IO, typename S>
 __global__ void __launch_bounds__(256)
-layernorm_wgrad_kernel(const IO *__restrict__ dy, const S *__restrict__ s, const float *__restrict__ mean,
-                       const float *__restrict__ rstd, float *__restrict__ pw, float *__restrict__ pb, int64_t M,
-                       int64_t D, int64_t rows_per) {
+layernorm_wgrad_wide_kernel(const IO *__restrict__ dy, const S *__restrict__ s, const float *__restrict__ mean,
+                            const float *__restrict__ rstd, float *__restrict__ pw, float *__restrict__ pb, int64_t M,
+                            int64_t D, int64_t rows_per) {
     const int64_t d = (int64_t)blockIdx.x * 256 + threadIdx.x;
     if (d >= D) return;
     const int64_t r1 = min(M, (blockIdx.y + 1) * rows_per);
@@ -101,21 +413,6 @@ layernorm_wgrad_kernel(const IO *__restrict__ dy, const S *__restrict__ s, const
     }
     pw[blockIdx.y * D + d] = a;
     pb[blockIdx.y * D + d] = b;
-}
-
-// out[d] = sum of the n rows of part, in order (both arrays in one launch).
-static __global__ void __launch_bounds__(256)
-layernorm_wgrad_sum_kernel(const float *__restrict__ pw, const float *__restrict__ pb, float *__restrict__ dw,
-                           float *__restrict__ db, int64_t n, int64_t D) {
-    const int64_t d = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (d >= D) return;
-    float a = 0.0f, b = 0.0f;
-    for (int64_t k = 0; k < n; ++k) {
-        a += pw[k * D + d];
-        b += pb[k * D + d];
-    }
-    if (dw) dw[d] = a;
-    if (db) db[d] = b;
 }
 
 }  // namespace ssm
