@@ -21,7 +21,8 @@ int check_gated_dims(const ssm_dims *dm, bool seq) {
                     (long long)dm->seqlen, (long long)dm->dim);
     if (dm->io_dtype != SSM_IO_F32 && dm->io_dtype != SSM_IO_BF16)
         return fail(SSM_ERR_DTYPE, "io_dtype %d is not SSM_IO_F32 (0) or SSM_IO_BF16 (1)", dm->io_dtype);
-    if (dm->dim > kMaxDim || dm->batch > kMaxDim) return fail(SSM_ERR_SHAPE, "dim or batch larger than 2^30");
+    if (dm->dim > kMaxDim / 2 || dm->batch > kMaxDim)   // (a row's bytes are addressed with 32 bits)
+        return fail(SSM_ERR_SHAPE, "dim larger than 2^29 or batch larger than 2^30");
     if (dm->batch > 0 && dm->dim > (int64_t(1) << 36) / dm->batch)
         return fail(SSM_ERR_SHAPE, "batch*dim exceeds 2^36 (grid size)");
     if (seq && (dm->seqlen > kMaxDim ||
@@ -38,79 +39,95 @@ int launched() {
     return ok();
 }
 
-// How the sequences are cut, and the workspace: the chain's words [batch][nchunk][dim], then the
-// counters; one chunk per sequence needs neither.
+// How the sequences are cut, and the workspace: the states [batch][nchunk][dim] that the backward
+// starts from, then the chain's words [batch][items per sequence][dim] and the counters; one chunk per
+// sequence needs none of it.
 struct Plan {
-    int64_t nchunk, tiles, chains, words;
+    int64_t nchunk, tiles, chains, cells;
     int V;
-    size_t word_bytes, bytes;
+    size_t state_bytes, word_bytes, bytes;
 };
-constexpr size_t kCounterBytes = sizeof(int) * ssm::kGatedGroups * ssm::kGatedCounterStride;
+constexpr int64_t kCounterInts = ssm::kGatedQueues * ssm::kGatedCounterStride;
 
 Plan make_plan(const ssm_dims *dm) {
     Plan p;
-    p.V = dm->dim >= 2 ? 2 : 1;
+    p.V = dm->io_dtype == SSM_IO_BF16 && dm->dim >= 2 ? 2 : 1;   // (a lane's access is four bytes either way)
     p.nchunk = std::max<int64_t>((dm->seqlen + ssm::kGatedChunk - 1) / ssm::kGatedChunk, 1);
     p.tiles = (dm->dim + 64 * p.V - 1) / (64 * p.V);
     p.chains = dm->batch * p.tiles;
-    p.words = dm->batch * p.nchunk * dm->dim;
-    p.word_bytes = p.nchunk > 1 ? align256((size_t)p.words * sizeof(uint64_t)) : 0;
-    p.bytes = p.nchunk > 1 ? p.word_bytes + kCounterBytes : 0;
+    p.cells = dm->batch * p.nchunk * dm->dim;
+    p.state_bytes = p.nchunk > 1 ? align256((size_t)p.cells * sizeof(float)) : 0;
+    p.word_bytes = p.nchunk > 1 ? align256((size_t)p.cells * sizeof(uint64_t)) : 0;
+    p.bytes = p.nchunk > 1 ? p.state_bytes + p.word_bytes + kCounterInts * sizeof(int) : 0;
     return p;
 }
 
-// One workgroup per (chain, chunk), the chains dealt to the groups in turn.
-int64_t items(const Plan &p) {
-    return (p.chains + ssm::kGatedGroups - 1) / ssm::kGatedGroups * ssm::kGatedGroups * p.nchunk;
+// Consecutive workgroups that draw from one queue (see the kernel): 1 while the launch is a few rounds
+// of the chip and hand-overs count (B2 L2048 D1536 fp32: 23 us, 26 with 8), 8 where it is longer and
+// bandwidth does.
+int run_of(const Plan &p, int64_t nitem) { return p.chains * nitem < 4096 ? 1 : 8; }
+
+// One workgroup per (chain, item), the chains dealt to the queues in turn.
+int64_t grid_of(const Plan &p, int64_t nitem) {
+    const int64_t per = (p.chains + ssm::kGatedQueues - 1) / ssm::kGatedQueues * nitem, run = run_of(p, nitem);
+    return (per + run - 1) / run * run * ssm::kGatedQueues;   // (per: items of the longest queue)
 }
 
 int check_items(const Plan &p) {
-    if (items(p) > (int64_t(1) << 31) - 1 || p.chains > (int64_t(1) << 31) - 1)
+    if (p.chains > (int64_t(1) << 31) - ssm::kGatedQueues || grid_of(p, p.nchunk) > (int64_t(1) << 31) - 1)
         return fail(SSM_ERR_SHAPE, "batch * ceil(dim / %d) * ceil(seqlen / %d) exceeds 2^31 work items", 64 * p.V,
                     ssm::kGatedChunk);
     return SSM_OK;
 }
 
-int *counters_of(const Plan &p, void *ws) {
-    return p.nchunk > 1 ? reinterpret_cast<int *>(static_cast<char *>(ws) + p.word_bytes) : nullptr;
+// The chain's words and counters behind `words`, made ready for nitem items per sequence; counters
+// are NULL where there is no chain.
+int *launch_clear(const Plan &p, uint64_t *words, int64_t nitem, const ssm_dims *dm, hipStream_t st) {
+    if (nitem == 1) return nullptr;
+    int *counters = reinterpret_cast<int *>(reinterpret_cast<char *>(words) + p.word_bytes);
+    const int64_t n = dm->batch * nitem * dm->dim;
+    hipLaunchKernelGGL(ssm::gated_clear_kernel, dim3((unsigned)((n + kCounterInts + 255) / 256)), dim3(256), 0, st,
+                       words, n, counters);
+    return counters;
 }
 
-void launch_clear(const Plan &p, void *ws, hipStream_t st) {
-    if (p.nchunk == 1) return;
-    const int64_t n = p.words + ssm::kGatedGroups * ssm::kGatedCounterStride;
-    hipLaunchKernelGGL(ssm::gated_clear_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, st,
-                       static_cast<uint64_t *>(ws), p.words, counters_of(p, ws));
-}
-
-template <typename IO, int V, bool OUT>
+template <typename IO, int V, int M, bool OUT>
 void launch_fwd_v(const void *x, const void *r, const void *g, const float *A, const void *z, const float *h0,
                   const int32_t *sl, void *y, float *last, void *ws, const ssm_dims *dm, const Plan &p,
                   hipStream_t st) {
-    launch_clear(p, ws, st);
-    hipLaunchKernelGGL((ssm::gated_scan_kernel<IO, V, OUT>), dim3((unsigned)items(p)), dim3(64 * ssm::kGatedWaves), 0,
-                       st, static_cast<const IO *>(x), static_cast<const IO *>(r), static_cast<const IO *>(g), A,
-                       static_cast<const IO *>(z), h0, sl, static_cast<IO *>(y), last, static_cast<uint64_t *>(ws),
-                       counters_of(p, ws), dm->seqlen, dm->dim, (int)p.tiles, (int)p.chains, (int)p.nchunk);
+    const int64_t nitem = (p.nchunk + M - 1) / M;
+    float *states = p.nchunk > 1 ? static_cast<float *>(ws) : nullptr;
+    uint64_t *words = reinterpret_cast<uint64_t *>(static_cast<char *>(ws) + p.state_bytes);
+    int *counters = launch_clear(p, words, nitem, dm, st);
+    hipLaunchKernelGGL((ssm::gated_scan_kernel<IO, V, M, OUT>), dim3((unsigned)grid_of(p, nitem)),
+                       dim3(64 * ssm::kGatedWaves), 0, st, static_cast<const IO *>(x), static_cast<const IO *>(r),
+                       static_cast<const IO *>(g), A, static_cast<const IO *>(z), h0, sl, static_cast<IO *>(y), last,
+                       states, words, counters, dm->seqlen, dm->dim, (int)p.tiles, (int)p.chains, (int)nitem,
+                       (int)p.nchunk, run_of(p, nitem));
 }
+
+// Items of two chunks halve the hand-overs of a chain, at two workgroups per CU instead of three.  They
+// pay where a few chains share the chip: a hand-over takes about 1.2 us and the group's chunks take
+// the bandwidth 0.11 us per chain (B1 L131072 D2048 bf16, 16 chains: 495 -> 468 us; B8 L2048 D5120, 320
+// chains: 169 -> 184 us), as long as the halved number of items still fills the chip.
+bool wide_items(const Plan &p) { return p.chains <= 32 && p.chains * p.nchunk >= 4096; }
 
 template <bool OUT>
 void launch_fwd(const void *x, const void *r, const void *g, const float *A, const void *z, const float *h0,
                 const int32_t *sl, void *y, float *last, void *ws, const ssm_dims *dm, const Plan &p,
                 hipStream_t st) {
-    if (dm->io_dtype == SSM_IO_BF16) {
-        if (p.V == 2) launch_fwd_v<uint16_t, 2, OUT>(x, r, g, A, z, h0, sl, y, last, ws, dm, p, st);
-        else launch_fwd_v<uint16_t, 1, OUT>(x, r, g, A, z, h0, sl, y, last, ws, dm, p, st);
-    } else {
-        if (p.V == 2) launch_fwd_v<float, 2, OUT>(x, r, g, A, z, h0, sl, y, last, ws, dm, p, st);
-        else launch_fwd_v<float, 1, OUT>(x, r, g, A, z, h0, sl, y, last, ws, dm, p, st);
-    }
+    const bool wide = wide_items(p);
+    auto launch = dm->io_dtype == SSM_IO_F32 ? (wide ? launch_fwd_v<float, 1, 2, OUT> : launch_fwd_v<float, 1, 1, OUT>)
+                  : p.V == 2 ? (wide ? launch_fwd_v<uint16_t, 2, 2, OUT> : launch_fwd_v<uint16_t, 2, 1, OUT>)
+                             : launch_fwd_v<uint16_t, 1, 1, OUT>;
+    launch(x, r, g, A, z, h0, sl, y, last, ws, dm, p, st);
 }
 
-// The backward's workspace: the forward's (used where no checkpoints are given), its own chain, and
-// dA's shares [batch][nchunk][dim].
+// The backward's workspace: the forward's (its states, where no checkpoints are given; its chain is the
+// backward's afterwards), and dA's shares [batch][nchunk][dim].
 size_t bwd_bytes(const ssm_dims *dm, const Plan &p) {
     if (dm->batch == 0 || dm->dim == 0) return 0;
-    return 2 * p.bytes + align256((size_t)p.words * sizeof(float));
+    return p.bytes + align256((size_t)p.cells * sizeof(float));
 }
 
 template <typename IO, int V>
@@ -118,13 +135,15 @@ void launch_bwd_v(const void *x, const void *r, const void *g, const float *A, c
                   const int32_t *sl, const void *dy, const float *dlast, const void *states, void *dx, void *dr,
                   void *dg, void *dz, float *part, float *dh0, void *ws, const ssm_dims *dm, const Plan &p,
                   hipStream_t st) {
-    launch_clear(p, ws, st);
-    hipLaunchKernelGGL((ssm::gated_bwd_kernel<IO, V>), dim3((unsigned)items(p)), dim3(64 * ssm::kGatedWaves), 0, st,
+    uint64_t *words = reinterpret_cast<uint64_t *>(static_cast<char *>(ws) + p.state_bytes);
+    int *counters = launch_clear(p, words, p.nchunk, dm, st);
+    auto kern = z ? ssm::gated_bwd_kernel<IO, V, true> : ssm::gated_bwd_kernel<IO, V, false>;
+    hipLaunchKernelGGL(kern, dim3((unsigned)grid_of(p, p.nchunk)), dim3(64 * ssm::kGatedWaves), 0, st,
                        static_cast<const IO *>(x), static_cast<const IO *>(r), static_cast<const IO *>(g), A,
                        static_cast<const IO *>(z), h0, sl, static_cast<const IO *>(dy), dlast,
-                       static_cast<const uint64_t *>(states), static_cast<IO *>(dx), static_cast<IO *>(dr),
-                       static_cast<IO *>(dg), static_cast<IO *>(dz), part, dh0, static_cast<uint64_t *>(ws),
-                       counters_of(p, ws), dm->seqlen, dm->dim, (int)p.tiles, (int)p.chains, (int)p.nchunk);
+                       static_cast<const float *>(states), static_cast<IO *>(dx), static_cast<IO *>(dr),
+                       static_cast<IO *>(dg), static_cast<IO *>(dz), part, dh0, words, counters, dm->seqlen, dm->dim,
+                       (int)p.tiles, (int)p.chains, (int)p.nchunk, run_of(p, p.nchunk));
 }
 
 }  // namespace
@@ -201,15 +220,16 @@ int ssm_gated_scan_bwd(const void *x, const void *r, const void *g, const float 
     }
     hipStream_t st = static_cast<hipStream_t>(stream);
     char *ws = static_cast<char *>(workspace);
-    float *part = reinterpret_cast<float *>(ws + 2 * p.bytes);
+    float *part = reinterpret_cast<float *>(ws + p.bytes);
     if (dims->batch > 0) {
         const void *states = checkpoints ? checkpoints : workspace;
         if (!checkpoints && p.nchunk > 1)   // (a single chunk starts from the initial state)
             launch_fwd<false>(x, r, g, A, nullptr, initial_state, seq_lens, nullptr, nullptr, workspace, dims, p, st);
-        auto bwd = dims->io_dtype == SSM_IO_BF16 ? (p.V == 2 ? launch_bwd_v<uint16_t, 2> : launch_bwd_v<uint16_t, 1>)
-                                                 : (p.V == 2 ? launch_bwd_v<float, 2> : launch_bwd_v<float, 1>);
+        auto bwd = dims->io_dtype == SSM_IO_F32 ? launch_bwd_v<float, 1>
+                   : p.V == 2                   ? launch_bwd_v<uint16_t, 2>
+                                                : launch_bwd_v<uint16_t, 1>;
         bwd(x, r, g, A, z, initial_state, seq_lens, dy, dlast_state, states, dx, dr, dg, dz, part, dinitial_state,
-            ws + p.bytes, dims, p, st);
+            ws, dims, p, st);
     }
     hipLaunchKernelGGL(ssm::column_sum_kernel, dim3((unsigned)((dims->dim + 63) / 64)),
                        dim3(64 * ssm::kColumnWaves), 0, st, part, dA, dims->batch * p.nchunk, dims->dim);

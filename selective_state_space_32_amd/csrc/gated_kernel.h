@@ -18,20 +18,25 @@
 //      from there, writing y.
 // The inputs are read once and the outputs written once, whatever the length.
 //
-// The chain.  word[sequence][chunk][channel] is 64 bits: (P, H) as two floats, P = -1 meaning that
-// H is the state itself, all ones meaning that nothing is there yet (the words are filled with ones
-// before the kernel starts).  A chunk publishes its map at once and the state at its end as soon as
-// it knows it; the two halves travel in one 64-bit store, so a word that is read is whole and
-// nothing else has to be ordered.  A chunk reads the kGatedWindow words before its own: with a
-// state among them and maps after it, the state at its start is the fold of those maps, oldest
-// first, onto that state -- the same operations in the same order whichever word held the state,
-// so that the results do not depend on timing.
+// The chain.  Handing the state from chunk to chunk would cost a round trip through memory per chunk,
+// so the chunks of a chain form groups of kGatedGroup.  word[sequence][item][channel] is 64 bits: a
+// chunk publishes its map (P, H), two floats, as soon as it has it; the last chunk of a group
+// publishes instead the state at its end, as (-1, h), once it knows it.  A chunk fetches the maps of
+// the chunks before it in its group (which wait for nobody), composes them, and applies them to the
+// state that the group before left.  Only the groups' last chunks wait in line.  The chain's first
+// chunk publishes the constant map (0, state at its end): it alone reads the initial state.  The words are filled
+// with ones ("nothing yet") before the kernel starts; the two halves travel in one 64-bit store, so a
+// word that is read is whole and nothing else has to be ordered.  Which words a chunk combines, and
+// in which order, is fixed: the results do not depend on timing.
 //
 // Every wait ends: an item's number is drawn from a counter when its workgroup starts, and the
 // items of a chain are numbered in the order of the chain.  Whoever waits, waits for items that
-// started earlier, and the earliest of those waits for nobody.  There is one counter per
-// blockIdx mod 8 (the XCDs take workgroups in turn), each with the chains of that residue, so that
-// a chain's words stay in one XCD's reach and the counters are not fought over by the whole chip.
+// started earlier, and the earliest of those waits for nobody.  There are kGatedQueues counters (one
+// alone is fought over by the whole chip: 768 workgroups that start together wait 9 us), each with
+// the chains of its residue; `run` consecutive workgroups draw from the same one.  The XCDs take
+// workgroups in turn, so with run = 1 a chain stays in one XCD, whose hand-overs are the fastest, and
+// with run = 8 every XCD works on all the chains: with run = 1 an XCD reads the same few columns of
+// every row, which lie in few of the memory's channels (B1 L131072 D2048 bf16: 514 against 468 us).
 #pragma once
 
 #include <float.h>
@@ -42,23 +47,32 @@ namespace ssm {
 
 constexpr int kGatedRows = 8;                            // tokens per wave
 constexpr int kGatedWaves = 8;                           // waves per workgroup
-constexpr int kGatedChunk = kGatedRows * kGatedWaves;    // tokens per work item
-constexpr int kGatedWindow = 4;                          // words of the chain read at a time
-constexpr int kGatedGroups = 8;                          // counters (one per XCD)
+constexpr int kGatedChunk = kGatedRows * kGatedWaves;    // tokens per stored state (and per item of the backward)
+constexpr int kGatedGroup = 8;                           // chunks of a chain that share a hand-over
+constexpr int kGatedQueues = 8;                          // counters (one per XCD)
 constexpr int kGatedCounterStride = 64;                  // ints between them: lines of their own
 
-// 1 - a^2 = -expm1(u), u = 2 log a <= 0, given a and y = log2(a).  Near a = 1 the difference
-// loses every digit that a was rounded in, so for |u| < 1/4 the series -u (1 + u/2 + u^2/6 +
-// ...) is used: its dropped terms are below u^6/5040 < 5e-8 of the value, and 1 - a^2 above
-// the threshold is at least 0.22 (an ulp of a^2 costs it 4e-7).
+// 1 - a^2 = -expm1(2 ln 2 y), given y = log2(a) <= 0 and a.  Near a = 1 the difference loses every
+// digit that a was rounded in, so there a polynomial in y takes its place, y (c0 + c1 y + ...),
+// interpolated at Chebyshev nodes of the interval: degree 3 for 1 - a^2 < 0.22 (relative error
+// below 2.6e-7, 1.3e-7 of the root), or degree 4 for 1 - a^2 < 0.33 (3e-8) where both the inputs
+// and the outputs are fp32.  Above the interval an ulp of a^2 costs the difference 8e-7 and 4e-7.
+template <typename IO>
 __device__ __forceinline__ float one_minus_square(float y, float a) {
-    const float u = y * (2.0f * kLn2);
-    float p = fmaf(u, 1.0f / 720.0f, 1.0f / 120.0f);
-    p = fmaf(p, u, 1.0f / 24.0f);
-    p = fmaf(p, u, 1.0f / 6.0f);
-    p = fmaf(p, u, 0.5f);
-    p = -u * fmaf(p, u, 1.0f);
-    return fabsf(u) < 0.25f ? p : fmaf(-a, a, 1.0f);
+    constexpr bool kLong = sizeof(IO) == 4;
+    constexpr float kEnd = -(kLong ? 0.4f : 0.25f) / (2.0f * kLn2);
+    float p;
+    if constexpr (kLong) {
+        p = fmaf(y, -3.617433190962575e-2f, -0.15229893496512706f);
+        p = fmaf(p, y, -0.44387109232657457f);
+        p = fmaf(p, y, -0.9609002283833515f);
+        p = fmaf(p, y, -1.386294327691407f);
+    } else {
+        p = fmaf(y, -0.1393467438699137f, -0.44242258435379367f);
+        p = fmaf(p, y, -0.9608483593855177f);
+        p = fmaf(p, y, -1.386294036555376f);
+    }
+    return y > kEnd ? p * y : fmaf(-a, a, 1.0f);
 }
 
 // V neighbouring I/O elements of a row as raw 32-bit words.  Rows of an odd width start at odd
@@ -67,9 +81,12 @@ __device__ __forceinline__ float one_minus_square(float y, float a) {
 template <int V, typename IO> struct row_words {
     static constexpr int W = V * (int)sizeof(IO) < 4 ? 1 : V * (int)sizeof(IO) / 4;
     uint32_t w[W];
-    __device__ __forceinline__ void load(const IO *p) {
+    // row: the row's start (the same for the wave), lofs: the lane's byte offset in it -- the memory
+    // instructions take the two as they are, without address arithmetic per lane.
+    __device__ __forceinline__ void load(const IO *row, uint32_t lofs) {
+        const char *p = reinterpret_cast<const char *>(row) + lofs;
         if constexpr (V * sizeof(IO) < 4) {
-            w[0] = *p;
+            w[0] = *reinterpret_cast<const IO *>(p);
         } else {
             typedef uint32_t any_u32 __attribute__((ext_vector_type(W), aligned(sizeof(IO))));
             const any_u32 v = __builtin_nontemporal_load(reinterpret_cast<const any_u32 *>(p));
@@ -80,9 +97,19 @@ template <int V, typename IO> struct row_words {
         if constexpr (sizeof(IO) == 4) return __uint_as_float(w[v]);
         else return __uint_as_float((v & 1) ? (w[v >> 1] & 0xffff0000u) : (w[v >> 1] << 16));
     }
-    __device__ __forceinline__ static void store(IO *p, const float (&y)[V]) {
+    __device__ __forceinline__ void fill(uint32_t v) {
+#pragma unroll
+        for (int i = 0; i < W; ++i) w[i] = v;
+    }
+    // The words as if written anew: nothing computed from them before is known to hold after.
+    __device__ __forceinline__ void opaque() {
+#pragma unroll
+        for (int i = 0; i < W; ++i) asm volatile("" : "+v"(w[i]));
+    }
+    __device__ __forceinline__ static void store(IO *row, uint32_t lofs, const float (&y)[V]) {
+        char *p = reinterpret_cast<char *>(row) + lofs;
         if constexpr (V * sizeof(IO) < 4) {
-            io<IO>::st(p, 0, y[0]);
+            io<IO>::st(reinterpret_cast<IO *>(p), 0, y[0]);
         } else {
             uint32_t o[W];
             if constexpr (sizeof(IO) == 2) {
@@ -100,6 +127,11 @@ template <int V, typename IO> struct row_words {
     }
 };
 
+// The words of -infinity.
+template <typename IO> __device__ __forceinline__ uint32_t minus_inf_words() {
+    return sizeof(IO) == 4 ? 0xff800000u : 0xff80ff80u;
+}
+
 // The chain's words.
 constexpr uint32_t kWordEmpty = 0xffffffffu;
 __device__ __forceinline__ uint64_t chain_word(float P, float H) {
@@ -109,41 +141,84 @@ __device__ __forceinline__ uint64_t chain_word(float P, float H) {
 __device__ __forceinline__ void chain_put(uint64_t *w, float P, float H) {
     __hip_atomic_store(w, chain_word(P, H), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
-// The state that the items before this one leave, for the lane's V channels: the words of items
-// first, first + step, ... are read, kGatedWindow of them, stopping at item `end` (which needs
-// nobody and publishes a state); stride: words between two items.  One wave.
+__device__ __forceinline__ uint64_t chain_read(const uint64_t *w) {
+    return __hip_atomic_load(const_cast<uint64_t *>(w), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
+// The chain's step for the item at position pos, called by the whole workgroup: base + p * stride is
+// the word of position p (the lane's first of V channels), (P, H) the item's map and start the state
+// at position 0's start (both read in wave 0 only; 0 at other positions), `ends`: nobody comes after.  Leaves the state at
+// the item's start in s_in (behind a barrier) and the one at its end in wave 0's `out`.
 template <int V>
-__device__ __forceinline__ void chain_get(const uint64_t *base, int64_t stride, int first, int step, int end, bool act,
-                                          float (&carry)[V]) {
-    for (;;) {
-        uint64_t w[kGatedWindow][V];
+__device__ __forceinline__ void chain_step(uint64_t *base, int64_t stride, int pos, bool ends, bool act, int lane,
+                                           int w, const float (&P)[V], const float (&H)[V], const float (&start)[V],
+                                           uint64_t (&s_map)[kGatedGroup][64 * V], float (&s_in)[64 * V],
+                                           float (&out)[V]) {
+    static_assert(kGatedGroup <= kGatedWaves, "a wave fetches a map");
+    const int g = pos % kGatedGroup;
+    uint64_t *own = base + pos * stride;
+    if (w == 0 && act && !ends && g != kGatedGroup - 1) {
 #pragma unroll
-        for (int k = 0; k < kGatedWindow; ++k) {
-            const int j = step < 0 ? max(first - k, end) : min(first + k, end);
+        for (int v = 0; v < V; ++v)
+            if (pos == 0) chain_put(own + v, 0.0f, fmaf(P[v], start[v], H[v]));
+            else chain_put(own + v, P[v], H[v]);
+    }
+    if (w < g) {   // the map of the group's item w
+        const uint64_t *src = base + (pos - g + w) * stride;
+        uint64_t u[V];
+        for (;;) {
+            bool all = true;
 #pragma unroll
-            for (int v = 0; v < V; ++v)
-                w[k][v] = __hip_atomic_load(const_cast<uint64_t *>(base + j * stride + v), __ATOMIC_RELAXED,
-                                            __HIP_MEMORY_SCOPE_AGENT);
+            for (int v = 0; v < V; ++v) {
+                u[v] = chain_read(src + v);
+                all = all && (uint32_t)(u[v] >> 32) != kWordEmpty;
+            }
+            if (__all(all || !act)) break;
+            __builtin_amdgcn_s_sleep(1);
         }
-        bool all = true;
+#pragma unroll
+        for (int v = 0; v < V; ++v) s_map[w][lane * V + v] = u[v];
+    }
+    if (g > 0) __syncthreads();
+    if (w == 0) {
+        float cp[V], ch[V], in[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) cp[v] = 1.0f, ch[v] = 0.0f;
+#pragma unroll 2
+        for (int k = 0; k < g; ++k)
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const uint64_t u = s_map[k][lane * V + v];
+                const float p = __uint_as_float((uint32_t)(u >> 32));
+                ch[v] = fmaf(p, ch[v], __uint_as_float((uint32_t)u));
+                cp[v] *= p;
+            }
+        if (pos == g) {   // the first group: position 0 has taken the start in (0 elsewhere)
+#pragma unroll
+            for (int v = 0; v < V; ++v) in[v] = start[v];
+        } else {
+            const uint64_t *src = base + (pos - g - 1) * stride;
+            for (;;) {
+                bool all = true;
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+                    const uint64_t u = chain_read(src + v);
+                    in[v] = __uint_as_float((uint32_t)u);
+                    all = all && (uint32_t)(u >> 32) == __float_as_uint(-1.0f);
+                }
+                if (__all(all || !act)) break;
+                __builtin_amdgcn_s_sleep(1);
+            }
+        }
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            bool ok = false;
-            float h = 0.0f;
-#pragma unroll
-            for (int k = kGatedWindow - 1; k >= 0; --k) {   // oldest first
-                const uint32_t p = (uint32_t)(w[k][v] >> 32);
-                const float H = __uint_as_float((uint32_t)w[k][v]);
-                const bool state = p == __float_as_uint(-1.0f);
-                h = state ? H : fmaf(__uint_as_float(p), h, H);
-                ok = state || (ok && p != kWordEmpty);
-            }
-            carry[v] = h;
-            all = all && ok;
+            in[v] = fmaf(cp[v], in[v], ch[v]);
+            out[v] = fmaf(P[v], in[v], H[v]);
+            if (act && !ends && g == kGatedGroup - 1) chain_put(own + v, -1.0f, out[v]);
+            s_in[lane * V + v] = in[v];
         }
-        if (__all(all || !act)) return;
-        __builtin_amdgcn_s_sleep(1);
     }
+    __syncthreads();
 }
 
 // Which item this workgroup takes: (chain, position along the chain), or chain < 0 for none.
@@ -151,20 +226,20 @@ __device__ __forceinline__ void chain_get(const uint64_t *base, int64_t stride, 
 struct GatedItem {
     int chain, pos;
 };
-__device__ __forceinline__ GatedItem gated_item(int chains, int nchunk, int *counters, int *slot) {
-    const int q = (int)blockIdx.x % kGatedGroups;
-    const int nq = (chains - q + kGatedGroups - 1) / kGatedGroups;
-    int n = (int)blockIdx.x / kGatedGroups;
-    if (counters) {   // (one chunk per sequence: no chain, any order will do)
+__device__ __forceinline__ GatedItem gated_item(int chains, int nitem, int *counters, int run, int *slot) {
+    const int q = (int)blockIdx.x / run % kGatedQueues;
+    const int nq = (chains - q + kGatedQueues - 1) / kGatedQueues;
+    int n = (int)blockIdx.x / (run * kGatedQueues) * run + (int)blockIdx.x % run;
+    if (counters) {   // (one item per sequence: no chain, any order will do)
         if (threadIdx.x == 0)
             *slot = __hip_atomic_fetch_add(&counters[q * kGatedCounterStride], 1, __ATOMIC_RELAXED,
                                            __HIP_MEMORY_SCOPE_AGENT);
         __syncthreads();
         n = __builtin_amdgcn_readfirstlane(*slot);
     }
-    if (nq <= 0 || n >= nq * nchunk) return {-1, 0};
+    if (nq <= 0 || n >= nq * nitem) return {-1, 0};
     const int pos = n / nq;
-    return {(n - pos * nq) * kGatedGroups + q, pos};
+    return {(n - pos * nq) * kGatedQueues + q, pos};
 }
 
 // Fills the chain's words with ones and clears the counters behind them.
@@ -172,36 +247,41 @@ static __global__ void __launch_bounds__(256)
 gated_clear_kernel(uint64_t *__restrict__ words, int64_t n, int *__restrict__ counters) {
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
     if (i < n) words[i] = ~uint64_t(0);
-    else if (i - n < kGatedGroups * kGatedCounterStride) counters[i - n] = 0;
+    else if (i - n < kGatedQueues * kGatedCounterStride) counters[i - n] = 0;
 }
 
 // A token's coefficients for one channel.
 struct GatedCoeff {
     float s, i, y, a, q;   // sigmoid(r), sigmoid(g), log2 a, a, 1 - a^2
 };
+template <typename IO>
 __device__ __forceinline__ GatedCoeff gated_coeff(float r, float g, float a2) {
     GatedCoeff c;
     c.s = sigmoid_f32(r);
     c.i = sigmoid_f32(g);
     c.y = a2 * c.s;
     c.a = hw_exp2(c.y);
-    c.q = one_minus_square(c.y, c.a);
+    c.q = one_minus_square<IO>(c.y, c.a);
     return c;
 }
 
-// OUT: y and last_state are written; otherwise only the chain's words (the states at the chunks'
-// ends, for the backward pass).
-template <typename IO, int V, bool OUT>
+// OUT: y and last_state are written; otherwise only the states.  states (nullable): the state at the
+// end of every kGatedChunk tokens but a sequence's last, for the backward pass.
+// M: the tokens of an item in units of kGatedChunk.
+template <typename IO, int V, int M, bool OUT>
 __global__ void __launch_bounds__(64 * kGatedWaves)
 gated_scan_kernel(const IO *__restrict__ x, const IO *__restrict__ r, const IO *__restrict__ g,
                   const float *__restrict__ A, const IO *__restrict__ z, const float *h0,
-                  const int32_t *__restrict__ seq_lens, IO *__restrict__ y, float *last, uint64_t *words,
-                  int *counters, int64_t L, int64_t D, int tiles, int chains, int nchunk) {
-    constexpr int T = kGatedRows, K = kGatedWaves, C = kGatedChunk;
+                  const int32_t *__restrict__ seq_lens, IO *__restrict__ y, float *last,
+                  float *__restrict__ states, uint64_t *words, int *counters, int64_t L, int64_t D, int tiles, int chains, int nitem, int nchunk,
+                  int run) {
+    constexpr int T = M * kGatedRows, K = kGatedWaves, C = M * kGatedChunk;
+    static_assert(K % M == 0, "a stored state is at a wave's end");
     using Row = row_words<V, IO>;
     __shared__ float s_P[K][64 * V], s_H[K][64 * V], s_in[64 * V];
+    __shared__ uint64_t s_map[kGatedGroup][64 * V];
     __shared__ int s_slot;
-    const GatedItem it = gated_item(chains, nchunk, counters, &s_slot);
+    const GatedItem it = gated_item(chains, nitem, counters, run, &s_slot);
     if (it.chain < 0) return;
     const int b = it.chain / tiles, c = it.pos;
     const int lane = threadIdx.x & 63;
@@ -211,16 +291,17 @@ gated_scan_kernel(const IO *__restrict__ x, const IO *__restrict__ r, const IO *
     const int64_t dl = (int64_t)(it.chain - b * tiles) * 64 * V + lane * V;
     const bool act = dl < D;
     const int64_t d = min(dl, D - V);
+    const uint32_t lofs = (uint32_t)d * (uint32_t)sizeof(IO);
     const int64_t Lb = seq_lens ? min((int64_t)max(seq_lens[b], 0), L) : L;
     const int64_t t0 = (int64_t)c * C + w * T;
     const int64_t row0 = (int64_t)b * L;
-    const int nlive = (int)((Lb + C - 1) / C);   // chunks of this sequence that hold tokens
+    const int nlive = (int)((Lb + C - 1) / C);   // items of this sequence that hold tokens
 
     if (c >= nlive) {   // past the sequence's end
         if constexpr (OUT) {
             if (act) {
                 const float zero[V] = {};
-                for (int64_t t = t0; t < min(t0 + T, L); ++t) Row::store(y + (row0 + t) * D + d, zero);
+                for (int64_t t = t0; t < min(t0 + T, L); ++t) Row::store(y + (row0 + t) * D, lofs, zero);
                 if (last && c == 0 && w == 0)
                     for (int v = 0; v < V; ++v) last[(int64_t)b * D + d + v] = h0 ? h0[(int64_t)b * D + d + v] : 0.0f;
             }
@@ -232,33 +313,43 @@ gated_scan_kernel(const IO *__restrict__ x, const IO *__restrict__ r, const IO *
     Row rr[T], rg[T], rx[T], rz[OUT ? T : 1];
 #pragma unroll
     for (int k = 0; k < T; ++k) {
-        const int64_t e = (row0 + min(t0 + k, Lb - 1)) * D + d;
-        rr[k].load(r + e);
-        rg[k].load(g + e);
-        rx[k].load(x + e);
+        const int64_t e = (row0 + min(t0 + k, Lb - 1)) * D;
+        rr[k].load(r + e, lofs);
+        rg[k].load(g + e, lofs);
+        rx[k].load(x + e, lofs);
     }
     if constexpr (OUT) {
         if (z) {
 #pragma unroll
-            for (int k = 0; k < T; ++k) rz[k].load(z + (row0 + min(t0 + k, Lb - 1)) * D + d);
+            for (int k = 0; k < T; ++k) rz[k].load(z + (row0 + min(t0 + k, Lb - 1)) * D, lofs);
         }
     }
     float a2[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) a2[v] = A[d + v] * kLog2e;
 
-    // 1. the coefficients (a token past the end is the identity) and the wave's map
+    // Tokens past the end become the identity (a = 1, an input of 0) without a test per value below.
+    if (t0 + T > Lb) {
+#pragma unroll
+        for (int k = 0; k < T; ++k)
+            if (t0 + k >= Lb) {
+                rr[k].fill(minus_inf_words<IO>());
+                rg[k].fill(0);
+                rx[k].fill(0);
+            }
+    }
+
+    // 1. the coefficients and the wave's map
     float a[T][V], bb[T][V], P[V], H[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) P[v] = 1.0f, H[v] = 0.0f;
 #pragma unroll
     for (int k = 0; k < T; ++k) {
-        const bool live = t0 + k < Lb;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            const GatedCoeff cf = gated_coeff(rr[k].get(v), rg[k].get(v), a2[v]);
-            a[k][v] = live ? cf.a : 1.0f;
-            bb[k][v] = live ? __builtin_amdgcn_sqrtf(cf.q) * cf.i * rx[k].get(v) : 0.0f;
+            const GatedCoeff cf = gated_coeff<IO>(rr[k].get(v), rg[k].get(v), a2[v]);
+            a[k][v] = cf.a;
+            bb[k][v] = __builtin_amdgcn_sqrtf(cf.q) * cf.i * rx[k].get(v);
             P[v] *= a[k][v];
             H[v] = fmaf(a[k][v], H[v], bb[k][v]);
         }
@@ -271,10 +362,9 @@ gated_scan_kernel(const IO *__restrict__ x, const IO *__restrict__ r, const IO *
     __syncthreads();
 
     // 2. the chunk's map, the state at its start, the state at its end
+    const bool ends = c == nlive - 1;
+    float start[V] = {}, out[V];
     if (w == 0) {
-        float in[V];
-        uint64_t *word = words + ((int64_t)b * nchunk + c) * D + d;
-        const bool ends = c == nlive - 1;
 #pragma unroll
         for (int k = 1; k < K; ++k)
 #pragma unroll
@@ -283,28 +373,23 @@ gated_scan_kernel(const IO *__restrict__ x, const IO *__restrict__ r, const IO *
                 H[v] = fmaf(p, H[v], s_H[k][lane * V + v]);
                 P[v] *= p;
             }
-        if (c == 0) {
+        // (read before anything is published: the chain's last item may write last_state over it)
+        if (c == 0 && h0) {
 #pragma unroll
-            for (int v = 0; v < V; ++v) in[v] = h0 ? h0[(int64_t)b * D + d + v] : 0.0f;
-        } else {
-            if (act && !ends) {
-#pragma unroll
-                for (int v = 0; v < V; ++v) chain_put(word + v, P[v], H[v]);
-            }
-            chain_get<V>(words + (int64_t)b * nchunk * D + d, D, c - 1, -1, 0, act, in);
-        }
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const float out = fmaf(P[v], in[v], H[v]);
-            s_in[lane * V + v] = in[v];
-            if (act) {
-                if (!ends) chain_put(word + v, -1.0f, out);
-                else if (OUT && last) last[(int64_t)b * D + d + v] = out;
-            }
+            for (int v = 0; v < V; ++v) start[v] = h0[(int64_t)b * D + d + v];
         }
     }
-    if constexpr (OUT) {
-        __syncthreads();
+    chain_step<V>(words + (int64_t)b * nitem * D + d, D, c, ends, act, lane, w, P, H, start, s_map,
+                  s_in, out);
+    float *st = states ? states + ((int64_t)b * nchunk + c * M) * D + d : nullptr;   // the item's states
+    if (w == 0 && act) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            if (ends && OUT && last) last[(int64_t)b * D + d + v] = out[v];
+            if (!ends && st) st[(M - 1) * D + v] = out[v];
+        }
+    }
+    if constexpr (OUT || M > 1) {
         // 3. the state at the wave's start, and its tokens from there
         float h[V];
 #pragma unroll
@@ -312,40 +397,51 @@ gated_scan_kernel(const IO *__restrict__ x, const IO *__restrict__ r, const IO *
         for (int k = 0; k < w; ++k)
 #pragma unroll
             for (int v = 0; v < V; ++v) h[v] = fmaf(s_P[k][lane * V + v], h[v], s_H[k][lane * V + v]);
+        if constexpr (M > 1) {   // the states inside the item
+            const int j = w / (K / M);
+            if (st && j > 0 && w % (K / M) == 0 && act && (int64_t)(c * M + j) * kGatedChunk < Lb) {
 #pragma unroll
-        for (int k = 0; k < T; ++k) {
-            float o[V];
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                h[v] = fmaf(a[k][v], h[v], bb[k][v]);
-                o[v] = z ? h[v] * silu_f32(rz[k].get(v)) : h[v];
-                if (t0 + k >= Lb) o[v] = 0.0f;
+                for (int v = 0; v < V; ++v) st[(j - 1) * D + v] = h[v];
             }
-            if (act && t0 + k < L) Row::store(y + (row0 + t0 + k) * D + d, o);
+        }
+        if constexpr (OUT) {
+#pragma unroll
+            for (int k = 0; k < T; ++k) {
+                float o[V];
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+                    h[v] = fmaf(a[k][v], h[v], bb[k][v]);
+                    o[v] = z ? h[v] * silu_f32(rz[k].get(v)) : h[v];
+                    if (t0 + k >= Lb) o[v] = 0.0f;
+                }
+                if (act && t0 + k < L) Row::store(y + (row0 + t0 + k) * D, lofs, o);
+            }
         }
     }
 }
 
 // The gradients.  lambda_t = dh_t + G_t with G_t = a_{t+1} lambda_{t+1}, dh_t = dy_t silu(z_t), is
 // the same kind of recurrence run from the end (the map of a span is G -> P G + H' with the same
-// P), so the items and the chain are the forward's in the other order; the states come from the
-// words that the forward left (the state at the end of every chunk).  Each wave forms both maps of
+// P), so the items and the chain are the forward's in the other order; the states come from
+// the array that the forward left (the state at the end of every chunk).  Each wave forms both maps of
 // its tokens, then walks them forwards for the states and backwards for the gradients.  The
 // coefficients that cost transcendentals (both sigmoids, the decay) stay in registers in between;
 // 1 - a^2 is formed again.  dA's share of the item goes to part[item], summed afterwards in order.
-template <typename IO, int V>
+template <typename IO, int V, bool GATE>
 __global__ void __launch_bounds__(64 * kGatedWaves)
+__attribute__((amdgpu_waves_per_eu(4)))
 gated_bwd_kernel(const IO *__restrict__ x, const IO *__restrict__ r, const IO *__restrict__ g,
                  const float *__restrict__ A, const IO *__restrict__ z, const float *__restrict__ h0,
                  const int32_t *__restrict__ seq_lens, const IO *__restrict__ dy, const float *__restrict__ dlast,
-                 const uint64_t *__restrict__ states, IO *__restrict__ dx, IO *__restrict__ dr, IO *__restrict__ dg,
+                 const float *__restrict__ states, IO *__restrict__ dx, IO *__restrict__ dr, IO *__restrict__ dg,
                  IO *__restrict__ dz, float *__restrict__ part, float *__restrict__ dh0, uint64_t *words,
-                 int *counters, int64_t L, int64_t D, int tiles, int chains, int nchunk) {
+                 int *counters, int64_t L, int64_t D, int tiles, int chains, int nchunk, int run) {
     constexpr int T = kGatedRows, K = kGatedWaves, C = kGatedChunk;
     using Row = row_words<V, IO>;
     __shared__ float s_P[K][64 * V], s_H[K][64 * V], s_G[K][64 * V], s_in[64 * V];
+    __shared__ uint64_t s_map[kGatedGroup][64 * V];
     __shared__ int s_slot;
-    const GatedItem it = gated_item(chains, nchunk, counters, &s_slot);
+    const GatedItem it = gated_item(chains, nchunk, counters, run, &s_slot);
     if (it.chain < 0) return;
     const int b = it.chain / tiles, c = nchunk - 1 - it.pos;
     const int lane = threadIdx.x & 63;
@@ -353,6 +449,7 @@ gated_bwd_kernel(const IO *__restrict__ x, const IO *__restrict__ r, const IO *_
     const int64_t dl = (int64_t)(it.chain - b * tiles) * 64 * V + lane * V;
     const bool act = dl < D;
     const int64_t d = min(dl, D - V);
+    const uint32_t lofs = (uint32_t)d * (uint32_t)sizeof(IO);
     const int64_t Lb = seq_lens ? min((int64_t)max(seq_lens[b], 0), L) : L;
     const int64_t t0 = (int64_t)c * C + w * T;
     const int64_t row0 = (int64_t)b * L;
@@ -364,11 +461,11 @@ gated_bwd_kernel(const IO *__restrict__ x, const IO *__restrict__ r, const IO *_
         if (act) {
             const float zero[V] = {};
             for (int64_t t = t0; t < min(t0 + T, L); ++t) {
-                const int64_t e = (row0 + t) * D + d;
-                Row::store(dx + e, zero);
-                Row::store(dr + e, zero);
-                Row::store(dg + e, zero);
-                if (z) Row::store(dz + e, zero);
+                const int64_t e = (row0 + t) * D;
+                Row::store(dx + e, lofs, zero);
+                Row::store(dr + e, lofs, zero);
+                Row::store(dg + e, lofs, zero);
+                if constexpr (GATE) Row::store(dz + e, lofs, zero);
             }
             if (w == 0)
                 for (int v = 0; v < V; ++v) {
@@ -379,25 +476,38 @@ gated_bwd_kernel(const IO *__restrict__ x, const IO *__restrict__ r, const IO *_
         return;
     }
 
-    Row rr[T], rg[T], rx[T], ry[T], rz[T];
+    Row rr[T], rg[T], rx[T], ry[T], rz[GATE ? T : 1];
 #pragma unroll
     for (int k = 0; k < T; ++k) {
-        const int64_t e = (row0 + min(t0 + k, Lb - 1)) * D + d;
-        rr[k].load(r + e);
-        rg[k].load(g + e);
-        rx[k].load(x + e);
-        ry[k].load(dy + e);
+        const int64_t e = (row0 + min(t0 + k, Lb - 1)) * D;
+        rr[k].load(r + e, lofs);
+        rg[k].load(g + e, lofs);
+        rx[k].load(x + e, lofs);
+        ry[k].load(dy + e, lofs);
     }
-    if (z) {
+    if constexpr (GATE) {
 #pragma unroll
-        for (int k = 0; k < T; ++k) rz[k].load(z + (row0 + min(t0 + k, Lb - 1)) * D + d);
+        for (int k = 0; k < T; ++k) rz[k].load(z + (row0 + min(t0 + k, Lb - 1)) * D, lofs);
     }
     float Ad[V], h[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
         Ad[v] = A[d + v];
-        // the state at the chunk's start (the low half of the word of the chunk before it)
-        h[v] = c == 0 ? (h0 ? h0[ch + v] : 0.0f) : __uint_as_float((uint32_t)states[item - D + v]);
+        // the state at the chunk's start
+        h[v] = c == 0 ? (h0 ? h0[ch + v] : 0.0f) : states[item - D + v];
+    }
+
+    // Tokens past the end become the identity, and their gradients zero, without a test per value below.
+    if (t0 + T > Lb) {
+#pragma unroll
+        for (int k = 0; k < T; ++k)
+            if (t0 + k >= Lb) {
+                rr[k].fill(minus_inf_words<IO>());
+                rg[k].fill(0);
+                rx[k].fill(0);
+                ry[k].fill(0);
+                if constexpr (GATE) rz[k].fill(0);
+            }
     }
 
     // 1. the coefficients and the wave's two maps
@@ -405,27 +515,32 @@ gated_bwd_kernel(const IO *__restrict__ x, const IO *__restrict__ r, const IO *_
 #pragma unroll
     for (int v = 0; v < V; ++v) P[v] = 1.0f, H[v] = 0.0f, G[v] = 0.0f;
 #pragma unroll
-    for (int k = 0; k < T; ++k) {
-        const bool live = t0 + k < Lb;
+    for (int k = 0; k < T; ++k)
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            const GatedCoeff cf = gated_coeff(rr[k].get(v), rg[k].get(v), Ad[v] * kLog2e);
+            const GatedCoeff cf = gated_coeff<IO>(rr[k].get(v), rg[k].get(v), Ad[v] * kLog2e);
             s[k][v] = cf.s;
             i[k][v] = cf.i;
-            a[k][v] = live ? cf.a : 1.0f;
-            bb[k][v] = live ? __builtin_amdgcn_sqrtf(cf.q) * cf.i * rx[k].get(v) : 0.0f;
-            P[v] *= a[k][v];
-            H[v] = fmaf(a[k][v], H[v], bb[k][v]);
+            a[k][v] = cf.a;
+            bb[k][v] = __builtin_amdgcn_sqrtf(cf.q) * cf.i * rx[k].get(v);
+            P[v] *= cf.a;
+            H[v] = fmaf(cf.a, H[v], bb[k][v]);
         }
-    }
-    auto grad_in = [&](int k, int v) {   // dh_t
+    // dh_t, and with a gate the factor of h_t in dz: silu(z) = z sz, silu'(z) = sz (1 + z (1 - sz))
+    auto grad_in = [&](int k, int v, float &dzh) {
         const float dyv = ry[k].get(v);
-        return t0 + k < Lb ? (z ? dyv * silu_f32(rz[k].get(v)) : dyv) : 0.0f;
+        if constexpr (!GATE) return dyv;
+        const float zz = rz[GATE ? k : 0].get(v), sz = sigmoid_f32(zz), g = zz * sz;
+        dzh = dyv * fmaf(g, 1.0f - sz, sz);
+        return dyv * g;
     };
 #pragma unroll
     for (int k = T - 1; k >= 0; --k)
 #pragma unroll
-        for (int v = 0; v < V; ++v) G[v] = a[k][v] * (grad_in(k, v) + G[v]);
+        for (int v = 0; v < V; ++v) {
+            float dzh;
+            G[v] = a[k][v] * (grad_in(k, v, dzh) + G[v]);
+        }
 #pragma unroll
     for (int v = 0; v < V; ++v) {
         s_P[w][lane * V + v] = P[v];
@@ -435,45 +550,46 @@ gated_bwd_kernel(const IO *__restrict__ x, const IO *__restrict__ r, const IO *_
     __syncthreads();
 
     // 2. the adjoint at the chunk's end, and the one that it hands on
-    if (w == 0) {
-        float in[V], PC[V], GC[V];
-        const bool starts = c == nlive - 1;
+    const bool starts = c == nlive - 1;
+    float start[V] = {}, out[V];
+    if (w == 0) {   // the chunk's map (over P and G, which wave 0 needs no more)
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            PC[v] = s_P[K - 1][lane * V + v];
-            GC[v] = s_G[K - 1][lane * V + v];
+            P[v] = s_P[K - 1][lane * V + v];
+            G[v] = s_G[K - 1][lane * V + v];
         }
 #pragma unroll
         for (int k = K - 2; k >= 0; --k)
 #pragma unroll
             for (int v = 0; v < V; ++v) {
                 const float p = s_P[k][lane * V + v];
-                GC[v] = fmaf(p, GC[v], s_G[k][lane * V + v]);
-                PC[v] *= p;
+                G[v] = fmaf(p, G[v], s_G[k][lane * V + v]);
+                P[v] *= p;
             }
-        if (starts) {
+        if (starts && dlast) {
 #pragma unroll
-            for (int v = 0; v < V; ++v) in[v] = dlast ? dlast[ch + v] : 0.0f;
-        } else {
-            if (act && c > 0) {
-#pragma unroll
-                for (int v = 0; v < V; ++v) chain_put(words + item + v, PC[v], GC[v]);
-            }
-            chain_get<V>(words + (int64_t)b * nchunk * D + d, D, c + 1, 1, nlive - 1, act, in);
-        }
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const float out = fmaf(PC[v], in[v], GC[v]);
-            s_in[lane * V + v] = in[v];
-            if (act) {
-                if (c > 0) chain_put(words + item + v, -1.0f, out);
-                else if (dh0) dh0[ch + v] = out;
-            }
+            for (int v = 0; v < V; ++v) start[v] = dlast[ch + v];
         }
     }
-    __syncthreads();
+    chain_step<V>(words + ((int64_t)b * nchunk + nlive - 1) * D + d, -D, nlive - 1 - c, c == 0, act, lane, w, P, G,
+                  start, s_map, s_in, out);
+    if (w == 0 && act && c == 0 && dh0) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) dh0[ch + v] = out[v];
+    }
 
-    // 3. the states before the wave's tokens (over bb), the adjoint after its last, the gradients
+    // 3. the states before the wave's tokens (over bb), the adjoint after its last, the gradients.
+    // What follows is computed from the registers named here alone: without this the compiler keeps
+    // what it derived from them above (1 - a^2, widened inputs), more registers than four waves
+    // per SIMD leave a lane.
+#pragma unroll
+    for (int k = 0; k < T; ++k) {
+        rx[k].opaque();
+        ry[k].opaque();
+        if constexpr (GATE) rz[k].opaque();
+#pragma unroll
+        for (int v = 0; v < V; ++v) asm volatile("" : "+v"(s[k][v]), "+v"(i[k][v]), "+v"(a[k][v]));
+    }
     for (int k = 0; k < w; ++k)
 #pragma unroll
         for (int v = 0; v < V; ++v) h[v] = fmaf(s_P[k][lane * V + v], h[v], s_H[k][lane * V + v]);
@@ -497,37 +613,30 @@ gated_bwd_kernel(const IO *__restrict__ x, const IO *__restrict__ r, const IO *_
 #pragma unroll
     for (int k = T - 1; k >= 0; --k) {
         float ox[V], og[V], orr[V], oz[V];
-        const bool live = t0 + k < Lb;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            const float xv = rx[k].get(v), dyv = ry[k].get(v);
-            float dh = dyv;
-            if (z) {   // silu(z) = z sz, silu'(z) = sz (1 + z (1 - sz))
-                const float zz = rz[k].get(v), sz = sigmoid_f32(zz);
-                oz[v] = live ? dyv * hT[v] * (sz * fmaf(zz, 1.0f - sz, 1.0f)) : 0.0f;
-                dh *= zz * sz;
-            }
-            const float lam = live ? dh + G[v] : G[v];
+            float dzh = 0.0f;
+            const float lam = grad_in(k, v, dzh) + G[v];
+            if constexpr (GATE) oz[v] = dzh * hT[v];
             G[v] = a[k][v] * lam;
-            const float q = one_minus_square(Ad[v] * kLog2e * s[k][v], a[k][v]);
+            const float q = one_minus_square<IO>(Ad[v] * kLog2e * s[k][v], a[k][v]);
             // 1 / beta; where 1 - a^2 is zero (or below what the unit resolves) the terms with it are dropped
             const float rb = fabsf(q) < FLT_MIN ? 0.0f : __builtin_amdgcn_rsqf(q);
-            const float ix = i[k][v] * xv;
-            const float lb = lam * (q * rb);             // lambda beta
-            const float dla = fmaf(G[v], bb[k][v], -(lam * ix) * (a[k][v] * a[k][v] * rb));
-            const float ds = live ? dla * s[k][v] : 0.0f;
+            ox[v] = lam * (q * rb) * i[k][v];            // lambda beta i
+            const float t = ox[v] * rx[k].get(v);        // lambda beta i x
+            og[v] = fmaf(-t, i[k][v], t);
+            const float e = a[k][v] * rb;                // i x a^2 / beta = beta i x (a / beta)^2
+            const float ds = fmaf(-t, e * e, G[v] * bb[k][v]) * s[k][v];
             dA[v] += ds;
-            orr[v] = ds * (Ad[v] * (1.0f - s[k][v]));
-            ox[v] = live ? lb * i[k][v] : 0.0f;
-            og[v] = live ? lb * ix * (1.0f - i[k][v]) : 0.0f;
+            orr[v] = ds * fmaf(-Ad[v], s[k][v], Ad[v]);
             hT[v] = bb[k][v];
         }
         if (act && t0 + k < L) {
-            const int64_t e = (row0 + t0 + k) * D + d;
-            Row::store(dx + e, ox);
-            Row::store(dr + e, orr);
-            Row::store(dg + e, og);
-            if (z) Row::store(dz + e, oz);
+            const int64_t e = (row0 + t0 + k) * D;
+            Row::store(dx + e, lofs, ox);
+            Row::store(dr + e, lofs, orr);
+            Row::store(dg + e, lofs, og);
+            if constexpr (GATE) Row::store(dz + e, lofs, oz);
         }
     }
     __syncthreads();   // (the maps are read)
@@ -573,7 +682,7 @@ gated_step_kernel(float *__restrict__ state, const IO *__restrict__ x, const IO 
                   IO *__restrict__ y, int64_t n, int64_t D) {
     const int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x;
     if (e >= n) return;
-    const GatedCoeff cf = gated_coeff(io<IO>::ld(r, e), io<IO>::ld(g, e), A[e % D] * kLog2e);
+    const GatedCoeff cf = gated_coeff<IO>(io<IO>::ld(r, e), io<IO>::ld(g, e), A[e % D] * kLog2e);
     const float h = fmaf(cf.a, state[e], __builtin_amdgcn_sqrtf(cf.q) * cf.i * io<IO>::ld(x, e));
     state[e] = h;
     io<IO>::st(y, e, z ? h * silu_f32(io<IO>::ld(z, e)) : h);
