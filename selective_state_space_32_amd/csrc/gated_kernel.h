@@ -19,7 +19,7 @@
 // The inputs are read once and the outputs written once, whatever the length.
 //
 // The chain.  Handing the state from chunk to chunk would cost a round trip through memory per chunk,
-// so the chunks of a chain form groups of kGatedGroup.  word[sequence][item][channel] is 64 bits: a
+// so with few chains the chunks of a chain form groups of up to kGatedGroup (the host chooses).  word[sequence][item][channel] is 64 bits: a
 // chunk publishes its map (P, H), two floats, as soon as it has it; the last chunk of a group
 // publishes instead the state at its end, as (-1, h), once it knows it.  A chunk fetches the maps of
 // the chunks before it in its group (which wait for nobody), composes them, and applies them to the
@@ -48,7 +48,7 @@ namespace ssm {
 constexpr int kGatedRows = 8;                            // tokens per wave
 constexpr int kGatedWaves = 8;                           // waves per workgroup
 constexpr int kGatedChunk = kGatedRows * kGatedWaves;    // tokens per stored state (and per item of the backward)
-constexpr int kGatedGroup = 8;                           // chunks of a chain that share a hand-over
+constexpr int kGatedGroup = 8;                           // most items of a chain that share a hand-over
 constexpr int kGatedQueues = 8;                          // counters (one per XCD)
 constexpr int kGatedCounterStride = 64;                  // ints between them: lines of their own
 
@@ -150,14 +150,14 @@ __device__ __forceinline__ uint64_t chain_read(const uint64_t *w) {
 // at position 0's start (both read in wave 0 only; 0 at other positions), `ends`: nobody comes after.  Leaves the state at
 // the item's start in s_in (behind a barrier) and the one at its end in wave 0's `out`.
 template <int V>
-__device__ __forceinline__ void chain_step(uint64_t *base, int64_t stride, int pos, bool ends, bool act, int lane,
+__device__ __forceinline__ void chain_step(uint64_t *base, int64_t stride, int pos, int group, bool ends, bool act, int lane,
                                            int w, const float (&P)[V], const float (&H)[V], const float (&start)[V],
                                            uint64_t (&s_map)[kGatedGroup][64 * V], float (&s_in)[64 * V],
                                            float (&out)[V]) {
     static_assert(kGatedGroup <= kGatedWaves, "a wave fetches a map");
-    const int g = pos % kGatedGroup;
+    const int g = pos % group;
     uint64_t *own = base + pos * stride;
-    if (w == 0 && act && !ends && g != kGatedGroup - 1) {
+    if (w == 0 && act && !ends && g != group - 1) {
 #pragma unroll
         for (int v = 0; v < V; ++v)
             if (pos == 0) chain_put(own + v, 0.0f, fmaf(P[v], start[v], H[v]));
@@ -214,7 +214,7 @@ __device__ __forceinline__ void chain_step(uint64_t *base, int64_t stride, int p
         for (int v = 0; v < V; ++v) {
             in[v] = fmaf(cp[v], in[v], ch[v]);
             out[v] = fmaf(P[v], in[v], H[v]);
-            if (act && !ends && g == kGatedGroup - 1) chain_put(own + v, -1.0f, out[v]);
+            if (act && !ends && g == group - 1) chain_put(own + v, -1.0f, out[v]);
             s_in[lane * V + v] = in[v];
         }
     }
@@ -242,12 +242,14 @@ __device__ __forceinline__ GatedItem gated_item(int chains, int nitem, int *coun
     return {(n - pos * nq) * kGatedQueues + q, pos};
 }
 
-// Fills the chain's words with ones and clears the counters behind them.
+// Fills the chain's words with ones (n 16-byte pairs of them: the array is padded) and clears the
+// counters behind them.
 static __global__ void __launch_bounds__(256)
-gated_clear_kernel(uint64_t *__restrict__ words, int64_t n, int *__restrict__ counters) {
+gated_clear_kernel(u32x4_t *__restrict__ words, int64_t n, u32x4_t *__restrict__ counters) {
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (i < n) words[i] = ~uint64_t(0);
-    else if (i - n < kGatedQueues * kGatedCounterStride) counters[i - n] = 0;
+    const u32x4_t ones = {~0u, ~0u, ~0u, ~0u}, zeros = {0, 0, 0, 0};
+    if (i < n) words[i] = ones;
+    else if (i - n < kGatedQueues * kGatedCounterStride / 4) counters[i - n] = zeros;
 }
 
 // A token's coefficients for one channel.
@@ -268,15 +270,15 @@ __device__ __forceinline__ GatedCoeff gated_coeff(float r, float g, float a2) {
 // OUT: y and last_state are written; otherwise only the states.  states (nullable): the state at the
 // end of every kGatedChunk tokens but a sequence's last, for the backward pass.
 // M: the tokens of an item in units of kGatedChunk.
-template <typename IO, int V, int M, bool OUT>
-__global__ void __launch_bounds__(64 * kGatedWaves)
+template <typename IO, int V, int T, int K, bool OUT>
+__global__ void __launch_bounds__(64 * K)
 gated_scan_kernel(const IO *__restrict__ x, const IO *__restrict__ r, const IO *__restrict__ g,
                   const float *__restrict__ A, const IO *__restrict__ z, const float *h0,
                   const int32_t *__restrict__ seq_lens, IO *__restrict__ y, float *last,
                   float *__restrict__ states, uint64_t *words, int *counters, int64_t L, int64_t D, int tiles, int chains, int nitem, int nchunk,
-                  int run) {
-    constexpr int T = M * kGatedRows, K = kGatedWaves, C = M * kGatedChunk;
-    static_assert(K % M == 0, "a stored state is at a wave's end");
+                  int run, int group) {
+    constexpr int C = T * K, M = C / kGatedChunk;
+    static_assert(C % kGatedChunk == 0 && K % M == 0, "a stored state is at a wave's end");
     using Row = row_words<V, IO>;
     __shared__ float s_P[K][64 * V], s_H[K][64 * V], s_in[64 * V];
     __shared__ uint64_t s_map[kGatedGroup][64 * V];
@@ -318,12 +320,6 @@ gated_scan_kernel(const IO *__restrict__ x, const IO *__restrict__ r, const IO *
         rg[k].load(g + e, lofs);
         rx[k].load(x + e, lofs);
     }
-    if constexpr (OUT) {
-        if (z) {
-#pragma unroll
-            for (int k = 0; k < T; ++k) rz[k].load(z + (row0 + min(t0 + k, Lb - 1)) * D, lofs);
-        }
-    }
     float a2[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) a2[v] = A[d + v] * kLog2e;
@@ -359,6 +355,13 @@ gated_scan_kernel(const IO *__restrict__ x, const IO *__restrict__ r, const IO *
         s_P[w][lane * V + v] = P[v];
         s_H[w][lane * V + v] = H[v];
     }
+    // (the gate is requested here: it is needed last, and comes while the chain is waited for)
+    if constexpr (OUT) {
+        if (z) {
+#pragma unroll
+            for (int k = 0; k < T; ++k) rz[k].load(z + (row0 + min(t0 + k, Lb - 1)) * D, lofs);
+        }
+    }
     __syncthreads();
 
     // 2. the chunk's map, the state at its start, the state at its end
@@ -379,7 +382,7 @@ gated_scan_kernel(const IO *__restrict__ x, const IO *__restrict__ r, const IO *
             for (int v = 0; v < V; ++v) start[v] = h0[(int64_t)b * D + d + v];
         }
     }
-    chain_step<V>(words + (int64_t)b * nitem * D + d, D, c, ends, act, lane, w, P, H, start, s_map,
+    chain_step<V>(words + (int64_t)b * nitem * D + d, D, c, group, ends, act, lane, w, P, H, start, s_map,
                   s_in, out);
     float *st = states ? states + ((int64_t)b * nchunk + c * M) * D + d : nullptr;   // the item's states
     if (w == 0 && act) {
@@ -435,7 +438,7 @@ gated_bwd_kernel(const IO *__restrict__ x, const IO *__restrict__ r, const IO *_
                  const int32_t *__restrict__ seq_lens, const IO *__restrict__ dy, const float *__restrict__ dlast,
                  const float *__restrict__ states, IO *__restrict__ dx, IO *__restrict__ dr, IO *__restrict__ dg,
                  IO *__restrict__ dz, float *__restrict__ part, float *__restrict__ dh0, uint64_t *words,
-                 int *counters, int64_t L, int64_t D, int tiles, int chains, int nchunk, int run) {
+                 int *counters, int64_t L, int64_t D, int tiles, int chains, int nchunk, int run, int group) {
     constexpr int T = kGatedRows, K = kGatedWaves, C = kGatedChunk;
     using Row = row_words<V, IO>;
     __shared__ float s_P[K][64 * V], s_H[K][64 * V], s_G[K][64 * V], s_in[64 * V];
@@ -571,7 +574,7 @@ gated_bwd_kernel(const IO *__restrict__ x, const IO *__restrict__ r, const IO *_
             for (int v = 0; v < V; ++v) start[v] = dlast[ch + v];
         }
     }
-    chain_step<V>(words + ((int64_t)b * nchunk + nlive - 1) * D + d, -D, nlive - 1 - c, c == 0, act, lane, w, P, G,
+    chain_step<V>(words + ((int64_t)b * nchunk + nlive - 1) * D + d, -D, nlive - 1 - c, group, c == 0, act, lane, w, P, G,
                   start, s_map, s_in, out);
     if (w == 0 && act && c == 0 && dh0) {
 #pragma unroll
@@ -664,6 +667,7 @@ column_sum_kernel(const float *__restrict__ part, float *__restrict__ out, int64
     const int64_t d = (int64_t)blockIdx.x * 64 + lane;
     float s = 0.0f;
     if (d < D)
+#pragma unroll 8
         for (int64_t k = w; k < n; k += kColumnWaves) s += part[k * D + d];
     red[w][lane] = s;
     __syncthreads();

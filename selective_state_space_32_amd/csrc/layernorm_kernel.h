@@ -314,7 +314,7 @@ layernorm_wgrad_sum_kernel(const float *__restrict__ pw, const float *__restrict
     const int64_t d = (int64_t)blockIdx.x * 64 + lane;
     float a = 0.0f, b = 0.0f;
     if (d < D) {
-#pragma unroll 4
+#pragma unroll 8
         for (int64_t k = w; k < n; k += kNormSumWaves) {
             a += pw[k * D + d];
             b += pb[k * D + d];
