@@ -430,7 +430,7 @@ SSMSCAN_API int ssm_step_act(float *state, const void *u, const void *delta, con
  *   h_t     = a_t h_{t-1} + sqrt(1 - a_t^2) * sigmoid(g_t) * x_t
  *   y_t     = h_t * silu(z_t)                       (z optional: without it y_t = h_t)
  *   x, r, g, z, y : [batch][seqlen][dim] (io_dtype); z may be NULL (no gate)
- *   A             : [dim] fp32, the logarithm of the decay at an open gate: A <= 0 (not checked;
+ *   A             : [dim] fp32, the logarithm of the decay at an open gate: finite, A <= 0 (not checked;
  *                   A > 0 gives NaN, A = 0 a state that ignores its input)
  *   initial_state : [batch][dim] fp32, or NULL (= zero).  It may be the last_state buffer (the
  *                   state advanced in place)
@@ -444,8 +444,10 @@ SSMSCAN_API int ssm_step_act(float *state, const void *u, const void *delta, con
  *                   when that is 0); its contents on entry do not matter.  After the call it
  *                   holds the states that ssm_gated_scan_bwd takes as checkpoints
  * Arithmetic and states are fp32; 1 - a^2 is formed without cancellation where a is near 1.
- * dims->dstate and dims->chunk_len are ignored; seqlen is at most 2^30.  Returns SSM_OK or a
- * negative ssm_status (nothing is launched on an error). */
+ * dims->dstate and dims->chunk_len are ignored; dim is at most 2^27, seqlen at most 2^30, and
+ * batch * ceil(dim / 64), rounded up to a multiple of 8, times ceil(seqlen / 64) below 2^23 - 64 (the
+ * work items of a launch; SSM_ERR_SHAPE may follow above that).
+ * Returns SSM_OK or a negative ssm_status (nothing is launched on an error). */
 SSMSCAN_API int ssm_gated_scan_fwd(const void *x, const void *r, const void *g, const float *A, const void *z,
                 const float *initial_state, const int32_t *seq_lens, void *y, float *last_state,
                 const ssm_dims *dims, void *workspace, size_t workspace_bytes, void *stream);
@@ -506,7 +508,9 @@ SSMSCAN_API int ssm_gated_step(float *state, const void *x, const void *r, const
  *                   residual stream advanced in place)
  *   mean, rstd    : [batch * seqlen] fp32 outputs for the backward pass, each may be NULL
  *   eps           : >= 0 and finite (SSM_ERR_VALUE otherwise)
- * dims->dstate and dims->chunk_len are ignored.  Returns SSM_OK or a negative ssm_status. */
+ * Outputs must not overlap inputs or each other otherwise.  dims->dstate and dims->chunk_len are
+ * ignored; at most 2^31 - 1 rows of at most 2^27 values.  Returns SSM_OK or a negative
+ * ssm_status. */
 SSMSCAN_API int ssm_layernorm_fwd(const void *x, const void *residual, const float *weight, const float *bias,
                 float eps, int flags, void *y, void *sum, float *mean, float *rstd, const ssm_dims *dims,
                 void *stream);
@@ -523,8 +527,8 @@ SSMSCAN_API int ssm_layernorm_fwd(const void *x, const void *residual, const flo
  *   dweight, dbias: [dim] fp32 outputs, each may be NULL (not wanted)
  *   workspace     : at least ssm_layernorm_bwd_workspace_bytes(dims) bytes, 16-byte aligned; may be
  *                   NULL when neither dweight nor dbias is wanted
- * ds may be the dresidual buffer.  The sums over rows have a fixed order: the results are the same
- * from run to run.  Returns SSM_OK or a negative ssm_status. */
+ * ds may be the dresidual buffer; outputs must not overlap inputs or each other otherwise.  The
+ * sums over rows have a fixed order: the results are the same from run to run.  Returns SSM_OK or a negative ssm_status. */
 SSMSCAN_API int ssm_layernorm_bwd(const void *dy, const void *s, const float *weight, const float *mean,
                 const float *rstd, const void *dresidual, int flags, void *ds, void *dx, float *dweight,
                 float *dbias, const ssm_dims *dims, void *workspace, size_t workspace_bytes, void *stream);

@@ -21,10 +21,10 @@ int check_gated_dims(const ssm_dims *dm, bool seq) {
                     (long long)dm->seqlen, (long long)dm->dim);
     if (dm->io_dtype != SSM_IO_F32 && dm->io_dtype != SSM_IO_BF16)
         return fail(SSM_ERR_DTYPE, "io_dtype %d is not SSM_IO_F32 (0) or SSM_IO_BF16 (1)", dm->io_dtype);
-    if (dm->dim > kMaxDim / 2 || dm->batch > kMaxDim)   // (a row's bytes are addressed with 32 bits)
-        return fail(SSM_ERR_SHAPE, "dim larger than 2^29 or batch larger than 2^30");
-    if (dm->batch > 0 && dm->dim > (int64_t(1) << 36) / dm->batch)
-        return fail(SSM_ERR_SHAPE, "batch*dim exceeds 2^36 (grid size)");
+    if (dm->dim > kMaxDim / 8 || dm->batch > kMaxDim)   // (the column sums launch 16 threads per column)
+        return fail(SSM_ERR_SHAPE, "dim larger than 2^27 or batch larger than 2^30");
+    if (dm->batch > 0 && dm->dim > (int64_t(1) << 33) / dm->batch)
+        return fail(SSM_ERR_SHAPE, "batch*dim exceeds 2^33 (grid size)");
     if (seq && (dm->seqlen > kMaxDim ||
                 (dm->batch > 0 && dm->dim > 0 && dm->seqlen > kMaxElems / dm->batch / dm->dim)))
         return fail(SSM_ERR_SHAPE, "seqlen exceeds 2^30 or batch*seqlen*dim exceeds 2^46 elements");
@@ -84,9 +84,11 @@ int64_t grid_of(const Plan &p, int64_t nitem) {
     return (per + run - 1) / run * run * ssm::kGatedQueues;   // (per: items of the longest queue)
 }
 
+// A launch holds fewer than 2^32 threads.
 int check_items(const Plan &p) {
-    if (p.chains > (int64_t(1) << 31) - ssm::kGatedQueues || grid_of(p, p.nchunk) > (int64_t(1) << 31) - 1)
-        return fail(SSM_ERR_SHAPE, "batch * ceil(dim / %d) * ceil(seqlen / %d) exceeds 2^31 work items", 64 * p.V,
+    constexpr int64_t most = ((int64_t(1) << 32) - 1) / (64 * ssm::kGatedWaves);
+    if (p.chains > most || grid_of(p, p.nchunk) > most)
+        return fail(SSM_ERR_SHAPE, "batch * ceil(dim / %d) * ceil(seqlen / %d) exceeds 2^23 work items", 64 * p.V,
                     ssm::kGatedChunk);
     return SSM_OK;
 }
@@ -260,7 +262,7 @@ int ssm_gated_step(float *state, const void *x, const void *r, const void *g, co
     if (!state || !x || !r || !g || !A || !y) return fail(SSM_ERR_NULL, "required pointer is NULL");
     hipStream_t st = static_cast<hipStream_t>(stream);
     const int64_t n = dims->batch * dims->dim;
-    const dim3 grid((unsigned)((n + 255) / 256));
+    const dim3 grid((unsigned)((n + 256 * ssm::kStepVec - 1) / (256 * ssm::kStepVec)));
     if (es == 2)
         hipLaunchKernelGGL(ssm::gated_step_kernel<uint16_t>, grid, dim3(256), 0, st, state,
                            static_cast<const uint16_t *>(x), static_cast<const uint16_t *>(r),

@@ -229,6 +229,7 @@ struct GatedItem {
 __device__ __forceinline__ GatedItem gated_item(int chains, int nitem, int *counters, int run, int *slot) {
     const int q = (int)blockIdx.x / run % kGatedQueues;
     const int nq = (chains - q + kGatedQueues - 1) / kGatedQueues;
+    if (nq <= 0) return {-1, 0};
     int n = (int)blockIdx.x / (run * kGatedQueues) * run + (int)blockIdx.x % run;
     if (counters) {   // (one item per sequence: no chain, any order will do)
         if (threadIdx.x == 0)
@@ -237,7 +238,7 @@ __device__ __forceinline__ GatedItem gated_item(int chains, int nitem, int *coun
         __syncthreads();
         n = __builtin_amdgcn_readfirstlane(*slot);
     }
-    if (nq <= 0 || n >= nq * nitem) return {-1, 0};
+    if (n >= nq * nitem) return {-1, 0};
     const int pos = n / nq;
     return {(n - pos * nq) * kGatedQueues + q, pos};
 }
@@ -678,18 +679,54 @@ column_sum_kernel(const float *__restrict__ part, float *__restrict__ out, int64
     }
 }
 
-// One token of every sequence, the state updated in place.
+// One token of every sequence, the state updated in place.  The tensors are walked as flat arrays,
+// kStepVec neighbouring elements per thread (they may lie in two rows; A's index wraps with them).
+// Bound: HBM, 8 bytes of state and 4 or 5 I/O elements per channel (S256 D5120 bf16 with its gate:
+// 23.6 MB, STEPUS us).  The state is left in the caches for the next token.
+constexpr int kStepVec = 4;
 template <typename IO>
 __global__ void __launch_bounds__(256)
 gated_step_kernel(float *__restrict__ state, const IO *__restrict__ x, const IO *__restrict__ r,
                   const IO *__restrict__ g, const float *__restrict__ A, const IO *__restrict__ z,
                   IO *__restrict__ y, int64_t n, int64_t D) {
-    const int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    typedef float any_f32 __attribute__((ext_vector_type(kStepVec), aligned(sizeof(float))));
+    const int64_t base = (int64_t)blockIdx.x * (256 * kStepVec);
+    const int64_t e = base + threadIdx.x * kStepVec;
     if (e >= n) return;
-    const GatedCoeff cf = gated_coeff<IO>(io<IO>::ld(r, e), io<IO>::ld(g, e), A[e % D] * kLog2e);
-    const float h = fmaf(cf.a, state[e], __builtin_amdgcn_sqrtf(cf.q) * cf.i * io<IO>::ld(x, e));
-    state[e] = h;
-    io<IO>::st(y, e, z ? h * silu_f32(io<IO>::ld(z, e)) : h);
+    auto token = [&](float rr, float gg, float xx, float Av, float h) {
+        const GatedCoeff cf = gated_coeff<IO>(rr, gg, Av * kLog2e);
+        return fmaf(cf.a, h, __builtin_amdgcn_sqrtf(cf.q) * cf.i * xx);
+    };
+    const int64_t d = e % D;
+    if (e + kStepVec > n) {   // the array's last elements
+        for (int64_t k = e; k < n; ++k) {
+            const float h = token(io<IO>::ld(r, k), io<IO>::ld(g, k), io<IO>::ld(x, k), A[k % D], state[k]);
+            state[k] = h;
+            io<IO>::st(y, k, z ? h * silu_f32(io<IO>::ld(z, k)) : h);
+        }
+        return;
+    }
+    const uint32_t lofs = threadIdx.x * kStepVec * (uint32_t)sizeof(IO);
+    row_words<kStepVec, IO> rr, rg, rx, rz;
+    rr.load(r + base, lofs);
+    rg.load(g + base, lofs);
+    rx.load(x + base, lofs);
+    if (z) rz.load(z + base, lofs);
+    any_f32 h = *reinterpret_cast<const any_f32 *>(state + e), Av;
+    if (d + kStepVec <= D) {
+        Av = *reinterpret_cast<const any_f32 *>(A + d);
+    } else {
+#pragma unroll
+        for (int k = 0; k < kStepVec; ++k) Av[k] = A[(d + k) % D];
+    }
+    float o[kStepVec];
+#pragma unroll
+    for (int k = 0; k < kStepVec; ++k) {
+        h[k] = token(rr.get(k), rg.get(k), rx.get(k), Av[k], h[k]);
+        o[k] = z ? h[k] * silu_f32(rz.get(k)) : h[k];
+    }
+    *reinterpret_cast<any_f32 *>(state + e) = h;
+    row_words<kStepVec, IO>::store(y + base, lofs, o);
 }
 
 }  // namespace ssm

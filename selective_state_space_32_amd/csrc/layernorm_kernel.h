@@ -340,33 +340,35 @@ template <typename IO, typename S>
 __global__ void __launch_bounds__(kNormWideThreads)
 layernorm_fwd_wide_kernel(const IO *__restrict__ x, const S *res, const float *__restrict__ w,
                           const float *__restrict__ bias, float eps, IO *__restrict__ y, S *sum,
-                          float *__restrict__ mean, float *__restrict__ rstd, int64_t D) {
+                          float *__restrict__ mean, float *__restrict__ rstd, int64_t M, int64_t D) {
     __shared__ float red[2][kNormWideThreads / 64];
-    const int64_t row = blockIdx.x, o = row * D;
     const float inv_d = 1.0f / (float)D;
-    auto value = [&](int64_t k) {
-        float v = io<IO>::ld(x, o + k);
-        if (res) v += io<S>::ld(res, o + k);
-        if constexpr (sizeof(S) == 2) v = bf16_to_f32(f32_to_bf16(v));
-        return v;
-    };
-    float m = 0.0f;
-    for (int64_t k = threadIdx.x; k < D; k += kNormWideThreads) m += value(k);
-    m = row_sum<kNormWideThreads>(m, red[0]) * inv_d;
-    float q = 0.0f;
-    for (int64_t k = threadIdx.x; k < D; k += kNormWideThreads) {
-        const float c = value(k) - m;
-        q = fmaf(c, c, q);
-    }
-    const float rs = 1.0f / sqrtf(fmaf(row_sum<kNormWideThreads>(q, red[1]), inv_d, eps));
-    for (int64_t k = threadIdx.x; k < D; k += kNormWideThreads) {
-        const float v = value(k), n = (v - m) * rs;
-        if (sum) io<S>::st(sum, o + k, v);
-        io<IO>::st(y, o + k, fmaf(n, w[k], bias ? bias[k] : 0.0f));
-    }
-    if (threadIdx.x == 0) {
-        if (mean) mean[row] = m;
-        if (rstd) rstd[row] = rs;
+    for (int64_t row = blockIdx.x; row < M; row += gridDim.x) {
+        const int64_t o = row * D;
+        auto value = [&](int64_t k) {
+            float v = io<IO>::ld(x, o + k);
+            if (res) v += io<S>::ld(res, o + k);
+            if constexpr (sizeof(S) == 2) v = bf16_to_f32(f32_to_bf16(v));
+            return v;
+        };
+        float m = 0.0f;
+        for (int64_t k = threadIdx.x; k < D; k += kNormWideThreads) m += value(k);
+        m = row_sum<kNormWideThreads>(m, red[0]) * inv_d;
+        float q = 0.0f;
+        for (int64_t k = threadIdx.x; k < D; k += kNormWideThreads) {
+            const float c = value(k) - m;
+            q = fmaf(c, c, q);
+        }
+        const float rs = 1.0f / sqrtf(fmaf(row_sum<kNormWideThreads>(q, red[1]), inv_d, eps));
+        for (int64_t k = threadIdx.x; k < D; k += kNormWideThreads) {
+            const float v = value(k), n = (v - m) * rs;
+            if (sum) io<S>::st(sum, o + k, v);
+            io<IO>::st(y, o + k, fmaf(n, w[k], bias ? bias[k] : 0.0f));
+        }
+        if (threadIdx.x == 0) {
+            if (mean) mean[row] = m;
+            if (rstd) rstd[row] = rs;
+        }
     }
 }
 
@@ -374,25 +376,29 @@ template <typename IO, typename S>
 __global__ void __launch_bounds__(kNormWideThreads)
 layernorm_bwd_wide_kernel(const IO *__restrict__ dy, const S *__restrict__ s, const float *__restrict__ w,
                           const float *__restrict__ mean, const float *__restrict__ rstd, const S *dres, S *ds,
-                          IO *__restrict__ dx, int64_t D) {
-    __shared__ float red[kNormWideThreads / 64][2];
-    const int64_t row = blockIdx.x, o = row * D;
-    const float m = mean[row], rs = rstd[row], inv_d = 1.0f / (float)D;
-    float p = 0.0f, q = 0.0f;
-    for (int64_t k = threadIdx.x; k < D; k += kNormWideThreads) {
-        const float t = io<IO>::ld(dy, o + k) * w[k];
-        p += t;
-        q = fmaf(t, (io<S>::ld(s, o + k) - m) * rs, q);
-    }
-    row_sum2<kNormWideThreads>(p, q, red);
-    p *= inv_d;
-    q *= inv_d;
-    for (int64_t k = threadIdx.x; k < D; k += kNormWideThreads) {
-        const float n = (io<S>::ld(s, o + k) - m) * rs;
-        float v = (io<IO>::ld(dy, o + k) * w[k] - fmaf(n, q, p)) * rs;
-        if (dres) v += io<S>::ld(dres, o + k);
-        io<S>::st(ds, o + k, v);
-        if (dx) io<IO>::st(dx, o + k, v);
+                          IO *__restrict__ dx, int64_t M, int64_t D) {
+    __shared__ float red[2][kNormWideThreads / 64][2];
+    const float inv_d = 1.0f / (float)D;
+    int turn = 0;
+    for (int64_t row = blockIdx.x; row < M; row += gridDim.x, turn ^= 1) {
+        const int64_t o = row * D;
+        const float m = mean[row], rs = rstd[row];
+        float p = 0.0f, q = 0.0f;
+        for (int64_t k = threadIdx.x; k < D; k += kNormWideThreads) {
+            const float t = io<IO>::ld(dy, o + k) * w[k];
+            p += t;
+            q = fmaf(t, (io<S>::ld(s, o + k) - m) * rs, q);
+        }
+        row_sum2<kNormWideThreads>(p, q, red[turn]);
+        p *= inv_d;
+        q *= inv_d;
+        for (int64_t k = threadIdx.x; k < D; k += kNormWideThreads) {
+            const float n = (io<S>::ld(s, o + k) - m) * rs;
+            float v = (io<IO>::ld(dy, o + k) * w[k] - fmaf(n, q, p)) * rs;
+            if (dres) v += io<S>::ld(dres, o + k);
+            io<S>::st(ds, o + k, v);
+            if (dx) io<IO>::st(dx, o + k, v);
+        }
     }
 }
 
