@@ -45,6 +45,7 @@ int launched() {
 struct Plan {
     int64_t nchunk, tiles, chains, cells;
     int V;
+    bool lines;   // rows start on 128-byte lines (of tensors that do)
     size_t state_bytes, word_bytes, bytes;
 };
 constexpr int64_t kCounterInts = ssm::kGatedQueues * ssm::kGatedCounterStride;
@@ -52,6 +53,7 @@ constexpr int64_t kCounterInts = ssm::kGatedQueues * ssm::kGatedCounterStride;
 Plan make_plan(const ssm_dims *dm) {
     Plan p;
     p.V = dm->io_dtype == SSM_IO_BF16 && dm->dim >= 2 ? 2 : 1;   // (a lane's access is four bytes either way)
+    p.lines = dm->dim * (int64_t)elem_size(dm) % 128 == 0;
     p.nchunk = std::max<int64_t>((dm->seqlen + ssm::kGatedChunk - 1) / ssm::kGatedChunk, 1);
     p.tiles = (dm->dim + 64 * p.V - 1) / (64 * p.V);
     p.chains = dm->batch * p.tiles;
@@ -62,10 +64,10 @@ Plan make_plan(const ssm_dims *dm) {
     return p;
 }
 
-// Consecutive workgroups that draw from one queue (see the kernel): 1 while the launch is a few rounds
-// of the chip and hand-overs count (B2 L2048 D1536 fp32: 23 us, 26 with 8), 8 where it is longer and
-// bandwidth does.
-int run_of(const Plan &p, int64_t nitem) { return p.chains * nitem < 4096 ? 1 : 8; }
+// Consecutive workgroups that draw from one queue (see the kernel): 8 where the launch is many rounds of
+// the chip and rows are whole lines, so that bandwidth counts; 1 where it is short and hand-overs count
+// (B2 L2048 D1536 fp32: 23 us, 26 with 8), or where neighbouring tiles share lines.
+int run_of(const Plan &p, int64_t nitem) { return p.lines && p.chains * nitem >= 4096 ? 8 : 1; }
 
 // Items of a chain that share a hand-over (see the kernel).  A hand-over takes about 1.2 us, and while it
 // runs the other chains move 0.013 us of data each per item: with many chains every item can wait for
@@ -81,7 +83,7 @@ int group_of(const Plan &p) {
 // One workgroup per (chain, item), the chains dealt to the queues in turn.
 int64_t grid_of(const Plan &p, int64_t nitem) {
     const int64_t per = (p.chains + ssm::kGatedQueues - 1) / ssm::kGatedQueues * nitem, run = run_of(p, nitem);
-    return (per + run - 1) / run * run * ssm::kGatedQueues;   // (per: items of the longest queue)
+    return (per + run - 1) / run * run * ssm::kGatedQueues;   // (per: items of the longest queue, or more)
 }
 
 // A launch holds fewer than 2^32 threads.
@@ -104,7 +106,7 @@ int *launch_clear(const Plan &p, uint64_t *words, int64_t nitem, const ssm_dims 
     return counters;
 }
 
-template <typename IO, int V, int T, int K, bool OUT>
+template <typename IO, int V, int T, int K, bool OUT, bool NT>
 void launch_fwd_v(const void *x, const void *r, const void *g, const float *A, const void *z, const float *h0,
                   const int32_t *sl, void *y, float *last, void *ws, const ssm_dims *dm, const Plan &p,
                   hipStream_t st) {
@@ -113,7 +115,7 @@ void launch_fwd_v(const void *x, const void *r, const void *g, const float *A, c
     float *states = p.nchunk > 1 ? static_cast<float *>(ws) : nullptr;
     uint64_t *words = reinterpret_cast<uint64_t *>(static_cast<char *>(ws) + p.state_bytes);
     int *counters = launch_clear(p, words, nitem, dm, st);
-    hipLaunchKernelGGL((ssm::gated_scan_kernel<IO, V, T, K, OUT>), dim3((unsigned)grid_of(p, nitem)), dim3(64 * K),
+    hipLaunchKernelGGL((ssm::gated_scan_kernel<IO, V, T, K, OUT, NT>), dim3((unsigned)grid_of(p, nitem)), dim3(64 * K),
                        0, st, static_cast<const IO *>(x), static_cast<const IO *>(r),
                        static_cast<const IO *>(g), A, static_cast<const IO *>(z), h0, sl, static_cast<IO *>(y), last,
                        states, words, counters, dm->seqlen, dm->dim, (int)p.tiles, (int)p.chains, (int)nitem,
@@ -126,15 +128,25 @@ void launch_fwd_v(const void *x, const void *r, const void *g, const float *A, c
 // chains: 169 -> 184 us), as long as the halved number of items still fills the chip.
 bool wide_items(const Plan &p) { return p.chains <= 32 && p.chains * p.nchunk >= 4096; }
 
+template <bool OUT, bool NT>
+void launch_fwd_n(const void *x, const void *r, const void *g, const float *A, const void *z, const float *h0,
+                const int32_t *sl, void *y, float *last, void *ws, const ssm_dims *dm, const Plan &p,
+                hipStream_t st) {
+    const bool wide = wide_items(p);
+    auto launch = dm->io_dtype == SSM_IO_F32
+                      ? (wide ? launch_fwd_v<float, 1, 16, 8, OUT, NT> : launch_fwd_v<float, 1, 8, 8, OUT, NT>)
+                  : p.V == 2 ? (wide ? launch_fwd_v<uint16_t, 2, 16, 8, OUT, NT>
+                                     : launch_fwd_v<uint16_t, 2, 8, 8, OUT, NT>)
+                             : launch_fwd_v<uint16_t, 1, 8, 8, OUT, NT>;
+    launch(x, r, g, A, z, h0, sl, y, last, ws, dm, p, st);
+}
+
 template <bool OUT>
 void launch_fwd(const void *x, const void *r, const void *g, const float *A, const void *z, const float *h0,
                 const int32_t *sl, void *y, float *last, void *ws, const ssm_dims *dm, const Plan &p,
                 hipStream_t st) {
-    const bool wide = wide_items(p);
-    auto launch = dm->io_dtype == SSM_IO_F32 ? (wide ? launch_fwd_v<float, 1, 16, 8, OUT> : launch_fwd_v<float, 1, 8, 8, OUT>)
-                  : p.V == 2 ? (wide ? launch_fwd_v<uint16_t, 2, 16, 8, OUT> : launch_fwd_v<uint16_t, 2, 8, 8, OUT>)
-                             : launch_fwd_v<uint16_t, 1, 8, 8, OUT>;
-    launch(x, r, g, A, z, h0, sl, y, last, ws, dm, p, st);
+    if (p.lines) launch_fwd_n<OUT, true>(x, r, g, A, z, h0, sl, y, last, ws, dm, p, st);
+    else launch_fwd_n<OUT, false>(x, r, g, A, z, h0, sl, y, last, ws, dm, p, st);
 }
 
 // The backward's workspace: the forward's (its states, where no checkpoints are given; its chain is the
@@ -151,7 +163,8 @@ void launch_bwd_v(const void *x, const void *r, const void *g, const float *A, c
                   hipStream_t st) {
     uint64_t *words = reinterpret_cast<uint64_t *>(static_cast<char *>(ws) + p.state_bytes);
     int *counters = launch_clear(p, words, p.nchunk, dm, st);
-    auto kern = z ? ssm::gated_bwd_kernel<IO, V, true> : ssm::gated_bwd_kernel<IO, V, false>;
+    auto kern = z ? (p.lines ? ssm::gated_bwd_kernel<IO, V, true, true> : ssm::gated_bwd_kernel<IO, V, true, false>)
+                  : (p.lines ? ssm::gated_bwd_kernel<IO, V, false, true> : ssm::gated_bwd_kernel<IO, V, false, false>);
     hipLaunchKernelGGL(kern, dim3((unsigned)grid_of(p, p.nchunk)), dim3(64 * ssm::kGatedWaves), 0, st,
                        static_cast<const IO *>(x), static_cast<const IO *>(r), static_cast<const IO *>(g), A,
                        static_cast<const IO *>(z), h0, sl, static_cast<const IO *>(dy), dlast,

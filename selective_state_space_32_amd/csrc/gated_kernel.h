@@ -32,11 +32,13 @@
 // Every wait ends: an item's number is drawn from a counter when its workgroup starts, and the
 // items of a chain are numbered in the order of the chain.  Whoever waits, waits for items that
 // started earlier, and the earliest of those waits for nobody.  There are kGatedQueues counters (one
-// alone is fought over by the whole chip: 768 workgroups that start together wait 9 us), each with
-// the chains of its residue; `run` consecutive workgroups draw from the same one.  The XCDs take
-// workgroups in turn, so with run = 1 a chain stays in one XCD, whose hand-overs are the fastest, and
-// with run = 8 every XCD works on all the chains: with run = 1 an XCD reads the same few columns of
-// every row, which lie in few of the memory's channels (B1 L131072 D2048 bf16: 514 against 468 us).
+// alone is fought over by the whole chip: 768 workgroups that start together wait 9 us), each with an
+// equal run of the chains; `run` consecutive workgroups draw from the same one.  The XCDs take
+// workgroups in turn, so with run = 1 a queue's chains stay in one XCD: its hand-overs are the
+// fastest, and neighbouring tiles, which share lines where rows do not start on one, meet in its L2
+// (B8 L2048 D5119 bf16 backward: 381 us, 440 with run = 8).  With run = 8 every XCD works on all the
+// chains, where with run = 1 it reads the same few columns of every row, which lie in few of the
+// memory's channels (B1 L131072 D2048 bf16: 552 against 513 us).
 #pragma once
 
 #include <float.h>
@@ -77,8 +79,10 @@ __device__ __forceinline__ float one_minus_square(float y, float a) {
 
 // V neighbouring I/O elements of a row as raw 32-bit words.  Rows of an odd width start at odd
 // elements, so the accesses assume no more than the element's own alignment (the memory unit takes
-// dwords at any byte address).
-template <int V, typename IO> struct row_words {
+// dwords at any byte address).  NT: past the caches, as data that is used once; not where rows start
+// inside a line, whose other part a neighbouring tile wants (B8 L2048 D5119 bf16: 214 against 231 us,
+// backward 417 against 527; at D5120 the other way round, 189 against 176 us).
+template <int V, typename IO, bool NT = true> struct row_words {
     static constexpr int W = V * (int)sizeof(IO) < 4 ? 1 : V * (int)sizeof(IO) / 4;
     uint32_t w[W];
     // row: the row's start (the same for the wave), lofs: the lane's byte offset in it -- the memory
@@ -89,7 +93,9 @@ template <int V, typename IO> struct row_words {
             w[0] = *reinterpret_cast<const IO *>(p);
         } else {
             typedef uint32_t any_u32 __attribute__((ext_vector_type(W), aligned(sizeof(IO))));
-            const any_u32 v = __builtin_nontemporal_load(reinterpret_cast<const any_u32 *>(p));
+            any_u32 v;
+            if constexpr (NT) v = __builtin_nontemporal_load(reinterpret_cast<const any_u32 *>(p));
+            else v = *reinterpret_cast<const any_u32 *>(p);
             __builtin_memcpy(w, &v, sizeof w);
         }
     }
@@ -122,7 +128,8 @@ template <int V, typename IO> struct row_words {
             typedef uint32_t any_u32 __attribute__((ext_vector_type(W), aligned(sizeof(IO))));
             any_u32 v;
             __builtin_memcpy(&v, o, sizeof o);
-            __builtin_nontemporal_store(v, reinterpret_cast<any_u32 *>(p));
+            if constexpr (NT) __builtin_nontemporal_store(v, reinterpret_cast<any_u32 *>(p));
+            else *reinterpret_cast<any_u32 *>(p) = v;
         }
     }
 };
@@ -221,15 +228,20 @@ __device__ __forceinline__ void chain_step(uint64_t *base, int64_t stride, int p
     __syncthreads();
 }
 
-// Which item this workgroup takes: (chain, position along the chain), or chain < 0 for none.
-// Chains of one residue are walked together, position by position.
+// Which item this workgroup takes: (sequence, tile, position along the chain), or pos < 0 for none.
+// A queue's chains are walked together, position by position.  Chains are numbered sequence by
+// sequence, or, where the sequences have lengths of their own, tile by tile, so that every queue gets
+// its share of the long ones (B8 L2048 D5120 bf16, lengths from 2048 down to 0, backward: 309 against
+// 233 us).
 struct GatedItem {
-    int chain, pos;
+    int b, tile, pos;
 };
-__device__ __forceinline__ GatedItem gated_item(int chains, int nitem, int *counters, int run, int *slot) {
+__device__ __forceinline__ GatedItem gated_item(int chains, int tiles, int nitem, bool ragged, int *counters, int run,
+                                                int *slot) {
     const int q = (int)blockIdx.x / run % kGatedQueues;
-    const int nq = (chains - q + kGatedQueues - 1) / kGatedQueues;
-    if (nq <= 0) return {-1, 0};
+    const int first = (int)((int64_t)chains * q / kGatedQueues);
+    const int nq = (int)((int64_t)chains * (q + 1) / kGatedQueues) - first;
+    if (nq == 0) return {0, 0, -1};
     int n = (int)blockIdx.x / (run * kGatedQueues) * run + (int)blockIdx.x % run;
     if (counters) {   // (one item per sequence: no chain, any order will do)
         if (threadIdx.x == 0)
@@ -238,9 +250,10 @@ __device__ __forceinline__ GatedItem gated_item(int chains, int nitem, int *coun
         __syncthreads();
         n = __builtin_amdgcn_readfirstlane(*slot);
     }
-    if (n >= nq * nitem) return {-1, 0};
-    const int pos = n / nq;
-    return {(n - pos * nq) * kGatedQueues + q, pos};
+    if (n >= nq * nitem) return {0, 0, -1};
+    const int pos = n / nq, chain = first + n - pos * nq;
+    const int per = ragged ? chains / tiles : tiles, hi = chain / per, lo = chain - hi * per;
+    return ragged ? GatedItem{lo, hi, pos} : GatedItem{hi, lo, pos};
 }
 
 // Fills the chain's words with ones (n 16-byte pairs of them: the array is padded) and clears the
@@ -271,7 +284,7 @@ __device__ __forceinline__ GatedCoeff gated_coeff(float r, float g, float a2) {
 // OUT: y and last_state are written; otherwise only the states.  states (nullable): the state at the
 // end of every kGatedChunk tokens but a sequence's last, for the backward pass.
 // M: the tokens of an item in units of kGatedChunk.
-template <typename IO, int V, int T, int K, bool OUT>
+template <typename IO, int V, int T, int K, bool OUT, bool NT>
 __global__ void __launch_bounds__(64 * K)
 gated_scan_kernel(const IO *__restrict__ x, const IO *__restrict__ r, const IO *__restrict__ g,
                   const float *__restrict__ A, const IO *__restrict__ z, const float *h0,
@@ -280,18 +293,18 @@ gated_scan_kernel(const IO *__restrict__ x, const IO *__restrict__ r, const IO *
                   int run, int group) {
     constexpr int C = T * K, M = C / kGatedChunk;
     static_assert(C % kGatedChunk == 0 && K % M == 0, "a stored state is at a wave's end");
-    using Row = row_words<V, IO>;
+    using Row = row_words<V, IO, NT>;
     __shared__ float s_P[K][64 * V], s_H[K][64 * V], s_in[64 * V];
     __shared__ uint64_t s_map[kGatedGroup][64 * V];
     __shared__ int s_slot;
-    const GatedItem it = gated_item(chains, nitem, counters, run, &s_slot);
-    if (it.chain < 0) return;
-    const int b = it.chain / tiles, c = it.pos;
+    const GatedItem it = gated_item(chains, tiles, nitem, seq_lens != nullptr, counters, run, &s_slot);
+    if (it.pos < 0) return;
+    const int b = it.b, c = it.pos;
     const int lane = threadIdx.x & 63;
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     // The lane's first channel.  Of an odd width the last lane takes the last V channels: those it
     // shares with its neighbour get the same values from both.
-    const int64_t dl = (int64_t)(it.chain - b * tiles) * 64 * V + lane * V;
+    const int64_t dl = (int64_t)it.tile * 64 * V + lane * V;
     const bool act = dl < D;
     const int64_t d = min(dl, D - V);
     const uint32_t lofs = (uint32_t)d * (uint32_t)sizeof(IO);
@@ -431,7 +444,7 @@ gated_scan_kernel(const IO *__restrict__ x, const IO *__restrict__ r, const IO *
 // its tokens, then walks them forwards for the states and backwards for the gradients.  The
 // coefficients that cost transcendentals (both sigmoids, the decay) stay in registers in between;
 // 1 - a^2 is formed again.  dA's share of the item goes to part[item], summed afterwards in order.
-template <typename IO, int V, bool GATE>
+template <typename IO, int V, bool GATE, bool NT>
 __global__ void __launch_bounds__(64 * kGatedWaves)
 __attribute__((amdgpu_waves_per_eu(4)))
 gated_bwd_kernel(const IO *__restrict__ x, const IO *__restrict__ r, const IO *__restrict__ g,
@@ -441,16 +454,16 @@ gated_bwd_kernel(const IO *__restrict__ x, const IO *__restrict__ r, const IO *_
                  IO *__restrict__ dz, float *__restrict__ part, float *__restrict__ dh0, uint64_t *words,
                  int *counters, int64_t L, int64_t D, int tiles, int chains, int nchunk, int run, int group) {
     constexpr int T = kGatedRows, K = kGatedWaves, C = kGatedChunk;
-    using Row = row_words<V, IO>;
+    using Row = row_words<V, IO, NT>;
     __shared__ float s_P[K][64 * V], s_H[K][64 * V], s_G[K][64 * V], s_in[64 * V];
     __shared__ uint64_t s_map[kGatedGroup][64 * V];
     __shared__ int s_slot;
-    const GatedItem it = gated_item(chains, nchunk, counters, run, &s_slot);
-    if (it.chain < 0) return;
-    const int b = it.chain / tiles, c = nchunk - 1 - it.pos;
+    const GatedItem it = gated_item(chains, tiles, nchunk, seq_lens != nullptr, counters, run, &s_slot);
+    if (it.pos < 0) return;
+    const int b = it.b, c = nchunk - 1 - it.pos;
     const int lane = threadIdx.x & 63;
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int64_t dl = (int64_t)(it.chain - b * tiles) * 64 * V + lane * V;
+    const int64_t dl = (int64_t)it.tile * 64 * V + lane * V;
     const bool act = dl < D;
     const int64_t d = min(dl, D - V);
     const uint32_t lofs = (uint32_t)d * (uint32_t)sizeof(IO);
