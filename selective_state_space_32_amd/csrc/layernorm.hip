@@ -61,6 +61,23 @@ int64_t norm_parts(int64_t rows, int64_t D) {
 }
 
 // The narrowest shape that holds a row of D values: lanes past the row's end do nothing.
+template <typename IO, typename S, bool NT>
+auto fwd_kernel_of(int64_t D) {
+    return D <= 256    ? ssm::layernorm_fwd_kernel<IO, S, 64, 1, NT>
+           : D <= 1024 ? ssm::layernorm_fwd_kernel<IO, S, 64, 4, NT>
+           : D <= 2048 ? ssm::layernorm_fwd_kernel<IO, S, 256, 2, NT>
+           : D <= 5120 ? ssm::layernorm_fwd_kernel<IO, S, 256, 5, NT>
+                       : ssm::layernorm_fwd_kernel<IO, S, 256, 8, NT>;
+}
+template <typename IO, typename S, bool NT>
+auto bwd_kernel_of(int64_t D) {
+    return D <= 256    ? ssm::layernorm_bwd_kernel<IO, S, 64, 1, NT>
+           : D <= 1024 ? ssm::layernorm_bwd_kernel<IO, S, 64, 4, NT>
+           : D <= 2048 ? ssm::layernorm_bwd_kernel<IO, S, 256, 2, NT>
+           : D <= 5120 ? ssm::layernorm_bwd_kernel<IO, S, 256, 5, NT>
+                       : ssm::layernorm_bwd_kernel<IO, S, 512, 4, NT>;
+}
+
 template <typename IO, typename S>
 void launch_norm(const void *x_, const void *res_, const float *w, const float *bias, float eps, void *y_, void *sum_,
                  float *mean, float *rstd, int64_t rows, int64_t D, hipStream_t st) {
@@ -73,11 +90,7 @@ void launch_norm(const void *x_, const void *res_, const float *w, const float *
                            dim3(ssm::kNormWideThreads), 0, st, x, res, w, bias, eps, y, sum, mean, rstd, rows, D);
         return;
     }
-    auto kern = D <= 256    ? ssm::layernorm_fwd_kernel<IO, S, 64, 1>
-                : D <= 1024 ? ssm::layernorm_fwd_kernel<IO, S, 64, 4>
-                : D <= 2048 ? ssm::layernorm_fwd_kernel<IO, S, 256, 2>
-                : D <= 5120 ? ssm::layernorm_fwd_kernel<IO, S, 256, 5>
-                            : ssm::layernorm_fwd_kernel<IO, S, 256, 8>;
+    auto kern = D * sizeof(IO) % 128 == 0 ? fwd_kernel_of<IO, S, true>(D) : fwd_kernel_of<IO, S, false>(D);
     const int64_t slots = norm_slots(D), grid = std::min<int64_t>((rows + slots - 1) / slots, kFwdGroups);
     hipLaunchKernelGGL(kern, dim3((unsigned)grid), dim3(256), 0, st, x, res, w, bias, eps, y, sum, mean, rstd, rows,
                        D);
@@ -98,11 +111,7 @@ void launch_norm_bwd(const void *dy_, const void *s_, const float *w, const floa
         hipLaunchKernelGGL((ssm::layernorm_bwd_wide_kernel<IO, S>), dim3((unsigned)std::min(rows, kWideGroups)),
                            dim3(ssm::kNormWideThreads), 0, st, dy, s, w, mean, rstd, dres, ds, dx, rows, D);
     } else if (rows > 0) {
-        auto kern = D <= 256    ? ssm::layernorm_bwd_kernel<IO, S, 64, 1>
-                    : D <= 1024 ? ssm::layernorm_bwd_kernel<IO, S, 64, 4>
-                    : D <= 2048 ? ssm::layernorm_bwd_kernel<IO, S, 256, 2>
-                    : D <= 5120 ? ssm::layernorm_bwd_kernel<IO, S, 256, 5>
-                                : ssm::layernorm_bwd_kernel<IO, S, 512, 4>;
+        auto kern = D * sizeof(IO) % 128 == 0 ? bwd_kernel_of<IO, S, true>(D) : bwd_kernel_of<IO, S, false>(D);
         hipLaunchKernelGGL(kern, dim3((unsigned)parts), dim3(D <= 5120 ? 256 : 512), 0, st, dy, s, w, mean, rstd,
                            dres, ds, dx, pw, pb, rows, D);
     }
