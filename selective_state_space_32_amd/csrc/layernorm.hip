@@ -45,9 +45,10 @@ int launched() {
     return ok();
 }
 
-// Workgroups of the forward: two per CU.  A workgroup takes several rows, so that its weights are worth
-// keeping (16384x5120 bf16 with an fp32 residual: 165 us with 512 or 256, 172 with 1024).
-constexpr int64_t kFwdGroups = 512;
+// Workgroups of the forward, at most.  A workgroup takes several rows, so that its weights are worth
+// keeping: two per CU for wide rows (16384x5120 bf16 with an fp32 residual: 165 us, 172 with four), four
+// for narrow ones, of which a workgroup requests fewer bytes at a time (32768x500: 39 us, 52 with two).
+int64_t fwd_groups(int64_t D) { return D <= 2048 ? 1024 : 512; }
 
 // Rows that a workgroup holds at a time (a wave each, up to 1024 values), by the row's width (0: wider than the registers hold).
 int64_t norm_slots(int64_t D) { return D <= 1024 ? 4 : D <= 8192 ? 1 : 0; }
@@ -91,7 +92,7 @@ void launch_norm(const void *x_, const void *res_, const float *w, const float *
         return;
     }
     auto kern = D * sizeof(IO) % 128 == 0 ? fwd_kernel_of<IO, S, true>(D) : fwd_kernel_of<IO, S, false>(D);
-    const int64_t slots = norm_slots(D), grid = std::min<int64_t>((rows + slots - 1) / slots, kFwdGroups);
+    const int64_t slots = norm_slots(D), grid = std::min<int64_t>((rows + slots - 1) / slots, fwd_groups(D));
     hipLaunchKernelGGL(kern, dim3((unsigned)grid), dim3(256), 0, st, x, res, w, bias, eps, y, sum, mean, rstd, rows,
                        D);
 }
