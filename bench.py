@@ -152,9 +152,13 @@ def scan_bwd_alg_bytes(bsz, L, D, N, io_bytes):
 
 
 def kernel_source_digest() -> str:
+    """Of the sources behind the workloads here (the gated recurrence and the layer norm, which no
+    workload runs, are in files of their own)."""
     h = hashlib.sha256()
     csrc = os.path.join(ROOT, "selective_state_space_32_amd", "csrc")
     for f in sorted(os.listdir(csrc)):
+        if f.startswith(("gated", "layernorm", "host_util")):
+            continue
         with open(os.path.join(csrc, f), "rb") as fh:
             h.update(f.encode() + fh.read())
     return h.hexdigest()[:16]

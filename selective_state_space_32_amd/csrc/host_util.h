@@ -1,5 +1,6 @@
-// What the entry points of every translation unit share on the host: the calling thread's
-// status and message, and alignment helpers.
+// Host helpers of the translation units that hold an operator's entry points and kernels together
+// (gated.hip, layernorm.hip) and so need nothing of launch.h, which declares the same ones for the
+// scan's: the calling thread's status and message, and alignment.
 #pragma once
 
 #include <cstddef>

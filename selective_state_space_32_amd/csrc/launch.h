@@ -9,7 +9,7 @@
 #include <cstdint>
 #include <type_traits>
 
-#include "host_util.h"
+#include "ssmscan.h"
 #include "carry_kernel.h"
 #include "scan_kernels.h"
 #include "step_kernel.h"
@@ -19,8 +19,15 @@
 
 namespace ssmlib {
 
+// The status and message of the calling thread's last failure (ssm_last_error); defined in
+// ssmscan.hip.
+int fail(int code, const char *fmt, ...);
+int ok();
 // How long a second half of the split schedule waits for its hand-over (ssmscan.hip).
 unsigned long long handover_wait_ticks();
+
+inline size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
+inline bool aligned(const void *p, size_t a) { return ((uintptr_t)p % a) == 0; }
 
 enum Schedule { kGrid = 0, kCarry = 1, kSplit = 2 };
 
