@@ -8,6 +8,7 @@ kernels of libssmscan.so; if the library is missing this module raises on import
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 from typing import Callable, Optional, Tuple
 
@@ -751,12 +752,11 @@ def _need_lens(seq_lens, bsz, dev):
 
 
 def _gated_inputs(x, r, g, A, z, initial_state, seq_lens):
-    """Checks of the inputs that the gated recurrence's scan and its backward share; their sizes."""
+    """Checks of the inputs that the gated recurrence's scan and its backward share; their sizes and dims."""
     if x.dim() != 3:
         raise ValueError("x must be (batch, L, dim)")
     bsz, L, dim = x.shape
     dev, io = x.device, x.dtype
-    _io_code(io)
     _want(x, "x", (bsz, L, dim), io, dev)
     _want(r, "r", (bsz, L, dim), io, dev)
     _want(g, "g", (bsz, L, dim), io, dev)
@@ -767,7 +767,7 @@ def _gated_inputs(x, r, g, A, z, initial_state, seq_lens):
         _want(initial_state, "initial_state", (bsz, dim), torch.float32, dev)
     if seq_lens is not None:
         _need_lens(seq_lens, bsz, dev)
-    return bsz, L, dim, dev, io
+    return bsz, L, dim, dev, io, ssm_dims(bsz, L, dim, 1, _io_code(io), 0)
 
 
 def gated_scan_fwd(x: torch.Tensor, r: torch.Tensor, g: torch.Tensor, A: torch.Tensor,
@@ -785,7 +785,7 @@ def gated_scan_fwd(x: torch.Tensor, r: torch.Tensor, g: torch.Tensor, A: torch.T
     Returns (y, last_state) -- last_state (batch, dim) float32, or None if not asked for -- and
     with save_checkpoints (a training forward) also the workspace, for gated_scan_bwd's
     `checkpoints`."""
-    bsz, L, dim, dev, io = _gated_inputs(x, r, g, A, z, initial_state, seq_lens)
+    bsz, L, dim, dev, io, dims = _gated_inputs(x, r, g, A, z, initial_state, seq_lens)
     if y is None:
         y = torch.empty_like(x)
     else:
@@ -794,7 +794,6 @@ def gated_scan_fwd(x: torch.Tensor, r: torch.Tensor, g: torch.Tensor, A: torch.T
         _want(last_state, "last_state", (bsz, dim), torch.float32, dev)
     elif return_last_state:
         last_state = torch.empty((bsz, dim), dtype=torch.float32, device=dev)
-    dims = make_dims(bsz, L, dim, 1, io)
     if workspace is None:
         need = int(lib.ssm_gated_scan_workspace_bytes(ctypes.byref(dims)))
         workspace = torch.empty(need, dtype=torch.uint8, device=dev)
@@ -814,7 +813,7 @@ def gated_scan_bwd(dy: torch.Tensor, x: torch.Tensor, r: torch.Tensor, g: torch.
     workspace a gated_scan_fwd(..., save_checkpoints=True) call on them returned (without it the
     states are recomputed).  Returns a dict: dx, dr, dg, dz (if z) of x's dtype, dA (dim,) float32,
     dinitial_state (batch, dim) float32 (if asked for)."""
-    bsz, L, dim, dev, io = _gated_inputs(x, r, g, A, z, initial_state, seq_lens)
+    bsz, L, dim, dev, io, dims = _gated_inputs(x, r, g, A, z, initial_state, seq_lens)
     _want(dy, "dy", (bsz, L, dim), io, dev)
     if dlast_state is not None:
         _want(dlast_state, "dlast_state", (bsz, dim), torch.float32, dev)
@@ -826,7 +825,6 @@ def gated_scan_bwd(dy: torch.Tensor, x: torch.Tensor, r: torch.Tensor, g: torch.
         grads["dz"] = torch.empty_like(x)
     if want_initial_state_grad:
         grads["dinitial_state"] = torch.empty((bsz, dim), dtype=torch.float32, device=dev)
-    dims = make_dims(bsz, L, dim, 1, io)
     if workspace is None:
         need = int(lib.ssm_gated_scan_bwd_workspace_bytes(ctypes.byref(dims)))
         workspace = torch.empty(need, dtype=torch.uint8, device=dev)
@@ -849,7 +847,7 @@ def gated_step(state: torch.Tensor, x: torch.Tensor, r: torch.Tensor, g: torch.T
         raise ValueError("x must be (sequences, dim)")
     S, dim = x.shape
     dev, io = x.device, x.dtype
-    _io_code(io)
+    dims = ssm_dims(S, 1, dim, 1, _io_code(io), 0)
     _want(state, "state", (S, dim), torch.float32, dev)
     _want(x, "x", (S, dim), io, dev)
     _want(r, "r", (S, dim), io, dev)
@@ -861,7 +859,6 @@ def gated_step(state: torch.Tensor, x: torch.Tensor, r: torch.Tensor, g: torch.T
         y = torch.empty_like(x)
     else:
         _want(y, "y", (S, dim), io, dev)
-    dims = make_dims(S, 1, dim, 1, io)
     _check(lib.ssm_gated_step(_addr(state), _addr(x), _addr(r), _addr(g), _addr(A), _addr(z), _addr(y), ctypes.byref(dims),
                               _stream_addr(stream)))
     return y
@@ -874,10 +871,7 @@ def _norm_shape(t, name):
     if t.dim() < 1:
         raise ValueError(f"{name} must have at least one axis")
     dim = t.shape[-1]
-    rows = 1
-    for n in t.shape[:-1]:
-        rows *= n
-    return rows, dim
+    return math.prod(t.shape[:-1]), dim
 
 
 def layernorm_fwd(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor] = None, eps: float = 1e-5, *,
@@ -892,7 +886,7 @@ def layernorm_fwd(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Te
     Returns (y, total, mean, rstd): y in x's dtype, mean and rstd float32 of x's leading shape."""
     rows, dim = _norm_shape(x, "x")
     dev, io = x.device, x.dtype
-    _io_code(io)
+    dims = ssm_dims(1, rows, dim, 1, _io_code(io), 0)
     shape = x.shape
     _want(x, "x", shape, io, dev)
     _want(weight, "weight", (dim,), torch.float32, dev)
@@ -912,11 +906,12 @@ def layernorm_fwd(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Te
         _want(y, "y", shape, io, dev)
     if total is not None:
         _want(total, "total", shape, kept, dev)
-    elif residual is not None or kept != io:
+    elif residual is not None:
+        total = torch.empty_like(residual)
+    elif kept != io:
         total = torch.empty(shape, dtype=kept, device=dev)
     mean = torch.empty(shape[:-1], dtype=torch.float32, device=dev)
-    rstd = torch.empty(shape[:-1], dtype=torch.float32, device=dev)
-    dims = make_dims(1, rows, dim, 1, io)
+    rstd = torch.empty_like(mean)
     _check(lib.ssm_layernorm_fwd(_addr(x), _addr(residual), _addr(weight), _addr(bias), float(eps),
                                  NORM_SUM_F32 if kept != io else 0, _addr(y), _addr(total), _addr(mean), _addr(rstd),
                                  ctypes.byref(dims), _stream_addr(stream)))
@@ -933,7 +928,7 @@ def layernorm_bwd(dy: torch.Tensor, total: torch.Tensor, weight: torch.Tensor, m
     float32.  ds may be the dresidual tensor itself (updated in place)."""
     rows, dim = _norm_shape(dy, "dy")
     dev, io = dy.device, dy.dtype
-    _io_code(io)
+    dims = ssm_dims(1, rows, dim, 1, _io_code(io), 0)
     shape, kept = dy.shape, total.dtype
     if kept != io and kept != torch.float32:
         raise TypeError(f"total: dtype {kept} is neither dy's nor float32")
@@ -951,10 +946,9 @@ def layernorm_bwd(dy: torch.Tensor, total: torch.Tensor, weight: torch.Tensor, m
     grads = dict(ds=ds)
     if kept != io:
         grads["dx"] = torch.empty_like(dy)
-    dims = make_dims(1, rows, dim, 1, io)
     if want_param_grads:
         grads["dweight"] = torch.empty((dim,), dtype=torch.float32, device=dev)
-        grads["dbias"] = torch.empty((dim,), dtype=torch.float32, device=dev)
+        grads["dbias"] = torch.empty_like(grads["dweight"])
         if workspace is None:
             need = int(lib.ssm_layernorm_bwd_workspace_bytes(ctypes.byref(dims)))
             workspace = torch.empty(need, dtype=torch.uint8, device=dev)
