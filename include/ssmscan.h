@@ -1,6 +1,7 @@
 /*
  * libssmscan -- the Mamba selective state-space scan (S6) and its single-token
- * recurrent step on AMD MI355X (gfx950).
+ * recurrent step on AMD MI355X (gfx950), and their neighbours in a block: the causal
+ * convolution, the state space dual layer, the gated linear recurrence, the layer norm.
  *
  * What is computed (per channel d of sequence b, state index n):
  *   step size       dt_t   = softplus(delta_t + delta_bias[d])   with SSM_SCAN_SOFTPLUS
@@ -444,7 +445,7 @@ SSMSCAN_API int ssm_step_act(float *state, const void *u, const void *delta, con
  *                   when that is 0); its contents on entry do not matter.  After the call it
  *                   holds the states that ssm_gated_scan_bwd takes as checkpoints
  * Arithmetic and states are fp32; 1 - a^2 is formed without cancellation where a is near 1.
- * dims->dstate and dims->chunk_len are ignored; dim is at most 2^27, seqlen at most 2^30, and
+ * dims->dstate and dims->chunk_len are ignored; dim is at most 2^26, seqlen at most 2^30, and
  * batch * ceil(dim / 64), rounded up to a multiple of 8, times ceil(seqlen / 64) below 2^23 - 64 (the
  * work items of a launch; SSM_ERR_SHAPE may follow above that).
  * Returns SSM_OK or a negative ssm_status (nothing is launched on an error). */
@@ -509,7 +510,7 @@ SSMSCAN_API int ssm_gated_step(float *state, const void *x, const void *r, const
  *   mean, rstd    : [batch * seqlen] fp32 outputs for the backward pass, each may be NULL
  *   eps           : >= 0 and finite (SSM_ERR_VALUE otherwise)
  * Outputs must not overlap inputs or each other otherwise.  dims->dstate and dims->chunk_len are
- * ignored; at most 2^31 - 1 rows of at most 2^27 values.  Returns SSM_OK or a negative
+ * ignored; at most 2^31 - 1 rows of at most 2^26 values.  Returns SSM_OK or a negative
  * ssm_status. */
 SSMSCAN_API int ssm_layernorm_fwd(const void *x, const void *residual, const float *weight, const float *bias,
                 float eps, int flags, void *y, void *sum, float *mean, float *rstd, const ssm_dims *dims,

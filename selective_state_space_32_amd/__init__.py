@@ -1,4 +1,5 @@
-"""libssmscan: the Mamba selective state-space scan (S6) for MI355X (gfx950).
+"""libssmscan: the Mamba selective state-space scan (S6) for MI355X (gfx950), with the gated linear
+recurrence and the layer norm of recurrent blocks.
 
 The compute path is the C-ABI shared library ``libssmscan.so`` (hand-written HIP
 kernels); ``selective_state_space_32_amd.ssmscan`` is its thin ctypes binding taking

@@ -21,8 +21,8 @@ int check_gated_dims(const ssm_dims *dm, bool seq) {
                     (long long)dm->seqlen, (long long)dm->dim);
     if (dm->io_dtype != SSM_IO_F32 && dm->io_dtype != SSM_IO_BF16)
         return fail(SSM_ERR_DTYPE, "io_dtype %d is not SSM_IO_F32 (0) or SSM_IO_BF16 (1)", dm->io_dtype);
-    if (dm->dim > kMaxDim / 8 || dm->batch > kMaxDim)   // (the column sums launch 16 threads per column)
-        return fail(SSM_ERR_SHAPE, "dim larger than 2^27 or batch larger than 2^30");
+    if (dm->dim > kMaxDim / 16 || dm->batch > kMaxDim)   // (the column sums launch 32 threads per column)
+        return fail(SSM_ERR_SHAPE, "dim larger than 2^26 or batch larger than 2^30");
     if (dm->batch > 0 && dm->dim > (int64_t(1) << 33) / dm->batch)
         return fail(SSM_ERR_SHAPE, "batch*dim exceeds 2^33 (grid size)");
     if (seq && (dm->seqlen > kMaxDim ||
@@ -266,8 +266,9 @@ int ssm_gated_scan_bwd(const void *x, const void *r, const void *g, const float 
         bwd(x, r, g, A, z, initial_state, seq_lens, dy, dlast_state, states, dx, dr, dg, dz, part, dinitial_state,
             ws, dims, p, st);
     }
-    hipLaunchKernelGGL(ssm::column_sum_kernel, dim3((unsigned)((dims->dim + 63) / 64)),
-                       dim3(64 * ssm::kColumnWaves), 0, st, part, dA, dims->batch * p.nchunk, dims->dim);
+    hipLaunchKernelGGL(ssm::column_sum_kernel,
+                       dim3((unsigned)((dims->dim + ssm::kColumnCols - 1) / ssm::kColumnCols)),
+                       dim3(ssm::kColumnCols * ssm::kColumnGroups), 0, st, part, dA, dims->batch * p.nchunk, dims->dim);
     return launched();
 }
 

@@ -16,7 +16,20 @@
 //      the chunks before it (the chain, below) and publishes the state at its end,
 //   3. every wave folds the maps of the waves before it onto that state and walks its tokens again
 //      from there, writing y.
-// The inputs are read once and the outputs written once, whatever the length.
+// The inputs are read once and the outputs written once, whatever the length.  Bound: HBM.  Per element
+// the forward moves 8 bytes in bf16 (10 with a gate) and issues about 45 VALU instructions, 7 of them
+// transcendental (two sigmoids, the decay, a root); the backward moves 14 (18) and issues about 95,
+// three quarters of what the VALU can do in the time that HBM takes.  The chain adds 1/64 of (8 to
+// clear, 8 to publish, 8 to 40 to read, 4 of state) bytes per element, 4 % of the gated forward's.
+// Measured (a copy of 1 GiB reaches 5.1 TB/s on this card): B8 L2048 D5120 bf16 gated 172 us for
+// 839 MB, its backward 313 us for 1,510 MB; B1 L131072 D2048 bf16 455 us for 2,148 MB; B2 L2048 D1536
+// fp32 22 us for 101 MB, its backward 37 us for 176 MB.
+//
+// The split.  Eight tokens per wave keep a lane's values of V channels in registers (70 registers, three
+// workgroups per CU, in the forward; 128, two, in the backward); eight waves make the chain's word an
+// item's thousandth part, and two or three workgroups per CU let one load while another computes or
+// waits.  Sixteen waves of eight tokens (221 us at B8 L2048 D5120) and eight of sixteen (184 us) were
+// slower than eight of eight (169 us): fewer workgroups overlap.
 //
 // The chain.  Handing the state from chunk to chunk would cost a round trip through memory per chunk,
 // so with few chains the chunks of a chain form groups of up to kGatedGroup (the host chooses).  word[sequence][item][channel] is 64 bits: a
@@ -671,23 +684,24 @@ gated_bwd_kernel(const IO *__restrict__ x, const IO *__restrict__ r, const IO *_
     }
 }
 
-// out[d] = sum of the n rows of part, in an order of their own: 16 waves take every 16th row, and
-// their sums are added in order.
-constexpr int kColumnWaves = 16;
-static __global__ void __launch_bounds__(64 * kColumnWaves)
+// out[d] = sum of the n rows of part, in an order of their own: kColumnGroups groups of threads take
+// every kColumnGroups-th row of kColumnCols columns, and their sums are added in order.  Bound: the
+// latency of a few dependent loads (64 rows of 1536 columns: 3.9 us).
+constexpr int kColumnCols = 32, kColumnGroups = 32;
+static __global__ void __launch_bounds__(kColumnCols * kColumnGroups)
 column_sum_kernel(const float *__restrict__ part, float *__restrict__ out, int64_t n, int64_t D) {
-    __shared__ float red[kColumnWaves][64];
-    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-    const int64_t d = (int64_t)blockIdx.x * 64 + lane;
+    __shared__ float red[kColumnGroups][kColumnCols];
+    const int col = threadIdx.x % kColumnCols, g = threadIdx.x / kColumnCols;
+    const int64_t d = (int64_t)blockIdx.x * kColumnCols + col;
     float s = 0.0f;
     if (d < D)
 #pragma unroll 8
-        for (int64_t k = w; k < n; k += kColumnWaves) s += part[k * D + d];
-    red[w][lane] = s;
+        for (int64_t k = g; k < n; k += kColumnGroups) s += part[k * D + d];
+    red[g][col] = s;
     __syncthreads();
-    if (w == 0 && d < D) {
+    if (g == 0 && d < D) {
 #pragma unroll
-        for (int k = 1; k < kColumnWaves; ++k) s += red[k][lane];
+        for (int k = 1; k < kColumnGroups; ++k) s += red[k][col];
         out[d] = s;
     }
 }
@@ -695,7 +709,7 @@ column_sum_kernel(const float *__restrict__ part, float *__restrict__ out, int64
 // One token of every sequence, the state updated in place.  The tensors are walked as flat arrays,
 // kStepVec neighbouring elements per thread (they may lie in two rows; A's index wraps with them).
 // Bound: HBM, 8 bytes of state and 4 or 5 I/O elements per channel (S256 D5120 bf16 with its gate:
-// 23.6 MB, STEPUS us).  The state is left in the caches for the next token.
+// 23.6 MB, 4.9 us on the device).  The state is left in the caches for the next token.
 constexpr int kStepVec = 4;
 template <typename IO>
 __global__ void __launch_bounds__(256)

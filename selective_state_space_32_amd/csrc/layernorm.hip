@@ -12,7 +12,7 @@ namespace {
 using namespace ssmlib;
 
 constexpr int64_t kMaxRows = (int64_t(1) << 31) - 1;
-constexpr int64_t kMaxNormDim = int64_t(1) << 27;   // (the column sums launch 16 threads per column)
+constexpr int64_t kMaxNormDim = int64_t(1) << 26;   // (the column sums launch 32 threads per column)
 constexpr int64_t kMaxElems = int64_t(1) << 46;
 constexpr int64_t kBwdGroups = 512;   // workgroups of the backward, and so partial sums, at most
 constexpr int64_t kWideGroups = int64_t(1) << 16;   // workgroups of the kernels for wider rows, at most
@@ -30,7 +30,7 @@ int check_norm_dims(const ssm_dims *dm) {
         return fail(SSM_ERR_SHAPE, "more than 2^31 - 1 rows");
     const int64_t rows = dm->batch * dm->seqlen;
     if (dm->dim > kMaxNormDim || (rows > 0 && dm->dim > kMaxElems / rows))
-        return fail(SSM_ERR_SHAPE, "dim exceeds 2^27 or the rows exceed 2^46 elements");
+        return fail(SSM_ERR_SHAPE, "dim exceeds 2^26 or the rows exceed 2^46 elements");
     return SSM_OK;
 }
 
@@ -124,8 +124,9 @@ void launch_norm_bwd(const void *dy_, const void *s_, const float *w, const floa
                            dim3((unsigned)((D + 255) / 256), (unsigned)parts), dim3(256), 0, st, dy, s, mean, rstd,
                            pw, pb, rows, D, per);
     }
-    hipLaunchKernelGGL(ssm::layernorm_wgrad_sum_kernel, dim3((unsigned)((D + 63) / 64)),
-                       dim3(64 * ssm::kNormSumWaves), 0, st, pw, pb, dw, db, parts, D);
+    hipLaunchKernelGGL(ssm::layernorm_wgrad_sum_kernel,
+                       dim3((unsigned)((D + ssm::kNormSumCols - 1) / ssm::kNormSumCols)),
+                       dim3(ssm::kNormSumCols * ssm::kNormSumGroups), 0, st, pw, pb, dw, db, parts, D);
 }
 
 }  // namespace
