@@ -103,15 +103,15 @@ int check_items(const Plan &p) {
     return SSM_OK;
 }
 
-// The chain's words and counters behind `words`, made ready for nitem items per sequence; counters
-// are NULL where there is no chain.
-int *launch_clear(const Plan &p, uint64_t *words, int64_t nitem, const ssm_dims *dm, hipStream_t st) {
+// The chain's words, made ready for nitem items per sequence, and the counters at the workspace's end;
+// returns the counters, NULL where there is no chain.
+int *launch_clear(const Plan &p, void *words, void *ws, int64_t nitem, const ssm_dims *dm, hipStream_t st) {
     if (nitem == 1) return nullptr;
-    int *counters = reinterpret_cast<int *>(reinterpret_cast<char *>(words) + p.word_bytes);
-    const int64_t n = (dm->batch * nitem * dm->dim + 1) / 2;
+    ssm::u32x4_t *counters = reinterpret_cast<ssm::u32x4_t *>(static_cast<char *>(ws) + p.state_bytes + p.word_bytes);
+    const int64_t bytes = dm->batch * nitem * dm->dim * (group_of(p) == 1 ? 4 : 8), n = (bytes + 15) / 16;
     hipLaunchKernelGGL(ssm::gated_clear_kernel, dim3((unsigned)((n + kCounterInts / 4 + 255) / 256)), dim3(256), 0, st,
-                       reinterpret_cast<ssm::u32x4_t *>(words), n, reinterpret_cast<ssm::u32x4_t *>(counters));
-    return counters;
+                       static_cast<ssm::u32x4_t *>(words), n, counters);
+    return reinterpret_cast<int *>(counters);
 }
 
 template <typename IO, int V, int T, int K, bool OUT, bool NT>
@@ -120,9 +120,11 @@ void launch_fwd_v(const void *x, const void *r, const void *g, const float *A, c
                   hipStream_t st) {
     constexpr int64_t M = T * K / ssm::kGatedChunk;
     const int64_t nitem = (p.nchunk + M - 1) / M;
-    float *states = p.nchunk > 1 ? static_cast<float *>(ws) : nullptr;
-    uint64_t *words = reinterpret_cast<uint64_t *>(static_cast<char *>(ws) + p.state_bytes);
-    int *counters = launch_clear(p, words, nitem, dm, st);
+    // (with groups of one the words are the states; wide items come with few chains, and so with groups)
+    const bool own = group_of(p) > 1;
+    float *states = p.nchunk > 1 && own ? static_cast<float *>(ws) : nullptr;
+    void *words = own ? static_cast<char *>(ws) + p.state_bytes : ws;
+    int *counters = launch_clear(p, words, ws, nitem, dm, st);
     hipLaunchKernelGGL((ssm::gated_scan_kernel<IO, V, T, K, OUT, NT>), dim3((unsigned)grid_of(p, nitem)), dim3(64 * K),
                        0, st, static_cast<const IO *>(x), static_cast<const IO *>(r),
                        static_cast<const IO *>(g), A, static_cast<const IO *>(z), h0, sl, static_cast<IO *>(y), last,
@@ -169,8 +171,8 @@ void launch_bwd_v(const void *x, const void *r, const void *g, const float *A, c
                   const int32_t *sl, const void *dy, const float *dlast, const void *states, void *dx, void *dr,
                   void *dg, void *dz, float *part, float *dh0, void *ws, const ssm_dims *dm, const Plan &p,
                   hipStream_t st) {
-    uint64_t *words = reinterpret_cast<uint64_t *>(static_cast<char *>(ws) + p.state_bytes);
-    int *counters = launch_clear(p, words, p.nchunk, dm, st);
+    void *words = static_cast<char *>(ws) + p.state_bytes;
+    int *counters = launch_clear(p, words, ws, p.nchunk, dm, st);
     auto kern = z ? (p.lines ? ssm::gated_bwd_kernel<IO, V, true, true> : ssm::gated_bwd_kernel<IO, V, true, false>)
                   : (p.lines ? ssm::gated_bwd_kernel<IO, V, false, true> : ssm::gated_bwd_kernel<IO, V, false, false>);
     hipLaunchKernelGGL(kern, dim3((unsigned)grid_of(p, p.nchunk)), dim3(64 * ssm::kGatedWaves), 0, st,

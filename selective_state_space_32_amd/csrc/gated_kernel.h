@@ -241,6 +241,44 @@ __device__ __forceinline__ void chain_step(uint64_t *base, int64_t stride, int p
     __syncthreads();
 }
 
+// The chain's step where every item waits for the one before it: the words are the states alone, four
+// bytes each (all ones meaning that nothing is there yet; a NaN state is published as the usual one).
+// Arguments and results as chain_step's.
+template <int V>
+__device__ __forceinline__ void chain_hand(uint32_t *base, int64_t stride, int pos, bool ends, bool act, int lane,
+                                           int w, const float (&P)[V], const float (&H)[V], const float (&start)[V],
+                                           float (&s_in)[64 * V], float (&out)[V]) {
+    if (w == 0) {
+        float in[V];
+        uint32_t *own = base + pos * stride;
+        if (pos == 0) {
+#pragma unroll
+            for (int v = 0; v < V; ++v) in[v] = start[v];
+        } else {
+            for (;;) {
+                bool all = true;
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+                    const uint32_t u = __hip_atomic_load(own - stride + v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+                    in[v] = __uint_as_float(u);
+                    all = all && u != kWordEmpty;
+                }
+                if (__all(all || !act)) break;
+                __builtin_amdgcn_s_sleep(1);
+            }
+        }
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            out[v] = fmaf(P[v], in[v], H[v]);
+            if (act && !ends)
+                __hip_atomic_store(own + v, out[v] != out[v] ? 0x7fc00000u : __float_as_uint(out[v]), __ATOMIC_RELAXED,
+                                   __HIP_MEMORY_SCOPE_AGENT);
+            s_in[lane * V + v] = in[v];
+        }
+    }
+    __syncthreads();
+}
+
 // Which item this workgroup takes: (sequence, tile, position along the chain), or pos < 0 for none.
 // A queue's chains are walked together, position by position.  Chains are numbered sequence by
 // sequence, or, where the sequences have lengths of their own, tile by tile, so that every queue gets
@@ -294,15 +332,16 @@ __device__ __forceinline__ GatedCoeff gated_coeff(float r, float g, float a2) {
     return c;
 }
 
-// OUT: y and last_state are written; otherwise only the states.  states (nullable): the state at the
-// end of every kGatedChunk tokens but a sequence's last, for the backward pass.
+// OUT: y and last_state are written; otherwise only the states.  states: the state at the end
+// of every kGatedChunk tokens but a sequence's last, for the backward pass (NULL where the words are that
+// already, or there is one chunk).
 // M: the tokens of an item in units of kGatedChunk.
 template <typename IO, int V, int T, int K, bool OUT, bool NT>
 __global__ void __launch_bounds__(64 * K)
 gated_scan_kernel(const IO *__restrict__ x, const IO *__restrict__ r, const IO *__restrict__ g,
                   const float *__restrict__ A, const IO *__restrict__ z, const float *h0,
                   const int32_t *__restrict__ seq_lens, IO *__restrict__ y, float *last,
-                  float *__restrict__ states, uint64_t *words, int *counters, int64_t L, int64_t D, int tiles, int chains, int nitem, int nchunk,
+                  float *states, void *words, int *counters, int64_t L, int64_t D, int tiles, int chains, int nitem, int nchunk,
                   int run, int group) {
     constexpr int C = T * K, M = C / kGatedChunk;
     static_assert(C % kGatedChunk == 0 && K % M == 0, "a stored state is at a wave's end");
@@ -409,8 +448,12 @@ gated_scan_kernel(const IO *__restrict__ x, const IO *__restrict__ r, const IO *
             for (int v = 0; v < V; ++v) start[v] = h0[(int64_t)b * D + d + v];
         }
     }
-    chain_step<V>(words + (int64_t)b * nitem * D + d, D, c, group, ends, act, lane, w, P, H, start, s_map,
-                  s_in, out);
+    const int64_t chain0 = (int64_t)b * nitem * D + d;
+    if (group == 1)
+        chain_hand<V>(static_cast<uint32_t *>(words) + chain0, D, c, ends, act, lane, w, P, H, start, s_in, out);
+    else
+        chain_step<V>(static_cast<uint64_t *>(words) + chain0, D, c, group, ends, act, lane, w, P, H, start, s_map,
+                      s_in, out);
     float *st = states ? states + ((int64_t)b * nchunk + c * M) * D + d : nullptr;   // the item's states
     if (w == 0 && act) {
 #pragma unroll
@@ -464,7 +507,7 @@ gated_bwd_kernel(const IO *__restrict__ x, const IO *__restrict__ r, const IO *_
                  const float *__restrict__ A, const IO *__restrict__ z, const float *__restrict__ h0,
                  const int32_t *__restrict__ seq_lens, const IO *__restrict__ dy, const float *__restrict__ dlast,
                  const float *__restrict__ states, IO *__restrict__ dx, IO *__restrict__ dr, IO *__restrict__ dg,
-                 IO *__restrict__ dz, float *__restrict__ part, float *__restrict__ dh0, uint64_t *words,
+                 IO *__restrict__ dz, float *__restrict__ part, float *__restrict__ dh0, void *words,
                  int *counters, int64_t L, int64_t D, int tiles, int chains, int nchunk, int run, int group) {
     constexpr int T = kGatedRows, K = kGatedWaves, C = kGatedChunk;
     using Row = row_words<V, IO, NT>;
@@ -601,8 +644,13 @@ gated_bwd_kernel(const IO *__restrict__ x, const IO *__restrict__ r, const IO *_
             for (int v = 0; v < V; ++v) start[v] = dlast[ch + v];
         }
     }
-    chain_step<V>(words + ((int64_t)b * nchunk + nlive - 1) * D + d, -D, nlive - 1 - c, group, c == 0, act, lane, w, P, G,
-                  start, s_map, s_in, out);
+    const int64_t chain0 = ((int64_t)b * nchunk + nlive - 1) * D + d;
+    if (group == 1)
+        chain_hand<V>(static_cast<uint32_t *>(words) + chain0, -D, nlive - 1 - c, c == 0, act, lane, w, P, G, start,
+                      s_in, out);
+    else
+        chain_step<V>(static_cast<uint64_t *>(words) + chain0, -D, nlive - 1 - c, group, c == 0, act, lane, w, P, G,
+                      start, s_map, s_in, out);
     if (w == 0 && act && c == 0 && dh0) {
 #pragma unroll
         for (int v = 0; v < V; ++v) dh0[ch + v] = out[v];
