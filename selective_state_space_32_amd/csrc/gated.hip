@@ -78,13 +78,14 @@ Plan make_plan(const ssm_dims *dm) {
 int run_of(const Plan &p, int64_t nitem) { return p.lines && p.chains * nitem >= 4096 ? 8 : 1; }
 
 // Items of a chain that share a hand-over (see the kernel).  A hand-over takes about 1.2 us, and while it
-// runs the other chains move 0.013 us of data each per item: with many chains every item can wait for
-// the one before it, and the maps' traffic is saved (B8 L2048 D5120 bf16, 320 chains: 172 us with groups
-// of one, 179 with eight; backward 312 and 323), with few the hand-overs have to be shared (B1 L131072
-// D2048, 16 chains: 662 us with one, 486 with four or eight; B2 L2048 D1536 fp32, 48 chains: 26.8, 22.3).
+// runs every chain moves 0.013 us of data per item: with many chains every item can wait for the one
+// before it, and the maps' traffic is saved (B8 L2048 D5120 bf16, 320 chains: 172 us with groups of one,
+// 179 with eight, backward 309 and 323; B2 L8192 D5120, 80 chains: 180 with one, 184 with four), with few
+// the hand-overs have to be shared (B1 L131072 D2048, 16 chains: 662 us with one, 486 with four or eight;
+// B2 L2048 D1536 fp32, 48 chains: 28, 25).
 int group_of(const Plan &p) {
     int g = 1;
-    while (g < ssm::kGatedGroup && g * p.chains < 192) g *= 2;
+    while (g < ssm::kGatedGroup && g * p.chains < 64) g *= 2;
     return g;
 }
 
