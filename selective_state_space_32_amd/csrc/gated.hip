@@ -72,27 +72,42 @@ Plan make_plan(const ssm_dims *dm) {
     return p;
 }
 
-// Consecutive workgroups that draw from one queue (see the kernel): 8 where the launch is many rounds of
-// the chip and rows are whole lines, so that bandwidth counts; 1 where it is short and hand-overs count
-// (B2 L2048 D1536 fp32: 23 us, 26 with 8), or where neighbouring tiles share lines.
+// Queues that share the chains (see the kernel): as many as there are XCDs, unless some would then be more
+// than a quarter longer than the average; every queue has as many workgroups as the longest needs, and
+// those without an item still have to be dispatched (B1 L65536 D64 bf16, one chain: 77 us with eight
+// queues, 34 with one).
+int queues_of(const Plan &p) {
+    auto slots = [&](int64_t q) { return (p.chains + q - 1) / q * q; };
+    int best = ssm::kGatedQueues;
+    if (4 * slots(best) <= 5 * p.chains) return best;
+    for (int q = best - 1; q >= 1; --q)
+        if (slots(q) < slots(best)) best = q;
+    return best;
+}
+
+// Consecutive workgroups that draw from one queue: 1 where the launch is short and hand-overs count (B2
+// L2048 D1536 fp32: 23 us, 26 with 8) or neighbouring tiles share lines; 8 where it is many rounds of the
+// chip and rows are whole lines, so that bandwidth counts.
 int run_of(const Plan &p, int64_t nitem) { return p.lines && p.chains * nitem >= 4096 ? 8 : 1; }
 
 // Items of a chain that share a hand-over (see the kernel).  A hand-over takes about 1.2 us, and while it
 // runs every chain moves 0.013 us of data per item: with many chains every item can wait for the one
 // before it, and the maps' traffic is saved (B8 L2048 D5120 bf16, 320 chains: 172 us with groups of one,
 // 179 with eight, backward 309 and 323; B2 L8192 D5120, 80 chains: 180 with one, 184 with four), with few
-// the hand-overs have to be shared (B1 L131072 D2048, 16 chains: 662 us with one, 486 with four or eight;
-// B2 L2048 D1536 fp32, 48 chains: 28, 25).
+// the hand-overs have to be shared (B1 L131072 D2048, 16 chains: 701 us with one, 520 with four or eight;
+// B1 L65536 D512, 4 chains: 168 with two, 97 with eight, 93 with 16 or 32; D64, 1 chain: 98 with eight, 34
+// with 64; B2 L2048 D1536 fp32, 48 chains: 28 with one, 25 with two or four).
 int group_of(const Plan &p) {
     int g = 1;
-    while (g < ssm::kGatedGroup && g * p.chains < 64) g *= 2;
+    if (p.chains < 64)
+        while (g < ssm::kGatedGroup && g * p.chains < 96) g *= 2;
     return g;
 }
 
 // One workgroup per (chain, item), the chains dealt to the queues in turn.
 int64_t grid_of(const Plan &p, int64_t nitem) {
-    const int64_t per = (p.chains + ssm::kGatedQueues - 1) / ssm::kGatedQueues * nitem, run = run_of(p, nitem);
-    return (per + run - 1) / run * run * ssm::kGatedQueues;   // (per: items of the longest queue, or more)
+    const int64_t q = queues_of(p), per = (p.chains + q - 1) / q * nitem, run = run_of(p, nitem);
+    return (per + run - 1) / run * run * q;   // (per: items of the longest queue)
 }
 
 // A launch holds fewer than 2^32 threads.
@@ -130,7 +145,7 @@ void launch_fwd_v(const void *x, const void *r, const void *g, const float *A, c
                        0, st, static_cast<const IO *>(x), static_cast<const IO *>(r),
                        static_cast<const IO *>(g), A, static_cast<const IO *>(z), h0, sl, static_cast<IO *>(y), last,
                        states, words, counters, dm->seqlen, dm->dim, (int)p.tiles, (int)p.chains, (int)nitem,
-                       (int)p.nchunk, run_of(p, nitem), group_of(p));
+                       (int)p.nchunk, queues_of(p), run_of(p, nitem), group_of(p));
 }
 
 // Items of two chunks halve the hand-overs of a chain, at two workgroups per CU instead of three.  They
@@ -181,7 +196,7 @@ void launch_bwd_v(const void *x, const void *r, const void *g, const float *A, c
                        static_cast<const IO *>(z), h0, sl, static_cast<const IO *>(dy), dlast,
                        static_cast<const float *>(states), static_cast<IO *>(dx), static_cast<IO *>(dr),
                        static_cast<IO *>(dg), static_cast<IO *>(dz), part, dh0, words, counters, dm->seqlen, dm->dim,
-                       (int)p.tiles, (int)p.chains, (int)p.nchunk, run_of(p, p.nchunk), group_of(p));
+                       (int)p.tiles, (int)p.chains, (int)p.nchunk, queues_of(p), run_of(p, p.nchunk), group_of(p));
 }
 
 }  // namespace

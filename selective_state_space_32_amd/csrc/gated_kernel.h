@@ -16,41 +16,44 @@
 //      the chunks before it (the chain, below) and publishes the state at its end,
 //   3. every wave folds the maps of the waves before it onto that state and walks its tokens again
 //      from there, writing y.
-// The inputs are read once and the outputs written once, whatever the length.  Bound: HBM.  Per element
-// the forward moves 8 bytes in bf16 (10 with a gate) and issues about 45 VALU instructions, 7 of them
-// transcendental (two sigmoids, the decay, a root); the backward moves 14 (18) and issues about 95,
-// three quarters of what the VALU can do in the time that HBM takes.  The chain adds 1/64 of (8 to
-// clear, 8 to publish, 8 to 40 to read, 4 of state) bytes per element, 4 % of the gated forward's.
-// Measured (a copy of 1 GiB reaches 5.1 TB/s on this card): B8 L2048 D5120 bf16 gated 172 us for
-// 839 MB, its backward 313 us for 1,510 MB; B1 L131072 D2048 bf16 455 us for 2,148 MB; B2 L2048 D1536
-// fp32 22 us for 101 MB, its backward 37 us for 176 MB.
+// The inputs are read once and the outputs written once, whatever the length.
 //
-// The split.  Eight tokens per wave keep a lane's values of V channels in registers (70 registers, three
-// workgroups per CU, in the forward; 128, two, in the backward); eight waves make the chain's word an
-// item's thousandth part, and two or three workgroups per CU let one load while another computes or
-// waits.  Sixteen waves of eight tokens (221 us at B8 L2048 D5120) and eight of sixteen (184 us) were
-// slower than eight of eight (169 us): fewer workgroups overlap.
+// Bound: HBM.  Per element the forward moves 8 bytes in bf16 (10 with a gate) and issues 47 VALU
+// instructions with its gate, 8 of them transcendental (three sigmoids, the decay, a root); the
+// backward moves 14 (18) and issues 90, which keeps the VALU busy for two thirds of its time.
+// Measured, where a copy of 1 GiB reaches 5.1 TB/s: B8 L2048 D5120 bf16 gated 172 us for 839 MB (855
+// by the counters), its backward 309 us for 1,510 MB (1,537); B1 L131072 D2048 bf16 455 us for 2,148
+// MB; B2 L2048 D1536 fp32 22 us for 101 MB, its backward 37 us for 176 MB.  Short launches are bound by
+// their latency: 7 us for one chunk in a few tiles.
 //
-// The chain.  Handing the state from chunk to chunk would cost a round trip through memory per chunk,
-// so with few chains the chunks of a chain form groups of up to kGatedGroup (the host chooses).  word[sequence][item][channel] is 64 bits: a
-// chunk publishes its map (P, H), two floats, as soon as it has it; the last chunk of a group
-// publishes instead the state at its end, as (-1, h), once it knows it.  A chunk fetches the maps of
-// the chunks before it in its group (which wait for nobody), composes them, and applies them to the
+// The split.  Eight tokens per wave keep a lane's values of V channels in registers (70 registers in
+// the forward, three workgroups per CU; 128 in the backward, two), and several workgroups per CU let
+// one load while another computes or waits.  At B8 L2048 D5120, sixteen waves of eight tokens took
+// 221 us and eight of sixteen 184 where eight of eight took 169: fewer workgroups overlap.
+//
+// The chain.  The state goes from chunk to chunk through memory.  With many chains every chunk waits for
+// the one before it (chain_hand): state[sequence][chunk][channel], four bytes, all ones meaning that
+// nothing is there yet; the forward's are also the states that the backward starts from.  With few
+// chains a round trip per chunk would be all that happens, so the chunks of a chain form groups (the
+// host chooses their size; chain_step): word[sequence][item][channel] is 64 bits, a chunk publishes
+// its map (P, H), two floats, as soon as it has it, and the last chunk of a group publishes instead the
+// state at its end, as (-1, h), once it knows it.  A chunk fetches the maps of the chunks before it in
+// its group (which wait for nobody; the waves share them), composes them, and applies them to the
 // state that the group before left.  Only the groups' last chunks wait in line.  The chain's first
-// chunk publishes the constant map (0, state at its end): it alone reads the initial state.  The words are filled
-// with ones ("nothing yet") before the kernel starts; the two halves travel in one 64-bit store, so a
-// word that is read is whole and nothing else has to be ordered.  Which words a chunk combines, and
-// in which order, is fixed: the results do not depend on timing.
+// chunk publishes the constant map (0, state at its end): it alone reads the initial state.
+// The words are filled with ones before the kernel starts.  A word travels in one store, so one that is
+// read is whole and nothing else has to be ordered.  Which words a chunk combines, and in which order,
+// is fixed: the results do not depend on timing.
 //
-// Every wait ends: an item's number is drawn from a counter when its workgroup starts, and the
-// items of a chain are numbered in the order of the chain.  Whoever waits, waits for items that
-// started earlier, and the earliest of those waits for nobody.  There are kGatedQueues counters (one
+// Every wait ends: an item's number is drawn from a counter when its workgroup starts, and the items
+// of a chain are numbered in the order of the chain.  Whoever waits, waits for items that started
+// earlier, and the earliest of those waits for nobody.  There are up to kGatedQueues counters (one
 // alone is fought over by the whole chip: 768 workgroups that start together wait 9 us), each with an
 // equal run of the chains; `run` consecutive workgroups draw from the same one.  The XCDs take
-// workgroups in turn, so with run = 1 a queue's chains stay in one XCD: its hand-overs are the
-// fastest, and neighbouring tiles, which share lines where rows do not start on one, meet in its L2
-// (B8 L2048 D5119 bf16 backward: 381 us, 440 with run = 8).  With run = 8 every XCD works on all the
-// chains, where with run = 1 it reads the same few columns of every row, which lie in few of the
+// workgroups in turn, so with eight queues and run = 1 a queue's chains stay in one XCD: its hand-overs
+// are the fastest, and neighbouring tiles, which share lines where rows do not start on one, meet in
+// its L2 (B8 L2048 D5119 bf16 backward: 381 us, 440 with run = 8).  With run = 8 every XCD works on all
+// the chains, where with run = 1 it reads the same few columns of every row, which lie in few of the
 // memory's channels (B1 L131072 D2048 bf16: 552 against 513 us).
 #pragma once
 
@@ -63,8 +66,8 @@ namespace ssm {
 constexpr int kGatedRows = 8;                            // tokens per wave
 constexpr int kGatedWaves = 8;                           // waves per workgroup
 constexpr int kGatedChunk = kGatedRows * kGatedWaves;    // tokens per stored state (and per item of the backward)
-constexpr int kGatedGroup = 8;                           // most items of a chain that share a hand-over
-constexpr int kGatedQueues = 8;                          // counters (one per XCD)
+constexpr int kGatedGroup = 64;                          // most items of a chain that share a hand-over
+constexpr int kGatedQueues = 8;                          // counters, at most (one per XCD)
 constexpr int kGatedCounterStride = 64;                  // ints between them: lines of their own
 
 // 1 - a^2 = -expm1(2 ln 2 y), given y = log2(a) <= 0 and a.  Near a = 1 the difference loses every
@@ -172,9 +175,8 @@ __device__ __forceinline__ uint64_t chain_read(const uint64_t *w) {
 template <int V>
 __device__ __forceinline__ void chain_step(uint64_t *base, int64_t stride, int pos, int group, bool ends, bool act, int lane,
                                            int w, const float (&P)[V], const float (&H)[V], const float (&start)[V],
-                                           uint64_t (&s_map)[kGatedGroup][64 * V], float (&s_in)[64 * V],
+                                           float (&s_map)[2][kGatedWaves][64 * V], float (&s_in)[64 * V],
                                            float (&out)[V]) {
-    static_assert(kGatedGroup <= kGatedWaves, "a wave fetches a map");
     const int g = pos % group;
     uint64_t *own = base + pos * stride;
     if (w == 0 && act && !ends && g != group - 1) {
@@ -183,21 +185,35 @@ __device__ __forceinline__ void chain_step(uint64_t *base, int64_t stride, int p
             if (pos == 0) chain_put(own + v, 0.0f, fmaf(P[v], start[v], H[v]));
             else chain_put(own + v, P[v], H[v]);
     }
-    if (w < g) {   // the map of the group's item w
-        const uint64_t *src = base + (pos - g + w) * stride;
-        uint64_t u[V];
-        for (;;) {
-            bool all = true;
+    // the maps of the group's items before this one, in equal runs over the waves: each composes its run
+    const int m = (g + kGatedWaves - 1) / kGatedWaves, lo = w * m, hi = min(lo + m, g);
+    if (lo < hi) {
+        const uint64_t *src = base + (pos - g + lo) * stride;
+        float cp[V], ch[V];
+        for (int k = lo; k < hi; ++k, src += stride) {
+            uint64_t u[V];
+            for (;;) {
+                bool all = true;
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+                    u[v] = chain_read(src + v);
+                    all = all && (uint32_t)(u[v] >> 32) != kWordEmpty;
+                }
+                if (__all(all || !act)) break;
+                __builtin_amdgcn_s_sleep(1);
+            }
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                u[v] = chain_read(src + v);
-                all = all && (uint32_t)(u[v] >> 32) != kWordEmpty;
+                const float p = __uint_as_float((uint32_t)(u[v] >> 32)), h = __uint_as_float((uint32_t)u[v]);
+                ch[v] = k == lo ? h : fmaf(p, ch[v], h);
+                cp[v] = k == lo ? p : cp[v] * p;
             }
-            if (__all(all || !act)) break;
-            __builtin_amdgcn_s_sleep(1);
         }
 #pragma unroll
-        for (int v = 0; v < V; ++v) s_map[w][lane * V + v] = u[v];
+        for (int v = 0; v < V; ++v) {
+            s_map[0][w][lane * V + v] = cp[v];
+            s_map[1][w][lane * V + v] = ch[v];
+        }
     }
     if (g > 0) __syncthreads();
     if (w == 0) {
@@ -205,12 +221,11 @@ __device__ __forceinline__ void chain_step(uint64_t *base, int64_t stride, int p
 #pragma unroll
         for (int v = 0; v < V; ++v) cp[v] = 1.0f, ch[v] = 0.0f;
 #pragma unroll 2
-        for (int k = 0; k < g; ++k)
+        for (int k = 0; k * m < g; ++k)
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                const uint64_t u = s_map[k][lane * V + v];
-                const float p = __uint_as_float((uint32_t)(u >> 32));
-                ch[v] = fmaf(p, ch[v], __uint_as_float((uint32_t)u));
+                const float p = s_map[0][k][lane * V + v];
+                ch[v] = fmaf(p, ch[v], s_map[1][k][lane * V + v]);
                 cp[v] *= p;
             }
         if (pos == g) {   // the first group: position 0 has taken the start in (0 elsewhere)
@@ -287,13 +302,13 @@ __device__ __forceinline__ void chain_hand(uint32_t *base, int64_t stride, int p
 struct GatedItem {
     int b, tile, pos;
 };
-__device__ __forceinline__ GatedItem gated_item(int chains, int tiles, int nitem, bool ragged, int *counters, int run,
-                                                int *slot) {
-    const int q = (int)blockIdx.x / run % kGatedQueues;
-    const int first = (int)((int64_t)chains * q / kGatedQueues);
-    const int nq = (int)((int64_t)chains * (q + 1) / kGatedQueues) - first;
+__device__ __forceinline__ GatedItem gated_item(int chains, int tiles, int nitem, bool ragged, int *counters,
+                                                int queues, int run, int *slot) {
+    const int q = (int)blockIdx.x / run % queues;
+    const int first = (int)((int64_t)chains * q / queues);
+    const int nq = (int)((int64_t)chains * (q + 1) / queues) - first;
     if (nq == 0) return {0, 0, -1};
-    int n = (int)blockIdx.x / (run * kGatedQueues) * run + (int)blockIdx.x % run;
+    int n = (int)blockIdx.x / (run * queues) * run + (int)blockIdx.x % run;
     if (counters) {   // (one item per sequence: no chain, any order will do)
         if (threadIdx.x == 0)
             *slot = __hip_atomic_fetch_add(&counters[q * kGatedCounterStride], 1, __ATOMIC_RELAXED,
@@ -342,14 +357,14 @@ gated_scan_kernel(const IO *__restrict__ x, const IO *__restrict__ r, const IO *
                   const float *__restrict__ A, const IO *__restrict__ z, const float *h0,
                   const int32_t *__restrict__ seq_lens, IO *__restrict__ y, float *last,
                   float *states, void *words, int *counters, int64_t L, int64_t D, int tiles, int chains, int nitem, int nchunk,
-                  int run, int group) {
+                  int queues, int run, int group) {
     constexpr int C = T * K, M = C / kGatedChunk;
-    static_assert(C % kGatedChunk == 0 && K % M == 0, "a stored state is at a wave's end");
+    static_assert(K == kGatedWaves && C % kGatedChunk == 0 && K % M == 0, "a stored state is at a wave's end");
     using Row = row_words<V, IO, NT>;
     __shared__ float s_P[K][64 * V], s_H[K][64 * V], s_in[64 * V];
-    __shared__ uint64_t s_map[kGatedGroup][64 * V];
+    __shared__ float s_map[2][kGatedWaves][64 * V];
     __shared__ int s_slot;
-    const GatedItem it = gated_item(chains, tiles, nitem, seq_lens != nullptr, counters, run, &s_slot);
+    const GatedItem it = gated_item(chains, tiles, nitem, seq_lens != nullptr, counters, queues, run, &s_slot);
     if (it.pos < 0) return;
     const int b = it.b, c = it.pos;
     const int lane = threadIdx.x & 63;
@@ -508,13 +523,14 @@ gated_bwd_kernel(const IO *__restrict__ x, const IO *__restrict__ r, const IO *_
                  const int32_t *__restrict__ seq_lens, const IO *__restrict__ dy, const float *__restrict__ dlast,
                  const float *__restrict__ states, IO *__restrict__ dx, IO *__restrict__ dr, IO *__restrict__ dg,
                  IO *__restrict__ dz, float *__restrict__ part, float *__restrict__ dh0, void *words,
-                 int *counters, int64_t L, int64_t D, int tiles, int chains, int nchunk, int run, int group) {
+                 int *counters, int64_t L, int64_t D, int tiles, int chains, int nchunk, int queues, int run,
+                 int group) {
     constexpr int T = kGatedRows, K = kGatedWaves, C = kGatedChunk;
     using Row = row_words<V, IO, NT>;
     __shared__ float s_P[K][64 * V], s_H[K][64 * V], s_G[K][64 * V], s_in[64 * V];
-    __shared__ uint64_t s_map[kGatedGroup][64 * V];
+    __shared__ float s_map[2][kGatedWaves][64 * V];
     __shared__ int s_slot;
-    const GatedItem it = gated_item(chains, tiles, nchunk, seq_lens != nullptr, counters, run, &s_slot);
+    const GatedItem it = gated_item(chains, tiles, nchunk, seq_lens != nullptr, counters, queues, run, &s_slot);
     if (it.pos < 0) return;
     const int b = it.b, c = nchunk - 1 - it.pos;
     const int lane = threadIdx.x & 63;
