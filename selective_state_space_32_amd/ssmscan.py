@@ -734,11 +734,19 @@ def _addr(t: Optional[torch.Tensor]):
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _stream_addr(stream):
+def _stream_addr(stream, dev: torch.device, *made: Optional[torch.Tensor]):
+    """The handle of the stream to launch on (None: the current one), for tensors on `dev`.  `made`:
+    tensors allocated for this call; on a stream of the caller's they are kept from being handed out
+    again before its work is done."""
+    if dev.type != "cuda" or dev.index != torch.cuda.current_device():
+        raise ValueError(f"the tensors are on {dev}, which is not the current GPU")
     if stream is not None:
+        for t in made:
+            if t is not None:
+                t.record_stream(stream)
         return stream.cuda_stream
     if _raw_stream is not None:
-        return _raw_stream(torch.cuda.current_device())
+        return _raw_stream(dev.index)
     return torch.cuda.current_stream().cuda_stream
 
 
@@ -797,9 +805,10 @@ def gated_scan_fwd(x: torch.Tensor, r: torch.Tensor, g: torch.Tensor, A: torch.T
     if workspace is None:
         need = int(lib.ssm_gated_scan_workspace_bytes(ctypes.byref(dims)))
         workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    _check(lib.ssm_gated_scan_fwd(_addr(x), _addr(r), _addr(g), _addr(A), _addr(z), _addr(initial_state), _addr(seq_lens),
-                                  _addr(y), _addr(last_state), ctypes.byref(dims), _addr(workspace),
-                                  workspace.numel() * workspace.element_size(), _stream_addr(stream)))
+    st = _stream_addr(stream, dev, y, last_state, workspace)
+    _check(lib.ssm_gated_scan_fwd(_addr(x), _addr(r), _addr(g), _addr(A), _addr(z), _addr(initial_state),
+                                  _addr(seq_lens), _addr(y), _addr(last_state), ctypes.byref(dims), _addr(workspace),
+                                  workspace.numel() * workspace.element_size(), st))
     return (y, last_state, workspace) if save_checkpoints else (y, last_state)
 
 
@@ -828,21 +837,18 @@ def gated_scan_bwd(dy: torch.Tensor, x: torch.Tensor, r: torch.Tensor, g: torch.
     if workspace is None:
         need = int(lib.ssm_gated_scan_bwd_workspace_bytes(ctypes.byref(dims)))
         workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    # (sequences of one chunk need no checkpoints, and their forward's workspace is empty)
     have = 0 if checkpoints is None else checkpoints.numel() * checkpoints.element_size()
-    # (a forward that needed no workspace left none to read: nothing is recomputed then either)
-    _check(lib.ssm_gated_scan_bwd(_addr(x), _addr(r), _addr(g), _addr(A), _addr(z), _addr(initial_state), _addr(seq_lens),
-                                  _addr(dy), _addr(dlast_state), _addr(checkpoints) if have else None, have,
+    st = _stream_addr(stream, dev, workspace, *grads.values())
+    _check(lib.ssm_gated_scan_bwd(_addr(x), _addr(r), _addr(g), _addr(A), _addr(z), _addr(initial_state),
+                                  _addr(seq_lens), _addr(dy), _addr(dlast_state), _addr(checkpoints) if have else None, have,
                                   _addr(grads["dx"]), _addr(grads["dr"]), _addr(grads["dg"]), _addr(grads["dA"]),
                                   _addr(grads.get("dz")), _addr(grads.get("dinitial_state")), ctypes.byref(dims),
-                                  _addr(workspace), workspace.numel() * workspace.element_size(),
-                                  _stream_addr(stream)))
+                                  _addr(workspace), workspace.numel() * workspace.element_size(), st))
     return grads
 
 
-def gated_step(state: torch.Tensor, x: torch.Tensor, r: torch.Tensor, g: torch.Tensor, A: torch.Tensor,
-               z: Optional[torch.Tensor] = None, *, y: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
-    """One token of the gated linear recurrence (ssm_gated_step); `state` (S, dim) float32 is
-    updated in place.  x, r, g, z: (S, dim) of one dtype; A: (dim,) float32.  Returns y (S, dim)."""
+def _gated_step_args(state, x, r, g, A, z, y, stream):
     if x.dim() != 2:
         raise ValueError("x must be (sequences, dim)")
     S, dim = x.shape
@@ -859,9 +865,29 @@ def gated_step(state: torch.Tensor, x: torch.Tensor, r: torch.Tensor, g: torch.T
         y = torch.empty_like(x)
     else:
         _want(y, "y", (S, dim), io, dev)
-    _check(lib.ssm_gated_step(_addr(state), _addr(x), _addr(r), _addr(g), _addr(A), _addr(z), _addr(y), ctypes.byref(dims),
-                              _stream_addr(stream)))
+    args = (_addr(state), _addr(x), _addr(r), _addr(g), _addr(A), _addr(z), _addr(y), ctypes.byref(dims),
+            _stream_addr(stream, dev, y))
+    return args, (state, x, r, g, A, z, y, dims), y
+
+
+def gated_step(state: torch.Tensor, x: torch.Tensor, r: torch.Tensor, g: torch.Tensor, A: torch.Tensor,
+               z: Optional[torch.Tensor] = None, *, y: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """One token of the gated linear recurrence (ssm_gated_step); `state` (S, dim) float32 is
+    updated in place.  x, r, g, z: (S, dim) of one dtype; A: (dim,) float32.  Returns y (S, dim)."""
+    args, _keep, y = _gated_step_args(state, x, r, g, A, z, y, stream)
+    _check(lib.ssm_gated_step(*args))
     return y
+
+
+def gated_step_call(state: torch.Tensor, x: torch.Tensor, r: torch.Tensor, g: torch.Tensor, A: torch.Tensor,
+                    z: Optional[torch.Tensor] = None, *, y: Optional[torch.Tensor] = None,
+                    stream=None) -> Callable[[], None]:
+    """The gated_step call checked and marshalled once (see scan_fwd_call)."""
+    args, keep, _y = _gated_step_args(state, x, r, g, A, z, y, stream)
+
+    def call(_args=args, _keep=keep):
+        _check(lib.ssm_gated_step(*_args))
+    return call
 
 
 NORM_SUM_F32 = 1   # flag bit of the layer norm's entry points (include/ssmscan.h)
@@ -912,9 +938,10 @@ def layernorm_fwd(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Te
         total = torch.empty(shape, dtype=kept, device=dev)
     mean = torch.empty(shape[:-1], dtype=torch.float32, device=dev)
     rstd = torch.empty_like(mean)
+    st = _stream_addr(stream, dev, y, total, mean, rstd)
     _check(lib.ssm_layernorm_fwd(_addr(x), _addr(residual), _addr(weight), _addr(bias), float(eps),
                                  NORM_SUM_F32 if kept != io else 0, _addr(y), _addr(total), _addr(mean), _addr(rstd),
-                                 ctypes.byref(dims), _stream_addr(stream)))
+                                 ctypes.byref(dims), st))
     return y, x if total is None else total, mean, rstd
 
 
@@ -953,8 +980,9 @@ def layernorm_bwd(dy: torch.Tensor, total: torch.Tensor, weight: torch.Tensor, m
             need = int(lib.ssm_layernorm_bwd_workspace_bytes(ctypes.byref(dims)))
             workspace = torch.empty(need, dtype=torch.uint8, device=dev)
     have = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    st = _stream_addr(stream, dev, workspace, *grads.values())
     _check(lib.ssm_layernorm_bwd(_addr(dy), _addr(total), _addr(weight), _addr(mean), _addr(rstd), _addr(dresidual),
                                  NORM_SUM_F32 if kept != io else 0, _addr(ds), _addr(grads.get("dx")),
                                  _addr(grads.get("dweight")), _addr(grads.get("dbias")), ctypes.byref(dims),
-                                 _addr(workspace) if have else None, have, _stream_addr(stream)))
+                                 _addr(workspace) if have else None, have, st))
     return grads

@@ -262,6 +262,20 @@ def test_step_unaligned():
     close(st, rlast, "f32", 1e-5, "state")
 
 
+def test_step_call_repeats():
+    """The marshalled call advances the same state token by token, like gated_step."""
+    c = Case(3, 1, 130, "bf16", seed=1960)
+    cut = [c.t[k][:, 0].contiguous() for k in ("x", "r", "g", "z")]
+    a, b = c.t["h0"].clone(), c.t["h0"].clone()
+    y = torch.empty_like(cut[0])
+    call = ssmscan.gated_step_call(a, *cut[:3], c.t["A"], cut[3], y=y)
+    for _ in range(4):
+        call()
+        y2 = ssmscan.gated_step(b, *cut[:3], c.t["A"], cut[3])
+        torch.cuda.synchronize()
+        assert torch.equal(a, b) and torch.equal(y, y2)
+
+
 def test_same_from_run_to_run():
     """No result depends on the order in which workgroups run: several calls are bitwise equal."""
     c = Case(4, 900, 300, "bf16", seed=2000, lens=[900, 5, 450, 899])
@@ -307,6 +321,22 @@ def test_another_stream():
         y3, last3 = ssmscan.gated_scan_fwd(*a, **k)
     s.synchronize()
     assert torch.equal(y, y2) and torch.equal(y, y3) and torch.equal(last, last3)
+
+
+def test_workspace_of_another_stream_is_kept():
+    """A call on a stream of the caller's: the workspace it allocated is not handed out again while that
+    stream may still use it (nothing is allocated on the caller's stream between the calls)."""
+    c = Case(8, 2000, 512, "bf16", seed=2025)
+    a, k = c.fwd_args()
+    y, last = run_fwd(c)
+    s = torch.cuda.Stream()
+    outs = [torch.empty_like(y) for _ in range(6)]
+    torch.cuda.synchronize()
+    for o in outs:
+        ssmscan.gated_scan_fwd(*a, **k, y=o, stream=s, return_last_state=False)
+        torch.empty(1 << 26, dtype=torch.uint8, device="cuda").fill_(0x3F)   # what the allocator hands out next
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, y) for o in outs)
 
 
 def test_graph_replays():

@@ -212,3 +212,14 @@ def test_binding_refusals(b):
         b.layernorm_bwd(v, torch.zeros(4, 8, dtype=torch.bfloat16), w, torch.zeros(4), torch.zeros(4))
     with pytest.raises((ValueError, TypeError)):
         b.layernorm_bwd(v, v, w, torch.zeros(4, 1), torch.zeros(4))
+
+
+def test_host_tensors_are_refused(b):
+    """Tensors in host memory, everything else right: refused by name, before the library is called."""
+    import torch
+    x, A, v, w = torch.zeros(2, 5, 8), torch.zeros(8), torch.zeros(4, 8), torch.zeros(8)
+    for call in (lambda: b.gated_scan_fwd(x, x, x, A), lambda: b.gated_scan_bwd(x, x, x, x, A),
+                 lambda: b.gated_step(v, v, v, v, A), lambda: b.layernorm_fwd(v, w),
+                 lambda: b.layernorm_bwd(v, v, w, torch.zeros(4), torch.zeros(4))):
+        with pytest.raises((ValueError, RuntimeError, AssertionError), match="cpu|CUDA|NVIDIA|HIP|GPU"):
+            call()
