@@ -98,20 +98,23 @@ __device__ __forceinline__ float one_minus_square(float y, float a) {
 // dwords at any byte address).  NT: past the caches, as data that is used once; not where rows start
 // inside a line, whose other part a neighbouring tile wants (B8 L2048 D5119 bf16: 214 against 231 us,
 // backward 417 against 527; at D5120 the other way round, 189 against 176 us).
+#define SSM_GLOBAL __attribute__((address_space(1)))   // memory of the device: no other kind is tried
 template <int V, typename IO, bool NT = true> struct row_words {
     static constexpr int W = V * (int)sizeof(IO) < 4 ? 1 : V * (int)sizeof(IO) / 4;
     uint32_t w[W];
     // row: the row's start (the same for the wave), lofs: the lane's byte offset in it -- the memory
-    // instructions take the two as they are, without address arithmetic per lane.
+    // instructions take the two as they are.  (Left to itself the compiler adds the offset to the
+    // tensor's start once and the row to that, a 64-bit addition per lane and access.)
     __device__ __forceinline__ void load(const IO *row, uint32_t lofs) {
-        const char *p = reinterpret_cast<const char *>(row) + lofs;
+        asm("" : "+s"(row));
+        const SSM_GLOBAL char *p = (const SSM_GLOBAL char *)row + lofs;
         if constexpr (V * sizeof(IO) < 4) {
-            w[0] = *reinterpret_cast<const IO *>(p);
+            w[0] = *(const SSM_GLOBAL IO *)p;
         } else {
             typedef uint32_t any_u32 __attribute__((ext_vector_type(W), aligned(sizeof(IO))));
             any_u32 v;
-            if constexpr (NT) v = __builtin_nontemporal_load(reinterpret_cast<const any_u32 *>(p));
-            else v = *reinterpret_cast<const any_u32 *>(p);
+            if constexpr (NT) v = __builtin_nontemporal_load((const SSM_GLOBAL any_u32 *)p);
+            else v = *(const SSM_GLOBAL any_u32 *)p;
             __builtin_memcpy(w, &v, sizeof w);
         }
     }
@@ -129,9 +132,10 @@ template <int V, typename IO, bool NT = true> struct row_words {
         for (int i = 0; i < W; ++i) asm volatile("" : "+v"(w[i]));
     }
     __device__ __forceinline__ static void store(IO *row, uint32_t lofs, const float (&y)[V]) {
-        char *p = reinterpret_cast<char *>(row) + lofs;
+        asm("" : "+s"(row), "+v"(lofs));
+        SSM_GLOBAL char *p = (SSM_GLOBAL char *)row + lofs;
         if constexpr (V * sizeof(IO) < 4) {
-            io<IO>::st(reinterpret_cast<IO *>(p), 0, y[0]);
+            *(SSM_GLOBAL IO *)p = (IO)f32x2_to_bf16x2(y[0], 0.0f);
         } else {
             uint32_t o[W];
             if constexpr (sizeof(IO) == 2) {
@@ -144,8 +148,8 @@ template <int V, typename IO, bool NT = true> struct row_words {
             typedef uint32_t any_u32 __attribute__((ext_vector_type(W), aligned(sizeof(IO))));
             any_u32 v;
             __builtin_memcpy(&v, o, sizeof o);
-            if constexpr (NT) __builtin_nontemporal_store(v, reinterpret_cast<any_u32 *>(p));
-            else *reinterpret_cast<any_u32 *>(p) = v;
+            if constexpr (NT) __builtin_nontemporal_store(v, (SSM_GLOBAL any_u32 *)p);
+            else *(SSM_GLOBAL any_u32 *)p = v;
         }
     }
 };
@@ -379,12 +383,15 @@ gated_scan_kernel(const IO *__restrict__ x, const IO *__restrict__ r, const IO *
     const int64_t t0 = (int64_t)c * C + w * T;
     const int64_t row0 = (int64_t)b * L;
     const int nlive = (int)((Lb + C - 1) / C);   // items of this sequence that hold tokens
+    // the wave's tokens that exist, and those with inputs (none or fewer: t0 is past the end)
+    const int nrow = (int)min((int64_t)T, L - t0), nin = (int)min((int64_t)T, Lb - t0);
+    const int64_t e0 = (row0 + t0) * D;
 
     if (c >= nlive) {   // past the sequence's end
         if constexpr (OUT) {
             if (act) {
                 const float zero[V] = {};
-                for (int64_t t = t0; t < min(t0 + T, L); ++t) Row::store(y + (row0 + t) * D, lofs, zero);
+                for (int k = 0; k < nrow; ++k) Row::store(y + (e0 + k * D), lofs, zero);
                 if (last && c == 0 && w == 0)
                     for (int v = 0; v < V; ++v) last[(int64_t)b * D + d + v] = h0 ? h0[(int64_t)b * D + d + v] : 0.0f;
             }
@@ -396,7 +403,7 @@ gated_scan_kernel(const IO *__restrict__ x, const IO *__restrict__ r, const IO *
     Row rr[T], rg[T], rx[T], rz[OUT ? T : 1];
 #pragma unroll
     for (int k = 0; k < T; ++k) {
-        const int64_t e = (row0 + min(t0 + k, Lb - 1)) * D;
+        const int64_t e = e0 + min(k, nin - 1) * D;
         rr[k].load(r + e, lofs);
         rg[k].load(g + e, lofs);
         rx[k].load(x + e, lofs);
@@ -406,10 +413,10 @@ gated_scan_kernel(const IO *__restrict__ x, const IO *__restrict__ r, const IO *
     for (int v = 0; v < V; ++v) a2[v] = A[d + v] * kLog2e;
 
     // Tokens past the end become the identity (a = 1, an input of 0) without a test per value below.
-    if (t0 + T > Lb) {
+    if (nin < T) {
 #pragma unroll
         for (int k = 0; k < T; ++k)
-            if (t0 + k >= Lb) {
+            if (k >= nin) {
                 rr[k].fill(minus_inf_words<IO>());
                 rg[k].fill(0);
                 rx[k].fill(0);
@@ -440,7 +447,7 @@ gated_scan_kernel(const IO *__restrict__ x, const IO *__restrict__ r, const IO *
     if constexpr (OUT) {
         if (z) {
 #pragma unroll
-            for (int k = 0; k < T; ++k) rz[k].load(z + (row0 + min(t0 + k, Lb - 1)) * D, lofs);
+            for (int k = 0; k < T; ++k) rz[k].load(z + (e0 + min(k, nin - 1) * D), lofs);
         }
     }
     __syncthreads();
@@ -500,9 +507,9 @@ gated_scan_kernel(const IO *__restrict__ x, const IO *__restrict__ r, const IO *
                 for (int v = 0; v < V; ++v) {
                     h[v] = fmaf(a[k][v], h[v], bb[k][v]);
                     o[v] = z ? h[v] * silu_f32(rz[k].get(v)) : h[v];
-                    if (t0 + k >= Lb) o[v] = 0.0f;
+                    if (k >= nin) o[v] = 0.0f;
                 }
-                if (act && t0 + k < L) Row::store(y + (row0 + t0 + k) * D, lofs, o);
+                if (act && k < nrow) Row::store(y + (e0 + k * D), lofs, o);
             }
         }
     }
@@ -545,12 +552,14 @@ gated_bwd_kernel(const IO *__restrict__ x, const IO *__restrict__ r, const IO *_
     const int64_t ch = (int64_t)b * D + d;                      // the channel's place in [batch][dim]
     const int64_t item = ((int64_t)b * nchunk + c) * D + d;     // and in [batch][chunk][dim]
     const int nlive = (int)((Lb + C - 1) / C);
+    const int nrow = (int)min((int64_t)T, L - t0), nin = (int)min((int64_t)T, Lb - t0);
+    const int64_t e0 = (row0 + t0) * D;
 
     if (c >= nlive) {
         if (act) {
             const float zero[V] = {};
-            for (int64_t t = t0; t < min(t0 + T, L); ++t) {
-                const int64_t e = (row0 + t) * D;
+            for (int k = 0; k < nrow; ++k) {
+                const int64_t e = e0 + k * D;
                 Row::store(dx + e, lofs, zero);
                 Row::store(dr + e, lofs, zero);
                 Row::store(dg + e, lofs, zero);
@@ -568,7 +577,7 @@ gated_bwd_kernel(const IO *__restrict__ x, const IO *__restrict__ r, const IO *_
     Row rr[T], rg[T], rx[T], ry[T], rz[GATE ? T : 1];
 #pragma unroll
     for (int k = 0; k < T; ++k) {
-        const int64_t e = (row0 + min(t0 + k, Lb - 1)) * D;
+        const int64_t e = e0 + min(k, nin - 1) * D;
         rr[k].load(r + e, lofs);
         rg[k].load(g + e, lofs);
         rx[k].load(x + e, lofs);
@@ -576,7 +585,7 @@ gated_bwd_kernel(const IO *__restrict__ x, const IO *__restrict__ r, const IO *_
     }
     if constexpr (GATE) {
 #pragma unroll
-        for (int k = 0; k < T; ++k) rz[k].load(z + (row0 + min(t0 + k, Lb - 1)) * D, lofs);
+        for (int k = 0; k < T; ++k) rz[k].load(z + (e0 + min(k, nin - 1) * D), lofs);
     }
     float Ad[V], h[V];
 #pragma unroll
@@ -587,10 +596,10 @@ gated_bwd_kernel(const IO *__restrict__ x, const IO *__restrict__ r, const IO *_
     }
 
     // Tokens past the end become the identity, and their gradients zero, without a test per value below.
-    if (t0 + T > Lb) {
+    if (nin < T) {
 #pragma unroll
         for (int k = 0; k < T; ++k)
-            if (t0 + k >= Lb) {
+            if (k >= nin) {
                 rr[k].fill(minus_inf_words<IO>());
                 rg[k].fill(0);
                 rx[k].fill(0);
@@ -725,8 +734,8 @@ gated_bwd_kernel(const IO *__restrict__ x, const IO *__restrict__ r, const IO *_
             orr[v] = ds * fmaf(-Ad[v], s[k][v], Ad[v]);
             hT[v] = bb[k][v];
         }
-        if (act && t0 + k < L) {
-            const int64_t e = (row0 + t0 + k) * D;
+        if (act && k < nrow) {
+            const int64_t e = e0 + k * D;
             Row::store(dx + e, lofs, ox);
             Row::store(dr + e, lofs, orr);
             Row::store(dg + e, lofs, og);
