@@ -52,9 +52,11 @@ constexpr int64_t kCounterInts = ssm::kGatedQueues * ssm::kGatedCounterStride;
 
 // Channels per lane: two bf16 or one fp32, four bytes an access; one bf16 too where tiles of two would
 // leave CUs idle (at most one workgroup each: B1 L512 D2048, 128 items: 7.7 against 9.0 us, backward 10.1
-// against 12.3; B1 L4096 D256: 10.4 and 15.8, 14.4 and 19.6).
+// against 12.3; B1 L4096 D256: 10.4 and 15.8, 14.4 and 19.6), and where the last of an odd width's
+// channels would be a tile of its own: its lane shares a channel with its neighbour, which has to be in
+// the same wave, as a state that is advanced in place is read by one and written by the other.
 int lane_channels(const ssm_dims *dm, int64_t nchunk) {
-    if (dm->io_dtype != SSM_IO_BF16 || dm->dim < 2) return 1;
+    if (dm->io_dtype != SSM_IO_BF16 || dm->dim % 128 == 1) return 1;
     return dm->batch * ((dm->dim + 127) / 128) * nchunk > 256 ? 2 : 1;
 }
 

@@ -374,7 +374,7 @@ gated_scan_kernel(const IO *__restrict__ x, const IO *__restrict__ r, const IO *
     const int lane = threadIdx.x & 63;
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     // The lane's first channel.  Of an odd width the last lane takes the last V channels: those it
-    // shares with its neighbour get the same values from both.
+    // shares with its neighbour (a lane of this wave: the host sees to it) get the same values from both.
     const int64_t dl = (int64_t)it.tile * 64 * V + lane * V;
     const bool act = dl < D;
     const int64_t d = min(dl, D - V);

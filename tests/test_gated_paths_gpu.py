@@ -104,6 +104,20 @@ def test_state_in_place(io, bsz, L, D):
         assert last2 is st and torch.equal(y, y2) and torch.equal(st, last)
 
 
+@pytest.mark.parametrize("ragged", [True, False])
+@pytest.mark.parametrize("bsz,L,D", [(3000, 40, 129), (1200, 130, 129), (1500, 40, 385), (3000, 40, 131)])
+def test_state_in_place_where_lanes_share_a_channel(bsz, L, D, ragged):
+    """Many sequences of an odd width, so that the tiles of a sequence run far apart in time: the state
+    advanced in place is the one written elsewhere, to the bit."""
+    c = Case(bsz, L, D, "bf16", gate=True, state=True, seed=7 * bsz + D, lens=lengths(bsz, L, 5) if ragged else None)
+    y, last = run_fwd(c)
+    state = c.t["h0"].clone()
+    a, k = c.fwd_args()
+    y2, last2 = ssmscan.gated_scan_fwd(*a, **dict(k, initial_state=state), last_state=state)
+    torch.cuda.synchronize()
+    assert last2 is state and torch.equal(y, y2) and torch.equal(last, state)
+
+
 @pytest.mark.parametrize("io", ["f32", "bf16"])
 def test_schedules_agree(io):
     """The same sequence alone, among others, and in a batch that selects other schedules."""
