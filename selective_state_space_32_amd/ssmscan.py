@@ -22,7 +22,8 @@ SSM_IO_F32 = 0
 SSM_IO_BF16 = 1
 
 STATUS = {0: "SSM_OK", -1: "SSM_ERR_NULL", -2: "SSM_ERR_SHAPE", -3: "SSM_ERR_DTYPE", -4: "SSM_ERR_ALIGN",
-          -5: "SSM_ERR_UNSUPPORTED_N", -6: "SSM_ERR_WORKSPACE", -7: "SSM_ERR_HIP", -8: "SSM_ERR_FLAGS", -9: "SSM_ERR_VALUE"}
+          -5: "SSM_ERR_UNSUPPORTED_N", -6: "SSM_ERR_WORKSPACE", -7: "SSM_ERR_HIP", -8: "SSM_ERR_FLAGS",
+          -9: "SSM_ERR_VALUE"}
 
 
 class ssm_dims(ctypes.Structure):
@@ -734,20 +735,39 @@ def _addr(t: Optional[torch.Tensor]):
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _stream_addr(stream, dev: torch.device, *made: Optional[torch.Tensor]):
-    """The handle of the stream to launch on (None: the current one), for tensors on `dev`.  `made`:
-    tensors allocated for this call; on a stream of the caller's they are kept from being handed out
-    again before its work is done."""
+def _stream_addr(stream, dev: torch.device):
+    """The handle of the stream to launch on (None: the current one), for tensors on `dev`."""
     if dev.type != "cuda" or dev.index != torch.cuda.current_device():
         raise ValueError(f"the tensors are on {dev}, which is not the current GPU")
     if stream is not None:
-        for t in made:
-            if t is not None:
-                t.record_stream(stream)
         return stream.cuda_stream
     if _raw_stream is not None:
         return _raw_stream(dev.index)
     return torch.cuda.current_stream().cuda_stream
+
+
+def _empty(shape, dtype, dev, stream):
+    """An output of a call on `stream` (None: the current one).  On a stream of the caller's it is that
+    stream's memory, so that no other work has to end before the call may write it, and also kept until
+    what the current stream does with it by then is done."""
+    if stream is None or dev.type != "cuda":
+        return torch.empty(shape, dtype=dtype, device=dev)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=dev)
+    t.record_stream(torch.cuda.current_stream())
+    return t
+
+
+def _workspace(given, need, dev, stream):
+    """The call's workspace: the caller's, or `need` bytes that it uses on `stream` alone."""
+    if given is not None:
+        if given.device != dev or not given.is_contiguous():
+            raise ValueError(f"workspace: must be contiguous and on {dev}")
+        return given
+    if stream is None or dev.type != "cuda":
+        return torch.empty(need, dtype=torch.uint8, device=dev)
+    with torch.cuda.stream(stream):
+        return torch.empty(need, dtype=torch.uint8, device=dev)
 
 
 def _need_lens(seq_lens, bsz, dev):
@@ -795,17 +815,18 @@ def gated_scan_fwd(x: torch.Tensor, r: torch.Tensor, g: torch.Tensor, A: torch.T
     `checkpoints`."""
     bsz, L, dim, dev, io, dims = _gated_inputs(x, r, g, A, z, initial_state, seq_lens)
     if y is None:
-        y = torch.empty_like(x)
+        y = _empty(x.shape, io, dev, stream)
     else:
         _want(y, "y", (bsz, L, dim), io, dev)
     if last_state is not None:
         _want(last_state, "last_state", (bsz, dim), torch.float32, dev)
     elif return_last_state:
-        last_state = torch.empty((bsz, dim), dtype=torch.float32, device=dev)
-    if workspace is None:
-        need = int(lib.ssm_gated_scan_workspace_bytes(ctypes.byref(dims)))
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    st = _stream_addr(stream, dev, y, last_state, workspace)
+        last_state = _empty((bsz, dim), torch.float32, dev, stream)
+    need = int(lib.ssm_gated_scan_workspace_bytes(ctypes.byref(dims))) if workspace is None else 0
+    if workspace is None and save_checkpoints:
+        workspace = _empty(need, torch.uint8, dev, stream)
+    workspace = _workspace(workspace, need, dev, stream)
+    st = _stream_addr(stream, dev)
     _check(lib.ssm_gated_scan_fwd(_addr(x), _addr(r), _addr(g), _addr(A), _addr(z), _addr(initial_state),
                                   _addr(seq_lens), _addr(y), _addr(last_state), ctypes.byref(dims), _addr(workspace),
                                   workspace.numel() * workspace.element_size(), st))
@@ -828,20 +849,19 @@ def gated_scan_bwd(dy: torch.Tensor, x: torch.Tensor, r: torch.Tensor, g: torch.
         _want(dlast_state, "dlast_state", (bsz, dim), torch.float32, dev)
     if checkpoints is not None and (checkpoints.device != dev or not checkpoints.is_contiguous()):
         raise ValueError("checkpoints: must be contiguous and on the device of x")
-    grads = dict(dx=torch.empty_like(x), dr=torch.empty_like(x), dg=torch.empty_like(x),
-                 dA=torch.empty((dim,), dtype=torch.float32, device=dev))
-    if z is not None:
-        grads["dz"] = torch.empty_like(x)
+    names = ("dx", "dr", "dg") if z is None else ("dx", "dr", "dg", "dz")
+    grads = {k: _empty(x.shape, io, dev, stream) for k in names}
+    grads["dA"] = _empty((dim,), torch.float32, dev, stream)
     if want_initial_state_grad:
-        grads["dinitial_state"] = torch.empty((bsz, dim), dtype=torch.float32, device=dev)
-    if workspace is None:
-        need = int(lib.ssm_gated_scan_bwd_workspace_bytes(ctypes.byref(dims)))
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        grads["dinitial_state"] = _empty((bsz, dim), torch.float32, dev, stream)
+    need = int(lib.ssm_gated_scan_bwd_workspace_bytes(ctypes.byref(dims))) if workspace is None else 0
+    workspace = _workspace(workspace, need, dev, stream)
     # (sequences of one chunk need no checkpoints, and their forward's workspace is empty)
     have = 0 if checkpoints is None else checkpoints.numel() * checkpoints.element_size()
-    st = _stream_addr(stream, dev, workspace, *grads.values())
+    st = _stream_addr(stream, dev)
     _check(lib.ssm_gated_scan_bwd(_addr(x), _addr(r), _addr(g), _addr(A), _addr(z), _addr(initial_state),
-                                  _addr(seq_lens), _addr(dy), _addr(dlast_state), _addr(checkpoints) if have else None, have,
+                                  _addr(seq_lens), _addr(dy), _addr(dlast_state),
+                                  _addr(checkpoints) if have else None, have,
                                   _addr(grads["dx"]), _addr(grads["dr"]), _addr(grads["dg"]), _addr(grads["dA"]),
                                   _addr(grads.get("dz")), _addr(grads.get("dinitial_state")), ctypes.byref(dims),
                                   _addr(workspace), workspace.numel() * workspace.element_size(), st))
@@ -862,11 +882,11 @@ def _gated_step_args(state, x, r, g, A, z, y, stream):
     if z is not None:
         _want(z, "z", (S, dim), io, dev)
     if y is None:
-        y = torch.empty_like(x)
+        y = _empty(x.shape, io, dev, stream)
     else:
         _want(y, "y", (S, dim), io, dev)
     args = (_addr(state), _addr(x), _addr(r), _addr(g), _addr(A), _addr(z), _addr(y), ctypes.byref(dims),
-            _stream_addr(stream, dev, y))
+            _stream_addr(stream, dev))
     return args, (state, x, r, g, A, z, y, dims), y
 
 
@@ -927,18 +947,16 @@ def layernorm_fwd(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Te
             raise TypeError("sum_f32 needs a float32 residual")
         _want(residual, "residual", shape, kept, dev)
     if y is None:
-        y = torch.empty_like(x)
+        y = _empty(x.shape, io, dev, stream)
     else:
         _want(y, "y", shape, io, dev)
     if total is not None:
         _want(total, "total", shape, kept, dev)
-    elif residual is not None:
-        total = torch.empty_like(residual)
-    elif kept != io:
-        total = torch.empty(shape, dtype=kept, device=dev)
-    mean = torch.empty(shape[:-1], dtype=torch.float32, device=dev)
-    rstd = torch.empty_like(mean)
-    st = _stream_addr(stream, dev, y, total, mean, rstd)
+    elif residual is not None or kept != io:
+        total = _empty(shape, kept, dev, stream)
+    mean = _empty(shape[:-1], torch.float32, dev, stream)
+    rstd = _empty(shape[:-1], torch.float32, dev, stream)
+    st = _stream_addr(stream, dev)
     _check(lib.ssm_layernorm_fwd(_addr(x), _addr(residual), _addr(weight), _addr(bias), float(eps),
                                  NORM_SUM_F32 if kept != io else 0, _addr(y), _addr(total), _addr(mean), _addr(rstd),
                                  ctypes.byref(dims), st))
@@ -967,20 +985,20 @@ def layernorm_bwd(dy: torch.Tensor, total: torch.Tensor, weight: torch.Tensor, m
     if dresidual is not None:
         _want(dresidual, "dresidual", shape, kept, dev)
     if ds is None:
-        ds = torch.empty_like(total)
+        ds = _empty(shape, kept, dev, stream)
     else:
         _want(ds, "ds", shape, kept, dev)
     grads = dict(ds=ds)
     if kept != io:
-        grads["dx"] = torch.empty_like(dy)
+        grads["dx"] = _empty(shape, io, dev, stream)
+    need = 0
     if want_param_grads:
-        grads["dweight"] = torch.empty((dim,), dtype=torch.float32, device=dev)
-        grads["dbias"] = torch.empty_like(grads["dweight"])
-        if workspace is None:
-            need = int(lib.ssm_layernorm_bwd_workspace_bytes(ctypes.byref(dims)))
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    have = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    st = _stream_addr(stream, dev, workspace, *grads.values())
+        grads["dweight"] = _empty((dim,), torch.float32, dev, stream)
+        grads["dbias"] = _empty((dim,), torch.float32, dev, stream)
+        need = int(lib.ssm_layernorm_bwd_workspace_bytes(ctypes.byref(dims))) if workspace is None else 0
+    workspace = _workspace(workspace, need, dev, stream)
+    have = workspace.numel() * workspace.element_size()
+    st = _stream_addr(stream, dev)
     _check(lib.ssm_layernorm_bwd(_addr(dy), _addr(total), _addr(weight), _addr(mean), _addr(rstd), _addr(dresidual),
                                  NORM_SUM_F32 if kept != io else 0, _addr(ds), _addr(grads.get("dx")),
                                  _addr(grads.get("dweight")), _addr(grads.get("dbias")), ctypes.byref(dims),

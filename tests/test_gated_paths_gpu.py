@@ -130,3 +130,43 @@ def test_schedules_agree(io):
     y2, last2 = run_fwd(many)
     assert raw_error(to_host_f64(last2[17]), to_host_f64(last[0])) <= 2e-5
     assert raw_error(to_host_f64(y2[17]), to_host_f64(y[0])) <= (2e-5 if io == "f32" else 1e-2)
+
+
+def test_outputs_of_another_stream_wait_for_nothing():
+    """A call on a stream of the caller's: what it allocates is not memory that the current stream has
+    yet to write, though that memory has been given back."""
+    c = Case(4, 1000, 256, "bf16", seed=4900)
+    y, last, _ = run_fwd(c, save_checkpoints=True)
+    grads = {n: t.clone() for n, t in run_bwd(c).items()}
+    a, k = c.fwd_args()
+    s = torch.cuda.Stream()
+    m = torch.randn(4096, 4096, device="cuda")
+    torch.cuda.synchronize()
+    busy = [torch.empty_like(y) for _ in range(8)]
+    for _ in range(8):
+        m = m @ m * 1e-3
+    for b in busy:
+        b.fill_(3.0)
+    del busy, b
+    y2, last2, ck = ssmscan.gated_scan_fwd(*a, **k, stream=s, save_checkpoints=True)
+    g2 = ssmscan.gated_scan_bwd(c.t["dy"], *a, **k, dlast_state=c.t["dlast"], want_initial_state_grad=True,
+                                checkpoints=ck, stream=s)
+    torch.cuda.synchronize()
+    assert torch.equal(y, y2) and torch.equal(last, last2)
+    assert all(torch.equal(grads[n], g2[n]) for n in grads)
+
+
+def test_workspace_refusals():
+    """A workspace is on the tensors' GPU and in one piece."""
+    c = Case(2, 200, 64, "f32", seed=4910)
+    a, k = c.fwd_args()
+    dy = c.t["dy"]
+    for bad in (torch.empty(1 << 22, dtype=torch.uint8), torch.empty(1 << 23, dtype=torch.uint8, device="cuda")[::2]):
+        with pytest.raises(ValueError, match="workspace"):
+            ssmscan.gated_scan_fwd(*a, **k, workspace=bad)
+        with pytest.raises(ValueError, match="workspace"):
+            ssmscan.gated_scan_bwd(dy, *a, **k, workspace=bad)
+        n = torch.ones(64, device="cuda")
+        rows = torch.ones(200, device="cuda")
+        with pytest.raises(ValueError, match="workspace"):
+            ssmscan.layernorm_bwd(dy[0], dy[0], n, rows, rows, workspace=bad)
