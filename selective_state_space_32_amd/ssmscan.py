@@ -758,6 +758,11 @@ def _empty(shape, dtype, dev, stream):
     return t
 
 
+def _like(t, stream):
+    """_empty of t's shape and type (without a stream the quickest way to a tensor)."""
+    return torch.empty_like(t) if stream is None else _empty(t.shape, t.dtype, t.device, stream)
+
+
 def _workspace(given, need, dev, stream):
     """The call's workspace: the caller's, or `need` bytes that it uses on `stream` alone."""
     if given is not None:
@@ -815,7 +820,7 @@ def gated_scan_fwd(x: torch.Tensor, r: torch.Tensor, g: torch.Tensor, A: torch.T
     `checkpoints`."""
     bsz, L, dim, dev, io, dims = _gated_inputs(x, r, g, A, z, initial_state, seq_lens)
     if y is None:
-        y = _empty(x.shape, io, dev, stream)
+        y = _like(x, stream)
     else:
         _want(y, "y", (bsz, L, dim), io, dev)
     if last_state is not None:
@@ -850,7 +855,7 @@ def gated_scan_bwd(dy: torch.Tensor, x: torch.Tensor, r: torch.Tensor, g: torch.
     if checkpoints is not None and (checkpoints.device != dev or not checkpoints.is_contiguous()):
         raise ValueError("checkpoints: must be contiguous and on the device of x")
     names = ("dx", "dr", "dg") if z is None else ("dx", "dr", "dg", "dz")
-    grads = {k: _empty(x.shape, io, dev, stream) for k in names}
+    grads = {k: _like(x, stream) for k in names}
     grads["dA"] = _empty((dim,), torch.float32, dev, stream)
     if want_initial_state_grad:
         grads["dinitial_state"] = _empty((bsz, dim), torch.float32, dev, stream)
@@ -882,7 +887,7 @@ def _gated_step_args(state, x, r, g, A, z, y, stream):
     if z is not None:
         _want(z, "z", (S, dim), io, dev)
     if y is None:
-        y = _empty(x.shape, io, dev, stream)
+        y = _like(x, stream)
     else:
         _want(y, "y", (S, dim), io, dev)
     args = (_addr(state), _addr(x), _addr(r), _addr(g), _addr(A), _addr(z), _addr(y), ctypes.byref(dims),
@@ -947,15 +952,17 @@ def layernorm_fwd(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Te
             raise TypeError("sum_f32 needs a float32 residual")
         _want(residual, "residual", shape, kept, dev)
     if y is None:
-        y = _empty(x.shape, io, dev, stream)
+        y = _like(x, stream)
     else:
         _want(y, "y", shape, io, dev)
     if total is not None:
         _want(total, "total", shape, kept, dev)
-    elif residual is not None or kept != io:
+    elif residual is not None:
+        total = _like(residual, stream)
+    elif kept != io:
         total = _empty(shape, kept, dev, stream)
     mean = _empty(shape[:-1], torch.float32, dev, stream)
-    rstd = _empty(shape[:-1], torch.float32, dev, stream)
+    rstd = _like(mean, stream)
     st = _stream_addr(stream, dev)
     _check(lib.ssm_layernorm_fwd(_addr(x), _addr(residual), _addr(weight), _addr(bias), float(eps),
                                  NORM_SUM_F32 if kept != io else 0, _addr(y), _addr(total), _addr(mean), _addr(rstd),
@@ -985,19 +992,20 @@ def layernorm_bwd(dy: torch.Tensor, total: torch.Tensor, weight: torch.Tensor, m
     if dresidual is not None:
         _want(dresidual, "dresidual", shape, kept, dev)
     if ds is None:
-        ds = _empty(shape, kept, dev, stream)
+        ds = _like(total, stream)
     else:
         _want(ds, "ds", shape, kept, dev)
     grads = dict(ds=ds)
     if kept != io:
-        grads["dx"] = _empty(shape, io, dev, stream)
+        grads["dx"] = _like(dy, stream)
     need = 0
     if want_param_grads:
         grads["dweight"] = _empty((dim,), torch.float32, dev, stream)
-        grads["dbias"] = _empty((dim,), torch.float32, dev, stream)
+        grads["dbias"] = _like(grads["dweight"], stream)
         need = int(lib.ssm_layernorm_bwd_workspace_bytes(ctypes.byref(dims))) if workspace is None else 0
-    workspace = _workspace(workspace, need, dev, stream)
-    have = workspace.numel() * workspace.element_size()
+    if need or workspace is not None:
+        workspace = _workspace(workspace, need, dev, stream)
+    have = 0 if workspace is None else workspace.numel() * workspace.element_size()
     st = _stream_addr(stream, dev)
     _check(lib.ssm_layernorm_bwd(_addr(dy), _addr(total), _addr(weight), _addr(mean), _addr(rstd), _addr(dresidual),
                                  NORM_SUM_F32 if kept != io else 0, _addr(ds), _addr(grads.get("dx")),
