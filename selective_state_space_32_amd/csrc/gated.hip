@@ -74,14 +74,16 @@ Plan make_plan(const ssm_dims *dm) {
     return p;
 }
 
-// Queues that share the chains (see the kernel): as many as there are XCDs, unless some would then be more
-// than a quarter longer than the average; every queue has as many workgroups as the longest needs, and
-// those without an item still have to be dispatched (B1 L65536 D64 bf16, one chain: 77 us with eight
-// queues, 34 with one).
+// Queues that share the chains (see the kernel): as many as there are XCDs, unless some would then be
+// much longer than the average; every queue has as many workgroups as the longest needs, those without
+// an item still have to be dispatched, and an XCD whose queue is done has nothing left.  Short chains,
+// where hand-overs count, take a quarter more (B6 L1000 D1700 bf16, 84 chains: backward 53 us with eight
+// queues, 57 with seven), long ones a thirty-second (B3 L10000 D772, 21 chains: 95 us with eight, 76 with
+// seven, backward 148 and 126; B1 L30000 D2900, 23 chains: 247 with eight, 224 with one, 474 and 415).
 int queues_of(const Plan &p) {
     auto slots = [&](int64_t q) { return (p.chains + q - 1) / q * q; };
     int best = ssm::kGatedQueues;
-    if (4 * slots(best) <= 5 * p.chains) return best;
+    if (p.nchunk < 32 ? 4 * slots(best) <= 5 * p.chains : 32 * slots(best) <= 33 * p.chains) return best;
     for (int q = best - 1; q >= 1; --q)
         if (slots(q) < slots(best)) best = q;
     return best;
@@ -89,8 +91,13 @@ int queues_of(const Plan &p) {
 
 // Consecutive workgroups that draw from one queue: 1 where the launch is short and hand-overs count (B2
 // L2048 D1536 fp32: 23 us, 26 with 8) or neighbouring tiles share lines; 8 where it is many rounds of the
-// chip and rows are whole lines, so that bandwidth counts.
-int run_of(const Plan &p, int64_t nitem) { return p.lines && p.chains * nitem >= 4096 ? 8 : 1; }
+// chip and rows are whole lines, so that bandwidth counts, or an XCD would have so few tiles that there
+// is little to share (B1 L131072 D2047 bf16, 16 chains: 748 us with 1, 636 with 8, backward 1,460 and
+// 1,323; B2 L65536 D1500, 24 chains: 511 and 474, 1,001 and 972; B8 L2048 D5119, 320 chains: 196 and 219,
+// 386 and 440).
+int run_of(const Plan &p, int64_t nitem) {
+    return (p.lines || p.chains <= 32) && p.chains * nitem >= 4096 ? 8 : 1;
+}
 
 // Items of a chain that share a hand-over (see the kernel).  A hand-over takes about 1.2 us, and while it
 // runs every chain moves 0.013 us of data per item: with many chains every item can wait for the one
