@@ -50,7 +50,12 @@ int launched() {
 // for narrow ones, of which a workgroup requests fewer bytes at a time (32768x500: 39 us, 52 with two).
 int64_t fwd_groups(int64_t D) { return D <= 2048 ? 1024 : 512; }
 
-// Rows that a workgroup holds at a time (a wave each, up to 1024 values), by the row's width (0: wider than the registers hold).
+// The widest rows that the forward holds in registers (of 1024 threads: 4096x12288 bf16 with fp32 sums, 92
+// us; passing over the row three times takes 300 without wide loads).
+constexpr int64_t kFwdDim = 16384;
+
+// Rows that a workgroup holds at a time (a wave each, up to 1024 values), by the row's width (0: wider
+// than the backward's registers hold).
 int64_t norm_slots(int64_t D) { return D <= 1024 ? 4 : D <= 8192 ? 1 : 0; }
 
 // Partial sums of the parameters' gradients: one per workgroup of the backward, two workgroups per CU
@@ -68,7 +73,8 @@ auto fwd_kernel_of(int64_t D) {
            : D <= 1024 ? ssm::layernorm_fwd_kernel<IO, S, 64, 4, NT>
            : D <= 2048 ? ssm::layernorm_fwd_kernel<IO, S, 256, 2, NT>
            : D <= 5120 ? ssm::layernorm_fwd_kernel<IO, S, 256, 5, NT>
-                       : ssm::layernorm_fwd_kernel<IO, S, 256, 8, NT>;
+           : D <= 8192 ? ssm::layernorm_fwd_kernel<IO, S, 256, 8, NT>
+                       : ssm::layernorm_fwd_kernel<IO, S, 1024, 4, NT>;
 }
 template <typename IO, typename S, bool NT>
 auto bwd_kernel_of(int64_t D) {
@@ -86,15 +92,16 @@ void launch_norm(const void *x_, const void *res_, const float *w, const float *
     const S *res = static_cast<const S *>(res_);
     IO *y = static_cast<IO *>(y_);
     S *sum = static_cast<S *>(sum_);
-    if (norm_slots(D) == 0) {
+    if (D > kFwdDim) {
         hipLaunchKernelGGL((ssm::layernorm_fwd_wide_kernel<IO, S>), dim3((unsigned)std::min(rows, kWideGroups)),
                            dim3(ssm::kNormWideThreads), 0, st, x, res, w, bias, eps, y, sum, mean, rstd, rows, D);
         return;
     }
     auto kern = D * sizeof(IO) % 128 == 0 ? fwd_kernel_of<IO, S, true>(D) : fwd_kernel_of<IO, S, false>(D);
-    const int64_t slots = norm_slots(D), grid = std::min<int64_t>((rows + slots - 1) / slots, fwd_groups(D));
-    hipLaunchKernelGGL(kern, dim3((unsigned)grid), dim3(256), 0, st, x, res, w, bias, eps, y, sum, mean, rstd, rows,
-                       D);
+    const int64_t slots = std::max<int64_t>(norm_slots(D), 1);
+    const int64_t grid = std::min<int64_t>((rows + slots - 1) / slots, fwd_groups(D));
+    hipLaunchKernelGGL(kern, dim3((unsigned)grid), dim3(D <= 8192 ? 256 : 1024), 0, st, x, res, w, bias, eps, y, sum,
+                       mean, rstd, rows, D);
 }
 
 template <typename IO, typename S>
@@ -121,8 +128,8 @@ void launch_norm_bwd(const void *dy_, const void *s_, const float *w, const floa
         // ds may have replaced dresidual, but dy and s are still there
         const int64_t per = (rows + parts - 1) / parts;
         hipLaunchKernelGGL((ssm::layernorm_wgrad_wide_kernel<IO, S>),
-                           dim3((unsigned)((D + 255) / 256), (unsigned)parts), dim3(256), 0, st, dy, s, mean, rstd,
-                           pw, pb, rows, D, per);
+                           dim3((unsigned)((D + 256 * ssm::kNormVec - 1) / (256 * ssm::kNormVec)), (unsigned)parts),
+                           dim3(256), 0, st, dy, s, mean, rstd, pw, pb, rows, D, per);
     }
     hipLaunchKernelGGL(ssm::layernorm_wgrad_sum_kernel,
                        dim3((unsigned)((D + ssm::kNormSumCols - 1) / ssm::kNormSumCols)),

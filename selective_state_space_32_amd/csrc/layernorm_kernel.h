@@ -343,8 +343,11 @@ layernorm_wgrad_sum_kernel(const float *__restrict__ pw, const float *__restrict
 }
 
 // ---- rows wider than the registers hold: one workgroup per row, several passes over it ----------
+// (2048x20000 bf16 with fp32 sums: 135 us for 492 MB; 4096x8200, the backward: 118 us for 537 MB and 44
+// for the parameters' sums, which read dy and s once more.)
 
 constexpr int kNormWideThreads = 1024;
+constexpr int kNormWideStep = kNormWideThreads * kNormVec;
 
 template <typename IO, typename S>
 __global__ void __launch_bounds__(kNormWideThreads)
@@ -353,27 +356,46 @@ layernorm_fwd_wide_kernel(const IO *__restrict__ x, const S *res, const float *_
                           float *__restrict__ mean, float *__restrict__ rstd, int64_t M, int64_t D) {
     __shared__ float red[2][kNormWideThreads / 64];
     const float inv_d = 1.0f / (float)D;
+    const int64_t c0 = threadIdx.x * kNormVec;
     for (int64_t row = blockIdx.x; row < M; row += gridDim.x) {
         const int64_t o = row * D;
-        auto value = [&](int64_t k) {
-            float v = io<IO>::ld(x, o + k);
-            if (res) v += io<S>::ld(res, o + k);
-            if constexpr (sizeof(S) == 2) v = bf16_to_f32(f32_to_bf16(v));
-            return v;
+        auto values = [&](int64_t c, float (&v)[kNormVec]) {   // (0 past the row's end)
+            norm_vec<IO, false> rx;
+            norm_vec<S, false> rr;
+            rx.load(x + o, c, D);
+            if (res) rr.load(res + o, c, D);
+#pragma unroll
+            for (int k = 0; k < kNormVec; ++k) {
+                v[k] = rx.get(k);
+                if (res) v[k] += rr.get(k);
+                if constexpr (sizeof(S) == 2) v[k] = bf16_to_f32(f32_to_bf16(v[k]));
+            }
         };
-        float m = 0.0f;
-        for (int64_t k = threadIdx.x; k < D; k += kNormWideThreads) m += value(k);
+        float m = 0.0f, q = 0.0f, v[kNormVec];
+        for (int64_t c = c0; c < D; c += kNormWideStep) {
+            values(c, v);
+#pragma unroll
+            for (int k = 0; k < kNormVec; ++k) m += v[k];
+        }
         m = row_sum<kNormWideThreads>(m, red[0]) * inv_d;
-        float q = 0.0f;
-        for (int64_t k = threadIdx.x; k < D; k += kNormWideThreads) {
-            const float c = value(k) - m;
-            q = fmaf(c, c, q);
+        for (int64_t c = c0; c < D; c += kNormWideStep) {
+            values(c, v);
+#pragma unroll
+            for (int k = 0; k < kNormVec; ++k) {
+                const float t = c + k < D ? v[k] - m : 0.0f;
+                q = fmaf(t, t, q);
+            }
         }
         const float rs = 1.0f / sqrtf(fmaf(row_sum<kNormWideThreads>(q, red[1]), inv_d, eps));
-        for (int64_t k = threadIdx.x; k < D; k += kNormWideThreads) {
-            const float v = value(k), n = (v - m) * rs;
-            if (sum) io<S>::st(sum, o + k, v);
-            io<IO>::st(y, o + k, fmaf(n, w[k], bias ? bias[k] : 0.0f));
+        for (int64_t c = c0; c < D; c += kNormWideStep) {
+            float wv[kNormVec], bv[kNormVec], n[kNormVec];
+            values(c, v);
+            load_params(w, c, D, wv);
+            load_params(bias, c, D, bv);
+#pragma unroll
+            for (int k = 0; k < kNormVec; ++k) n[k] = fmaf((v[k] - m) * rs, wv[k], bv[k]);
+            if (sum) norm_vec<S, false>::store(sum + o, c, D, v);
+            norm_vec<IO, false>::store(y + o, c, D, n);
         }
         if (threadIdx.x == 0) {
             if (mean) mean[row] = m;
@@ -389,46 +411,75 @@ layernorm_bwd_wide_kernel(const IO *__restrict__ dy, const S *__restrict__ s, co
                           IO *__restrict__ dx, int64_t M, int64_t D) {
     __shared__ float red[2][kNormWideThreads / 64][2];
     const float inv_d = 1.0f / (float)D;
+    const int64_t c0 = threadIdx.x * kNormVec;
     int turn = 0;
     for (int64_t row = blockIdx.x; row < M; row += gridDim.x, turn ^= 1) {
         const int64_t o = row * D;
         const float m = mean[row], rs = rstd[row];
-        float p = 0.0f, q = 0.0f;
-        for (int64_t k = threadIdx.x; k < D; k += kNormWideThreads) {
-            const float t = io<IO>::ld(dy, o + k) * w[k];
-            p += t;
-            q = fmaf(t, (io<S>::ld(s, o + k) - m) * rs, q);
+        auto values = [&](int64_t c, float (&t)[kNormVec], float (&n)[kNormVec]) {   // dy w and n
+            norm_vec<IO, false> rg;
+            norm_vec<S, false> rv;
+            float wv[kNormVec];
+            rg.load(dy + o, c, D);
+            rv.load(s + o, c, D);
+            load_params(w, c, D, wv);
+#pragma unroll
+            for (int k = 0; k < kNormVec; ++k) {
+                t[k] = rg.get(k) * wv[k];
+                n[k] = c + k < D ? (rv.get(k) - m) * rs : 0.0f;
+            }
+        };
+        float p = 0.0f, q = 0.0f, t[kNormVec], n[kNormVec];
+        for (int64_t c = c0; c < D; c += kNormWideStep) {
+            values(c, t, n);
+#pragma unroll
+            for (int k = 0; k < kNormVec; ++k) {
+                p += t[k];
+                q = fmaf(t[k], n[k], q);
+            }
         }
         row_sum2<kNormWideThreads>(p, q, red[turn]);
         p *= inv_d;
         q *= inv_d;
-        for (int64_t k = threadIdx.x; k < D; k += kNormWideThreads) {
-            const float n = (io<S>::ld(s, o + k) - m) * rs;
-            float v = (io<IO>::ld(dy, o + k) * w[k] - fmaf(n, q, p)) * rs;
-            if (dres) v += io<S>::ld(dres, o + k);
-            io<S>::st(ds, o + k, v);
-            if (dx) io<IO>::st(dx, o + k, v);
+        for (int64_t c = c0; c < D; c += kNormWideStep) {
+            norm_vec<S, false> rd;
+            values(c, t, n);
+            if (dres) rd.load(dres + o, c, D);
+#pragma unroll
+            for (int k = 0; k < kNormVec; ++k) {
+                t[k] = (t[k] - fmaf(n[k], q, p)) * rs;
+                if (dres) t[k] += rd.get(k);
+            }
+            norm_vec<S, false>::store(ds + o, c, D, t);
+            if (dx) norm_vec<IO, false>::store(dx + o, c, D, t);
         }
     }
 }
 
-// The parameters' gradients over rows [blockIdx.y * rows_per, ...), one column per thread.
+// The parameters' gradients over rows [blockIdx.y * rows_per, ...), kNormVec columns per thread.
 template <typename IO, typename S>
 __global__ void __launch_bounds__(256)
 layernorm_wgrad_wide_kernel(const IO *__restrict__ dy, const S *__restrict__ s, const float *__restrict__ mean,
                             const float *__restrict__ rstd, float *__restrict__ pw, float *__restrict__ pb, int64_t M,
                             int64_t D, int64_t rows_per) {
-    const int64_t d = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (d >= D) return;
+    const int64_t c = ((int64_t)blockIdx.x * 256 + threadIdx.x) * kNormVec;
+    if (c >= D) return;
     const int64_t r1 = min(M, (blockIdx.y + 1) * rows_per);
-    float a = 0.0f, b = 0.0f;
+    float a[kNormVec] = {}, b[kNormVec] = {};
+#pragma unroll 4
     for (int64_t i = blockIdx.y * rows_per; i < r1; ++i) {
-        const float g = io<IO>::ld(dy, i * D + d);
-        a = fmaf(g, (io<S>::ld(s, i * D + d) - mean[i]) * rstd[i], a);
-        b += g;
+        norm_vec<IO, false> rg;
+        norm_vec<S, false> rv;
+        rg.load(dy + i * D, c, D);
+        rv.load(s + i * D, c, D);
+#pragma unroll
+        for (int k = 0; k < kNormVec; ++k) {
+            a[k] = fmaf(rg.get(k), (rv.get(k) - mean[i]) * rstd[i], a[k]);
+            b[k] += rg.get(k);
+        }
     }
-    pw[blockIdx.y * D + d] = a;
-    pb[blockIdx.y * D + d] = b;
+    norm_vec<float, false>::store(pw + blockIdx.y * D, c, D, a);
+    norm_vec<float, false>::store(pb + blockIdx.y * D, c, D, b);
 }
 
 }  // namespace ssm
