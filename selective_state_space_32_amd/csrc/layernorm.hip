@@ -14,7 +14,6 @@ using namespace ssmlib;
 constexpr int64_t kMaxRows = (int64_t(1) << 31) - 1;
 constexpr int64_t kMaxNormDim = int64_t(1) << 26;   // (the column sums launch 32 threads per column)
 constexpr int64_t kMaxElems = int64_t(1) << 46;
-constexpr int64_t kBwdGroups = 512;   // workgroups of the backward, and so partial sums, at most
 constexpr int64_t kWideGroups = int64_t(1) << 16;   // workgroups of the kernels for wider rows, at most
 constexpr int64_t kWideParts = 256;   // partial sums for rows wider than the registers hold
 
@@ -58,12 +57,21 @@ constexpr int64_t kFwdDim = 16384;
 // than the backward's registers hold).
 int64_t norm_slots(int64_t D) { return D <= 1024 ? 4 : D <= 8192 ? 1 : 0; }
 
-// Partial sums of the parameters' gradients: one per workgroup of the backward, two workgroups per CU
-// (16384x5120 bf16, fp32 sums: 215 us and 5 us for the sums with 512; 254 with 256, 221 + 9 with 1024).
-int64_t norm_parts(int64_t rows, int64_t D) {
+// Rows start on 128-byte lines (of tensors that do).
+bool whole_lines(int64_t D, int64_t es) { return D * es % 128 == 0; }
+
+// Workgroups of the backward, at most, and so partial sums of the parameters' gradients.  Two per CU, as
+// many as the registers of wider rows admit (16384x5120 bf16, fp32 sums: 215 us and 5 us for the sums with
+// 512; 254 with 256, 221 + 9 with 1024; 32768x768: 70 and 72 us), four for the narrowest rows, which
+// request few bytes at a time (32768x200: 31 us with 512, 21 + 2 with 1024), and for narrow ones that go
+// through the caches (32768x1500: 214 and 148 + 3; whole lines, 16384x2048: 88 and 95).
+int64_t bwd_groups(int64_t D, int64_t es) {
+    return D <= 256 || (D > 1024 && D <= 2048 && !whole_lines(D, es)) ? 1024 : 512;
+}
+int64_t norm_parts(int64_t rows, int64_t D, int64_t es) {
     const int64_t slots = norm_slots(D);
     if (slots == 0) return std::min<int64_t>(rows, kWideParts);
-    return std::min<int64_t>((rows + slots - 1) / slots, kBwdGroups);
+    return std::min<int64_t>((rows + slots - 1) / slots, bwd_groups(D, es));
 }
 
 // The narrowest shape that holds a row of D values: lanes past the row's end do nothing.
@@ -97,7 +105,7 @@ void launch_norm(const void *x_, const void *res_, const float *w, const float *
                            dim3(ssm::kNormWideThreads), 0, st, x, res, w, bias, eps, y, sum, mean, rstd, rows, D);
         return;
     }
-    auto kern = D * sizeof(IO) % 128 == 0 ? fwd_kernel_of<IO, S, true>(D) : fwd_kernel_of<IO, S, false>(D);
+    auto kern = whole_lines(D, sizeof(IO)) ? fwd_kernel_of<IO, S, true>(D) : fwd_kernel_of<IO, S, false>(D);
     const int64_t slots = std::max<int64_t>(norm_slots(D), 1);
     const int64_t grid = std::min<int64_t>((rows + slots - 1) / slots, fwd_groups(D));
     hipLaunchKernelGGL(kern, dim3((unsigned)grid), dim3(D <= 8192 ? 256 : 1024), 0, st, x, res, w, bias, eps, y, sum,
@@ -112,14 +120,14 @@ void launch_norm_bwd(const void *dy_, const void *s_, const float *w, const floa
     const S *s = static_cast<const S *>(s_), *dres = static_cast<const S *>(dres_);
     S *ds = static_cast<S *>(ds_);
     IO *dx = static_cast<IO *>(dx_);
-    const int64_t parts = norm_parts(rows, D);
+    const int64_t parts = norm_parts(rows, D, sizeof(IO));
     const bool sums = dw || db;   // (without rows there are no parts: the sums are zero)
     float *pw = sums ? part : nullptr, *pb = sums ? part + parts * D : nullptr;
     if (rows > 0 && norm_slots(D) == 0) {
         hipLaunchKernelGGL((ssm::layernorm_bwd_wide_kernel<IO, S>), dim3((unsigned)std::min(rows, kWideGroups)),
                            dim3(ssm::kNormWideThreads), 0, st, dy, s, w, mean, rstd, dres, ds, dx, rows, D);
     } else if (rows > 0) {
-        auto kern = D * sizeof(IO) % 128 == 0 ? bwd_kernel_of<IO, S, true>(D) : bwd_kernel_of<IO, S, false>(D);
+        auto kern = whole_lines(D, sizeof(IO)) ? bwd_kernel_of<IO, S, true>(D) : bwd_kernel_of<IO, S, false>(D);
         hipLaunchKernelGGL(kern, dim3((unsigned)parts), dim3(D <= 5120 ? 256 : 512), 0, st, dy, s, w, mean, rstd,
                            dres, ds, dx, pw, pb, rows, D);
     }
@@ -165,7 +173,8 @@ int ssm_layernorm_fwd(const void *x, const void *residual, const float *weight, 
 
 size_t ssm_layernorm_bwd_workspace_bytes(const ssm_dims *dims) {
     if (check_norm_dims(dims) != SSM_OK) return 0;
-    return align256((size_t)(2 * norm_parts(dims->batch * dims->seqlen, dims->dim) * dims->dim) * sizeof(float));
+    const int64_t es = dims->io_dtype == SSM_IO_BF16 ? 2 : 4;
+    return align256((size_t)(2 * norm_parts(dims->batch * dims->seqlen, dims->dim, es) * dims->dim) * sizeof(float));
 }
 
 int ssm_layernorm_bwd(const void *dy, const void *s, const float *weight, const float *mean, const float *rstd,
