@@ -110,6 +110,13 @@ def test_many_rows_wide():
     check(1500, 5120, "bf16", "f32", seed=3311)
 
 
+@pytest.mark.parametrize("io,res", KINDS)
+@pytest.mark.parametrize("M,D", [(4999, 200), (2500, 1290), (2500, 1500), (600, 8200), (300, 20001)])
+def test_many_rows_per_sum(io, res, M, D):
+    """More rows than workgroups, in every split of the sums over rows."""
+    check(M, D, io, res, seed=3320 + D, tol=2 * TOL if D > 8192 else TOL)
+
+
 def test_large_mean():
     """Rows around 1000 with deviations of one: the variance is taken from centred values.  The mean
     itself is good to a few ulps of 1000 (6e-5), which shifts y by as much."""
