@@ -96,7 +96,7 @@ int queues_of(const Plan &p) {
 // 1,323; B2 L65536 D1500, 24 chains: 511 and 474, 1,001 and 972; B8 L2048 D5119, 320 chains: 196 and 219,
 // 386 and 440).
 int run_of(const Plan &p, int64_t nitem) {
-    return (p.lines || p.chains <= 32) && p.chains * nitem >= 4096 ? 8 : 1;
+    return (p.lines || p.chains <= 32) && p.chains * nitem >= 4096 ? ssm::kGatedRun : 1;
 }
 
 // Items of a chain that share a hand-over (see the kernel).  A hand-over takes about 1.2 us, and while it

@@ -68,6 +68,7 @@ constexpr int kGatedWaves = 8;                           // waves per workgroup
 constexpr int kGatedChunk = kGatedRows * kGatedWaves;    // tokens per stored state (and per item of the backward)
 constexpr int kGatedGroup = 64;                          // most items of a chain that share a hand-over
 constexpr int kGatedQueues = 8;                          // counters, at most (one per XCD)
+constexpr int kGatedRun = 8;                             // workgroups in a row at a counter, or one
 constexpr int kGatedCounterStride = 64;                  // ints between them: lines of their own
 
 // 1 - a^2 = -expm1(2 ln 2 y), given y = log2(a) <= 0 and a.  Near a = 1 the difference loses every
@@ -102,12 +103,10 @@ __device__ __forceinline__ float one_minus_square(float y, float a) {
 template <int V, typename IO, bool NT = true> struct row_words {
     static constexpr int W = V * (int)sizeof(IO) < 4 ? 1 : V * (int)sizeof(IO) / 4;
     uint32_t w[W];
-    // row: the row's start (the same for the wave), lofs: the lane's byte offset in it -- the memory
-    // instructions take the two as they are.  (Left to itself the compiler adds the offset to the
-    // tensor's start once and the row to that, a 64-bit addition per lane and access.)
-    __device__ __forceinline__ void load(const IO *row, uint32_t lofs) {
-        asm("" : "+s"(row));
-        const SSM_GLOBAL char *p = (const SSM_GLOBAL char *)row + lofs;
+    // base: the same for the wave; ofs: the lane's byte offset from it -- the memory instructions take the
+    // two as they are.
+    __device__ __forceinline__ void load(const IO *base, uint32_t ofs) {
+        const SSM_GLOBAL char *p = (const SSM_GLOBAL char *)base + ofs;
         if constexpr (V * sizeof(IO) < 4) {
             w[0] = *(const SSM_GLOBAL IO *)p;
         } else {
@@ -131,9 +130,9 @@ template <int V, typename IO, bool NT = true> struct row_words {
 #pragma unroll
         for (int i = 0; i < W; ++i) asm volatile("" : "+v"(w[i]));
     }
-    __device__ __forceinline__ static void store(IO *row, uint32_t lofs, const float (&y)[V]) {
-        asm("" : "+s"(row), "+v"(lofs));
-        SSM_GLOBAL char *p = (SSM_GLOBAL char *)row + lofs;
+    __device__ __forceinline__ static void store(IO *base, uint32_t ofs, const float (&y)[V]) {
+        asm("" : "+v"(ofs));   // (or the offset is widened, and added, ahead of the branch that this is in)
+        SSM_GLOBAL char *p = (SSM_GLOBAL char *)base + ofs;
         if constexpr (V * sizeof(IO) < 4) {
             *(SSM_GLOBAL IO *)p = (IO)f32x2_to_bf16x2(y[0], 0.0f);
         } else {
@@ -181,7 +180,7 @@ __device__ __forceinline__ void chain_step(uint64_t *base, int64_t stride, int p
                                            int w, const float (&P)[V], const float (&H)[V], const float (&start)[V],
                                            float (&s_map)[2][kGatedWaves][64 * V], float (&s_in)[64 * V],
                                            float (&out)[V]) {
-    const int g = pos % group;
+    const int g = pos & (group - 1);   // (a power of two)
     uint64_t *own = base + pos * stride;
     if (w == 0 && act && !ends && g != group - 1) {
 #pragma unroll
@@ -306,13 +305,14 @@ __device__ __forceinline__ void chain_hand(uint32_t *base, int64_t stride, int p
 struct GatedItem {
     int b, tile, pos;
 };
-__device__ __forceinline__ GatedItem gated_item(int chains, int tiles, int nitem, bool ragged, int *counters,
-                                                int queues, int run, int *slot) {
-    const int q = (int)blockIdx.x / run % queues;
-    const int first = (int)((int64_t)chains * q / queues);
-    const int nq = (int)((int64_t)chains * (q + 1) / queues) - first;
+// (32-bit unsigned: chains and items are below 2^23, and 64-bit divisions cost every wave's start.)
+__device__ __forceinline__ GatedItem gated_item(uint32_t chains, uint32_t tiles, uint32_t nitem, bool ragged,
+                                                int *counters, uint32_t queues, uint32_t run, int *slot) {
+    const uint32_t turn = run == 1 ? blockIdx.x : blockIdx.x / kGatedRun, lane = run == 1 ? 0 : blockIdx.x % kGatedRun;
+    const uint32_t round = turn / queues, q = turn - round * queues;
+    const uint32_t first = chains * q / queues, nq = chains * (q + 1) / queues - first;
     if (nq == 0) return {0, 0, -1};
-    int n = (int)blockIdx.x / (run * queues) * run + (int)blockIdx.x % run;
+    uint32_t n = round * run + lane;
     if (counters) {   // (one item per sequence: no chain, any order will do)
         if (threadIdx.x == 0)
             *slot = __hip_atomic_fetch_add(&counters[q * kGatedCounterStride], 1, __ATOMIC_RELAXED,
@@ -321,9 +321,9 @@ __device__ __forceinline__ GatedItem gated_item(int chains, int tiles, int nitem
         n = __builtin_amdgcn_readfirstlane(*slot);
     }
     if (n >= nq * nitem) return {0, 0, -1};
-    const int pos = n / nq, chain = first + n - pos * nq;
-    const int per = ragged ? chains / tiles : tiles, hi = chain / per, lo = chain - hi * per;
-    return ragged ? GatedItem{lo, hi, pos} : GatedItem{hi, lo, pos};
+    const uint32_t pos = n / nq, chain = first + n - pos * nq;
+    const uint32_t per = ragged ? chains / tiles : tiles, hi = chain / per, lo = chain - hi * per;
+    return ragged ? GatedItem{(int)lo, (int)hi, (int)pos} : GatedItem{(int)hi, (int)lo, (int)pos};
 }
 
 // Fills the chain's words with ones (n 16-byte pairs of them: the array is padded) and clears the
@@ -385,13 +385,16 @@ gated_scan_kernel(const IO *__restrict__ x, const IO *__restrict__ r, const IO *
     const int nlive = (int)((Lb + C - 1) / C);   // items of this sequence that hold tokens
     // the wave's tokens that exist, and those with inputs (none or fewer: t0 is past the end)
     const int nrow = (int)min((int64_t)T, L - t0), nin = (int)min((int64_t)T, Lb - t0);
+    // Row k of the wave is at lofs + k * pitch from its first one, in 32 bits (dim is at most 2^26): an
+    // addition for the row's accesses, whatever their number.
+    const uint32_t pitch = (uint32_t)D * (uint32_t)sizeof(IO);
     const int64_t e0 = (row0 + t0) * D;
 
     if (c >= nlive) {   // past the sequence's end
         if constexpr (OUT) {
             if (act) {
                 const float zero[V] = {};
-                for (int k = 0; k < nrow; ++k) Row::store(y + (e0 + k * D), lofs, zero);
+                for (int k = 0; k < nrow; ++k) Row::store(y + e0, lofs + k * pitch, zero);
                 if (last && c == 0 && w == 0)
                     for (int v = 0; v < V; ++v) last[(int64_t)b * D + d + v] = h0 ? h0[(int64_t)b * D + d + v] : 0.0f;
             }
@@ -400,13 +403,15 @@ gated_scan_kernel(const IO *__restrict__ x, const IO *__restrict__ r, const IO *
     }
 
     // every load of the wave first (rows past the end: the last row again)
+    const int64_t ei = (row0 + min(t0, Lb - 1)) * D;
+    const int klast = max(nin, 1) - 1;
     Row rr[T], rg[T], rx[T], rz[OUT ? T : 1];
 #pragma unroll
     for (int k = 0; k < T; ++k) {
-        const int64_t e = e0 + min(k, nin - 1) * D;
-        rr[k].load(r + e, lofs);
-        rg[k].load(g + e, lofs);
-        rx[k].load(x + e, lofs);
+        const uint32_t ofs = lofs + min(k, klast) * pitch;
+        rr[k].load(r + ei, ofs);
+        rg[k].load(g + ei, ofs);
+        rx[k].load(x + ei, ofs);
     }
     float a2[V];
 #pragma unroll
@@ -447,7 +452,7 @@ gated_scan_kernel(const IO *__restrict__ x, const IO *__restrict__ r, const IO *
     if constexpr (OUT) {
         if (z) {
 #pragma unroll
-            for (int k = 0; k < T; ++k) rz[k].load(z + (e0 + min(k, nin - 1) * D), lofs);
+            for (int k = 0; k < T; ++k) rz[k].load(z + ei, lofs + min(k, klast) * pitch);
         }
     }
     __syncthreads();
@@ -509,7 +514,7 @@ gated_scan_kernel(const IO *__restrict__ x, const IO *__restrict__ r, const IO *
                     o[v] = z ? h[v] * silu_f32(rz[k].get(v)) : h[v];
                     if (k >= nin) o[v] = 0.0f;
                 }
-                if (act && k < nrow) Row::store(y + (e0 + k * D), lofs, o);
+                if (act && k < nrow) Row::store(y + e0, lofs + k * pitch, o);
             }
         }
     }
@@ -553,17 +558,18 @@ gated_bwd_kernel(const IO *__restrict__ x, const IO *__restrict__ r, const IO *_
     const int64_t item = ((int64_t)b * nchunk + c) * D + d;     // and in [batch][chunk][dim]
     const int nlive = (int)((Lb + C - 1) / C);
     const int nrow = (int)min((int64_t)T, L - t0), nin = (int)min((int64_t)T, Lb - t0);
+    const uint32_t pitch = (uint32_t)D * (uint32_t)sizeof(IO);
     const int64_t e0 = (row0 + t0) * D;
 
     if (c >= nlive) {
         if (act) {
             const float zero[V] = {};
             for (int k = 0; k < nrow; ++k) {
-                const int64_t e = e0 + k * D;
-                Row::store(dx + e, lofs, zero);
-                Row::store(dr + e, lofs, zero);
-                Row::store(dg + e, lofs, zero);
-                if constexpr (GATE) Row::store(dz + e, lofs, zero);
+                const uint32_t ofs = lofs + k * pitch;
+                Row::store(dx + e0, ofs, zero);
+                Row::store(dr + e0, ofs, zero);
+                Row::store(dg + e0, ofs, zero);
+                if constexpr (GATE) Row::store(dz + e0, ofs, zero);
             }
             if (w == 0)
                 for (int v = 0; v < V; ++v) {
@@ -574,18 +580,20 @@ gated_bwd_kernel(const IO *__restrict__ x, const IO *__restrict__ r, const IO *_
         return;
     }
 
+    const int64_t ei = (row0 + min(t0, Lb - 1)) * D;
+    const int klast = max(nin, 1) - 1;
     Row rr[T], rg[T], rx[T], ry[T], rz[GATE ? T : 1];
 #pragma unroll
     for (int k = 0; k < T; ++k) {
-        const int64_t e = e0 + min(k, nin - 1) * D;
-        rr[k].load(r + e, lofs);
-        rg[k].load(g + e, lofs);
-        rx[k].load(x + e, lofs);
-        ry[k].load(dy + e, lofs);
+        const uint32_t ofs = lofs + min(k, klast) * pitch;
+        rr[k].load(r + ei, ofs);
+        rg[k].load(g + ei, ofs);
+        rx[k].load(x + ei, ofs);
+        ry[k].load(dy + ei, ofs);
     }
     if constexpr (GATE) {
 #pragma unroll
-        for (int k = 0; k < T; ++k) rz[k].load(z + (e0 + min(k, nin - 1) * D), lofs);
+        for (int k = 0; k < T; ++k) rz[k].load(z + ei, lofs + min(k, klast) * pitch);
     }
     float Ad[V], h[V];
 #pragma unroll
@@ -735,11 +743,11 @@ gated_bwd_kernel(const IO *__restrict__ x, const IO *__restrict__ r, const IO *_
             hT[v] = bb[k][v];
         }
         if (act && k < nrow) {
-            const int64_t e = e0 + k * D;
-            Row::store(dx + e, lofs, ox);
-            Row::store(dr + e, lofs, orr);
-            Row::store(dg + e, lofs, og);
-            if constexpr (GATE) Row::store(dz + e, lofs, oz);
+            const uint32_t ofs = lofs + k * pitch;
+            Row::store(dx + e0, ofs, ox);
+            Row::store(dr + e0, ofs, orr);
+            Row::store(dg + e0, ofs, og);
+            if constexpr (GATE) Row::store(dz + e0, ofs, oz);
         }
     }
     __syncthreads();   // (the maps are read)
