@@ -51,8 +51,8 @@ struct Plan {
 constexpr int64_t kCounterInts = ssm::kGatedQueues * ssm::kGatedCounterStride;
 
 // Channels per lane: two bf16 or one fp32, four bytes an access; one bf16 too where tiles of two would
-// leave CUs idle (at most one workgroup each: B1 L512 D2048, 128 items: 7.7 against 9.0 us, backward 10.1
-// against 12.3; B1 L4096 D256: 10.4 and 15.8, 14.4 and 19.6), and where the last of an odd width's
+// leave CUs idle (at most one workgroup each: B1 L512 D2048, 128 items: 7.2 against 8.8 us, backward 9.6
+// against 11.8; B1 L4096 D256: 8.6 and 11.0, 11.1 and 14.0), and where the last of an odd width's
 // channels would be a tile of its own: its lane shares a channel with its neighbour, which has to be in
 // the same wave, as a state that is advanced in place is read by one and written by the other.
 int lane_channels(const ssm_dims *dm, int64_t nchunk) {
@@ -77,9 +77,10 @@ Plan make_plan(const ssm_dims *dm) {
 // Queues that share the chains (see the kernel): as many as there are XCDs, unless some would then be
 // much longer than the average; every queue has as many workgroups as the longest needs, those without
 // an item still have to be dispatched, and an XCD whose queue is done has nothing left.  Short chains,
-// where hand-overs count, take a quarter more (B6 L1000 D1700 bf16, 84 chains: backward 53 us with eight
-// queues, 57 with seven), long ones a thirty-second (B3 L10000 D772, 21 chains: 95 us with eight, 76 with
-// seven, backward 148 and 126; B1 L30000 D2900, 23 chains: 247 with eight, 224 with one, 474 and 415).
+// where hand-overs count, take a quarter more (B6 L1000 D1700 bf16, 84 chains: backward 51 us with eight
+// queues, 58 with seven), long ones a thirty-second (B3 L10000 D772, 21 chains: 95 us with eight, 74 with
+// seven, backward 145 and 122; B1 L30000 D2900, 23 chains: 231 with eight, 217 with one, 429 and 401; B1
+// L65536 D64, one chain: 131 with eight, 33 with one).
 int queues_of(const Plan &p) {
     auto slots = [&](int64_t q) { return (p.chains + q - 1) / q * q; };
     int best = ssm::kGatedQueues;
@@ -90,22 +91,22 @@ int queues_of(const Plan &p) {
 }
 
 // Consecutive workgroups that draw from one queue: 1 where the launch is short and hand-overs count (B2
-// L2048 D1536 fp32: 23 us, 26 with 8) or neighbouring tiles share lines; 8 where it is many rounds of the
+// L2048 D1536 fp32: 24 us, 27 with 8) or neighbouring tiles share lines; 8 where it is many rounds of the
 // chip and rows are whole lines, so that bandwidth counts, or an XCD would have so few tiles that there
-// is little to share (B1 L131072 D2047 bf16, 16 chains: 748 us with 1, 636 with 8, backward 1,460 and
-// 1,323; B2 L65536 D1500, 24 chains: 511 and 474, 1,001 and 972; B8 L2048 D5119, 320 chains: 196 and 219,
-// 386 and 440).
+// is little to share (B1 L131072 D2047 bf16, 16 chains: 723 us with 1, 656 with 8, backward 1,429 and
+// 1,300; B2 L65536 D1500, 24 chains: 499 and 476, 979 and 964; B8 L2048 D5119, 320 chains: 201 and 223,
+// 367 and 429).
 int run_of(const Plan &p, int64_t nitem) {
     return (p.lines || p.chains <= 32) && p.chains * nitem >= 4096 ? ssm::kGatedRun : 1;
 }
 
-// Items of a chain that share a hand-over (see the kernel).  A hand-over takes about 1.2 us, and while it
-// runs every chain moves 0.013 us of data per item: with many chains every item can wait for the one
-// before it, and the maps' traffic is saved (B8 L2048 D5120 bf16, 320 chains: 172 us with groups of one,
-// 179 with eight, backward 309 and 323; B2 L8192 D5120, 80 chains: 180 with one, 184 with four), with few
-// the hand-overs have to be shared (B1 L131072 D2048, 16 chains: 701 us with one, 520 with four or eight;
-// B1 L65536 D512, 4 chains: 168 with two, 97 with eight, 93 with 16 or 32; D64, 1 chain: 98 with eight, 34
-// with 64; B2 L2048 D1536 fp32, 48 chains: 28 with one, 25 with two or four).
+// Items of a chain that share a hand-over (see the kernel), a power of two.  A hand-over takes about 1.2
+// us, and while it runs every chain moves 0.013 us of data per item: with many chains every item can wait
+// for the one before it, and the maps' traffic is saved (B8 L2048 D5120 bf16, 320 chains: 168 us with
+// groups of one, 179 with eight, backward 309 and 324; B2 L8192 D5120, 80 chains: backward 308 with one,
+// 320 with four), with few the hand-overs have to be shared (B1 L131072 D2048, 16 chains: 689 us with one,
+// 499 with four or eight; B1 L65536 D512, 4 chains: 165 with two, 93 with eight, 89 with 16 or 32; D64, 1
+// chain: 96 with eight, 33 with 64; B2 L2048 D1536 fp32, 48 chains: 28 with one, 23 with two or four).
 int group_of(const Plan &p) {
     int g = 1;
     if (p.chains < 64)
@@ -145,8 +146,8 @@ void launch_fwd_v(const void *x, const void *r, const void *g, const float *A, c
                   hipStream_t st) {
     constexpr int64_t M = T * K / ssm::kGatedChunk;
     const int64_t nitem = (p.nchunk + M - 1) / M;
-    // (with groups of one the words are the states; wide items come with few chains, and so with groups)
-    const bool own = group_of(p) > 1;
+    // (with groups of one and an item per state the words are the states)
+    const bool own = M > 1 || group_of(p) > 1;
     float *states = p.nchunk > 1 && own ? static_cast<float *>(ws) : nullptr;
     void *words = own ? static_cast<char *>(ws) + p.state_bytes : ws;
     int *counters = launch_clear(p, words, ws, nitem, dm, st);
@@ -158,10 +159,10 @@ void launch_fwd_v(const void *x, const void *r, const void *g, const float *A, c
 }
 
 // Items of two chunks halve the hand-overs of a chain, at two workgroups per CU instead of three.  They
-// pay where a few chains share the chip: a hand-over takes about 1.2 us and the group's chunks take
-// the bandwidth 0.11 us per chain (B1 L131072 D2048 bf16, 16 chains: 495 -> 468 us; B8 L2048 D5120, 320
-// chains: 169 -> 184 us), as long as the halved number of items still fills the chip.
-bool wide_items(const Plan &p) { return p.chains <= 32 && p.chains * p.nchunk >= 4096; }
+// pay where chains are long, as long as the halved number of items still fills the chip (B1 L131072 D2048
+// bf16 gated: 556 -> 498 us; B2 L8192 D3000: 144 -> 128; B2 L8192 D2048 fp32: 126 -> 111; but 32 chunks, B8
+// L2048 D5120: 168 and 168, fp32: 290 -> 307; B3 L4096 D1400, 2112 chunks in all: 54 -> 57).
+bool wide_items(const Plan &p) { return p.nchunk >= 64 && p.chains * p.nchunk >= 2304; }
 
 template <bool OUT, bool NT>
 void launch_fwd_n(const void *x, const void *r, const void *g, const float *A, const void *z, const float *h0,

@@ -72,6 +72,20 @@ def test_items_of_two_chunks(io, D):
         assert torch.equal(one[k], two[k]), f"{k}: other values without the forward's states"
 
 
+@pytest.mark.parametrize("io,D", [("bf16", 1023), ("f32", 500)])
+def test_items_of_two_chunks_in_groups_of_one(io, D):
+    """72 chains of 65 chunks: every item of two chunks waits for the one before it; tolerances as above."""
+    c = Case(9, 4100, D, io, seed=4450, lens=[4100, 4097, 4096, 4095, 4033, 4032, 3000, 64, 0])
+    y, last, ck = run_fwd(c, save_checkpoints=True)
+    ry, rlast, rg = c.reference()
+    close(y, ry, io, TOL * 1.5, "y")
+    close(last, rlast, "f32", TOL * 1.5, "last_state")
+    one, two = run_bwd(c, ck), run_bwd(c)
+    for k, ref in rg.items():
+        close(one[k], ref, "f32" if k in ("dA", "dinitial_state") else io, 5e-4 if k == "dA" else TOL * 1.5, k)
+        assert torch.equal(one[k], two[k]), f"{k}: other values without the forward's states"
+
+
 @pytest.mark.parametrize("io,D", [("bf16", 130), ("f32", 67)])
 def test_nan_in_groups_of_one(io, D):
     """A NaN state is handed on as one (and not taken for a missing one); nothing else changes."""
