@@ -18,18 +18,18 @@
 //      from there, writing y.
 // The inputs are read once and the outputs written once, whatever the length.
 //
-// Bound: HBM.  Per element the forward moves 8 bytes in bf16 (10 with a gate) and issues 47 VALU
-// instructions with its gate, 8 of them transcendental (three sigmoids, the decay, a root); the
-// backward moves 14 (18) and issues 90, which keeps the VALU busy for two thirds of its time.
-// Measured, where a copy of 1 GiB reaches 5.1 TB/s: B8 L2048 D5120 bf16 gated 172 us for 839 MB (855
-// by the counters), its backward 309 us for 1,510 MB (1,537); B1 L131072 D2048 bf16 455 us for 2,148
-// MB; B2 L2048 D1536 fp32 22 us for 101 MB, its backward 37 us for 176 MB.  Short launches are bound by
-// their latency: 7 us for one chunk in a few tiles.
+// Bound: HBM.  Per element the forward moves 8 bytes in bf16 (10 with a gate) and issues 42 VALU
+// instructions with its gate, 8 of them transcendental (three sigmoids, the decay, a root), which keeps
+// the VALU busy for two thirds of its time; the backward moves 14 (18), issues 84 and keeps it as busy.
+// Measured (averages at settled clocks), where a copy of 1 GiB reaches 5.1 TB/s: B8 L2048 D5120 bf16 gated
+// 167 us for 839 MB (855 by the counters), its backward 306 us for 1,510 MB (1,537); B1 L131072 D2048 bf16
+// 423 us for 2,148 MB; B2 L2048 D1536 fp32 25 us for 101 MB, its backward 38 us for 176 MB.  Short
+// launches are bound by their latency: 6 us for one chunk in a few tiles.
 //
-// The split.  Eight tokens per wave keep a lane's values of V channels in registers (70 registers in
+// The split.  Eight tokens per wave keep a lane's values of V channels in registers (69 registers in
 // the forward, three workgroups per CU; 128 in the backward, two), and several workgroups per CU let
 // one load while another computes or waits.  At B8 L2048 D5120, sixteen waves of eight tokens took
-// 221 us and eight of sixteen 184 where eight of eight took 169: fewer workgroups overlap.
+// 221 us where eight of eight took 169; eight of sixteen are an item of two chunks, taken for long chains.
 //
 // The chain.  The state goes from chunk to chunk through memory.  With many chains every chunk waits for
 // the one before it (chain_hand): state[sequence][chunk][channel], four bytes, all ones meaning that
@@ -52,9 +52,9 @@
 // equal run of the chains; `run` consecutive workgroups draw from the same one.  The XCDs take
 // workgroups in turn, so with eight queues and run = 1 a queue's chains stay in one XCD: its hand-overs
 // are the fastest, and neighbouring tiles, which share lines where rows do not start on one, meet in
-// its L2 (B8 L2048 D5119 bf16 backward: 381 us, 440 with run = 8).  With run = 8 every XCD works on all
+// its L2 (B8 L2048 D5119 bf16 backward: 367 us, 429 with run = 8).  With run = 8 every XCD works on all
 // the chains, where with run = 1 it reads the same few columns of every row, which lie in few of the
-// memory's channels (B1 L131072 D2048 bf16: 552 against 513 us).
+// memory's channels (B1 L131072 D2048 bf16 gated: 545 against 501 us).
 #pragma once
 
 #include <float.h>
@@ -173,11 +173,11 @@ __device__ __forceinline__ uint64_t chain_read(const uint64_t *w) {
 
 // The chain's step for the item at position pos, called by the whole workgroup: base + p * stride is
 // the word of position p (the lane's first of V channels), (P, H) the item's map and start the state
-// at position 0's start (both read in wave 0 only; 0 at other positions), `ends`: nobody comes after.  Leaves the state at
-// the item's start in s_in (behind a barrier) and the one at its end in wave 0's `out`.
+// at position 0's start (both read in wave 0 only; 0 at other positions), `ends`: nobody comes after.
+// Leaves the state at the item's start in s_in (behind a barrier) and the one at its end in wave 0's `out`.
 template <int V>
-__device__ __forceinline__ void chain_step(uint64_t *base, int64_t stride, int pos, int group, bool ends, bool act, int lane,
-                                           int w, const float (&P)[V], const float (&H)[V], const float (&start)[V],
+__device__ __forceinline__ void chain_step(uint64_t *base, int64_t stride, int pos, int group, bool ends, bool act,
+                                           int lane, int w, const float (&P)[V], const float (&H)[V], const float (&start)[V],
                                            float (&s_map)[2][kGatedWaves][64 * V], float (&s_in)[64 * V],
                                            float (&out)[V]) {
     const int g = pos & (group - 1);   // (a power of two)
@@ -373,8 +373,8 @@ __global__ void __launch_bounds__(64 * K)
 gated_scan_kernel(const IO *__restrict__ x, const IO *__restrict__ r, const IO *__restrict__ g,
                   const float *__restrict__ A, const IO *__restrict__ z, const float *h0,
                   const int32_t *__restrict__ seq_lens, IO *__restrict__ y, float *last,
-                  float *states, void *words, int *counters, int64_t L, int64_t D, int tiles, int chains, int nitem, int nchunk,
-                  int queues, int run, int group) {
+                  float *states, void *words, int *counters, int64_t L, int64_t D, int tiles, int chains, int nitem,
+                  int nchunk, int queues, int run, int group) {
     constexpr int C = T * K, M = C / kGatedChunk;
     static_assert(K == kGatedWaves && C % kGatedChunk == 0 && K % M == 0, "a stored state is at a wave's end");
     using Row = row_words<V, IO, NT>;

@@ -12,8 +12,8 @@
 // so do the sums over rows behind dw and db.  The next row is requested before the current one is
 // reduced.  Rows wider than the registers hold take the kernels at the end, which pass over a row
 // several times (its later passes come from the cache).  Measured (a copy of 1 GiB reaches 5.1 TB/s on
-// this card): 16384x5120 bf16 with an fp32 residual 168 us for 1,007 MB, its backward 223 us for
-// 1,342 MB; 4096x1536 fp32 backward 18.5 us for 76 MB; 256x5120 bf16 5.6 us for 16 MB, the latency of a
+// this card): 16384x5120 bf16 with an fp32 residual 176 us for 1,007 MB, its backward 226 us for
+// 1,342 MB; 4096x1536 fp32 backward 19 us for 76 MB; 256x5120 bf16 5.6 us for 16 MB, the latency of a
 // load, two sums over a workgroup and a store.
 #pragma once
 
