@@ -503,7 +503,8 @@ SSMSCAN_API int ssm_gated_step(float *state, const void *x, const void *r, const
  *   s = x + residual,   y = (s - mean(s)) * rstd * weight + bias,
  *   rstd = 1 / sqrt(mean((s - mean(s))^2) + eps)
  * s is rounded to the type it is kept in before it is normalised, so that the call equals a sum
- * followed by a norm; means and variances are fp32, the variance from the centred values.
+ * followed by a norm; means and variances are fp32, both from the centred values (a row of one value
+ * has that mean and no variance, whatever dim).
  *   x, y          : rows (io_dtype);   weight : [dim] fp32;   bias : [dim] fp32, or NULL (= 0)
  *   residual      : rows, or NULL (s = x);   sum : rows, receives s, or NULL (not wanted); both of
  *                   io_dtype, or fp32 with SSM_NORM_SUM_F32.  sum may be the residual buffer (the

@@ -135,6 +135,17 @@ __device__ __forceinline__ void load_params(const float *p, int64_t c, int64_t D
     }
 }
 
+// 1 / sqrt(variance + eps) of values centred with a mean that still lacks e: q / D - e^2, which is not
+// below zero but for rounding (and infinite or NaN as q is).
+__device__ __forceinline__ float rstd_of(float q, float inv_d, float e, float eps) {
+    float var = q * inv_d;
+    if (var < __builtin_inff()) var = fmaxf(fmaf(-e, e, var), 0.0f);
+    return 1.0f / sqrtf(var + eps);
+}
+
+// The mean m of a first sum is off by the sum's roundings and by that of 1 / D: an ulp or several, which
+// rstd makes visible where a row varies little (rows of 1900 at D = 500: 3.9e-2 of y with the default eps).
+// v - m is exact there, so its mean e, summed along with the squares, is what m lacks.
 // SLOTS = threads / TPR rows at a time.  S: the type of residual and sum.
 template <typename IO, typename S, int TPR, int NV, bool NT>
 __global__ void __launch_bounds__(TPR > 64 ? TPR : 256)
@@ -142,7 +153,7 @@ layernorm_fwd_kernel(const IO *__restrict__ x, const S *res, const float *__rest
                      const float *__restrict__ bias, float eps, IO *__restrict__ y, S *sum,
                      float *__restrict__ mean, float *__restrict__ rstd, int64_t M, int64_t D) {
     constexpr int SLOTS = TPR > 64 ? 1 : 256 / TPR;
-    __shared__ float red[2][TPR / 64];
+    __shared__ float red[TPR / 64], red2[TPR / 64][2];
     const int tid = threadIdx.x % TPR;
     const float inv_d = 1.0f / (float)D;
     float wv[NV][kNormVec], bv[NV][kNormVec];
@@ -178,8 +189,8 @@ layernorm_fwd_kernel(const IO *__restrict__ x, const S *res, const float *__rest
                 m += t;
             }
         if (row + step < M) fetch(row + step);
-        m = row_sum<TPR>(m, red[0]) * inv_d;
-        float q = 0.0f;
+        m = row_sum<TPR>(m, red) * inv_d;
+        float e = 0.0f, q = 0.0f;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             const int64_t c = (int64_t)(j * TPR + tid) * kNormVec;
@@ -187,20 +198,23 @@ layernorm_fwd_kernel(const IO *__restrict__ x, const S *res, const float *__rest
 #pragma unroll
             for (int k = 0; k < kNormVec; ++k) {
                 v[j][k] = c + k < D ? v[j][k] - m : 0.0f;
+                e += v[j][k];
                 q = fmaf(v[j][k], v[j][k], q);
             }
         }
-        const float rs = 1.0f / sqrtf(fmaf(row_sum<TPR>(q, red[1]), inv_d, eps));
+        row_sum2<TPR>(e, q, red2);
+        e *= inv_d;
+        const float rs = rstd_of(q, inv_d, e, eps), shift = -e * rs;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             const int64_t c = (int64_t)(j * TPR + tid) * kNormVec;
             float o[kNormVec];
 #pragma unroll
-            for (int k = 0; k < kNormVec; ++k) o[k] = fmaf(v[j][k] * rs, wv[j][k], bv[j][k]);
+            for (int k = 0; k < kNormVec; ++k) o[k] = fmaf(fmaf(v[j][k], rs, shift), wv[j][k], bv[j][k]);
             if (c < D) norm_vec<IO, NT>::store(y + row * D, c, D, o);
         }
         if (tid == 0) {
-            if (mean) mean[row] = m;
+            if (mean) mean[row] = m + e;
             if (rstd) rstd[row] = rs;
         }
     }
@@ -216,7 +230,6 @@ layernorm_bwd_kernel(const IO *__restrict__ dy, const S *__restrict__ s, const f
     __shared__ float red[2][TPR / 64][2];
     const int tid = threadIdx.x % TPR;
     const int slot = SLOTS > 1 ? __builtin_amdgcn_readfirstlane(threadIdx.x / TPR) : 0;
-    const float inv_d = 1.0f / (float)D;
     float wv[NV][kNormVec], aw[NV][kNormVec], ab[NV][kNormVec];
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
@@ -263,8 +276,8 @@ layernorm_bwd_kernel(const IO *__restrict__ dy, const S *__restrict__ s, const f
         }
         if (row + step < M) fetch(row + step);
         row_sum2<TPR>(p, q, red[turn]);
-        p *= inv_d;
-        q *= inv_d;
+        p /= (float)D;   // (not times 1 / D, whose rounding equal terms would keep, an ulp of theirs)
+        q /= (float)D;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             const int64_t c = (int64_t)(j * TPR + tid) * kNormVec;
@@ -354,7 +367,7 @@ __global__ void __launch_bounds__(kNormWideThreads)
 layernorm_fwd_wide_kernel(const IO *__restrict__ x, const S *res, const float *__restrict__ w,
                           const float *__restrict__ bias, float eps, IO *__restrict__ y, S *sum,
                           float *__restrict__ mean, float *__restrict__ rstd, int64_t M, int64_t D) {
-    __shared__ float red[2][kNormWideThreads / 64];
+    __shared__ float red[kNormWideThreads / 64], red2[kNormWideThreads / 64][2];
     const float inv_d = 1.0f / (float)D;
     const int64_t c0 = threadIdx.x * kNormVec;
     for (int64_t row = blockIdx.x; row < M; row += gridDim.x) {
@@ -371,34 +384,37 @@ layernorm_fwd_wide_kernel(const IO *__restrict__ x, const S *res, const float *_
                 if constexpr (sizeof(S) == 2) v[k] = bf16_to_f32(f32_to_bf16(v[k]));
             }
         };
-        float m = 0.0f, q = 0.0f, v[kNormVec];
+        float m = 0.0f, e = 0.0f, q = 0.0f, v[kNormVec];
         for (int64_t c = c0; c < D; c += kNormWideStep) {
             values(c, v);
 #pragma unroll
             for (int k = 0; k < kNormVec; ++k) m += v[k];
         }
-        m = row_sum<kNormWideThreads>(m, red[0]) * inv_d;
+        m = row_sum<kNormWideThreads>(m, red) * inv_d;
         for (int64_t c = c0; c < D; c += kNormWideStep) {
             values(c, v);
 #pragma unroll
             for (int k = 0; k < kNormVec; ++k) {
                 const float t = c + k < D ? v[k] - m : 0.0f;
+                e += t;
                 q = fmaf(t, t, q);
             }
         }
-        const float rs = 1.0f / sqrtf(fmaf(row_sum<kNormWideThreads>(q, red[1]), inv_d, eps));
+        row_sum2<kNormWideThreads>(e, q, red2);
+        e *= inv_d;
+        const float rs = rstd_of(q, inv_d, e, eps), shift = -e * rs;
         for (int64_t c = c0; c < D; c += kNormWideStep) {
             float wv[kNormVec], bv[kNormVec], n[kNormVec];
             values(c, v);
             load_params(w, c, D, wv);
             load_params(bias, c, D, bv);
 #pragma unroll
-            for (int k = 0; k < kNormVec; ++k) n[k] = fmaf((v[k] - m) * rs, wv[k], bv[k]);
+            for (int k = 0; k < kNormVec; ++k) n[k] = fmaf(fmaf(v[k] - m, rs, shift), wv[k], bv[k]);
             if (sum) norm_vec<S, false>::store(sum + o, c, D, v);
             norm_vec<IO, false>::store(y + o, c, D, n);
         }
         if (threadIdx.x == 0) {
-            if (mean) mean[row] = m;
+            if (mean) mean[row] = m + e;
             if (rstd) rstd[row] = rs;
         }
     }
@@ -410,7 +426,6 @@ layernorm_bwd_wide_kernel(const IO *__restrict__ dy, const S *__restrict__ s, co
                           const float *__restrict__ mean, const float *__restrict__ rstd, const S *dres, S *ds,
                           IO *__restrict__ dx, int64_t M, int64_t D) {
     __shared__ float red[2][kNormWideThreads / 64][2];
-    const float inv_d = 1.0f / (float)D;
     const int64_t c0 = threadIdx.x * kNormVec;
     int turn = 0;
     for (int64_t row = blockIdx.x; row < M; row += gridDim.x, turn ^= 1) {
@@ -439,8 +454,8 @@ layernorm_bwd_wide_kernel(const IO *__restrict__ dy, const S *__restrict__ s, co
             }
         }
         row_sum2<kNormWideThreads>(p, q, red[turn]);
-        p *= inv_d;
-        q *= inv_d;
+        p /= (float)D;   // (not times 1 / D, whose rounding equal terms would keep, an ulp of theirs)
+        q /= (float)D;
         for (int64_t c = c0; c < D; c += kNormWideStep) {
             norm_vec<S, false> rd;
             values(c, t, n);
