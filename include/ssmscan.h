@@ -509,7 +509,8 @@ SSMSCAN_API int ssm_gated_step(float *state, const void *x, const void *r, const
  *   residual      : rows, or NULL (s = x);   sum : rows, receives s, or NULL (not wanted); both of
  *                   io_dtype, or fp32 with SSM_NORM_SUM_F32.  sum may be the residual buffer (the
  *                   residual stream advanced in place)
- *   mean, rstd    : [batch * seqlen] fp32 outputs for the backward pass, each may be NULL
+ *   mean, rstd    : [batch * seqlen] fp32 outputs for the backward pass, each may be NULL (NaN where
+ *                   dim is 0)
  *   eps           : >= 0 and finite (SSM_ERR_VALUE otherwise)
  * Outputs must not overlap inputs or each other otherwise.  dims->dstate and dims->chunk_len are
  * ignored; at most 2^31 - 1 rows of at most 2^26 values.  Returns SSM_OK or a negative

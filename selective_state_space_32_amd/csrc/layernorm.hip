@@ -159,8 +159,9 @@ int ssm_layernorm_fwd(const void *x, const void *residual, const float *weight, 
         !aligned(bias, 4) || !aligned(mean, 4) || !aligned(rstd, 4))
         return fail(SSM_ERR_ALIGN, "a tensor pointer is not aligned to its element size");
     const int64_t rows = dims->batch * dims->seqlen, D = dims->dim;
-    if (rows == 0 || D == 0) return ok();
-    if (!x || !weight || !y) return fail(SSM_ERR_NULL, "x, weight or y is NULL");
+    // (rows without values still have statistics: a mean of 0 / 0)
+    if (rows == 0 || (D == 0 && !mean && !rstd)) return ok();
+    if (D > 0 && (!x || !weight || !y)) return fail(SSM_ERR_NULL, "x, weight or y is NULL");
     hipStream_t st = static_cast<hipStream_t>(stream);
     if (es == 4)
         launch_norm<float, float>(x, residual, weight, bias, eps, y, sum, mean, rstd, rows, D, st);

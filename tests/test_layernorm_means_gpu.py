@@ -52,3 +52,26 @@ def test_gradient_of_equal_terms(io, kept, D):
     g = ssmscan.layernorm_bwd(dy, s.to(IO[kept]), torch.full((D,), 1.25, device="cuda"), torch.zeros_like(rows), rows)
     torch.cuda.synchronize()
     assert not torch.count_nonzero(g["ds"])
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+def test_statistics_of_rows_without_values(io):
+    """Rows of width 0: their mean is 0 / 0, so both statistics are NaN, and no row keeps what was there."""
+    import ctypes
+    mean, rstd = torch.full((9,), 7.0, device="cuda"), torch.full((9,), 7.0, device="cuda")
+    dims = ssmscan.ssm_dims(1, 9, 0, 1, 1 if io == "bf16" else 0, 0)
+
+    def call(m, r):
+        return ssmscan.lib.ssm_layernorm_fwd(None, None, None, None, 1e-5, 0, None, None, m, r, ctypes.byref(dims),
+                                             torch.cuda.current_stream().cuda_stream)
+    assert call(mean.data_ptr(), None) == 0 and call(None, None) == 0
+    torch.cuda.synchronize()
+    assert torch.isnan(mean).all() and torch.equal(rstd, torch.full_like(rstd, 7.0))
+    assert call(None, rstd.data_ptr()) == 0
+    torch.cuda.synchronize()
+    assert torch.isnan(rstd).all()
+    x, w = torch.empty((2, 3, 0), dtype=IO[io], device="cuda"), torch.ones(0, device="cuda")
+    y, total, m, r = ssmscan.layernorm_fwd(x, w, w, residual=x.clone())
+    torch.cuda.synchronize()
+    assert y.shape == x.shape and total.shape == x.shape and m.shape == r.shape == (2, 3)
+    assert torch.isnan(m).all() and torch.isnan(r).all()
