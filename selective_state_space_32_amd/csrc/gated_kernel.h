@@ -71,27 +71,29 @@ constexpr int kGatedQueues = 8;                          // counters, at most (o
 constexpr int kGatedRun = 8;                             // workgroups in a row at a counter, or one
 constexpr int kGatedCounterStride = 64;                  // ints between them: lines of their own
 
-// 1 - a^2 = -expm1(2 ln 2 y), given y = log2(a) <= 0 and a.  Near a = 1 the difference loses every
-// digit that a was rounded in, so there a polynomial in y takes its place, y (c0 + c1 y + ...),
-// interpolated at Chebyshev nodes of the interval: degree 3 for 1 - a^2 < 0.22 (relative error
-// below 2.6e-7, 1.3e-7 of the root), or degree 4 for 1 - a^2 < 0.33 (3e-8) where both the inputs
-// and the outputs are fp32.  Above the interval an ulp of a^2 costs the difference 8e-7 and 4e-7.
-template <typename IO>
-__device__ __forceinline__ float one_minus_square(float y, float a) {
-    constexpr bool kLong = sizeof(IO) == 4;
-    constexpr float kEnd = -(kLong ? 0.4f : 0.25f) / (2.0f * kLn2);
+// u = 1 - a = -expm1(ln 2 y), given y = log2(a) <= 0 and 2^y.  Near a = 1 the difference loses every digit
+// that 2^y was rounded in, so there a polynomial in y takes its place, y (c0 + c1 y + ...), interpolated at
+// Chebyshev nodes of the interval: degree 4 for a > 0.82 where both the inputs and the outputs are fp32
+// (relative error below 1e-9, 1.1e-7 as it is evaluated; the difference below that 3e-7), or degree 2 for
+// a > 0.94 (4e-7; the difference 9e-7).  From u come both
+//   a       = 1 - u, rounded once: 2^y of the exponential unit is good to an ulp, but near 1 its error has a
+//             mean (-7e-9 for 1 - a below 2e-3), which a slow channel adds up over its memory of 1 / (1 - a)
+//             tokens (sequences of 4100 tokens were off by up to 1.7e-4 of their rms); an error relative to u is
+//             only that error of the state,
+//   1 - a^2 = u + u a.
+template <typename IO> constexpr float kNearOne = sizeof(IO) == 4 ? -0.289f : -0.09f;   // y from which u is near
+template <typename IO> __device__ __forceinline__ float one_minus(float y, float exp2_y) {
     float p;
-    if constexpr (kLong) {
-        p = fmaf(y, -3.617433190962575e-2f, -0.15229893496512706f);
-        p = fmaf(p, y, -0.44387109232657457f);
-        p = fmaf(p, y, -0.9609002283833515f);
-        p = fmaf(p, y, -1.386294327691407f);
+    if constexpr (sizeof(IO) == 4) {
+        p = fmaf(y, -1.2270708102732897e-3f, -9.591649286448956e-3f);
+        p = fmaf(p, y, -5.550139397382736e-2f);
+        p = fmaf(p, y, -0.2402264028787613f);
+        p = fmaf(p, y, -0.6931471824645996f);
     } else {
-        p = fmaf(y, -0.1393467438699137f, -0.44242258435379367f);
-        p = fmaf(p, y, -0.9608483593855177f);
-        p = fmaf(p, y, -1.386294036555376f);
+        p = fmaf(y, -5.4223693907260895e-2f, -0.24018345773220062f);
+        p = fmaf(p, y, -0.6931469440460205f);
     }
-    return y > kEnd ? p * y : fmaf(-a, a, 1.0f);
+    return y > kNearOne<IO> ? p * y : 1.0f - exp2_y;
 }
 
 // V neighbouring I/O elements of a row as raw 32-bit words.  Rows of an odd width start at odd
@@ -336,19 +338,6 @@ gated_clear_kernel(u32x4_t *__restrict__ words, int64_t n, u32x4_t *__restrict__
     else if (i - n < kGatedQueues * kGatedCounterStride / 4) counters[i - n] = zeros;
 }
 
-// a = 2^y.  The exponential unit is good to an ulp, but near 1 its error has a mean (-6e-9 for 1 - a of
-// 1e-4 to 2e-3), which a slow channel adds up over its memory of 1 / (1 - a) tokens: fp32 values of 9
-// sequences of 4100 tokens were off by up to 1.7e-4 of their rms, where plain fp32 arithmetic with an
-// unbiased exponential is at 0.7e-4.  So for fp32, within 1/32 of 0, 1 + y (c0 + c1 y + c2 y^2), interpolated at
-// Chebyshev nodes (error 4e-10) and rounded once.  In bf16 the inputs' own rounding is far above that.
-template <typename IO> __device__ __forceinline__ float decay(float y) {
-    const float a = hw_exp2(y);
-    if constexpr (sizeof(IO) == 2) return a;
-    float p = fmaf(y, 0.05505544692277908f, 0.24022126197814941f);
-    p = fmaf(p, y, 0.6931471824645996f);
-    return y > -0.03125f ? fmaf(p, y, 1.0f) : a;
-}
-
 // A token's coefficients for one channel.
 struct GatedCoeff {
     float s, i, y, a, q;   // sigmoid(r), sigmoid(g), log2 a, a, 1 - a^2
@@ -359,8 +348,9 @@ __device__ __forceinline__ GatedCoeff gated_coeff(float r, float g, float a2) {
     c.s = sigmoid_f32(r);
     c.i = sigmoid_f32(g);
     c.y = a2 * c.s;
-    c.a = decay<IO>(c.y);
-    c.q = one_minus_square<IO>(c.y, c.a);
+    const float e = hw_exp2(c.y), u = one_minus<IO>(c.y, e);
+    c.a = c.y > kNearOne<IO> ? 1.0f - u : e;
+    c.q = fmaf(u, c.a, u);
     return c;
 }
 
@@ -743,7 +733,7 @@ gated_bwd_kernel(const IO *__restrict__ x, const IO *__restrict__ r, const IO *_
             const float lam = grad_in(k, v, dzh) + G[v];
             if constexpr (GATE) oz[v] = dzh * hT[v];
             G[v] = a[k][v] * lam;
-            const float q = one_minus_square<IO>(Ad[v] * kLog2e * s[k][v], a[k][v]);
+            const float u = one_minus<IO>(Ad[v] * kLog2e * s[k][v], a[k][v]), q = fmaf(u, a[k][v], u);
             // 1 / beta; where 1 - a^2 is zero (or below what the unit resolves) the terms with it are dropped
             const float rb = fabsf(q) < FLT_MIN ? 0.0f : __builtin_amdgcn_rsqf(q);
             ox[v] = lam * (q * rb) * i[k][v];            // lambda beta i
