@@ -445,7 +445,7 @@ SSMSCAN_API int ssm_step_act(float *state, const void *u, const void *delta, con
  *                   when that is 0); its contents on entry do not matter.  After the call it
  *                   holds the states that ssm_gated_scan_bwd takes as checkpoints
  * Outputs must not overlap inputs or each other otherwise.  Arithmetic and states are fp32; 1 - a^2 is
- * formed without cancellation where a is near 1.
+ * formed without cancellation where a is near 1, and long products of decays from the sums of log a.
  * dims->dstate and dims->chunk_len are ignored; dim is at most 2^26, seqlen at most 2^30, and
  * batch * ceil(dim / 64), rounded up to a multiple of 8, times ceil(seqlen / 64) below 2^23 - 64 (the
  * work items of a launch; SSM_ERR_SHAPE may follow above that).
@@ -490,8 +490,8 @@ SSMSCAN_API size_t ssm_gated_scan_bwd_workspace_bytes(const ssm_dims *dims);
  *   state      : [batch][dim] fp32, read and overwritten with the new state
  *   x, r, g, y : [batch][dim] (io_dtype); z likewise, or NULL
  *   A          : [dim] fp32
- * The state and y are formed with the scan's arithmetic; y must not overlap the other tensors.  dims->seqlen, dstate and chunk_len are
- * ignored.  Returns SSM_OK or a negative ssm_status. */
+ * The arithmetic is fp32 as the scan's is; y must not overlap the other tensors.  dims->seqlen, dstate and
+ * chunk_len are ignored.  Returns SSM_OK or a negative ssm_status. */
 SSMSCAN_API int ssm_gated_step(float *state, const void *x, const void *r, const void *g, const float *A,
                 const void *z, void *y, const ssm_dims *dims, void *stream);
 

@@ -10,7 +10,9 @@
 // 64 V (lane = V neighbouring channels); one workgroup takes one (sequence, tile, chunk).  Its
 // kGatedWaves waves hold kGatedRows tokens each in registers.  Over a span of tokens the
 // recurrence is the map h -> P h + H (P: product of the decays, H: the state reached from zero),
-// and maps compose, so that
+// and maps compose.  P is carried as its logarithm, the sum of log2 a: products of decays near 1 are rounded
+// with a mean (1 - a of both is a few thousand ulps of 1, and their product is cut off), which slow channels
+// add up (the last state of 30,000 tokens at 1 / (1 - a) = 20,000 was off by 1.1e-4 of the rms).  So
 //   1. every wave forms (P, H) of its tokens,
 //   2. wave 0 folds the waves' maps into the chunk's, fetches the state at the chunk's start from
 //      the chunks before it (the chain, below) and publishes the state at its end,
@@ -36,11 +38,11 @@
 // nothing is there yet; the forward's are also the states that the backward starts from.  With few
 // chains a round trip per chunk would be all that happens, so the chunks of a chain form groups (the
 // host chooses their size; chain_step): word[sequence][item][channel] is 64 bits, a chunk publishes
-// its map (P, H), two floats, as soon as it has it, and the last chunk of a group publishes instead the
-// state at its end, as (-1, h), once it knows it.  A chunk fetches the maps of the chunks before it in
+// its map (log2 P, H), two floats, as soon as it has it, and the last chunk of a group publishes instead the
+// state at its end, as (1, h), once it knows it.  A chunk fetches the maps of the chunks before it in
 // its group (which wait for nobody; the waves share them), composes them, and applies them to the
 // state that the group before left.  Only the groups' last chunks wait in line.  The chain's first
-// chunk publishes the constant map (0, state at its end): it alone reads the initial state.
+// chunk publishes the constant map (-infinity, state at its end): it alone reads the initial state.
 // The words are filled with ones before the kernel starts.  A word travels in one store, so one that is
 // read is whole and nothing else has to be ordered.  Which words a chunk combines, and in which order,
 // is fixed: the results do not depend on timing.
@@ -75,12 +77,12 @@ constexpr int kGatedCounterStride = 64;                  // ints between them: l
 // that 2^y was rounded in, so there a polynomial in y takes its place, y (c0 + c1 y + ...), interpolated at
 // Chebyshev nodes of the interval: degree 4 for a > 0.82 where both the inputs and the outputs are fp32
 // (relative error below 1e-9, 1.1e-7 as it is evaluated; the difference below that 3e-7), or degree 2 for
-// a > 0.94 (4e-7; the difference 9e-7).  From u come both
-//   a       = 1 - u, rounded once: 2^y of the exponential unit is good to an ulp, but near 1 its error has a
-//             mean (-7e-9 for 1 - a below 2e-3), which a slow channel adds up over its memory of 1 / (1 - a)
-//             tokens (sequences of 4100 tokens were off by up to 1.7e-4 of their rms); an error relative to u is
-//             only that error of the state,
-//   1 - a^2 = u + u a.
+// a > 0.94 (4e-7; the difference 9e-7).  From u come
+//   1 - a^2 = u + u a,
+//   a       = 1 - u, rounded once, where it matters (gated_coeff): 2^y of the exponential unit is good to an
+//             ulp, but near 1 its error has a mean (-7e-9 for 1 - a below 2e-3), which a slow channel adds up
+//             over its memory of 1 / (1 - a) tokens wherever decays are all that a state goes on by, whereas an
+//             error relative to u is only that error of the state.
 template <typename IO> constexpr float kNearOne = sizeof(IO) == 4 ? -0.289f : -0.09f;   // y from which u is near
 template <typename IO> __device__ __forceinline__ float one_minus(float y, float exp2_y) {
     float p;
@@ -94,6 +96,11 @@ template <typename IO> __device__ __forceinline__ float one_minus(float y, float
         p = fmaf(p, y, -0.6931469440460205f);
     }
     return y > kNearOne<IO> ? p * y : 1.0f - exp2_y;
+}
+// 2^y, the decay over a span of tokens.
+__device__ __forceinline__ float decay(float y) {
+    const float e = hw_exp2(y), u = one_minus<float>(y, e);
+    return y > kNearOne<float> ? 1.0f - u : e;
 }
 
 // V neighbouring I/O elements of a row as raw 32-bit words.  Rows of an odd width start at odd
@@ -162,39 +169,39 @@ template <typename IO> __device__ __forceinline__ uint32_t minus_inf_words() {
 
 // The chain's words.
 constexpr uint32_t kWordEmpty = 0xffffffffu;
-__device__ __forceinline__ uint64_t chain_word(float P, float H) {
-    const uint32_t p = P != P ? 0x7fc00000u : __float_as_uint(P);   // (a NaN's bits could read as "empty")
-    return ((uint64_t)p << 32) | __float_as_uint(H);
+__device__ __forceinline__ uint64_t chain_word(float Y, float H) {
+    const uint32_t y = Y != Y ? 0x7fc00000u : __float_as_uint(Y);   // (a NaN's bits could read as "empty")
+    return ((uint64_t)y << 32) | __float_as_uint(H);
 }
-__device__ __forceinline__ void chain_put(uint64_t *w, float P, float H) {
-    __hip_atomic_store(w, chain_word(P, H), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+__device__ __forceinline__ void chain_put(uint64_t *w, float Y, float H) {
+    __hip_atomic_store(w, chain_word(Y, H), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 __device__ __forceinline__ uint64_t chain_read(const uint64_t *w) {
     return __hip_atomic_load(const_cast<uint64_t *>(w), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
 // The chain's step for the item at position pos, called by the whole workgroup: base + p * stride is
-// the word of position p (the lane's first of V channels), (P, H) the item's map and start the state
+// the word of position p (the lane's first of V channels), (2^Y, H) the item's map and start the state
 // at position 0's start (both read in wave 0 only; 0 at other positions), `ends`: nobody comes after.
 // Leaves the state at the item's start in s_in (behind a barrier) and the one at its end in wave 0's `out`.
 template <int V>
 __device__ __forceinline__ void chain_step(uint64_t *base, int64_t stride, int pos, int group, bool ends, bool act,
-                                           int lane, int w, const float (&P)[V], const float (&H)[V], const float (&start)[V],
-                                           float (&s_map)[2][kGatedWaves][64 * V], float (&s_in)[64 * V],
+                                           int lane, int w, const float (&Y)[V], const float (&H)[V], const float (&start)[V],
+                                           float (&s_map)[3][kGatedWaves][64 * V], float (&s_in)[64 * V],
                                            float (&out)[V]) {
     const int g = pos & (group - 1);   // (a power of two)
     uint64_t *own = base + pos * stride;
     if (w == 0 && act && !ends && g != group - 1) {
 #pragma unroll
         for (int v = 0; v < V; ++v)
-            if (pos == 0) chain_put(own + v, 0.0f, fmaf(P[v], start[v], H[v]));
-            else chain_put(own + v, P[v], H[v]);
+            if (pos == 0) chain_put(own + v, -__builtin_inff(), fmaf(decay(Y[v]), start[v], H[v]));
+            else chain_put(own + v, Y[v], H[v]);
     }
     // the maps of the group's items before this one, in equal runs over the waves: each composes its run
     const int m = (g + kGatedWaves - 1) / kGatedWaves, lo = w * m, hi = min(lo + m, g);
     if (lo < hi) {
         const uint64_t *src = base + (pos - g + lo) * stride;
-        float cp[V], ch[V];
+        float cy[V], ch[V];
         for (int k = lo; k < hi; ++k, src += stride) {
             uint64_t u[V];
             for (;;) {
@@ -209,30 +216,35 @@ __device__ __forceinline__ void chain_step(uint64_t *base, int64_t stride, int p
             }
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                const float p = __uint_as_float((uint32_t)(u[v] >> 32)), h = __uint_as_float((uint32_t)u[v]);
-                ch[v] = k == lo ? h : fmaf(p, ch[v], h);
-                cp[v] = k == lo ? p : cp[v] * p;
+                const float y = __uint_as_float((uint32_t)(u[v] >> 32)), h = __uint_as_float((uint32_t)u[v]);
+                ch[v] = k == lo ? h : fmaf(decay(y), ch[v], h);
+                cy[v] = k == lo ? y : cy[v] + y;
             }
         }
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            s_map[0][w][lane * V + v] = cp[v];
+            s_map[0][w][lane * V + v] = cy[v];
             s_map[1][w][lane * V + v] = ch[v];
+            s_map[2][w][lane * V + v] = decay(cy[v]);
         }
     }
     if (g > 0) __syncthreads();
     if (w == 0) {
-        float cp[V], ch[V], in[V];
+        float cy[V], ch[V], in[V], P[V], cp[V];
 #pragma unroll
-        for (int v = 0; v < V; ++v) cp[v] = 1.0f, ch[v] = 0.0f;
-#pragma unroll 2
+        for (int v = 0; v < V; ++v) cy[v] = 0.0f, ch[v] = 0.0f, P[v] = decay(Y[v]);
+#pragma unroll 1   // (two at a time spill registers in the backward)
         for (int k = 0; k * m < g; ++k)
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                const float p = s_map[0][k][lane * V + v];
-                ch[v] = fmaf(p, ch[v], s_map[1][k][lane * V + v]);
-                cp[v] *= p;
+                ch[v] = fmaf(s_map[2][k][lane * V + v], ch[v], s_map[1][k][lane * V + v]);
+                cy[v] += s_map[0][k][lane * V + v];
             }
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            cp[v] = decay(cy[v]);
+            asm volatile("" : "+v"(cp[v]), "+v"(P[v]));   // (ready before the wait, which they would lengthen)
+        }
         if (pos == g) {   // the first group: position 0 has taken the start in (0 elsewhere)
 #pragma unroll
             for (int v = 0; v < V; ++v) in[v] = start[v];
@@ -244,7 +256,7 @@ __device__ __forceinline__ void chain_step(uint64_t *base, int64_t stride, int p
                 for (int v = 0; v < V; ++v) {
                     const uint64_t u = chain_read(src + v);
                     in[v] = __uint_as_float((uint32_t)u);
-                    all = all && (uint32_t)(u >> 32) == __float_as_uint(-1.0f);
+                    all = all && (uint32_t)(u >> 32) == __float_as_uint(1.0f);
                 }
                 if (__all(all || !act)) break;
                 __builtin_amdgcn_s_sleep(1);
@@ -254,7 +266,7 @@ __device__ __forceinline__ void chain_step(uint64_t *base, int64_t stride, int p
         for (int v = 0; v < V; ++v) {
             in[v] = fmaf(cp[v], in[v], ch[v]);
             out[v] = fmaf(P[v], in[v], H[v]);
-            if (act && !ends && g == group - 1) chain_put(own + v, -1.0f, out[v]);
+            if (act && !ends && g == group - 1) chain_put(own + v, 1.0f, out[v]);
             s_in[lane * V + v] = in[v];
         }
     }
@@ -266,11 +278,16 @@ __device__ __forceinline__ void chain_step(uint64_t *base, int64_t stride, int p
 // Arguments and results as chain_step's.
 template <int V>
 __device__ __forceinline__ void chain_hand(uint32_t *base, int64_t stride, int pos, bool ends, bool act, int lane,
-                                           int w, const float (&P)[V], const float (&H)[V], const float (&start)[V],
+                                           int w, const float (&Y)[V], const float (&H)[V], const float (&start)[V],
                                            float (&s_in)[64 * V], float (&out)[V]) {
     if (w == 0) {
-        float in[V];
+        float in[V], P[V];
         uint32_t *own = base + pos * stride;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            P[v] = decay(Y[v]);
+            asm volatile("" : "+v"(P[v]));   // (ready before the wait, which it would lengthen)
+        }
         if (pos == 0) {
 #pragma unroll
             for (int v = 0; v < V; ++v) in[v] = start[v];
@@ -338,18 +355,21 @@ gated_clear_kernel(u32x4_t *__restrict__ words, int64_t n, u32x4_t *__restrict__
     else if (i - n < kGatedQueues * kGatedCounterStride / 4) counters[i - n] = zeros;
 }
 
-// A token's coefficients for one channel.
+// A token's coefficients for one channel.  STEP: the state goes from token to token by a alone.  (Between the
+// chunks of a scan it goes by the sums of y; inside one, 64 or 128 tokens add up to 4e-7 on average, below the
+// polynomial's own error for bf16, which therefore leaves the unit's value: B8 L2048 D5120 168 us, 171 with
+// 1 - u.)
 struct GatedCoeff {
     float s, i, y, a, q;   // sigmoid(r), sigmoid(g), log2 a, a, 1 - a^2
 };
-template <typename IO>
+template <typename IO, bool STEP = false>
 __device__ __forceinline__ GatedCoeff gated_coeff(float r, float g, float a2) {
     GatedCoeff c;
     c.s = sigmoid_f32(r);
     c.i = sigmoid_f32(g);
     c.y = a2 * c.s;
     const float e = hw_exp2(c.y), u = one_minus<IO>(c.y, e);
-    c.a = c.y > kNearOne<IO> ? 1.0f - u : e;
+    c.a = (STEP || sizeof(IO) == 4) && c.y > kNearOne<IO> ? 1.0f - u : e;
     c.q = fmaf(u, c.a, u);
     return c;
 }
@@ -368,8 +388,8 @@ gated_scan_kernel(const IO *__restrict__ x, const IO *__restrict__ r, const IO *
     constexpr int C = T * K, M = C / kGatedChunk;
     static_assert(K == kGatedWaves && C % kGatedChunk == 0 && K % M == 0, "a stored state is at a wave's end");
     using Row = row_words<V, IO, NT>;
-    __shared__ float s_P[K][64 * V], s_H[K][64 * V], s_in[64 * V];
-    __shared__ float s_map[2][kGatedWaves][64 * V];
+    __shared__ float s_P[K][64 * V], s_Y[K][64 * V], s_H[K][64 * V], s_in[64 * V];
+    __shared__ float s_map[3][kGatedWaves][64 * V];
     __shared__ int s_slot;
     const GatedItem it = gated_item(chains, tiles, nitem, seq_lens != nullptr, counters, queues, run, &s_slot);
     if (it.pos < 0) return;
@@ -432,9 +452,9 @@ gated_scan_kernel(const IO *__restrict__ x, const IO *__restrict__ r, const IO *
     }
 
     // 1. the coefficients and the wave's map
-    float a[T][V], bb[T][V], P[V], H[V];
+    float a[T][V], bb[T][V], Y[V], H[V];
 #pragma unroll
-    for (int v = 0; v < V; ++v) P[v] = 1.0f, H[v] = 0.0f;
+    for (int v = 0; v < V; ++v) Y[v] = 0.0f, H[v] = 0.0f;
 #pragma unroll
     for (int k = 0; k < T; ++k) {
 #pragma unroll
@@ -442,13 +462,14 @@ gated_scan_kernel(const IO *__restrict__ x, const IO *__restrict__ r, const IO *
             const GatedCoeff cf = gated_coeff<IO>(rr[k].get(v), rg[k].get(v), a2[v]);
             a[k][v] = cf.a;
             bb[k][v] = __builtin_amdgcn_sqrtf(cf.q) * cf.i * rx[k].get(v);
-            P[v] *= a[k][v];
+            Y[v] += cf.y;
             H[v] = fmaf(a[k][v], H[v], bb[k][v]);
         }
     }
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-        s_P[w][lane * V + v] = P[v];
+        s_P[w][lane * V + v] = hw_exp2(Y[v]);   // (inside the chunk, where nothing adds up, it will do)
+        s_Y[w][lane * V + v] = Y[v];
         s_H[w][lane * V + v] = H[v];
     }
     // (the gate is requested here: it is needed last, and comes while the chain is waited for)
@@ -468,9 +489,8 @@ gated_scan_kernel(const IO *__restrict__ x, const IO *__restrict__ r, const IO *
         for (int k = 1; k < K; ++k)
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                const float p = s_P[k][lane * V + v];
-                H[v] = fmaf(p, H[v], s_H[k][lane * V + v]);
-                P[v] *= p;
+                H[v] = fmaf(s_P[k][lane * V + v], H[v], s_H[k][lane * V + v]);
+                Y[v] += s_Y[k][lane * V + v];
             }
         // (read before anything is published: the chain's last item may write last_state over it)
         if (c == 0 && h0) {
@@ -480,9 +500,9 @@ gated_scan_kernel(const IO *__restrict__ x, const IO *__restrict__ r, const IO *
     }
     const int64_t chain0 = (int64_t)b * nitem * D + d;
     if (group == 1)
-        chain_hand<V>(static_cast<uint32_t *>(words) + chain0, D, c, ends, act, lane, w, P, H, start, s_in, out);
+        chain_hand<V>(static_cast<uint32_t *>(words) + chain0, D, c, ends, act, lane, w, Y, H, start, s_in, out);
     else
-        chain_step<V>(static_cast<uint64_t *>(words) + chain0, D, c, group, ends, act, lane, w, P, H, start, s_map,
+        chain_step<V>(static_cast<uint64_t *>(words) + chain0, D, c, group, ends, act, lane, w, Y, H, start, s_map,
                       s_in, out);
     float *st = states ? states + ((int64_t)b * nchunk + c * M) * D + d : nullptr;   // the item's states
     if (w == 0 && act) {
@@ -542,8 +562,8 @@ gated_bwd_kernel(const IO *__restrict__ x, const IO *__restrict__ r, const IO *_
                  int group) {
     constexpr int T = kGatedRows, K = kGatedWaves, C = kGatedChunk;
     using Row = row_words<V, IO, NT>;
-    __shared__ float s_P[K][64 * V], s_H[K][64 * V], s_G[K][64 * V], s_in[64 * V];
-    __shared__ float s_map[2][kGatedWaves][64 * V];
+    __shared__ float s_P[K][64 * V], s_Y[K][64 * V], s_H[K][64 * V], s_G[K][64 * V], s_in[64 * V];
+    __shared__ float s_map[3][kGatedWaves][64 * V];
     __shared__ int s_slot;
     const GatedItem it = gated_item(chains, tiles, nchunk, seq_lens != nullptr, counters, queues, run, &s_slot);
     if (it.pos < 0) return;
@@ -620,9 +640,9 @@ gated_bwd_kernel(const IO *__restrict__ x, const IO *__restrict__ r, const IO *_
     }
 
     // 1. the coefficients and the wave's two maps
-    float s[T][V], i[T][V], a[T][V], bb[T][V], P[V], H[V], G[V];
+    float s[T][V], i[T][V], a[T][V], bb[T][V], Y[V], H[V], G[V];
 #pragma unroll
-    for (int v = 0; v < V; ++v) P[v] = 1.0f, H[v] = 0.0f, G[v] = 0.0f;
+    for (int v = 0; v < V; ++v) Y[v] = 0.0f, H[v] = 0.0f, G[v] = 0.0f;
 #pragma unroll
     for (int k = 0; k < T; ++k)
 #pragma unroll
@@ -632,7 +652,7 @@ gated_bwd_kernel(const IO *__restrict__ x, const IO *__restrict__ r, const IO *_
             i[k][v] = cf.i;
             a[k][v] = cf.a;
             bb[k][v] = __builtin_amdgcn_sqrtf(cf.q) * cf.i * rx[k].get(v);
-            P[v] *= cf.a;
+            Y[v] += cf.y;
             H[v] = fmaf(cf.a, H[v], bb[k][v]);
         }
     // dh_t, and with a gate the factor of h_t in dz: silu(z) = z sz, silu'(z) = sz (1 + z (1 - sz))
@@ -652,7 +672,8 @@ gated_bwd_kernel(const IO *__restrict__ x, const IO *__restrict__ r, const IO *_
         }
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-        s_P[w][lane * V + v] = P[v];
+        s_P[w][lane * V + v] = hw_exp2(Y[v]);
+        s_Y[w][lane * V + v] = Y[v];
         s_H[w][lane * V + v] = H[v];
         s_G[w][lane * V + v] = G[v];
     }
@@ -661,19 +682,18 @@ gated_bwd_kernel(const IO *__restrict__ x, const IO *__restrict__ r, const IO *_
     // 2. the adjoint at the chunk's end, and the one that it hands on
     const bool starts = c == nlive - 1;
     float start[V] = {}, out[V];
-    if (w == 0) {   // the chunk's map (over P and G, which wave 0 needs no more)
+    if (w == 0) {   // the chunk's map (over Y and G, which wave 0 needs no more)
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            P[v] = s_P[K - 1][lane * V + v];
+            Y[v] = s_Y[K - 1][lane * V + v];
             G[v] = s_G[K - 1][lane * V + v];
         }
 #pragma unroll
         for (int k = K - 2; k >= 0; --k)
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                const float p = s_P[k][lane * V + v];
-                G[v] = fmaf(p, G[v], s_G[k][lane * V + v]);
-                P[v] *= p;
+                G[v] = fmaf(s_P[k][lane * V + v], G[v], s_G[k][lane * V + v]);
+                Y[v] += s_Y[k][lane * V + v];
             }
         if (starts && dlast) {
 #pragma unroll
@@ -682,10 +702,10 @@ gated_bwd_kernel(const IO *__restrict__ x, const IO *__restrict__ r, const IO *_
     }
     const int64_t chain0 = ((int64_t)b * nchunk + nlive - 1) * D + d;
     if (group == 1)
-        chain_hand<V>(static_cast<uint32_t *>(words) + chain0, -D, nlive - 1 - c, c == 0, act, lane, w, P, G, start,
+        chain_hand<V>(static_cast<uint32_t *>(words) + chain0, -D, nlive - 1 - c, c == 0, act, lane, w, Y, G, start,
                       s_in, out);
     else
-        chain_step<V>(static_cast<uint64_t *>(words) + chain0, -D, nlive - 1 - c, group, c == 0, act, lane, w, P, G,
+        chain_step<V>(static_cast<uint64_t *>(words) + chain0, -D, nlive - 1 - c, group, c == 0, act, lane, w, Y, G,
                       start, s_map, s_in, out);
     if (w == 0 && act && c == 0 && dh0) {
 #pragma unroll
@@ -805,7 +825,7 @@ gated_step_kernel(float *__restrict__ state, const IO *__restrict__ x, const IO 
     const int64_t e = base + threadIdx.x * kStepVec;
     if (e >= n) return;
     auto token = [&](float rr, float gg, float xx, float Av, float h) {
-        const GatedCoeff cf = gated_coeff<IO>(rr, gg, Av * kLog2e);
+        const GatedCoeff cf = gated_coeff<IO, true>(rr, gg, Av * kLog2e);
         return fmaf(cf.a, h, __builtin_amdgcn_sqrtf(cf.q) * cf.i * xx);
     };
     const int64_t d = e % D;
