@@ -50,7 +50,7 @@
 extern "C" {
 #endif
 
-#define SSMSCAN_VERSION 16
+#define SSMSCAN_VERSION 17
 
 /* Bits of the `flags` argument of the scan entry points. */
 #define SSM_SCAN_SOFTPLUS 1     /* step size = softplus(delta + delta_bias) */
@@ -457,6 +457,22 @@ SSMSCAN_API int ssm_gated_scan_fwd(const void *x, const void *r, const void *g, 
 /* Bytes of device workspace ssm_gated_scan_fwd needs for these sizes (0 for an invalid or empty
  * problem, and for sequences that are scanned in one piece). */
 SSMSCAN_API size_t ssm_gated_scan_workspace_bytes(const ssm_dims *dims);
+
+/* The schedule that ssm_gated_scan_fwd (backward = 0) or ssm_gated_scan_bwd (1) takes for these sizes; the
+ * results do not depend on the order in which its work items happen to run.  A chain is the run of work items
+ * of one sequence and one tile of 64 * lane_channels channels.  Fills *out (zeros for an empty problem);
+ * returns SSM_OK or a negative ssm_status. */
+typedef struct ssm_gated_plan {
+    int64_t chains;
+    int64_t items;          /* work items of a chain */
+    int64_t workgroups;     /* of the launch: an item each, or none */
+    int32_t lane_channels;  /* neighbouring channels per lane */
+    int32_t item_chunks;    /* units of 64 tokens per work item */
+    int32_t group;          /* items that share a hand-over of the state (1: each waits for the one before) */
+    int32_t queues;         /* counters that the items are drawn from, chains dealt to them in turn */
+    int32_t run;            /* consecutive workgroups that draw from the same counter */
+} ssm_gated_plan;
+SSMSCAN_API int ssm_gated_scan_plan(const ssm_dims *dims, int backward, ssm_gated_plan *out);
 
 /* Gradients of ssm_gated_scan_fwd given dy = dLoss/dy and dlast_state = dLoss/d(last_state).
  * With dh_t = dy_t silu(z_t) and lambda_t = dh_t + a_{t+1} lambda_{t+1} (dlast_state added after

@@ -140,6 +140,15 @@ int *launch_clear(const Plan &p, void *words, void *ws, int64_t nitem, const ssm
     return reinterpret_cast<int *>(counters);
 }
 
+// Items of two chunks halve the hand-overs of a chain, at two workgroups per CU instead of three.  They
+// pay where chains are long, as long as the halved number of items still fills the chip (B1 L131072 D2048
+// bf16 gated: 556 -> 498 us; B2 L8192 D3000: 144 -> 128; B2 L8192 D2048 fp32: 126 -> 111; but 32 chunks, B8
+// L2048 D5120: 168 and 168, fp32: 290 -> 307; B3 L4096 D1400, 2112 chunks in all: 54 -> 57).
+int fwd_item_chunks(const ssm_dims *dm, const Plan &p) {
+    const bool one_bf16 = dm->io_dtype == SSM_IO_BF16 && p.V == 1;   // (narrow or few: short chains, or few items)
+    return !one_bf16 && p.nchunk >= 64 && p.chains * p.nchunk >= 2304 ? 2 : 1;
+}
+
 template <typename IO, int V, int T, int K, bool OUT, bool NT>
 void launch_fwd_v(const void *x, const void *r, const void *g, const float *A, const void *z, const float *h0,
                   const int32_t *sl, void *y, float *last, void *ws, const ssm_dims *dm, const Plan &p,
@@ -158,17 +167,11 @@ void launch_fwd_v(const void *x, const void *r, const void *g, const float *A, c
                        (int)p.nchunk, queues_of(p), run_of(p, nitem), group_of(p));
 }
 
-// Items of two chunks halve the hand-overs of a chain, at two workgroups per CU instead of three.  They
-// pay where chains are long, as long as the halved number of items still fills the chip (B1 L131072 D2048
-// bf16 gated: 556 -> 498 us; B2 L8192 D3000: 144 -> 128; B2 L8192 D2048 fp32: 126 -> 111; but 32 chunks, B8
-// L2048 D5120: 168 and 168, fp32: 290 -> 307; B3 L4096 D1400, 2112 chunks in all: 54 -> 57).
-bool wide_items(const Plan &p) { return p.nchunk >= 64 && p.chains * p.nchunk >= 2304; }
-
 template <bool OUT, bool NT>
 void launch_fwd_n(const void *x, const void *r, const void *g, const float *A, const void *z, const float *h0,
                 const int32_t *sl, void *y, float *last, void *ws, const ssm_dims *dm, const Plan &p,
                 hipStream_t st) {
-    const bool wide = wide_items(p);
+    const bool wide = fwd_item_chunks(dm, p) == 2;
     auto launch = dm->io_dtype == SSM_IO_F32
                       ? (wide ? launch_fwd_v<float, 1, 16, 8, OUT, NT> : launch_fwd_v<float, 1, 8, 8, OUT, NT>)
                   : p.V == 2 ? (wide ? launch_fwd_v<uint16_t, 2, 16, 8, OUT, NT>
@@ -217,6 +220,26 @@ size_t ssm_gated_scan_workspace_bytes(const ssm_dims *dims) {
     if (check_gated_dims(dims, true) != SSM_OK || dims->batch == 0 || dims->dim == 0) return 0;
     const Plan p = make_plan(dims);
     return check_items(p) == SSM_OK ? p.bytes : 0;
+}
+
+int ssm_gated_scan_plan(const ssm_dims *dims, int backward, ssm_gated_plan *out) {
+    if (!out) return fail(SSM_ERR_NULL, "out is NULL");
+    *out = {};
+    const int rc = check_gated_dims(dims, true);
+    if (rc != SSM_OK) return rc;
+    if (dims->batch == 0 || dims->dim == 0) return ok();
+    const Plan p = make_plan(dims);
+    if (const int e = check_items(p)) return e;
+    out->item_chunks = backward ? 1 : fwd_item_chunks(dims, p);
+    const int64_t nitem = (p.nchunk + out->item_chunks - 1) / out->item_chunks;
+    out->chains = p.chains;
+    out->items = nitem;
+    out->workgroups = grid_of(p, nitem);
+    out->lane_channels = p.V;
+    out->group = group_of(p);
+    out->queues = queues_of(p);
+    out->run = run_of(p, nitem);
+    return ok();
 }
 
 size_t ssm_gated_scan_bwd_workspace_bytes(const ssm_dims *dims) {

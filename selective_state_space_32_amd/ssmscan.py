@@ -43,6 +43,11 @@ class ssm_plan_info(ctypes.Structure):
                 ("workspace_bytes", ctypes.c_size_t)]
 
 
+class ssm_gated_plan(ctypes.Structure):
+    _fields_ = ([(f, ctypes.c_int64) for f in ("chains", "items", "workgroups")] +
+                [(f, ctypes.c_int32) for f in ("lane_channels", "item_chunks", "group", "queues", "run")])
+
+
 class SSMError(RuntimeError):
     def __init__(self, code: int, msg: str):
         super().__init__(f"{STATUS.get(code, code)}: {msg}")
@@ -97,6 +102,8 @@ def _load() -> ctypes.CDLL:
     lib.ssm_gated_scan_workspace_bytes.restype = ctypes.c_size_t
     lib.ssm_gated_scan_bwd_workspace_bytes.argtypes = [D]
     lib.ssm_gated_scan_bwd_workspace_bytes.restype = ctypes.c_size_t
+    lib.ssm_gated_scan_plan.argtypes = [D, ctypes.c_int, ctypes.POINTER(ssm_gated_plan)]
+    lib.ssm_gated_scan_plan.restype = ctypes.c_int
     lib.ssm_gated_scan_fwd.argtypes = [P] * 9 + [D, P, ctypes.c_size_t, P]
     lib.ssm_gated_scan_fwd.restype = ctypes.c_int
     lib.ssm_gated_scan_bwd.argtypes = [P] * 10 + [ctypes.c_size_t] + [P] * 6 + [D, P, ctypes.c_size_t, P]
@@ -801,6 +808,15 @@ def _gated_inputs(x, r, g, A, z, initial_state, seq_lens):
     if seq_lens is not None:
         _need_lens(seq_lens, bsz, dev)
     return bsz, L, dim, dev, io, ssm_dims(bsz, L, dim, 1, _io_code(io), 0)
+
+
+def gated_plan(batch: int, seqlen: int, dim: int, io_dtype, backward: bool = False) -> dict:
+    """The gated recurrence's schedule for these sizes (ssm_gated_scan_plan), as a dict of the ssm_gated_plan
+    fields."""
+    d = make_dims(batch, seqlen, dim, 1, io_dtype)
+    out = ssm_gated_plan()
+    _check(lib.ssm_gated_scan_plan(ctypes.byref(d), int(backward), ctypes.byref(out)))
+    return {f: getattr(out, f) for f, _ in ssm_gated_plan._fields_}
 
 
 def gated_scan_fwd(x: torch.Tensor, r: torch.Tensor, g: torch.Tensor, A: torch.Tensor,
