@@ -6,7 +6,6 @@ import random
 import pytest
 
 
-
 @pytest.fixture(scope="module")
 def b():
     from selective_state_space_32_amd import ssmscan
