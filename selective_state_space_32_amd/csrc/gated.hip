@@ -51,8 +51,8 @@ struct Plan {
 constexpr int64_t kCounterInts = ssm::kGatedQueues * ssm::kGatedCounterStride;
 
 // Channels per lane: two bf16 or one fp32, four bytes an access; one bf16 too where tiles of two would
-// leave CUs idle (at most one workgroup each: B1 L512 D2048, 128 items: 7.2 against 8.8 us, backward 9.6
-// against 11.8; B1 L4096 D256: 8.6 and 11.0, 11.1 and 14.0), and where the last of an odd width's
+// leave CUs idle (at most one workgroup each: B1 L512 D2048, 128 items: 7.4 against 9.8 us, backward 10.1
+// against 12.9; B1 L4096 D256: 9.0 and 11.7, 11.8 and 15.3), and where the last of an odd width's
 // channels would be a tile of its own: its lane shares a channel with its neighbour, which has to be in
 // the same wave, as a state that is advanced in place is read by one and written by the other.
 int lane_channels(const ssm_dims *dm, int64_t nchunk) {
@@ -77,10 +77,10 @@ Plan make_plan(const ssm_dims *dm) {
 // Queues that share the chains (see the kernel): as many as there are XCDs, unless some would then be
 // much longer than the average; every queue has as many workgroups as the longest needs, those without
 // an item still have to be dispatched, and an XCD whose queue is done has nothing left.  Short chains,
-// where hand-overs count, take a quarter more (B6 L1000 D1700 bf16, 84 chains: backward 51 us with eight
-// queues, 58 with seven), long ones a thirty-second (B3 L10000 D772, 21 chains: 95 us with eight, 74 with
-// seven, backward 145 and 122; B1 L30000 D2900, 23 chains: 231 with eight, 217 with one, 429 and 401; B1
-// L65536 D64, one chain: 131 with eight, 33 with one).
+// where hand-overs count, take a quarter more (B6 L1000 D1700 bf16, 84 chains: 29 us with eight queues, 31
+// with seven, backward 53 and 59), long ones a thirty-second (B3 L10000 D772, 21 chains: 83 us with eight, 73
+// with seven, backward 148 and 123; B1 L30000 D2900, 23 chains: 224 with eight, 213 with one, 436 and 407; B1
+// L65536 D64, one chain: 146 with eight, 35 with one).
 int queues_of(const Plan &p) {
     auto slots = [&](int64_t q) { return (p.chains + q - 1) / q * q; };
     int best = ssm::kGatedQueues;
@@ -90,23 +90,23 @@ int queues_of(const Plan &p) {
     return best;
 }
 
-// Consecutive workgroups that draw from one queue: 1 where the launch is short and hand-overs count (B2
-// L2048 D1536 fp32: 24 us, 27 with 8) or neighbouring tiles share lines; 8 where it is many rounds of the
-// chip and rows are whole lines, so that bandwidth counts, or an XCD would have so few tiles that there
-// is little to share (B1 L131072 D2047 bf16, 16 chains: 723 us with 1, 656 with 8, backward 1,429 and
-// 1,300; B2 L65536 D1500, 24 chains: 499 and 476, 979 and 964; B8 L2048 D5119, 320 chains: 201 and 223,
-// 367 and 429).
+// Consecutive workgroups that draw from one queue: 1 where the launch is short (B2 L2048 D1536 fp32: 25 us
+// with either, its backward 38.0 with 1, 38.4 with 8) or neighbouring tiles share lines; 8 where it is many
+// rounds of the chip and rows are whole lines (B1 L131072 D2048 bf16, 16 chains: 534 us with 1, 475 with 8; B8
+// L2048 D5120, 320 chains: 165 with either), or an XCD would have so few tiles that there is little to share
+// (B1 L131072 D2047, 16 chains: 720 with 1, 628 with 8, backward 1,453 and 1,305; B2 L65536 D1500, 24 chains:
+// 498 and 470, 991 and 962; but B8 L2048 D5119, 320 chains: 199 and 233, 368 and 429).
 int run_of(const Plan &p, int64_t nitem) {
     return (p.lines || p.chains <= 32) && p.chains * nitem >= 4096 ? ssm::kGatedRun : 1;
 }
 
 // Items of a chain that share a hand-over (see the kernel), a power of two.  A hand-over takes about 1.2
 // us, and while it runs every chain moves 0.013 us of data per item: with many chains every item can wait
-// for the one before it, and the maps' traffic is saved (B8 L2048 D5120 bf16, 320 chains: 168 us with
-// groups of one, 179 with eight, backward 309 and 324; B2 L8192 D5120, 80 chains: backward 308 with one,
-// 320 with four), with few the hand-overs have to be shared (B1 L131072 D2048, 16 chains: 689 us with one,
-// 499 with four or eight; B1 L65536 D512, 4 chains: 165 with two, 93 with eight, 89 with 16 or 32; D64, 1
-// chain: 96 with eight, 33 with 64; B2 L2048 D1536 fp32, 48 chains: 28 with one, 23 with two or four).
+// for the one before it, and the maps' traffic is saved (B8 L2048 D5120 bf16, 320 chains: 166 us with
+// groups of one, 176 with eight, backward 303 and 313; B2 L8192 D5120, 80 chains: backward 301 with one,
+// 308 with four), with few the hand-overs have to be shared (B1 L131072 D2048, 16 chains: 704 us with one,
+// 482 with four, 475 with eight; B1 L65536 D512, 4 chains: 167 with two, 92 with eight, 86 with 16 or 32; D64,
+// 1 chain: 98 with eight, 35 with 64; B2 L2048 D1536 fp32, 48 chains: 28 with one, 25 with two or four).
 int group_of(const Plan &p) {
     int g = 1;
     if (p.chains < 64)
@@ -142,8 +142,9 @@ int *launch_clear(const Plan &p, void *words, void *ws, int64_t nitem, const ssm
 
 // Items of two chunks halve the hand-overs of a chain, at two workgroups per CU instead of three.  They
 // pay where chains are long, as long as the halved number of items still fills the chip (B1 L131072 D2048
-// bf16 gated: 556 -> 498 us; B2 L8192 D3000: 144 -> 128; B2 L8192 D2048 fp32: 126 -> 111; but 32 chunks, B8
-// L2048 D5120: 168 and 168, fp32: 290 -> 307; B3 L4096 D1400, 2112 chunks in all: 54 -> 57).
+// bf16 gated: 563 us with one, 474 with two; B2 L8192 D3000: 146 and 126; B2 L8192 D2048 fp32: 132 and 116; but
+// B3 L4096 D1400, 2112 chunks in all: 55 and 57).  Chains of 32 chunks gain in bf16 and lose in fp32, so that
+// the rule leaves them (B8 L2048 D5120: 166 and 155, fp32 291 and 308).
 int fwd_item_chunks(const ssm_dims *dm, const Plan &p) {
     const bool one_bf16 = dm->io_dtype == SSM_IO_BF16 && p.V == 1;   // (narrow or few: short chains, or few items)
     return !one_bf16 && p.nchunk >= 64 && p.chains * p.nchunk >= 2304 ? 2 : 1;

@@ -20,18 +20,19 @@
 //      from there, writing y.
 // The inputs are read once and the outputs written once, whatever the length.
 //
-// Bound: HBM.  Per element the forward moves 8 bytes in bf16 (10 with a gate) and issues 42 VALU
+// Bound: HBM.  Per element the forward moves 8 bytes in bf16 (10 with a gate) and issues 43 VALU
 // instructions with its gate, 8 of them transcendental (three sigmoids, the decay, a root), which keeps
 // the VALU busy for two thirds of its time; the backward moves 14 (18), issues 84 and keeps it as busy.
 // Measured (averages at settled clocks), where a copy of 1 GiB reaches 5.1 TB/s: B8 L2048 D5120 bf16 gated
-// 167 us for 839 MB (855 by the counters), its backward 306 us for 1,510 MB (1,537); B1 L131072 D2048 bf16
-// 423 us for 2,148 MB; B2 L2048 D1536 fp32 25 us for 101 MB, its backward 38 us for 176 MB.  Short
-// launches are bound by their latency: 6 us for one chunk in a few tiles.
+// 167 us for 839 MB (855 by the counters), its backward 305 us for 1,510 MB (1,537); B1 L131072 D2048 bf16
+// 410 us for 2,148 MB; B2 L2048 D1536 fp32 25 us for 101 MB, its backward 39 us for 176 MB.  Short
+// launches are bound by their latency: 4.5 us for one chunk in four tiles, its backward 6.8.
 //
-// The split.  Eight tokens per wave keep a lane's values of V channels in registers (69 registers in
+// The split.  Eight tokens per wave keep a lane's values of V channels in registers (72 registers in
 // the forward, three workgroups per CU; 128 in the backward, two), and several workgroups per CU let
 // one load while another computes or waits.  At B8 L2048 D5120, sixteen waves of eight tokens took
-// 221 us where eight of eight took 169; eight of sixteen are an item of two chunks, taken for long chains.
+// 221 us where eight of eight took 169 (an earlier form of this kernel); eight of sixteen are an item of two
+// chunks, taken for long chains.
 //
 // The chain.  The state goes from chunk to chunk through memory.  With many chains every chunk waits for
 // the one before it (chain_hand): state[sequence][chunk][channel], four bytes, all ones meaning that
@@ -54,9 +55,9 @@
 // equal run of the chains; `run` consecutive workgroups draw from the same one.  The XCDs take
 // workgroups in turn, so with eight queues and run = 1 a queue's chains stay in one XCD: its hand-overs
 // are the fastest, and neighbouring tiles, which share lines where rows do not start on one, meet in
-// its L2 (B8 L2048 D5119 bf16 backward: 367 us, 429 with run = 8).  With run = 8 every XCD works on all
+// its L2 (B8 L2048 D5119 bf16 backward: 368 us, 429 with run = 8).  With run = 8 every XCD works on all
 // the chains, where with run = 1 it reads the same few columns of every row, which lie in few of the
-// memory's channels (B1 L131072 D2048 bf16 gated: 545 against 501 us).
+// memory's channels (B1 L131072 D2048 bf16 gated: 534 against 475 us).
 #pragma once
 
 #include <float.h>
@@ -106,8 +107,8 @@ __device__ __forceinline__ float decay(float y) {
 // V neighbouring I/O elements of a row as raw 32-bit words.  Rows of an odd width start at odd
 // elements, so the accesses assume no more than the element's own alignment (the memory unit takes
 // dwords at any byte address).  NT: past the caches, as data that is used once; not where rows start
-// inside a line, whose other part a neighbouring tile wants (B8 L2048 D5119 bf16: 214 against 231 us,
-// backward 417 against 527; at D5120 the other way round, 189 against 176 us).
+// inside a line, whose other part a neighbouring tile wants (B8 L2048 D5119 bf16: 199 us through the
+// caches, 205 past them, backward 368 and 484; at D5120 185 and 166, 310 and 304).
 #define SSM_GLOBAL __attribute__((address_space(1)))   // memory of the device: no other kind is tried
 template <int V, typename IO, bool NT = true> struct row_words {
     static constexpr int W = V * (int)sizeof(IO) < 4 ? 1 : V * (int)sizeof(IO) / 4;
@@ -181,14 +182,14 @@ __device__ __forceinline__ uint64_t chain_read(const uint64_t *w) {
 }
 
 // The chain's step for the item at position pos, called by the whole workgroup: base + p * stride is
-// the word of position p (the lane's first of V channels), (2^Y, H) the item's map and start the state
+// the word of position p (the lane's first of V channels), h -> 2^Y h + H the item's map and start the state
 // at position 0's start (both read in wave 0 only; 0 at other positions), `ends`: nobody comes after.
 // Leaves the state at the item's start in s_in (behind a barrier) and the one at its end in wave 0's `out`.
 template <int V>
 __device__ __forceinline__ void chain_step(uint64_t *base, int64_t stride, int pos, int group, bool ends, bool act,
-                                           int lane, int w, const float (&Y)[V], const float (&H)[V], const float (&start)[V],
-                                           float (&s_map)[3][kGatedWaves][64 * V], float (&s_in)[64 * V],
-                                           float (&out)[V]) {
+                                           int lane, int w, const float (&Y)[V], const float (&H)[V],
+                                           const float (&start)[V], float (&s_map)[3][kGatedWaves][64 * V],
+                                           float (&s_in)[64 * V], float (&out)[V]) {
     const int g = pos & (group - 1);   // (a power of two)
     uint64_t *own = base + pos * stride;
     if (w == 0 && act && !ends && g != group - 1) {
@@ -319,8 +320,8 @@ __device__ __forceinline__ void chain_hand(uint32_t *base, int64_t stride, int p
 // Which item this workgroup takes: (sequence, tile, position along the chain), or pos < 0 for none.
 // A queue's chains are walked together, position by position.  Chains are numbered sequence by
 // sequence, or, where the sequences have lengths of their own, tile by tile, so that every queue gets
-// its share of the long ones (B8 L2048 D5120 bf16, lengths from 2048 down to 0, backward: 309 against
-// 233 us).
+// its share of the long ones (B8 L2048 D5120 bf16 gated, lengths from 2048 down to 0: 134 us in the order of
+// the sequences, 112 like this, backward 266 and 232).
 struct GatedItem {
     int b, tile, pos;
 };
@@ -357,8 +358,8 @@ gated_clear_kernel(u32x4_t *__restrict__ words, int64_t n, u32x4_t *__restrict__
 
 // A token's coefficients for one channel.  STEP: the state goes from token to token by a alone.  (Between the
 // chunks of a scan it goes by the sums of y; inside one, 64 or 128 tokens add up to 4e-7 on average, below the
-// polynomial's own error for bf16, which therefore leaves the unit's value: B8 L2048 D5120 168 us, 171 with
-// 1 - u.)
+// polynomial's own error for bf16, which therefore leaves the unit's value: B8 L2048 D5120 166 us, 167 to 170
+// with 1 - u.)
 struct GatedCoeff {
     float s, i, y, a, q;   // sigmoid(r), sigmoid(g), log2 a, a, 1 - a^2
 };
@@ -790,7 +791,7 @@ gated_bwd_kernel(const IO *__restrict__ x, const IO *__restrict__ r, const IO *_
 
 // out[d] = sum of the n rows of part, in an order of their own: kColumnGroups groups of threads take
 // every kColumnGroups-th row of kColumnCols columns, and their sums are added in order.  Bound: the
-// latency of a few dependent loads (64 rows of 1536 columns: 3.9 us).
+// latency of a few dependent loads (64 rows of 1536 columns: 4.3 us).
 constexpr int kColumnCols = 32, kColumnGroups = 32;
 static __global__ void __launch_bounds__(kColumnCols * kColumnGroups)
 column_sum_kernel(const float *__restrict__ part, float *__restrict__ out, int64_t n, int64_t D) {
@@ -813,7 +814,7 @@ column_sum_kernel(const float *__restrict__ part, float *__restrict__ out, int64
 // One token of every sequence, the state updated in place.  The tensors are walked as flat arrays,
 // kStepVec neighbouring elements per thread (they may lie in two rows; A's index wraps with them).
 // Bound: HBM, 8 bytes of state and 4 or 5 I/O elements per channel (S256 D5120 bf16 with its gate:
-// 23.6 MB, 4.9 us on the device).  The state is left in the caches for the next token.
+// 23.6 MB, 5.3 us on the device).  The state is left in the caches for the next token.
 constexpr int kStepVec = 4;
 template <typename IO>
 __global__ void __launch_bounds__(256)

@@ -45,12 +45,12 @@ int launched() {
 }
 
 // Workgroups of the forward, at most.  A workgroup takes several rows, so that its weights are worth
-// keeping: two per CU for wide rows (16384x5120 bf16 with an fp32 residual: 165 us, 172 with four), four
-// for narrow ones, of which a workgroup requests fewer bytes at a time (32768x500: 39 us, 52 with two).
+// keeping: two per CU for wide rows (16384x5120 bf16 with an fp32 residual: 177 us, 185 with four), four
+// for narrow ones, of which a workgroup requests fewer bytes at a time (32768x500: 40 us, 60 with two).
 int64_t fwd_groups(int64_t D) { return D <= 2048 ? 1024 : 512; }
 
-// The widest rows that the forward holds in registers (of 1024 threads: 4096x12288 bf16 with fp32 sums, 92
-// us; passing over the row three times takes 300 without wide loads).
+// The widest rows that the forward holds in registers (of 1024 threads: 4096x12288 bf16 with fp32 sums, 106
+// us; passing over the row three times takes 142).
 constexpr int64_t kFwdDim = 16384;
 
 // Rows that a workgroup holds at a time (a wave each, up to 1024 values), by the row's width (0: wider
@@ -60,11 +60,12 @@ int64_t norm_slots(int64_t D) { return D <= 1024 ? 4 : D <= 8192 ? 1 : 0; }
 // Rows start on 128-byte lines (of tensors that do).
 bool whole_lines(int64_t D, int64_t es) { return D * es % 128 == 0; }
 
-// Workgroups of the backward, at most, and so partial sums of the parameters' gradients.  Two per CU, as
-// many as the registers of wider rows admit (16384x5120 bf16, fp32 sums: 215 us and 5 us for the sums with
-// 512; 254 with 256, 221 + 9 with 1024; 32768x768: 70 and 72 us), four for the narrowest rows, which
-// request few bytes at a time (32768x200: 31 us with 512, 21 + 2 with 1024), and for narrow ones that go
-// through the caches (32768x1500: 214 and 148 + 3; whole lines, 16384x2048: 88 and 95).
+// Workgroups of the backward, at most, and so partial sums of the parameters' gradients.  Two per CU
+// (16384x5120 bf16, fp32 sums: 225 us and 5 for the sums with 512; 264 + 5 with 256, 237 + 8 with 1024;
+// 32768x768: 71 + 5 and 74 + 6; a wave per SIMD is all that the registers of 2049 to 5120 fp32 values admit,
+// half of 512 workgroups at a time: 16384x5120 fp32, fp32 sums 257 + 5), four for the narrowest rows, which
+// request few bytes at a time (32768x200: 30 + 5 us with 512, 21 + 6 with 1024), and for narrow ones that go
+// through the caches (32768x1500: 213 + 5 and 152 + 7; whole lines, 16384x2048: 88 + 5 and 98 + 6).
 int64_t bwd_groups(int64_t D, int64_t es) {
     return D <= 256 || (D > 1024 && D <= 2048 && !whole_lines(D, es)) ? 1024 : 512;
 }

@@ -12,8 +12,8 @@
 // so do the sums over rows behind dw and db.  The next row is requested before the current one is
 // reduced.  Rows wider than the registers hold take the kernels at the end, which pass over a row
 // several times (its later passes come from the cache).  Measured (a copy of 1 GiB reaches 5.1 TB/s on
-// this card): 16384x5120 bf16 with an fp32 residual 176 us for 1,007 MB, its backward 226 us for
-// 1,342 MB; 4096x1536 fp32 backward 19 us for 76 MB; 256x5120 bf16 5.6 us for 16 MB, the latency of a
+// this card): 16384x5120 bf16 with an fp32 residual 177 us for 1,007 MB, its backward 225 us for
+// 1,342 MB; 4096x1536 fp32 backward 20 us for 76 MB; 256x5120 bf16 5.8 us for 16 MB, the latency of a
 // load, two sums over a workgroup and a store.
 #pragma once
 
@@ -73,8 +73,8 @@ __device__ __forceinline__ float row_sum(float p, float *red) {
 // beyond the element's own (rows of an odd width start anywhere).  The vector that crosses the
 // row's end is read by elements, columns past it are zero.  NT: past the caches, as data that is used
 // once; not where rows start inside a line, whose other part the neighbouring access wants (32768x771
-// bf16 with fp32 sums: 65 against 77 us, backward 84 against 102; at 768 columns the other way round,
-// 55 against 48 and 76 against 69 us).
+// bf16 with fp32 sums: 63 us through the caches, 65 past them, backward 86 and 103; at 768 columns 54 and 52,
+// 76 and 71).
 template <typename T, bool NT> struct norm_vec {
     static constexpr int W = kNormVec * (int)sizeof(T) / 4;
     typedef uint32_t any_u32 __attribute__((ext_vector_type(W), aligned(sizeof(T))));
@@ -327,7 +327,7 @@ layernorm_bwd_kernel(const IO *__restrict__ dy, const S *__restrict__ s, const f
 
 // out[d] = sum of the n rows of each part, in an order of their own: kNormSumGroups groups of threads
 // take every kNormSumGroups-th row of kNormSumCols columns, and their sums are added in order.  Bound:
-// the latency of a few dependent loads (512 parts of 1536 columns: 3.5 us).
+// the latency of a few dependent loads (512 parts of 1536 columns: 3.9 us).
 constexpr int kNormSumCols = 32, kNormSumGroups = 32;
 static __global__ void __launch_bounds__(kNormSumCols * kNormSumGroups)
 layernorm_wgrad_sum_kernel(const float *__restrict__ pw, const float *__restrict__ pb, float *__restrict__ dw,
@@ -356,7 +356,7 @@ layernorm_wgrad_sum_kernel(const float *__restrict__ pw, const float *__restrict
 }
 
 // ---- rows wider than the registers hold: one workgroup per row, several passes over it ----------
-// (2048x20000 bf16 with fp32 sums: 135 us for 492 MB; 4096x8200, the backward: 118 us for 537 MB and 44
+// (2048x20000 bf16 with fp32 sums: 138 us for 492 MB; 4096x8200, the backward: 119 us for 537 MB and 46
 // for the parameters' sums, which read dy and s once more.)
 
 constexpr int kNormWideThreads = 1024;
