@@ -50,7 +50,7 @@
 extern "C" {
 #endif
 
-#define SSMSCAN_VERSION 17
+#define SSMSCAN_VERSION 18
 
 /* Bits of the `flags` argument of the scan entry points. */
 #define SSM_SCAN_SOFTPLUS 1     /* step size = softplus(delta + delta_bias) */
@@ -555,6 +555,146 @@ SSMSCAN_API int ssm_layernorm_bwd(const void *dy, const void *s, const float *we
 
 /* Bytes of device workspace ssm_layernorm_bwd needs (0 for an invalid or empty problem). */
 SSMSCAN_API size_t ssm_layernorm_bwd_workspace_bytes(const ssm_dims *dims);
+
+/* Sizes of the state space dual layer with its convolution (ssm_ssd_conv_*). */
+typedef struct ssm_ssd_conv_dims {
+    int64_t batch;      /* sequences */
+    int64_t seqlen;     /* tokens per sequence (ignored by ssm_ssd_conv_step) */
+    int64_t nheads;     /* heads H */
+    int64_t headdim;    /* channels per head P: a multiple of 8 */
+    int64_t ngroups;    /* groups G of B and C; H % G == 0 */
+    int64_t dstate;     /* states N: a multiple of 8 up to 128 */
+    int64_t xbc_stride; /* elements between tokens of xbc (at least its row), or 0 = packed rows */
+    int64_t dt_stride;  /* elements between tokens of dt (at least H), or 0 = packed rows */
+    int32_t io_dtype;   /* an ssm_io_dtype */
+    int32_t width;      /* taps W of the convolution, 1 to 4 */
+} ssm_ssd_conv_dims;
+
+/* The state space dual layer from the block's projected row: the causal convolution of x, B and C over
+ * W tokens with SiLU, then the layer's recurrence.  A row of xbc holds R = H*P + 2*G*N values: x (the
+ * heads' channels), B, C (the groups' states).  Per token, and per head h with its group's B and C:
+ *   u_t  = silu(conv_b + sum_k conv_w[:, k] * xbc_{t - (W-1) + k}), rounded to fp32 and io_dtype (the rounding
+ *          of the exact value with bf16, whatever call forms it);  x_t, B_t, C_t are u_t's parts
+ *   dt_t = softplus(dt[t,h] + dt_bias[h])  (SSM_SCAN_SOFTPLUS), else dt + dt_bias
+ *   S_t  = exp(dt_t A[h]) S_{t-1} + dt_t x_t B_t^T        (P x N)
+ *   y_t  = S_t C_t + D[h] x_t
+ *   xbc            : [batch][seqlen] rows of R values, xbc_stride apart (sequences seqlen * xbc_stride
+ *                    apart): a part of a wider projected row as well (io_dtype)
+ *   dt             : [batch][seqlen] rows of H values, dt_stride apart (io_dtype)
+ *   conv_w, conv_b : [R][W], [R] fp32; conv_b may be NULL (= 0)
+ *   conv_state     : [batch][W-1][R] (io_dtype), the rows before token 0, oldest first, or NULL (= zeros)
+ *   A, D, dt_bias  : [H] fp32; D and dt_bias may be NULL.  A <= 0 and step sizes >= 0 are expected (not
+ *                    checked: exponentials of sums of A dt may overflow otherwise)
+ *   initial_state  : [batch][H][P][N] fp32, or NULL (= zero); it may be the last_state buffer
+ *   seq_lens       : [batch] int32 in device memory, or NULL: sequence b has seq_lens[b] tokens (values
+ *                    outside [0, seqlen] are taken as 0 or seqlen).  What xbc and dt hold past a length
+ *                    changes nothing; y is zero there
+ *   y              : [batch][seqlen][H][P] (io_dtype) output, written completely
+ *   last_state     : [batch][H][P][N] fp32 output, the state after each sequence's last token, or NULL
+ *   conv_state_out : [batch][W-1][R] (io_dtype) output, the last W-1 rows of (conv_state, xbc up to the
+ *                    sequence's length), or NULL; it may be the conv_state buffer
+ *   flags          : SSM_SCAN_SOFTPLUS, SSM_SCAN_CHECKPOINTS (a training forward: the workspace then holds
+ *                    what ssm_ssd_conv_bwd takes as checkpoints)
+ *   workspace      : at least ssm_ssd_conv_workspace_bytes(dims, flags) bytes, 16-byte aligned; its
+ *                    contents on entry do not matter
+ * y, the states and the rows of the convolution's state are 16-byte aligned.  Outputs must not overlap inputs
+ * or each other otherwise.  Products of bf16 u take u's values as they are; what is formed in between is carried
+ * to 16 bits where the result leaves in bf16 and to 24 where it is kept in fp32, sums and states are fp32; with fp32
+ * I/O all products are fp32.  Tokens are taken 64 at a time: a NaN or infinity in a token may reach the
+ * outputs of the 63 tokens before it, and no others before it.  nheads*headdim is at most 2^24.
+ * Returns SSM_OK or a negative ssm_status (nothing is launched on an error). */
+SSMSCAN_API int ssm_ssd_conv_fwd(const void *xbc, const float *conv_w, const float *conv_b, const void *conv_state,
+                const void *dt, const float *A, const float *D, const float *dt_bias, const float *initial_state,
+                const int32_t *seq_lens, int flags, void *y, float *last_state, void *conv_state_out,
+                const ssm_ssd_conv_dims *dims, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Bytes of device workspace ssm_ssd_conv_fwd needs with these flags (0 for an invalid or empty problem). */
+SSMSCAN_API size_t ssm_ssd_conv_workspace_bytes(const ssm_ssd_conv_dims *dims, int flags);
+
+/* Gradients of ssm_ssd_conv_fwd given dy = dLoss/dy and dlast_state = dLoss/d(last_state); conv_state_out is taken
+ * to carry none.
+ *   xbc .. seq_lens : exactly those of the forward call
+ *   flags           : SSM_SCAN_SOFTPLUS as the forward's; SSM_SCAN_CHECKPOINTS: `checkpoints` is the workspace that
+ *                     a forward call with that flag and the same inputs and dims left (contents not checked; of
+ *                     checkpoints_bytes bytes); without it u and the states are formed again
+ *   dy              : [batch][seqlen][H][P] (io_dtype); what it holds past a length changes nothing
+ *   dlast_state     : [batch][H][P][N] fp32, or NULL (= 0)
+ *   dxbc, ddt       : [batch][seqlen][R], [batch][seqlen][H] (io_dtype) outputs, packed; zero past a length
+ *   dconv_w         : [R][W] fp32 output;  dconv_b: [R], or NULL (not wanted)
+ *   dconv_state     : [batch][W-1][R] (io_dtype) output, or NULL (not wanted); also where conv_state is NULL
+ *   dA, dD, ddt_bias: [H] fp32 outputs; dD and ddt_bias may be NULL (not wanted)
+ *   dinitial_state  : [batch][H][P][N] fp32 output, or NULL (not wanted)
+ *   workspace       : at least ssm_ssd_conv_bwd_workspace_bytes(dims, flags) bytes, 16-byte aligned
+ * dy, dxbc, the states, the convolution's rows and the checkpoints are 16-byte aligned.  u's gradient stays fp32 on its
+ * way back through the convolution.  All sums have a fixed order: the results are the same from run to run.
+ * Outputs must not overlap inputs or each other.  Returns SSM_OK or a negative ssm_status. */
+SSMSCAN_API int ssm_ssd_conv_bwd(const void *xbc, const float *conv_w, const float *conv_b, const void *conv_state,
+                const void *dt, const float *A, const float *D, const float *dt_bias, const float *initial_state,
+                const int32_t *seq_lens, int flags, const void *dy, const float *dlast_state, const void *checkpoints,
+                size_t checkpoints_bytes, void *dxbc, float *dconv_w, float *dconv_b, void *dconv_state, void *ddt,
+                float *dA, float *dD, float *ddt_bias, float *dinitial_state, const ssm_ssd_conv_dims *dims,
+                void *workspace, size_t workspace_bytes, void *stream);
+
+/* Bytes of device workspace ssm_ssd_conv_bwd needs with these flags (0 for an invalid or empty problem). */
+SSMSCAN_API size_t ssm_ssd_conv_bwd_workspace_bytes(const ssm_ssd_conv_dims *dims, int flags);
+
+/* One token of the same layer for `batch` independent sequences.
+ *   state      : [batch][H][P][N] fp32, read and overwritten with the new state
+ *   conv_state : [batch][W-1][R] (io_dtype), the rows before this one, oldest first, advanced in place
+ *                (may be NULL with W = 1)
+ *   xbc        : [batch] rows of R values, xbc_stride apart;  dt: [batch] rows of H, dt_stride apart
+ *   y          : [batch][H][P] (io_dtype)
+ *   workspace  : at least ssm_ssd_conv_step_workspace_bytes(dims) bytes, 16-byte aligned
+ * Everything else as ssm_ssd_conv_fwd, whose u, decays and inputs it repeats: a sequence may go from the one to
+ * the other at any token. */
+SSMSCAN_API int ssm_ssd_conv_step(float *state, void *conv_state, const void *xbc, const float *conv_w,
+                const float *conv_b, const void *dt, const float *A, const float *D, const float *dt_bias, int flags,
+                void *y, const ssm_ssd_conv_dims *dims, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Bytes of device workspace ssm_ssd_conv_step needs (0 for an invalid or empty problem). */
+SSMSCAN_API size_t ssm_ssd_conv_step_workspace_bytes(const ssm_ssd_conv_dims *dims);
+
+/* Bits of the `flags` argument of the group norm's entry points. */
+#define SSM_GROUPNORM_RMS 1         /* the mean is not taken off */
+#define SSM_GROUPNORM_GATE_FIRST 2  /* x is gated by silu(z) before it is normalised, not the result after */
+#define SSM_GROUPNORM_SILU 4        /* without z: y is silu of the normalised values */
+
+/* Group norm over the channels of a row (channels last) with an activation: batch * seqlen rows of dim
+ * values in `groups` groups of dim / groups neighbours; per row and group
+ *   v = x * silu(z) (SSM_GROUPNORM_GATE_FIRST) or x
+ *   n = (v - mean(v)) * rstd, or v * rstd with SSM_GROUPNORM_RMS
+ *   rstd = 1 / sqrt(mean((v - mean(v))^2) + eps), or 1 / sqrt(mean(v^2) + eps)
+ *   o = n * weight + bias;   y = o, or o * silu(z) (z without SSM_GROUPNORM_GATE_FIRST), or silu(o)
+ *   (SSM_GROUPNORM_SILU, not together with z)
+ *   x, y         : rows (io_dtype)
+ *   z            : rows z_stride elements apart (0 = packed), a part of a wider row as well, or NULL
+ *   weight, bias : [dim] fp32; bias may be NULL (= 0)
+ *   mean, rstd   : [batch * seqlen][groups] fp32 outputs for the backward pass, each may be NULL (mean: of
+ *                  v with the mean taken off; zeros with SSM_GROUPNORM_RMS)
+ *   eps          : >= 0 and finite (SSM_ERR_VALUE otherwise)
+ * Sums and statistics are fp32 from centred values, as the layer norm's.  Outputs must not overlap inputs or
+ * each other.  dims->dstate and dims->chunk_len are ignored; at most 2^31 - 1 rows of at most 2^26 values.
+ * Returns SSM_OK or a negative ssm_status. */
+SSMSCAN_API int ssm_groupnorm_fwd(const void *x, const void *z, int64_t z_stride, const float *weight, const float *bias,
+                int64_t groups, float eps, int flags, void *y, float *mean, float *rstd, const ssm_dims *dims, void *stream);
+
+/* Gradients of ssm_groupnorm_fwd given dy = dLoss/dy.  With do = dLoss/do and dn = do * weight:
+ *   dv      = rstd * (dn - mean(dn) (not with SSM_GROUPNORM_RMS) - n * mean(dn * n))
+ *   dweight = sum over rows of do * n,   dbias = sum over rows of do
+ *   x, z, z_stride, weight, bias, groups, flags : the forward's;   mean, rstd : what it wrote (mean is not read,
+ *                 and may be NULL, with SSM_GROUPNORM_RMS)
+ *   dy, dx, dz  : packed rows (io_dtype); dz is required with z, and left alone without
+ *   dweight, dbias : [dim] fp32 outputs, each may be NULL (not wanted)
+ *   workspace   : at least ssm_groupnorm_bwd_workspace_bytes(dims, groups) bytes, 16-byte aligned; may be
+ *                 NULL when neither dweight nor dbias is wanted
+ * Outputs must not overlap inputs or each other.  The sums over rows have a fixed order: the results are the
+ * same from run to run.  Returns SSM_OK or a negative ssm_status. */
+SSMSCAN_API int ssm_groupnorm_bwd(const void *dy, const void *x, const void *z, int64_t z_stride, const float *weight,
+                const float *bias, const float *mean, const float *rstd, int64_t groups, int flags, void *dx, void *dz,
+                float *dweight, float *dbias, const ssm_dims *dims, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Bytes of device workspace ssm_groupnorm_bwd needs (0 for an invalid or empty problem). */
+SSMSCAN_API size_t ssm_groupnorm_bwd_workspace_bytes(const ssm_dims *dims, int64_t groups);
 
 /* Message describing the last non-OK status returned on this thread ("" if none). */
 SSMSCAN_API const char *ssm_last_error(void);

@@ -1,0 +1,368 @@
+// The state space dual layer with its convolution (include/ssmscan.h): validation and launches.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+
+#include "host_util.h"
+#include "ssd_conv_bwd_kernel.h"
+#include "ssd_conv_kernel.h"
+
+namespace {
+
+using namespace ssmlib;
+
+constexpr int64_t kMaxTokens = int64_t(1) << 30;
+constexpr int64_t kMaxElems = int64_t(1) << 46;
+constexpr int64_t kMaxGrid = (int64_t(1) << 31) - 1;
+
+int64_t row_of(const ssm_ssd_conv_dims *dm) { return dm->nheads * dm->headdim + 2 * dm->ngroups * dm->dstate; }
+size_t elem_size(const ssm_ssd_conv_dims *dm) { return dm->io_dtype == SSM_IO_BF16 ? 2 : 4; }
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+int64_t p_tiles(const ssm_ssd_conv_dims *dm) { return ceil_div(dm->headdim, 64); }
+int64_t chunks(const ssm_ssd_conv_dims *dm) { return ceil_div(dm->seqlen, ssm::kSdQ); }
+
+int check_dims(const ssm_ssd_conv_dims *dm) {
+    if (!dm) return fail(SSM_ERR_NULL, "dims is NULL");
+    if (dm->batch < 0 || dm->seqlen < 0 || dm->nheads < 0)
+        return fail(SSM_ERR_SHAPE, "negative size (batch=%lld seqlen=%lld nheads=%lld)", (long long)dm->batch,
+                    (long long)dm->seqlen, (long long)dm->nheads);
+    if (dm->io_dtype != SSM_IO_F32 && dm->io_dtype != SSM_IO_BF16)
+        return fail(SSM_ERR_DTYPE, "io_dtype %d is not SSM_IO_F32 (0) or SSM_IO_BF16 (1)", dm->io_dtype);
+    if (dm->headdim < 8 || dm->headdim % 8 || dm->headdim > 65536)
+        return fail(SSM_ERR_SHAPE, "headdim %lld is not a multiple of 8 from 8 to 65536", (long long)dm->headdim);
+    if (dm->dstate < 8 || dm->dstate % 8 || dm->dstate > 128)
+        return fail(SSM_ERR_SHAPE, "dstate %lld is not a multiple of 8 from 8 to 128", (long long)dm->dstate);
+    if (dm->ngroups < 1 || dm->nheads % dm->ngroups)
+        return fail(SSM_ERR_SHAPE, "nheads %lld is not a multiple of ngroups %lld", (long long)dm->nheads, (long long)dm->ngroups);
+    if (dm->width < 1 || dm->width > ssm::kSdTaps)
+        return fail(SSM_ERR_SHAPE, "convolution width %d is not 1 to %d", dm->width, ssm::kSdTaps);
+    if (dm->nheads > (int64_t(1) << 24) / dm->headdim || dm->ngroups > (int64_t(1) << 23) / dm->dstate)
+        return fail(SSM_ERR_SHAPE, "nheads*headdim or 2*ngroups*dstate exceeds 2^24");
+    if (dm->seqlen > kMaxTokens || dm->batch > kMaxTokens)
+        return fail(SSM_ERR_SHAPE, "seqlen or batch exceeds 2^30");
+    const int64_t row = row_of(dm);
+    if (dm->nheads > 0 && dm->batch > 0 &&
+        (dm->batch > kMaxElems / row / std::max<int64_t>(dm->seqlen, 1) ||
+         dm->batch > kMaxElems / (dm->nheads * dm->headdim * dm->dstate) / std::max<int64_t>(chunks(dm), 1)))
+        return fail(SSM_ERR_SHAPE, "the rows or the states exceed 2^46 elements");
+    if (dm->batch > 0 && dm->nheads * p_tiles(dm) > kMaxGrid / dm->batch)
+        return fail(SSM_ERR_SHAPE, "batch*nheads*ceil(headdim/64) exceeds 2^31 - 1 (grid size)");
+    if (dm->xbc_stride < 0 || dm->dt_stride < 0 || (dm->xbc_stride && dm->xbc_stride < row) ||
+        (dm->dt_stride && dm->dt_stride < dm->nheads) || dm->xbc_stride > kMaxTokens || dm->dt_stride > kMaxTokens)
+        return fail(SSM_ERR_SHAPE, "a stride between tokens is smaller than the row or larger than 2^30");
+    return SSM_OK;
+}
+
+int launched() {
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return fail(SSM_ERR_HIP, "kernel launch failed: %s", hipGetErrorString(e));
+    return ok();
+}
+
+ssm::sd_shape shape_of(const ssm_ssd_conv_dims *dm, int flags) {
+    ssm::sd_shape s;
+    s.L = dm->seqlen;
+    s.H = (int)dm->nheads;
+    s.P = (int)dm->headdim;
+    s.G = (int)dm->ngroups;
+    s.N = (int)dm->dstate;
+    s.PT = (int)p_tiles(dm);
+    s.dc = (int)row_of(dm);
+    s.dt_stride = dm->dt_stride ? dm->dt_stride : dm->nheads;
+    s.softplus = flags & SSM_SCAN_SOFTPLUS;
+    s.nchunk = chunks(dm);
+    return s;
+}
+
+// The workspace of the forward: u, and in training the states entering the chunks.
+size_t u_bytes(const ssm_ssd_conv_dims *dm) { return align256((size_t)(dm->batch * dm->seqlen * row_of(dm)) * elem_size(dm)); }
+size_t state_bytes(const ssm_ssd_conv_dims *dm) {
+    return align256((size_t)(dm->batch * chunks(dm) * dm->nheads * dm->headdim * dm->dstate) * sizeof(float));
+}
+
+bool conv_grid(const ssm_ssd_conv_dims *dm, int tt, int64_t &vblocks, int64_t &tiles) {
+    vblocks = ceil_div(row_of(dm) / ssm::kSdConvV, 256);
+    tiles = std::max<int64_t>(ceil_div(dm->seqlen, tt), 1);
+    return dm->batch <= kMaxGrid / vblocks / tiles;
+}
+
+template <typename IO>
+void launch_conv(const void *x_, const float *w, const float *bias, const void *st_in, void *st_out, const int32_t *lens,
+                 void *u, const ssm_ssd_conv_dims *dm, int tt, hipStream_t st) {
+    const int64_t stride = dm->xbc_stride ? dm->xbc_stride : row_of(dm);
+    int64_t vblocks, tiles;
+    conv_grid(dm, tt, vblocks, tiles);
+    const bool al = aligned(x_, ssm::kSdConvV * sizeof(IO)) && stride % ssm::kSdConvV == 0;
+    auto kern = al ? ssm::sd_conv_kernel<IO, true> : ssm::sd_conv_kernel<IO, false>;
+    hipLaunchKernelGGL(kern, dim3((unsigned)(vblocks * tiles * dm->batch)), dim3(256), 0, st, static_cast<const IO *>(x_),
+                       stride, w, bias, (int)dm->width, static_cast<const IO *>(st_in), static_cast<IO *>(st_out), lens,
+                       static_cast<IO *>(u), dm->seqlen, (int)row_of(dm), tt, (int)vblocks, (int)tiles);
+}
+
+constexpr int kConvTokens = 32;   // tokens per thread of the convolution
+
+template <typename E, int NT>
+void launch_scan(const void *u, const void *dt, const float *A, const float *D, const float *dt_bias, const int32_t *lens,
+                 const float *h0, void *y, float *last, float *ckpt, const ssm_ssd_conv_dims *dm, int flags, hipStream_t st) {
+    using IO = typename ssm::sd<E>::io;
+    const ssm::sd_shape s = shape_of(dm, flags);
+    hipLaunchKernelGGL((ssm::sd_scan_kernel<E, NT>), dim3((unsigned)(dm->batch * s.H * s.PT)), dim3(ssm::kSdThreads), 0, st,
+                       static_cast<const IO *>(u), static_cast<const IO *>(dt), A, D, dt_bias, lens, h0,
+                       static_cast<IO *>(y), last, ckpt, s);
+}
+
+template <typename IO>
+void launch_step(float *state, const void *u, const void *dt, const float *A, const float *D, const float *dt_bias, void *y,
+                 const ssm_ssd_conv_dims *dm, int flags, hipStream_t st) {
+    const ssm::sd_shape s = shape_of(dm, flags);
+    const int lanes = s.N / 4;
+    auto kern = lanes <= 2 ? ssm::sd_step_kernel<IO, 2> : lanes <= 4 ? ssm::sd_step_kernel<IO, 4>
+              : lanes <= 8 ? ssm::sd_step_kernel<IO, 8> : lanes <= 16 ? ssm::sd_step_kernel<IO, 16> : ssm::sd_step_kernel<IO, 32>;
+    hipLaunchKernelGGL(kern, dim3((unsigned)(dm->batch * s.H)), dim3(256), 0, st, state, static_cast<const IO *>(u),
+                       static_cast<const IO *>(dt), s.dt_stride, A, D, dt_bias, s.softplus, static_cast<IO *>(y), s.H, s.P,
+                       s.G, s.N);
+}
+
+// How the backward cuts its work, and its workspace.
+constexpr int kConvBwdTokens = 64;   // tokens per thread of the convolution's backward
+struct BwdPlan {
+    int HS, hpw;
+    int64_t tiles;
+    size_t u, states, adjoints, du, dbc, part, conv_part, bytes;   // offsets (u, states: without checkpoints)
+};
+BwdPlan bwd_plan(const ssm_ssd_conv_dims *dm, bool have_checkpoints) {
+    BwdPlan p;
+    const int64_t per = dm->nheads / dm->ngroups, items = std::max<int64_t>(dm->batch * chunks(dm) * dm->ngroups, 1);
+    // parts of a group's heads: as many as give 2048 workgroups
+    const int64_t parts = std::min(per, std::max<int64_t>(ceil_div(2048, items), 1));
+    p.hpw = (int)ceil_div(per, parts);
+    p.HS = (int)ceil_div(per, p.hpw);
+    p.tiles = std::max<int64_t>(ceil_div(dm->seqlen, kConvBwdTokens), 1);
+    size_t at = 0;
+    auto take = [&](size_t bytes) {
+        const size_t o = at;
+        at += align256(bytes);
+        return o;
+    };
+    const size_t tokens = (size_t)(dm->batch * dm->seqlen);
+    p.u = take(have_checkpoints ? 0 : u_bytes(dm));
+    p.states = take(have_checkpoints ? 0 : state_bytes(dm));
+    p.adjoints = take(state_bytes(dm));
+    p.du = take(tokens * dm->nheads * dm->headdim * 4);
+    p.dbc = take(tokens * p.HS * 2 * dm->ngroups * dm->dstate * 4);
+    p.part = take((size_t)(dm->batch * chunks(dm) * 3 * dm->nheads) * 4);
+    p.conv_part = take((size_t)(dm->batch * p.tiles * 5 * row_of(dm)) * 4);
+    p.bytes = at;
+    return p;
+}
+
+template <typename E, int NT, bool ADJ>
+void launch_walk(const void *u, const void *dy, const void *dt, const float *A, const float *dt_bias, const int32_t *lens,
+                 const float *from, float *each, float *to, const ssm_ssd_conv_dims *dm, int flags, hipStream_t st) {
+    using IO = typename ssm::sd<E>::io;
+    const ssm::sd_shape s = shape_of(dm, flags);
+    hipLaunchKernelGGL((ssm::sd_walk_kernel<E, NT, ADJ>), dim3((unsigned)(dm->batch * s.H * s.PT)), dim3(ssm::kSdThreads), 0, st,
+                       static_cast<const IO *>(u), static_cast<const IO *>(dy), static_cast<const IO *>(dt), A, dt_bias, lens,
+                       from, each, to, s);
+}
+
+template <typename E, int NT>
+void launch_bwd(const void *u, const void *dy, const void *dt, const float *A, const float *D, const float *dt_bias,
+                const int32_t *lens, const float *states, const float *adjoints, void *ddt, const ssm::sd_grad &g,
+                const ssm_ssd_conv_dims *dm, int flags, hipStream_t st) {
+    using IO = typename ssm::sd<E>::io;
+    const ssm::sd_shape s = shape_of(dm, flags);
+    hipLaunchKernelGGL((ssm::sd_bwd_kernel<E, NT>), dim3((unsigned)(dm->batch * s.nchunk * s.G * g.HS)), dim3(ssm::kSdThreads), 0, st,
+                       static_cast<const IO *>(u), static_cast<const IO *>(dy), static_cast<const IO *>(dt), A, D, dt_bias, lens,
+                       states, adjoints, static_cast<IO *>(ddt), g, s);
+}
+
+template <typename IO>
+void launch_conv_bwd(const void *x_, const float *w, const float *bias, const void *st_in, const int32_t *lens, const float *du,
+                     const float *dbc, int HS, void *dx, void *dst, float *parts, const ssm_ssd_conv_dims *dm, hipStream_t st) {
+    const int64_t stride = dm->xbc_stride ? dm->xbc_stride : row_of(dm);
+    int64_t vblocks, tiles;
+    conv_grid(dm, kConvBwdTokens, vblocks, tiles);
+    const bool al = aligned(x_, ssm::kSdConvV * sizeof(IO)) && stride % ssm::kSdConvV == 0;
+    auto kern = al ? ssm::sd_conv_bwd_kernel<IO, true> : ssm::sd_conv_bwd_kernel<IO, false>;
+    hipLaunchKernelGGL(kern, dim3((unsigned)(vblocks * tiles * dm->batch)), dim3(256), 0, st, static_cast<const IO *>(x_), stride,
+                       w, bias, (int)dm->width, static_cast<const IO *>(st_in), lens, du, dbc, HS, static_cast<IO *>(dx),
+                       static_cast<IO *>(dst), parts, dm->batch, dm->seqlen, (int)row_of(dm), (int)(dm->nheads * dm->headdim),
+                       kConvBwdTokens, (int)vblocks, (int)tiles);
+}
+
+void launch_sums(const float *part, int64_t n, int cols, int planes, const ssm::sd_sums &o, hipStream_t st) {
+    const int blocks = (cols + ssm::kSdSumCols - 1) / ssm::kSdSumCols * planes;
+    hipLaunchKernelGGL(ssm::sd_sum_kernel, dim3((unsigned)blocks), dim3(ssm::kSdSumCols * ssm::kSdSumGroups), 0, st, part, n, cols,
+                       planes, o);
+}
+
+int check_workspace(const void *ws, size_t have, size_t need) {
+    if (need > 0 && !ws) return fail(SSM_ERR_WORKSPACE, "workspace is NULL (%zu bytes needed)", need);
+    if (have < need) return fail(SSM_ERR_WORKSPACE, "workspace of %zu bytes is smaller than the %zu needed", have, need);
+    if (need > 0 && !aligned(ws, 16)) return fail(SSM_ERR_ALIGN, "workspace not 16-byte aligned");
+    return SSM_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t ssm_ssd_conv_workspace_bytes(const ssm_ssd_conv_dims *dims, int flags) {
+    if (check_dims(dims) != SSM_OK || dims->batch == 0 || dims->nheads == 0) return 0;
+    return u_bytes(dims) + ((flags & SSM_SCAN_CHECKPOINTS) ? state_bytes(dims) : 0);
+}
+
+int ssm_ssd_conv_fwd(const void *xbc, const float *conv_w, const float *conv_b, const void *conv_state, const void *dt,
+                     const float *A, const float *D, const float *dt_bias, const float *initial_state,
+                     const int32_t *seq_lens, int flags, void *y, float *last_state, void *conv_state_out,
+                     const ssm_ssd_conv_dims *dims, void *workspace, size_t workspace_bytes, void *stream) {
+    int rc = check_dims(dims);
+    if (rc != SSM_OK) return rc;
+    if (flags & ~(SSM_SCAN_SOFTPLUS | SSM_SCAN_CHECKPOINTS)) return fail(SSM_ERR_FLAGS, "unknown flag bits 0x%x", flags);
+    const size_t es = elem_size(dims);
+    if (!aligned(xbc, es) || !aligned(dt, es) || !aligned(conv_w, 4) || !aligned(conv_b, 4) || !aligned(A, 4) || !aligned(D, 4) ||
+        !aligned(dt_bias, 4) || !aligned(seq_lens, 4))
+        return fail(SSM_ERR_ALIGN, "a tensor pointer is not aligned to its element size");
+    if (!aligned(y, 16) || !aligned(initial_state, 16) || !aligned(last_state, 16) || !aligned(conv_state, 16) ||
+        !aligned(conv_state_out, 16))
+        return fail(SSM_ERR_ALIGN, "y, the states or the convolution's rows are not 16-byte aligned");
+    if (dims->batch == 0 || dims->nheads == 0) return ok();
+    if (!conv_w || !A) return fail(SSM_ERR_NULL, "conv_w or A is NULL");
+    if (dims->seqlen > 0 && (!xbc || !dt || !y)) return fail(SSM_ERR_NULL, "xbc, dt or y is NULL");
+    rc = check_workspace(workspace, workspace_bytes, ssm_ssd_conv_workspace_bytes(dims, flags));
+    if (rc != SSM_OK) return rc;
+    int64_t vblocks, tiles;
+    if (!conv_grid(dims, kConvTokens, vblocks, tiles)) return fail(SSM_ERR_SHAPE, "batch*seqlen exceeds the grid of the convolution");
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    float *ckpt = (flags & SSM_SCAN_CHECKPOINTS) ? reinterpret_cast<float *>(static_cast<char *>(workspace) + u_bytes(dims)) : nullptr;
+    if (es == 2) {
+        launch_conv<uint16_t>(xbc, conv_w, conv_b, conv_state, conv_state_out, seq_lens, workspace, dims, kConvTokens, st);
+        auto f = dims->dstate <= 64 ? launch_scan<__bf16, 64> : launch_scan<__bf16, 128>;
+        f(workspace, dt, A, D, dt_bias, seq_lens, initial_state, y, last_state, ckpt, dims, flags, st);
+    } else {
+        launch_conv<float>(xbc, conv_w, conv_b, conv_state, conv_state_out, seq_lens, workspace, dims, kConvTokens, st);
+        auto f = dims->dstate <= 64 ? launch_scan<float, 64> : launch_scan<float, 128>;
+        f(workspace, dt, A, D, dt_bias, seq_lens, initial_state, y, last_state, ckpt, dims, flags, st);
+    }
+    return launched();
+}
+
+size_t ssm_ssd_conv_bwd_workspace_bytes(const ssm_ssd_conv_dims *dims, int flags) {
+    if (check_dims(dims) != SSM_OK || dims->batch == 0 || dims->nheads == 0) return 0;
+    return bwd_plan(dims, flags & SSM_SCAN_CHECKPOINTS).bytes;
+}
+
+int ssm_ssd_conv_bwd(const void *xbc, const float *conv_w, const float *conv_b, const void *conv_state, const void *dt,
+                     const float *A, const float *D, const float *dt_bias, const float *initial_state,
+                     const int32_t *seq_lens, int flags, const void *dy, const float *dlast_state, const void *checkpoints,
+                     size_t checkpoints_bytes, void *dxbc, float *dconv_w, float *dconv_b, void *dconv_state, void *ddt,
+                     float *dA, float *dD, float *ddt_bias, float *dinitial_state, const ssm_ssd_conv_dims *dims,
+                     void *workspace, size_t workspace_bytes, void *stream) {
+    int rc = check_dims(dims);
+    if (rc != SSM_OK) return rc;
+    if (flags & ~(SSM_SCAN_SOFTPLUS | SSM_SCAN_CHECKPOINTS)) return fail(SSM_ERR_FLAGS, "unknown flag bits 0x%x", flags);
+    const size_t es = elem_size(dims);
+    if (!aligned(xbc, es) || !aligned(dt, es) || !aligned(ddt, es) || !aligned(conv_w, 4) || !aligned(conv_b, 4) || !aligned(A, 4) ||
+        !aligned(D, 4) || !aligned(dt_bias, 4) || !aligned(seq_lens, 4) || !aligned(dconv_w, 4) || !aligned(dconv_b, 4) ||
+        !aligned(dA, 4) || !aligned(dD, 4) || !aligned(ddt_bias, 4))
+        return fail(SSM_ERR_ALIGN, "a tensor pointer is not aligned to its element size");
+    if (!aligned(dy, 16) || !aligned(dxbc, 16) || !aligned(initial_state, 16) || !aligned(dlast_state, 16) ||
+        !aligned(dinitial_state, 16) || !aligned(conv_state, 16) || !aligned(dconv_state, 16) || !aligned(checkpoints, 16))
+        return fail(SSM_ERR_ALIGN, "dy, dxbc, the states, the convolution's rows or the checkpoints are not 16-byte aligned");
+    if (dims->nheads == 0) return ok();
+    if (!conv_w || !A || !dconv_w || !dA) return fail(SSM_ERR_NULL, "conv_w, A, dconv_w or dA is NULL");
+    if (dims->batch > 0 && dims->seqlen > 0 && (!xbc || !dt || !dy || !dxbc || !ddt))
+        return fail(SSM_ERR_NULL, "xbc, dt, dy, dxbc or ddt is NULL");
+    const bool kept = flags & SSM_SCAN_CHECKPOINTS;
+    if (kept) {
+        const size_t need = ssm_ssd_conv_workspace_bytes(dims, SSM_SCAN_CHECKPOINTS);
+        if (need > 0 && !checkpoints) return fail(SSM_ERR_NULL, "checkpoints is NULL with SSM_SCAN_CHECKPOINTS");
+        if (checkpoints_bytes < need)
+            return fail(SSM_ERR_WORKSPACE, "checkpoints of %zu bytes are smaller than the %zu of the forward", checkpoints_bytes, need);
+    }
+    rc = check_workspace(workspace, workspace_bytes, ssm_ssd_conv_bwd_workspace_bytes(dims, flags));
+    if (rc != SSM_OK) return rc;
+    const BwdPlan p = bwd_plan(dims, kept);
+    int64_t vblocks, tiles;
+    if (!conv_grid(dims, kConvTokens, vblocks, tiles) || dims->batch * chunks(dims) > kMaxGrid / dims->ngroups / p.HS)
+        return fail(SSM_ERR_SHAPE, "batch*seqlen exceeds the grids of the backward");
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    char *ws = static_cast<char *>(workspace);
+    auto at = [&](size_t o) { return reinterpret_cast<float *>(ws + o); };
+    const char *ck = static_cast<const char *>(checkpoints);
+    const void *u = kept ? ck : ws + p.u;
+    const float *states = kept ? reinterpret_cast<const float *>(ck + u_bytes(dims)) : at(p.states);
+    const bool bf = es == 2, wide = dims->dstate > 64;
+    if (dims->batch > 0) {
+        if (!kept) {
+            if (bf) launch_conv<uint16_t>(xbc, conv_w, conv_b, conv_state, nullptr, seq_lens, ws + p.u, dims, kConvTokens, st);
+            else launch_conv<float>(xbc, conv_w, conv_b, conv_state, nullptr, seq_lens, ws + p.u, dims, kConvTokens, st);
+            auto f = bf ? wide ? launch_walk<__bf16, 128, false> : launch_walk<__bf16, 64, false>
+                        : wide ? launch_walk<float, 128, false> : launch_walk<float, 64, false>;
+            f(u, nullptr, dt, A, dt_bias, seq_lens, initial_state, at(p.states), nullptr, dims, flags, st);
+        }
+        auto f = bf ? wide ? launch_walk<__bf16, 128, true> : launch_walk<__bf16, 64, true>
+                    : wide ? launch_walk<float, 128, true> : launch_walk<float, 64, true>;
+        f(u, dy, dt, A, dt_bias, seq_lens, dlast_state, at(p.adjoints), dinitial_state, dims, flags, st);
+        if (dims->seqlen > 0) {
+            const ssm::sd_grad g = {at(p.du), at(p.dbc), at(p.part), p.HS, p.hpw};
+            auto k = bf ? wide ? launch_bwd<__bf16, 128> : launch_bwd<__bf16, 64> : wide ? launch_bwd<float, 128> : launch_bwd<float, 64>;
+            k(u, dy, dt, A, D, dt_bias, seq_lens, states, at(p.adjoints), ddt, g, dims, flags, st);
+        }
+        auto c = bf ? launch_conv_bwd<uint16_t> : launch_conv_bwd<float>;
+        c(xbc, conv_w, conv_b, conv_state, seq_lens, at(p.du), at(p.dbc), p.HS, dxbc, dconv_state, at(p.conv_part), dims, st);
+    }
+    const int W = dims->width, H = (int)dims->nheads;
+    ssm::sd_sums o = {};
+    for (int j = 0; j < ssm::kSdTaps; ++j) {
+        const int tap = j - (ssm::kSdTaps - W);
+        o.out[j] = tap >= 0 ? dconv_w + tap : nullptr;
+        o.stride[j] = W;
+    }
+    o.out[4] = dconv_b;
+    o.stride[4] = 1;
+    launch_sums(at(p.conv_part), dims->batch * p.tiles, (int)row_of(dims), 5, o, st);
+    const ssm::sd_sums h = {{dA, ddt_bias, dD}, {1, 1, 1}};
+    launch_sums(at(p.part), dims->batch * chunks(dims), H, 3, h, st);
+    return launched();
+}
+
+size_t ssm_ssd_conv_step_workspace_bytes(const ssm_ssd_conv_dims *dims) {
+    if (check_dims(dims) != SSM_OK) return 0;
+    return align256((size_t)(dims->batch * row_of(dims)) * elem_size(dims));
+}
+
+int ssm_ssd_conv_step(float *state, void *conv_state, const void *xbc, const float *conv_w, const float *conv_b,
+                      const void *dt, const float *A, const float *D, const float *dt_bias, int flags, void *y,
+                      const ssm_ssd_conv_dims *dims, void *workspace, size_t workspace_bytes, void *stream) {
+    int rc = check_dims(dims);
+    if (rc != SSM_OK) return rc;
+    if (flags & ~SSM_SCAN_SOFTPLUS) return fail(SSM_ERR_FLAGS, "unknown flag bits 0x%x", flags);
+    const size_t es = elem_size(dims);
+    if (!aligned(xbc, es) || !aligned(dt, es) || !aligned(y, es) || !aligned(conv_w, 4) || !aligned(conv_b, 4) || !aligned(A, 4) ||
+        !aligned(D, 4) || !aligned(dt_bias, 4))
+        return fail(SSM_ERR_ALIGN, "a tensor pointer is not aligned to its element size");
+    if (!aligned(state, 16) || !aligned(conv_state, 16))
+        return fail(SSM_ERR_ALIGN, "the state or the convolution's rows are not 16-byte aligned");
+    if (dims->batch == 0 || dims->nheads == 0) return ok();
+    if (!state || !xbc || !conv_w || !dt || !A || !y || (dims->width > 1 && !conv_state))
+        return fail(SSM_ERR_NULL, "required pointer is NULL");
+    rc = check_workspace(workspace, workspace_bytes, ssm_ssd_conv_step_workspace_bytes(dims));
+    if (rc != SSM_OK) return rc;
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    ssm_ssd_conv_dims one = *dims;
+    one.seqlen = 1;
+    int64_t vblocks, tiles;
+    if (!conv_grid(&one, kConvTokens, vblocks, tiles)) return fail(SSM_ERR_SHAPE, "batch exceeds the grid of the convolution");
+    if (es == 2) {
+        launch_conv<uint16_t>(xbc, conv_w, conv_b, conv_state, conv_state, nullptr, workspace, &one, kConvTokens, st);
+        launch_step<uint16_t>(state, workspace, dt, A, D, dt_bias, y, &one, flags, st);
+    } else {
+        launch_conv<float>(xbc, conv_w, conv_b, conv_state, conv_state, nullptr, workspace, &one, kConvTokens, st);
+        launch_step<float>(state, workspace, dt, A, D, dt_bias, y, &one, flags, st);
+    }
+    return launched();
+}
+
+}  // extern "C"

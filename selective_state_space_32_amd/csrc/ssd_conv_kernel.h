@@ -1,0 +1,549 @@
+// The state space dual layer with its short convolution: prompts, single tokens, gradients.
+//
+// Per head h (P channels, its group's B and C of N states), with u = silu(conv) rounded to the I/O
+// type, dt = softplus(raw + bias) and g = A dt the logarithm of a token's decay:
+//   S_t = e^{g_t} S_{t-1} + dt_t x_t B_t^T,   y_t = S_t C_t + D x_t
+// Over a chunk of 64 tokens, with c_t = g_0 + .. + g_t, K[t,s] = e^{c_t - c_s} for s <= t, and S the
+// state entering the chunk:
+//   G = C B^T,  M[t,s] = G[t,s] K[t,s] dt_s,   Y = M X + e^{c_t} C S^T + D X
+//   S <- e^{c_last} S + sum_s (e^{c_last - c_s} dt_s x_s) B_s^T
+#pragma once
+
+#include <type_traits>
+
+#include "device_math.h"
+
+namespace ssm {
+
+constexpr int kSdQ = 64;           // tokens per chunk
+constexpr int kSdThreads = 256;    // four waves; wave w owns the 16 channels 16 w .. of a 64-channel tile
+constexpr int kSdTaps = 4;         // taps of the convolution at most
+constexpr int kSdConvV = 4;        // channels per thread of the convolution's kernels
+
+// ---- operands of the matrix products --------------------------------------------------------
+//
+// An operand comes in fragments of 16 values of the contraction index k: lane l holds, for its row
+// (A) or column (B) l % 16, the four consecutive k at 4 (l / 16).  That is also the layout of an
+// accumulator (rows 4 (l / 16) + e, column l % 16), so an accumulator is a fragment of the product
+// that contracts over its rows without leaving its registers.  bf16: two fragments make one operand of
+// v_mfma_f32_16x16x32_bf16 (both operands order k alike); fp32: a fragment feeds four
+// v_mfma_f32_16x16x4_f32.  Operands that are formed in fp32 are split into NS bf16 parts of 8 bits each:
+// two where the result leaves in bf16 (2^-17 of a value is lost), three where it is carried in fp32.
+typedef __bf16 sd_bf16x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 sd_bf16x8 __attribute__((ext_vector_type(8)));
+typedef short sd_i16x4 __attribute__((ext_vector_type(4)));
+
+template <typename E> struct sd;
+template <> struct sd<__bf16> {
+    using io = uint16_t;
+    using frag = sd_bf16x4;
+    static constexpr int pad = 8;
+    static constexpr bool split = true;
+};
+template <> struct sd<float> {
+    using io = float;
+    using frag = f32x4_t;
+    static constexpr int pad = 4;
+    static constexpr bool split = false;
+};
+// Row stride of a tile of W columns in LDS: rows start 16 bytes apart modulo the banks.
+template <typename E> constexpr int sd_ld(int w) { return w + sd<E>::pad; }
+
+// k contiguous in the tile: four values of row r0 + l % 16 from column k0 + 4 (l / 16)
+template <typename E, int W>
+__device__ __forceinline__ typename sd<E>::frag ld_row(const E *t, int r0, int k0, int lane) {
+    return *reinterpret_cast<const typename sd<E>::frag *>(t + (r0 + (lane & 15)) * sd_ld<E>(W) + k0 + 4 * (lane >> 4));
+}
+// k along the tile's rows: column m0 + l % 16 of rows k0 + 4 (l / 16) .. + 3.  (bf16: the transposing LDS
+// read returns to lane j of a group of 16 the four rows' element j % 16 of the 4 x 16 block that the
+// group addresses, lane i row i / 4, columns 4 (i % 4).)
+template <typename E, int W>
+__device__ __forceinline__ typename sd<E>::frag ld_col(const E *t, int k0, int m0, int lane) {
+    if constexpr (sd<E>::split) {
+        const int i = lane & 15;
+        typedef __attribute__((address_space(3))) sd_i16x4 lds_i16x4;
+        const __bf16 *p = t + (k0 + 4 * (lane >> 4) + (i >> 2)) * sd_ld<E>(W) + m0 + 4 * (i & 3);
+        return __builtin_bit_cast(sd_bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4 *)p));
+    } else {
+        const float *p = t + (k0 + 4 * (lane >> 4)) * sd_ld<E>(W) + m0 + (lane & 15);
+        return f32x4_t{p[0], p[sd_ld<E>(W)], p[2 * sd_ld<E>(W)], p[3 * sd_ld<E>(W)]};
+    }
+}
+__device__ __forceinline__ f32x4_t mma(sd_bf16x4 a0, sd_bf16x4 a1, sd_bf16x4 b0, sd_bf16x4 b1, f32x4_t c) {
+    const sd_bf16x8 a = __builtin_shufflevector(a0, a1, 0, 1, 2, 3, 4, 5, 6, 7);
+    const sd_bf16x8 b = __builtin_shufflevector(b0, b1, 0, 1, 2, 3, 4, 5, 6, 7);
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ f32x4_t mma(f32x4_t a0, f32x4_t a1, f32x4_t b0, f32x4_t b1, f32x4_t c) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a0[e], b0[e], c, 0, 0, 0);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a1[e], b1[e], c, 0, 0, 0);
+    return c;
+}
+// A fragment formed in fp32, in NS parts (one with fp32 operands).
+template <typename E, int NS> struct formed {
+    static constexpr int N = sd<E>::split ? NS : 1;
+    typename sd<E>::frag p[N];
+    __device__ __forceinline__ formed() {}
+    __device__ __forceinline__ explicit formed(f32x4_t v) {
+        if constexpr (sd<E>::split) {
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const __bf16 h = (__bf16)v[e];
+                    p[i][e] = h;
+                    if (i + 1 < N) v[e] -= (float)h;
+                }
+        } else {
+            p[0] = v;
+        }
+    }
+};
+template <typename E, int NS>
+__device__ __forceinline__ f32x4_t mma_fa(const formed<E, NS> &a0, const formed<E, NS> &a1, typename sd<E>::frag b0,
+                                          typename sd<E>::frag b1, f32x4_t c) {
+#pragma unroll
+    for (int i = 0; i < formed<E, NS>::N; ++i) c = mma(a0.p[i], a1.p[i], b0, b1, c);
+    return c;
+}
+template <typename E, int NS>
+__device__ __forceinline__ f32x4_t mma_fb(typename sd<E>::frag a0, typename sd<E>::frag a1, const formed<E, NS> &b0,
+                                          const formed<E, NS> &b1, f32x4_t c) {
+#pragma unroll
+    for (int i = 0; i < formed<E, NS>::N; ++i) c = mma(a0, a1, b0.p[i], b1.p[i], c);
+    return c;
+}
+__device__ __forceinline__ f32x4_t widen(sd_bf16x4 v) { return f32x4_t{(float)v[0], (float)v[1], (float)v[2], (float)v[3]}; }
+__device__ __forceinline__ f32x4_t widen(f32x4_t v) { return v; }
+
+// ---- tiles ----------------------------------------------------------------------------------
+
+// 64 rows (tokens) of W elements between memory and LDS, 16 bytes per thread and access.
+template <typename E, int W> struct tile64 {
+    static constexpr int EPU = 16 / (int)sizeof(E);           // elements per unit
+    static constexpr int UPR = W / EPU;                       // units per row
+    static constexpr int NU = 64 * UPR / kSdThreads;          // units per thread
+    static_assert(64 * UPR % kSdThreads == 0, "whole units per thread");
+    u32x4_t r[NU];
+    // rows [0, rows) of `src` (elements `stride` apart), columns [0, cols); zeros elsewhere
+    __device__ __forceinline__ void load(const E *src, int64_t stride, int rows, int cols) {
+#pragma unroll
+        for (int i = 0; i < NU; ++i) {
+            const int id = threadIdx.x + kSdThreads * i, row = id / UPR, c = (id % UPR) * EPU;
+            r[i] = u32x4_t{0u, 0u, 0u, 0u};
+            if (row < rows && c < cols) r[i] = *reinterpret_cast<const u32x4_t *>(src + row * stride + c);
+        }
+    }
+    __device__ __forceinline__ void stage(E *t) const {
+#pragma unroll
+        for (int i = 0; i < NU; ++i) {
+            const int id = threadIdx.x + kSdThreads * i, row = id / UPR, c = (id % UPR) * EPU;
+            *reinterpret_cast<u32x4_t *>(t + row * sd_ld<E>(W) + c) = r[i];
+        }
+    }
+};
+
+// Inclusive sum over the 64 lanes of a wave in 64 bits: the logarithms of a chunk's decays add up to
+// hundreds, and their differences are exponents.
+__device__ __forceinline__ double wave_incl_sum64(double v) {
+    auto moved = [](double x, auto ctrl, auto mask) {
+        const uint64_t b = __builtin_bit_cast(uint64_t, x);
+        const uint32_t lo = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)b, ctrl.value, mask.value, 0xf, false);
+        const uint32_t hi = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)(b >> 32), ctrl.value, mask.value, 0xf, false);
+        return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+    };
+    using std::integral_constant;
+    v += moved(v, integral_constant<int, 0x111>{}, integral_constant<int, 0xf>{});   // row_shr 1, 2, 4, 8
+    v += moved(v, integral_constant<int, 0x112>{}, integral_constant<int, 0xf>{});
+    v += moved(v, integral_constant<int, 0x114>{}, integral_constant<int, 0xf>{});
+    v += moved(v, integral_constant<int, 0x118>{}, integral_constant<int, 0xf>{});
+    v += moved(v, integral_constant<int, 0x142>{}, integral_constant<int, 0xa>{});   // row_bcast 15, 31
+    v += moved(v, integral_constant<int, 0x143>{}, integral_constant<int, 0xc>{});
+    return v;
+}
+__device__ __forceinline__ double wave_last(double v) {
+    const uint64_t b = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = __builtin_amdgcn_readlane((int)(uint32_t)b, 63), hi = __builtin_amdgcn_readlane((int)(uint32_t)(b >> 32), 63);
+    return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+
+// A chunk's per-token values, formed by one wave (token = lane).  c: in log2 units, as a float and
+// what it lacks.
+struct sd_tokens {
+    float ch[kSdQ], cl[kSdQ];   // c_t
+    float dt[kSdQ];             // 0 past the sequence's end
+    float w[kSdQ];              // e^{c_last - c_t} dt_t
+    float e[kSdQ];              // e^{c_t}
+    float dec, pad[3];          // e^{c_last}
+};
+// dt of token `lane` of the chunk at t0 (0 at and past `len`); sig: softplus's derivative (1 without it)
+template <typename IO>
+__device__ __forceinline__ float sd_dt(const IO *dt, int64_t stride, int64_t t0, int64_t len, float bias, int softplus,
+                                       int lane, float &sig) {
+    sig = 0.0f;
+    if (t0 + lane >= len) return 0.0f;
+    const float v = io<IO>::ld(dt, (t0 + lane) * stride) + bias;
+    sig = 1.0f;
+    return softplus ? softplus_f32(v, sig) : v;
+}
+__device__ __forceinline__ void sd_form_tokens(sd_tokens &s, float dt, float a2, int lane) {
+    const double c = wave_incl_sum64((double)(a2 * dt)), tot = wave_last(c);
+    const float ch = (float)c;
+    s.ch[lane] = ch;
+    s.cl[lane] = (float)(c - (double)ch);
+    s.dt[lane] = dt;
+    s.w[lane] = hw_exp2((float)(tot - c)) * dt;
+    s.e[lane] = hw_exp2((float)c);
+    if (lane == 0) s.dec = hw_exp2((float)tot);
+}
+__device__ __forceinline__ f32x4_t ld4(const float *p) { return *reinterpret_cast<const f32x4_t *>(p); }
+
+// ---- the convolution ------------------------------------------------------------------------
+
+// v sigmoid(v) rounded to fp32 and then to bf16, as the exact value would be: u is rounded in the middle of the
+// path, and every kernel that forms it has to form the same one.  v comes in 64 bits; the fp32 value is off by at most
+// 8 + 3 |v| of its last places, and only where a border between two bf16 values is that near (one value in
+// a thousand) is it formed in 64 bits.
+__device__ __forceinline__ uint16_t silu_bf16(double v64) {
+    const float v = (float)v64, av = fabsf(v);
+    const float u = silu_f32(v);
+    const float off = fabsf((float)(int)(__float_as_uint(u) & 0xffffu) - 32768.0f);
+    if (off <= fmaf(av, 4.0f, 12.0f) || av > 64.0f) return f32_to_bf16((float)(v64 / (1.0 + exp(-v64))));
+    return f32_to_bf16(u);
+}
+
+// kSdConvV channels of a row, as raw words; rows of a projected tensor start anywhere (aligned: 4 elements).
+template <typename IO, bool AL> struct conv_vec {
+    __device__ __forceinline__ static void load(const IO *p, IO (&v)[kSdConvV]) {
+        if constexpr (AL) {
+            typedef uint32_t words __attribute__((ext_vector_type(sizeof(IO))));
+            const words w = *reinterpret_cast<const words *>(p);
+            __builtin_memcpy(v, &w, sizeof w);
+        } else {
+#pragma unroll
+            for (int k = 0; k < kSdConvV; ++k) v[k] = p[k];
+        }
+    }
+    __device__ __forceinline__ static void store(IO *p, const IO (&v)[kSdConvV]) {
+        if constexpr (AL) {
+            typedef uint32_t words __attribute__((ext_vector_type(sizeof(IO))));
+            words w;
+            __builtin_memcpy(&w, v, sizeof w);
+            *reinterpret_cast<words *>(p) = w;
+        } else {
+#pragma unroll
+            for (int k = 0; k < kSdConvV; ++k) p[k] = v[k];
+        }
+    }
+};
+template <typename IO> __device__ __forceinline__ float io_f32(IO v) {
+    if constexpr (sizeof(IO) == 2) return bf16_to_f32(v);
+    else return v;
+}
+
+// u[b][t][c] = silu(bias + sum_k w[c][k] row_{t - (W-1) + k}), zero at and past a sequence's length; thread:
+// kSdConvV channels of `tt` tokens.  A row before token 0 comes from st_in (zero without it).  The thread of
+// the first tokens also writes the W - 1 rows before token len (st_out may be st_in).
+// w4: the taps at [c][4], the oldest first, zeros in front (W < 4 taps).
+template <typename IO, bool AL>
+__global__ void __launch_bounds__(256)
+sd_conv_kernel(const IO *__restrict__ x, int64_t xstride, const float *__restrict__ w, const float *__restrict__ bias,
+               int width, const IO *st_in, IO *st_out, const int32_t *__restrict__ lens, IO *__restrict__ u, int64_t L,
+               int dc, int tt, int vblocks, int ntiles) {
+    const int v = blockIdx.x % vblocks * 256 + threadIdx.x;
+    if (v >= dc / kSdConvV) return;
+    const int c = v * kSdConvV;
+    const int64_t b = blockIdx.x / vblocks / ntiles, t0 = (int64_t)(blockIdx.x / vblocks % ntiles) * tt, t1 = min(t0 + tt, L);
+    const int64_t len = lens ? min(max((int64_t)lens[b], (int64_t)0), L) : L;
+    const IO *xb = x + b * L * xstride + c;
+    IO *ub = u + b * L * dc + c;
+    const int h = width - 1;
+    auto row = [&](int64_t t, IO (&o)[kSdConvV]) {   // t >= -3
+        if (t >= 0) conv_vec<IO, AL>::load(xb + t * xstride, o);
+        else if (st_in && t >= -h) conv_vec<IO, true>::load(st_in + (b * h + h + t) * dc + c, o);
+        else
+            for (int k = 0; k < kSdConvV; ++k) o[k] = 0;
+    };
+    using acc_t = std::conditional_t<sizeof(IO) == 2, double, float>;
+    acc_t wv[kSdConvV][kSdTaps], bv[kSdConvV], past[kSdTaps - 1][kSdConvV];
+#pragma unroll
+    for (int k = 0; k < kSdConvV; ++k) {
+#pragma unroll
+        for (int j = 0; j < kSdTaps; ++j) {
+            const int tap = j - (kSdTaps - width);
+            wv[k][j] = tap >= 0 ? (acc_t)w[(int64_t)(c + k) * width + tap] : (acc_t)0;
+        }
+        bv[k] = bias ? (acc_t)bias[c + k] : (acc_t)0;
+    }
+#pragma unroll
+    for (int j = 0; j < kSdTaps - 1; ++j) {
+        IO r[kSdConvV];
+        row(t0 - 3 + j, r);
+#pragma unroll
+        for (int k = 0; k < kSdConvV; ++k) past[j][k] = (acc_t)io_f32(r[k]);
+    }
+    if (st_out && t0 == 0) {
+        IO keep[kSdTaps - 1][kSdConvV];
+#pragma unroll
+        for (int j = 0; j < kSdTaps - 1; ++j)
+            if (j < h) row(len - h + j, keep[j]);
+#pragma unroll
+        for (int j = 0; j < kSdTaps - 1; ++j)
+            if (j < h) conv_vec<IO, true>::store(st_out + (b * h + j) * dc + c, keep[j]);
+    }
+    for (int64_t t = t0; t < t1; ++t) {
+        IO o[kSdConvV];
+        if (t < len) {
+            IO r[kSdConvV];
+            conv_vec<IO, AL>::load(xb + t * xstride, r);
+#pragma unroll
+            for (int k = 0; k < kSdConvV; ++k) {
+                const acc_t now = (acc_t)io_f32(r[k]);
+                acc_t p = fma(wv[k][0], past[0][k], bv[k]);
+                p = fma(wv[k][1], past[1][k], p);
+                p = fma(wv[k][2], past[2][k], p);
+                p = fma(wv[k][3], now, p);
+                past[0][k] = past[1][k];
+                past[1][k] = past[2][k];
+                past[2][k] = now;
+                if constexpr (sizeof(IO) == 2) o[k] = silu_bf16(p);
+                else o[k] = silu_f32(p);
+            }
+        } else {
+#pragma unroll
+            for (int k = 0; k < kSdConvV; ++k) o[k] = 0;
+        }
+        conv_vec<IO, true>::store(ub + t * dc, o);
+    }
+}
+
+// ---- the layer over a sequence --------------------------------------------------------------
+
+struct sd_shape {
+    int64_t L;              // tokens (padded length)
+    int H, P, G, N;         // heads, channels per head, groups, states
+    int PT;                 // 64-channel tiles per head
+    int dc;                 // elements per row of u: H P + 2 G N
+    int64_t dt_stride;      // elements between tokens of the step sizes
+    int softplus;
+    int64_t nchunk;         // chunks of a sequence
+};
+
+// Where workgroup (sequence b, head h, tile pt) finds its rows.
+template <typename IO> struct sd_view {
+    const IO *x, *B, *C;
+    int pw;                 // channels of the tile that exist
+    __device__ __forceinline__ sd_view(const IO *u, const sd_shape &s, int64_t b, int h, int pt) {
+        const IO *r = u + b * s.L * s.dc;
+        const int g = h / (s.H / s.G);
+        x = r + h * s.P + pt * 64;
+        B = r + s.H * s.P + g * s.N;
+        C = B + s.G * s.N;
+        pw = min(64, s.P - pt * 64);
+    }
+};
+
+// State accumulators of a wave: D[n][p], rows n = 16 nb + 4 (lane / 16) + e, column p = 16 w + lane % 16.
+// In memory [p][n]: four consecutive n per lane.
+template <int NB>
+__device__ __forceinline__ void sd_load_state(f32x4_t (&S)[NB], const float *m, int N, int pw, int w, int lane) {
+    const int p = 16 * w + (lane & 15);
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+        const int n = 16 * nb + 4 * (lane >> 4);
+        S[nb] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+        if (p < pw && n < N) S[nb] = ld4(m + (int64_t)p * N + n);
+    }
+}
+template <int NB>
+__device__ __forceinline__ void sd_store_state(const f32x4_t (&S)[NB], float *m, int N, int pw, int w, int lane) {
+    const int p = 16 * w + (lane & 15);
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+        const int n = 16 * nb + 4 * (lane >> 4);
+        if (p < pw && n < N) *reinterpret_cast<f32x4_t *>(m + (int64_t)p * N + n) = S[nb];
+    }
+}
+
+// One workgroup per (sequence, head, 64-channel tile): the sequence's chunks in order, the state in
+// accumulators.  ckpt: [b][h][chunk][P][N], receives the state entering each chunk, or null.
+template <typename E, int NT>
+__global__ void __launch_bounds__(kSdThreads)
+sd_scan_kernel(const typename sd<E>::io *__restrict__ u_, const typename sd<E>::io *__restrict__ dt,
+               const float *__restrict__ A, const float *__restrict__ Dv, const float *__restrict__ dt_bias,
+               const int32_t *__restrict__ lens, const float *h0, typename sd<E>::io *__restrict__ y_, float *last,
+               float *__restrict__ ckpt, sd_shape s) {
+    using IO = typename sd<E>::io;
+    using F = typename sd<E>::frag;
+    constexpr int NB = NT / 16;
+    __shared__ __attribute__((aligned(16))) E tB[64 * sd_ld<E>(NT)], tC[64 * sd_ld<E>(NT)], tX[64 * sd_ld<E>(64)];
+    __shared__ __attribute__((aligned(16))) E tM[(sd<E>::split ? 2 : 1)][64 * sd_ld<E>(64)];
+    __shared__ sd_tokens tk;
+    const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int c16 = lane & 15, q4 = 4 * (lane >> 4);
+    const int pt = blockIdx.x % s.PT, h = blockIdx.x / s.PT % s.H;
+    const int64_t b = blockIdx.x / s.PT / s.H;
+    const sd_view<IO> v(u_, s, b, h, pt);
+    const E *xs = reinterpret_cast<const E *>(v.x), *Bs = reinterpret_cast<const E *>(v.B), *Cs = reinterpret_cast<const E *>(v.C);
+    const int64_t len = lens ? min(max((int64_t)lens[b], (int64_t)0), s.L) : s.L;
+    const float a2 = A[h] * kLog2e, bias = dt_bias ? dt_bias[h] : 0.0f, skip = Dv ? Dv[h] : 0.0f;
+    const IO *dtp = dt + b * s.L * s.dt_stride + h;
+    const int64_t st_at = (b * s.H + h) * s.P * s.N + (int64_t)pt * 64 * s.N;
+    IO *yb = y_ + (b * s.L * s.H + h) * s.P + pt * 64;
+    f32x4_t S[NB];
+    if (h0) {
+        sd_load_state(S, h0 + st_at, s.N, v.pw, w, lane);
+    } else {
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) S[nb] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+    }
+    tile64<E, NT> rB, rC;
+    tile64<E, 64> rX;
+    float rdt = 0.0f, sig;
+    auto fetch = [&](int64_t t0) {
+        const int rows = (int)min((int64_t)64, len - t0);
+        rB.load(Bs + t0 * s.dc, s.dc, rows, s.N);
+        rC.load(Cs + t0 * s.dc, s.dc, rows, s.N);
+        rX.load(xs + t0 * s.dc, s.dc, rows, v.pw);
+        if (w == 0) rdt = sd_dt(dtp, s.dt_stride, t0, len, bias, s.softplus, lane, sig);
+    };
+    const int64_t live = (len + kSdQ - 1) / kSdQ;   // chunks with tokens
+    if (live > 0) fetch(0);
+    for (int64_t c = 0; c < live; ++c) {
+        const int64_t t0 = c * kSdQ;
+        rB.stage(tB);
+        rC.stage(tC);
+        rX.stage(tX);
+        if (w == 0) sd_form_tokens(tk, rdt, a2, lane);
+        if (c + 1 < live) fetch(t0 + kSdQ);
+        if (ckpt) sd_store_state(S, ckpt + (((b * s.H + h) * s.nchunk + c) * s.P + (int64_t)pt * 64) * s.N, s.N, v.pw, w, lane);
+        __syncthreads();
+        F xf[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) xf[i] = ld_col<E, 64>(tX, 16 * i, 16 * w, lane);
+        // Y^T[p][t] from the state entering, and G^T[s][t] for this wave's 16 tokens s
+        f32x4_t Y[4] = {}, Gt[4] = {};
+#pragma unroll
+        for (int k = 0; k < NB; k += 2) {
+            const formed<E, 2> s0(S[k]), s1(S[k + 1]);
+            const F b0 = ld_row<E, NT>(tB, 16 * w, 16 * k, lane), b1 = ld_row<E, NT>(tB, 16 * w, 16 * k + 16, lane);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const F c0 = ld_row<E, NT>(tC, 16 * j, 16 * k, lane), c1 = ld_row<E, NT>(tC, 16 * j, 16 * k + 16, lane);
+                Y[j] = mma_fa<E, 2>(s0, s1, c0, c1, Y[j]);
+                if (j >= w) Gt[j] = mma(b0, b1, c0, c1, Gt[j]);
+            }
+        }
+        // M[t][s], D on its diagonal
+        {
+            const int s0 = 16 * w + q4;
+            const f32x4_t sh = ld4(tk.ch + s0), sl = ld4(tk.cl + s0), sd4 = ld4(tk.dt + s0);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int t = 16 * j + c16;
+                f32x4_t m = {0.0f, 0.0f, 0.0f, 0.0f};
+                if (j >= w) {
+                    const float th = tk.ch[t], tl = tk.cl[t];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float k = hw_exp2((th - sh[e]) + (tl - sl[e]));
+                        m[e] = s0 + e <= t ? Gt[j][e] * (k * sd4[e]) : 0.0f;
+                        if (s0 + e == t) m[e] += skip;
+                    }
+                }
+                const formed<E, 2> f(m);
+#pragma unroll
+                for (int i = 0; i < formed<E, 2>::N; ++i) *reinterpret_cast<F *>(&tM[i][t * sd_ld<E>(64) + s0]) = f.p[i];
+            }
+        }
+        // the state leaving the chunk
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) S[nb] *= tk.dec;
+#pragma unroll
+        for (int i = 0; i < 4; i += 2) {
+            const formed<E, 3> x0(widen(xf[i]) * ld4(tk.w + 16 * i + q4)), x1(widen(xf[i + 1]) * ld4(tk.w + 16 * i + 16 + q4));
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb)
+                S[nb] = mma_fb<E, 3>(ld_col<E, NT>(tB, 16 * i, 16 * nb, lane), ld_col<E, NT>(tB, 16 * i + 16, 16 * nb, lane), x0, x1, S[nb]);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) Y[j] *= tk.e[16 * j + c16];
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int i = 0; i <= j; i += 2)
+#pragma unroll
+                for (int m = 0; m < formed<E, 2>::N; ++m)
+                    Y[j] = mma(xf[i], xf[i + 1], ld_row<E, 64>(tM[m], 16 * j, 16 * i, lane), ld_row<E, 64>(tM[m], 16 * j, 16 * i + 16, lane), Y[j]);
+        if (16 * w + q4 < v.pw) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int64_t t = t0 + 16 * j + c16;
+                if (t >= s.L) continue;
+                const f32x4_t o = t < len ? Y[j] : f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+                IO *yp = yb + t * s.H * s.P + 16 * w + q4;
+                if constexpr (sizeof(IO) == 2)
+                    *reinterpret_cast<u32x2_t *>(yp) = u32x2_t{f32x2_to_bf16x2(o[0], o[1]), f32x2_to_bf16x2(o[2], o[3])};
+                else *reinterpret_cast<f32x4_t *>(yp) = o;
+            }
+        }
+    }
+    // chunks past the sequence's end: the state stays, y is zero
+    for (int64_t c = live; c < s.nchunk; ++c) {
+        if (ckpt) sd_store_state(S, ckpt + (((b * s.H + h) * s.nchunk + c) * s.P + (int64_t)pt * 64) * s.N, s.N, v.pw, w, lane);
+        if (16 * w + q4 >= v.pw) continue;
+        for (int j = 0; j < 4; ++j) {
+            const int64_t t = c * kSdQ + 16 * j + c16;
+            if (t >= s.L) continue;
+            IO *yp = yb + t * s.H * s.P + 16 * w + q4;
+            for (int e = 0; e < 4; ++e) yp[e] = 0;
+        }
+    }
+    if (last) sd_store_state(S, last + st_at, s.N, v.pw, w, lane);
+}
+
+// ---- one token ------------------------------------------------------------------------------
+
+// One workgroup per (sequence, head, rows of P): LPR lanes hold a channel's N states, four each.
+template <typename IO, int LPR>
+__global__ void __launch_bounds__(256)
+sd_step_kernel(float *__restrict__ state, const IO *__restrict__ u, const IO *__restrict__ dt, int64_t dt_stride,
+               const float *__restrict__ A, const float *__restrict__ Dv, const float *__restrict__ dt_bias,
+               int softplus, IO *__restrict__ y, int H, int P, int G, int N) {
+    constexpr int ROWS = 256 / LPR;
+    const int h = blockIdx.x % H;
+    const int64_t b = blockIdx.x / H;
+    const IO *r = u + b * (H * P + 2 * G * N);
+    const int g = h / (H / G), n = (threadIdx.x % LPR) * 4;
+    const float v = io<IO>::ld(dt, b * dt_stride + h) + (dt_bias ? dt_bias[h] : 0.0f);
+    const float d = softplus ? softplus_f32(v) : v;
+    const float a = hw_exp2((A[h] * kLog2e) * d), skip = Dv ? Dv[h] : 0.0f;
+    f32x4_t Bv = {0.0f, 0.0f, 0.0f, 0.0f}, Cv = Bv;
+    if (n < N) {
+        const IO *Bp = r + H * P + g * N + n, *Cp = Bp + G * N;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            Bv[e] = io<IO>::ld(Bp, e);
+            Cv[e] = io<IO>::ld(Cp, e);
+        }
+    }
+    float *sb = state + (b * H + h) * P * N;
+    for (int p = threadIdx.x / LPR; p < P; p += ROWS) {
+        const float x = io<IO>::ld(r, h * P + p);
+        float o = 0.0f;
+        if (n < N) {
+            f32x4_t *sp = reinterpret_cast<f32x4_t *>(sb + (int64_t)p * N + n);
+            const f32x4_t st = *sp * a + Bv * (d * x);
+            *sp = st;
+            o = st[0] * Cv[0] + st[1] * Cv[1] + st[2] * Cv[2] + st[3] * Cv[3];
+        }
+#pragma unroll
+        for (int m = 1; m < LPR; m *= 2) o += __shfl_xor(o, m, 64);
+        if (n == 0) io<IO>::st(y, (b * H + h) * P + p, o + skip * x);
+    }
+}
+
+}  // namespace ssm

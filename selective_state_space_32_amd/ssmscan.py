@@ -48,6 +48,12 @@ class ssm_gated_plan(ctypes.Structure):
                 [(f, ctypes.c_int32) for f in ("lane_channels", "item_chunks", "group", "queues", "run")])
 
 
+class ssm_ssd_conv_dims(ctypes.Structure):
+    _fields_ = ([(f, ctypes.c_int64) for f in ("batch", "seqlen", "nheads", "headdim", "ngroups", "dstate", "xbc_stride",
+                                               "dt_stride")] +
+                [(f, ctypes.c_int32) for f in ("io_dtype", "width")])
+
+
 class SSMError(RuntimeError):
     def __init__(self, code: int, msg: str):
         super().__init__(f"{STATUS.get(code, code)}: {msg}")
@@ -116,6 +122,28 @@ def _load() -> ctypes.CDLL:
     lib.ssm_layernorm_bwd_workspace_bytes.restype = ctypes.c_size_t
     lib.ssm_layernorm_bwd.argtypes = [P] * 6 + [ctypes.c_int] + [P] * 4 + [D, P, ctypes.c_size_t, P]
     lib.ssm_layernorm_bwd.restype = ctypes.c_int
+    V = ctypes.POINTER(ssm_ssd_conv_dims)
+    lib.ssm_ssd_conv_workspace_bytes.argtypes = [V, ctypes.c_int]
+    lib.ssm_ssd_conv_workspace_bytes.restype = ctypes.c_size_t
+    lib.ssm_ssd_conv_fwd.argtypes = [P] * 10 + [ctypes.c_int] + [P] * 3 + [V, P, ctypes.c_size_t, P]
+    lib.ssm_ssd_conv_fwd.restype = ctypes.c_int
+    lib.ssm_ssd_conv_bwd_workspace_bytes.argtypes = [V, ctypes.c_int]
+    lib.ssm_ssd_conv_bwd_workspace_bytes.restype = ctypes.c_size_t
+    lib.ssm_ssd_conv_bwd.argtypes = ([P] * 10 + [ctypes.c_int, P, P, P, ctypes.c_size_t] + [P] * 9 +
+                                     [V, P, ctypes.c_size_t, P])
+    lib.ssm_ssd_conv_bwd.restype = ctypes.c_int
+    lib.ssm_ssd_conv_step_workspace_bytes.argtypes = [V]
+    lib.ssm_ssd_conv_step_workspace_bytes.restype = ctypes.c_size_t
+    lib.ssm_ssd_conv_step.argtypes = [P] * 9 + [ctypes.c_int, P, V, P, ctypes.c_size_t, P]
+    lib.ssm_ssd_conv_step.restype = ctypes.c_int
+    i64 = ctypes.c_int64
+    lib.ssm_groupnorm_fwd.argtypes = [P, P, i64, P, P, i64, ctypes.c_float, ctypes.c_int, P, P, P, D, P]
+    lib.ssm_groupnorm_fwd.restype = ctypes.c_int
+    lib.ssm_groupnorm_bwd_workspace_bytes.argtypes = [D, i64]
+    lib.ssm_groupnorm_bwd_workspace_bytes.restype = ctypes.c_size_t
+    lib.ssm_groupnorm_bwd.argtypes = ([P, P, P, i64, P, P, P, P, i64, ctypes.c_int] + [P] * 4 +
+                                      [D, P, ctypes.c_size_t, P])
+    lib.ssm_groupnorm_bwd.restype = ctypes.c_int
     return lib
 
 
@@ -1027,4 +1055,295 @@ def layernorm_bwd(dy: torch.Tensor, total: torch.Tensor, weight: torch.Tensor, m
                                  NORM_SUM_F32 if kept != io else 0, _addr(ds), _addr(grads.get("dx")),
                                  _addr(grads.get("dweight")), _addr(grads.get("dbias")), ctypes.byref(dims),
                                  _addr(workspace) if have else None, have, st))
+    return grads
+
+
+def _rows(t: torch.Tensor, name: str, lead, width: int, dtype, device) -> int:
+    """Checks rows of `width` neighbouring values of leading shape `lead`, packed or parts of wider rows; the
+    elements between one row and the next."""
+    if t.dim() != len(lead) + 1 or t.shape[:-1] != lead or t.shape[-1] != width:
+        raise ValueError(f"{name}: shape {tuple(t.shape)} != {tuple(lead) + (width,)}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: dtype {t.dtype} != {dtype}")
+    if t.device != device:
+        raise ValueError(f"{name}: on {t.device}, expected {device}")
+    if t.is_contiguous():
+        return width
+    st, shape = t.stride(), t.shape
+    row = span = 0
+    for k in range(t.dim() - 2, -1, -1):
+        if shape[k] == 1:
+            continue
+        if row == 0:
+            row = span = st[k]
+        elif st[k] != span:
+            row = -1
+            break
+        span *= shape[k]
+    if (width > 1 and st[-1] != 1) or (row != 0 and row < width):
+        raise ValueError(f"{name}: rows must be contiguous and evenly spaced (strides {tuple(st)})")
+    return row or width
+
+
+def _ssd_conv_inputs(xbc, conv_w, conv_b, dt, A, D, dt_bias, dstate, ngroups, conv_state, lead):
+    """Checks of the inputs that the layer's entry points share; their dims."""
+    if A.dim() != 1:
+        raise ValueError("A must be (heads,)")
+    if conv_w.dim() != 2:
+        raise ValueError("conv_w must be (row, width)")
+    dev, io = xbc.device, xbc.dtype
+    H, row = A.shape[0], xbc.shape[-1]
+    inner = row - 2 * ngroups * dstate
+    if H < 1 or ngroups < 1 or dstate < 1 or inner < H or inner % H:
+        raise ValueError(f"xbc: rows of {row} values are not {H} heads and 2 * {ngroups} * {dstate} states")
+    width = conv_w.shape[1]
+    xs = _rows(xbc, "xbc", lead, row, io, dev)
+    ds = _rows(dt, "dt", lead, H, io, dev)
+    _want(conv_w, "conv_w", (row, width), torch.float32, dev)
+    _want(A, "A", (H,), torch.float32, dev)
+    if conv_b is not None:
+        _want(conv_b, "conv_b", (row,), torch.float32, dev)
+    if D is not None:
+        _want(D, "D", (H,), torch.float32, dev)
+    if dt_bias is not None:
+        _want(dt_bias, "dt_bias", (H,), torch.float32, dev)
+    if conv_state is not None:
+        _want(conv_state, "conv_state", (lead[0], width - 1, row), io, dev)
+    return ssm_ssd_conv_dims(lead[0], lead[1] if len(lead) > 1 else 1, H, inner // H, ngroups, dstate, xs, ds,
+                             _io_code(io), width)
+
+
+def _ssd_conv_seq(xbc, conv_w, conv_b, dt, A, D, dt_bias, dstate, ngroups, conv_state, initial_state, seq_lens):
+    if xbc.dim() != 3:
+        raise ValueError("xbc must be (batch, L, row)")
+    dims = _ssd_conv_inputs(xbc, conv_w, conv_b, dt, A, D, dt_bias, dstate, ngroups, conv_state, xbc.shape[:2])
+    if initial_state is not None:
+        _want(initial_state, "initial_state", (dims.batch, dims.nheads, dims.headdim, dstate), torch.float32, xbc.device)
+    if seq_lens is not None:
+        _need_lens(seq_lens, dims.batch, xbc.device)
+    return dims
+
+
+def ssd_conv_fwd(xbc: torch.Tensor, conv_w: torch.Tensor, conv_b: Optional[torch.Tensor], dt: torch.Tensor,
+                 A: torch.Tensor, D: Optional[torch.Tensor] = None, dt_bias: Optional[torch.Tensor] = None,
+                 softplus: bool = True, *, dstate: int, ngroups: int = 1, conv_state: Optional[torch.Tensor] = None,
+                 initial_state: Optional[torch.Tensor] = None, seq_lens: Optional[torch.Tensor] = None,
+                 y: Optional[torch.Tensor] = None, last_state: Optional[torch.Tensor] = None,
+                 conv_state_out: Optional[torch.Tensor] = None, return_states: bool = True,
+                 workspace: Optional[torch.Tensor] = None, stream=None, save_checkpoints: bool = False):
+    """The state space dual layer with its causal convolution (ssm_ssd_conv_fwd), over whole sequences.
+
+    xbc: (batch, L, H P + 2 G N) float32 or bfloat16, the projected x, B and C; dt: (batch, L, H) of the same
+    dtype; both may be parts of a wider projected row.  conv_w: (row, width), conv_b: (row,), A, D, dt_bias:
+    (H,) float32; dstate N and ngroups G.  conv_state: (batch, width-1, row), the rows before token 0; initial_state:
+    (batch, H, P, N) float32; seq_lens: (batch,) int32 on the device, sequence b then has seq_lens[b] tokens and y
+    is zero past them.  last_state may be initial_state and conv_state_out conv_state (advanced in place).
+    Returns (y (batch, L, H, P), last_state, conv_state_out) -- the states None if neither given nor
+    wanted -- and with save_checkpoints (a training forward) also the workspace, for ssd_conv_bwd's `checkpoints`."""
+    dims = _ssd_conv_seq(xbc, conv_w, conv_b, dt, A, D, dt_bias, dstate, ngroups, conv_state, initial_state, seq_lens)
+    dev, io = xbc.device, xbc.dtype
+    bsz, L, H, P = dims.batch, dims.seqlen, dims.nheads, dims.headdim
+    if y is None:
+        y = _empty((bsz, L, H, P), io, dev, stream)
+    else:
+        _want(y, "y", (bsz, L, H, P), io, dev)
+    if last_state is not None:
+        _want(last_state, "last_state", (bsz, H, P, dstate), torch.float32, dev)
+    elif return_states:
+        last_state = _empty((bsz, H, P, dstate), torch.float32, dev, stream)
+    if conv_state_out is not None:
+        _want(conv_state_out, "conv_state_out", (bsz, dims.width - 1, xbc.shape[2]), io, dev)
+    elif return_states:
+        conv_state_out = _empty((bsz, dims.width - 1, xbc.shape[2]), io, dev, stream)
+    flags = (SCAN_SOFTPLUS if softplus else 0) | (SCAN_CHECKPOINTS if save_checkpoints else 0)
+    need = int(lib.ssm_ssd_conv_workspace_bytes(ctypes.byref(dims), flags)) if workspace is None else 0
+    if workspace is None and save_checkpoints:
+        workspace = _empty(need, torch.uint8, dev, stream)
+    workspace = _workspace(workspace, need, dev, stream)
+    st = _stream_addr(stream, dev)
+    _check(lib.ssm_ssd_conv_fwd(_addr(xbc), _addr(conv_w), _addr(conv_b), _addr(conv_state), _addr(dt), _addr(A), _addr(D),
+                                _addr(dt_bias), _addr(initial_state), _addr(seq_lens), flags, _addr(y), _addr(last_state),
+                                _addr(conv_state_out), ctypes.byref(dims), _addr(workspace),
+                                workspace.numel() * workspace.element_size(), st))
+    out = (y, last_state, conv_state_out)
+    return out + (workspace,) if save_checkpoints else out
+
+
+def ssd_conv_bwd(dy: torch.Tensor, xbc: torch.Tensor, conv_w: torch.Tensor, conv_b: Optional[torch.Tensor],
+                 dt: torch.Tensor, A: torch.Tensor, D: Optional[torch.Tensor] = None,
+                 dt_bias: Optional[torch.Tensor] = None, softplus: bool = True, *, dstate: int, ngroups: int = 1,
+                 conv_state: Optional[torch.Tensor] = None, initial_state: Optional[torch.Tensor] = None,
+                 seq_lens: Optional[torch.Tensor] = None, dlast_state: Optional[torch.Tensor] = None,
+                 want_initial_state_grad: bool = False, want_conv_state_grad: Optional[bool] = None,
+                 checkpoints: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                 stream=None) -> dict:
+    """Gradients of ssd_conv_fwd (ssm_ssd_conv_bwd) given dy (batch, L, H, P) and optionally dlast_state
+    (batch, H, P, N); conv_state_out is taken to carry none.  The forward inputs are passed as they were;
+    `checkpoints`: the workspace an ssd_conv_fwd(..., save_checkpoints=True) call on them returned (without it
+    the states are recomputed).  Returns a dict: dxbc (batch, L, row), ddt (batch, L, H) of xbc's dtype, packed;
+    dconv_w, dconv_b (if conv_b), dA, dD (if D), ddt_bias (if dt_bias) float32; dinitial_state float32 (if asked
+    for); dconv_state of xbc's dtype (default: when conv_state is given)."""
+    dims = _ssd_conv_seq(xbc, conv_w, conv_b, dt, A, D, dt_bias, dstate, ngroups, conv_state, initial_state, seq_lens)
+    dev, io = xbc.device, xbc.dtype
+    bsz, L, H, P = dims.batch, dims.seqlen, dims.nheads, dims.headdim
+    _want(dy, "dy", (bsz, L, H, P), io, dev)
+    if dlast_state is not None:
+        _want(dlast_state, "dlast_state", (bsz, H, P, dstate), torch.float32, dev)
+    if checkpoints is not None and (checkpoints.device != dev or not checkpoints.is_contiguous()):
+        raise ValueError("checkpoints: must be contiguous and on the device of xbc")
+    if want_conv_state_grad is None:
+        want_conv_state_grad = conv_state is not None
+    row = xbc.shape[2]
+    g = dict(dxbc=_empty((bsz, L, row), io, dev, stream), ddt=_empty((bsz, L, H), io, dev, stream),
+             dconv_w=_like(conv_w, stream), dA=_like(A, stream))
+    if conv_b is not None:
+        g["dconv_b"] = _like(conv_b, stream)
+    if D is not None:
+        g["dD"] = _like(D, stream)
+    if dt_bias is not None:
+        g["ddt_bias"] = _like(dt_bias, stream)
+    if want_initial_state_grad:
+        g["dinitial_state"] = _empty((bsz, H, P, dstate), torch.float32, dev, stream)
+    if want_conv_state_grad:
+        g["dconv_state"] = _empty((bsz, dims.width - 1, row), io, dev, stream)
+    have = 0 if checkpoints is None else checkpoints.numel() * checkpoints.element_size()
+    flags = (SCAN_SOFTPLUS if softplus else 0) | (SCAN_CHECKPOINTS if have else 0)
+    need = int(lib.ssm_ssd_conv_bwd_workspace_bytes(ctypes.byref(dims), flags)) if workspace is None else 0
+    workspace = _workspace(workspace, need, dev, stream)
+    st = _stream_addr(stream, dev)
+    _check(lib.ssm_ssd_conv_bwd(_addr(xbc), _addr(conv_w), _addr(conv_b), _addr(conv_state), _addr(dt), _addr(A), _addr(D),
+                                _addr(dt_bias), _addr(initial_state), _addr(seq_lens), flags, _addr(dy),
+                                _addr(dlast_state), _addr(checkpoints) if have else None, have, _addr(g["dxbc"]),
+                                _addr(g["dconv_w"]), _addr(g.get("dconv_b")), _addr(g.get("dconv_state")), _addr(g["ddt"]),
+                                _addr(g["dA"]), _addr(g.get("dD")), _addr(g.get("ddt_bias")),
+                                _addr(g.get("dinitial_state")), ctypes.byref(dims), _addr(workspace),
+                                workspace.numel() * workspace.element_size(), st))
+    return g
+
+
+def _ssd_conv_step_args(state, conv_state, xbc, conv_w, conv_b, dt, A, D, dt_bias, softplus, dstate, ngroups, y, workspace,
+                        stream):
+    if xbc.dim() != 2:
+        raise ValueError("xbc must be (sequences, row)")
+    dev, io = xbc.device, xbc.dtype
+    dims = _ssd_conv_inputs(xbc, conv_w, conv_b, dt, A, D, dt_bias, dstate, ngroups, conv_state, xbc.shape[:1])
+    shape = (dims.batch, dims.nheads, dims.headdim)
+    _want(state, "state", shape + (dstate,), torch.float32, dev)
+    if y is None:
+        y = _empty(shape, io, dev, stream)
+    else:
+        _want(y, "y", shape, io, dev)
+    need = int(lib.ssm_ssd_conv_step_workspace_bytes(ctypes.byref(dims))) if workspace is None else 0
+    workspace = _workspace(workspace, need, dev, stream)
+    args = (_addr(state), _addr(conv_state), _addr(xbc), _addr(conv_w), _addr(conv_b), _addr(dt), _addr(A), _addr(D),
+            _addr(dt_bias), SCAN_SOFTPLUS if softplus else 0, _addr(y), ctypes.byref(dims), _addr(workspace),
+            workspace.numel() * workspace.element_size(), _stream_addr(stream, dev))
+    return args, (state, conv_state, xbc, conv_w, conv_b, dt, A, D, dt_bias, y, dims, workspace), y
+
+
+def ssd_conv_step(state: torch.Tensor, conv_state: Optional[torch.Tensor], xbc: torch.Tensor, conv_w: torch.Tensor,
+                  conv_b: Optional[torch.Tensor], dt: torch.Tensor, A: torch.Tensor, D: Optional[torch.Tensor] = None,
+                  dt_bias: Optional[torch.Tensor] = None, softplus: bool = True, *, dstate: int, ngroups: int = 1,
+                  y: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """One token of the state space dual layer with its convolution (ssm_ssd_conv_step): `state` (S, H, P, N)
+    float32 and `conv_state` (S, width-1, row) are advanced in place (conv_state None only for a convolution of one tap).
+    xbc: (S, row), dt: (S, H), packed or parts of wider rows; the parameters as in ssd_conv_fwd.  Returns y (S, H, P)."""
+    args, _keep, y = _ssd_conv_step_args(state, conv_state, xbc, conv_w, conv_b, dt, A, D, dt_bias, softplus, dstate,
+                                         ngroups, y, workspace, stream)
+    _check(lib.ssm_ssd_conv_step(*args))
+    return y
+
+
+def ssd_conv_step_call(state: torch.Tensor, conv_state: Optional[torch.Tensor], xbc: torch.Tensor, conv_w: torch.Tensor,
+                       conv_b: Optional[torch.Tensor], dt: torch.Tensor, A: torch.Tensor, D: Optional[torch.Tensor] = None,
+                       dt_bias: Optional[torch.Tensor] = None, softplus: bool = True, *, dstate: int, ngroups: int = 1,
+                       y: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                       stream=None) -> Callable[[], None]:
+    """The ssd_conv_step call checked and marshalled once (see scan_fwd_call)."""
+    args, keep, _y = _ssd_conv_step_args(state, conv_state, xbc, conv_w, conv_b, dt, A, D, dt_bias, softplus, dstate,
+                                         ngroups, y, workspace, stream)
+
+    def call(_args=args, _keep=keep):
+        _check(lib.ssm_ssd_conv_step(*_args))
+    return call
+
+
+GROUPNORM_RMS = 1          # flag bits of the group norm's entry points (include/ssmscan.h)
+GROUPNORM_GATE_FIRST = 2
+GROUPNORM_SILU = 4
+
+
+def _groupnorm_inputs(x, weight, bias, groups, z, gate_first, silu, centre):
+    rows, dim = _norm_shape(x, "x")
+    dev, io = x.device, x.dtype
+    if groups < 1 or dim % groups:
+        raise ValueError(f"x: rows of {dim} values are not {groups} equal groups")
+    if silu and z is not None:
+        raise ValueError("silu is the activation without a gate z")
+    if gate_first and z is None:
+        raise ValueError("gate_first needs the gate z")
+    dims = ssm_dims(1, rows, dim, 1, _io_code(io), 0)
+    _want(x, "x", x.shape, io, dev)
+    _want(weight, "weight", (dim,), torch.float32, dev)
+    if bias is not None:
+        _want(bias, "bias", (dim,), torch.float32, dev)
+    zs = 0 if z is None else _rows(z, "z", x.shape[:-1], dim, io, dev)
+    flags = (0 if centre else GROUPNORM_RMS) | (GROUPNORM_GATE_FIRST if gate_first else 0) | (GROUPNORM_SILU if silu else 0)
+    return dims, zs, flags
+
+
+def groupnorm_fwd(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor] = None, eps: float = 1e-5, *,
+                  groups: int = 1, centre: bool = True, z: Optional[torch.Tensor] = None, gate_first: bool = False,
+                  silu: bool = False, y: Optional[torch.Tensor] = None, stream=None):
+    """Group norm over the last axis in `groups` equal groups, with an activation (ssm_groupnorm_fwd):
+    n = (v - mean) rstd over each group (v rstd with centre=False), o = n weight + bias, and y = o, or with a
+    gate z: v = x silu(z) (gate_first) or y = o silu(z), or y = silu(o) (silu).
+
+    x: (..., dim) float32 or bfloat16; z: the same shape, packed or part of a wider row; weight, bias: (dim,)
+    float32.  Returns (y, mean, rstd): mean (None with centre=False) and rstd (..., groups) float32."""
+    dims, zs, flags = _groupnorm_inputs(x, weight, bias, groups, z, gate_first, silu, centre)
+    dev, io = x.device, x.dtype
+    if y is None:
+        y = _like(x, stream)
+    else:
+        _want(y, "y", x.shape, io, dev)
+    stats = x.shape[:-1] + (groups,)
+    mean = _empty(stats, torch.float32, dev, stream) if centre else None
+    rstd = _empty(stats, torch.float32, dev, stream)
+    st = _stream_addr(stream, dev)
+    _check(lib.ssm_groupnorm_fwd(_addr(x), _addr(z), zs, _addr(weight), _addr(bias), groups, float(eps), flags, _addr(y),
+                                 _addr(mean), _addr(rstd), ctypes.byref(dims), st))
+    return y, mean, rstd
+
+
+def groupnorm_bwd(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor],
+                  mean: Optional[torch.Tensor], rstd: torch.Tensor, *, groups: int = 1, z: Optional[torch.Tensor] = None,
+                  gate_first: bool = False, silu: bool = False, want_param_grads: bool = True,
+                  workspace: Optional[torch.Tensor] = None, stream=None) -> dict:
+    """Gradients of groupnorm_fwd (ssm_groupnorm_bwd) given dy of x's shape and dtype; mean (None: it was not
+    centred) and rstd are what the forward returned, the rest is passed as it was.  Returns a dict: dx, dz (if z) of
+    x's dtype, packed, and with want_param_grads dweight, dbias (if bias) float32."""
+    dims, zs, flags = _groupnorm_inputs(x, weight, bias, groups, z, gate_first, silu, mean is not None)
+    dev, io = x.device, x.dtype
+    _want(dy, "dy", x.shape, io, dev)
+    stats = x.shape[:-1] + (groups,)
+    _want(rstd, "rstd", stats, torch.float32, dev)
+    if mean is not None:
+        _want(mean, "mean", stats, torch.float32, dev)
+    grads = dict(dx=_like(x, stream))
+    if z is not None:
+        grads["dz"] = _like(x, stream)
+    need = 0
+    if want_param_grads:
+        grads["dweight"] = _like(weight, stream)
+        if bias is not None:
+            grads["dbias"] = _like(bias, stream)
+        need = int(lib.ssm_groupnorm_bwd_workspace_bytes(ctypes.byref(dims), groups)) if workspace is None else 0
+    if need or workspace is not None:
+        workspace = _workspace(workspace, need, dev, stream)
+    have = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    st = _stream_addr(stream, dev)
+    _check(lib.ssm_groupnorm_bwd(_addr(dy), _addr(x), _addr(z), zs, _addr(weight), _addr(bias), _addr(mean), _addr(rstd),
+                                 groups, flags, _addr(grads["dx"]), _addr(grads.get("dz")), _addr(grads.get("dweight")),
+                                 _addr(grads.get("dbias")), ctypes.byref(dims), _addr(workspace) if have else None, have, st))
     return grads
