@@ -601,7 +601,8 @@ typedef struct ssm_ssd_conv_dims {
  * or each other otherwise.  Products of bf16 u take u's values as they are; what is formed in between is carried
  * to 16 bits where the result leaves in bf16 and to 24 where it is kept in fp32, sums and states are fp32; with fp32
  * I/O all products are fp32.  Tokens are taken 64 at a time: a NaN or infinity in a token may reach the
- * outputs of the 63 tokens before it, and no others before it.  nheads*headdim is at most 2^24.
+ * outputs of the 63 tokens before it, and no others before it.  nheads*headdim and 2*ngroups*dstate are at most
+ * 2^22.
  * Returns SSM_OK or a negative ssm_status (nothing is launched on an error). */
 SSMSCAN_API int ssm_ssd_conv_fwd(const void *xbc, const float *conv_w, const float *conv_b, const void *conv_state,
                 const void *dt, const float *A, const float *D, const float *dt_bias, const float *initial_state,

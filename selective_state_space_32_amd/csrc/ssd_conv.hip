@@ -36,8 +36,9 @@ int check_dims(const ssm_ssd_conv_dims *dm) {
         return fail(SSM_ERR_SHAPE, "nheads %lld is not a multiple of ngroups %lld", (long long)dm->nheads, (long long)dm->ngroups);
     if (dm->width < 1 || dm->width > ssm::kSdTaps)
         return fail(SSM_ERR_SHAPE, "convolution width %d is not 1 to %d", dm->width, ssm::kSdTaps);
-    if (dm->nheads > (int64_t(1) << 24) / dm->headdim || dm->ngroups > (int64_t(1) << 23) / dm->dstate)
-        return fail(SSM_ERR_SHAPE, "nheads*headdim or 2*ngroups*dstate exceeds 2^24");
+    // (64 rows of u, at most 2^23 elements each, are addressed by 32-bit offsets)
+    if (dm->nheads > (int64_t(1) << 22) / dm->headdim || dm->ngroups > (int64_t(1) << 21) / dm->dstate)
+        return fail(SSM_ERR_SHAPE, "nheads*headdim or 2*ngroups*dstate exceeds 2^22");
     if (dm->seqlen > kMaxTokens || dm->batch > kMaxTokens)
         return fail(SSM_ERR_SHAPE, "seqlen or batch exceeds 2^30");
     const int64_t row = row_of(dm);
@@ -74,41 +75,54 @@ ssm::sd_shape shape_of(const ssm_ssd_conv_dims *dm, int flags) {
     return s;
 }
 
-// The workspace of the forward: u, and in training the states entering the chunks.
+// The workspace of the forward: u, the tokens' decays, and in training the states entering the chunks.
 size_t u_bytes(const ssm_ssd_conv_dims *dm) { return align256((size_t)(dm->batch * dm->seqlen * row_of(dm)) * elem_size(dm)); }
+size_t tok_bytes(const ssm_ssd_conv_dims *dm) { return align256((size_t)(dm->batch * dm->nheads * chunks(dm) * ssm::kSdTok) * sizeof(float)); }
 size_t state_bytes(const ssm_ssd_conv_dims *dm) {
     return align256((size_t)(dm->batch * chunks(dm) * dm->nheads * dm->headdim * dm->dstate) * sizeof(float));
 }
 
-bool conv_grid(const ssm_ssd_conv_dims *dm, int tt, int64_t &vblocks, int64_t &tiles) {
-    vblocks = ceil_div(row_of(dm) / ssm::kSdConvV, 256);
-    tiles = std::max<int64_t>(ceil_div(dm->seqlen, tt), 1);
-    return dm->batch <= kMaxGrid / vblocks / tiles;
+// Tokens per thread of the convolution: 32 (a thread reads three rows more than it has), 8 where that leaves CUs
+// with less than four waves per SIMD.
+int conv_tokens(const ssm_ssd_conv_dims *dm) {
+    return dm->batch * dm->seqlen * (row_of(dm) / ssm::kSdConvV) >= (int64_t)32 * 64 * 4096 ? 32 : 8;
+}
+struct ConvGrid {
+    int64_t vblocks, tiles, blocks, quads;   // workgroups of the convolution: vblocks * tiles * batch; then the tokens'
+    bool fits() const { return blocks + quads <= kMaxGrid; }
+};
+ConvGrid conv_grid(const ssm_ssd_conv_dims *dm, int tt, bool tokens) {
+    ConvGrid g;
+    g.vblocks = ceil_div(row_of(dm) / ssm::kSdConvV, 256);
+    g.tiles = std::max<int64_t>(ceil_div(dm->seqlen, tt), 1);
+    g.blocks = g.vblocks * g.tiles * dm->batch;
+    g.quads = tokens ? dm->batch * chunks(dm) * ceil_div(dm->nheads, 4) : 0;
+    return g;
 }
 
+// u, the rows after the last token, and with `tok` the tokens' decays
 template <typename IO>
 void launch_conv(const void *x_, const float *w, const float *bias, const void *st_in, void *st_out, const int32_t *lens,
-                 void *u, const ssm_ssd_conv_dims *dm, int tt, hipStream_t st) {
+                 void *u, const void *dt, const float *A, const float *dt_bias, float *tok, const ssm_ssd_conv_dims *dm,
+                 int flags, hipStream_t st) {
     const int64_t stride = dm->xbc_stride ? dm->xbc_stride : row_of(dm);
-    int64_t vblocks, tiles;
-    conv_grid(dm, tt, vblocks, tiles);
+    const int tt = conv_tokens(dm);
+    const ConvGrid g = conv_grid(dm, tt, tok);
+    const ssm::sd_tok_args k = {dt, A, dt_bias, tok, dm->dt_stride ? dm->dt_stride : dm->nheads, chunks(dm), (int)dm->nheads,
+                                flags & SSM_SCAN_SOFTPLUS, (int)g.blocks};
     const bool al = aligned(x_, ssm::kSdConvV * sizeof(IO)) && stride % ssm::kSdConvV == 0;
     auto kern = al ? ssm::sd_conv_kernel<IO, true> : ssm::sd_conv_kernel<IO, false>;
-    hipLaunchKernelGGL(kern, dim3((unsigned)(vblocks * tiles * dm->batch)), dim3(256), 0, st, static_cast<const IO *>(x_),
-                       stride, w, bias, (int)dm->width, static_cast<const IO *>(st_in), static_cast<IO *>(st_out), lens,
-                       static_cast<IO *>(u), dm->seqlen, (int)row_of(dm), tt, (int)vblocks, (int)tiles);
+    hipLaunchKernelGGL(kern, dim3((unsigned)(g.blocks + g.quads)), dim3(256), 0, st, static_cast<const IO *>(x_), stride, w, bias,
+                       (int)dm->width, static_cast<const IO *>(st_in), static_cast<IO *>(st_out), lens, static_cast<IO *>(u),
+                       dm->seqlen, (int)row_of(dm), tt, (int)g.vblocks, (int)g.tiles, k);
 }
 
-constexpr int kConvTokens = 32;   // tokens per thread of the convolution
-
 template <typename E, int NT>
-void launch_scan(const void *u, const void *dt, const float *A, const float *D, const float *dt_bias, const int32_t *lens,
-                 const float *h0, void *y, float *last, float *ckpt, const ssm_ssd_conv_dims *dm, int flags, hipStream_t st) {
+void launch_scan(const void *u, const float *tok, const float *D, const int32_t *lens, const float *h0, void *y, float *last, float *ckpt, const ssm_ssd_conv_dims *dm, int flags, hipStream_t st) {
     using IO = typename ssm::sd<E>::io;
     const ssm::sd_shape s = shape_of(dm, flags);
     hipLaunchKernelGGL((ssm::sd_scan_kernel<E, NT>), dim3((unsigned)(dm->batch * s.H * s.PT)), dim3(ssm::kSdThreads), 0, st,
-                       static_cast<const IO *>(u), static_cast<const IO *>(dt), A, D, dt_bias, lens, h0,
-                       static_cast<IO *>(y), last, ckpt, s);
+                       static_cast<const IO *>(u), tok, D, lens, h0, static_cast<IO *>(y), last, ckpt, s);
 }
 
 template <typename IO>
@@ -128,7 +142,7 @@ constexpr int kConvBwdTokens = 64;   // tokens per thread of the convolution's b
 struct BwdPlan {
     int HS, hpw;
     int64_t tiles;
-    size_t u, states, adjoints, du, dbc, part, conv_part, bytes;   // offsets (u, states: without checkpoints)
+    size_t u, tok, states, adjoints, du, dbc, part, conv_part, bytes;   // offsets (u, tok, states: without checkpoints)
 };
 BwdPlan bwd_plan(const ssm_ssd_conv_dims *dm, bool have_checkpoints) {
     BwdPlan p;
@@ -146,6 +160,7 @@ BwdPlan bwd_plan(const ssm_ssd_conv_dims *dm, bool have_checkpoints) {
     };
     const size_t tokens = (size_t)(dm->batch * dm->seqlen);
     p.u = take(have_checkpoints ? 0 : u_bytes(dm));
+    p.tok = take(have_checkpoints ? 0 : tok_bytes(dm));
     p.states = take(have_checkpoints ? 0 : state_bytes(dm));
     p.adjoints = take(state_bytes(dm));
     p.du = take(tokens * dm->nheads * dm->headdim * 4);
@@ -157,23 +172,21 @@ BwdPlan bwd_plan(const ssm_ssd_conv_dims *dm, bool have_checkpoints) {
 }
 
 template <typename E, int NT, bool ADJ>
-void launch_walk(const void *u, const void *dy, const void *dt, const float *A, const float *dt_bias, const int32_t *lens,
-                 const float *from, float *each, float *to, const ssm_ssd_conv_dims *dm, int flags, hipStream_t st) {
+void launch_walk(const void *u, const void *dy, const float *tok, const int32_t *lens, const float *from, float *each, float *to, const ssm_ssd_conv_dims *dm, int flags, hipStream_t st) {
     using IO = typename ssm::sd<E>::io;
     const ssm::sd_shape s = shape_of(dm, flags);
     hipLaunchKernelGGL((ssm::sd_walk_kernel<E, NT, ADJ>), dim3((unsigned)(dm->batch * s.H * s.PT)), dim3(ssm::kSdThreads), 0, st,
-                       static_cast<const IO *>(u), static_cast<const IO *>(dy), static_cast<const IO *>(dt), A, dt_bias, lens,
-                       from, each, to, s);
+                       static_cast<const IO *>(u), static_cast<const IO *>(dy), tok, lens, from, each, to, s);
 }
 
 template <typename E, int NT>
-void launch_bwd(const void *u, const void *dy, const void *dt, const float *A, const float *D, const float *dt_bias,
+void launch_bwd(const void *u, const void *dy, const float *tok, const void *dt, const float *A, const float *D, const float *dt_bias,
                 const int32_t *lens, const float *states, const float *adjoints, void *ddt, const ssm::sd_grad &g,
                 const ssm_ssd_conv_dims *dm, int flags, hipStream_t st) {
     using IO = typename ssm::sd<E>::io;
     const ssm::sd_shape s = shape_of(dm, flags);
     hipLaunchKernelGGL((ssm::sd_bwd_kernel<E, NT>), dim3((unsigned)(dm->batch * s.nchunk * s.G * g.HS)), dim3(ssm::kSdThreads), 0, st,
-                       static_cast<const IO *>(u), static_cast<const IO *>(dy), static_cast<const IO *>(dt), A, D, dt_bias, lens,
+                       static_cast<const IO *>(u), static_cast<const IO *>(dy), tok, static_cast<const IO *>(dt), A, D, dt_bias, lens,
                        states, adjoints, static_cast<IO *>(ddt), g, s);
 }
 
@@ -181,14 +194,13 @@ template <typename IO>
 void launch_conv_bwd(const void *x_, const float *w, const float *bias, const void *st_in, const int32_t *lens, const float *du,
                      const float *dbc, int HS, void *dx, void *dst, float *parts, const ssm_ssd_conv_dims *dm, hipStream_t st) {
     const int64_t stride = dm->xbc_stride ? dm->xbc_stride : row_of(dm);
-    int64_t vblocks, tiles;
-    conv_grid(dm, kConvBwdTokens, vblocks, tiles);
+    const ConvGrid g = conv_grid(dm, kConvBwdTokens, false);
     const bool al = aligned(x_, ssm::kSdConvV * sizeof(IO)) && stride % ssm::kSdConvV == 0;
     auto kern = al ? ssm::sd_conv_bwd_kernel<IO, true> : ssm::sd_conv_bwd_kernel<IO, false>;
-    hipLaunchKernelGGL(kern, dim3((unsigned)(vblocks * tiles * dm->batch)), dim3(256), 0, st, static_cast<const IO *>(x_), stride,
-                       w, bias, (int)dm->width, static_cast<const IO *>(st_in), lens, du, dbc, HS, static_cast<IO *>(dx),
+    hipLaunchKernelGGL(kern, dim3((unsigned)g.blocks), dim3(256), 0, st, static_cast<const IO *>(x_), stride, w, bias,
+                       (int)dm->width, static_cast<const IO *>(st_in), lens, du, dbc, HS, static_cast<IO *>(dx),
                        static_cast<IO *>(dst), parts, dm->batch, dm->seqlen, (int)row_of(dm), (int)(dm->nheads * dm->headdim),
-                       kConvBwdTokens, (int)vblocks, (int)tiles);
+                       kConvBwdTokens, (int)g.vblocks, (int)g.tiles);
 }
 
 void launch_sums(const float *part, int64_t n, int cols, int planes, const ssm::sd_sums &o, hipStream_t st) {
@@ -210,7 +222,7 @@ extern "C" {
 
 size_t ssm_ssd_conv_workspace_bytes(const ssm_ssd_conv_dims *dims, int flags) {
     if (check_dims(dims) != SSM_OK || dims->batch == 0 || dims->nheads == 0) return 0;
-    return u_bytes(dims) + ((flags & SSM_SCAN_CHECKPOINTS) ? state_bytes(dims) : 0);
+    return u_bytes(dims) + tok_bytes(dims) + ((flags & SSM_SCAN_CHECKPOINTS) ? state_bytes(dims) : 0);
 }
 
 int ssm_ssd_conv_fwd(const void *xbc, const float *conv_w, const float *conv_b, const void *conv_state, const void *dt,
@@ -232,19 +244,15 @@ int ssm_ssd_conv_fwd(const void *xbc, const float *conv_w, const float *conv_b, 
     if (dims->seqlen > 0 && (!xbc || !dt || !y)) return fail(SSM_ERR_NULL, "xbc, dt or y is NULL");
     rc = check_workspace(workspace, workspace_bytes, ssm_ssd_conv_workspace_bytes(dims, flags));
     if (rc != SSM_OK) return rc;
-    int64_t vblocks, tiles;
-    if (!conv_grid(dims, kConvTokens, vblocks, tiles)) return fail(SSM_ERR_SHAPE, "batch*seqlen exceeds the grid of the convolution");
+    if (!conv_grid(dims, conv_tokens(dims), true).fits()) return fail(SSM_ERR_SHAPE, "batch*seqlen exceeds the grid of the convolution");
     hipStream_t st = static_cast<hipStream_t>(stream);
-    float *ckpt = (flags & SSM_SCAN_CHECKPOINTS) ? reinterpret_cast<float *>(static_cast<char *>(workspace) + u_bytes(dims)) : nullptr;
-    if (es == 2) {
-        launch_conv<uint16_t>(xbc, conv_w, conv_b, conv_state, conv_state_out, seq_lens, workspace, dims, kConvTokens, st);
-        auto f = dims->dstate <= 64 ? launch_scan<__bf16, 64> : launch_scan<__bf16, 128>;
-        f(workspace, dt, A, D, dt_bias, seq_lens, initial_state, y, last_state, ckpt, dims, flags, st);
-    } else {
-        launch_conv<float>(xbc, conv_w, conv_b, conv_state, conv_state_out, seq_lens, workspace, dims, kConvTokens, st);
-        auto f = dims->dstate <= 64 ? launch_scan<float, 64> : launch_scan<float, 128>;
-        f(workspace, dt, A, D, dt_bias, seq_lens, initial_state, y, last_state, ckpt, dims, flags, st);
-    }
+    float *tok = reinterpret_cast<float *>(static_cast<char *>(workspace) + u_bytes(dims));
+    float *ckpt = (flags & SSM_SCAN_CHECKPOINTS) ? tok + tok_bytes(dims) / sizeof(float) : nullptr;
+    const bool bf = es == 2, wide = dims->dstate > 64;
+    auto conv = bf ? launch_conv<uint16_t> : launch_conv<float>;
+    conv(xbc, conv_w, conv_b, conv_state, conv_state_out, seq_lens, workspace, dt, A, dt_bias, tok, dims, flags, st);
+    auto scan = bf ? wide ? launch_scan<__bf16, 128> : launch_scan<__bf16, 64> : wide ? launch_scan<float, 128> : launch_scan<float, 64>;
+    scan(workspace, tok, D, seq_lens, initial_state, y, last_state, ckpt, dims, flags, st);
     return launched();
 }
 
@@ -284,31 +292,31 @@ int ssm_ssd_conv_bwd(const void *xbc, const float *conv_w, const float *conv_b, 
     rc = check_workspace(workspace, workspace_bytes, ssm_ssd_conv_bwd_workspace_bytes(dims, flags));
     if (rc != SSM_OK) return rc;
     const BwdPlan p = bwd_plan(dims, kept);
-    int64_t vblocks, tiles;
-    if (!conv_grid(dims, kConvTokens, vblocks, tiles) || dims->batch * chunks(dims) > kMaxGrid / dims->ngroups / p.HS)
+    if (!conv_grid(dims, 8, true).fits() || dims->batch * chunks(dims) > kMaxGrid / dims->ngroups / p.HS)
         return fail(SSM_ERR_SHAPE, "batch*seqlen exceeds the grids of the backward");
     hipStream_t st = static_cast<hipStream_t>(stream);
     char *ws = static_cast<char *>(workspace);
     auto at = [&](size_t o) { return reinterpret_cast<float *>(ws + o); };
     const char *ck = static_cast<const char *>(checkpoints);
     const void *u = kept ? ck : ws + p.u;
-    const float *states = kept ? reinterpret_cast<const float *>(ck + u_bytes(dims)) : at(p.states);
+    const float *tok = kept ? reinterpret_cast<const float *>(ck + u_bytes(dims)) : at(p.tok);
+    const float *states = kept ? tok + tok_bytes(dims) / sizeof(float) : at(p.states);
     const bool bf = es == 2, wide = dims->dstate > 64;
     if (dims->batch > 0) {
         if (!kept) {
-            if (bf) launch_conv<uint16_t>(xbc, conv_w, conv_b, conv_state, nullptr, seq_lens, ws + p.u, dims, kConvTokens, st);
-            else launch_conv<float>(xbc, conv_w, conv_b, conv_state, nullptr, seq_lens, ws + p.u, dims, kConvTokens, st);
+            auto conv = bf ? launch_conv<uint16_t> : launch_conv<float>;
+            conv(xbc, conv_w, conv_b, conv_state, nullptr, seq_lens, ws + p.u, dt, A, dt_bias, at(p.tok), dims, flags, st);
             auto f = bf ? wide ? launch_walk<__bf16, 128, false> : launch_walk<__bf16, 64, false>
                         : wide ? launch_walk<float, 128, false> : launch_walk<float, 64, false>;
-            f(u, nullptr, dt, A, dt_bias, seq_lens, initial_state, at(p.states), nullptr, dims, flags, st);
+            f(u, nullptr, tok, seq_lens, initial_state, at(p.states), nullptr, dims, flags, st);
         }
         auto f = bf ? wide ? launch_walk<__bf16, 128, true> : launch_walk<__bf16, 64, true>
                     : wide ? launch_walk<float, 128, true> : launch_walk<float, 64, true>;
-        f(u, dy, dt, A, dt_bias, seq_lens, dlast_state, at(p.adjoints), dinitial_state, dims, flags, st);
+        f(u, dy, tok, seq_lens, dlast_state, at(p.adjoints), dinitial_state, dims, flags, st);
         if (dims->seqlen > 0) {
             const ssm::sd_grad g = {at(p.du), at(p.dbc), at(p.part), p.HS, p.hpw};
             auto k = bf ? wide ? launch_bwd<__bf16, 128> : launch_bwd<__bf16, 64> : wide ? launch_bwd<float, 128> : launch_bwd<float, 64>;
-            k(u, dy, dt, A, D, dt_bias, seq_lens, states, at(p.adjoints), ddt, g, dims, flags, st);
+            k(u, dy, tok, dt, A, D, dt_bias, seq_lens, states, at(p.adjoints), ddt, g, dims, flags, st);
         }
         auto c = bf ? launch_conv_bwd<uint16_t> : launch_conv_bwd<float>;
         c(xbc, conv_w, conv_b, conv_state, seq_lens, at(p.du), at(p.dbc), p.HS, dxbc, dconv_state, at(p.conv_part), dims, st);
@@ -353,13 +361,14 @@ int ssm_ssd_conv_step(float *state, void *conv_state, const void *xbc, const flo
     hipStream_t st = static_cast<hipStream_t>(stream);
     ssm_ssd_conv_dims one = *dims;
     one.seqlen = 1;
-    int64_t vblocks, tiles;
-    if (!conv_grid(&one, kConvTokens, vblocks, tiles)) return fail(SSM_ERR_SHAPE, "batch exceeds the grid of the convolution");
+    if (!conv_grid(&one, conv_tokens(&one), false).fits()) return fail(SSM_ERR_SHAPE, "batch exceeds the grid of the convolution");
     if (es == 2) {
-        launch_conv<uint16_t>(xbc, conv_w, conv_b, conv_state, conv_state, nullptr, workspace, &one, kConvTokens, st);
+        launch_conv<uint16_t>(xbc, conv_w, conv_b, conv_state, conv_state, nullptr, workspace, nullptr, nullptr, nullptr, nullptr,
+                              &one, 0, st);
         launch_step<uint16_t>(state, workspace, dt, A, D, dt_bias, y, &one, flags, st);
     } else {
-        launch_conv<float>(xbc, conv_w, conv_b, conv_state, conv_state, nullptr, workspace, &one, kConvTokens, st);
+        launch_conv<float>(xbc, conv_w, conv_b, conv_state, conv_state, nullptr, workspace, nullptr, nullptr, nullptr, nullptr, &one,
+                           0, st);
         launch_step<float>(state, workspace, dt, A, D, dt_bias, y, &one, flags, st);
     }
     return launched();

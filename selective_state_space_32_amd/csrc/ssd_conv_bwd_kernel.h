@@ -26,8 +26,7 @@ namespace ssm {
 template <typename E, int NT, bool ADJ>
 __global__ void __launch_bounds__(kSdThreads)
 sd_walk_kernel(const typename sd<E>::io *__restrict__ u_, const typename sd<E>::io *__restrict__ dy_,
-               const typename sd<E>::io *__restrict__ dt, const float *__restrict__ A, const float *__restrict__ dt_bias,
-               const int32_t *__restrict__ lens, const float *__restrict__ from, float *__restrict__ each,
+               const float *__restrict__ tok, const int32_t *__restrict__ lens, const float *__restrict__ from, float *__restrict__ each,
                float *__restrict__ to, sd_shape s) {
     using IO = typename sd<E>::io;
     using F = typename sd<E>::frag;
@@ -39,12 +38,11 @@ sd_walk_kernel(const typename sd<E>::io *__restrict__ u_, const typename sd<E>::
     const int pt = blockIdx.x % s.PT, h = blockIdx.x / s.PT % s.H;
     const int64_t b = blockIdx.x / s.PT / s.H;
     const sd_view<IO> v(u_, s, b, h, pt);
-    const int64_t xrow = ADJ ? (int64_t)s.H * s.P : s.dc;
+    const int xrow = ADJ ? s.H * s.P : s.dc;
     const E *xs = reinterpret_cast<const E *>(ADJ ? dy_ + (b * s.L * s.H + h) * s.P + pt * 64 : v.x);
     const E *Bs = reinterpret_cast<const E *>(ADJ ? v.C : v.B);
     const int64_t len = lens ? min(max((int64_t)lens[b], (int64_t)0), s.L) : s.L;
-    const float a2 = A[h] * kLog2e, bias = dt_bias ? dt_bias[h] : 0.0f;
-    const IO *dtp = dt + b * s.L * s.dt_stride + h;
+    tok += (b * s.H + h) * s.nchunk * kSdTok;
     const int64_t st_at = (b * s.H + h) * s.P * s.N + (int64_t)pt * 64 * s.N;
     f32x4_t S[NB];
     if (from) {
@@ -61,20 +59,20 @@ sd_walk_kernel(const typename sd<E>::io *__restrict__ u_, const typename sd<E>::
         for (int64_t c = live; c < s.nchunk; ++c) keep(c);
     tile64<E, NT> rB;
     tile64<E, 64> rX;
-    float rdt = 0.0f, sig;
+    sd_tok rt = {};
     auto fetch = [&](int64_t c) {
         const int64_t t0 = c * kSdQ;
         const int rows = (int)min((int64_t)64, len - t0);
         rB.load(Bs + t0 * s.dc, s.dc, rows, s.N);
-        rX.load(xs + t0 * xrow, xrow, rows, v.pw);
-        if (w == 0) rdt = sd_dt(dtp, s.dt_stride, t0, len, bias, s.softplus, lane, sig);
+        rX.load(xs + t0 * xrow, (uint32_t)xrow, rows, v.pw);
+        if (w == 0) rt = sd_load_tokens(tok + c * kSdTok, lane);
     };
     if (live > 0) fetch(ADJ ? live - 1 : 0);
     for (int64_t i = 0; i < live; ++i) {
         const int64_t c = ADJ ? live - 1 - i : i;
         rB.stage(tB);
         rX.stage(tX);
-        if (w == 0) sd_form_tokens(tk, rdt, a2, lane);
+        if (w == 0) sd_stage_tokens(tk, rt, lane);
         if (i + 1 < live) fetch(ADJ ? c - 1 : c + 1);
         keep(c);
         __syncthreads();
@@ -86,8 +84,18 @@ sd_walk_kernel(const typename sd<E>::io *__restrict__ u_, const typename sd<E>::
             const F x0 = ld_col<E, 64>(tX, 16 * k, 16 * w, lane), x1 = ld_col<E, 64>(tX, 16 * k + 16, 16 * w, lane);
             const formed<E, 3> f0(widen(x0) * ld4(wt)), f1(widen(x1) * ld4(wt + 16));
 #pragma unroll
-            for (int nb = 0; nb < NB; ++nb)
-                S[nb] = mma_fb<E, 3>(ld_col<E, NT>(tB, 16 * k, 16 * nb, lane), ld_col<E, NT>(tB, 16 * k + 16, 16 * nb, lane), f0, f1, S[nb]);
+            for (int n0 = 0; n0 < NB; n0 += 4) {
+                F b0[4], b1[4];
+#pragma unroll
+                for (int nb = 0; nb < 4; ++nb) {
+                    b0[nb] = ld_col<E, NT>(tB, 16 * k, 16 * (n0 + nb), lane);
+                    b1[nb] = ld_col<E, NT>(tB, 16 * k + 16, 16 * (n0 + nb), lane);
+                }
+#pragma unroll
+                for (int m = 0; m < formed<E, 3>::N; ++m)
+#pragma unroll
+                    for (int nb = 0; nb < 4; ++nb) S[n0 + nb] = mma(b0[nb], b1[nb], f0.p[m], f1.p[m], S[n0 + nb]);
+            }
         }
         __syncthreads();
     }
@@ -126,6 +134,12 @@ template <typename E, int NS> struct state64 {
         return a;
     }
 };
+__device__ __forceinline__ double wave_last(double v) {
+    const uint64_t b = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = __builtin_amdgcn_readlane((int)(uint32_t)b, 63), hi = __builtin_amdgcn_readlane((int)(uint32_t)(b >> 32), 63);
+    return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+
 // sum over the four 16-lane rows of a wave, in every lane
 __device__ __forceinline__ float quads_sum(float v) {
     v += __shfl_xor(v, 16, 64);
@@ -144,8 +158,9 @@ struct sd_grad {
 template <typename E, int NT>
 __global__ void __launch_bounds__(kSdThreads)
 sd_bwd_kernel(const typename sd<E>::io *__restrict__ u_, const typename sd<E>::io *__restrict__ dy_,
-              const typename sd<E>::io *__restrict__ dt, const float *__restrict__ A, const float *__restrict__ Dv,
-              const float *__restrict__ dt_bias, const int32_t *__restrict__ lens, const float *__restrict__ st_in,
+              const float *__restrict__ tok, const typename sd<E>::io *__restrict__ dt, const float *__restrict__ A,
+              const float *__restrict__ Dv, const float *__restrict__ dt_bias, const int32_t *__restrict__ lens,
+              const float *__restrict__ st_in,
               const float *__restrict__ ds_out, typename sd<E>::io *__restrict__ ddt, sd_grad gr, sd_shape s) {
     using IO = typename sd<E>::io;
     using F = typename sd<E>::frag;
@@ -198,14 +213,18 @@ sd_bwd_kernel(const typename sd<E>::io *__restrict__ u_, const typename sd<E>::i
                 if (nh == 0) {
                     tile64<E, 64> rX, rY;
                     rX.load(reinterpret_cast<const E *>(ub + h * s.P + pt * 64), s.dc, rows, pw);
-                    rY.load(reinterpret_cast<const E *>(dyb + h * s.P + pt * 64), (int64_t)s.H * s.P, rows, pw);
+                    rY.load(reinterpret_cast<const E *>(dyb + h * s.P + pt * 64), (uint32_t)(s.H * s.P), rows, pw);
                     rX.stage(tX);
                     rY.stage(tY);
                     if (pt == 0 && w == 0) {
-                        rdt = sd_dt(dt + b * s.L * s.dt_stride + h, s.dt_stride, t0, len, dt_bias ? dt_bias[h] : 0.0f, s.softplus, lane, sig);
-                        sd_form_tokens(tk, rdt, a * kLog2e, lane);
-                        const double c = (double)tk.ch[lane] + tk.cl[lane];
-                        to_end[lane] = hw_exp2((float)(wave_last(c) - c));
+                        const sd_tok rt = sd_load_tokens(tok + ((b * s.H + h) * s.nchunk + chunk) * kSdTok, lane);
+                        to_end[lane] = sd_stage_tokens(tk, rt, lane);
+                        rdt = rt.d;
+                        sig = 0.0f;
+                        if (lane < rows) {
+                            sig = 1.0f;
+                            if (s.softplus) softplus_f32(io<IO>::ld(dt, (b * s.L + t0 + lane) * s.dt_stride + h) + (dt_bias ? dt_bias[h] : 0.0f), sig);
+                        }
                     }
                 }
                 state64<E, 2> rS, rD;

@@ -120,28 +120,35 @@ __device__ __forceinline__ f32x4_t widen(f32x4_t v) { return v; }
 
 // ---- tiles ----------------------------------------------------------------------------------
 
-// 64 rows (tokens) of W elements between memory and LDS, 16 bytes per thread and access.
+// 64 rows (tokens) of W elements between memory and LDS, 16 bytes per thread and access.  Addresses are a
+// uniform base and a 32-bit offset per lane (64 rows of at most 2^25 elements of 4 bytes).
 template <typename E, int W> struct tile64 {
     static constexpr int EPU = 16 / (int)sizeof(E);           // elements per unit
     static constexpr int UPR = W / EPU;                       // units per row
     static constexpr int NU = 64 * UPR / kSdThreads;          // units per thread
+    static constexpr int RPP = kSdThreads / UPR;              // rows per pass
     static_assert(64 * UPR % kSdThreads == 0, "whole units per thread");
     u32x4_t r[NU];
     // rows [0, rows) of `src` (elements `stride` apart), columns [0, cols); zeros elsewhere
-    __device__ __forceinline__ void load(const E *src, int64_t stride, int rows, int cols) {
+    __device__ __forceinline__ void load(const E *src, uint32_t stride, int rows, int cols) {
+        const int row = threadIdx.x / UPR, c = threadIdx.x % UPR * EPU;
+        const uint32_t off = ((uint32_t)row * stride + (uint32_t)c) * (uint32_t)sizeof(E), step = RPP * stride * (uint32_t)sizeof(E);
+        const char *base = reinterpret_cast<const char *>(src);
+        if (rows >= 64 && cols >= W) {
 #pragma unroll
-        for (int i = 0; i < NU; ++i) {
-            const int id = threadIdx.x + kSdThreads * i, row = id / UPR, c = (id % UPR) * EPU;
-            r[i] = u32x4_t{0u, 0u, 0u, 0u};
-            if (row < rows && c < cols) r[i] = *reinterpret_cast<const u32x4_t *>(src + row * stride + c);
+            for (int i = 0; i < NU; ++i) r[i] = *reinterpret_cast<const u32x4_t *>(base + (off + i * step));
+        } else {
+#pragma unroll
+            for (int i = 0; i < NU; ++i) {
+                r[i] = u32x4_t{0u, 0u, 0u, 0u};
+                if (row + RPP * i < rows && c < cols) r[i] = *reinterpret_cast<const u32x4_t *>(base + (off + i * step));
+            }
         }
     }
     __device__ __forceinline__ void stage(E *t) const {
+        const int row = threadIdx.x / UPR, c = threadIdx.x % UPR * EPU;
 #pragma unroll
-        for (int i = 0; i < NU; ++i) {
-            const int id = threadIdx.x + kSdThreads * i, row = id / UPR, c = (id % UPR) * EPU;
-            *reinterpret_cast<u32x4_t *>(t + row * sd_ld<E>(W) + c) = r[i];
-        }
+        for (int i = 0; i < NU; ++i) *reinterpret_cast<u32x4_t *>(t + (row + RPP * i) * sd_ld<E>(W) + c) = r[i];
     }
 };
 
@@ -163,62 +170,77 @@ __device__ __forceinline__ double wave_incl_sum64(double v) {
     v += moved(v, integral_constant<int, 0x143>{}, integral_constant<int, 0xc>{});
     return v;
 }
-__device__ __forceinline__ double wave_last(double v) {
-    const uint64_t b = __builtin_bit_cast(uint64_t, v);
-    const uint32_t lo = __builtin_amdgcn_readlane((int)(uint32_t)b, 63), hi = __builtin_amdgcn_readlane((int)(uint32_t)(b >> 32), 63);
-    return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+// A chunk's per-token values.  c_t = log2 e^{g_0 + .. + g_t}, as a float and what it lacks; formed once for every
+// (sequence, head, chunk) and kept as [3][64]: c's two floats, dt (0 past the sequence's end).
+constexpr int kSdTok = 3 * kSdQ;
+template <typename IO>
+__device__ __forceinline__ void sd_write_tokens(float *o, const IO *dt, int64_t stride, int64_t t0, int64_t len, float bias,
+                                                int softplus, float a2, int lane) {   // one wave, token = lane
+    float d = 0.0f;
+    if (t0 + lane < len) {
+        d = io<IO>::ld(dt, (t0 + lane) * stride) + bias;
+        if (softplus) d = softplus_f32(d);
+    }
+    const double c = wave_incl_sum64((double)(a2 * d));
+    const float ch = (float)c;
+    o[lane] = ch;
+    o[kSdQ + lane] = (float)(c - (double)ch);
+    o[2 * kSdQ + lane] = d;
 }
-
-// A chunk's per-token values, formed by one wave (token = lane).  c: in log2 units, as a float and
-// what it lacks.
+// In LDS, with what follows from them.
 struct sd_tokens {
-    float ch[kSdQ], cl[kSdQ];   // c_t
-    float dt[kSdQ];             // 0 past the sequence's end
+    float ch[kSdQ], cl[kSdQ];
+    float dt[kSdQ];
     float w[kSdQ];              // e^{c_last - c_t} dt_t
     float e[kSdQ];              // e^{c_t}
     float dec, pad[3];          // e^{c_last}
 };
-// dt of token `lane` of the chunk at t0 (0 at and past `len`); sig: softplus's derivative (1 without it)
-template <typename IO>
-__device__ __forceinline__ float sd_dt(const IO *dt, int64_t stride, int64_t t0, int64_t len, float bias, int softplus,
-                                       int lane, float &sig) {
-    sig = 0.0f;
-    if (t0 + lane >= len) return 0.0f;
-    const float v = io<IO>::ld(dt, (t0 + lane) * stride) + bias;
-    sig = 1.0f;
-    return softplus ? softplus_f32(v, sig) : v;
-}
-__device__ __forceinline__ void sd_form_tokens(sd_tokens &s, float dt, float a2, int lane) {
-    const double c = wave_incl_sum64((double)(a2 * dt)), tot = wave_last(c);
-    const float ch = (float)c;
-    s.ch[lane] = ch;
-    s.cl[lane] = (float)(c - (double)ch);
-    s.dt[lane] = dt;
-    s.w[lane] = hw_exp2((float)(tot - c)) * dt;
-    s.e[lane] = hw_exp2((float)c);
-    if (lane == 0) s.dec = hw_exp2((float)tot);
+struct sd_tok { float h, l, d; };   // a lane's token
+__device__ __forceinline__ sd_tok sd_load_tokens(const float *o, int lane) { return {o[lane], o[kSdQ + lane], o[2 * kSdQ + lane]}; }
+__device__ __forceinline__ float sd_stage_tokens(sd_tokens &s, sd_tok v, int lane) {   // one wave; e^{c_last - c_t}
+    auto last = [](float x) { return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(x), kSdQ - 1)); };
+    const float th = last(v.h), tl = last(v.l), r = hw_exp2((th - v.h) + (tl - v.l));
+    s.ch[lane] = v.h;
+    s.cl[lane] = v.l;
+    s.dt[lane] = v.d;
+    s.w[lane] = r * v.d;
+    s.e[lane] = hw_exp2(v.h + v.l);
+    if (lane == 0) s.dec = hw_exp2(th + tl);
+    return r;
 }
 __device__ __forceinline__ f32x4_t ld4(const float *p) { return *reinterpret_cast<const f32x4_t *>(p); }
 
 // ---- the convolution ------------------------------------------------------------------------
 
-// v sigmoid(v) rounded to fp32 and then to bf16, as the exact value would be: u is rounded in the middle of the
-// path, and every kernel that forms it has to form the same one.  v comes in 64 bits; the fp32 value is off by at most
-// 8 + 3 |v| of its last places, and only where a border between two bf16 values is that near (one value in
-// a thousand) is it formed in 64 bits.
-__device__ __forceinline__ uint16_t silu_bf16(double v64) {
-    const float v = (float)v64, av = fabsf(v);
+// u is rounded in the middle of the path, and every kernel that forms it has to form the same one: the exact value
+// rounded to fp32 and then to bf16.  The fp32 value u = silu(v) that conv_silu returns, with v from four products whose
+// absolute sum (and the bias's) is `size`, is off by at most
+//   1.1 * 4 * 2^-24 size           (v's roundings; silu's slope is below 1.1)
+//   (7 + 2.2 |v|) 2^-24 |u|        (the exponent's roundings, where v < 0; the exponential and the reciprocal, 2 each; a sum,
+//                                   a product and v itself, 1 each)
+// and `near` says whether a border between two bf16 values is that near (one value in two thousand): then it is formed
+// again in 64 bits.
+__device__ __forceinline__ float conv_silu(float v, float size, bool &near) {
     const float u = silu_f32(v);
-    const float off = fabsf((float)(int)(__float_as_uint(u) & 0xffffu) - 32768.0f);
-    if (off <= fmaf(av, 4.0f, 12.0f) || av > 64.0f) return f32_to_bf16((float)(v64 / (1.0 + exp(-v64))));
-    return f32_to_bf16(u);
+    const float border = __uint_as_float((__float_as_uint(u) & 0xffff0000u) | 0x8000u);
+    const float rel = fmaf(fmaxf(-v, 0.0f), 2.5f, 8.0f) * 0x1p-24f;
+    // (not "<=", so that a NaN is near; a large negative v too, whose exponential leaves fp32)
+    near = !(fabsf(u - border) > fmaf(size, 5.0f * 0x1p-24f, rel * fabsf(u))) || v < -64.0f;
+    return u;
+}
+
+// (The second rounding on the bits: conversions in a row would be taken as one.)
+__device__ __forceinline__ uint16_t silu_bf16_64(double v) {
+    const uint32_t b = __float_as_uint((float)(v / (1.0 + exp(-v))));
+    if ((b & 0x7fffffffu) > 0x7f800000u) return (uint16_t)(b >> 16 | 0x40u);   // NaN
+    return (uint16_t)((b + 0x7fffu + (b >> 16 & 1u)) >> 16);
 }
 
 // kSdConvV channels of a row, as raw words; rows of a projected tensor start anywhere (aligned: 4 elements).
 template <typename IO, bool AL> struct conv_vec {
     __device__ __forceinline__ static void load(const IO *p, IO (&v)[kSdConvV]) {
         if constexpr (AL) {
-            typedef uint32_t words __attribute__((ext_vector_type(sizeof(IO))));
+            typedef uint32_t words __attribute__((ext_vector_type(sizeof(IO)), may_alias));
             const words w = *reinterpret_cast<const words *>(p);
             __builtin_memcpy(v, &w, sizeof w);
         } else {
@@ -228,7 +250,7 @@ template <typename IO, bool AL> struct conv_vec {
     }
     __device__ __forceinline__ static void store(IO *p, const IO (&v)[kSdConvV]) {
         if constexpr (AL) {
-            typedef uint32_t words __attribute__((ext_vector_type(sizeof(IO))));
+            typedef uint32_t words __attribute__((ext_vector_type(sizeof(IO)), may_alias));
             words w;
             __builtin_memcpy(&w, v, sizeof w);
             *reinterpret_cast<words *>(p) = w;
@@ -243,15 +265,36 @@ template <typename IO> __device__ __forceinline__ float io_f32(IO v) {
     else return v;
 }
 
+// What a forward's first launch does besides the convolution: the tokens' step sizes and decays.
+struct sd_tok_args {
+    const void *dt;
+    const float *A, *bias;
+    float *tok;             // [b][h][chunk][3][64]
+    int64_t stride, nchunk;
+    int H, softplus, first; // first: the workgroup that starts with them (four heads of a chunk each)
+};
+
 // u[b][t][c] = silu(bias + sum_k w[c][k] row_{t - (W-1) + k}), zero at and past a sequence's length; thread:
-// kSdConvV channels of `tt` tokens.  A row before token 0 comes from st_in (zero without it).  The thread of
-// the first tokens also writes the W - 1 rows before token len (st_out may be st_in).
-// w4: the taps at [c][4], the oldest first, zeros in front (W < 4 taps).
+// kSdConvV channels of `tt` tokens, kSdConvT at a time, the next ones' rows requested before.  A row before token 0 comes
+// from st_in (zero without it).  The thread of the first tokens also writes the W - 1 rows before token len
+// (st_out may be st_in: nothing else reads it, as tt >= 3).  Taps short of four count as zeros in front.
+constexpr int kSdConvT = 4;
 template <typename IO, bool AL>
 __global__ void __launch_bounds__(256)
 sd_conv_kernel(const IO *__restrict__ x, int64_t xstride, const float *__restrict__ w, const float *__restrict__ bias,
                int width, const IO *st_in, IO *st_out, const int32_t *__restrict__ lens, IO *__restrict__ u, int64_t L,
-               int dc, int tt, int vblocks, int ntiles) {
+               int dc, int tt, int vblocks, int ntiles, sd_tok_args k) {
+    if ((int)blockIdx.x >= k.first) {
+        const int lane = threadIdx.x & 63, quads = (k.H + 3) / 4;
+        const int64_t item = blockIdx.x - k.first;
+        const int h = (int)(item % quads) * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+        const int64_t c = item / quads % k.nchunk, b = item / quads / k.nchunk;
+        if (h >= k.H) return;
+        const int64_t len = lens ? min(max((int64_t)lens[b], (int64_t)0), L) : L;
+        sd_write_tokens(k.tok + ((b * k.H + h) * k.nchunk + c) * kSdTok, static_cast<const IO *>(k.dt) + b * L * k.stride + h,
+                        k.stride, c * kSdQ, len, k.bias ? k.bias[h] : 0.0f, k.softplus, k.A[h] * kLog2e, lane);
+        return;
+    }
     const int v = blockIdx.x % vblocks * 256 + threadIdx.x;
     if (v >= dc / kSdConvV) return;
     const int c = v * kSdConvV;
@@ -264,27 +307,77 @@ sd_conv_kernel(const IO *__restrict__ x, int64_t xstride, const float *__restric
         if (t >= 0) conv_vec<IO, AL>::load(xb + t * xstride, o);
         else if (st_in && t >= -h) conv_vec<IO, true>::load(st_in + (b * h + h + t) * dc + c, o);
         else
-            for (int k = 0; k < kSdConvV; ++k) o[k] = 0;
+            for (int i = 0; i < kSdConvV; ++i) o[i] = 0;
     };
-    using acc_t = std::conditional_t<sizeof(IO) == 2, double, float>;
-    acc_t wv[kSdConvV][kSdTaps], bv[kSdConvV], past[kSdTaps - 1][kSdConvV];
+    IO r[kSdConvT][kSdConvV] = {};
+    auto fetch = [&](int64_t t) {
 #pragma unroll
-    for (int k = 0; k < kSdConvV; ++k) {
+        for (int i = 0; i < kSdConvT; ++i)
+            if (t + i < min(t1, len)) conv_vec<IO, AL>::load(xb + (t + i) * xstride, r[i]);
+    };
+    fetch(t0);
+    float wv[kSdTaps][kSdConvV], bv[kSdConvV], past[kSdTaps - 1][kSdConvV];
+#pragma unroll
+    for (int i = 0; i < kSdConvV; ++i) {
 #pragma unroll
         for (int j = 0; j < kSdTaps; ++j) {
             const int tap = j - (kSdTaps - width);
-            wv[k][j] = tap >= 0 ? (acc_t)w[(int64_t)(c + k) * width + tap] : (acc_t)0;
+            wv[j][i] = tap >= 0 ? w[(int64_t)(c + i) * width + tap] : 0.0f;
         }
-        bv[k] = bias ? (acc_t)bias[c + k] : (acc_t)0;
+        bv[i] = bias ? bias[c + i] : 0.0f;
     }
 #pragma unroll
     for (int j = 0; j < kSdTaps - 1; ++j) {
-        IO r[kSdConvV];
-        row(t0 - 3 + j, r);
+        IO o[kSdConvV];
+        row(t0 - 3 + j, o);
 #pragma unroll
-        for (int k = 0; k < kSdConvV; ++k) past[j][k] = (acc_t)io_f32(r[k]);
+        for (int i = 0; i < kSdConvV; ++i) past[j][i] = io_f32(o[i]);
     }
-    if (st_out && t0 == 0) {
+    for (int64_t t = t0; t < t1; t += kSdConvT) {
+        IO now[kSdConvT][kSdConvV];
+#pragma unroll
+        for (int i = 0; i < kSdConvT; ++i)
+#pragma unroll
+            for (int e = 0; e < kSdConvV; ++e) now[i][e] = r[i][e];
+        fetch(t + kSdConvT);
+#pragma unroll
+        for (int i = 0; i < kSdConvT; ++i) {
+            if (t + i >= t1) break;
+            IO o[kSdConvV];
+#pragma unroll
+            for (int e = 0; e < kSdConvV; ++e) {
+                const float last = io_f32(now[i][e]);
+                float p = fmaf(wv[0][e], past[0][e], bv[e]);
+                p = fmaf(wv[1][e], past[1][e], p);
+                p = fmaf(wv[2][e], past[2][e], p);
+                p = fmaf(wv[3][e], last, p);
+                if constexpr (sizeof(IO) == 2) {
+                    float size = fmaf(fabsf(wv[0][e]), fabsf(past[0][e]), fabsf(bv[e]));
+                    size = fmaf(fabsf(wv[1][e]), fabsf(past[1][e]), size);
+                    size = fmaf(fabsf(wv[2][e]), fabsf(past[2][e]), size);
+                    size = fmaf(fabsf(wv[3][e]), fabsf(last), size);
+                    bool near;
+                    o[e] = f32_to_bf16(conv_silu(p, size, near));
+                    if (near) {
+                        double q = fma((double)wv[0][e], (double)past[0][e], (double)bv[e]);
+                        q = fma((double)wv[1][e], (double)past[1][e], q);
+                        q = fma((double)wv[2][e], (double)past[2][e], q);
+                        q = fma((double)wv[3][e], (double)last, q);
+                        o[e] = silu_bf16_64(q);
+                    }
+                } else {
+                    o[e] = silu_f32(p);
+                }
+                past[0][e] = past[1][e];
+                past[1][e] = past[2][e];
+                past[2][e] = last;
+            }
+            if (t + i >= len)
+                for (int e = 0; e < kSdConvV; ++e) o[e] = 0;
+            conv_vec<IO, true>::store(ub + (t + i) * dc, o);
+        }
+    }
+    if (st_out && t0 == 0) {   // (last: st_out may be st_in)
         IO keep[kSdTaps - 1][kSdConvV];
 #pragma unroll
         for (int j = 0; j < kSdTaps - 1; ++j)
@@ -292,30 +385,6 @@ sd_conv_kernel(const IO *__restrict__ x, int64_t xstride, const float *__restric
 #pragma unroll
         for (int j = 0; j < kSdTaps - 1; ++j)
             if (j < h) conv_vec<IO, true>::store(st_out + (b * h + j) * dc + c, keep[j]);
-    }
-    for (int64_t t = t0; t < t1; ++t) {
-        IO o[kSdConvV];
-        if (t < len) {
-            IO r[kSdConvV];
-            conv_vec<IO, AL>::load(xb + t * xstride, r);
-#pragma unroll
-            for (int k = 0; k < kSdConvV; ++k) {
-                const acc_t now = (acc_t)io_f32(r[k]);
-                acc_t p = fma(wv[k][0], past[0][k], bv[k]);
-                p = fma(wv[k][1], past[1][k], p);
-                p = fma(wv[k][2], past[2][k], p);
-                p = fma(wv[k][3], now, p);
-                past[0][k] = past[1][k];
-                past[1][k] = past[2][k];
-                past[2][k] = now;
-                if constexpr (sizeof(IO) == 2) o[k] = silu_bf16(p);
-                else o[k] = silu_f32(p);
-            }
-        } else {
-#pragma unroll
-            for (int k = 0; k < kSdConvV; ++k) o[k] = 0;
-        }
-        conv_vec<IO, true>::store(ub + t * dc, o);
     }
 }
 
@@ -371,8 +440,8 @@ __device__ __forceinline__ void sd_store_state(const f32x4_t (&S)[NB], float *m,
 // accumulators.  ckpt: [b][h][chunk][P][N], receives the state entering each chunk, or null.
 template <typename E, int NT>
 __global__ void __launch_bounds__(kSdThreads)
-sd_scan_kernel(const typename sd<E>::io *__restrict__ u_, const typename sd<E>::io *__restrict__ dt,
-               const float *__restrict__ A, const float *__restrict__ Dv, const float *__restrict__ dt_bias,
+__attribute__((amdgpu_waves_per_eu(sd<E>::split && NT == 64 ? 3 : 2)))
+sd_scan_kernel(const typename sd<E>::io *__restrict__ u_, const float *__restrict__ tok, const float *__restrict__ Dv,
                const int32_t *__restrict__ lens, const float *h0, typename sd<E>::io *__restrict__ y_, float *last,
                float *__restrict__ ckpt, sd_shape s) {
     using IO = typename sd<E>::io;
@@ -388,8 +457,8 @@ sd_scan_kernel(const typename sd<E>::io *__restrict__ u_, const typename sd<E>::
     const sd_view<IO> v(u_, s, b, h, pt);
     const E *xs = reinterpret_cast<const E *>(v.x), *Bs = reinterpret_cast<const E *>(v.B), *Cs = reinterpret_cast<const E *>(v.C);
     const int64_t len = lens ? min(max((int64_t)lens[b], (int64_t)0), s.L) : s.L;
-    const float a2 = A[h] * kLog2e, bias = dt_bias ? dt_bias[h] : 0.0f, skip = Dv ? Dv[h] : 0.0f;
-    const IO *dtp = dt + b * s.L * s.dt_stride + h;
+    const float skip = Dv ? Dv[h] : 0.0f;
+    tok += (b * s.H + h) * s.nchunk * kSdTok;
     const int64_t st_at = (b * s.H + h) * s.P * s.N + (int64_t)pt * 64 * s.N;
     IO *yb = y_ + (b * s.L * s.H + h) * s.P + pt * 64;
     f32x4_t S[NB];
@@ -401,13 +470,13 @@ sd_scan_kernel(const typename sd<E>::io *__restrict__ u_, const typename sd<E>::
     }
     tile64<E, NT> rB, rC;
     tile64<E, 64> rX;
-    float rdt = 0.0f, sig;
+    sd_tok rt = {};
     auto fetch = [&](int64_t t0) {
         const int rows = (int)min((int64_t)64, len - t0);
         rB.load(Bs + t0 * s.dc, s.dc, rows, s.N);
         rC.load(Cs + t0 * s.dc, s.dc, rows, s.N);
         rX.load(xs + t0 * s.dc, s.dc, rows, v.pw);
-        if (w == 0) rdt = sd_dt(dtp, s.dt_stride, t0, len, bias, s.softplus, lane, sig);
+        if (w == 0) rt = sd_load_tokens(tok + t0 / kSdQ * kSdTok, lane);
     };
     const int64_t live = (len + kSdQ - 1) / kSdQ;   // chunks with tokens
     if (live > 0) fetch(0);
@@ -416,7 +485,7 @@ sd_scan_kernel(const typename sd<E>::io *__restrict__ u_, const typename sd<E>::
         rB.stage(tB);
         rC.stage(tC);
         rX.stage(tX);
-        if (w == 0) sd_form_tokens(tk, rdt, a2, lane);
+        if (w == 0) sd_stage_tokens(tk, rt, lane);
         if (c + 1 < live) fetch(t0 + kSdQ);
         if (ckpt) sd_store_state(S, ckpt + (((b * s.H + h) * s.nchunk + c) * s.P + (int64_t)pt * 64) * s.N, s.N, v.pw, w, lane);
         __syncthreads();
@@ -429,30 +498,45 @@ sd_scan_kernel(const typename sd<E>::io *__restrict__ u_, const typename sd<E>::
         for (int k = 0; k < NB; k += 2) {
             const formed<E, 2> s0(S[k]), s1(S[k + 1]);
             const F b0 = ld_row<E, NT>(tB, 16 * w, 16 * k, lane), b1 = ld_row<E, NT>(tB, 16 * w, 16 * k + 16, lane);
+            F c0[4], c1[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const F c0 = ld_row<E, NT>(tC, 16 * j, 16 * k, lane), c1 = ld_row<E, NT>(tC, 16 * j, 16 * k + 16, lane);
-                Y[j] = mma_fa<E, 2>(s0, s1, c0, c1, Y[j]);
-                if (j >= w) Gt[j] = mma(b0, b1, c0, c1, Gt[j]);
+                c0[j] = ld_row<E, NT>(tC, 16 * j, 16 * k, lane);
+                c1[j] = ld_row<E, NT>(tC, 16 * j, 16 * k + 16, lane);
             }
+#pragma unroll
+            for (int m = 0; m < formed<E, 2>::N; ++m)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) Y[j] = mma(s0.p[m], s1.p[m], c0[j], c1[j], Y[j]);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (j >= w) Gt[j] = mma(b0, b1, c0[j], c1[j], Gt[j]);
         }
-        // M[t][s], D on its diagonal
+        // M[t][s], D on its diagonal.  Past the diagonal block the decay is taken over the block's last token r, in
+        // two factors of at most 1: e^{c_t - c_r} and e^{c_r - c_s} dt_s
         {
             const int s0 = 16 * w + q4;
             const f32x4_t sh = ld4(tk.ch + s0), sl = ld4(tk.cl + s0), sd4 = ld4(tk.dt + s0);
+            const float rh = tk.ch[16 * w + 15], rl = tk.cl[16 * w + 15];
+            f32x4_t fs;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) fs[e] = hw_exp2((rh - sh[e]) + (rl - sl[e])) * sd4[e];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const int t = 16 * j + c16;
                 f32x4_t m = {0.0f, 0.0f, 0.0f, 0.0f};
-                if (j >= w) {
+                if (j > w) {
+                    m = Gt[j] * fs * hw_exp2((tk.ch[t] - rh) + (tk.cl[t] - rl));
+                } else if (j == w) {
                     const float th = tk.ch[t], tl = tk.cl[t];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         const float k = hw_exp2((th - sh[e]) + (tl - sl[e]));
-                        m[e] = s0 + e <= t ? Gt[j][e] * (k * sd4[e]) : 0.0f;
-                        if (s0 + e == t) m[e] += skip;
+                        m[e] = q4 + e <= c16 ? Gt[j][e] * (k * sd4[e]) : 0.0f;
+                        if (q4 + e == c16) m[e] += skip;
                     }
                 }
+                if (j < (w & ~1)) continue;   // (the products read pairs of 16 tokens s up to t's)
                 const formed<E, 2> f(m);
 #pragma unroll
                 for (int i = 0; i < formed<E, 2>::N; ++i) *reinterpret_cast<F *>(&tM[i][t * sd_ld<E>(64) + s0]) = f.p[i];
@@ -465,30 +549,47 @@ sd_scan_kernel(const typename sd<E>::io *__restrict__ u_, const typename sd<E>::
         for (int i = 0; i < 4; i += 2) {
             const formed<E, 3> x0(widen(xf[i]) * ld4(tk.w + 16 * i + q4)), x1(widen(xf[i + 1]) * ld4(tk.w + 16 * i + 16 + q4));
 #pragma unroll
-            for (int nb = 0; nb < NB; ++nb)
-                S[nb] = mma_fb<E, 3>(ld_col<E, NT>(tB, 16 * i, 16 * nb, lane), ld_col<E, NT>(tB, 16 * i + 16, 16 * nb, lane), x0, x1, S[nb]);
+            for (int n0 = 0; n0 < NB; n0 += 4) {
+                F b0[4], b1[4];
+#pragma unroll
+                for (int nb = 0; nb < 4; ++nb) {
+                    b0[nb] = ld_col<E, NT>(tB, 16 * i, 16 * (n0 + nb), lane);
+                    b1[nb] = ld_col<E, NT>(tB, 16 * i + 16, 16 * (n0 + nb), lane);
+                }
+#pragma unroll
+                for (int m = 0; m < formed<E, 3>::N; ++m)
+#pragma unroll
+                    for (int nb = 0; nb < 4; ++nb) S[n0 + nb] = mma(b0[nb], b1[nb], x0.p[m], x1.p[m], S[n0 + nb]);
+            }
         }
 #pragma unroll
         for (int j = 0; j < 4; ++j) Y[j] *= tk.e[16 * j + c16];
         __syncthreads();
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
+        for (int i = 0; i < 4; i += 2)
 #pragma unroll
-            for (int i = 0; i <= j; i += 2)
+            for (int m = 0; m < formed<E, 2>::N; ++m)
 #pragma unroll
-                for (int m = 0; m < formed<E, 2>::N; ++m)
+                for (int j = i; j < 4; ++j)
                     Y[j] = mma(xf[i], xf[i + 1], ld_row<E, 64>(tM[m], 16 * j, 16 * i, lane), ld_row<E, 64>(tM[m], 16 * j, 16 * i + 16, lane), Y[j]);
-        if (16 * w + q4 < v.pw) {
+        const int rows = (int)min((int64_t)64, len - t0);
+        char *yc = reinterpret_cast<char *>(yb + t0 * s.H * s.P);
+        const uint32_t yrow = (uint32_t)(s.H * s.P) * (uint32_t)sizeof(IO), yoff = (uint32_t)c16 * yrow + (uint32_t)(16 * w + q4) * (uint32_t)sizeof(IO);
+        auto put = [&](int j, f32x4_t o) {
+            char *yp = yc + (yoff + (uint32_t)(16 * j) * yrow);
+            if constexpr (sizeof(IO) == 2)
+                *reinterpret_cast<u32x2_t *>(yp) = u32x2_t{f32x2_to_bf16x2(o[0], o[1]), f32x2_to_bf16x2(o[2], o[3])};
+            else *reinterpret_cast<f32x4_t *>(yp) = o;
+        };
+        if (rows == 64) {
+            if (16 * w + q4 < v.pw) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int64_t t = t0 + 16 * j + c16;
-                if (t >= s.L) continue;
-                const f32x4_t o = t < len ? Y[j] : f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-                IO *yp = yb + t * s.H * s.P + 16 * w + q4;
-                if constexpr (sizeof(IO) == 2)
-                    *reinterpret_cast<u32x2_t *>(yp) = u32x2_t{f32x2_to_bf16x2(o[0], o[1]), f32x2_to_bf16x2(o[2], o[3])};
-                else *reinterpret_cast<f32x4_t *>(yp) = o;
+                for (int j = 0; j < 4; ++j) put(j, Y[j]);
             }
+        } else if (16 * w + q4 < v.pw) {   // the sequence's last chunk
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (t0 + 16 * j + c16 < s.L) put(j, 16 * j + c16 < rows ? Y[j] : f32x4_t{0.0f, 0.0f, 0.0f, 0.0f});
         }
     }
     // chunks past the sequence's end: the state stays, y is zero
