@@ -60,6 +60,15 @@ int launched() {
     return ok();
 }
 
+// Segments of a sequence, which run beside each other: a pass over the state alone finds what each of them starts
+// from.  One, unless the sequences' heads leave most of the workgroups that fit on the chip without work; at least two
+// chunks each.
+constexpr int64_t kSegTarget = 512;
+int64_t segments(const ssm_ssd_conv_dims *dm) {
+    const int64_t items = dm->batch * dm->nheads * p_tiles(dm), most = std::max<int64_t>(chunks(dm) / 2, 1);
+    return std::min(std::max<int64_t>(kSegTarget / std::max<int64_t>(items, 1), 1), most);
+}
+
 ssm::sd_shape shape_of(const ssm_ssd_conv_dims *dm, int flags) {
     ssm::sd_shape s;
     s.L = dm->seqlen;
@@ -72,6 +81,8 @@ ssm::sd_shape shape_of(const ssm_ssd_conv_dims *dm, int flags) {
     s.dt_stride = dm->dt_stride ? dm->dt_stride : dm->nheads;
     s.softplus = flags & SSM_SCAN_SOFTPLUS;
     s.nchunk = chunks(dm);
+    s.cps = std::max<int64_t>(ceil_div(s.nchunk, segments(dm)), 1);
+    s.nseg = (int)std::max<int64_t>(ceil_div(s.nchunk, s.cps), 1);
     return s;
 }
 
@@ -80,6 +91,12 @@ size_t u_bytes(const ssm_ssd_conv_dims *dm) { return align256((size_t)(dm->batch
 size_t tok_bytes(const ssm_ssd_conv_dims *dm) { return align256((size_t)(dm->batch * dm->nheads * chunks(dm) * ssm::kSdTok) * sizeof(float)); }
 size_t state_bytes(const ssm_ssd_conv_dims *dm) {
     return align256((size_t)(dm->batch * chunks(dm) * dm->nheads * dm->headdim * dm->dstate) * sizeof(float));
+}
+
+// The segments' states (none where there is one segment).
+size_t seg_bytes(const ssm_ssd_conv_dims *dm) {
+    const int64_t n = shape_of(dm, 0).nseg;
+    return n > 1 ? align256((size_t)(dm->batch * dm->nheads * n * dm->headdim * dm->dstate) * sizeof(float)) : 0;
 }
 
 // Tokens per thread of the convolution: 32 (a thread reads three rows more than it has), 8 where that leaves CUs
@@ -117,12 +134,42 @@ void launch_conv(const void *x_, const float *w, const float *bias, const void *
                        dm->seqlen, (int)row_of(dm), tt, (int)g.vblocks, (int)g.tiles, k);
 }
 
-template <typename E, int NT>
-void launch_scan(const void *u, const float *tok, const float *D, const int32_t *lens, const float *h0, void *y, float *last, float *ckpt, const ssm_ssd_conv_dims *dm, int flags, hipStream_t st) {
+template <typename E, int NT, bool ADJ>
+void launch_walk(const void *u, const void *dy, const float *tok, const int32_t *lens, const float *from, float *each, float *to,
+                 int ends, const ssm_ssd_conv_dims *dm, int flags, hipStream_t st) {
     using IO = typename ssm::sd<E>::io;
     const ssm::sd_shape s = shape_of(dm, flags);
-    hipLaunchKernelGGL((ssm::sd_scan_kernel<E, NT>), dim3((unsigned)(dm->batch * s.H * s.PT)), dim3(ssm::kSdThreads), 0, st,
-                       static_cast<const IO *>(u), tok, D, lens, h0, static_cast<IO *>(y), last, ckpt, s);
+    hipLaunchKernelGGL((ssm::sd_walk_kernel<E, NT, ADJ>), dim3((unsigned)(dm->batch * s.H * s.PT * s.nseg)), dim3(ssm::kSdThreads), 0,
+                       st, static_cast<const IO *>(u), static_cast<const IO *>(dy), tok, lens, from, each, to, ends, s);
+}
+template <bool ADJ>
+void walk(const void *u, const void *dy, const float *tok, const int32_t *lens, const float *from, float *each, float *to, int ends,
+          const ssm_ssd_conv_dims *dm, int flags, hipStream_t st) {
+    const bool bf = dm->io_dtype == SSM_IO_BF16, wide = dm->dstate > 64;
+    auto f = bf ? wide ? launch_walk<__bf16, 128, ADJ> : launch_walk<__bf16, 64, ADJ>
+                : wide ? launch_walk<float, 128, ADJ> : launch_walk<float, 64, ADJ>;
+    f(u, dy, tok, lens, from, each, to, ends, dm, flags, st);
+}
+
+// What the segments start from: `first` where there is one, else found in `seg` by a pass over the state alone.
+template <bool ADJ>
+const float *segment_starts(const void *u, const void *dy, const float *tok, const int32_t *lens, const float *first, float *seg,
+                            const ssm_ssd_conv_dims *dm, int flags, hipStream_t st) {
+    const ssm::sd_shape s = shape_of(dm, flags);
+    if (s.nseg == 1) return first;
+    walk<ADJ>(u, dy, tok, lens, nullptr, nullptr, seg, 1, dm, flags, st);
+    const int blocks = (int)ceil_div((int64_t)s.P * s.N, 1024);
+    hipLaunchKernelGGL(ssm::sd_combine_kernel<ADJ>, dim3((unsigned)(dm->batch * s.H * blocks)), dim3(256), s.nseg * sizeof(float), st,
+                       tok, first, seg, s, blocks);
+    return seg;
+}
+
+template <typename E, int NT>
+void launch_scan(const void *u, const float *tok, const float *D, const int32_t *lens, const float *from, void *y, float *last, float *ckpt, const ssm_ssd_conv_dims *dm, int flags, hipStream_t st) {
+    using IO = typename ssm::sd<E>::io;
+    const ssm::sd_shape s = shape_of(dm, flags);
+    hipLaunchKernelGGL((ssm::sd_scan_kernel<E, NT>), dim3((unsigned)(dm->batch * s.H * s.PT * s.nseg)), dim3(ssm::kSdThreads), 0, st,
+                       static_cast<const IO *>(u), tok, D, lens, from, static_cast<IO *>(y), last, ckpt, s);
 }
 
 template <typename IO>
@@ -138,11 +185,15 @@ void launch_step(float *state, const void *u, const void *dt, const float *A, co
 }
 
 // How the backward cuts its work, and its workspace.
-constexpr int kConvBwdTokens = 64;   // tokens per thread of the convolution's backward
+// Tokens per thread of the convolution's backward: 64 (a thread goes three tokens further than its own), 16 where
+// that leaves CUs with less than four waves per SIMD.
+int conv_bwd_tokens(const ssm_ssd_conv_dims *dm) {
+    return dm->batch * dm->seqlen * (row_of(dm) / ssm::kSdConvV) >= (int64_t)64 * 64 * 4096 ? 64 : 16;
+}
 struct BwdPlan {
     int HS, hpw;
     int64_t tiles;
-    size_t u, tok, states, adjoints, du, dbc, part, conv_part, bytes;   // offsets (u, tok, states: without checkpoints)
+    size_t u, tok, states, seg, adjoints, du, dbc, part, conv_part, bytes;   // offsets (u, tok, states: without checkpoints)
 };
 BwdPlan bwd_plan(const ssm_ssd_conv_dims *dm, bool have_checkpoints) {
     BwdPlan p;
@@ -151,7 +202,7 @@ BwdPlan bwd_plan(const ssm_ssd_conv_dims *dm, bool have_checkpoints) {
     const int64_t parts = std::min(per, std::max<int64_t>(ceil_div(2048, items), 1));
     p.hpw = (int)ceil_div(per, parts);
     p.HS = (int)ceil_div(per, p.hpw);
-    p.tiles = std::max<int64_t>(ceil_div(dm->seqlen, kConvBwdTokens), 1);
+    p.tiles = std::max<int64_t>(ceil_div(dm->seqlen, conv_bwd_tokens(dm)), 1);
     size_t at = 0;
     auto take = [&](size_t bytes) {
         const size_t o = at;
@@ -162,6 +213,7 @@ BwdPlan bwd_plan(const ssm_ssd_conv_dims *dm, bool have_checkpoints) {
     p.u = take(have_checkpoints ? 0 : u_bytes(dm));
     p.tok = take(have_checkpoints ? 0 : tok_bytes(dm));
     p.states = take(have_checkpoints ? 0 : state_bytes(dm));
+    p.seg = take(seg_bytes(dm));
     p.adjoints = take(state_bytes(dm));
     p.du = take(tokens * dm->nheads * dm->headdim * 4);
     p.dbc = take(tokens * p.HS * 2 * dm->ngroups * dm->dstate * 4);
@@ -169,14 +221,6 @@ BwdPlan bwd_plan(const ssm_ssd_conv_dims *dm, bool have_checkpoints) {
     p.conv_part = take((size_t)(dm->batch * p.tiles * 5 * row_of(dm)) * 4);
     p.bytes = at;
     return p;
-}
-
-template <typename E, int NT, bool ADJ>
-void launch_walk(const void *u, const void *dy, const float *tok, const int32_t *lens, const float *from, float *each, float *to, const ssm_ssd_conv_dims *dm, int flags, hipStream_t st) {
-    using IO = typename ssm::sd<E>::io;
-    const ssm::sd_shape s = shape_of(dm, flags);
-    hipLaunchKernelGGL((ssm::sd_walk_kernel<E, NT, ADJ>), dim3((unsigned)(dm->batch * s.H * s.PT)), dim3(ssm::kSdThreads), 0, st,
-                       static_cast<const IO *>(u), static_cast<const IO *>(dy), tok, lens, from, each, to, s);
 }
 
 template <typename E, int NT>
@@ -192,15 +236,15 @@ void launch_bwd(const void *u, const void *dy, const float *tok, const void *dt,
 
 template <typename IO>
 void launch_conv_bwd(const void *x_, const float *w, const float *bias, const void *st_in, const int32_t *lens, const float *du,
-                     const float *dbc, int HS, void *dx, void *dst, float *parts, const ssm_ssd_conv_dims *dm, hipStream_t st) {
+                     const float *dbc, void *dx, void *dst, float *parts, const ssm_ssd_conv_dims *dm, hipStream_t st) {
     const int64_t stride = dm->xbc_stride ? dm->xbc_stride : row_of(dm);
-    const ConvGrid g = conv_grid(dm, kConvBwdTokens, false);
+    const ConvGrid g = conv_grid(dm, conv_bwd_tokens(dm), false);
     const bool al = aligned(x_, ssm::kSdConvV * sizeof(IO)) && stride % ssm::kSdConvV == 0;
     auto kern = al ? ssm::sd_conv_bwd_kernel<IO, true> : ssm::sd_conv_bwd_kernel<IO, false>;
     hipLaunchKernelGGL(kern, dim3((unsigned)g.blocks), dim3(256), 0, st, static_cast<const IO *>(x_), stride, w, bias,
-                       (int)dm->width, static_cast<const IO *>(st_in), lens, du, dbc, HS, static_cast<IO *>(dx),
-                       static_cast<IO *>(dst), parts, dm->batch, dm->seqlen, (int)row_of(dm), (int)(dm->nheads * dm->headdim),
-                       kConvBwdTokens, (int)g.vblocks, (int)g.tiles);
+                       (int)dm->width, static_cast<const IO *>(st_in), lens, du, dbc, static_cast<IO *>(dx),
+                       static_cast<IO *>(dst), parts, dm->seqlen, (int)row_of(dm), (int)(dm->nheads * dm->headdim),
+                       conv_bwd_tokens(dm), (int)g.vblocks, (int)g.tiles);
 }
 
 void launch_sums(const float *part, int64_t n, int cols, int planes, const ssm::sd_sums &o, hipStream_t st) {
@@ -222,7 +266,7 @@ extern "C" {
 
 size_t ssm_ssd_conv_workspace_bytes(const ssm_ssd_conv_dims *dims, int flags) {
     if (check_dims(dims) != SSM_OK || dims->batch == 0 || dims->nheads == 0) return 0;
-    return u_bytes(dims) + tok_bytes(dims) + ((flags & SSM_SCAN_CHECKPOINTS) ? state_bytes(dims) : 0);
+    return u_bytes(dims) + tok_bytes(dims) + ((flags & SSM_SCAN_CHECKPOINTS) ? state_bytes(dims) : 0) + seg_bytes(dims);
 }
 
 int ssm_ssd_conv_fwd(const void *xbc, const float *conv_w, const float *conv_b, const void *conv_state, const void *dt,
@@ -252,7 +296,9 @@ int ssm_ssd_conv_fwd(const void *xbc, const float *conv_w, const float *conv_b, 
     auto conv = bf ? launch_conv<uint16_t> : launch_conv<float>;
     conv(xbc, conv_w, conv_b, conv_state, conv_state_out, seq_lens, workspace, dt, A, dt_bias, tok, dims, flags, st);
     auto scan = bf ? wide ? launch_scan<__bf16, 128> : launch_scan<__bf16, 64> : wide ? launch_scan<float, 128> : launch_scan<float, 64>;
-    scan(workspace, tok, D, seq_lens, initial_state, y, last_state, ckpt, dims, flags, st);
+    float *seg = tok + (tok_bytes(dims) + (ckpt ? state_bytes(dims) : 0)) / sizeof(float);
+    const float *from = segment_starts<false>(workspace, nullptr, tok, seq_lens, initial_state, seg, dims, flags, st);
+    scan(workspace, tok, D, seq_lens, from, y, last_state, ckpt, dims, flags, st);
     return launched();
 }
 
@@ -306,20 +352,21 @@ int ssm_ssd_conv_bwd(const void *xbc, const float *conv_w, const float *conv_b, 
         if (!kept) {
             auto conv = bf ? launch_conv<uint16_t> : launch_conv<float>;
             conv(xbc, conv_w, conv_b, conv_state, nullptr, seq_lens, ws + p.u, dt, A, dt_bias, at(p.tok), dims, flags, st);
-            auto f = bf ? wide ? launch_walk<__bf16, 128, false> : launch_walk<__bf16, 64, false>
-                        : wide ? launch_walk<float, 128, false> : launch_walk<float, 64, false>;
-            f(u, nullptr, tok, seq_lens, initial_state, at(p.states), nullptr, dims, flags, st);
+            const float *from = segment_starts<false>(u, nullptr, tok, seq_lens, initial_state, at(p.seg), dims, flags, st);
+            walk<false>(u, nullptr, tok, seq_lens, from, at(p.states), nullptr, 0, dims, flags, st);
         }
-        auto f = bf ? wide ? launch_walk<__bf16, 128, true> : launch_walk<__bf16, 64, true>
-                    : wide ? launch_walk<float, 128, true> : launch_walk<float, 64, true>;
-        f(u, dy, tok, seq_lens, dlast_state, at(p.adjoints), dinitial_state, dims, flags, st);
+        const float *from = segment_starts<true>(u, dy, tok, seq_lens, dlast_state, at(p.seg), dims, flags, st);
+        walk<true>(u, dy, tok, seq_lens, from, at(p.adjoints), dinitial_state, 0, dims, flags, st);
         if (dims->seqlen > 0) {
             const ssm::sd_grad g = {at(p.du), at(p.dbc), at(p.part), p.HS, p.hpw};
             auto k = bf ? wide ? launch_bwd<__bf16, 128> : launch_bwd<__bf16, 64> : wide ? launch_bwd<float, 128> : launch_bwd<float, 64>;
             k(u, dy, tok, dt, A, D, dt_bias, seq_lens, states, at(p.adjoints), ddt, g, dims, flags, st);
         }
+        const int64_t nbc = dims->batch * dims->seqlen * 2 * dims->ngroups * dims->dstate;
+        if (p.HS > 1 && nbc > 0)
+            hipLaunchKernelGGL(ssm::sd_parts_kernel, dim3((unsigned)ceil_div(nbc, 1024)), dim3(256), 0, st, at(p.dbc), nbc, p.HS);
         auto c = bf ? launch_conv_bwd<uint16_t> : launch_conv_bwd<float>;
-        c(xbc, conv_w, conv_b, conv_state, seq_lens, at(p.du), at(p.dbc), p.HS, dxbc, dconv_state, at(p.conv_part), dims, st);
+        c(xbc, conv_w, conv_b, conv_state, seq_lens, at(p.du), at(p.dbc), dxbc, dconv_state, at(p.conv_part), dims, st);
     }
     const int W = dims->width, H = (int)dims->nheads;
     ssm::sd_sums o = {};

@@ -21,13 +21,13 @@ namespace ssm {
 
 // The states entering the chunks (ADJ = false: rows x, weights e^{c_last - c} dt, with B) or the adjoints of the
 // states leaving them (ADJ: rows dy, weights e^c, with C, chunks from the last), one workgroup per (sequence, head,
-// 64-channel tile).  each: [b][h][chunk][P][N].  from / to: [b][h][P][N], the first and what the last chunk leaves,
-// each may be null.
+// 64-channel tile, segment).  each: [b][h][chunk][P][N], or null.  from: [b][h][segment][P][N], or null (zero).  to: with
+// `ends` [b][h][segment][P][N], what every segment leaves, else [b][h][P][N], what the last (ADJ: first) one leaves, or null.
 template <typename E, int NT, bool ADJ>
 __global__ void __launch_bounds__(kSdThreads)
 sd_walk_kernel(const typename sd<E>::io *__restrict__ u_, const typename sd<E>::io *__restrict__ dy_,
                const float *__restrict__ tok, const int32_t *__restrict__ lens, const float *__restrict__ from, float *__restrict__ each,
-               float *__restrict__ to, sd_shape s) {
+               float *__restrict__ to, int ends, sd_shape s) {
     using IO = typename sd<E>::io;
     using F = typename sd<E>::frag;
     constexpr int NB = NT / 16;
@@ -35,28 +35,26 @@ sd_walk_kernel(const typename sd<E>::io *__restrict__ u_, const typename sd<E>::
     __shared__ sd_tokens tk;
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int q4 = 4 * (lane >> 4);
-    const int pt = blockIdx.x % s.PT, h = blockIdx.x / s.PT % s.H;
-    const int64_t b = blockIdx.x / s.PT / s.H;
+    const sd_segment at(s, lens);
+    const int64_t b = at.b, len = at.len;
+    const int h = at.h, pt = at.pt;
     const sd_view<IO> v(u_, s, b, h, pt);
     const int xrow = ADJ ? s.H * s.P : s.dc;
     const E *xs = reinterpret_cast<const E *>(ADJ ? dy_ + (b * s.L * s.H + h) * s.P + pt * 64 : v.x);
     const E *Bs = reinterpret_cast<const E *>(ADJ ? v.C : v.B);
-    const int64_t len = lens ? min(max((int64_t)lens[b], (int64_t)0), s.L) : s.L;
     tok += (b * s.H + h) * s.nchunk * kSdTok;
-    const int64_t st_at = (b * s.H + h) * s.P * s.N + (int64_t)pt * 64 * s.N;
     f32x4_t S[NB];
     if (from) {
-        sd_load_state(S, from + st_at, s.N, v.pw, w, lane);
+        sd_load_state(S, from + at.state_at(s, s.nseg, at.seg), s.N, v.pw, w, lane);
     } else {
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) S[nb] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
     }
     auto keep = [&](int64_t c) {
-        sd_store_state(S, each + (((b * s.H + h) * s.nchunk + c) * s.P + (int64_t)pt * 64) * s.N, s.N, v.pw, w, lane);
+        if (each) sd_store_state(S, each + at.state_at(s, s.nchunk, c), s.N, v.pw, w, lane);
     };
-    const int64_t live = (len + kSdQ - 1) / kSdQ;
     if (ADJ)   // chunks past the sequence's end leave the adjoint as it is
-        for (int64_t c = live; c < s.nchunk; ++c) keep(c);
+        for (int64_t c = at.live; c < at.c1; ++c) keep(c);
     tile64<E, NT> rB;
     tile64<E, 64> rX;
     sd_tok rt = {};
@@ -67,13 +65,14 @@ sd_walk_kernel(const typename sd<E>::io *__restrict__ u_, const typename sd<E>::
         rX.load(xs + t0 * xrow, (uint32_t)xrow, rows, v.pw);
         if (w == 0) rt = sd_load_tokens(tok + c * kSdTok, lane);
     };
-    if (live > 0) fetch(ADJ ? live - 1 : 0);
-    for (int64_t i = 0; i < live; ++i) {
-        const int64_t c = ADJ ? live - 1 - i : i;
+    const int64_t n = at.live - at.c0;
+    if (n > 0) fetch(ADJ ? at.live - 1 : at.c0);
+    for (int64_t i = 0; i < n; ++i) {
+        const int64_t c = ADJ ? at.live - 1 - i : at.c0 + i;
         rB.stage(tB);
         rX.stage(tX);
         if (w == 0) sd_stage_tokens(tk, rt, lane);
-        if (i + 1 < live) fetch(ADJ ? c - 1 : c + 1);
+        if (i + 1 < n) fetch(ADJ ? c - 1 : c + 1);
         keep(c);
         __syncthreads();
 #pragma unroll
@@ -100,8 +99,9 @@ sd_walk_kernel(const typename sd<E>::io *__restrict__ u_, const typename sd<E>::
         __syncthreads();
     }
     if (!ADJ)
-        for (int64_t c = live; c < s.nchunk; ++c) keep(c);
-    if (to) sd_store_state(S, to + st_at, s.N, v.pw, w, lane);
+        for (int64_t c = at.live; c < at.c1; ++c) keep(c);
+    if (ends) sd_store_state(S, to + at.state_at(s, s.nseg, at.seg), s.N, v.pw, w, lane);
+    else if (to && at.seg == (ADJ ? 0 : s.nseg - 1)) sd_store_state(S, to + at.state_at(s, 1, 0), s.N, v.pw, w, lane);
 }
 
 // 64 x 64 of a state [p][n] in fp32 from memory to LDS, as NS operand parts.
@@ -411,22 +411,49 @@ sd_bwd_kernel(const typename sd<E>::io *__restrict__ u_, const typename sd<E>::i
     }
 }
 
-// Back through silu and the convolution; thread: kSdConvV channels of `tt` tokens.  With g_t = du_t silu'(pre_t):
+// dbc's HS parts of n elements each, added up in the first.
+static __global__ void __launch_bounds__(256) sd_parts_kernel(float *dbc, int64_t n, int HS) {
+    const int64_t e = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
+    if (e >= n) return;
+    f32x4_t a = ld4(dbc + e);
+#pragma unroll 8
+    for (int i = 1; i < HS; ++i) a += ld4(dbc + i * n + e);
+    *reinterpret_cast<f32x4_t *>(dbc + e) = a;
+}
+
+// Back through silu and the convolution; thread: kSdConvV channels of `tt` tokens, kSdConvT at a time, the next ones'
+// rows requested before.  With g_t = du_t silu'(pre_t):
 //   dx_t = sum_j w[j] g_{t+3-j},   dw[j] = sum g_t x_{t-3+j},   db = sum g_t         (w[j]: four taps, oldest first)
-// parts: [b * tile][5][dc] sums over the tile's tokens of dw's four taps and of db.
+// so a thread forms g for three tokens past its own.  parts: [b * tile][5][dc] sums over the tile's tokens of dw's four
+// taps and of db.
 template <typename IO, bool AL>
 __global__ void __launch_bounds__(256)
 sd_conv_bwd_kernel(const IO *__restrict__ x, int64_t xstride, const float *__restrict__ w, const float *__restrict__ bias,
                    int width, const IO *__restrict__ st_in, const int32_t *__restrict__ lens, const float *__restrict__ du,
-                   const float *__restrict__ dbc, int HS, IO *__restrict__ dx, IO *__restrict__ dst,
-                   float *__restrict__ parts, int64_t batch, int64_t L, int dc, int hp, int tt, int vblocks, int ntiles) {
+                   const float *__restrict__ dbc, IO *__restrict__ dx, IO *__restrict__ dst, float *__restrict__ parts,
+                   int64_t L, int dc, int hp, int tt, int vblocks, int ntiles) {
     const int v = blockIdx.x % vblocks * 256 + threadIdx.x;
     if (v >= dc / kSdConvV) return;
     const int c = v * kSdConvV, bc = dc - hp;
     const int64_t b = blockIdx.x / vblocks / ntiles, tile = blockIdx.x / vblocks % ntiles, t0 = tile * tt, t1 = min(t0 + tt, L);
-    const int64_t len = lens ? min(max((int64_t)lens[b], (int64_t)0), L) : L;
+    const int64_t len = lens ? min(max((int64_t)lens[b], (int64_t)0), L) : L, end = min(t1 + 3, len);
     const IO *xb = x + b * L * xstride + c;
+    const float *db_ = c < hp ? du + b * L * hp + c : dbc + b * L * bc + (c - hp);
+    const int64_t drow = c < hp ? hp : bc;
     const int hw = width - 1;
+    IO r[kSdConvT][kSdConvV] = {};
+    f32x4_t d[kSdConvT] = {};
+    auto fetch = [&](int64_t t) {
+#pragma unroll
+        for (int i = 0; i < kSdConvT; ++i) {
+            d[i] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+            if (t + i < end) {
+                conv_vec<IO, AL>::load(xb + (t + i) * xstride, r[i]);
+                d[i] = ld4(db_ + (t + i) * drow);
+            }
+        }
+    };
+    fetch(t0);
     float wv[kSdTaps][kSdConvV], bv[kSdConvV], past[3][kSdConvV], g[kSdTaps][kSdConvV] = {}, aw[kSdTaps][kSdConvV] = {}, ab[kSdConvV] = {};
 #pragma unroll
     for (int k = 0; k < kSdConvV; ++k) {
@@ -440,61 +467,62 @@ sd_conv_bwd_kernel(const IO *__restrict__ x, int64_t xstride, const float *__res
 #pragma unroll
     for (int j = 0; j < 3; ++j) {
         const int64_t t = t0 - 3 + j;
-        IO r[kSdConvV] = {};
-        if (t >= 0) conv_vec<IO, AL>::load(xb + t * xstride, r);
-        else if (st_in && t >= -hw) conv_vec<IO, true>::load(st_in + (b * hw + hw + t) * dc + c, r);
+        IO o[kSdConvV] = {};
+        if (t >= 0) conv_vec<IO, AL>::load(xb + t * xstride, o);
+        else if (st_in && t >= -hw) conv_vec<IO, true>::load(st_in + (b * hw + hw + t) * dc + c, o);
 #pragma unroll
-        for (int k = 0; k < kSdConvV; ++k) past[j][k] = io_f32(r[k]);
+        for (int k = 0; k < kSdConvV; ++k) past[j][k] = io_f32(o[k]);
     }
-    for (int64_t t = t0; t < t1 + 3; ++t) {
+    for (int64_t tb = t0; tb < t1 + 3; tb += kSdConvT) {
+        IO rn[kSdConvT][kSdConvV];
+        f32x4_t dn[kSdConvT];
 #pragma unroll
-        for (int k = 0; k < kSdConvV; ++k) {
-            g[3][k] = g[2][k];   // g[j]: of token t - j
-            g[2][k] = g[1][k];
-            g[1][k] = g[0][k];
-            g[0][k] = 0.0f;
+        for (int i = 0; i < kSdConvT; ++i) {
+            dn[i] = d[i];
+#pragma unroll
+            for (int k = 0; k < kSdConvV; ++k) rn[i][k] = r[i][k];
         }
-        if (t < len) {
-            IO r[kSdConvV];
-            conv_vec<IO, AL>::load(xb + t * xstride, r);
-            f32x4_t d = {0.0f, 0.0f, 0.0f, 0.0f};
-            if (c < hp) {
-                d = ld4(du + (b * L + t) * hp + c);
-            } else {
-                for (int i = 0; i < HS; ++i) d += ld4(dbc + (((int64_t)i * batch + b) * L + t) * bc + (c - hp));
-            }
+        fetch(tb + kSdConvT);
+#pragma unroll
+        for (int i = 0; i < kSdConvT; ++i) {
+            const int64_t t = tb + i;
+            if (t >= t1 + 3) break;
+            const bool live = t < len, own = t < t1;
 #pragma unroll
             for (int k = 0; k < kSdConvV; ++k) {
-                const float now = io_f32(r[k]);
+                g[3][k] = g[2][k];   // g[j]: of token t - j
+                g[2][k] = g[1][k];
+                g[1][k] = g[0][k];
+                const float now = io_f32(rn[i][k]);
                 float p = fmaf(wv[0][k], past[0][k], bv[k]);
                 p = fmaf(wv[1][k], past[1][k], p);
                 p = fmaf(wv[2][k], past[2][k], p);
                 p = fmaf(wv[3][k], now, p);
-                const float sg = sigmoid_f32(p);
-                g[0][k] = d[k] * (sg * fmaf(p, 1.0f - sg, 1.0f));
-                if (t < t1) {
-                    aw[0][k] = fmaf(g[0][k], past[0][k], aw[0][k]);
-                    aw[1][k] = fmaf(g[0][k], past[1][k], aw[1][k]);
-                    aw[2][k] = fmaf(g[0][k], past[2][k], aw[2][k]);
-                    aw[3][k] = fmaf(g[0][k], now, aw[3][k]);
-                    ab[k] += g[0][k];
+                const float sg = sigmoid_f32(p), gt = dn[i][k] * (sg * fmaf(p, 1.0f - sg, 1.0f));
+                g[0][k] = live ? gt : 0.0f;   // (p may be NaN past the end)
+                if (own && live) {
+                    aw[0][k] = fmaf(gt, past[0][k], aw[0][k]);
+                    aw[1][k] = fmaf(gt, past[1][k], aw[1][k]);
+                    aw[2][k] = fmaf(gt, past[2][k], aw[2][k]);
+                    aw[3][k] = fmaf(gt, now, aw[3][k]);
+                    ab[k] += gt;
                 }
                 past[0][k] = past[1][k];
                 past[1][k] = past[2][k];
                 past[2][k] = now;
             }
-        }
-        const int64_t to = t - 3;
-        if (to >= t0 || (to < 0 && dst && to >= -hw)) {
-            IO o[kSdConvV];
+            const int64_t to = t - 3;
+            if (to >= t0 || (to < 0 && dst && to >= -hw)) {
+                IO o[kSdConvV];
 #pragma unroll
-            for (int k = 0; k < kSdConvV; ++k) {
-                const float r = fmaf(wv[0][k], g[0][k], fmaf(wv[1][k], g[1][k], fmaf(wv[2][k], g[2][k], wv[3][k] * g[3][k])));
-                if constexpr (sizeof(IO) == 2) o[k] = f32_to_bf16(r);
-                else o[k] = r;
+                for (int k = 0; k < kSdConvV; ++k) {
+                    const float q = fmaf(wv[0][k], g[0][k], fmaf(wv[1][k], g[1][k], fmaf(wv[2][k], g[2][k], wv[3][k] * g[3][k])));
+                    if constexpr (sizeof(IO) == 2) o[k] = f32_to_bf16(q);
+                    else o[k] = q;
+                }
+                if (to >= 0) conv_vec<IO, true>::store(dx + (b * L + to) * dc + c, o);
+                else conv_vec<IO, true>::store(dst + (b * hw + hw + to) * dc + c, o);
             }
-            if (to >= 0) conv_vec<IO, true>::store(dx + (b * L + to) * dc + c, o);
-            else conv_vec<IO, true>::store(dst + (b * hw + hw + to) * dc + c, o);
         }
     }
     float *p = parts + (b * ntiles + tile) * 5 * dc + c;

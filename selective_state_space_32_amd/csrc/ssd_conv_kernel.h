@@ -398,6 +398,8 @@ struct sd_shape {
     int64_t dt_stride;      // elements between tokens of the step sizes
     int softplus;
     int64_t nchunk;         // chunks of a sequence
+    int nseg;               // segments of a sequence, one after the other in workgroups of their own
+    int64_t cps;            // chunks per segment
 };
 
 // Where workgroup (sequence b, head h, tile pt) finds its rows.
@@ -436,13 +438,61 @@ __device__ __forceinline__ void sd_store_state(const f32x4_t (&S)[NB], float *m,
     }
 }
 
-// One workgroup per (sequence, head, 64-channel tile): the sequence's chunks in order, the state in
-// accumulators.  ckpt: [b][h][chunk][P][N], receives the state entering each chunk, or null.
+// A workgroup's segment: of sequence b, head h, tile pt the chunks [c0, c1), of which [c0, live) have tokens.
+struct sd_segment {
+    int64_t b, c0, c1, live, len;
+    int h, pt, seg;
+    __device__ __forceinline__ sd_segment(const sd_shape &s, const int32_t *lens) {
+        seg = blockIdx.x % s.nseg;
+        pt = blockIdx.x / s.nseg % s.PT;
+        h = blockIdx.x / s.nseg / s.PT % s.H;
+        b = blockIdx.x / s.nseg / s.PT / s.H;
+        len = lens ? min(max((int64_t)lens[b], (int64_t)0), s.L) : s.L;
+        c0 = seg * s.cps;
+        c1 = min(c0 + s.cps, s.nchunk);
+        live = max(c0, min(c1, (len + kSdQ - 1) / kSdQ));
+    }
+    // element (p, n) = (64 pt, 0) of the tile in [b][h][k of n][P][N]
+    __device__ __forceinline__ int64_t state_at(const sd_shape &s, int64_t n, int64_t k) const {
+        return (((b * s.H + h) * n + k) * s.P + (int64_t)pt * 64) * s.N;
+    }
+};
+
+// The states (or adjoints, REV) that the segments start from, from those that they leave when they start from zero:
+// one workgroup per 1024 elements of a (sequence, head).  seg: [b][h][segment][P N], in place.
+template <bool REV>
+__global__ void __launch_bounds__(256)
+sd_combine_kernel(const float *__restrict__ tok, const float *__restrict__ first, float *__restrict__ seg, sd_shape s, int blocks) {
+    extern __shared__ float dec[];   // nseg decays
+    const int64_t bh = blockIdx.x / blocks;
+    tok += bh * s.nchunk * kSdTok;
+    for (int k = threadIdx.x; k < s.nseg; k += 256) {
+        double sum = 0.0;
+        for (int64_t c = k * s.cps; c < min((k + 1) * s.cps, s.nchunk); ++c)
+            sum += (double)tok[c * kSdTok + kSdQ - 1] + (double)tok[c * kSdTok + 2 * kSdQ - 1];
+        dec[k] = hw_exp2((float)sum);
+    }
+    __syncthreads();
+    const int pn = s.P * s.N, e = (blockIdx.x % blocks * 256 + threadIdx.x) * 4;
+    if (e >= pn) return;
+    f32x4_t cur = first ? ld4(first + bh * pn + e) : f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int i = 0; i < s.nseg; ++i) {
+        const int k = REV ? s.nseg - 1 - i : i;
+        float *m = seg + (bh * s.nseg + k) * pn + e;
+        const f32x4_t own = ld4(m);
+        *reinterpret_cast<f32x4_t *>(m) = cur;
+        cur = cur * dec[k] + own;
+    }
+}
+
+// One workgroup per (sequence, head, 64-channel tile, segment): the segment's chunks in order, the state in
+// accumulators.  from: the segments' first states [b][h][segment][P][N], or null (zero); last: [b][h][P][N].  ckpt:
+// [b][h][chunk][P][N], receives the state entering each chunk, or null.
 template <typename E, int NT>
 __global__ void __launch_bounds__(kSdThreads)
 __attribute__((amdgpu_waves_per_eu(sd<E>::split && NT == 64 ? 3 : 2)))
 sd_scan_kernel(const typename sd<E>::io *__restrict__ u_, const float *__restrict__ tok, const float *__restrict__ Dv,
-               const int32_t *__restrict__ lens, const float *h0, typename sd<E>::io *__restrict__ y_, float *last,
+               const int32_t *__restrict__ lens, const float *from, typename sd<E>::io *__restrict__ y_, float *last,
                float *__restrict__ ckpt, sd_shape s) {
     using IO = typename sd<E>::io;
     using F = typename sd<E>::frag;
@@ -452,22 +502,22 @@ sd_scan_kernel(const typename sd<E>::io *__restrict__ u_, const float *__restric
     __shared__ sd_tokens tk;
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int c16 = lane & 15, q4 = 4 * (lane >> 4);
-    const int pt = blockIdx.x % s.PT, h = blockIdx.x / s.PT % s.H;
-    const int64_t b = blockIdx.x / s.PT / s.H;
+    const sd_segment at(s, lens);
+    const int64_t b = at.b, len = at.len;
+    const int h = at.h, pt = at.pt;
     const sd_view<IO> v(u_, s, b, h, pt);
     const E *xs = reinterpret_cast<const E *>(v.x), *Bs = reinterpret_cast<const E *>(v.B), *Cs = reinterpret_cast<const E *>(v.C);
-    const int64_t len = lens ? min(max((int64_t)lens[b], (int64_t)0), s.L) : s.L;
     const float skip = Dv ? Dv[h] : 0.0f;
     tok += (b * s.H + h) * s.nchunk * kSdTok;
-    const int64_t st_at = (b * s.H + h) * s.P * s.N + (int64_t)pt * 64 * s.N;
     IO *yb = y_ + (b * s.L * s.H + h) * s.P + pt * 64;
     f32x4_t S[NB];
-    if (h0) {
-        sd_load_state(S, h0 + st_at, s.N, v.pw, w, lane);
+    if (from) {
+        sd_load_state(S, from + at.state_at(s, s.nseg, at.seg), s.N, v.pw, w, lane);
     } else {
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) S[nb] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
     }
+    auto keep = [&](int64_t c) { sd_store_state(S, ckpt + at.state_at(s, s.nchunk, c), s.N, v.pw, w, lane); };
     tile64<E, NT> rB, rC;
     tile64<E, 64> rX;
     sd_tok rt = {};
@@ -478,16 +528,15 @@ sd_scan_kernel(const typename sd<E>::io *__restrict__ u_, const float *__restric
         rX.load(xs + t0 * s.dc, s.dc, rows, v.pw);
         if (w == 0) rt = sd_load_tokens(tok + t0 / kSdQ * kSdTok, lane);
     };
-    const int64_t live = (len + kSdQ - 1) / kSdQ;   // chunks with tokens
-    if (live > 0) fetch(0);
-    for (int64_t c = 0; c < live; ++c) {
+    if (at.c0 < at.live) fetch(at.c0 * kSdQ);
+    for (int64_t c = at.c0; c < at.live; ++c) {
         const int64_t t0 = c * kSdQ;
         rB.stage(tB);
         rC.stage(tC);
         rX.stage(tX);
         if (w == 0) sd_stage_tokens(tk, rt, lane);
-        if (c + 1 < live) fetch(t0 + kSdQ);
-        if (ckpt) sd_store_state(S, ckpt + (((b * s.H + h) * s.nchunk + c) * s.P + (int64_t)pt * 64) * s.N, s.N, v.pw, w, lane);
+        if (c + 1 < at.live) fetch(t0 + kSdQ);
+        if (ckpt) keep(c);
         __syncthreads();
         F xf[4];
 #pragma unroll
@@ -593,8 +642,8 @@ sd_scan_kernel(const typename sd<E>::io *__restrict__ u_, const float *__restric
         }
     }
     // chunks past the sequence's end: the state stays, y is zero
-    for (int64_t c = live; c < s.nchunk; ++c) {
-        if (ckpt) sd_store_state(S, ckpt + (((b * s.H + h) * s.nchunk + c) * s.P + (int64_t)pt * 64) * s.N, s.N, v.pw, w, lane);
+    for (int64_t c = at.live; c < at.c1; ++c) {
+        if (ckpt) keep(c);
         if (16 * w + q4 >= v.pw) continue;
         for (int j = 0; j < 4; ++j) {
             const int64_t t = c * kSdQ + 16 * j + c16;
@@ -603,7 +652,7 @@ sd_scan_kernel(const typename sd<E>::io *__restrict__ u_, const float *__restric
             for (int e = 0; e < 4; ++e) yp[e] = 0;
         }
     }
-    if (last) sd_store_state(S, last + st_at, s.N, v.pw, w, lane);
+    if (last && at.seg == s.nseg - 1) sd_store_state(S, last + at.state_at(s, 1, 0), s.N, v.pw, w, lane);
 }
 
 // ---- one token ------------------------------------------------------------------------------
