@@ -229,7 +229,7 @@ void launch_bwd(const void *u, const void *dy, const float *tok, const void *dt,
                 const ssm_ssd_conv_dims *dm, int flags, hipStream_t st) {
     using IO = typename ssm::sd<E>::io;
     const ssm::sd_shape s = shape_of(dm, flags);
-    hipLaunchKernelGGL((ssm::sd_bwd_kernel<E, NT>), dim3((unsigned)(dm->batch * s.nchunk * s.G * g.HS)), dim3(ssm::kSdThreads), 0, st,
+    hipLaunchKernelGGL((ssm::sd_bwd_kernel<E, NT>), dim3((unsigned)(dm->batch * s.nchunk * s.G * g.HS)), dim3(ssm::kSdBwdThreads), 0, st,
                        static_cast<const IO *>(u), static_cast<const IO *>(dy), tok, static_cast<const IO *>(dt), A, D, dt_bias, lens,
                        states, adjoints, static_cast<IO *>(ddt), g, s);
 }

@@ -104,34 +104,34 @@ sd_walk_kernel(const typename sd<E>::io *__restrict__ u_, const typename sd<E>::
     else if (to && at.seg == (ADJ ? 0 : s.nseg - 1)) sd_store_state(S, to + at.state_at(s, 1, 0), s.N, v.pw, w, lane);
 }
 
-// 64 x 64 of a state [p][n] in fp32 from memory to LDS, as NS operand parts.
-template <typename E, int NS> struct state64 {
-    static constexpr int NP = formed<E, NS>::N;
-    f32x4_t r[4];
+// What is formed in the backward is carried to 24 bits (three bf16 parts): the sums over tokens that u's gradient
+// goes into leave in fp32.
+constexpr int kSdParts = 3;
+
+constexpr int kSdBwdThreads = 512;
+
+// 64 x 64 of an adjoint [p][n] in fp32 from memory to LDS, as operand parts.
+template <typename E> struct state64 {
+    static constexpr int NP = formed<E, kSdParts>::N, NU = 1024 / kSdBwdThreads, RPP = kSdBwdThreads / 16;
+    f32x4_t r[NU];
     __device__ __forceinline__ void load(const float *m, int N, int pw, int nw) {   // N: row stride; pw x nw exist
+        const int p = threadIdx.x / 16, n = threadIdx.x % 16 * 4;
+        const char *base = reinterpret_cast<const char *>(m);
+        const uint32_t off = (uint32_t)(p * N + n) * 4u;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int id = threadIdx.x + kSdThreads * i, p = id / 16, n = id % 16 * 4;
+        for (int i = 0; i < NU; ++i) {
             r[i] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-            if (p < pw && n < nw) r[i] = ld4(m + (int64_t)p * N + n);
+            if (p + RPP * i < pw && n < nw) r[i] = *reinterpret_cast<const f32x4_t *>(base + (int64_t)(RPP * i * N) * 4 + off);
         }
     }
     __device__ __forceinline__ void stage(E (&t)[NP][64 * sd_ld<E>(64)]) const {
+        const int p = threadIdx.x / 16, n = threadIdx.x % 16 * 4;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int id = threadIdx.x + kSdThreads * i, p = id / 16, n = id % 16 * 4;
-            const formed<E, NS> f(r[i]);
+        for (int i = 0; i < NU; ++i) {
+            const formed<E, kSdParts> f(r[i]);
 #pragma unroll
-            for (int k = 0; k < NP; ++k) *reinterpret_cast<typename sd<E>::frag *>(&t[k][p * sd_ld<E>(64) + n]) = f.p[k];
+            for (int k = 0; k < NP; ++k) *reinterpret_cast<typename sd<E>::frag *>(&t[k][(p + RPP * i) * sd_ld<E>(64) + n]) = f.p[k];
         }
-    }
-    __device__ __forceinline__ float dot(const state64 &o) const {
-        float a = 0.0f;
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) a = fmaf(r[i][e], o.r[i][e], a);
-        return a;
     }
 };
 __device__ __forceinline__ double wave_last(double v) {
@@ -153,260 +153,387 @@ struct sd_grad {
     int HS, hpw;    // parts of a group's heads; heads per part
 };
 
-// One workgroup per (chunk, sequence, group, part of its heads), the heads in turn.  Wave w owns the 16 tokens
-// 16 w .. of the chunk (as s of T, G, v, dB and as t of dC).
+// One workgroup per (chunk, sequence, group, part of its heads), the heads in turn, the next one's rows and states
+// requested while one is worked on.  Eight waves: wave (w, z) owns the 16 tokens 16 w .. of the chunk as s of T, G and v, of
+// these the tokens t in blocks z and 3 - z of T and the channels 32 z .. of every 64 of v; and of every 64 states the 16
+// from 16 w, z = 0 of dC, z = 1 of dB.
 template <typename E, int NT>
-__global__ void __launch_bounds__(kSdThreads)
+__global__ void __launch_bounds__(kSdBwdThreads) __attribute__((amdgpu_waves_per_eu(2)))
 sd_bwd_kernel(const typename sd<E>::io *__restrict__ u_, const typename sd<E>::io *__restrict__ dy_,
               const float *__restrict__ tok, const typename sd<E>::io *__restrict__ dt, const float *__restrict__ A,
               const float *__restrict__ Dv, const float *__restrict__ dt_bias, const int32_t *__restrict__ lens,
-              const float *__restrict__ st_in,
-              const float *__restrict__ ds_out, typename sd<E>::io *__restrict__ ddt, sd_grad gr, sd_shape s) {
+              const float *__restrict__ st_in, const float *__restrict__ ds_out, typename sd<E>::io *__restrict__ ddt,
+              sd_grad gr, sd_shape s) {
     using IO = typename sd<E>::io;
     using F = typename sd<E>::frag;
-    constexpr int NB = NT / 16, NP = formed<E, 2>::N, LD = sd_ld<E>(64);
-    __shared__ __attribute__((aligned(16))) E tB[64 * sd_ld<E>(NT)], tC[64 * sd_ld<E>(NT)], tX[64 * LD], tY[64 * LD];
-    __shared__ __attribute__((aligned(16))) E tS[NP][64 * LD], tD[NP][64 * LD];
-    __shared__ sd_tokens tk;
-    __shared__ float to_end[64];                        // e^{c_last - c_t}
-    __shared__ float sR[4][64], sCol[64], sYS[64], sXS[64], sQ[64], sXY[64], sDot[4];
-    const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int c16 = lane & 15, q4 = 4 * (lane >> 4), mine = 16 * w + c16;   // the lane's token of the wave's 16
+    constexpr int NB = NT / 16, NH = NT / 64, NP = formed<E, kSdParts>::N, LD = sd_ld<E>(64);
+    // Two sets of an item's tiles where they fit in LDS: the next item's are staged while one is worked on, and a
+    // barrier an item is enough.
+    constexpr int NBUF = sd<E>::split || NT == 64 ? 2 : 1;
+    __shared__ __attribute__((aligned(16))) E tB[64 * sd_ld<E>(NT)], tC[64 * sd_ld<E>(NT)], tXs[NBUF][64 * LD], tYs[NBUF][64 * LD];
+    __shared__ __attribute__((aligned(16))) E tDs[NBUF][NP][64 * LD];
+    // a head's tokens and sums (heads in turn)
+    struct head_t {
+        sd_tokens tk;
+        float to_end[64], near[64], sig[64];            // e^{c_last - c_t}; e^{c_t - c_r}, r the first of t's 16 tokens; softplus'
+        float R[4][64], YS[4][64], col[2][64], XS[2][64], Q[2][64], XY[2][64], dot[4];
+    };
+    __shared__ __attribute__((aligned(16))) head_t hd[2];
+    const int lane = threadIdx.x & 63, w8 = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), w = w8 & 3, z = w8 >> 2;
+    const int c16 = lane & 15, q4 = 4 * (lane >> 4), mine = 16 * w + c16;   // mine: the lane's token of the wave's 16
     const int64_t chunk = blockIdx.x % s.nchunk, rest = blockIdx.x / s.nchunk;
     const int hs = rest % gr.HS, g = rest / gr.HS % s.G;
     const int64_t b = rest / gr.HS / s.G, t0 = chunk * kSdQ;
     const int per = s.H / s.G, h0 = g * per + hs * gr.hpw, h1 = min(h0 + gr.hpw, (g + 1) * per);
     const int64_t len = lens ? min(max((int64_t)lens[b], (int64_t)0), s.L) : s.L;
     const int rows = (int)min((int64_t)64, max(len - t0, (int64_t)0)), tokens = (int)min((int64_t)64, s.L - t0);
-    const bool have = t0 + mine < s.L;
+    const bool have = mine < tokens;
     const IO *ub = u_ + (b * s.L + t0) * s.dc, *dyb = dy_ + (b * s.L + t0) * s.H * s.P;
+
+    // An item: 64 states of 64 channels of a head.
+    struct item_t {
+        int h, pt, nh;
+    };
+    auto next = [&](item_t i) -> item_t {
+        if (i.nh + 64 < s.N) return {i.h, i.pt, i.nh + 64};
+        if (i.pt + 1 < s.PT) return {i.h, i.pt + 1, 0};
+        return {i.h + 1, 0, 0};
+    };
+    tile64<E, 64, kSdBwdThreads> rX, rY;
+    state64<E> rD;
+    f32x4_t rS[4];                       // (z = 0) the state entering, as operand: rows n (this wave's 16), k = p
+    sd_tok rt = {};
+    float rraw = 0.0f;
+    auto state_at = [&](item_t i) { return (((b * s.H + i.h) * s.nchunk + chunk) * s.P + (int64_t)i.pt * 64) * s.N + i.nh; };
+    auto fetch = [&](item_t i) {         // the tiles
+        if (i.h >= h1) return;
+        const int pw = min(64, s.P - i.pt * 64);
+        if (i.nh == 0) {
+            rX.load(reinterpret_cast<const E *>(ub + i.h * s.P + i.pt * 64), (uint32_t)s.dc, rows, pw);
+            rY.load(reinterpret_cast<const E *>(dyb + i.h * s.P + i.pt * 64), (uint32_t)(s.H * s.P), rows, pw);
+            if (i.pt == 0 && w8 == 7) {
+                rt = sd_load_tokens(tok + ((b * s.H + i.h) * s.nchunk + chunk) * kSdTok, lane);
+                if (lane < rows) rraw = io<IO>::ld(dt, (b * s.L + t0 + lane) * s.dt_stride + i.h) + (dt_bias ? dt_bias[i.h] : 0.0f);
+            }
+        }
+        rD.load(ds_out + state_at(i), s.N, pw, s.N - i.nh);
+    };
+    auto fetch_state = [&](item_t i) {
+        if (i.h >= h1 || z) return;
+        const int pw = min(64, s.P - i.pt * 64);
+        const char *m = reinterpret_cast<const char *>(st_in + state_at(i));
+        const uint32_t off = (uint32_t)(q4 * s.N + mine) * 4u;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {   // (groups of four channels exist or not as a whole)
+            rS[k] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+            if (16 * k + q4 < pw && mine < s.N - i.nh) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) rS[k][e] = *reinterpret_cast<const float *>(m + (int64_t)((16 * k + e) * s.N) * 4 + off);
+            }
+        }
+    };
+    int xbuf = 0, dbuf = 0;              // the current item's buffers (x and dy are a head's 64 channels', dS an item's)
+    auto stage = [&](item_t i, int xb, int db) {
+        if (i.h >= h1) return;
+        if (i.nh == 0) {
+            rX.stage(tXs[xb]);
+            rY.stage(tYs[xb]);
+            if (i.pt == 0 && w8 == 7) {
+                head_t &n = hd[i.h & 1];
+                n.to_end[lane] = sd_stage_tokens(n.tk, rt, lane);
+                const float rh = __shfl(rt.h, lane & 48, 64), rl = __shfl(rt.l, lane & 48, 64);
+                n.near[lane] = hw_exp2((rt.h - rh) + (rt.l - rl));
+                float sig = 1.0f;
+                if (s.softplus) softplus_f32(rraw, sig);
+                n.sig[lane] = lane < rows ? sig : 0.0f;
+            }
+        }
+        rD.stage(tDs[db]);
+    };
+    // from a head's sums over pairs of tokens to its gradients (one wave, token = lane)
+    auto finish = [&](int h) {
+        head_t &n = hd[h & 1];
+        const float a = A[h];
+        const double v = (double)(n.R[0][lane] + n.R[1][lane] + n.R[2][lane] + n.R[3][lane]) - (n.col[0][lane] + n.col[1][lane]) +
+                         (n.YS[0][lane] + n.YS[1][lane] + n.YS[2][lane] + n.YS[3][lane]);
+        const double p = wave_incl_sum64(v), x = n.XS[0][lane] + n.XS[1][lane], px = wave_incl_sum64(x);
+        const double ends = (double)n.tk.dec * ((n.dot[0] + n.dot[1]) + (n.dot[2] + n.dot[3]));
+        const float dg = (float)((wave_last(p) - p + v) + (px - x) + ends);
+        const float dr = (n.Q[0][lane] + n.Q[1][lane] + a * dg) * n.sig[lane];
+        if (lane < tokens) io<IO>::st(ddt, (b * s.L + t0 + lane) * s.H + h, dr);
+        const float pa = wave_sum(n.tk.dt[lane] * dg), pb = wave_sum(dr), pd = wave_sum(n.XY[0][lane] + n.XY[1][lane]);
+        if (lane == 0) {
+            float *o = gr.part + (b * s.nchunk + chunk) * 3 * s.H + h;
+            o[0] = pa;
+            o[s.H] = pb;
+            o[2 * s.H] = pd;
+        }
+    };
+    item_t now = {h0, 0, 0}, then = next(now);   // then: the item after
     {
-        tile64<E, NT> rB, rC;
+        tile64<E, NT, kSdBwdThreads> rB, rC;
         const E *B = reinterpret_cast<const E *>(ub + s.H * s.P + g * s.N);
-        rB.load(B, s.dc, rows, s.N);
-        rC.load(B + s.G * s.N, s.dc, rows, s.N);
+        rB.load(B, (uint32_t)s.dc, rows, s.N);
+        rC.load(B + s.G * s.N, (uint32_t)s.dc, rows, s.N);
+        fetch(now);
+        fetch_state(now);
         rB.stage(tB);
         rC.stage(tC);
+        if constexpr (NBUF == 2) {
+            stage(now, 0, 0);
+            fetch(then);
+        }
     }
-    __syncthreads();
-    f32x4_t G[4] = {}, Z[4] = {}, dB[NB] = {}, dC[NB] = {};
-#pragma unroll
-    for (int k = 0; k < NB; k += 2) {
-        const F b0 = ld_row<E, NT>(tB, 16 * w, 16 * k, lane), b1 = ld_row<E, NT>(tB, 16 * w, 16 * k + 16, lane);
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (i >= w) G[i] = mma(ld_row<E, NT>(tC, 16 * i, 16 * k, lane), ld_row<E, NT>(tC, 16 * i, 16 * k + 16, lane), b0, b1, G[i]);
-    }
+    // blocks of tokens t: z and 3 - z, of which those before w have nothing
+    const int tb[2] = {z, 3 - z};
+    f32x4_t Z[2] = {}, acc[NH][4] = {};   // acc: z = 0 dC^T[n][t], z = 1 dB^T[n][s]
     for (int h = h0; h < h1; ++h) {
-        const float a = A[h], skip = Dv ? Dv[h] : 0.0f;
-        float rdt = 0.0f, sig = 0.0f;
-        f32x4_t T[4] = {};
-        float xs = 0.0f, ys = 0.0f, q = 0.0f, dot = 0.0f, xy = 0.0f;
-        f32x4_t kk[4];
+        const float skip = Dv ? Dv[h] : 0.0f;
+        head_t &hn = hd[h & 1];
+        const sd_tokens &tk = hn.tk;
+        f32x4_t T[2] = {}, gk[4] = {}, kk[2] = {};   // gk: G K for t in all blocks; kk: K for t in the wave's two
+        float xs = 0.0f, q = 0.0f, dot = 0.0f, xy = 0.0f, ys[4] = {};
         for (int pt = 0; pt < s.PT; ++pt) {
-            const int pw = min(64, s.P - pt * 64);
-            const int64_t st_at = (((b * s.H + h) * s.nchunk + chunk) * s.P + (int64_t)pt * 64) * s.N;
-            f32x4_t V[4] = {};
-            F xf[4], yf[4];
-            for (int nh = 0; nh < s.N; nh += 64) {   // 64 states at a time
+            const int pw = min(64, s.P - pt * 64), xcur = xbuf;
+            f32x4_t V[2] = {};
+#pragma unroll
+            for (int half = 0; half < NH; ++half) {   // 64 states at a time
+                const int nh = 64 * half;
+                if (nh >= s.N) break;
                 __syncthreads();
-                if (nh == 0) {
-                    tile64<E, 64> rX, rY;
-                    rX.load(reinterpret_cast<const E *>(ub + h * s.P + pt * 64), s.dc, rows, pw);
-                    rY.load(reinterpret_cast<const E *>(dyb + h * s.P + pt * 64), (uint32_t)(s.H * s.P), rows, pw);
-                    rX.stage(tX);
-                    rY.stage(tY);
-                    if (pt == 0 && w == 0) {
-                        const sd_tok rt = sd_load_tokens(tok + ((b * s.H + h) * s.nchunk + chunk) * kSdTok, lane);
-                        to_end[lane] = sd_stage_tokens(tk, rt, lane);
-                        rdt = rt.d;
-                        sig = 0.0f;
-                        if (lane < rows) {
-                            sig = 1.0f;
-                            if (s.softplus) softplus_f32(io<IO>::ld(dt, (b * s.L + t0 + lane) * s.dt_stride + h) + (dt_bias ? dt_bias[h] : 0.0f), sig);
-                        }
-                    }
+                const formed<E, kSdParts> S[4] = {formed<E, kSdParts>(rS[0]), formed<E, kSdParts>(rS[1]), formed<E, kSdParts>(rS[2]), formed<E, kSdParts>(rS[3])};
+                if (nh == 0 && pt == 0 && h > h0 && w8 == 7) finish(h - 1);
+                if constexpr (NBUF == 2) {
+                    stage(then, xbuf ^ (then.nh == 0), dbuf ^ 1);
+                    fetch(next(then));
+                } else {
+                    stage(now, 0, 0);
+                    fetch(then);
+                    __syncthreads();
                 }
-                state64<E, 2> rS, rD;
-                rS.load(st_in + st_at + nh, s.N, pw, s.N - nh);
-                rD.load(ds_out + st_at + nh, s.N, pw, s.N - nh);
-                rS.stage(tS);
-                rD.stage(tD);
-                dot += rS.dot(rD);
-                __syncthreads();
-                const float et = tk.e[mine], ws = tk.w[mine];
-                if (nh == 0) {
+                const E *tX = tXs[xbuf], *tY = tYs[xbuf];
+                const E(&tD)[NP][64 * LD] = tDs[dbuf];
+                if (nh == 0 && pt == 0) {
+                    const float sh = tk.ch[mine], sl = tk.cl[mine];
+                    F b0[NB];
+#pragma unroll
+                    for (int k = 0; k < NB; ++k) b0[k] = ld_row<E, NT>(tB, 16 * w, 16 * k, lane);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        xf[i] = ld_row<E, 64>(tX, 16 * w, 16 * i, lane);
-                        yf[i] = ld_row<E, 64>(tY, 16 * w, 16 * i, lane);
-                    }
-                    // T[t][s], rows t >= s only
+                        if (i < w) continue;
+                        f32x4_t G = {};
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        if (i >= w) {
-#pragma unroll
-                            for (int k = 0; k < 4; k += 2)
-                                T[i] = mma(ld_row<E, 64>(tY, 16 * i, 16 * k, lane), ld_row<E, 64>(tY, 16 * i, 16 * k + 16, lane), xf[k], xf[k + 1], T[i]);
-                        }
-                    if (pt == 0) {
-                        const float sh = tk.ch[mine], sl = tk.cl[mine];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            kk[i] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-                            if (i < w) continue;
+                        for (int k = 0; k < NB; k += 2)
+                            G = mma(ld_row<E, NT>(tC, 16 * i, 16 * k, lane), ld_row<E, NT>(tC, 16 * i, 16 * k + 16, lane), b0[k], b0[k + 1], G);
+                        f32x4_t k4;
+                        if (i == w) {
                             const f32x4_t th = ld4(tk.ch + 16 * i + q4), tl = ld4(tk.cl + 16 * i + q4);
 #pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                if (16 * i + q4 + e >= mine) kk[i][e] = hw_exp2((th[e] - sh) + (tl[e] - sl));
+                            for (int e = 0; e < 4; ++e) k4[e] = q4 + e >= c16 ? hw_exp2((th[e] - sh) + (tl[e] - sl)) : 0.0f;
+                        } else {   // in two factors of at most 1, over the block's first token
+                            k4 = ld4(hn.near + 16 * i + q4) * hw_exp2((tk.ch[16 * i] - sh) + (tk.cl[16 * i] - sl));
                         }
+                        gk[i] = G * k4;
+                        if (i == tb[0]) kk[0] = k4;
+                        if (i == tb[1]) kk[1] = k4;
                     }
                 }
-                // through the state leaving the chunk: V^T[p][s] and dB^T[n][s]; through the state entering: dC^T[n][t]
+                if (nh == 0) {   // T[t][s]
 #pragma unroll
-                for (int k = 0; k < 4; k += 2) {
-                    if (nh + 16 * k >= NT) continue;
-                    const F b0 = ld_row<E, NT>(tB, 16 * w, nh + 16 * k, lane), b1 = ld_row<E, NT>(tB, 16 * w, nh + 16 * k + 16, lane);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-#pragma unroll
-                        for (int m = 0; m < NP; ++m)
-                            V[j] = mma(ld_row<E, 64>(tD[m], 16 * j, 16 * k, lane), ld_row<E, 64>(tD[m], 16 * j, 16 * k + 16, lane), b0, b1, V[j]);
-                }
-#pragma unroll
-                for (int half = 0; half < NT / 64; ++half) {
-                    if (nh != 64 * half) continue;
-#pragma unroll
-                    for (int nb = 0; nb < 4; ++nb) {
-                        f32x4_t db = {}, dc = {};
+                    for (int j = 0; j < 2; ++j) {
+                        if (tb[j] < w) continue;
 #pragma unroll
                         for (int k = 0; k < 4; k += 2)
-#pragma unroll
-                            for (int m = 0; m < NP; ++m) {
-                                db = mma(ld_col<E, 64>(tD[m], 16 * k, 16 * nb, lane), ld_col<E, 64>(tD[m], 16 * k + 16, 16 * nb, lane), xf[k], xf[k + 1], db);
-                                dc = mma(ld_col<E, 64>(tS[m], 16 * k, 16 * nb, lane), ld_col<E, 64>(tS[m], 16 * k + 16, 16 * nb, lane), yf[k], yf[k + 1], dc);
-                            }
-                        const f32x4_t cf = widen(ld_row<E, NT>(tC, 16 * w, nh + 16 * nb, lane));
-                        dc *= et;
-                        dB[4 * half + nb] += db * ws;
-                        dC[4 * half + nb] += dc;
-                        ys += dc[0] * cf[0] + dc[1] * cf[1] + dc[2] * cf[2] + dc[3] * cf[3];
+                            T[j] = mma(ld_row<E, 64>(tY, 16 * tb[j], 16 * k, lane), ld_row<E, 64>(tY, 16 * tb[j], 16 * k + 16, lane),
+                                       ld_row<E, 64>(tX, 16 * w, 16 * k, lane), ld_row<E, 64>(tX, 16 * w, 16 * k + 16, lane), T[j]);
                     }
                 }
+                if (z == 0) {   // through the state entering: dC^T[n][t]
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        f32x4_t v = widen(ld_col<E, 64>(tD[0], 16 * k, 16 * w, lane));
+#pragma unroll
+                        for (int m = 1; m < NP; ++m) v += widen(ld_col<E, 64>(tD[m], 16 * k, 16 * w, lane));
+                        dot += v[0] * rS[k][0] + v[1] * rS[k][1] + v[2] * rS[k][2] + v[3] * rS[k][3];
+                    }
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        F y0[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) y0[k] = ld_row<E, 64>(tY, 16 * j, 16 * k, lane);
+                        f32x4_t c0 = {}, c1 = {};
+#pragma unroll
+                        for (int m = 0; m < NP; ++m) {
+                            c0 = mma(S[0].p[m], S[1].p[m], y0[0], y0[1], c0);
+                            c1 = mma(S[2].p[m], S[3].p[m], y0[2], y0[3], c1);
+                        }
+                        c0 = (c0 + c1) * tk.e[16 * j + c16];
+                        const f32x4_t cf = widen(ld_row<E, NT>(tC, 16 * j, nh + 16 * w, lane));
+                        acc[half][j] += c0;
+                        ys[j] += c0[0] * cf[0] + c0[1] * cf[1] + c0[2] * cf[2] + c0[3] * cf[3];
+                    }
+                } else {        // through the state leaving: dB^T[n][s]
+                    F d0[NP][4];
+#pragma unroll
+                    for (int m = 0; m < NP; ++m)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) d0[m][k] = ld_col<E, 64>(tD[m], 16 * k, 16 * w, lane);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        F x0[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) x0[k] = ld_row<E, 64>(tX, 16 * j, 16 * k, lane);
+                        f32x4_t c0 = {}, c1 = {};
+#pragma unroll
+                        for (int m = 0; m < NP; ++m) {
+                            c0 = mma(d0[m][0], d0[m][1], x0[0], x0[1], c0);
+                            c1 = mma(d0[m][2], d0[m][3], x0[2], x0[3], c1);
+                        }
+                        acc[half][j] += (c0 + c1) * tk.w[16 * j + c16];
+                    }
+                }
+                fetch_state(then);
+                // and V^T[p][s]
+#pragma unroll
+                for (int k = 0; k < 4; k += 2) {
+                    const F b0 = ld_row<E, NT>(tB, 16 * w, nh + 16 * k, lane), b1 = ld_row<E, NT>(tB, 16 * w, nh + 16 * k + 16, lane);
+#pragma unroll
+                    for (int m = 0; m < NP; ++m)
+#pragma unroll
+                        for (int j = 0; j < 2; ++j)
+                            V[j] = mma(ld_row<E, 64>(tD[m], 32 * z + 16 * j, 16 * k, lane), ld_row<E, 64>(tD[m], 32 * z + 16 * j, 16 * k + 16, lane), b0, b1, V[j]);
+                }
+                if constexpr (NBUF == 2) {
+                    xbuf ^= then.nh == 0;
+                    dbuf ^= 1;
+                }
+                now = then;
+                then = next(then);
             }
             {
-                const float te = to_end[mine], d = tk.dt[mine];
-                float x0 = 0.0f, q0 = 0.0f;
+                const E *tX = tXs[xcur], *tY = tYs[xcur];
+                const float te = hn.to_end[mine], d = tk.dt[mine];
+                f32x4_t x[2], y[2];
+                float x0 = 0.0f;
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
+                for (int j = 0; j < 2; ++j) {
                     V[j] *= te;
-                    const f32x4_t x = widen(xf[j]), y = widen(yf[j]);
-                    x0 += V[j][0] * x[0] + V[j][1] * x[1] + V[j][2] * x[2] + V[j][3] * x[3];
-                    xy += x[0] * y[0] + x[1] * y[1] + x[2] * y[2] + x[3] * y[3];
+                    x[j] = widen(ld_row<E, 64>(tX, 16 * w, 32 * z + 16 * j, lane));
+                    y[j] = widen(ld_row<E, 64>(tY, 16 * w, 32 * z + 16 * j, lane));
+                    x0 += V[j][0] * x[j][0] + V[j][1] * x[j][1] + V[j][2] * x[j][2] + V[j][3] * x[j][3];
+                    xy += x[j][0] * y[j][0] + x[j][1] * y[j][1] + x[j][2] * y[j][2] + x[j][3] * y[j][3];
                 }
                 xs += x0 * d;
 #pragma unroll
                 for (int i = 0; i < 4; i += 2) {
                     if (i + 1 < w) continue;
-                    const formed<E, 2> g0(G[i] * kk[i]), g1(G[i + 1] * kk[i + 1]);
+                    const formed<E, kSdParts> g0(gk[i]), g1(gk[i + 1]);
+                    F y0[2], y1[2];
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        V[j] = mma_fb<E, 2>(ld_col<E, 64>(tY, 16 * i, 16 * j, lane), ld_col<E, 64>(tY, 16 * i + 16, 16 * j, lane), g0, g1, V[j]);
-                }
+                    for (int j = 0; j < 2; ++j) {
+                        y0[j] = ld_col<E, 64>(tY, 16 * i, 32 * z + 16 * j, lane);
+                        y1[j] = ld_col<E, 64>(tY, 16 * i + 16, 32 * z + 16 * j, lane);
+                    }
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const f32x4_t x = widen(xf[j]), y = widen(yf[j]);
-                    q0 += V[j][0] * x[0] + V[j][1] * x[1] + V[j][2] * x[2] + V[j][3] * x[3];
-                    if (have && 16 * j + q4 < pw)
-                        *reinterpret_cast<f32x4_t *>(gr.du + ((b * s.L + t0 + mine) * s.H + h) * s.P + pt * 64 + 16 * j + q4) = V[j] * d + y * skip;
+                    for (int m = 0; m < NP; ++m)
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) V[j] = mma(y0[j], y1[j], g0.p[m], g1.p[m], V[j]);
                 }
-                q += q0;
+                char *o = reinterpret_cast<char *>(gr.du + ((b * s.L + t0) * s.H + h) * s.P + pt * 64);
+                const uint32_t off = ((uint32_t)mine * (uint32_t)(s.H * s.P) + (uint32_t)(32 * z + q4)) * 4u;
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    q += V[j][0] * x[j][0] + V[j][1] * x[j][1] + V[j][2] * x[j][2] + V[j][3] * x[j][3];
+                    if (have && 32 * z + 16 * j + q4 < pw) *reinterpret_cast<f32x4_t *>(o + (off + 64 * j)) = V[j] * d + y[j] * skip;
+                }
             }
         }
         // the head's sums over pairs of tokens
         const float d = tk.dt[mine];
         float col = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const f32x4_t z = T[i] * kk[i] * d;
-            Z[i] += z;
+        for (int j = 0; j < 2; ++j) {
+            const int t = 16 * tb[j] + q4;
+            if (tb[j] < w) {
+                if (c16 < 4) hn.R[w][t + c16] = 0.0f;
+                continue;
+            }
+            Z[j] += T[j] * kk[j] * d;
+            // (G K of the wave's block: a copy by selection, as the blocks' number is the wave's)
+            f32x4_t gt = gk[0];
+            gt = tb[j] == 1 ? gk[1] : gt;
+            gt = tb[j] == 2 ? gk[2] : gt;
+            gt = tb[j] == 3 ? gk[3] : gt;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const int t = 16 * i + q4 + e;
-                const float wv = t > mine ? z[e] * G[i][e] : 0.0f;
+                const float wv = t + e > mine ? T[j][e] * gt[e] * d : 0.0f;
                 col += wv;
                 const float r = lanes_sum<16>(wv);
-                if (c16 == 0) sR[w][t] = r;
+                if (c16 == 0) hn.R[w][t + e] = r;
             }
         }
         col = quads_sum(col);
         xs = quads_sum(xs);
-        ys = quads_sum(ys);
         q = quads_sum(q);
         xy = quads_sum(xy);
-        dot = wave_sum(dot);
-        if (lane < 16) {
-            sCol[mine] = col;
-            sXS[mine] = xs;
-            sYS[mine] = ys;
-            sQ[mine] = q;
-            sXY[mine] = xy;
+        if (z == 0) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) ys[j] = quads_sum(ys[j]);
+            dot = wave_sum(dot);
+            if (lane == 0) hn.dot[w] = dot;
         }
-        if (lane == 0) sDot[w] = dot;
-        __syncthreads();
-        if (w == 0) {   // token = lane
-            const double v = (double)(sR[0][lane] + sR[1][lane] + sR[2][lane] + sR[3][lane]) - sCol[lane] + sYS[lane];
-            const double p = wave_incl_sum64(v), x = sXS[lane], px = wave_incl_sum64(x);
-            const double ends = (double)tk.dec * ((sDot[0] + sDot[1]) + (sDot[2] + sDot[3]));
-            const float dg = (float)((wave_last(p) - p + v) + (px - x) + ends);
-            const float dr = (sQ[lane] + a * dg) * sig;
-            if (lane < tokens) io<IO>::st(ddt, (b * s.L + t0 + lane) * s.H + h, dr);
-            const float pa = wave_sum(rdt * dg), pb = wave_sum(dr), pd = wave_sum(sXY[lane]);
-            if (lane == 0) {
-                float *o = gr.part + (b * s.nchunk + chunk) * 3 * s.H + h;
-                o[0] = pa;
-                o[s.H] = pb;
-                o[2 * s.H] = pd;
+        if (lane < 16) {
+            hn.col[z][mine] = col;
+            hn.XS[z][mine] = xs;
+            hn.Q[z][mine] = q;
+            hn.XY[z][mine] = xy;
+            if (z == 0) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) hn.YS[w][16 * j + c16] = ys[j];
             }
         }
     }
-    // the products that the group's heads share: Z to LDS as [t][s] for dC, from registers for dB
     __syncthreads();
+    if (w8 == 7) finish(h1 - 1);
+    // the products that the group's heads share, with Z [t][s] in LDS
+    E(&tD)[NP][64 * LD] = tDs[0];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const formed<E, 2> f(Z[i]);
+    for (int j = 0; j < 2; ++j) {
+        const formed<E, kSdParts> f(Z[j]);
 #pragma unroll
         for (int m = 0; m < NP; ++m)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) tS[m][(16 * i + q4 + e) * LD + mine] = f.p[m][e];
+            for (int e = 0; e < 4; ++e) tD[m][(16 * tb[j] + q4 + e) * LD + mine] = f.p[m][e];
     }
     __syncthreads();
+    float *o = gr.dbc + (((int64_t)hs * (gridDim.x / s.nchunk / gr.HS / s.G) + b) * s.L + t0) * 2 * s.G * s.N + g * s.N + (z ? 0 : s.G * s.N);
 #pragma unroll
-    for (int i = 0; i < 4; i += 2) {
-        const formed<E, 2> z0(Z[i]), z1(Z[i + 1]);
-        F r0[NP], r1[NP];
+    for (int half = 0; half < NH; ++half) {
+        const int n0 = 64 * half + 16 * w;
+        if (64 * half >= s.N) break;
 #pragma unroll
-        for (int m = 0; m < NP; ++m) {
-            r0[m] = ld_row<E, 64>(tS[m], 16 * w, 16 * i, lane);
-            r1[m] = ld_row<E, 64>(tS[m], 16 * w, 16 * i + 16, lane);
-        }
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb) {
-            dB[nb] = mma_fb<E, 2>(ld_col<E, NT>(tC, 16 * i, 16 * nb, lane), ld_col<E, NT>(tC, 16 * i + 16, 16 * nb, lane), z0, z1, dB[nb]);
+        for (int i = 0; i < 4; i += 2) {
+            const E *src = z ? tC : tB;   // dB: over t; dC: over s
+            const F f0 = ld_col<E, NT>(src, 16 * i, n0, lane), f1 = ld_col<E, NT>(src, 16 * i + 16, n0, lane);
 #pragma unroll
             for (int m = 0; m < NP; ++m)
-                dC[nb] = mma(ld_col<E, NT>(tB, 16 * i, 16 * nb, lane), ld_col<E, NT>(tB, 16 * i + 16, 16 * nb, lane), r0[m], r1[m], dC[nb]);
-        }
-    }
-    if (have) {
-        float *o = gr.dbc + (((int64_t)hs * (gridDim.x / s.nchunk / gr.HS / s.G) + b) * s.L + t0 + mine) * 2 * s.G * s.N + g * s.N;
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb) {
-            const int n = 16 * nb + q4;
-            if (n < s.N) {
-                *reinterpret_cast<f32x4_t *>(o + n) = dB[nb];
-                *reinterpret_cast<f32x4_t *>(o + s.G * s.N + n) = dC[nb];
-            }
+                for (int j = 0; j < 4; ++j) {
+                    F z0, z1;
+                    if (z) {
+                        z0 = ld_col<E, 64>(tD[m], 16 * i, 16 * j, lane);
+                        z1 = ld_col<E, 64>(tD[m], 16 * i + 16, 16 * j, lane);
+                    } else {
+                        z0 = ld_row<E, 64>(tD[m], 16 * j, 16 * i, lane);
+                        z1 = ld_row<E, 64>(tD[m], 16 * j, 16 * i + 16, lane);
+                    }
+                    acc[half][j] = mma(f0, f1, z0, z1, acc[half][j]);
+                }
+        }
+        if (n0 + q4 < s.N) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (16 * j + c16 < tokens) *reinterpret_cast<f32x4_t *>(o + (int64_t)(16 * j + c16) * 2 * s.G * s.N + n0 + q4) = acc[half][j];
         }
     }
 }

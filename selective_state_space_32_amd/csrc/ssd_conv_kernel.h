@@ -122,12 +122,12 @@ __device__ __forceinline__ f32x4_t widen(f32x4_t v) { return v; }
 
 // 64 rows (tokens) of W elements between memory and LDS, 16 bytes per thread and access.  Addresses are a
 // uniform base and a 32-bit offset per lane (64 rows of at most 2^25 elements of 4 bytes).
-template <typename E, int W> struct tile64 {
+template <typename E, int W, int THREADS = kSdThreads> struct tile64 {
     static constexpr int EPU = 16 / (int)sizeof(E);           // elements per unit
     static constexpr int UPR = W / EPU;                       // units per row
-    static constexpr int NU = 64 * UPR / kSdThreads;          // units per thread
-    static constexpr int RPP = kSdThreads / UPR;              // rows per pass
-    static_assert(64 * UPR % kSdThreads == 0, "whole units per thread");
+    static constexpr int NU = 64 * UPR / THREADS;             // units per thread
+    static constexpr int RPP = THREADS / UPR;                 // rows per pass
+    static_assert(64 * UPR % THREADS == 0, "whole units per thread");
     u32x4_t r[NU];
     // rows [0, rows) of `src` (elements `stride` apart), columns [0, cols); zeros elsewhere
     __device__ __forceinline__ void load(const E *src, uint32_t stride, int rows, int cols) {
@@ -344,33 +344,41 @@ sd_conv_kernel(const IO *__restrict__ x, int64_t xstride, const float *__restric
         for (int i = 0; i < kSdConvT; ++i) {
             if (t + i >= t1) break;
             IO o[kSdConvV];
+            float last[kSdConvV];
+            bool near[kSdConvV] = {};
 #pragma unroll
             for (int e = 0; e < kSdConvV; ++e) {
-                const float last = io_f32(now[i][e]);
+                last[e] = io_f32(now[i][e]);
                 float p = fmaf(wv[0][e], past[0][e], bv[e]);
                 p = fmaf(wv[1][e], past[1][e], p);
                 p = fmaf(wv[2][e], past[2][e], p);
-                p = fmaf(wv[3][e], last, p);
+                p = fmaf(wv[3][e], last[e], p);
                 if constexpr (sizeof(IO) == 2) {
                     float size = fmaf(fabsf(wv[0][e]), fabsf(past[0][e]), fabsf(bv[e]));
                     size = fmaf(fabsf(wv[1][e]), fabsf(past[1][e]), size);
                     size = fmaf(fabsf(wv[2][e]), fabsf(past[2][e]), size);
-                    size = fmaf(fabsf(wv[3][e]), fabsf(last), size);
-                    bool near;
-                    o[e] = f32_to_bf16(conv_silu(p, size, near));
-                    if (near) {
-                        double q = fma((double)wv[0][e], (double)past[0][e], (double)bv[e]);
-                        q = fma((double)wv[1][e], (double)past[1][e], q);
-                        q = fma((double)wv[2][e], (double)past[2][e], q);
-                        q = fma((double)wv[3][e], (double)last, q);
-                        o[e] = silu_bf16_64(q);
-                    }
+                    size = fmaf(fabsf(wv[3][e]), fabsf(last[e]), size);
+                    o[e] = f32_to_bf16(conv_silu(p, size, near[e]));
                 } else {
                     o[e] = silu_f32(p);
                 }
+            }
+            if (near[0] || near[1] || near[2] || near[3]) {   // (one branch a token: four cost a third more)
+#pragma unroll
+                for (int e = 0; e < kSdConvV; ++e)
+                    if (near[e]) {
+                        double q = fma((double)wv[0][e], (double)past[0][e], (double)bv[e]);
+                        q = fma((double)wv[1][e], (double)past[1][e], q);
+                        q = fma((double)wv[2][e], (double)past[2][e], q);
+                        q = fma((double)wv[3][e], (double)last[e], q);
+                        if constexpr (sizeof(IO) == 2) o[e] = silu_bf16_64(q);
+                    }
+            }
+#pragma unroll
+            for (int e = 0; e < kSdConvV; ++e) {
                 past[0][e] = past[1][e];
                 past[1][e] = past[2][e];
-                past[2][e] = last;
+                past[2][e] = last[e];
             }
             if (t + i >= len)
                 for (int e = 0; e < kSdConvV; ++e) o[e] = 0;
@@ -466,11 +474,13 @@ sd_combine_kernel(const float *__restrict__ tok, const float *__restrict__ first
     extern __shared__ float dec[];   // nseg decays
     const int64_t bh = blockIdx.x / blocks;
     tok += bh * s.nchunk * kSdTok;
-    for (int k = threadIdx.x; k < s.nseg; k += 256) {
+    for (int k = threadIdx.x >> 6; k < s.nseg; k += 4) {   // a wave per segment
         double sum = 0.0;
-        for (int64_t c = k * s.cps; c < min((k + 1) * s.cps, s.nchunk); ++c)
+        for (int64_t c = k * s.cps + (threadIdx.x & 63); c < min((k + 1) * s.cps, s.nchunk); c += 64)
             sum += (double)tok[c * kSdTok + kSdQ - 1] + (double)tok[c * kSdTok + 2 * kSdQ - 1];
-        dec[k] = hw_exp2((float)sum);
+#pragma unroll
+        for (int m = 1; m < 64; m *= 2) sum += __shfl_xor(sum, m, 64);
+        if ((threadIdx.x & 63) == 0) dec[k] = hw_exp2((float)sum);
     }
     __syncthreads();
     const int pn = s.P * s.N, e = (blockIdx.x % blocks * 256 + threadIdx.x) * 4;
