@@ -229,7 +229,9 @@ void launch_bwd(const void *u, const void *dy, const float *tok, const void *dt,
                 const ssm_ssd_conv_dims *dm, int flags, hipStream_t st) {
     using IO = typename ssm::sd<E>::io;
     const ssm::sd_shape s = shape_of(dm, flags);
-    hipLaunchKernelGGL((ssm::sd_bwd_kernel<E, NT>), dim3((unsigned)(dm->batch * s.nchunk * s.G * g.HS)), dim3(ssm::kSdBwdThreads), 0, st,
+    auto kern = s.N == 64 && s.P == 64 ? ssm::sd_bwd_kernel<E, NT, NT == 64 ? 2 : 1>
+              : s.N == NT && s.P % 64 == 0 ? ssm::sd_bwd_kernel<E, NT, 1> : ssm::sd_bwd_kernel<E, NT, 0>;
+    hipLaunchKernelGGL(kern, dim3((unsigned)(dm->batch * s.nchunk * s.G * g.HS)), dim3(ssm::kSdBwdThreads), 0, st,
                        static_cast<const IO *>(u), static_cast<const IO *>(dy), tok, static_cast<const IO *>(dt), A, D, dt_bias, lens,
                        states, adjoints, static_cast<IO *>(ddt), g, s);
 }
@@ -338,7 +340,7 @@ int ssm_ssd_conv_bwd(const void *xbc, const float *conv_w, const float *conv_b, 
     rc = check_workspace(workspace, workspace_bytes, ssm_ssd_conv_bwd_workspace_bytes(dims, flags));
     if (rc != SSM_OK) return rc;
     const BwdPlan p = bwd_plan(dims, kept);
-    if (!conv_grid(dims, 8, true).fits() || dims->batch * chunks(dims) > kMaxGrid / dims->ngroups / p.HS)
+    if (!conv_grid(dims, 8, true).fits() || dims->batch * chunks(dims) > kMaxGrid / dims->nheads)
         return fail(SSM_ERR_SHAPE, "batch*seqlen exceeds the grids of the backward");
     hipStream_t st = static_cast<hipStream_t>(stream);
     char *ws = static_cast<char *>(workspace);

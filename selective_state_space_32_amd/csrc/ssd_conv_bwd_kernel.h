@@ -108,7 +108,7 @@ sd_walk_kernel(const typename sd<E>::io *__restrict__ u_, const typename sd<E>::
 // goes into leave in fp32.
 constexpr int kSdParts = 3;
 
-constexpr int kSdBwdThreads = 512;
+constexpr int kSdBwdThreads = 1024;
 
 // 64 x 64 of an adjoint [p][n] in fp32 from memory to LDS, as operand parts.
 template <typename E> struct state64 {
@@ -154,11 +154,12 @@ struct sd_grad {
 };
 
 // One workgroup per (chunk, sequence, group, part of its heads), the heads in turn, the next one's rows and states
-// requested while one is worked on.  Eight waves: wave (w, z) owns the 16 tokens 16 w .. of the chunk as s of T, G and v, of
-// these the tokens t in blocks z and 3 - z of T and the channels 32 z .. of every 64 of v; and of every 64 states the 16
-// from 16 w, z = 0 of dC, z = 1 of dB.
-template <typename E, int NT>
-__global__ void __launch_bounds__(kSdBwdThreads) __attribute__((amdgpu_waves_per_eu(2)))
+// requested while one is worked on.  Sixteen waves, four to a SIMD, of four kinds: kind 0 owns of every 64 states the
+// 16 from 16 w of dC, kind 1 those of dB; kinds 2 and 3 (z = 0, 1) the 16 tokens 16 w .. of the chunk as s of T, G and v, of
+// these the tokens t in blocks z and 3 - z of T and the channels 32 z .. of every 64 of v.
+// MODE 1: whole tiles (P a multiple of 64, N = NT), without the checks for less; 2: and one item per head (P = N = 64).
+template <typename E, int NT, int MODE>
+__global__ void __launch_bounds__(kSdBwdThreads) __attribute__((amdgpu_waves_per_eu(4)))
 sd_bwd_kernel(const typename sd<E>::io *__restrict__ u_, const typename sd<E>::io *__restrict__ dy_,
               const float *__restrict__ tok, const typename sd<E>::io *__restrict__ dt, const float *__restrict__ A,
               const float *__restrict__ Dv, const float *__restrict__ dt_bias, const int32_t *__restrict__ lens,
@@ -166,6 +167,8 @@ sd_bwd_kernel(const typename sd<E>::io *__restrict__ u_, const typename sd<E>::i
               sd_grad gr, sd_shape s) {
     using IO = typename sd<E>::io;
     using F = typename sd<E>::frag;
+    constexpr bool FULL = MODE >= 1, ONE = MODE == 2;
+    const int N = FULL ? NT : s.N, P = ONE ? 64 : s.P;
     constexpr int NB = NT / 16, NH = NT / 64, NP = formed<E, kSdParts>::N, LD = sd_ld<E>(64);
     // Two sets of an item's tiles where they fit in LDS: the next item's are staged while one is worked on, and a
     // barrier an item is enough.
@@ -179,56 +182,58 @@ sd_bwd_kernel(const typename sd<E>::io *__restrict__ u_, const typename sd<E>::i
         float R[4][64], YS[4][64], col[2][64], XS[2][64], Q[2][64], XY[2][64], dot[4];
     };
     __shared__ __attribute__((aligned(16))) head_t hd[2];
-    const int lane = threadIdx.x & 63, w8 = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), w = w8 & 3, z = w8 >> 2;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), kind = wave >> 2, z = kind & 1;
+    // (a SIMD's waves are those of one wave % 4; the tokens' blocks have less to do the later they are)
+    const int w = kind == 3 ? 3 - (wave & 3) : wave & 3;
+    const bool first = wave < kSdBwdThreads / 128;   // this half of the threads moves B and x, the other C and dy
+    const int tid = threadIdx.x % (kSdBwdThreads / 2);
     const int c16 = lane & 15, q4 = 4 * (lane >> 4), mine = 16 * w + c16;   // mine: the lane's token of the wave's 16
-    const int64_t chunk = blockIdx.x % s.nchunk, rest = blockIdx.x / s.nchunk;
-    const int hs = rest % gr.HS, g = rest / gr.HS % s.G;
-    const int64_t b = rest / gr.HS / s.G, t0 = chunk * kSdQ;
+    const uint32_t nchunk = (uint32_t)s.nchunk, chunk = blockIdx.x % nchunk, rest = blockIdx.x / nchunk;
+    const int hs = rest % (uint32_t)gr.HS, g = rest / (uint32_t)gr.HS % (uint32_t)s.G;
+    const uint32_t b = rest / (uint32_t)gr.HS / (uint32_t)s.G;
+    const int64_t t0 = (int64_t)chunk * kSdQ;
     const int per = s.H / s.G, h0 = g * per + hs * gr.hpw, h1 = min(h0 + gr.hpw, (g + 1) * per);
     const int64_t len = lens ? min(max((int64_t)lens[b], (int64_t)0), s.L) : s.L;
     const int rows = (int)min((int64_t)64, max(len - t0, (int64_t)0)), tokens = (int)min((int64_t)64, s.L - t0);
     const bool have = mine < tokens;
-    const IO *ub = u_ + (b * s.L + t0) * s.dc, *dyb = dy_ + (b * s.L + t0) * s.H * s.P;
+    const IO *ub = u_ + (b * s.L + t0) * s.dc, *dyb = dy_ + (b * s.L + t0) * s.H * P;
 
     // An item: 64 states of 64 channels of a head.
     struct item_t {
         int h, pt, nh;
     };
     auto next = [&](item_t i) -> item_t {
-        if (i.nh + 64 < s.N) return {i.h, i.pt, i.nh + 64};
-        if (i.pt + 1 < s.PT) return {i.h, i.pt + 1, 0};
+        if (ONE) return {i.h + 1, 0, 0};
+        if (i.nh + 64 < N) return {i.h, i.pt, i.nh + 64};
+        if (i.pt + 1 < (P + 63) / 64) return {i.h, i.pt + 1, 0};
         return {i.h + 1, 0, 0};
     };
-    tile64<E, 64, kSdBwdThreads> rX, rY;
+    tile64<E, 64, kSdBwdThreads / 2> rXY;
     state64<E> rD;
-    f32x4_t rS[4];                       // (z = 0) the state entering, as operand: rows n (this wave's 16), k = p
-    sd_tok rt = {};
-    float rraw = 0.0f;
-    auto state_at = [&](item_t i) { return (((b * s.H + i.h) * s.nchunk + chunk) * s.P + (int64_t)i.pt * 64) * s.N + i.nh; };
+    f32x4_t rS[4];                       // (kind 0) the state entering, as operand: rows n (this wave's 16), k = p
+    auto state_at = [&](item_t i) {
+        return ((int64_t)((b * s.H + i.h) * nchunk + chunk) * P + (int64_t)i.pt * 64) * N + i.nh;
+    };
     auto fetch = [&](item_t i) {         // the tiles
         if (i.h >= h1) return;
-        const int pw = min(64, s.P - i.pt * 64);
+        const int pw = FULL ? 64 : min(64, P - i.pt * 64);
         if (i.nh == 0) {
-            rX.load(reinterpret_cast<const E *>(ub + i.h * s.P + i.pt * 64), (uint32_t)s.dc, rows, pw);
-            rY.load(reinterpret_cast<const E *>(dyb + i.h * s.P + i.pt * 64), (uint32_t)(s.H * s.P), rows, pw);
-            if (i.pt == 0 && w8 == 7) {
-                rt = sd_load_tokens(tok + ((b * s.H + i.h) * s.nchunk + chunk) * kSdTok, lane);
-                if (lane < rows) rraw = io<IO>::ld(dt, (b * s.L + t0 + lane) * s.dt_stride + i.h) + (dt_bias ? dt_bias[i.h] : 0.0f);
-            }
+            rXY.load(reinterpret_cast<const E *>((first ? ub : dyb) + i.h * P + i.pt * 64), (uint32_t)(first ? s.dc : s.H * P), rows, pw, tid);
         }
-        rD.load(ds_out + state_at(i), s.N, pw, s.N - i.nh);
+        rD.load(ds_out + state_at(i), N, pw, FULL ? 64 : N - i.nh);
     };
     auto fetch_state = [&](item_t i) {
-        if (i.h >= h1 || z) return;
-        const int pw = min(64, s.P - i.pt * 64);
+        if (i.h >= h1 || kind != 0) return;
+        const int pw = FULL ? 64 : min(64, P - i.pt * 64);
         const char *m = reinterpret_cast<const char *>(st_in + state_at(i));
-        const uint32_t off = (uint32_t)(q4 * s.N + mine) * 4u;
+        const uint32_t off = (uint32_t)(q4 * N + mine) * 4u, row = (uint32_t)N * 4u;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {   // (groups of four channels exist or not as a whole)
             rS[k] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-            if (16 * k + q4 < pw && mine < s.N - i.nh) {
+            if (FULL || (16 * k + q4 < pw && mine < N - i.nh)) {
+                const uint32_t at = off + 16 * k * row;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) rS[k][e] = *reinterpret_cast<const float *>(m + (int64_t)((16 * k + e) * s.N) * 4 + off);
+                for (int e = 0; e < 4; ++e) rS[k][e] = *reinterpret_cast<const float *>(m + (size_t)(e * row) + at);
             }
         }
     };
@@ -236,21 +241,29 @@ sd_bwd_kernel(const typename sd<E>::io *__restrict__ u_, const typename sd<E>::i
     auto stage = [&](item_t i, int xb, int db) {
         if (i.h >= h1) return;
         if (i.nh == 0) {
-            rX.stage(tXs[xb]);
-            rY.stage(tYs[xb]);
-            if (i.pt == 0 && w8 == 7) {
-                head_t &n = hd[i.h & 1];
-                n.to_end[lane] = sd_stage_tokens(n.tk, rt, lane);
-                const float rh = __shfl(rt.h, lane & 48, 64), rl = __shfl(rt.l, lane & 48, 64);
-                n.near[lane] = hw_exp2((rt.h - rh) + (rt.l - rl));
-                float sig = 1.0f;
-                if (s.softplus) softplus_f32(rraw, sig);
-                n.sig[lane] = lane < rows ? sig : 0.0f;
-            }
+            rXY.stage(first ? tXs[xb] : tYs[xb], tid);
         }
         rD.stage(tDs[db]);
     };
-    // from a head's sums over pairs of tokens to its gradients (one wave, token = lane)
+    // One wave's (of kind 1, the last): the next head's tokens, token = lane.
+    sd_tok rt = {};
+    float rraw = 0.0f;
+    auto fetch_tokens = [&](int h) {
+        if (h >= h1) return;
+        rt = sd_load_tokens(tok + (int64_t)((b * s.H + h) * nchunk + chunk) * kSdTok, lane);
+        if (lane < rows) rraw = io<IO>::ld(dt, ((int64_t)b * s.L + t0 + lane) * s.dt_stride + h) + (dt_bias ? dt_bias[h] : 0.0f);
+    };
+    auto stage_tokens = [&](int h) {
+        if (h >= h1) return;
+        head_t &n = hd[h & 1];
+        n.to_end[lane] = sd_stage_tokens(n.tk, rt, lane);
+        const float rh = __shfl(rt.h, lane & 48, 64), rl = __shfl(rt.l, lane & 48, 64);
+        n.near[lane] = hw_exp2((rt.h - rh) + (rt.l - rl));
+        float sig = 1.0f;
+        if (s.softplus) softplus_f32(rraw, sig);
+        n.sig[lane] = lane < rows ? sig : 0.0f;
+    };
+    // and from a head's sums over pairs of tokens to its gradients
     auto finish = [&](int h) {
         head_t &n = hd[h & 1];
         const float a = A[h];
@@ -269,150 +282,227 @@ sd_bwd_kernel(const typename sd<E>::io *__restrict__ u_, const typename sd<E>::i
             o[2 * s.H] = pd;
         }
     };
-    item_t now = {h0, 0, 0}, then = next(now);   // then: the item after
+    // The kinds' loops over the items are apart, so that each kind's registers are its own; every wave comes by the
+    // same barriers: one (two with a single set of tiles) at an item's start, two at the end.
+    const item_t start = {h0, 0, 0};
     {
-        tile64<E, NT, kSdBwdThreads> rB, rC;
-        const E *B = reinterpret_cast<const E *>(ub + s.H * s.P + g * s.N);
-        rB.load(B, (uint32_t)s.dc, rows, s.N);
-        rC.load(B + s.G * s.N, (uint32_t)s.dc, rows, s.N);
-        fetch(now);
-        fetch_state(now);
-        rB.stage(tB);
-        rC.stage(tC);
+        tile64<E, NT, kSdBwdThreads / 2> rBC;
+        rBC.load(reinterpret_cast<const E *>(ub + s.H * P + g * N) + (first ? 0 : s.G * N), (uint32_t)s.dc, rows, FULL ? NT : N, tid);
+        fetch(start);
+        rBC.stage(first ? tB : tC, tid);
         if constexpr (NBUF == 2) {
-            stage(now, 0, 0);
-            fetch(then);
+            stage(start, 0, 0);
+            fetch(next(start));
+        }
+        if (wave == 7) {
+            fetch_tokens(h0);
+            stage_tokens(h0);
+            fetch_tokens(h0 + 1);
         }
     }
-    // blocks of tokens t: z and 3 - z, of which those before w have nothing
-    const int tb[2] = {z, 3 - z};
-    f32x4_t Z[2] = {}, acc[NH][4] = {};   // acc: z = 0 dC^T[n][t], z = 1 dB^T[n][s]
-    for (int h = h0; h < h1; ++h) {
-        const float skip = Dv ? Dv[h] : 0.0f;
-        head_t &hn = hd[h & 1];
-        const sd_tokens &tk = hn.tk;
-        f32x4_t T[2] = {}, gk[4] = {}, kk[2] = {};   // gk: G K for t in all blocks; kk: K for t in the wave's two
-        float xs = 0.0f, q = 0.0f, dot = 0.0f, xy = 0.0f, ys[4] = {};
-        for (int pt = 0; pt < s.PT; ++pt) {
-            const int pw = min(64, s.P - pt * 64), xcur = xbuf;
-            f32x4_t V[2] = {};
+    auto begin = [&](item_t now, item_t then) {
+        __syncthreads();
+        if constexpr (NBUF == 2) {
+            stage(then, xbuf ^ (then.nh == 0), dbuf ^ 1);
+            fetch(next(then));
+        } else {
+            stage(now, 0, 0);
+            fetch(then);
+            __syncthreads();
+        }
+    };
+    auto turn = [&](item_t then) {   // to the other buffers
+        if constexpr (NBUF == 2) {
+            xbuf ^= then.nh == 0;
+            dbuf ^= 1;
+        }
+    };
+    using parts_t = E[NP][64 * LD];
+    // kinds 0 and 1, in the end: the products that the group's heads share, with Z [t][s] in LDS.  src: C for dB (over
+    // t), B for dC (over s)
+    auto shared_products = [&](f32x4_t (&acc)[NH][4], const E *src, bool over_t) {
+        const parts_t &tZ = tDs[0];
+        float *o = gr.dbc + (((int64_t)hs * (gridDim.x / nchunk / (uint32_t)gr.HS / (uint32_t)s.G) + b) * s.L + t0) * 2 * s.G * N + g * N + (over_t ? 0 : s.G * N);
 #pragma unroll
-            for (int half = 0; half < NH; ++half) {   // 64 states at a time
-                const int nh = 64 * half;
-                if (nh >= s.N) break;
-                __syncthreads();
-                const formed<E, kSdParts> S[4] = {formed<E, kSdParts>(rS[0]), formed<E, kSdParts>(rS[1]), formed<E, kSdParts>(rS[2]), formed<E, kSdParts>(rS[3])};
-                if (nh == 0 && pt == 0 && h > h0 && w8 == 7) finish(h - 1);
-                if constexpr (NBUF == 2) {
-                    stage(then, xbuf ^ (then.nh == 0), dbuf ^ 1);
-                    fetch(next(then));
-                } else {
-                    stage(now, 0, 0);
-                    fetch(then);
-                    __syncthreads();
-                }
-                const E *tX = tXs[xbuf], *tY = tYs[xbuf];
-                const E(&tD)[NP][64 * LD] = tDs[dbuf];
-                if (nh == 0 && pt == 0) {
-                    const float sh = tk.ch[mine], sl = tk.cl[mine];
-                    F b0[NB];
+        for (int half = 0; half < NH; ++half) {
+            const int n0 = 64 * half + 16 * w;
+            if (64 * half >= N) break;
 #pragma unroll
-                    for (int k = 0; k < NB; ++k) b0[k] = ld_row<E, NT>(tB, 16 * w, 16 * k, lane);
+            for (int i = 0; i < 4; i += 2) {
+                const F f0 = ld_col<E, NT>(src, 16 * i, n0, lane), f1 = ld_col<E, NT>(src, 16 * i + 16, n0, lane);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        if (i < w) continue;
-                        f32x4_t G = {};
-#pragma unroll
-                        for (int k = 0; k < NB; k += 2)
-                            G = mma(ld_row<E, NT>(tC, 16 * i, 16 * k, lane), ld_row<E, NT>(tC, 16 * i, 16 * k + 16, lane), b0[k], b0[k + 1], G);
-                        f32x4_t k4;
-                        if (i == w) {
-                            const f32x4_t th = ld4(tk.ch + 16 * i + q4), tl = ld4(tk.cl + 16 * i + q4);
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) k4[e] = q4 + e >= c16 ? hw_exp2((th[e] - sh) + (tl[e] - sl)) : 0.0f;
-                        } else {   // in two factors of at most 1, over the block's first token
-                            k4 = ld4(hn.near + 16 * i + q4) * hw_exp2((tk.ch[16 * i] - sh) + (tk.cl[16 * i] - sl));
-                        }
-                        gk[i] = G * k4;
-                        if (i == tb[0]) kk[0] = k4;
-                        if (i == tb[1]) kk[1] = k4;
-                    }
-                }
-                if (nh == 0) {   // T[t][s]
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        if (tb[j] < w) continue;
-#pragma unroll
-                        for (int k = 0; k < 4; k += 2)
-                            T[j] = mma(ld_row<E, 64>(tY, 16 * tb[j], 16 * k, lane), ld_row<E, 64>(tY, 16 * tb[j], 16 * k + 16, lane),
-                                       ld_row<E, 64>(tX, 16 * w, 16 * k, lane), ld_row<E, 64>(tX, 16 * w, 16 * k + 16, lane), T[j]);
-                    }
-                }
-                if (z == 0) {   // through the state entering: dC^T[n][t]
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        f32x4_t v = widen(ld_col<E, 64>(tD[0], 16 * k, 16 * w, lane));
-#pragma unroll
-                        for (int m = 1; m < NP; ++m) v += widen(ld_col<E, 64>(tD[m], 16 * k, 16 * w, lane));
-                        dot += v[0] * rS[k][0] + v[1] * rS[k][1] + v[2] * rS[k][2] + v[3] * rS[k][3];
-                    }
+                for (int m = 0; m < NP; ++m)
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        F y0[4];
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) y0[k] = ld_row<E, 64>(tY, 16 * j, 16 * k, lane);
-                        f32x4_t c0 = {}, c1 = {};
-#pragma unroll
-                        for (int m = 0; m < NP; ++m) {
-                            c0 = mma(S[0].p[m], S[1].p[m], y0[0], y0[1], c0);
-                            c1 = mma(S[2].p[m], S[3].p[m], y0[2], y0[3], c1);
-                        }
-                        c0 = (c0 + c1) * tk.e[16 * j + c16];
-                        const f32x4_t cf = widen(ld_row<E, NT>(tC, 16 * j, nh + 16 * w, lane));
-                        acc[half][j] += c0;
-                        ys[j] += c0[0] * cf[0] + c0[1] * cf[1] + c0[2] * cf[2] + c0[3] * cf[3];
+                        const F z0 = over_t ? ld_col<E, 64>(tZ[m], 16 * i, 16 * j, lane) : ld_row<E, 64>(tZ[m], 16 * j, 16 * i, lane);
+                        const F z1 = over_t ? ld_col<E, 64>(tZ[m], 16 * i + 16, 16 * j, lane) : ld_row<E, 64>(tZ[m], 16 * j, 16 * i + 16, lane);
+                        acc[half][j] = mma(f0, f1, z0, z1, acc[half][j]);
                     }
-                } else {        // through the state leaving: dB^T[n][s]
-                    F d0[NP][4];
-#pragma unroll
-                    for (int m = 0; m < NP; ++m)
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) d0[m][k] = ld_col<E, 64>(tD[m], 16 * k, 16 * w, lane);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        F x0[4];
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) x0[k] = ld_row<E, 64>(tX, 16 * j, 16 * k, lane);
-                        f32x4_t c0 = {}, c1 = {};
-#pragma unroll
-                        for (int m = 0; m < NP; ++m) {
-                            c0 = mma(d0[m][0], d0[m][1], x0[0], x0[1], c0);
-                            c1 = mma(d0[m][2], d0[m][3], x0[2], x0[3], c1);
-                        }
-                        acc[half][j] += (c0 + c1) * tk.w[16 * j + c16];
-                    }
-                }
-                fetch_state(then);
-                // and V^T[p][s]
-#pragma unroll
-                for (int k = 0; k < 4; k += 2) {
-                    const F b0 = ld_row<E, NT>(tB, 16 * w, nh + 16 * k, lane), b1 = ld_row<E, NT>(tB, 16 * w, nh + 16 * k + 16, lane);
-#pragma unroll
-                    for (int m = 0; m < NP; ++m)
-#pragma unroll
-                        for (int j = 0; j < 2; ++j)
-                            V[j] = mma(ld_row<E, 64>(tD[m], 32 * z + 16 * j, 16 * k, lane), ld_row<E, 64>(tD[m], 32 * z + 16 * j, 16 * k + 16, lane), b0, b1, V[j]);
-                }
-                if constexpr (NBUF == 2) {
-                    xbuf ^= then.nh == 0;
-                    dbuf ^= 1;
-                }
-                now = then;
-                then = next(then);
             }
-            {
-                const E *tX = tXs[xcur], *tY = tYs[xcur];
-                const float te = hn.to_end[mine], d = tk.dt[mine];
+            if (FULL || n0 + q4 < N) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (16 * j + c16 < tokens) *reinterpret_cast<f32x4_t *>(o + (int64_t)(16 * j + c16) * 2 * s.G * N + n0 + q4) = acc[half][j];
+            }
+        }
+    };
+    if (kind == 0) {   // through the state entering: dC^T[n][t]
+        f32x4_t acc[NH][4] = {};
+        float dot = 0.0f, ys[4] = {};
+        fetch_state(start);
+        for (item_t now = start, then = next(now); now.h < h1; now = then, then = next(then)) {
+            begin(now, then);
+            const sd_tokens &tk = hd[now.h & 1].tk;
+            const E *tY = tYs[xbuf];
+            const parts_t &tD = tDs[dbuf];
+            const formed<E, kSdParts> S[4] = {formed<E, kSdParts>(rS[0]), formed<E, kSdParts>(rS[1]), formed<E, kSdParts>(rS[2]), formed<E, kSdParts>(rS[3])};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                f32x4_t v = widen(ld_col<E, 64>(tD[0], 16 * k, 16 * w, lane));
+#pragma unroll
+                for (int m = 1; m < NP; ++m) v += widen(ld_col<E, 64>(tD[m], 16 * k, 16 * w, lane));
+                dot += v[0] * rS[k][0] + v[1] * rS[k][1] + v[2] * rS[k][2] + v[3] * rS[k][3];
+            }
+            fetch_state(then);
+#pragma unroll
+            for (int half = 0; half < NH; ++half) {
+                if (now.nh != 64 * half) continue;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    F y0[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) y0[k] = ld_row<E, 64>(tY, 16 * j, 16 * k, lane);
+                    f32x4_t c0 = {}, c1 = {};
+#pragma unroll
+                    for (int m = 0; m < NP; ++m) {
+                        c0 = mma(S[0].p[m], S[1].p[m], y0[0], y0[1], c0);
+                        c1 = mma(S[2].p[m], S[3].p[m], y0[2], y0[3], c1);
+                    }
+                    c0 = (c0 + c1) * tk.e[16 * j + c16];
+                    const f32x4_t cf = widen(ld_row<E, NT>(tC, 16 * j, 64 * half + 16 * w, lane));
+                    acc[half][j] += c0;
+                    ys[j] += c0[0] * cf[0] + c0[1] * cf[1] + c0[2] * cf[2] + c0[3] * cf[3];
+                }
+            }
+            if (then.h != now.h) {
+                head_t &hn = hd[now.h & 1];
+                dot = wave_sum(dot);
+                if (lane == 0) hn.dot[w] = dot;
+                dot = 0.0f;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float r = quads_sum(ys[j]);
+                    if (lane < 16) hn.YS[w][16 * j + c16] = r;
+                    ys[j] = 0.0f;
+                }
+            }
+            turn(then);
+        }
+        __syncthreads();
+        __syncthreads();
+        shared_products(acc, tB, false);
+    } else if (kind == 1) {   // through the state leaving: dB^T[n][s]
+        f32x4_t acc[NH][4] = {};
+        for (item_t now = start, then = next(now); now.h < h1; now = then, then = next(then)) {
+            begin(now, then);
+            if (wave == 7 && now.nh == 0 && now.pt == 0) {   // (the head before is done, its tokens' place free)
+                if (now.h > h0) finish(now.h - 1);
+                stage_tokens(now.h + 1);
+                fetch_tokens(now.h + 2);
+            }
+            const sd_tokens &tk = hd[now.h & 1].tk;
+            const E *tX = tXs[xbuf];
+            const parts_t &tD = tDs[dbuf];
+            F d0[NP][4];
+#pragma unroll
+            for (int m = 0; m < NP; ++m)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) d0[m][k] = ld_col<E, 64>(tD[m], 16 * k, 16 * w, lane);
+#pragma unroll
+            for (int half = 0; half < NH; ++half) {
+                if (now.nh != 64 * half) continue;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    F x0[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) x0[k] = ld_row<E, 64>(tX, 16 * j, 16 * k, lane);
+                    f32x4_t c0 = {}, c1 = {};
+#pragma unroll
+                    for (int m = 0; m < NP; ++m) {
+                        c0 = mma(d0[m][0], d0[m][1], x0[0], x0[1], c0);
+                        c1 = mma(d0[m][2], d0[m][3], x0[2], x0[3], c1);
+                    }
+                    acc[half][j] += (c0 + c1) * tk.w[16 * j + c16];
+                }
+            }
+            turn(then);
+        }
+        __syncthreads();
+        if (wave == 7) finish(h1 - 1);
+        __syncthreads();
+        shared_products(acc, tC, true);
+    } else {
+        // blocks of tokens t: z and 3 - z, of which those before w have nothing
+        const int tb[2] = {z, 3 - z};
+        f32x4_t Z[2] = {}, T[2], V[2], gk[4], kk[2];   // gk: G K for t in all blocks; kk: K for t in the wave's two
+        float xs = 0.0f, q = 0.0f, xy = 0.0f;
+        for (item_t now = start, then = next(now); now.h < h1; now = then, then = next(then)) {
+            begin(now, then);
+            head_t &hn = hd[now.h & 1];
+            const sd_tokens &tk = hn.tk;
+            const E *tX = tXs[xbuf], *tY = tYs[xbuf];
+            const parts_t &tD = tDs[dbuf];
+            if (now.nh == 0 && now.pt == 0) {
+                const float sh = tk.ch[mine], sl = tk.cl[mine];
+#pragma unroll
+                for (int j = 0; j < 2; ++j) T[j] = kk[j] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    gk[i] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+                    if (i < w) continue;
+                    f32x4_t G = {};
+#pragma unroll
+                    for (int k = 0; k < NB; k += 2)
+                        G = mma(ld_row<E, NT>(tC, 16 * i, 16 * k, lane), ld_row<E, NT>(tC, 16 * i, 16 * k + 16, lane),
+                                ld_row<E, NT>(tB, 16 * w, 16 * k, lane), ld_row<E, NT>(tB, 16 * w, 16 * k + 16, lane), G);
+                    f32x4_t k4;
+                    if (i == w) {
+                        const f32x4_t th = ld4(tk.ch + 16 * i + q4), tl = ld4(tk.cl + 16 * i + q4);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) k4[e] = q4 + e >= c16 ? hw_exp2((th[e] - sh) + (tl[e] - sl)) : 0.0f;
+                    } else {   // in two factors of at most 1, over the block's first token
+                        k4 = ld4(hn.near + 16 * i + q4) * hw_exp2((tk.ch[16 * i] - sh) + (tk.cl[16 * i] - sl));
+                    }
+                    gk[i] = G * k4;
+                    if (i == tb[0]) kk[0] = k4;
+                    if (i == tb[1]) kk[1] = k4;
+                }
+            }
+            if (now.nh == 0) {   // T[t][s]
+                V[0] = V[1] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    if (tb[j] < w) continue;
+#pragma unroll
+                    for (int k = 0; k < 4; k += 2)
+                        T[j] = mma(ld_row<E, 64>(tY, 16 * tb[j], 16 * k, lane), ld_row<E, 64>(tY, 16 * tb[j], 16 * k + 16, lane),
+                                   ld_row<E, 64>(tX, 16 * w, 16 * k, lane), ld_row<E, 64>(tX, 16 * w, 16 * k + 16, lane), T[j]);
+                }
+            }
+            // through the state leaving: V^T[p][s]
+#pragma unroll
+            for (int k = 0; k < 4; k += 2) {
+                const F b0 = ld_row<E, NT>(tB, 16 * w, now.nh + 16 * k, lane), b1 = ld_row<E, NT>(tB, 16 * w, now.nh + 16 * k + 16, lane);
+#pragma unroll
+                for (int m = 0; m < NP; ++m)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+                        V[j] = mma(ld_row<E, 64>(tD[m], 32 * z + 16 * j, 16 * k, lane), ld_row<E, 64>(tD[m], 32 * z + 16 * j, 16 * k + 16, lane), b0, b1, V[j]);
+            }
+            const float d = tk.dt[mine];
+            if (then.nh == 0) {   // the 64 channels' last states: v is whole but for the pairs of tokens
+                const int pw = FULL ? 64 : min(64, P - now.pt * 64);
+                const float te = hn.to_end[mine];
                 f32x4_t x[2], y[2];
                 float x0 = 0.0f;
 #pragma unroll
@@ -439,102 +529,62 @@ sd_bwd_kernel(const typename sd<E>::io *__restrict__ u_, const typename sd<E>::i
 #pragma unroll
                         for (int j = 0; j < 2; ++j) V[j] = mma(y0[j], y1[j], g0.p[m], g1.p[m], V[j]);
                 }
-                char *o = reinterpret_cast<char *>(gr.du + ((b * s.L + t0) * s.H + h) * s.P + pt * 64);
-                const uint32_t off = ((uint32_t)mine * (uint32_t)(s.H * s.P) + (uint32_t)(32 * z + q4)) * 4u;
+                const float skip = Dv ? Dv[now.h] : 0.0f;
+                char *o = reinterpret_cast<char *>(gr.du + ((b * s.L + t0) * s.H + now.h) * P + now.pt * 64);
+                const uint32_t off = ((uint32_t)mine * (uint32_t)(s.H * P) + (uint32_t)(32 * z + q4)) * 4u;
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
                     q += V[j][0] * x[j][0] + V[j][1] * x[j][1] + V[j][2] * x[j][2] + V[j][3] * x[j][3];
-                    if (have && 32 * z + 16 * j + q4 < pw) *reinterpret_cast<f32x4_t *>(o + (off + 64 * j)) = V[j] * d + y[j] * skip;
+                    if (have && (FULL || 32 * z + 16 * j + q4 < pw)) *reinterpret_cast<f32x4_t *>(o + (off + 64 * j)) = V[j] * d + y[j] * skip;
                 }
             }
+            if (then.h != now.h) {   // the head's sums over pairs of tokens
+                float col = 0.0f;
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const int t = 16 * tb[j] + q4;
+                    if (tb[j] < w) {
+                        if (c16 < 4) hn.R[w][t + c16] = 0.0f;
+                        continue;
+                    }
+                    Z[j] += T[j] * kk[j] * d;
+                    // (G K of the wave's block: a copy by selection, as the blocks' number is the wave's)
+                    f32x4_t gt = gk[0];
+                    gt = tb[j] == 1 ? gk[1] : gt;
+                    gt = tb[j] == 2 ? gk[2] : gt;
+                    gt = tb[j] == 3 ? gk[3] : gt;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float wv = t + e > mine ? T[j][e] * gt[e] * d : 0.0f;
+                        col += wv;
+                        const float r = lanes_sum<16>(wv);
+                        if (c16 == 0) hn.R[w][t + e] = r;
+                    }
+                }
+                col = quads_sum(col);
+                xs = quads_sum(xs);
+                q = quads_sum(q);
+                xy = quads_sum(xy);
+                if (lane < 16) {
+                    hn.col[z][mine] = col;
+                    hn.XS[z][mine] = xs;
+                    hn.Q[z][mine] = q;
+                    hn.XY[z][mine] = xy;
+                }
+                xs = q = xy = 0.0f;
+            }
+            turn(then);
         }
-        // the head's sums over pairs of tokens
-        const float d = tk.dt[mine];
-        float col = 0.0f;
+        __syncthreads();
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-            const int t = 16 * tb[j] + q4;
-            if (tb[j] < w) {
-                if (c16 < 4) hn.R[w][t + c16] = 0.0f;
-                continue;
-            }
-            Z[j] += T[j] * kk[j] * d;
-            // (G K of the wave's block: a copy by selection, as the blocks' number is the wave's)
-            f32x4_t gt = gk[0];
-            gt = tb[j] == 1 ? gk[1] : gt;
-            gt = tb[j] == 2 ? gk[2] : gt;
-            gt = tb[j] == 3 ? gk[3] : gt;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float wv = t + e > mine ? T[j][e] * gt[e] * d : 0.0f;
-                col += wv;
-                const float r = lanes_sum<16>(wv);
-                if (c16 == 0) hn.R[w][t + e] = r;
-            }
-        }
-        col = quads_sum(col);
-        xs = quads_sum(xs);
-        q = quads_sum(q);
-        xy = quads_sum(xy);
-        if (z == 0) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) ys[j] = quads_sum(ys[j]);
-            dot = wave_sum(dot);
-            if (lane == 0) hn.dot[w] = dot;
-        }
-        if (lane < 16) {
-            hn.col[z][mine] = col;
-            hn.XS[z][mine] = xs;
-            hn.Q[z][mine] = q;
-            hn.XY[z][mine] = xy;
-            if (z == 0) {
-#pragma unroll
-                for (int j = 0; j < 4; ++j) hn.YS[w][16 * j + c16] = ys[j];
-            }
-        }
-    }
-    __syncthreads();
-    if (w8 == 7) finish(h1 - 1);
-    // the products that the group's heads share, with Z [t][s] in LDS
-    E(&tD)[NP][64 * LD] = tDs[0];
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-        const formed<E, kSdParts> f(Z[j]);
-#pragma unroll
-        for (int m = 0; m < NP; ++m)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) tD[m][(16 * tb[j] + q4 + e) * LD + mine] = f.p[m][e];
-    }
-    __syncthreads();
-    float *o = gr.dbc + (((int64_t)hs * (gridDim.x / s.nchunk / gr.HS / s.G) + b) * s.L + t0) * 2 * s.G * s.N + g * s.N + (z ? 0 : s.G * s.N);
-#pragma unroll
-    for (int half = 0; half < NH; ++half) {
-        const int n0 = 64 * half + 16 * w;
-        if (64 * half >= s.N) break;
-#pragma unroll
-        for (int i = 0; i < 4; i += 2) {
-            const E *src = z ? tC : tB;   // dB: over t; dC: over s
-            const F f0 = ld_col<E, NT>(src, 16 * i, n0, lane), f1 = ld_col<E, NT>(src, 16 * i + 16, n0, lane);
+            const formed<E, kSdParts> f(Z[j]);
 #pragma unroll
             for (int m = 0; m < NP; ++m)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    F z0, z1;
-                    if (z) {
-                        z0 = ld_col<E, 64>(tD[m], 16 * i, 16 * j, lane);
-                        z1 = ld_col<E, 64>(tD[m], 16 * i + 16, 16 * j, lane);
-                    } else {
-                        z0 = ld_row<E, 64>(tD[m], 16 * j, 16 * i, lane);
-                        z1 = ld_row<E, 64>(tD[m], 16 * j, 16 * i + 16, lane);
-                    }
-                    acc[half][j] = mma(f0, f1, z0, z1, acc[half][j]);
-                }
+                for (int e = 0; e < 4; ++e) tDs[0][m][(16 * tb[j] + q4 + e) * LD + mine] = f.p[m][e];
         }
-        if (n0 + q4 < s.N) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                if (16 * j + c16 < tokens) *reinterpret_cast<f32x4_t *>(o + (int64_t)(16 * j + c16) * 2 * s.G * s.N + n0 + q4) = acc[half][j];
-        }
+        __syncthreads();
     }
 }
 

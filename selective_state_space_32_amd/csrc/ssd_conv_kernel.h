@@ -130,8 +130,8 @@ template <typename E, int W, int THREADS = kSdThreads> struct tile64 {
     static_assert(64 * UPR % THREADS == 0, "whole units per thread");
     u32x4_t r[NU];
     // rows [0, rows) of `src` (elements `stride` apart), columns [0, cols); zeros elsewhere
-    __device__ __forceinline__ void load(const E *src, uint32_t stride, int rows, int cols) {
-        const int row = threadIdx.x / UPR, c = threadIdx.x % UPR * EPU;
+    __device__ __forceinline__ void load(const E *src, uint32_t stride, int rows, int cols, int tid = threadIdx.x) {
+        const int row = tid / UPR, c = tid % UPR * EPU;
         const uint32_t off = ((uint32_t)row * stride + (uint32_t)c) * (uint32_t)sizeof(E), step = RPP * stride * (uint32_t)sizeof(E);
         const char *base = reinterpret_cast<const char *>(src);
         if (rows >= 64 && cols >= W) {
@@ -145,8 +145,8 @@ template <typename E, int W, int THREADS = kSdThreads> struct tile64 {
             }
         }
     }
-    __device__ __forceinline__ void stage(E *t) const {
-        const int row = threadIdx.x / UPR, c = threadIdx.x % UPR * EPU;
+    __device__ __forceinline__ void stage(E *t, int tid = threadIdx.x) const {
+        const int row = tid / UPR, c = tid % UPR * EPU;
 #pragma unroll
         for (int i = 0; i < NU; ++i) *reinterpret_cast<u32x4_t *>(t + (row + RPP * i) * sd_ld<E>(W) + c) = r[i];
     }
