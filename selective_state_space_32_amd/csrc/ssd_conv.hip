@@ -198,10 +198,19 @@ struct BwdPlan {
 BwdPlan bwd_plan(const ssm_ssd_conv_dims *dm, bool have_checkpoints) {
     BwdPlan p;
     const int64_t per = dm->nheads / dm->ngroups, items = std::max<int64_t>(dm->batch * chunks(dm) * dm->ngroups, 1);
-    // parts of a group's heads: as many as give 2048 workgroups
-    const int64_t parts = std::min(per, std::max<int64_t>(ceil_div(2048, items), 1));
-    p.hpw = (int)ceil_div(per, parts);
-    p.HS = (int)ceil_div(per, p.hpw);
+    // Parts of a group's heads: what takes the fewest rounds of a workgroup per CU, a workgroup's start and end
+    // counted as kStart heads (and its part of dB and dC written and read again)
+    constexpr int64_t kCUs = 256, kStart = 3;
+    int64_t best = -1;
+    for (int64_t parts = 1; parts <= per; ++parts) {
+        const int64_t hpw = ceil_div(per, parts), hs = ceil_div(per, hpw), cost = ceil_div(items * hs, kCUs) * (hpw + kStart);
+        if (best < 0 || cost < best) {
+            best = cost;
+            p.hpw = (int)hpw;
+            p.HS = (int)hs;
+        }
+        if (items * hs > 8 * kCUs) break;
+    }
     p.tiles = std::max<int64_t>(ceil_div(dm->seqlen, conv_bwd_tokens(dm)), 1);
     size_t at = 0;
     auto take = [&](size_t bytes) {
