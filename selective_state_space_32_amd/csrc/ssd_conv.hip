@@ -139,7 +139,8 @@ void launch_walk(const void *u, const void *dy, const float *tok, const int32_t 
                  int ends, const ssm_ssd_conv_dims *dm, int flags, hipStream_t st) {
     using IO = typename ssm::sd<E>::io;
     const ssm::sd_shape s = shape_of(dm, flags);
-    hipLaunchKernelGGL((ssm::sd_walk_kernel<E, NT, ADJ>), dim3((unsigned)(dm->batch * s.H * s.PT * s.nseg)), dim3(ssm::kSdThreads), 0,
+    auto kern = s.N == NT && s.P % 64 == 0 ? ssm::sd_walk_kernel<E, NT, ADJ, true> : ssm::sd_walk_kernel<E, NT, ADJ, false>;
+    hipLaunchKernelGGL(kern, dim3((unsigned)(dm->batch * s.H * s.PT * s.nseg)), dim3(ssm::kSdThreads), 0,
                        st, static_cast<const IO *>(u), static_cast<const IO *>(dy), tok, lens, from, each, to, ends, s);
 }
 template <bool ADJ>
@@ -168,7 +169,8 @@ template <typename E, int NT>
 void launch_scan(const void *u, const float *tok, const float *D, const int32_t *lens, const float *from, void *y, float *last, float *ckpt, const ssm_ssd_conv_dims *dm, int flags, hipStream_t st) {
     using IO = typename ssm::sd<E>::io;
     const ssm::sd_shape s = shape_of(dm, flags);
-    hipLaunchKernelGGL((ssm::sd_scan_kernel<E, NT>), dim3((unsigned)(dm->batch * s.H * s.PT * s.nseg)), dim3(ssm::kSdThreads), 0, st,
+    auto kern = s.N == NT && s.P % 64 == 0 ? ssm::sd_scan_kernel<E, NT, true> : ssm::sd_scan_kernel<E, NT, false>;
+    hipLaunchKernelGGL(kern, dim3((unsigned)(dm->batch * s.H * s.PT * s.nseg)), dim3(ssm::kSdThreads), 0, st,
                        static_cast<const IO *>(u), tok, D, lens, from, static_cast<IO *>(y), last, ckpt, s);
 }
 

@@ -23,7 +23,8 @@ namespace ssm {
 // states leaving them (ADJ: rows dy, weights e^c, with C, chunks from the last), one workgroup per (sequence, head,
 // 64-channel tile, segment).  each: [b][h][chunk][P][N], or null.  from: [b][h][segment][P][N], or null (zero).  to: with
 // `ends` [b][h][segment][P][N], what every segment leaves, else [b][h][P][N], what the last (ADJ: first) one leaves, or null.
-template <typename E, int NT, bool ADJ>
+// FULL as in sd_scan_kernel.
+template <typename E, int NT, bool ADJ, bool FULL>
 __global__ void __launch_bounds__(kSdThreads)
 sd_walk_kernel(const typename sd<E>::io *__restrict__ u_, const typename sd<E>::io *__restrict__ dy_,
                const float *__restrict__ tok, const int32_t *__restrict__ lens, const float *__restrict__ from, float *__restrict__ each,
@@ -31,27 +32,28 @@ sd_walk_kernel(const typename sd<E>::io *__restrict__ u_, const typename sd<E>::
     using IO = typename sd<E>::io;
     using F = typename sd<E>::frag;
     constexpr int NB = NT / 16;
+    const int N = FULL ? NT : s.N;
     __shared__ __attribute__((aligned(16))) E tB[64 * sd_ld<E>(NT)], tX[64 * sd_ld<E>(64)];
     __shared__ sd_tokens tk;
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int q4 = 4 * (lane >> 4);
     const sd_segment at(s, lens);
     const int64_t b = at.b, len = at.len;
     const int h = at.h, pt = at.pt;
     const sd_view<IO> v(u_, s, b, h, pt);
+    const int pw = FULL ? 64 : v.pw;
     const int xrow = ADJ ? s.H * s.P : s.dc;
     const E *xs = reinterpret_cast<const E *>(ADJ ? dy_ + (b * s.L * s.H + h) * s.P + pt * 64 : v.x);
     const E *Bs = reinterpret_cast<const E *>(ADJ ? v.C : v.B);
     tok += (b * s.H + h) * s.nchunk * kSdTok;
     f32x4_t S[NB];
     if (from) {
-        sd_load_state(S, from + at.state_at(s, s.nseg, at.seg), s.N, v.pw, w, lane);
+        sd_load_state(S, from + at.state_at(s, s.nseg, at.seg), N, pw, w, lane);
     } else {
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) S[nb] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
     }
     auto keep = [&](int64_t c) {
-        if (each) sd_store_state(S, each + at.state_at(s, s.nchunk, c), s.N, v.pw, w, lane);
+        if (each) sd_store_state(S, each + at.state_at(s, s.nchunk, c), N, pw, w, lane);
     };
     if (ADJ)   // chunks past the sequence's end leave the adjoint as it is
         for (int64_t c = at.live; c < at.c1; ++c) keep(c);
@@ -61,8 +63,8 @@ sd_walk_kernel(const typename sd<E>::io *__restrict__ u_, const typename sd<E>::
     auto fetch = [&](int64_t c) {
         const int64_t t0 = c * kSdQ;
         const int rows = (int)min((int64_t)64, len - t0);
-        rB.load(Bs + t0 * s.dc, s.dc, rows, s.N);
-        rX.load(xs + t0 * xrow, (uint32_t)xrow, rows, v.pw);
+        rB.load(Bs + t0 * s.dc, s.dc, rows, FULL ? NT : N);
+        rX.load(xs + t0 * xrow, (uint32_t)xrow, rows, pw);
         if (w == 0) rt = sd_load_tokens(tok + c * kSdTok, lane);
     };
     const int64_t n = at.live - at.c0;
@@ -78,30 +80,27 @@ sd_walk_kernel(const typename sd<E>::io *__restrict__ u_, const typename sd<E>::
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) S[nb] *= tk.dec;
 #pragma unroll
-        for (int k = 0; k < 4; k += 2) {
-            const float *wt = (ADJ ? tk.e : tk.w) + 16 * k + q4;
-            const F x0 = ld_col<E, 64>(tX, 16 * k, 16 * w, lane), x1 = ld_col<E, 64>(tX, 16 * k + 16, 16 * w, lane);
-            const formed<E, 3> f0(widen(x0) * ld4(wt)), f1(widen(x1) * ld4(wt + 16));
+        for (int k = 0; k < 2; ++k) {
+            const float *wt = (ADJ ? tk.e : tk.w) + 32 * k + 8 * (lane >> 4);
+            const op32<E> x = col32<E, 64>(tX, 32 * k, 16 * w, lane);
+            const formed<E, 3> f0(widen(x.lo) * ld4(wt)), f1(widen(x.hi) * ld4(wt + 4));
 #pragma unroll
             for (int n0 = 0; n0 < NB; n0 += 4) {
-                F b0[4], b1[4];
+                op32<E> bv[4];
 #pragma unroll
-                for (int nb = 0; nb < 4; ++nb) {
-                    b0[nb] = ld_col<E, NT>(tB, 16 * k, 16 * (n0 + nb), lane);
-                    b1[nb] = ld_col<E, NT>(tB, 16 * k + 16, 16 * (n0 + nb), lane);
-                }
+                for (int nb = 0; nb < 4; ++nb) bv[nb] = col32<E, NT>(tB, 32 * k, 16 * (n0 + nb), lane);
 #pragma unroll
                 for (int m = 0; m < formed<E, 3>::N; ++m)
 #pragma unroll
-                    for (int nb = 0; nb < 4; ++nb) S[n0 + nb] = mma(b0[nb], b1[nb], f0.p[m], f1.p[m], S[n0 + nb]);
+                    for (int nb = 0; nb < 4; ++nb) S[n0 + nb] = mma(bv[nb].lo, bv[nb].hi, f0.p[m], f1.p[m], S[n0 + nb]);
             }
         }
         __syncthreads();
     }
     if (!ADJ)
         for (int64_t c = at.live; c < at.c1; ++c) keep(c);
-    if (ends) sd_store_state(S, to + at.state_at(s, s.nseg, at.seg), s.N, v.pw, w, lane);
-    else if (to && at.seg == (ADJ ? 0 : s.nseg - 1)) sd_store_state(S, to + at.state_at(s, 1, 0), s.N, v.pw, w, lane);
+    if (ends) sd_store_state(S, to + at.state_at(s, s.nseg, at.seg), N, pw, w, lane);
+    else if (to && at.seg == (ADJ ? 0 : s.nseg - 1)) sd_store_state(S, to + at.state_at(s, 1, 0), N, pw, w, lane);
 }
 
 // What is formed in the backward is carried to 24 bits (three bf16 parts): the sums over tokens that u's gradient
@@ -169,7 +168,7 @@ sd_bwd_kernel(const typename sd<E>::io *__restrict__ u_, const typename sd<E>::i
     using F = typename sd<E>::frag;
     constexpr bool FULL = MODE >= 1, ONE = MODE == 2;
     const int N = FULL ? NT : s.N, P = ONE ? 64 : s.P;
-    constexpr int NB = NT / 16, NH = NT / 64, NP = formed<E, kSdParts>::N, LD = sd_ld<E>(64);
+    constexpr int NH = NT / 64, NP = formed<E, kSdParts>::N, LD = sd_ld<E>(64);
     // Two sets of an item's tiles where they fit in LDS: the next item's are staged while one is worked on, and a
     // barrier an item is enough.
     constexpr int NBUF = sd<E>::split || NT == 64 ? 2 : 1;
@@ -226,12 +225,13 @@ sd_bwd_kernel(const typename sd<E>::io *__restrict__ u_, const typename sd<E>::i
         if (i.h >= h1 || kind != 0) return;
         const int pw = FULL ? 64 : min(64, P - i.pt * 64);
         const char *m = reinterpret_cast<const char *>(st_in + state_at(i));
-        const uint32_t off = (uint32_t)(q4 * N + mine) * 4u, row = (uint32_t)N * 4u;
+        const uint32_t off = (uint32_t)(2 * q4 * N + mine) * 4u, row = (uint32_t)N * 4u;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {   // (groups of four channels exist or not as a whole)
+        for (int k = 0; k < 4; ++k) {   // channels 32 (k / 2) + 8 (lane / 16) + 4 (k % 2) .. + 3, which exist or not as a whole
+            const int p0 = 32 * (k >> 1) + 4 * (k & 1);
             rS[k] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-            if (FULL || (16 * k + q4 < pw && mine < N - i.nh)) {
-                const uint32_t at = off + 16 * k * row;
+            if (FULL || (p0 + 2 * q4 < pw && mine < N - i.nh)) {
+                const uint32_t at = off + p0 * row;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) rS[k][e] = *reinterpret_cast<const float *>(m + (size_t)(e * row) + at);
             }
@@ -328,16 +328,13 @@ sd_bwd_kernel(const typename sd<E>::io *__restrict__ u_, const typename sd<E>::i
             const int n0 = 64 * half + 16 * w;
             if (64 * half >= N) break;
 #pragma unroll
-            for (int i = 0; i < 4; i += 2) {
-                const F f0 = ld_col<E, NT>(src, 16 * i, n0, lane), f1 = ld_col<E, NT>(src, 16 * i + 16, n0, lane);
+            for (int i = 0; i < 2; ++i) {
+                const op32<E> f = col32<E, NT>(src, 32 * i, n0, lane);
 #pragma unroll
                 for (int m = 0; m < NP; ++m)
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const F z0 = over_t ? ld_col<E, 64>(tZ[m], 16 * i, 16 * j, lane) : ld_row<E, 64>(tZ[m], 16 * j, 16 * i, lane);
-                        const F z1 = over_t ? ld_col<E, 64>(tZ[m], 16 * i + 16, 16 * j, lane) : ld_row<E, 64>(tZ[m], 16 * j, 16 * i + 16, lane);
-                        acc[half][j] = mma(f0, f1, z0, z1, acc[half][j]);
-                    }
+                    for (int j = 0; j < 4; ++j)
+                        acc[half][j] = mma(f, over_t ? col32<E, 64>(tZ[m], 32 * i, 16 * j, lane) : row32<E, 64>(tZ[m], 16 * j, 32 * i, lane), acc[half][j]);
             }
             if (FULL || n0 + q4 < N) {
 #pragma unroll
@@ -357,11 +354,17 @@ sd_bwd_kernel(const typename sd<E>::io *__restrict__ u_, const typename sd<E>::i
             const parts_t &tD = tDs[dbuf];
             const formed<E, kSdParts> S[4] = {formed<E, kSdParts>(rS[0]), formed<E, kSdParts>(rS[1]), formed<E, kSdParts>(rS[2]), formed<E, kSdParts>(rS[3])};
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                f32x4_t v = widen(ld_col<E, 64>(tD[0], 16 * k, 16 * w, lane));
+            for (int k = 0; k < 2; ++k) {
+                op32<E> d = col32<E, 64>(tD[0], 32 * k, 16 * w, lane);
+                f32x4_t lo = widen(d.lo), hi = widen(d.hi);
 #pragma unroll
-                for (int m = 1; m < NP; ++m) v += widen(ld_col<E, 64>(tD[m], 16 * k, 16 * w, lane));
-                dot += v[0] * rS[k][0] + v[1] * rS[k][1] + v[2] * rS[k][2] + v[3] * rS[k][3];
+                for (int m = 1; m < NP; ++m) {
+                    d = col32<E, 64>(tD[m], 32 * k, 16 * w, lane);
+                    lo += widen(d.lo);
+                    hi += widen(d.hi);
+                }
+                lo = lo * rS[2 * k] + hi * rS[2 * k + 1];
+                dot += (lo[0] + lo[1]) + (lo[2] + lo[3]);
             }
             fetch_state(then);
 #pragma unroll
@@ -369,14 +372,12 @@ sd_bwd_kernel(const typename sd<E>::io *__restrict__ u_, const typename sd<E>::i
                 if (now.nh != 64 * half) continue;
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    F y0[4];
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) y0[k] = ld_row<E, 64>(tY, 16 * j, 16 * k, lane);
+                    const op32<E> y0 = row32<E, 64>(tY, 16 * j, 0, lane), y1 = row32<E, 64>(tY, 16 * j, 32, lane);
                     f32x4_t c0 = {}, c1 = {};
 #pragma unroll
                     for (int m = 0; m < NP; ++m) {
-                        c0 = mma(S[0].p[m], S[1].p[m], y0[0], y0[1], c0);
-                        c1 = mma(S[2].p[m], S[3].p[m], y0[2], y0[3], c1);
+                        c0 = mma(S[0].p[m], S[1].p[m], y0.lo, y0.hi, c0);
+                        c1 = mma(S[2].p[m], S[3].p[m], y1.lo, y1.hi, c1);
                     }
                     c0 = (c0 + c1) * tk.e[16 * j + c16];
                     const f32x4_t cf = widen(ld_row<E, NT>(tC, 16 * j, 64 * half + 16 * w, lane));
@@ -413,24 +414,22 @@ sd_bwd_kernel(const typename sd<E>::io *__restrict__ u_, const typename sd<E>::i
             const sd_tokens &tk = hd[now.h & 1].tk;
             const E *tX = tXs[xbuf];
             const parts_t &tD = tDs[dbuf];
-            F d0[NP][4];
+            op32<E> d0[NP][2];
 #pragma unroll
             for (int m = 0; m < NP; ++m)
 #pragma unroll
-                for (int k = 0; k < 4; ++k) d0[m][k] = ld_col<E, 64>(tD[m], 16 * k, 16 * w, lane);
+                for (int k = 0; k < 2; ++k) d0[m][k] = col32<E, 64>(tD[m], 32 * k, 16 * w, lane);
 #pragma unroll
             for (int half = 0; half < NH; ++half) {
                 if (now.nh != 64 * half) continue;
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    F x0[4];
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) x0[k] = ld_row<E, 64>(tX, 16 * j, 16 * k, lane);
+                    const op32<E> x0 = row32<E, 64>(tX, 16 * j, 0, lane), x1 = row32<E, 64>(tX, 16 * j, 32, lane);
                     f32x4_t c0 = {}, c1 = {};
 #pragma unroll
                     for (int m = 0; m < NP; ++m) {
-                        c0 = mma(d0[m][0], d0[m][1], x0[0], x0[1], c0);
-                        c1 = mma(d0[m][2], d0[m][3], x0[2], x0[3], c1);
+                        c0 = mma(d0[m][0], x0, c0);
+                        c1 = mma(d0[m][1], x1, c1);
                     }
                     acc[half][j] += (c0 + c1) * tk.w[16 * j + c16];
                 }
@@ -462,9 +461,7 @@ sd_bwd_kernel(const typename sd<E>::io *__restrict__ u_, const typename sd<E>::i
                     if (i < w) continue;
                     f32x4_t G = {};
 #pragma unroll
-                    for (int k = 0; k < NB; k += 2)
-                        G = mma(ld_row<E, NT>(tC, 16 * i, 16 * k, lane), ld_row<E, NT>(tC, 16 * i, 16 * k + 16, lane),
-                                ld_row<E, NT>(tB, 16 * w, 16 * k, lane), ld_row<E, NT>(tB, 16 * w, 16 * k + 16, lane), G);
+                    for (int k = 0; k < NT; k += 32) G = mma(row32<E, NT>(tC, 16 * i, k, lane), row32<E, NT>(tB, 16 * w, k, lane), G);
                     f32x4_t k4;
                     if (i == w) {
                         const f32x4_t th = ld4(tk.ch + 16 * i + q4), tl = ld4(tk.cl + 16 * i + q4);
@@ -484,20 +481,17 @@ sd_bwd_kernel(const typename sd<E>::io *__restrict__ u_, const typename sd<E>::i
                 for (int j = 0; j < 2; ++j) {
                     if (tb[j] < w) continue;
 #pragma unroll
-                    for (int k = 0; k < 4; k += 2)
-                        T[j] = mma(ld_row<E, 64>(tY, 16 * tb[j], 16 * k, lane), ld_row<E, 64>(tY, 16 * tb[j], 16 * k + 16, lane),
-                                   ld_row<E, 64>(tX, 16 * w, 16 * k, lane), ld_row<E, 64>(tX, 16 * w, 16 * k + 16, lane), T[j]);
+                    for (int k = 0; k < 64; k += 32) T[j] = mma(row32<E, 64>(tY, 16 * tb[j], k, lane), row32<E, 64>(tX, 16 * w, k, lane), T[j]);
                 }
             }
             // through the state leaving: V^T[p][s]
 #pragma unroll
-            for (int k = 0; k < 4; k += 2) {
-                const F b0 = ld_row<E, NT>(tB, 16 * w, now.nh + 16 * k, lane), b1 = ld_row<E, NT>(tB, 16 * w, now.nh + 16 * k + 16, lane);
+            for (int k = 0; k < 64; k += 32) {
+                const op32<E> bv = row32<E, NT>(tB, 16 * w, now.nh + k, lane);
 #pragma unroll
                 for (int m = 0; m < NP; ++m)
 #pragma unroll
-                    for (int j = 0; j < 2; ++j)
-                        V[j] = mma(ld_row<E, 64>(tD[m], 32 * z + 16 * j, 16 * k, lane), ld_row<E, 64>(tD[m], 32 * z + 16 * j, 16 * k + 16, lane), b0, b1, V[j]);
+                    for (int j = 0; j < 2; ++j) V[j] = mma(row32<E, 64>(tD[m], 32 * z + 16 * j, k, lane), bv, V[j]);
             }
             const float d = tk.dt[mine];
             if (then.nh == 0) {   // the 64 channels' last states: v is whole but for the pairs of tokens

@@ -115,6 +115,36 @@ __device__ __forceinline__ f32x4_t mma_fb(typename sd<E>::frag a0, typename sd<E
     for (int i = 0; i < formed<E, NS>::N; ++i) c = mma(a0, a1, b0.p[i], b1.p[i], c);
     return c;
 }
+// Two fragments of operands that both come from LDS, whose order of k is free: a lane holds the eight consecutive k at
+// 8 (l / 16) of a 32-wide step (16-byte reads move twice the bytes of 8-byte ones in the same time).
+template <typename E> struct op32 {
+    typename sd<E>::frag lo, hi;
+};
+template <typename E, int W> __device__ __forceinline__ op32<E> row32(const E *t, int r0, int k0, int lane) {
+    const E *p = t + (r0 + (lane & 15)) * sd_ld<E>(W) + k0 + 8 * (lane >> 4);
+    if constexpr (sd<E>::split) {
+        const sd_bf16x8 v = *reinterpret_cast<const sd_bf16x8 *>(p);
+        return {__builtin_shufflevector(v, v, 0, 1, 2, 3), __builtin_shufflevector(v, v, 4, 5, 6, 7)};
+    } else {
+        return {*reinterpret_cast<const f32x4_t *>(p), *reinterpret_cast<const f32x4_t *>(p + 4)};
+    }
+}
+template <typename E, int W> __device__ __forceinline__ op32<E> col32(const E *t, int k0, int m0, int lane) {
+    if constexpr (sd<E>::split) {
+        const int i = lane & 15;
+        typedef __attribute__((address_space(3))) sd_i16x4 lds_i16x4;
+        const __bf16 *p = t + (k0 + 8 * (lane >> 4) + (i >> 2)) * sd_ld<E>(W) + m0 + 4 * (i & 3);
+        return {__builtin_bit_cast(sd_bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4 *)p)),
+                __builtin_bit_cast(sd_bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4 *)(p + 4 * sd_ld<E>(W))))};
+    } else {
+        constexpr int LD = sd_ld<E>(W);
+        const float *p = t + (k0 + 8 * (lane >> 4)) * LD + m0 + (lane & 15);
+        return {f32x4_t{p[0], p[LD], p[2 * LD], p[3 * LD]}, f32x4_t{p[4 * LD], p[5 * LD], p[6 * LD], p[7 * LD]}};
+    }
+}
+template <typename E> __device__ __forceinline__ f32x4_t mma(const op32<E> &a, const op32<E> &b, f32x4_t c) {
+    return mma(a.lo, a.hi, b.lo, b.hi, c);
+}
 __device__ __forceinline__ f32x4_t widen(sd_bf16x4 v) { return f32x4_t{(float)v[0], (float)v[1], (float)v[2], (float)v[3]}; }
 __device__ __forceinline__ f32x4_t widen(f32x4_t v) { return v; }
 
@@ -498,7 +528,8 @@ sd_combine_kernel(const float *__restrict__ tok, const float *__restrict__ first
 // One workgroup per (sequence, head, 64-channel tile, segment): the segment's chunks in order, the state in
 // accumulators.  from: the segments' first states [b][h][segment][P][N], or null (zero); last: [b][h][P][N].  ckpt:
 // [b][h][chunk][P][N], receives the state entering each chunk, or null.
-template <typename E, int NT>
+// FULL: whole tiles (P a multiple of 64, N = NT), without the checks for less.
+template <typename E, int NT, bool FULL>
 __global__ void __launch_bounds__(kSdThreads)
 __attribute__((amdgpu_waves_per_eu(sd<E>::split && NT == 64 ? 3 : 2)))
 sd_scan_kernel(const typename sd<E>::io *__restrict__ u_, const float *__restrict__ tok, const float *__restrict__ Dv,
@@ -507,6 +538,7 @@ sd_scan_kernel(const typename sd<E>::io *__restrict__ u_, const float *__restric
     using IO = typename sd<E>::io;
     using F = typename sd<E>::frag;
     constexpr int NB = NT / 16;
+    const int N = FULL ? NT : s.N;
     __shared__ __attribute__((aligned(16))) E tB[64 * sd_ld<E>(NT)], tC[64 * sd_ld<E>(NT)], tX[64 * sd_ld<E>(64)];
     __shared__ __attribute__((aligned(16))) E tM[(sd<E>::split ? 2 : 1)][64 * sd_ld<E>(64)];
     __shared__ sd_tokens tk;
@@ -516,26 +548,27 @@ sd_scan_kernel(const typename sd<E>::io *__restrict__ u_, const float *__restric
     const int64_t b = at.b, len = at.len;
     const int h = at.h, pt = at.pt;
     const sd_view<IO> v(u_, s, b, h, pt);
+    const int pw = FULL ? 64 : v.pw;
     const E *xs = reinterpret_cast<const E *>(v.x), *Bs = reinterpret_cast<const E *>(v.B), *Cs = reinterpret_cast<const E *>(v.C);
     const float skip = Dv ? Dv[h] : 0.0f;
     tok += (b * s.H + h) * s.nchunk * kSdTok;
     IO *yb = y_ + (b * s.L * s.H + h) * s.P + pt * 64;
     f32x4_t S[NB];
     if (from) {
-        sd_load_state(S, from + at.state_at(s, s.nseg, at.seg), s.N, v.pw, w, lane);
+        sd_load_state(S, from + at.state_at(s, s.nseg, at.seg), N, pw, w, lane);
     } else {
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) S[nb] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
     }
-    auto keep = [&](int64_t c) { sd_store_state(S, ckpt + at.state_at(s, s.nchunk, c), s.N, v.pw, w, lane); };
+    auto keep = [&](int64_t c) { sd_store_state(S, ckpt + at.state_at(s, s.nchunk, c), N, pw, w, lane); };
     tile64<E, NT> rB, rC;
     tile64<E, 64> rX;
     sd_tok rt = {};
     auto fetch = [&](int64_t t0) {
         const int rows = (int)min((int64_t)64, len - t0);
-        rB.load(Bs + t0 * s.dc, s.dc, rows, s.N);
-        rC.load(Cs + t0 * s.dc, s.dc, rows, s.N);
-        rX.load(xs + t0 * s.dc, s.dc, rows, v.pw);
+        rB.load(Bs + t0 * s.dc, s.dc, rows, FULL ? NT : N);
+        rC.load(Cs + t0 * s.dc, s.dc, rows, FULL ? NT : N);
+        rX.load(xs + t0 * s.dc, s.dc, rows, pw);
         if (w == 0) rt = sd_load_tokens(tok + t0 / kSdQ * kSdTok, lane);
     };
     if (at.c0 < at.live) fetch(at.c0 * kSdQ);
@@ -548,9 +581,6 @@ sd_scan_kernel(const typename sd<E>::io *__restrict__ u_, const float *__restric
         if (c + 1 < at.live) fetch(t0 + kSdQ);
         if (ckpt) keep(c);
         __syncthreads();
-        F xf[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) xf[i] = ld_col<E, 64>(tX, 16 * i, 16 * w, lane);
         // Y^T[p][t] from the state entering, and G^T[s][t] for this wave's 16 tokens s
         f32x4_t Y[4] = {}, Gt[4] = {};
 #pragma unroll
@@ -569,7 +599,7 @@ sd_scan_kernel(const typename sd<E>::io *__restrict__ u_, const float *__restric
                 for (int j = 0; j < 4; ++j) Y[j] = mma(s0.p[m], s1.p[m], c0[j], c1[j], Y[j]);
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-                if (j >= w) Gt[j] = mma(b0, b1, c0[j], c1[j], Gt[j]);
+                Gt[j] = mma(b0, b1, c0[j], c1[j], Gt[j]);   // (all four blocks: branches around those before w cost registers and more)
         }
         // M[t][s], D on its diagonal.  Past the diagonal block the decay is taken over the block's last token r, in
         // two factors of at most 1: e^{c_t - c_r} and e^{c_r - c_s} dt_s
@@ -602,35 +632,33 @@ sd_scan_kernel(const typename sd<E>::io *__restrict__ u_, const float *__restric
             }
         }
         // the state leaving the chunk
+        const op32<E> xf[2] = {col32<E, 64>(tX, 0, 16 * w, lane), col32<E, 64>(tX, 32, 16 * w, lane)};
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) S[nb] *= tk.dec;
 #pragma unroll
-        for (int i = 0; i < 4; i += 2) {
-            const formed<E, 3> x0(widen(xf[i]) * ld4(tk.w + 16 * i + q4)), x1(widen(xf[i + 1]) * ld4(tk.w + 16 * i + 16 + q4));
+        for (int i = 0; i < 2; ++i) {
+            const float *wt = tk.w + 32 * i + 2 * q4;
+            const formed<E, 3> x0(widen(xf[i].lo) * ld4(wt)), x1(widen(xf[i].hi) * ld4(wt + 4));
 #pragma unroll
             for (int n0 = 0; n0 < NB; n0 += 4) {
-                F b0[4], b1[4];
+                op32<E> bv[4];
 #pragma unroll
-                for (int nb = 0; nb < 4; ++nb) {
-                    b0[nb] = ld_col<E, NT>(tB, 16 * i, 16 * (n0 + nb), lane);
-                    b1[nb] = ld_col<E, NT>(tB, 16 * i + 16, 16 * (n0 + nb), lane);
-                }
+                for (int nb = 0; nb < 4; ++nb) bv[nb] = col32<E, NT>(tB, 32 * i, 16 * (n0 + nb), lane);
 #pragma unroll
                 for (int m = 0; m < formed<E, 3>::N; ++m)
 #pragma unroll
-                    for (int nb = 0; nb < 4; ++nb) S[n0 + nb] = mma(b0[nb], b1[nb], x0.p[m], x1.p[m], S[n0 + nb]);
+                    for (int nb = 0; nb < 4; ++nb) S[n0 + nb] = mma(bv[nb].lo, bv[nb].hi, x0.p[m], x1.p[m], S[n0 + nb]);
             }
         }
 #pragma unroll
         for (int j = 0; j < 4; ++j) Y[j] *= tk.e[16 * j + c16];
         __syncthreads();
 #pragma unroll
-        for (int i = 0; i < 4; i += 2)
+        for (int i = 0; i < 2; ++i)
 #pragma unroll
             for (int m = 0; m < formed<E, 2>::N; ++m)
 #pragma unroll
-                for (int j = i; j < 4; ++j)
-                    Y[j] = mma(xf[i], xf[i + 1], ld_row<E, 64>(tM[m], 16 * j, 16 * i, lane), ld_row<E, 64>(tM[m], 16 * j, 16 * i + 16, lane), Y[j]);
+                for (int j = 2 * i; j < 4; ++j) Y[j] = mma(xf[i], row32<E, 64>(tM[m], 16 * j, 32 * i, lane), Y[j]);
         const int rows = (int)min((int64_t)64, len - t0);
         char *yc = reinterpret_cast<char *>(yb + t0 * s.H * s.P);
         const uint32_t yrow = (uint32_t)(s.H * s.P) * (uint32_t)sizeof(IO), yoff = (uint32_t)c16 * yrow + (uint32_t)(16 * w + q4) * (uint32_t)sizeof(IO);
@@ -641,11 +669,11 @@ sd_scan_kernel(const typename sd<E>::io *__restrict__ u_, const float *__restric
             else *reinterpret_cast<f32x4_t *>(yp) = o;
         };
         if (rows == 64) {
-            if (16 * w + q4 < v.pw) {
+            if (16 * w + q4 < pw) {
 #pragma unroll
                 for (int j = 0; j < 4; ++j) put(j, Y[j]);
             }
-        } else if (16 * w + q4 < v.pw) {   // the sequence's last chunk
+        } else if (16 * w + q4 < pw) {   // the sequence's last chunk
 #pragma unroll
             for (int j = 0; j < 4; ++j)
                 if (t0 + 16 * j + c16 < s.L) put(j, 16 * j + c16 < rows ? Y[j] : f32x4_t{0.0f, 0.0f, 0.0f, 0.0f});
@@ -654,7 +682,7 @@ sd_scan_kernel(const typename sd<E>::io *__restrict__ u_, const float *__restric
     // chunks past the sequence's end: the state stays, y is zero
     for (int64_t c = at.live; c < at.c1; ++c) {
         if (ckpt) keep(c);
-        if (16 * w + q4 >= v.pw) continue;
+        if (16 * w + q4 >= pw) continue;
         for (int j = 0; j < 4; ++j) {
             const int64_t t = c * kSdQ + 16 * j + c16;
             if (t >= s.L) continue;
@@ -662,7 +690,7 @@ sd_scan_kernel(const typename sd<E>::io *__restrict__ u_, const float *__restric
             for (int e = 0; e < 4; ++e) yp[e] = 0;
         }
     }
-    if (last && at.seg == s.nseg - 1) sd_store_state(S, last + at.state_at(s, 1, 0), s.N, v.pw, w, lane);
+    if (last && at.seg == s.nseg - 1) sd_store_state(S, last + at.state_at(s, 1, 0), N, pw, w, lane);
 }
 
 // ---- one token ------------------------------------------------------------------------------
