@@ -178,12 +178,26 @@ template <typename IO>
 void launch_step(float *state, const void *u, const void *dt, const float *A, const float *D, const float *dt_bias, void *y,
                  const ssm_ssd_conv_dims *dm, int flags, hipStream_t st) {
     const ssm::sd_shape s = shape_of(dm, flags);
-    const int lanes = s.N / 4;
-    auto kern = lanes <= 2 ? ssm::sd_step_kernel<IO, 2> : lanes <= 4 ? ssm::sd_step_kernel<IO, 4>
-              : lanes <= 8 ? ssm::sd_step_kernel<IO, 8> : lanes <= 16 ? ssm::sd_step_kernel<IO, 16> : ssm::sd_step_kernel<IO, 32>;
-    hipLaunchKernelGGL(kern, dim3((unsigned)(dm->batch * s.H)), dim3(256), 0, st, state, static_cast<const IO *>(u),
+    // Lanes per channel; two channels of a thread at a time, and a head's channels in several workgroups where there
+    // are few heads
+    const int lanes = s.N / 4, lpr = lanes <= 2 ? 2 : lanes <= 4 ? 4 : lanes <= 8 ? 8 : lanes <= 16 ? 16 : 32;
+    const int64_t heads = dm->batch * s.H, most = ceil_div(s.P, 2 * (256 / lpr));
+    const int parts = (int)std::min<int64_t>(most, std::max<int64_t>(2048 / heads, 1));
+    auto kern = lpr == 2 ? ssm::sd_step_kernel<IO, 2, 2> : lpr == 4 ? ssm::sd_step_kernel<IO, 4, 2>
+              : lpr == 8 ? ssm::sd_step_kernel<IO, 8, 2> : lpr == 16 ? ssm::sd_step_kernel<IO, 16, 2> : ssm::sd_step_kernel<IO, 32, 2>;
+    hipLaunchKernelGGL(kern, dim3((unsigned)(heads * parts)), dim3(256), 0, st, state, static_cast<const IO *>(u),
                        static_cast<const IO *>(dt), s.dt_stride, A, D, dt_bias, s.softplus, static_cast<IO *>(y), s.H, s.P,
-                       s.G, s.N);
+                       s.G, s.N, parts);
+}
+
+template <typename IO>
+void launch_conv_step(const void *x_, const float *w, const float *bias, void *st_rows, void *u, const ssm_ssd_conv_dims *dm,
+                      hipStream_t st) {
+    const int64_t stride = dm->xbc_stride ? dm->xbc_stride : row_of(dm), vblocks = ceil_div(row_of(dm) / ssm::kSdConvV, 256);
+    const bool al = aligned(x_, ssm::kSdConvV * sizeof(IO)) && stride % ssm::kSdConvV == 0;
+    auto kern = al ? ssm::sd_conv_step_kernel<IO, true> : ssm::sd_conv_step_kernel<IO, false>;
+    hipLaunchKernelGGL(kern, dim3((unsigned)(vblocks * dm->batch)), dim3(256), 0, st, static_cast<const IO *>(x_), stride, w, bias,
+                       (int)dm->width, static_cast<IO *>(st_rows), static_cast<IO *>(u), (int)row_of(dm), (int)vblocks);
 }
 
 // How the backward cuts its work, and its workspace.
@@ -421,14 +435,13 @@ int ssm_ssd_conv_step(float *state, void *conv_state, const void *xbc, const flo
     hipStream_t st = static_cast<hipStream_t>(stream);
     ssm_ssd_conv_dims one = *dims;
     one.seqlen = 1;
-    if (!conv_grid(&one, conv_tokens(&one), false).fits()) return fail(SSM_ERR_SHAPE, "batch exceeds the grid of the convolution");
+    if (dims->batch > kMaxGrid / std::max(ceil_div(row_of(dims) / ssm::kSdConvV, 256), dims->nheads))
+        return fail(SSM_ERR_SHAPE, "batch exceeds the grid of the step");
     if (es == 2) {
-        launch_conv<uint16_t>(xbc, conv_w, conv_b, conv_state, conv_state, nullptr, workspace, nullptr, nullptr, nullptr, nullptr,
-                              &one, 0, st);
+        launch_conv_step<uint16_t>(xbc, conv_w, conv_b, conv_state, workspace, &one, st);
         launch_step<uint16_t>(state, workspace, dt, A, D, dt_bias, y, &one, flags, st);
     } else {
-        launch_conv<float>(xbc, conv_w, conv_b, conv_state, conv_state, nullptr, workspace, nullptr, nullptr, nullptr, nullptr, &one,
-                           0, st);
+        launch_conv_step<float>(xbc, conv_w, conv_b, conv_state, workspace, &one, st);
         launch_step<float>(state, workspace, dt, A, D, dt_bias, y, &one, flags, st);
     }
     return launched();

@@ -626,15 +626,8 @@ sd_conv_bwd_kernel(const IO *__restrict__ x, int64_t xstride, const float *__res
     };
     fetch(t0);
     float wv[kSdTaps][kSdConvV], bv[kSdConvV], past[3][kSdConvV], g[kSdTaps][kSdConvV] = {}, aw[kSdTaps][kSdConvV] = {}, ab[kSdConvV] = {};
-#pragma unroll
-    for (int k = 0; k < kSdConvV; ++k) {
-#pragma unroll
-        for (int j = 0; j < kSdTaps; ++j) {
-            const int tap = j - (kSdTaps - width);
-            wv[j][k] = tap >= 0 ? w[(int64_t)(c + k) * width + tap] : 0.0f;
-        }
-        bv[k] = bias ? bias[c + k] : 0.0f;
-    }
+    conv_weights(w, width, c, wv);
+    conv_bias(bias, c, bv);
 #pragma unroll
     for (int j = 0; j < 3; ++j) {
         const int64_t t = t0 - 3 + j;

@@ -295,6 +295,69 @@ template <typename IO> __device__ __forceinline__ float io_f32(IO v) {
     else return v;
 }
 
+// The taps of kSdConvV channels from c on, oldest first, zeros in front where there are fewer than four.
+__device__ __forceinline__ void conv_weights(const float *w, int width, int c, float (&o)[kSdTaps][kSdConvV]) {
+    if (width == kSdTaps) {
+        typedef float any4 __attribute__((ext_vector_type(4), aligned(4)));
+#pragma unroll
+        for (int i = 0; i < kSdConvV; ++i) {
+            const any4 v = *reinterpret_cast<const any4 *>(w + (int64_t)(c + i) * kSdTaps);
+#pragma unroll
+            for (int j = 0; j < kSdTaps; ++j) o[j][i] = v[j];
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < kSdConvV; ++i)
+#pragma unroll
+            for (int j = 0; j < kSdTaps; ++j) {
+                const int tap = j - (kSdTaps - width);
+                o[j][i] = tap >= 0 ? w[(int64_t)(c + i) * width + tap] : 0.0f;
+            }
+    }
+}
+__device__ __forceinline__ void conv_bias(const float *b, int c, float (&o)[kSdConvV]) {
+    typedef float any4 __attribute__((ext_vector_type(4), aligned(4)));
+    any4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (b) v = *reinterpret_cast<const any4 *>(b + c);
+#pragma unroll
+    for (int i = 0; i < kSdConvV; ++i) o[i] = v[i];
+}
+// u of a token in its type, from its taps' inputs (oldest first).
+template <typename IO>
+__device__ __forceinline__ void conv_token(const float (&w)[kSdTaps][kSdConvV], const float (&b)[kSdConvV], const float (&x0)[kSdConvV],
+                                           const float (&x1)[kSdConvV], const float (&x2)[kSdConvV], const float (&x3)[kSdConvV],
+                                           IO (&o)[kSdConvV]) {
+    bool near[kSdConvV] = {};
+#pragma unroll
+    for (int e = 0; e < kSdConvV; ++e) {
+        float p = fmaf(w[0][e], x0[e], b[e]);
+        p = fmaf(w[1][e], x1[e], p);
+        p = fmaf(w[2][e], x2[e], p);
+        p = fmaf(w[3][e], x3[e], p);
+        if constexpr (sizeof(IO) == 2) {
+            float size = fmaf(fabsf(w[0][e]), fabsf(x0[e]), fabsf(b[e]));
+            size = fmaf(fabsf(w[1][e]), fabsf(x1[e]), size);
+            size = fmaf(fabsf(w[2][e]), fabsf(x2[e]), size);
+            size = fmaf(fabsf(w[3][e]), fabsf(x3[e]), size);
+            o[e] = f32_to_bf16(conv_silu(p, size, near[e]));
+        } else {
+            o[e] = silu_f32(p);
+        }
+    }
+    if constexpr (sizeof(IO) == 2)
+        if (near[0] || near[1] || near[2] || near[3]) {   // (one branch a token: one an element cost more)
+#pragma unroll
+            for (int e = 0; e < kSdConvV; ++e)
+                if (near[e]) {
+                    double q = fma((double)w[0][e], (double)x0[e], (double)b[e]);
+                    q = fma((double)w[1][e], (double)x1[e], q);
+                    q = fma((double)w[2][e], (double)x2[e], q);
+                    q = fma((double)w[3][e], (double)x3[e], q);
+                    o[e] = silu_bf16_64(q);
+                }
+        }
+}
+
 // What a forward's first launch does besides the convolution: the tokens' step sizes and decays.
 struct sd_tok_args {
     const void *dt;
@@ -347,15 +410,8 @@ sd_conv_kernel(const IO *__restrict__ x, int64_t xstride, const float *__restric
     };
     fetch(t0);
     float wv[kSdTaps][kSdConvV], bv[kSdConvV], past[kSdTaps - 1][kSdConvV];
-#pragma unroll
-    for (int i = 0; i < kSdConvV; ++i) {
-#pragma unroll
-        for (int j = 0; j < kSdTaps; ++j) {
-            const int tap = j - (kSdTaps - width);
-            wv[j][i] = tap >= 0 ? w[(int64_t)(c + i) * width + tap] : 0.0f;
-        }
-        bv[i] = bias ? bias[c + i] : 0.0f;
-    }
+    conv_weights(w, width, c, wv);
+    conv_bias(bias, c, bv);
 #pragma unroll
     for (int j = 0; j < kSdTaps - 1; ++j) {
         IO o[kSdConvV];
@@ -375,35 +431,9 @@ sd_conv_kernel(const IO *__restrict__ x, int64_t xstride, const float *__restric
             if (t + i >= t1) break;
             IO o[kSdConvV];
             float last[kSdConvV];
-            bool near[kSdConvV] = {};
 #pragma unroll
-            for (int e = 0; e < kSdConvV; ++e) {
-                last[e] = io_f32(now[i][e]);
-                float p = fmaf(wv[0][e], past[0][e], bv[e]);
-                p = fmaf(wv[1][e], past[1][e], p);
-                p = fmaf(wv[2][e], past[2][e], p);
-                p = fmaf(wv[3][e], last[e], p);
-                if constexpr (sizeof(IO) == 2) {
-                    float size = fmaf(fabsf(wv[0][e]), fabsf(past[0][e]), fabsf(bv[e]));
-                    size = fmaf(fabsf(wv[1][e]), fabsf(past[1][e]), size);
-                    size = fmaf(fabsf(wv[2][e]), fabsf(past[2][e]), size);
-                    size = fmaf(fabsf(wv[3][e]), fabsf(last[e]), size);
-                    o[e] = f32_to_bf16(conv_silu(p, size, near[e]));
-                } else {
-                    o[e] = silu_f32(p);
-                }
-            }
-            if (near[0] || near[1] || near[2] || near[3]) {   // (one branch a token: four cost a third more)
-#pragma unroll
-                for (int e = 0; e < kSdConvV; ++e)
-                    if (near[e]) {
-                        double q = fma((double)wv[0][e], (double)past[0][e], (double)bv[e]);
-                        q = fma((double)wv[1][e], (double)past[1][e], q);
-                        q = fma((double)wv[2][e], (double)past[2][e], q);
-                        q = fma((double)wv[3][e], (double)last[e], q);
-                        if constexpr (sizeof(IO) == 2) o[e] = silu_bf16_64(q);
-                    }
-            }
+            for (int e = 0; e < kSdConvV; ++e) last[e] = io_f32(now[i][e]);
+            conv_token<IO>(wv, bv, past[0], past[1], past[2], last, o);
 #pragma unroll
             for (int e = 0; e < kSdConvV; ++e) {
                 past[0][e] = past[1][e];
@@ -695,20 +725,49 @@ sd_scan_kernel(const typename sd<E>::io *__restrict__ u_, const float *__restric
 
 // ---- one token ------------------------------------------------------------------------------
 
-// One workgroup per (sequence, head, rows of P): LPR lanes hold a channel's N states, four each.
-template <typename IO, int LPR>
+// The convolution of one token a sequence, its rows advanced in place; thread: kSdConvV channels of a sequence.
+template <typename IO, bool AL>
+__global__ void __launch_bounds__(256)
+sd_conv_step_kernel(const IO *__restrict__ x, int64_t xstride, const float *__restrict__ w, const float *__restrict__ bias,
+                    int width, IO *__restrict__ st, IO *__restrict__ u, int dc, int vblocks) {
+    const int v = blockIdx.x % vblocks * 256 + threadIdx.x;
+    if (v >= dc / kSdConvV) return;
+    const int c = v * kSdConvV, h = width - 1;
+    const int64_t b = blockIdx.x / vblocks;
+    IO r[kSdTaps][kSdConvV] = {}, o[kSdConvV];
+    conv_vec<IO, AL>::load(x + b * xstride + c, r[3]);
+#pragma unroll
+    for (int j = 0; j < kSdTaps - 1; ++j)
+        if (j >= kSdTaps - width) conv_vec<IO, true>::load(st + (b * h + j - (kSdTaps - width)) * dc + c, r[j]);
+    float wv[kSdTaps][kSdConvV], bv[kSdConvV], xv[kSdTaps][kSdConvV];
+    conv_weights(w, width, c, wv);
+    conv_bias(bias, c, bv);
+#pragma unroll
+    for (int j = 0; j < kSdTaps; ++j)
+#pragma unroll
+        for (int e = 0; e < kSdConvV; ++e) xv[j][e] = io_f32(r[j][e]);
+    conv_token<IO>(wv, bv, xv[0], xv[1], xv[2], xv[3], o);
+    conv_vec<IO, true>::store(u + b * dc + c, o);
+#pragma unroll
+    for (int j = 1; j < kSdTaps; ++j)
+        if (j > kSdTaps - width) conv_vec<IO, true>::store(st + (b * h + j - 1 - (kSdTaps - width)) * dc + c, r[j]);
+}
+
+// One workgroup per (sequence, head, part of its channels): LPR lanes hold a channel's N states, four each; U channels
+// at a time.
+template <typename IO, int LPR, int U>
 __global__ void __launch_bounds__(256)
 sd_step_kernel(float *__restrict__ state, const IO *__restrict__ u, const IO *__restrict__ dt, int64_t dt_stride,
                const float *__restrict__ A, const float *__restrict__ Dv, const float *__restrict__ dt_bias,
-               int softplus, IO *__restrict__ y, int H, int P, int G, int N) {
+               int softplus, IO *__restrict__ y, int H, int P, int G, int N, int parts) {
     constexpr int ROWS = 256 / LPR;
-    const int h = blockIdx.x % H;
-    const int64_t b = blockIdx.x / H;
+    const int part = blockIdx.x % (unsigned)parts, h = blockIdx.x / (unsigned)parts % (unsigned)H;
+    const int64_t b = blockIdx.x / (unsigned)parts / (unsigned)H;
     const IO *r = u + b * (H * P + 2 * G * N);
     const int g = h / (H / G), n = (threadIdx.x % LPR) * 4;
+    float *sb = state + (b * H + h) * P * N;
+    const int row = threadIdx.x / LPR;
     const float v = io<IO>::ld(dt, b * dt_stride + h) + (dt_bias ? dt_bias[h] : 0.0f);
-    const float d = softplus ? softplus_f32(v) : v;
-    const float a = hw_exp2((A[h] * kLog2e) * d), skip = Dv ? Dv[h] : 0.0f;
     f32x4_t Bv = {0.0f, 0.0f, 0.0f, 0.0f}, Cv = Bv;
     if (n < N) {
         const IO *Bp = r + H * P + g * N + n, *Cp = Bp + G * N;
@@ -718,19 +777,33 @@ sd_step_kernel(float *__restrict__ state, const IO *__restrict__ u, const IO *__
             Cv[e] = io<IO>::ld(Cp, e);
         }
     }
-    float *sb = state + (b * H + h) * P * N;
-    for (int p = threadIdx.x / LPR; p < P; p += ROWS) {
-        const float x = io<IO>::ld(r, h * P + p);
-        float o = 0.0f;
-        if (n < N) {
-            f32x4_t *sp = reinterpret_cast<f32x4_t *>(sb + (int64_t)p * N + n);
-            const f32x4_t st = *sp * a + Bv * (d * x);
-            *sp = st;
-            o = st[0] * Cv[0] + st[1] * Cv[1] + st[2] * Cv[2] + st[3] * Cv[3];
-        }
+    const float skip = Dv ? Dv[h] : 0.0f, a2 = A[h] * kLog2e;
+    for (int p0 = part * ROWS * U; p0 < P; p0 += parts * ROWS * U) {
+        f32x4_t st[U];
+        float x[U];
 #pragma unroll
-        for (int m = 1; m < LPR; m *= 2) o += __shfl_xor(o, m, 64);
-        if (n == 0) io<IO>::st(y, (b * H + h) * P + p, o + skip * x);
+        for (int i = 0; i < U; ++i) {
+            const int p = p0 + i * ROWS + row;
+            if (p < P) {
+                x[i] = io<IO>::ld(r, h * P + p);
+                if (n < N) st[i] = ld4(sb + (int64_t)p * N + n);
+            }
+        }
+        const float d = softplus ? softplus_f32(v) : v, a = hw_exp2(a2 * d);
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            const int p = p0 + i * ROWS + row;
+            if (p >= P) continue;   // (a channel's lanes together)
+            float o = 0.0f;
+            if (n < N) {
+                st[i] = st[i] * a + Bv * (d * x[i]);
+                *reinterpret_cast<f32x4_t *>(sb + (int64_t)p * N + n) = st[i];
+                o = st[i][0] * Cv[0] + st[i][1] * Cv[1] + st[i][2] * Cv[2] + st[i][3] * Cv[3];
+            }
+#pragma unroll
+            for (int m = 1; m < LPR; m *= 2) o += __shfl_xor(o, m, 64);
+            if (n == 0) io<IO>::st(y, (b * H + h) * P + p, o + skip * x[i]);
+        }
     }
 }
 
