@@ -87,12 +87,15 @@ sd_walk_kernel(const typename sd<E>::io *__restrict__ u_, const typename sd<E>::
 #pragma unroll
             for (int n0 = 0; n0 < NB; n0 += 4) {
                 op32<E> bv[4];
+                f32x4_t add[4] = {};
 #pragma unroll
                 for (int nb = 0; nb < 4; ++nb) bv[nb] = col32<E, NT>(tB, 32 * k, 16 * (n0 + nb), lane);
 #pragma unroll
                 for (int m = 0; m < formed<E, 3>::N; ++m)
 #pragma unroll
-                    for (int nb = 0; nb < 4; ++nb) S[n0 + nb] = mma(bv[nb].lo, bv[nb].hi, f0.p[m], f1.p[m], S[n0 + nb]);
+                    for (int nb = 0; nb < 4; ++nb) add[nb] = mma(bv[nb].lo, bv[nb].hi, f0.p[m], f1.p[m], add[nb]);
+#pragma unroll
+                for (int nb = 0; nb < 4; ++nb) S[n0 + nb] += add[nb];
             }
         }
         __syncthreads();
@@ -104,7 +107,9 @@ sd_walk_kernel(const typename sd<E>::io *__restrict__ u_, const typename sd<E>::
 }
 
 // What is formed in the backward is carried to 24 bits (three bf16 parts): the sums over tokens that u's gradient
-// goes into leave in fp32.
+// goes into leave in fp32.  For their sake too products that are not of a smaller part start from zero and are added up
+// by vector instructions: the bf16 matrix instruction cuts its addend downward to 2^-24 of its largest product, a bias
+// that sums over tokens collect (B8 L2048 H80 N64: the error of dt_bias's gradient 2.4e-6 that way).
 constexpr int kSdParts = 3;
 
 constexpr int kSdBwdThreads = 1024;
@@ -330,11 +335,14 @@ sd_bwd_kernel(const typename sd<E>::io *__restrict__ u_, const typename sd<E>::i
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const op32<E> f = col32<E, NT>(src, 32 * i, n0, lane);
+                f32x4_t add[4] = {};
 #pragma unroll
                 for (int m = 0; m < NP; ++m)
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
-                        acc[half][j] = mma(f, over_t ? col32<E, 64>(tZ[m], 32 * i, 16 * j, lane) : row32<E, 64>(tZ[m], 16 * j, 32 * i, lane), acc[half][j]);
+                        add[j] = mma(f, over_t ? col32<E, 64>(tZ[m], 32 * i, 16 * j, lane) : row32<E, 64>(tZ[m], 16 * j, 32 * i, lane), add[j]);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) acc[half][j] += add[j];
             }
             if (FULL || n0 + q4 < N) {
 #pragma unroll
@@ -443,76 +451,80 @@ sd_bwd_kernel(const typename sd<E>::io *__restrict__ u_, const typename sd<E>::i
     } else {
         // blocks of tokens t: z and 3 - z, of which those before w have nothing
         const int tb[2] = {z, 3 - z};
-        f32x4_t Z[2] = {}, T[2], V[2], gk[4], kk[2];   // gk: G K for t in all blocks; kk: K for t in the wave's two
-        float xs = 0.0f, q = 0.0f, xy = 0.0f;
+        f32x4_t Z[2] = {}, V[2];
+        float xs = 0.0f, q = 0.0f, xy = 0.0f, col = 0.0f;
         for (item_t now = start, then = next(now); now.h < h1; now = then, then = next(then)) {
             begin(now, then);
             head_t &hn = hd[now.h & 1];
             const sd_tokens &tk = hn.tk;
             const E *tX = tXs[xbuf], *tY = tYs[xbuf];
             const parts_t &tD = tDs[dbuf];
-            if (now.nh == 0 && now.pt == 0) {
-                const float sh = tk.ch[mine], sl = tk.cl[mine];
-#pragma unroll
-                for (int j = 0; j < 2; ++j) T[j] = kk[j] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    gk[i] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-                    if (i < w) continue;
-                    f32x4_t G = {};
-#pragma unroll
-                    for (int k = 0; k < NT; k += 32) G = mma(row32<E, NT>(tC, 16 * i, k, lane), row32<E, NT>(tB, 16 * w, k, lane), G);
-                    f32x4_t k4;
-                    if (i == w) {
-                        const f32x4_t th = ld4(tk.ch + 16 * i + q4), tl = ld4(tk.cl + 16 * i + q4);
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) k4[e] = q4 + e >= c16 ? hw_exp2((th[e] - sh) + (tl[e] - sl)) : 0.0f;
-                    } else {   // in two factors of at most 1, over the block's first token
-                        k4 = ld4(hn.near + 16 * i + q4) * hw_exp2((tk.ch[16 * i] - sh) + (tk.cl[16 * i] - sl));
-                    }
-                    gk[i] = G * k4;
-                    if (i == tb[0]) kk[0] = k4;
-                    if (i == tb[1]) kk[1] = k4;
-                }
-            }
-            if (now.nh == 0) {   // T[t][s]
-                V[0] = V[1] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    if (tb[j] < w) continue;
-#pragma unroll
-                    for (int k = 0; k < 64; k += 32) T[j] = mma(row32<E, 64>(tY, 16 * tb[j], k, lane), row32<E, 64>(tX, 16 * w, k, lane), T[j]);
-                }
-            }
+            if (now.nh == 0) V[0] = V[1] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
             // through the state leaving: V^T[p][s]
 #pragma unroll
             for (int k = 0; k < 64; k += 32) {
                 const op32<E> bv = row32<E, NT>(tB, 16 * w, now.nh + k, lane);
+                f32x4_t add[2] = {};
 #pragma unroll
                 for (int m = 0; m < NP; ++m)
 #pragma unroll
-                    for (int j = 0; j < 2; ++j) V[j] = mma(row32<E, 64>(tD[m], 32 * z + 16 * j, k, lane), bv, V[j]);
+                    for (int j = 0; j < 2; ++j) add[j] = mma(row32<E, 64>(tD[m], 32 * z + 16 * j, k, lane), bv, add[j]);
+                V[0] += add[0];
+                V[1] += add[1];
             }
-            const float d = tk.dt[mine];
-            if (then.nh == 0) {   // the 64 channels' last states: v is whole but for the pairs of tokens
+            if (then.nh == 0) {   // the 64 channels' last states: the pairs of tokens (all linear in the channels)
                 const int pw = FULL ? 64 : min(64, P - now.pt * 64);
-                const float te = hn.to_end[mine];
-                f32x4_t x[2], y[2];
+                const float te = hn.to_end[mine], d = tk.dt[mine], sh = tk.ch[mine], sl = tk.cl[mine];
+                f32x4_t x[2];
                 float x0 = 0.0f;
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
                     V[j] *= te;
                     x[j] = widen(ld_row<E, 64>(tX, 16 * w, 32 * z + 16 * j, lane));
-                    y[j] = widen(ld_row<E, 64>(tY, 16 * w, 32 * z + 16 * j, lane));
                     x0 += V[j][0] * x[j][0] + V[j][1] * x[j][1] + V[j][2] * x[j][2] + V[j][3] * x[j][3];
-                    xy += x[j][0] * y[j][0] + x[j][1] * y[j][1] + x[j][2] * y[j][2] + x[j][3] * y[j][3];
                 }
                 xs += x0 * d;
 #pragma unroll
                 for (int i = 0; i < 4; i += 2) {
+                    const int mineb = tb[i / 2], t = 16 * mineb + q4;   // the pair's block whose T is the wave's
+                    if (mineb < w && c16 < 4 && now.pt == 0) hn.R[w][t + c16] = 0.0f;
                     if (i + 1 < w) continue;
-                    const formed<E, kSdParts> g0(gk[i]), g1(gk[i + 1]);
+                    f32x4_t gk[2], kk[2];
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        gk[u] = kk[u] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+                        if (i + u < w) continue;
+                        f32x4_t G = {};
+#pragma unroll
+                        for (int k = 0; k < NT; k += 32) G += mma(row32<E, NT>(tC, 16 * (i + u), k, lane), row32<E, NT>(tB, 16 * w, k, lane), f32x4_t{});
+                        if (i + u == w) {
+                            const f32x4_t th = ld4(tk.ch + 16 * (i + u) + q4), tl = ld4(tk.cl + 16 * (i + u) + q4);
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) kk[u][e] = q4 + e >= c16 ? hw_exp2((th[e] - sh) + (tl[e] - sl)) : 0.0f;
+                        } else {   // in two factors of at most 1, over the block's first token
+                            kk[u] = ld4(hn.near + 16 * (i + u) + q4) * hw_exp2((tk.ch[16 * (i + u)] - sh) + (tk.cl[16 * (i + u)] - sl));
+                        }
+                        gk[u] = G * kk[u];
+                    }
+                    if (mineb >= w) {
+                        f32x4_t T = {};
+#pragma unroll
+                        for (int k = 0; k < 64; k += 32) T += mma(row32<E, 64>(tY, 16 * mineb, k, lane), row32<E, 64>(tX, 16 * w, k, lane), f32x4_t{});
+                        T *= d;
+                        const bool second = mineb != i;   // (the wave's: a copy by selection)
+                        Z[i / 2] += T * (second ? kk[1] : kk[0]);
+                        T *= second ? gk[1] : gk[0];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float wv = t + e > mine ? T[e] : 0.0f;
+                            col += wv;
+                            const float r = lanes_sum<16>(wv);
+                            if (c16 == 0) hn.R[w][t + e] = ONE || now.pt == 0 ? r : hn.R[w][t + e] + r;
+                        }
+                    }
+                    const formed<E, kSdParts> g0(gk[0]), g1(gk[1]);
                     F y0[2], y1[2];
+                    f32x4_t add[2] = {};
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
                         y0[j] = ld_col<E, 64>(tY, 16 * i, 32 * z + 16 * j, lane);
@@ -521,40 +533,22 @@ sd_bwd_kernel(const typename sd<E>::io *__restrict__ u_, const typename sd<E>::i
 #pragma unroll
                     for (int m = 0; m < NP; ++m)
 #pragma unroll
-                        for (int j = 0; j < 2; ++j) V[j] = mma(y0[j], y1[j], g0.p[m], g1.p[m], V[j]);
+                        for (int j = 0; j < 2; ++j) add[j] = mma(y0[j], y1[j], g0.p[m], g1.p[m], add[j]);
+                    V[0] += add[0];
+                    V[1] += add[1];
                 }
                 const float skip = Dv ? Dv[now.h] : 0.0f;
                 char *o = reinterpret_cast<char *>(gr.du + ((b * s.L + t0) * s.H + now.h) * P + now.pt * 64);
                 const uint32_t off = ((uint32_t)mine * (uint32_t)(s.H * P) + (uint32_t)(32 * z + q4)) * 4u;
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
+                    const f32x4_t y = widen(ld_row<E, 64>(tY, 16 * w, 32 * z + 16 * j, lane));
                     q += V[j][0] * x[j][0] + V[j][1] * x[j][1] + V[j][2] * x[j][2] + V[j][3] * x[j][3];
-                    if (have && (FULL || 32 * z + 16 * j + q4 < pw)) *reinterpret_cast<f32x4_t *>(o + (off + 64 * j)) = V[j] * d + y[j] * skip;
+                    xy += x[j][0] * y[0] + x[j][1] * y[1] + x[j][2] * y[2] + x[j][3] * y[3];
+                    if (have && (FULL || 32 * z + 16 * j + q4 < pw)) *reinterpret_cast<f32x4_t *>(o + (off + 64 * j)) = V[j] * d + y * skip;
                 }
             }
-            if (then.h != now.h) {   // the head's sums over pairs of tokens
-                float col = 0.0f;
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const int t = 16 * tb[j] + q4;
-                    if (tb[j] < w) {
-                        if (c16 < 4) hn.R[w][t + c16] = 0.0f;
-                        continue;
-                    }
-                    Z[j] += T[j] * kk[j] * d;
-                    // (G K of the wave's block: a copy by selection, as the blocks' number is the wave's)
-                    f32x4_t gt = gk[0];
-                    gt = tb[j] == 1 ? gk[1] : gt;
-                    gt = tb[j] == 2 ? gk[2] : gt;
-                    gt = tb[j] == 3 ? gk[3] : gt;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float wv = t + e > mine ? T[j][e] * gt[e] * d : 0.0f;
-                        col += wv;
-                        const float r = lanes_sum<16>(wv);
-                        if (c16 == 0) hn.R[w][t + e] = r;
-                    }
-                }
+            if (then.h != now.h) {   // the head's sums over the tokens
                 col = quads_sum(col);
                 xs = quads_sum(xs);
                 q = quads_sum(q);
@@ -565,7 +559,7 @@ sd_bwd_kernel(const typename sd<E>::io *__restrict__ u_, const typename sd<E>::i
                     hn.Q[z][mine] = q;
                     hn.XY[z][mine] = xy;
                 }
-                xs = q = xy = 0.0f;
+                xs = q = xy = col = 0.0f;
             }
             turn(then);
         }
