@@ -87,15 +87,20 @@ sd_walk_kernel(const typename sd<E>::io *__restrict__ u_, const typename sd<E>::
 #pragma unroll
             for (int n0 = 0; n0 < NB; n0 += 4) {
                 op32<E> bv[4];
-                f32x4_t add[4] = {};
+                f32x4_t add[4] = {};   // (the states on their accumulators, as in the scan, bit for bit)
 #pragma unroll
                 for (int nb = 0; nb < 4; ++nb) bv[nb] = col32<E, NT>(tB, 32 * k, 16 * (n0 + nb), lane);
 #pragma unroll
                 for (int m = 0; m < formed<E, 3>::N; ++m)
 #pragma unroll
-                    for (int nb = 0; nb < 4; ++nb) add[nb] = mma(bv[nb].lo, bv[nb].hi, f0.p[m], f1.p[m], add[nb]);
+                    for (int nb = 0; nb < 4; ++nb) {
+                        f32x4_t &to = ADJ ? add[nb] : S[n0 + nb];
+                        to = mma(bv[nb].lo, bv[nb].hi, f0.p[m], f1.p[m], to);
+                    }
+                if (ADJ) {
 #pragma unroll
-                for (int nb = 0; nb < 4; ++nb) S[n0 + nb] += add[nb];
+                    for (int nb = 0; nb < 4; ++nb) S[n0 + nb] += add[nb];
+                }
             }
         }
         __syncthreads();
@@ -689,7 +694,7 @@ sd_conv_bwd_kernel(const IO *__restrict__ x, int64_t xstride, const float *__res
     *reinterpret_cast<f32x4_t *>(p + 4 * (int64_t)dc) = f32x4_t{ab[0], ab[1], ab[2], ab[3]};
 }
 
-// Sums over n parts of `planes` planes of `cols` columns, in a fixed order, to the parameters' gradients:
+// Sums over n parts of `planes` planes of `cols` columns, in a fixed order and in 64 bits (the parts cancel), to the parameters' gradients:
 // out[plane] + col * stride[plane] (null: not wanted).
 struct sd_sums {
     float *out[5];
@@ -698,11 +703,11 @@ struct sd_sums {
 constexpr int kSdSumCols = 32, kSdSumGroups = 32;
 static __global__ void __launch_bounds__(kSdSumCols *kSdSumGroups)
 sd_sum_kernel(const float *__restrict__ part, int64_t n, int cols, int planes, sd_sums o) {
-    __shared__ float red[kSdSumGroups][kSdSumCols + 1];
+    __shared__ double red[kSdSumGroups][kSdSumCols + 1];
     const int col = threadIdx.x % kSdSumCols, g = threadIdx.x / kSdSumCols;
     const int cblocks = (cols + kSdSumCols - 1) / kSdSumCols, plane = blockIdx.x / cblocks;
     const int c = blockIdx.x % cblocks * kSdSumCols + col;
-    float a = 0.0f;
+    double a = 0.0;
     if (c < cols) {
 #pragma unroll 8
         for (int64_t k = g; k < n; k += kSdSumGroups) a += part[(k * planes + plane) * cols + c];
@@ -712,7 +717,7 @@ sd_sum_kernel(const float *__restrict__ part, int64_t n, int cols, int planes, s
     if (g == 0 && c < cols && o.out[plane]) {
 #pragma unroll
         for (int k = 1; k < kSdSumGroups; ++k) a += red[k][col];
-        o.out[plane][(int64_t)c * o.stride[plane]] = a;
+        o.out[plane][(int64_t)c * o.stride[plane]] = (float)a;
     }
 }
 
