@@ -51,8 +51,11 @@ int launched() {
 // Threads per group (and vectors of four values per thread) by the group's width: the fewest that hold it.
 int group_threads(int64_t D) { return D <= 32 ? 8 : D <= 64 ? 16 : D <= 128 ? 32 : D <= 1024 ? 64 : D <= 5120 ? 256 : 512; }
 
-// Workgroups, at most: they take several rows each, so that the weights they hold are worth it.
-constexpr int64_t kFwdGroups = 1024, kBwdGroups = 512;
+// Workgroups, at most: they take several rows each, so that the weights they hold are worth it; as many as the chip
+// holds at once, or nearly (16384x5120 bf16, 8 groups, gate first: forward 120 us with 1024, 102 with 1536, 109 with
+// 4096; backward 242 with 768, 223 with 1024, which fit where a thread holds up to three vectors).
+constexpr int64_t kFwdGroups = 1536;
+int64_t bwd_groups(int64_t D) { return D <= 768 || (D > 1024 && D <= 2048) ? 1024 : 512; }
 
 ssm::gn_shape shape_of(const ssm_dims *dm, int64_t groups, int64_t z_stride, int flags, const void *z) {
     ssm::gn_shape s;
@@ -76,32 +79,44 @@ int64_t row_blocks(const ssm::gn_shape &s, int64_t most) {
 }
 int64_t norm_parts(const ssm::gn_shape &s) {
     if (s.M == 0) return 0;
-    return s.D > kRegDim ? std::min<int64_t>(s.M, kWideParts) : row_blocks(s, kBwdGroups) * s.rpb;
+    return s.D > kRegDim ? std::min<int64_t>(s.M, kWideParts) : row_blocks(s, bwd_groups(s.D)) * s.rpb;
 }
 
-template <typename IO> auto fwd_kernel_of(int64_t D) {
-    return D <= 32   ? ssm::groupnorm_fwd_kernel<IO, 8, 1>
-         : D <= 64   ? ssm::groupnorm_fwd_kernel<IO, 16, 1>
-         : D <= 128  ? ssm::groupnorm_fwd_kernel<IO, 32, 1>
-         : D <= 256  ? ssm::groupnorm_fwd_kernel<IO, 64, 1>
-         : D <= 512  ? ssm::groupnorm_fwd_kernel<IO, 64, 2>
-         : D <= 768  ? ssm::groupnorm_fwd_kernel<IO, 64, 3>
-         : D <= 1024 ? ssm::groupnorm_fwd_kernel<IO, 64, 4>
-         : D <= 2048 ? ssm::groupnorm_fwd_kernel<IO, 256, 2>
-         : D <= 5120 ? ssm::groupnorm_fwd_kernel<IO, 256, 5>
-                     : ssm::groupnorm_fwd_kernel<IO, 512, 4>;
+template <typename IO, int ACT> auto fwd_kernel_of(int64_t D) {
+    return D <= 32   ? ssm::groupnorm_fwd_kernel<IO, 8, 1, ACT>
+         : D <= 64   ? ssm::groupnorm_fwd_kernel<IO, 16, 1, ACT>
+         : D <= 128  ? ssm::groupnorm_fwd_kernel<IO, 32, 1, ACT>
+         : D <= 256  ? ssm::groupnorm_fwd_kernel<IO, 64, 1, ACT>
+         : D <= 512  ? ssm::groupnorm_fwd_kernel<IO, 64, 2, ACT>
+         : D <= 768  ? ssm::groupnorm_fwd_kernel<IO, 64, 3, ACT>
+         : D <= 1024 ? ssm::groupnorm_fwd_kernel<IO, 64, 4, ACT>
+         : D <= 2048 ? ssm::groupnorm_fwd_kernel<IO, 256, 2, ACT>
+         : D <= 5120 ? ssm::groupnorm_fwd_kernel<IO, 256, 5, ACT>
+                      : ssm::groupnorm_fwd_kernel<IO, 512, 4, ACT>;
 }
-template <typename IO> auto bwd_kernel_of(int64_t D) {
-    return D <= 32   ? ssm::groupnorm_bwd_kernel<IO, 8, 1>
-         : D <= 64   ? ssm::groupnorm_bwd_kernel<IO, 16, 1>
-         : D <= 128  ? ssm::groupnorm_bwd_kernel<IO, 32, 1>
-         : D <= 256  ? ssm::groupnorm_bwd_kernel<IO, 64, 1>
-         : D <= 512  ? ssm::groupnorm_bwd_kernel<IO, 64, 2>
-         : D <= 768  ? ssm::groupnorm_bwd_kernel<IO, 64, 3>
-         : D <= 1024 ? ssm::groupnorm_bwd_kernel<IO, 64, 4>
-         : D <= 2048 ? ssm::groupnorm_bwd_kernel<IO, 256, 2>
-         : D <= 5120 ? ssm::groupnorm_bwd_kernel<IO, 256, 5>
-                     : ssm::groupnorm_bwd_kernel<IO, 512, 4>;
+template <typename IO, int ACT> auto bwd_kernel_of(int64_t D) {
+    return D <= 32   ? ssm::groupnorm_bwd_kernel<IO, 8, 1, ACT>
+         : D <= 64   ? ssm::groupnorm_bwd_kernel<IO, 16, 1, ACT>
+         : D <= 128  ? ssm::groupnorm_bwd_kernel<IO, 32, 1, ACT>
+         : D <= 256  ? ssm::groupnorm_bwd_kernel<IO, 64, 1, ACT>
+         : D <= 512  ? ssm::groupnorm_bwd_kernel<IO, 64, 2, ACT>
+         : D <= 768  ? ssm::groupnorm_bwd_kernel<IO, 64, 3, ACT>
+         : D <= 1024 ? ssm::groupnorm_bwd_kernel<IO, 64, 4, ACT>
+         : D <= 2048 ? ssm::groupnorm_bwd_kernel<IO, 256, 2, ACT>
+         : D <= 5120 ? ssm::groupnorm_bwd_kernel<IO, 256, 5, ACT>
+                      : ssm::groupnorm_bwd_kernel<IO, 512, 4, ACT>;
+}
+template <typename IO> auto fwd_kernel_of(const ssm::gn_shape &s) {
+    return s.act == ssm::kGnPlain       ? fwd_kernel_of<IO, ssm::kGnPlain>(s.D)
+         : s.act == ssm::kGnGateFirst ? fwd_kernel_of<IO, ssm::kGnGateFirst>(s.D)
+         : s.act == ssm::kGnGateAfter ? fwd_kernel_of<IO, ssm::kGnGateAfter>(s.D)
+                                      : fwd_kernel_of<IO, ssm::kGnSilu>(s.D);
+}
+template <typename IO> auto bwd_kernel_of(const ssm::gn_shape &s) {
+    return s.act == ssm::kGnPlain       ? bwd_kernel_of<IO, ssm::kGnPlain>(s.D)
+         : s.act == ssm::kGnGateFirst ? bwd_kernel_of<IO, ssm::kGnGateFirst>(s.D)
+         : s.act == ssm::kGnGateAfter ? bwd_kernel_of<IO, ssm::kGnGateAfter>(s.D)
+                                      : bwd_kernel_of<IO, ssm::kGnSilu>(s.D);
 }
 
 template <typename IO>
@@ -114,7 +129,7 @@ void launch_fwd(const void *x_, const void *z_, const float *w, const float *bia
                            dim3(ssm::kNormWideThreads), 0, st, x, z, w, bias, eps, y, mean, rstd, s);
         return;
     }
-    hipLaunchKernelGGL(fwd_kernel_of<IO>(s.D), dim3((unsigned)(row_blocks(s, kFwdGroups) * s.gblocks)),
+    hipLaunchKernelGGL(fwd_kernel_of<IO>(s), dim3((unsigned)(row_blocks(s, kFwdGroups) * s.gblocks)),
                        dim3(std::max(group_threads(s.D), 256)), 0, st, x, z, w, bias, eps, y, mean, rstd, s);
 }
 
@@ -136,7 +151,7 @@ void launch_bwd(const void *dy_, const void *x_, const void *z_, const float *w,
                                dim3(256), 0, st, dy, x, z, w, bias, mean, rstd, pw, pb, s, per);
         }
     } else if (s.M > 0) {
-        hipLaunchKernelGGL(bwd_kernel_of<IO>(s.D), dim3((unsigned)(row_blocks(s, kBwdGroups) * s.gblocks)),
+        hipLaunchKernelGGL(bwd_kernel_of<IO>(s), dim3((unsigned)(row_blocks(s, bwd_groups(s.D)) * s.gblocks)),
                            dim3(std::max(group_threads(s.D), 256)), 0, st, dy, x, z, w, bias, mean, rstd, dx, dz, pw, pb, s);
     }
     if (sums)
