@@ -243,19 +243,18 @@ __device__ __forceinline__ f32x4_t ld4(const float *p) { return *reinterpret_cas
 // ---- the convolution ------------------------------------------------------------------------
 
 // u is rounded in the middle of the path, and every kernel that forms it has to form the same one: the exact value
-// rounded to fp32 and then to bf16.  The fp32 value u = silu(v) that conv_silu returns, with v from four products whose
-// absolute sum (and the bias's) is `size`, is off by at most
-//   1.1 * 4 * 2^-24 size           (v's roundings; silu's slope is below 1.1)
+// rounded to fp32 and then to bf16.  The fp32 value u = silu(v) that conv_silu returns, with v from four products added up
+// one after the other and `size` the sum of the sizes of the four sums (v the last), is off by at most
+//   1.1 * 2^-24 size               (the sums' roundings; silu's slope is below 1.1)
 //   (7 + 2.2 |v|) 2^-24 |u|        (the exponent's roundings, where v < 0; the exponential and the reciprocal, 2 each; a sum,
 //                                   a product and v itself, 1 each)
-// and `near` says whether a border between two bf16 values is that near (one value in two thousand): then it is formed
-// again in 64 bits.
+// and `near` says whether a border between two bf16 values is that near (one value in a few thousand): then it is formed
+// again in 64 bits.  (Where e^-v leaves fp32, v is near by its size.)
 __device__ __forceinline__ float conv_silu(float v, float size, bool &near) {
     const float u = silu_f32(v);
     const float border = __uint_as_float((__float_as_uint(u) & 0xffff0000u) | 0x8000u);
-    const float rel = fmaf(fmaxf(-v, 0.0f), 2.5f, 8.0f) * 0x1p-24f;
-    // (not "<=", so that a NaN is near; a large negative v too, whose exponential leaves fp32)
-    near = !(fabsf(u - border) > fmaf(size, 5.0f * 0x1p-24f, rel * fabsf(u))) || v < -64.0f;
+    const float rel = fmaf(fmaxf(-v, 0.0f), 2.5f * 0x1p-24f, 8.0f * 0x1p-24f);
+    near = !(fabsf(u - border) > fmaf(size, 1.125f * 0x1p-24f, rel * fabsf(u)));   // (not "<=", so that a NaN is near)
     return u;
 }
 
@@ -330,24 +329,18 @@ __device__ __forceinline__ void conv_token(const float (&w)[kSdTaps][kSdConvV], 
     bool near[kSdConvV] = {};
 #pragma unroll
     for (int e = 0; e < kSdConvV; ++e) {
-        float p = fmaf(w[0][e], x0[e], b[e]);
-        p = fmaf(w[1][e], x1[e], p);
-        p = fmaf(w[2][e], x2[e], p);
-        p = fmaf(w[3][e], x3[e], p);
+        const float p1 = fmaf(w[0][e], x0[e], b[e]), p2 = fmaf(w[1][e], x1[e], p1), p3 = fmaf(w[2][e], x2[e], p2);
+        const float p = fmaf(w[3][e], x3[e], p3);
         if constexpr (sizeof(IO) == 2) {
-            float size = fmaf(fabsf(w[0][e]), fabsf(x0[e]), fabsf(b[e]));
-            size = fmaf(fabsf(w[1][e]), fabsf(x1[e]), size);
-            size = fmaf(fabsf(w[2][e]), fabsf(x2[e]), size);
-            size = fmaf(fabsf(w[3][e]), fabsf(x3[e]), size);
-            o[e] = f32_to_bf16(conv_silu(p, size, near[e]));
+            o[e] = f32_to_bf16(conv_silu(p, (fabsf(p1) + fabsf(p2)) + (fabsf(p3) + fabsf(p)), near[e]));
         } else {
             o[e] = silu_f32(p);
         }
     }
     if constexpr (sizeof(IO) == 2)
-        if (near[0] || near[1] || near[2] || near[3]) {   // (one branch a token: one an element cost more)
-#pragma unroll
-            for (int e = 0; e < kSdConvV; ++e)
+        if (near[0] || near[1] || near[2] || near[3]) {   // 
+#pragma unroll 1
+            for (int e = 0; e < kSdConvV; ++e)   // (unrolled it took registers from the rest: B1 L65536 of 4096 channels 280 us for 265)
                 if (near[e]) {
                     double q = fma((double)w[0][e], (double)x0[e], (double)b[e]);
                     q = fma((double)w[1][e], (double)x1[e], q);
