@@ -1,7 +1,8 @@
 /*
  * libssmscan -- the Mamba selective state-space scan (S6) and its single-token
  * recurrent step on AMD MI355X (gfx950), and their neighbours in a block: the causal
- * convolution, the state space dual layer, the gated linear recurrence, the layer norm.
+ * convolution, the state space dual layer (alone, or with its convolution: prompts, single
+ * tokens, gradients), the gated linear recurrence, the layer norm, the group norm with a gate.
  *
  * What is computed (per channel d of sequence b, state index n):
  *   step size       dt_t   = softplus(delta_t + delta_bias[d])   with SSM_SCAN_SOFTPLUS

@@ -24,6 +24,8 @@ namespace ssm {
 // 64-channel tile, segment).  each: [b][h][chunk][P][N], or null.  from: [b][h][segment][P][N], or null (zero).  to: with
 // `ends` [b][h][segment][P][N], what every segment leaves, else [b][h][P][N], what the last (ADJ: first) one leaves, or null.
 // FULL as in sd_scan_kernel.
+// Bound: HBM where every chunk's state is written (B8 L2048 H80 N64 bf16, adjoints: 157 us, 506 MB, 3.2 TB/s), the chunks'
+// chain otherwise (B1 L65536 H32 N128, 16 segments: 155 us).
 template <typename E, int NT, bool ADJ, bool FULL>
 __global__ void __launch_bounds__(kSdThreads)
 sd_walk_kernel(const typename sd<E>::io *__restrict__ u_, const typename sd<E>::io *__restrict__ dy_,
@@ -167,6 +169,13 @@ struct sd_grad {
 // 16 from 16 w of dC, kind 1 those of dB; kinds 2 and 3 (z = 0, 1) the 16 tokens 16 w .. of the chunk as s of T, G and v, of
 // these the tokens t in blocks z and 3 - z of T and the channels 32 z .. of every 64 of v.
 // MODE 1: whole tiles (P a multiple of 64, N = NT), without the checks for less; 2: and one item per head (P = N = 64).
+// (B5 L777 H20 N128 bf16: 125 us, 154 without MODE; B2 L2048 H24 N64 fp32: 70, 79.)
+// The pairs of tokens are worked on once a head's 64 channels have their last states, 32 tokens t at a time: G, K, T and
+// what comes of them then live for a few products only (492 us for B8 L2048 H80 N64 with G K of all tokens held over a
+// head, 351 - 370 this way).  Waves of kinds in loops of their own took less than eight waves of every kind's work (559) and
+// four (683): a kind's accumulators stay in 128 registers.
+// Bound: LDS reads (40 - 56 % of the time), vector instructions and the barrier of an item, none of them full; HBM sees
+// 1.1 GB there.
 template <typename E, int NT, int MODE>
 __global__ void __launch_bounds__(kSdBwdThreads) __attribute__((amdgpu_waves_per_eu(4)))
 sd_bwd_kernel(const typename sd<E>::io *__restrict__ u_, const typename sd<E>::io *__restrict__ dy_,
@@ -581,7 +590,7 @@ sd_bwd_kernel(const typename sd<E>::io *__restrict__ u_, const typename sd<E>::i
     }
 }
 
-// dbc's HS parts of n elements each, added up in the first.
+// dbc's HS parts of n elements each, added up in the first (HBM; 4.8 us for B2 L2048 G1 N64).
 static __global__ void __launch_bounds__(256) sd_parts_kernel(float *dbc, int64_t n, int HS) {
     const int64_t e = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
     if (e >= n) return;
@@ -594,7 +603,8 @@ static __global__ void __launch_bounds__(256) sd_parts_kernel(float *dbc, int64_
 // Back through silu and the convolution; thread: kSdConvV channels of `tt` tokens, kSdConvT at a time, the next ones'
 // rows requested before.  With g_t = du_t silu'(pre_t):
 //   dx_t = sum_j w[j] g_{t+3-j},   dw[j] = sum g_t x_{t-3+j},   db = sum g_t         (w[j]: four taps, oldest first)
-// so a thread forms g for three tokens past its own.  parts: [b * tile][5][dc] sums over the tile's tokens of dw's four
+// so a thread forms g for three tokens past its own.  Bound: HBM (B8 L2048 of 5,248 channels bf16: 148 us, 688 MB, 4.6 TB/s;
+// B2 L2048 of 1,664 fp32 20 us).  parts: [b * tile][5][dc] sums over the tile's tokens of dw's four
 // taps and of db.
 template <typename IO, bool AL>
 __global__ void __launch_bounds__(256)

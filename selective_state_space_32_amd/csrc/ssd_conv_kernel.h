@@ -101,20 +101,6 @@ template <typename E, int NS> struct formed {
         }
     }
 };
-template <typename E, int NS>
-__device__ __forceinline__ f32x4_t mma_fa(const formed<E, NS> &a0, const formed<E, NS> &a1, typename sd<E>::frag b0,
-                                          typename sd<E>::frag b1, f32x4_t c) {
-#pragma unroll
-    for (int i = 0; i < formed<E, NS>::N; ++i) c = mma(a0.p[i], a1.p[i], b0, b1, c);
-    return c;
-}
-template <typename E, int NS>
-__device__ __forceinline__ f32x4_t mma_fb(typename sd<E>::frag a0, typename sd<E>::frag a1, const formed<E, NS> &b0,
-                                          const formed<E, NS> &b1, f32x4_t c) {
-#pragma unroll
-    for (int i = 0; i < formed<E, NS>::N; ++i) c = mma(a0, a1, b0.p[i], b1.p[i], c);
-    return c;
-}
 // Two fragments of operands that both come from LDS, whose order of k is free: a lane holds the eight consecutive k at
 // 8 (l / 16) of a 32-wide step (16-byte reads move twice the bytes of 8-byte ones in the same time).
 template <typename E> struct op32 {
@@ -151,7 +137,7 @@ __device__ __forceinline__ f32x4_t widen(f32x4_t v) { return v; }
 // ---- tiles ----------------------------------------------------------------------------------
 
 // 64 rows (tokens) of W elements between memory and LDS, 16 bytes per thread and access.  Addresses are a
-// uniform base and a 32-bit offset per lane (64 rows of at most 2^25 elements of 4 bytes).
+// uniform base and a 32-bit offset per lane (64 rows of at most 2^23 elements of 4 bytes).
 template <typename E, int W, int THREADS = kSdThreads> struct tile64 {
     static constexpr int EPU = 16 / (int)sizeof(E);           // elements per unit
     static constexpr int UPR = W / EPU;                       // units per row
@@ -364,6 +350,10 @@ struct sd_tok_args {
 // kSdConvV channels of `tt` tokens, kSdConvT at a time, the next ones' rows requested before.  A row before token 0 comes
 // from st_in (zero without it).  The thread of the first tokens also writes the W - 1 rows before token len
 // (st_out may be st_in: nothing else reads it, as tt >= 3).  Taps short of four count as zeros in front.
+// Bound: vector instructions in bf16, of which the exact rounding is a third, then HBM: B8 L2048 of 5,248 channels bf16
+// 105 - 113 us (344 MB, 3.2 TB/s; 83 without the rounding's test), B1 L65536 of 4,096 263 us (1.07 GB, 4.1 TB/s; 203);
+// B2 L2048 of 1,664 fp32 12.5 us.  Workgroups behind the convolution's write the tokens' decays, as the work of a launch of
+// their own is small.
 constexpr int kSdConvT = 4;
 template <typename IO, bool AL>
 __global__ void __launch_bounds__(256)
@@ -520,7 +510,8 @@ struct sd_segment {
 };
 
 // The states (or adjoints, REV) that the segments start from, from those that they leave when they start from zero:
-// one workgroup per 1024 elements of a (sequence, head).  seg: [b][h][segment][P N], in place.
+// one workgroup per 1024 elements of a (sequence, head).  seg: [b][h][segment][P N], in place.  Bound: the chain of
+// segments, a read and a write each (B1 L65536 H32 P64 N128, 16 segments: 19 us).
 template <bool REV>
 __global__ void __launch_bounds__(256)
 sd_combine_kernel(const float *__restrict__ tok, const float *__restrict__ first, float *__restrict__ seg, sd_shape s, int blocks) {
@@ -551,7 +542,12 @@ sd_combine_kernel(const float *__restrict__ tok, const float *__restrict__ first
 // One workgroup per (sequence, head, 64-channel tile, segment): the segment's chunks in order, the state in
 // accumulators.  from: the segments' first states [b][h][segment][P][N], or null (zero); last: [b][h][P][N].  ckpt:
 // [b][h][chunk][P][N], receives the state entering each chunk, or null.
-// FULL: whole tiles (P a multiple of 64, N = NT), without the checks for less.
+// FULL: whole tiles (P a multiple of 64, N = NT), without the checks for less (B8 L2048 H80 N64: 195 us, 207 with them).
+// The state stays in accumulators, so HBM sees rows and y only (rows through L2 where heads share B and C).  Bound: the
+// chain of a chunk's products, each workgroup's waves waiting 70 % of the time at two barriers a chunk, vector
+// instructions (forming operands) beside them half of it; B8 L2048 H80 N64 bf16 158 us in a call (rows
+// and y: 340 MB at 2.2 TB/s), with the chunks' states written 250; B1 L65536 H32 N128 in 16 segments 370; B2 L2048 H24
+// fp32 46.  Three waves a SIMD (N <= 64, bf16) is what LDS allows.
 template <typename E, int NT, bool FULL>
 __global__ void __launch_bounds__(kSdThreads)
 __attribute__((amdgpu_waves_per_eu(sd<E>::split && NT == 64 ? 3 : 2)))
@@ -719,6 +715,8 @@ sd_scan_kernel(const typename sd<E>::io *__restrict__ u_, const float *__restric
 // ---- one token ------------------------------------------------------------------------------
 
 // The convolution of one token a sequence, its rows advanced in place; thread: kSdConvV channels of a sequence.
+// Bound: its reads' latency (256 sequences of 5,248 channels bf16: 10.6 us, 13.4 MB; one of 4,096: 3.0 us).  The prompt's
+// kernel took 24 us: a thread of it reads past tokens and writes the rows after its own work.
 template <typename IO, bool AL>
 __global__ void __launch_bounds__(256)
 sd_conv_step_kernel(const IO *__restrict__ x, int64_t xstride, const float *__restrict__ w, const float *__restrict__ bias,
@@ -747,7 +745,8 @@ sd_conv_step_kernel(const IO *__restrict__ x, int64_t xstride, const float *__re
 }
 
 // One workgroup per (sequence, head, part of its channels): LPR lanes hold a channel's N states, four each; U channels
-// at a time.
+// at a time.  Bound: HBM, the state read and written once (256 sequences of 80 heads P64 N64: 671 MB in 119 us, 5.6 TB/s;
+// one of 32 heads N128: 3.9 us, 6.5 with one workgroup a head).
 template <typename IO, int LPR, int U>
 __global__ void __launch_bounds__(256)
 sd_step_kernel(float *__restrict__ state, const IO *__restrict__ u, const IO *__restrict__ dt, int64_t dt_stride,
