@@ -351,7 +351,7 @@ struct sd_tok_args {
 // from st_in (zero without it).  The thread of the first tokens also writes the W - 1 rows before token len
 // (st_out may be st_in: nothing else reads it, as tt >= 3).  Taps short of four count as zeros in front.
 // Bound: vector instructions in bf16, of which the exact rounding is a third, then HBM: B8 L2048 of 5,248 channels bf16
-// 105 - 113 us (344 MB, 3.2 TB/s; 83 without the rounding's test), B1 L65536 of 4,096 263 us (1.07 GB, 4.1 TB/s; 203);
+// 95 - 113 us (344 MB, 3.0 - 3.6 TB/s; 83 without the rounding's test), B1 L65536 of 4,096 249 - 263 us (1.07 GB, 4.1 - 4.3 TB/s; 203);
 // B2 L2048 of 1,664 fp32 12.5 us.  Workgroups behind the convolution's write the tokens' decays, as the work of a launch of
 // their own is small.
 constexpr int kSdConvT = 4;
@@ -544,10 +544,10 @@ sd_combine_kernel(const float *__restrict__ tok, const float *__restrict__ first
 // [b][h][chunk][P][N], receives the state entering each chunk, or null.
 // FULL: whole tiles (P a multiple of 64, N = NT), without the checks for less (B8 L2048 H80 N64: 195 us, 207 with them).
 // The state stays in accumulators, so HBM sees rows and y only (rows through L2 where heads share B and C).  Bound: the
-// chain of a chunk's products, each workgroup's waves waiting 70 % of the time at two barriers a chunk, vector
-// instructions (forming operands) beside them half of it; B8 L2048 H80 N64 bf16 158 us in a call (rows
-// and y: 340 MB at 2.2 TB/s), with the chunks' states written 250; B1 L65536 H32 N128 in 16 segments 370; B2 L2048 H24
-// fp32 46.  Three waves a SIMD (N <= 64, bf16) is what LDS allows.
+// chain of a chunk's products: the waves wait half of the time (two barriers a chunk), while vector instructions and LDS
+// are busy 40 % of it each; B8 L2048 H80 N64 bf16 169 us (rows and y, 340 MB, 2.0 TB/s; reads of C without their bank
+// conflicts took LDS to 33 % and changed nothing), with the chunks' states written 246; B1 L65536 H32 N128 in 16
+// segments 354 - 370; B2 L2048 H24 fp32 46.  Three waves a SIMD (N <= 64, bf16) is what LDS allows.
 template <typename E, int NT, bool FULL>
 __global__ void __launch_bounds__(kSdThreads)
 __attribute__((amdgpu_waves_per_eu(sd<E>::split && NT == 64 ? 3 : 2)))
