@@ -174,8 +174,8 @@ struct sd_grad {
 // what comes of them then live for a few products only (492 us for B8 L2048 H80 N64 with G K of all tokens held over a
 // head, 351 - 370 this way).  Waves of kinds in loops of their own took less than eight waves of every kind's work (559) and
 // four (683): a kind's accumulators stay in 128 registers.
-// Bound: LDS reads (40 - 56 % of the time), vector instructions and the barrier of an item, none of them full; HBM sees
-// 1.1 GB there.
+// Bound: HBM, 1.5 GB in 349 us there (4.3 TB/s; each chunk's states and adjoints are 45 % of it), with vector
+// instructions busy 52 % and LDS 36 % of the time beside it.
 template <typename E, int NT, int MODE>
 __global__ void __launch_bounds__(kSdBwdThreads) __attribute__((amdgpu_waves_per_eu(4)))
 sd_bwd_kernel(const typename sd<E>::io *__restrict__ u_, const typename sd<E>::io *__restrict__ dy_,

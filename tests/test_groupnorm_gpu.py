@@ -272,3 +272,24 @@ def test_offsets_beyond_32_bits():
     g2 = ssmscan.groupnorm_bwd(tail, tail, w, None, None, r2, groups=8, z=tail, gate_first=True)
     torch.cuda.synchronize()
     assert torch.equal(y[-100:], y2) and torch.equal(g["dx"][-100:], g2["dx"]) and torch.equal(g["dz"][-100:], g2["dz"])
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("gate", GATES)
+def test_group_of_one_channel_is_its_mean(io, gate):
+    """n = 0 exactly, so y is the bias (under its gate or activation) and x, z (gate first) and the weight get no gradient."""
+    c = Case(50, 37, 37, io, gate, True, seed=77, offset=3.0)
+    y, mean, rstd = c.fwd()
+    g = c.bwd(mean, rstd)
+    assert not torch.any(g["dx"]) and not torch.any(g["dweight"])
+    if gate == "before":
+        assert not torch.any(g["dz"])
+        assert torch.equal(y.float(), c.t["b"].to(y.dtype).float().expand(50, 37))
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("gate", GATES)
+@pytest.mark.parametrize("dim,groups", [(640, 1), (5120, 8), (1536, 24), (2500, 1)])
+def test_more_rows_than_workgroups(io, gate, dim, groups):
+    """Workgroups that take several rows each, of which the last is short."""
+    check(Case(3001, dim, groups, io, gate, groups != 8, seed=80 + groups))

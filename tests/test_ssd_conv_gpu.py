@@ -373,3 +373,45 @@ def test_offsets_beyond_32_bits():
     ys, lasts, rowss = ssmscan.ssd_conv_fwd(x[1:], w, None, dt[1:], A, None, bias, dstate=N)
     torch.cuda.synchronize()
     assert torch.equal(y[1:], ys) and torch.equal(last[1:], lasts) and torch.equal(rows[1:], rowss)
+
+
+@pytest.mark.parametrize("io", IOS)
+@pytest.mark.parametrize("S,H,P,G,N", [(1, 1, 1000, 1, 8), (1, 2, 264, 2, 128), (1050, 2, 40, 1, 64), (1, 3, 72, 1, 104)])
+def test_step_in_parts(io, S, H, P, G, N):
+    """A head's channels in several workgroups, with a last part of few or none, and in turns of one workgroup."""
+    c = Case(S, 2, H, P, G, N, io, seed=1400 + P)
+    ry, rlast, rrows = c.oracle().scan()
+    a, st, cs = c.layer(), c.t["h0"].clone(), c.t["conv_state"].clone()
+    for t in range(2):
+        y = ssmscan.ssd_conv_step(st, cs, a[0][:, t], *a[1:3], a[3][:, t], *a[4:], **c.shape())
+        torch.cuda.synchronize()
+        close(y, ry[:, t], io, F32, f"token {t}")
+    close(st, rlast, "f32", F32, "state")
+    assert np.array_equal(to_host_f64(cs), rrows)
+
+
+@pytest.mark.parametrize("io", IOS)
+@pytest.mark.parametrize("H,P,G,N", [(4, 192, 2, 128), (2, 200, 1, 72), (3, 128, 1, 64), (1, 320, 1, 8)])
+def test_heads_of_several_tiles(io, H, P, G, N):
+    """What the backward adds up over a head's tiles of 64 channels, over more than one chunk."""
+    check(Case(2, 150, H, P, G, N, io, seed=1500 + P, lens=[150, 97]), label=f"{P} channels")
+
+
+def test_two_streams_at_once():
+    """Calls in flight together, each with a workspace of its own, give what they give alone."""
+    cases = [Case(2, 700, 6, 64, 2, 64, "bf16", seed=1600 + i) for i in range(2)]
+    alone = [run_fwd(c) + tuple(run_bwd(c).values()) for c in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    for _ in range(3):
+        out = []
+        for s in streams:
+            s.wait_stream(torch.cuda.current_stream())
+        for c, s in zip(cases, streams):
+            with torch.cuda.stream(s):
+                fwd = ssmscan.ssd_conv_fwd(*c.layer(), **c.shape(), **c.start())
+                g = ssmscan.ssd_conv_bwd(c.t["dy"], *c.layer(), **c.shape(), **c.start(), dlast_state=c.t.get("dlast"),
+                                         want_initial_state_grad=True, want_conv_state_grad=True)
+                out.append(tuple(fwd) + tuple(g.values()))
+        torch.cuda.synchronize()
+        for got, ref in zip(out, alone):
+            assert all(torch.equal(x, y) for x, y in zip(got, ref))
