@@ -219,7 +219,7 @@ BwdPlan bwd_plan(const ssm_ssd_conv_dims *dm, bool have_checkpoints) {
     const int64_t per = dm->nheads / dm->ngroups, items = std::max<int64_t>(dm->batch * chunks(dm) * dm->ngroups, 1);
     // Parts of a group's heads: what takes the fewest rounds of a workgroup per CU, a workgroup's start and end
     // counted as kStart heads (and its part of dB and dC written and read again).  B5 L777 G4 of five heads each: 125 us
-    // in one part, 144 + 15 in five, as 0 would have it; 8 chose the same there.
+    // in one part, 144 + 15 in five, as 0 would have it (106 in one part since); 8 chose the same there.
     constexpr int64_t kCUs = 256, kStart = 3;
     int64_t best = -1;
     for (int64_t parts = 1; parts <= per; ++parts) {

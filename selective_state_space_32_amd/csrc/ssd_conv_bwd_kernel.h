@@ -169,7 +169,7 @@ struct sd_grad {
 // 16 from 16 w of dC, kind 1 those of dB; kinds 2 and 3 (z = 0, 1) the 16 tokens 16 w .. of the chunk as s of T, G and v, of
 // these the tokens t in blocks z and 3 - z of T and the channels 32 z .. of every 64 of v.
 // MODE 1: whole tiles (P a multiple of 64, N = NT), without the checks for less; 2: and one item per head (P = N = 64).
-// (B5 L777 H20 N128 bf16: 125 us, 154 without MODE; B2 L2048 H24 N64 fp32: 70, 79.)
+// (B5 L777 H20 N128 bf16: 125 us, 154 without MODE, since then 106; B2 L2048 H24 N64 fp32: 70, 79.)
 // The pairs of tokens are worked on once a head's 64 channels have their last states, 32 tokens t at a time: G, K, T and
 // what comes of them then live for a few products only (492 us for B8 L2048 H80 N64 with G K of all tokens held over a
 // head, 351 - 370 this way).  Waves of kinds in loops of their own took less than eight waves of every kind's work (559) and
@@ -366,6 +366,9 @@ sd_bwd_kernel(const typename sd<E>::io *__restrict__ u_, const typename sd<E>::i
         }
     };
     if (kind == 0) {   // through the state entering: dC^T[n][t]
+        // (two blocks of tokens at a time where both halves' accumulators are held: with four they spill, B5 L777 H20 N128
+        // 126 us for 106; with two at N <= 64 the B8 case takes 529)
+        constexpr int kTogether = NH == 1 ? 4 : 2;
         f32x4_t acc[NH][4] = {};
         float dot = 0.0f, ys[4] = {};
         fetch_state(start);
@@ -392,7 +395,7 @@ sd_bwd_kernel(const typename sd<E>::io *__restrict__ u_, const typename sd<E>::i
 #pragma unroll
             for (int half = 0; half < NH; ++half) {
                 if (now.nh != 64 * half) continue;
-#pragma unroll
+#pragma unroll kTogether
                 for (int j = 0; j < 4; ++j) {
                     const op32<E> y0 = row32<E, 64>(tY, 16 * j, 0, lane), y1 = row32<E, 64>(tY, 16 * j, 32, lane);
                     f32x4_t c0 = {}, c1 = {};
