@@ -32,7 +32,6 @@ sd_walk_kernel(const typename sd<E>::io *__restrict__ u_, const typename sd<E>::
                const float *__restrict__ tok, const int32_t *__restrict__ lens, const float *__restrict__ from, float *__restrict__ each,
                float *__restrict__ to, int ends, sd_shape s) {
     using IO = typename sd<E>::io;
-    using F = typename sd<E>::frag;
     constexpr int NB = NT / 16;
     const int N = FULL ? NT : s.N;
     __shared__ __attribute__((aligned(16))) E tB[64 * sd_ld<E>(NT)], tX[64 * sd_ld<E>(64)];
