@@ -1069,20 +1069,19 @@ def _rows(t: torch.Tensor, name: str, lead, width: int, dtype, device) -> int:
         raise ValueError(f"{name}: on {t.device}, expected {device}")
     if t.is_contiguous():
         return width
-    st, shape = t.stride(), t.shape
-    row = span = 0
-    for k in range(t.dim() - 2, -1, -1):
-        if shape[k] == 1:
+    st, row, span = t.stride(), None, 0
+    for k in range(t.dim() - 2, -1, -1):   # (an axis of one has any stride, and none of it counts)
+        if t.shape[k] == 1:
             continue
-        if row == 0:
+        if row is None:
             row = span = st[k]
         elif st[k] != span:
             row = -1
             break
-        span *= shape[k]
-    if (width > 1 and st[-1] != 1) or (row != 0 and row < width):
+        span *= t.shape[k]
+    if (width > 1 and st[-1] != 1) or (row is not None and row < width):   # (0: one row broadcast over the axis)
         raise ValueError(f"{name}: rows must be contiguous and evenly spaced (strides {tuple(st)})")
-    return row or width
+    return width if row is None else row
 
 
 def _ssd_conv_inputs(xbc, conv_w, conv_b, dt, A, D, dt_bias, dstate, ngroups, conv_state, lead):
@@ -1134,7 +1133,7 @@ def ssd_conv_fwd(xbc: torch.Tensor, conv_w: torch.Tensor, conv_b: Optional[torch
     """The state space dual layer with its causal convolution (ssm_ssd_conv_fwd), over whole sequences.
 
     xbc: (batch, L, H P + 2 G N) float32 or bfloat16, the projected x, B and C; dt: (batch, L, H) of the same
-    dtype; both may be parts of a wider projected row.  conv_w: (row, width), conv_b: (row,), A, D, dt_bias:
+    dtype; both may be parts of a wider projected row, not one row broadcast over an axis.  conv_w: (row, width), conv_b: (row,), A, D, dt_bias:
     (H,) float32; dstate N and ngroups G.  conv_state: (batch, width-1, row), the rows before token 0; initial_state:
     (batch, H, P, N) float32; seq_lens: (batch,) int32 on the device, sequence b then has seq_lens[b] tokens and y
     is zero past them.  last_state may be initial_state and conv_state_out conv_state (advanced in place).
@@ -1299,7 +1298,7 @@ def groupnorm_fwd(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Te
     n = (v - mean) rstd over each group (v rstd with centre=False), o = n weight + bias, and y = o, or with a
     gate z: v = x silu(z) (gate_first) or y = o silu(z), or y = silu(o) (silu).
 
-    x: (..., dim) float32 or bfloat16; z: the same shape, packed or part of a wider row; weight, bias: (dim,)
+    x: (..., dim) float32 or bfloat16; z: the same shape, packed or part of a wider row (not broadcast); weight, bias: (dim,)
     float32.  Returns (y, mean, rstd): mean (None with centre=False) and rstd (..., groups) float32."""
     dims, zs, flags = _groupnorm_inputs(x, weight, bias, groups, z, gate_first, silu, centre)
     dev, io = x.device, x.dtype
