@@ -13,7 +13,8 @@ using namespace ssmlib;
 
 constexpr int64_t kMaxTokens = int64_t(1) << 30;
 constexpr int64_t kMaxElems = int64_t(1) << 46;
-constexpr int64_t kMaxGrid = (int64_t(1) << 31) - 1;
+// Workgroups of a launch at most: HIP refuses 2^32 threads or more in a dimension.
+constexpr int64_t max_groups(int threads) { return ((int64_t(1) << 32) - 1) / threads; }
 
 int64_t row_of(const ssm_ssd_conv_dims *dm) { return dm->nheads * dm->headdim + 2 * dm->ngroups * dm->dstate; }
 size_t elem_size(const ssm_ssd_conv_dims *dm) { return dm->io_dtype == SSM_IO_BF16 ? 2 : 4; }
@@ -46,8 +47,6 @@ int check_dims(const ssm_ssd_conv_dims *dm) {
         (dm->batch > kMaxElems / row / std::max<int64_t>(dm->seqlen, 1) ||
          dm->batch > kMaxElems / (dm->nheads * dm->headdim * dm->dstate) / std::max<int64_t>(chunks(dm), 1)))
         return fail(SSM_ERR_SHAPE, "the rows or the states exceed 2^46 elements");
-    if (dm->batch > 0 && dm->nheads * p_tiles(dm) > kMaxGrid / dm->batch)
-        return fail(SSM_ERR_SHAPE, "batch*nheads*ceil(headdim/64) exceeds 2^31 - 1 (grid size)");
     if (dm->xbc_stride < 0 || dm->dt_stride < 0 || (dm->xbc_stride && dm->xbc_stride < row) ||
         (dm->dt_stride && dm->dt_stride < dm->nheads) || dm->xbc_stride > kMaxTokens || dm->dt_stride > kMaxTokens)
         return fail(SSM_ERR_SHAPE, "a stride between tokens is smaller than the row or larger than 2^30");
@@ -108,7 +107,7 @@ int conv_tokens(const ssm_ssd_conv_dims *dm) {
 }
 struct ConvGrid {
     int64_t vblocks, tiles, blocks, quads;   // workgroups of the convolution: vblocks * tiles * batch; then the tokens'
-    bool fits() const { return blocks + quads <= kMaxGrid; }
+    bool fits() const { return blocks + quads <= max_groups(256); }
 };
 ConvGrid conv_grid(const ssm_ssd_conv_dims *dm, int tt, bool tokens) {
     ConvGrid g;
@@ -117,6 +116,18 @@ ConvGrid conv_grid(const ssm_ssd_conv_dims *dm, int tt, bool tokens) {
     g.blocks = g.vblocks * g.tiles * dm->batch;
     g.quads = tokens ? dm->batch * chunks(dm) * ceil_div(dm->nheads, 4) : 0;
     return g;
+}
+
+// Whether the forward's launches can be made (the last of them as well as the first: none is made otherwise).
+int check_forward(const ssm_ssd_conv_dims *dm) {
+    const int rc = check_dims(dm);
+    if (rc != SSM_OK || dm->batch == 0 || dm->nheads == 0) return rc;
+    if (dm->nheads * p_tiles(dm) > max_groups(ssm::kSdThreads) / dm->batch)   // (segments only add to less than kSegTarget)
+        return fail(SSM_ERR_SHAPE, "batch*nheads*ceil(headdim/64) exceeds %lld, the workgroups of a launch",
+                    (long long)max_groups(ssm::kSdThreads));
+    if (!conv_grid(dm, conv_tokens(dm), true).fits())
+        return fail(SSM_ERR_SHAPE, "batch*seqlen exceeds the convolution's launch (%lld workgroups)", (long long)max_groups(256));
+    return SSM_OK;
 }
 
 // u, the rows after the last token, and with `tok` the tokens' decays
@@ -174,6 +185,16 @@ void launch_scan(const void *u, const float *tok, const float *D, const int32_t 
     auto kern = s.N == NT && s.P % 64 == 0 ? ssm::sd_scan_kernel<E, NT, true> : ssm::sd_scan_kernel<E, NT, false>;
     hipLaunchKernelGGL(kern, dim3((unsigned)(dm->batch * s.H * s.PT * s.nseg)), dim3(ssm::kSdThreads), 0, st,
                        static_cast<const IO *>(u), tok, D, lens, from, static_cast<IO *>(y), last, ckpt, s);
+}
+
+// The step's launches (of few heads in parts there are at most 2048 and as many again).
+int check_step(const ssm_ssd_conv_dims *dm) {
+    const int rc = check_dims(dm);
+    if (rc != SSM_OK) return rc;
+    if (dm->batch > max_groups(256) / std::max(ceil_div(row_of(dm) / ssm::kSdConvV, 256), dm->nheads))
+        return fail(SSM_ERR_SHAPE, "batch*nheads or batch*ceil(row/1024) exceeds %lld, the workgroups of a launch",
+                    (long long)max_groups(256));
+    return SSM_OK;
 }
 
 template <typename IO>
@@ -252,6 +273,19 @@ BwdPlan bwd_plan(const ssm_ssd_conv_dims *dm, bool have_checkpoints) {
     return p;
 }
 
+// The backward's launches (those of a forward among them, which forms what there are no checkpoints of).
+int check_backward(const ssm_ssd_conv_dims *dm, int flags) {
+    const int rc = check_forward(dm);
+    if (rc != SSM_OK || dm->batch == 0 || dm->nheads == 0) return rc;
+    if (dm->batch * chunks(dm) > max_groups(ssm::kSdBwdThreads) / (dm->ngroups * bwd_plan(dm, flags & SSM_SCAN_CHECKPOINTS).HS))
+        return fail(SSM_ERR_SHAPE, "batch*ceil(seqlen/64)*ngroups exceeds the backward's launch (%lld workgroups)",
+                    (long long)max_groups(ssm::kSdBwdThreads));
+    if (!conv_grid(dm, conv_bwd_tokens(dm), false).fits())
+        return fail(SSM_ERR_SHAPE, "batch*seqlen exceeds the launch of the convolution's backward (%lld workgroups)",
+                    (long long)max_groups(256));
+    return SSM_OK;   // (there are parts of a group's heads for few items only: their sums are of at most 2^25 elements)
+}
+
 template <typename E, int NT>
 void launch_bwd(const void *u, const void *dy, const float *tok, const void *dt, const float *A, const float *D, const float *dt_bias,
                 const int32_t *lens, const float *states, const float *adjoints, void *ddt, const ssm::sd_grad &g,
@@ -296,7 +330,7 @@ int check_workspace(const void *ws, size_t have, size_t need) {
 extern "C" {
 
 size_t ssm_ssd_conv_workspace_bytes(const ssm_ssd_conv_dims *dims, int flags) {
-    if (check_dims(dims) != SSM_OK || dims->batch == 0 || dims->nheads == 0) return 0;
+    if (check_forward(dims) != SSM_OK || dims->batch == 0 || dims->nheads == 0) return 0;
     return u_bytes(dims) + tok_bytes(dims) + ((flags & SSM_SCAN_CHECKPOINTS) ? state_bytes(dims) : 0) + seg_bytes(dims);
 }
 
@@ -304,7 +338,7 @@ int ssm_ssd_conv_fwd(const void *xbc, const float *conv_w, const float *conv_b, 
                      const float *A, const float *D, const float *dt_bias, const float *initial_state,
                      const int32_t *seq_lens, int flags, void *y, float *last_state, void *conv_state_out,
                      const ssm_ssd_conv_dims *dims, void *workspace, size_t workspace_bytes, void *stream) {
-    int rc = check_dims(dims);
+    int rc = check_forward(dims);
     if (rc != SSM_OK) return rc;
     if (flags & ~(SSM_SCAN_SOFTPLUS | SSM_SCAN_CHECKPOINTS)) return fail(SSM_ERR_FLAGS, "unknown flag bits 0x%x", flags);
     const size_t es = elem_size(dims);
@@ -319,7 +353,6 @@ int ssm_ssd_conv_fwd(const void *xbc, const float *conv_w, const float *conv_b, 
     if (dims->seqlen > 0 && (!xbc || !dt || !y)) return fail(SSM_ERR_NULL, "xbc, dt or y is NULL");
     rc = check_workspace(workspace, workspace_bytes, ssm_ssd_conv_workspace_bytes(dims, flags));
     if (rc != SSM_OK) return rc;
-    if (!conv_grid(dims, conv_tokens(dims), true).fits()) return fail(SSM_ERR_SHAPE, "batch*seqlen exceeds the grid of the convolution");
     hipStream_t st = static_cast<hipStream_t>(stream);
     float *tok = reinterpret_cast<float *>(static_cast<char *>(workspace) + u_bytes(dims));
     float *ckpt = (flags & SSM_SCAN_CHECKPOINTS) ? tok + tok_bytes(dims) / sizeof(float) : nullptr;
@@ -334,7 +367,7 @@ int ssm_ssd_conv_fwd(const void *xbc, const float *conv_w, const float *conv_b, 
 }
 
 size_t ssm_ssd_conv_bwd_workspace_bytes(const ssm_ssd_conv_dims *dims, int flags) {
-    if (check_dims(dims) != SSM_OK || dims->batch == 0 || dims->nheads == 0) return 0;
+    if (check_backward(dims, flags) != SSM_OK || dims->batch == 0 || dims->nheads == 0) return 0;
     return bwd_plan(dims, flags & SSM_SCAN_CHECKPOINTS).bytes;
 }
 
@@ -344,7 +377,7 @@ int ssm_ssd_conv_bwd(const void *xbc, const float *conv_w, const float *conv_b, 
                      size_t checkpoints_bytes, void *dxbc, float *dconv_w, float *dconv_b, void *dconv_state, void *ddt,
                      float *dA, float *dD, float *ddt_bias, float *dinitial_state, const ssm_ssd_conv_dims *dims,
                      void *workspace, size_t workspace_bytes, void *stream) {
-    int rc = check_dims(dims);
+    int rc = check_backward(dims, flags);
     if (rc != SSM_OK) return rc;
     if (flags & ~(SSM_SCAN_SOFTPLUS | SSM_SCAN_CHECKPOINTS)) return fail(SSM_ERR_FLAGS, "unknown flag bits 0x%x", flags);
     const size_t es = elem_size(dims);
@@ -369,8 +402,6 @@ int ssm_ssd_conv_bwd(const void *xbc, const float *conv_w, const float *conv_b, 
     rc = check_workspace(workspace, workspace_bytes, ssm_ssd_conv_bwd_workspace_bytes(dims, flags));
     if (rc != SSM_OK) return rc;
     const BwdPlan p = bwd_plan(dims, kept);
-    if (!conv_grid(dims, 8, true).fits() || dims->batch * chunks(dims) > kMaxGrid / dims->nheads)
-        return fail(SSM_ERR_SHAPE, "batch*seqlen exceeds the grids of the backward");
     hipStream_t st = static_cast<hipStream_t>(stream);
     char *ws = static_cast<char *>(workspace);
     auto at = [&](size_t o) { return reinterpret_cast<float *>(ws + o); };
@@ -415,14 +446,14 @@ int ssm_ssd_conv_bwd(const void *xbc, const float *conv_w, const float *conv_b, 
 }
 
 size_t ssm_ssd_conv_step_workspace_bytes(const ssm_ssd_conv_dims *dims) {
-    if (check_dims(dims) != SSM_OK) return 0;
+    if (check_step(dims) != SSM_OK) return 0;
     return align256((size_t)(dims->batch * row_of(dims)) * elem_size(dims));
 }
 
 int ssm_ssd_conv_step(float *state, void *conv_state, const void *xbc, const float *conv_w, const float *conv_b,
                       const void *dt, const float *A, const float *D, const float *dt_bias, int flags, void *y,
                       const ssm_ssd_conv_dims *dims, void *workspace, size_t workspace_bytes, void *stream) {
-    int rc = check_dims(dims);
+    int rc = check_step(dims);
     if (rc != SSM_OK) return rc;
     if (flags & ~SSM_SCAN_SOFTPLUS) return fail(SSM_ERR_FLAGS, "unknown flag bits 0x%x", flags);
     const size_t es = elem_size(dims);
@@ -439,8 +470,6 @@ int ssm_ssd_conv_step(float *state, void *conv_state, const void *xbc, const flo
     hipStream_t st = static_cast<hipStream_t>(stream);
     ssm_ssd_conv_dims one = *dims;
     one.seqlen = 1;
-    if (dims->batch > kMaxGrid / std::max(ceil_div(row_of(dims) / ssm::kSdConvV, 256), dims->nheads))
-        return fail(SSM_ERR_SHAPE, "batch exceeds the grid of the step");
     if (es == 2) {
         launch_conv_step<uint16_t>(xbc, conv_w, conv_b, conv_state, workspace, &one, st);
         launch_step<uint16_t>(state, workspace, dt, A, D, dt_bias, y, &one, flags, st);
