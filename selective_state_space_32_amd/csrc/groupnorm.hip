@@ -57,6 +57,7 @@ int group_threads(int64_t D) { return D <= 32 ? 8 : D <= 64 ? 16 : D <= 128 ? 32
 constexpr int64_t kFwdGroups = 1536;
 int64_t bwd_groups(int64_t D) { return D <= 768 || (D > 1024 && D <= 2048) ? 1024 : 512; }
 
+// (of rows with values: their groups are at most dim, which an int holds)
 ssm::gn_shape shape_of(const ssm_dims *dm, int64_t groups, int64_t z_stride, int flags, const void *z) {
     ssm::gn_shape s;
     s.M = dm->batch * dm->seqlen;
@@ -172,8 +173,8 @@ int ssm_groupnorm_fwd(const void *x, const void *z, int64_t z_stride, const floa
     if (!aligned(x, es) || !aligned(z, es) || !aligned(y, es) || !aligned(weight, 4) || !aligned(bias, 4) ||
         !aligned(mean, 4) || !aligned(rstd, 4))
         return fail(SSM_ERR_ALIGN, "a tensor pointer is not aligned to its element size");
+    if (dims->batch == 0 || dims->seqlen == 0 || dims->dim == 0) return ok();   // (nothing is of any number of groups)
     const ssm::gn_shape s = shape_of(dims, groups, z_stride, flags, z);
-    if (s.M == 0 || s.C == 0) return ok();
     if (!x || !weight || !y) return fail(SSM_ERR_NULL, "x, weight or y is NULL");
     hipStream_t st = static_cast<hipStream_t>(stream);
     if (es == 2) launch_fwd<uint16_t>(x, z, weight, bias, eps, y, mean, rstd, s, st);
@@ -195,8 +196,8 @@ int ssm_groupnorm_bwd(const void *dy, const void *x, const void *z, int64_t z_st
     if (!aligned(dy, es) || !aligned(x, es) || !aligned(z, es) || !aligned(dx, es) || !aligned(dz, es) || !aligned(weight, 4) ||
         !aligned(bias, 4) || !aligned(mean, 4) || !aligned(rstd, 4) || !aligned(dweight, 4) || !aligned(dbias, 4))
         return fail(SSM_ERR_ALIGN, "a tensor pointer is not aligned to its element size");
+    if (dims->dim == 0) return ok();
     const ssm::gn_shape s = shape_of(dims, groups, z_stride, flags, z);
-    if (s.C == 0) return ok();
     if (s.M > 0 && (!dy || !x || !weight || !rstd || !dx || (s.centre && !mean) || (z && !dz)))
         return fail(SSM_ERR_NULL, "required pointer is NULL");
     const size_t need = dweight || dbias ? ssm_groupnorm_bwd_workspace_bytes(dims, groups) : 0;
