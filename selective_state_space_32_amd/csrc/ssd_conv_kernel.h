@@ -203,14 +203,15 @@ __device__ __forceinline__ void sd_write_tokens(float *o, const IO *dt, int64_t 
     o[kSdQ + lane] = (float)(c - (double)ch);
     o[2 * kSdQ + lane] = d;
 }
-// In LDS, with what follows from them.
-struct sd_tokens {
+// In LDS, with what follows from them (read four tokens at a time, 16 bytes).
+struct alignas(16) sd_tokens {
     float ch[kSdQ], cl[kSdQ];
     float dt[kSdQ];
     float w[kSdQ];              // e^{c_last - c_t} dt_t
     float e[kSdQ];              // e^{c_t}
     float dec, pad[3];          // e^{c_last}
 };
+static_assert(sizeof(sd_tokens) % 16 == 0 && alignof(sd_tokens) == 16, "four tokens in a 16-byte read");
 struct sd_tok { float h, l, d; };   // a lane's token
 __device__ __forceinline__ sd_tok sd_load_tokens(const float *o, int lane) { return {o[lane], o[kSdQ + lane], o[2 * kSdQ + lane]}; }
 __device__ __forceinline__ float sd_stage_tokens(sd_tokens &s, sd_tok v, int lane) {   // one wave; e^{c_last - c_t}
