@@ -695,8 +695,8 @@ sd_conv_bwd_kernel(const IO *__restrict__ x, int64_t xstride, const float *__res
                     if constexpr (sizeof(IO) == 2) o[k] = f32_to_bf16(q);
                     else o[k] = q;
                 }
-                if (to >= 0) conv_vec<IO, true>::store(dx + (b * L + to) * dc + c, o);
-                else conv_vec<IO, true>::store(dst + (b * hw + hw + to) * dc + c, o);
+                if (to >= 0) conv_store<IO>(dx + (b * L + to) * dc + c, o);
+                else conv_store<IO>(dst + (b * hw + hw + to) * dc + c, o);
             }
         }
     }

@@ -264,18 +264,14 @@ template <typename IO, bool AL> struct conv_vec {
             for (int k = 0; k < kSdConvV; ++k) v[k] = p[k];
         }
     }
-    __device__ __forceinline__ static void store(IO *p, const IO (&v)[kSdConvV]) {
-        if constexpr (AL) {
-            typedef uint32_t words __attribute__((ext_vector_type(sizeof(IO)), may_alias));
-            words w;
-            __builtin_memcpy(&w, v, sizeof w);
-            *reinterpret_cast<words *>(p) = w;
-        } else {
-#pragma unroll
-            for (int k = 0; k < kSdConvV; ++k) p[k] = v[k];
-        }
-    }
 };
+// To the layer's own tensors, whose rows hold a multiple of eight elements.
+template <typename IO> __device__ __forceinline__ void conv_store(IO *p, const IO (&v)[kSdConvV]) {
+    typedef uint32_t words __attribute__((ext_vector_type(sizeof(IO)), may_alias));
+    words w;
+    __builtin_memcpy(&w, v, sizeof w);
+    *reinterpret_cast<words *>(p) = w;
+}
 template <typename IO> __device__ __forceinline__ float io_f32(IO v) {
     if constexpr (sizeof(IO) == 2) return bf16_to_f32(v);
     else return v;
@@ -325,7 +321,7 @@ __device__ __forceinline__ void conv_token(const float (&w)[kSdTaps][kSdConvV], 
         }
     }
     if constexpr (sizeof(IO) == 2)
-        if (near[0] || near[1] || near[2] || near[3]) {   // 
+        if (near[0] || near[1] || near[2] || near[3]) {
 #pragma unroll 1
             for (int e = 0; e < kSdConvV; ++e)   // (unrolled it took registers from the rest: B1 L65536 of 4096 channels 280 us for 265)
                 if (near[e]) {
@@ -426,7 +422,7 @@ sd_conv_kernel(const IO *__restrict__ x, int64_t xstride, const float *__restric
             }
             if (t + i >= len)
                 for (int e = 0; e < kSdConvV; ++e) o[e] = 0;
-            conv_vec<IO, true>::store(ub + (t + i) * dc, o);
+            conv_store<IO>(ub + (t + i) * dc, o);
         }
     }
     if (st_out && t0 == 0) {   // (last: st_out may be st_in)
@@ -436,7 +432,7 @@ sd_conv_kernel(const IO *__restrict__ x, int64_t xstride, const float *__restric
             if (j < h) row(len - h + j, keep[j]);
 #pragma unroll
         for (int j = 0; j < kSdTaps - 1; ++j)
-            if (j < h) conv_vec<IO, true>::store(st_out + (b * h + j) * dc + c, keep[j]);
+            if (j < h) conv_store<IO>(st_out + (b * h + j) * dc + c, keep[j]);
     }
 }
 
@@ -739,10 +735,10 @@ sd_conv_step_kernel(const IO *__restrict__ x, int64_t xstride, const float *__re
 #pragma unroll
         for (int e = 0; e < kSdConvV; ++e) xv[j][e] = io_f32(r[j][e]);
     conv_token<IO>(wv, bv, xv[0], xv[1], xv[2], xv[3], o);
-    conv_vec<IO, true>::store(u + b * dc + c, o);
+    conv_store<IO>(u + b * dc + c, o);
 #pragma unroll
     for (int j = 1; j < kSdTaps; ++j)
-        if (j > kSdTaps - width) conv_vec<IO, true>::store(st + (b * h + j - 1 - (kSdTaps - width)) * dc + c, r[j]);
+        if (j > kSdTaps - width) conv_store<IO>(st + (b * h + j - 1 - (kSdTaps - width)) * dc + c, r[j]);
 }
 
 // One workgroup per (sequence, head, part of its channels): LPR lanes hold a channel's N states, four each; U channels
