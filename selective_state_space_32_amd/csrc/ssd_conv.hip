@@ -141,7 +141,8 @@ void launch_conv(const void *x_, const float *w, const float *bias, const void *
     const ssm::sd_tok_args k = {dt, A, dt_bias, tok, dm->dt_stride ? dm->dt_stride : dm->nheads, chunks(dm), (int)dm->nheads,
                                 flags & SSM_SCAN_SOFTPLUS, (int)g.blocks};
     const bool al = aligned(x_, ssm::kSdConvV * sizeof(IO)) && stride % ssm::kSdConvV == 0;
-    auto kern = al ? ssm::sd_conv_kernel<IO, true> : ssm::sd_conv_kernel<IO, false>;
+    auto kern = dm->width == ssm::kSdTaps ? al ? ssm::sd_conv_kernel<IO, true, true> : ssm::sd_conv_kernel<IO, false, true>
+              : al ? ssm::sd_conv_kernel<IO, true, false> : ssm::sd_conv_kernel<IO, false, false>;
     hipLaunchKernelGGL(kern, dim3((unsigned)(g.blocks + g.quads)), dim3(256), 0, st, static_cast<const IO *>(x_), stride, w, bias,
                        (int)dm->width, static_cast<const IO *>(st_in), static_cast<IO *>(st_out), lens, static_cast<IO *>(u),
                        dm->seqlen, (int)row_of(dm), tt, (int)g.vblocks, (int)g.tiles, k);
@@ -305,7 +306,8 @@ void launch_conv_bwd(const void *x_, const float *w, const float *bias, const vo
     const int64_t stride = dm->xbc_stride ? dm->xbc_stride : row_of(dm);
     const ConvGrid g = conv_grid(dm, conv_bwd_tokens(dm), false);
     const bool al = aligned(x_, ssm::kSdConvV * sizeof(IO)) && stride % ssm::kSdConvV == 0;
-    auto kern = al ? ssm::sd_conv_bwd_kernel<IO, true> : ssm::sd_conv_bwd_kernel<IO, false>;
+    auto kern = dm->width == ssm::kSdTaps ? al ? ssm::sd_conv_bwd_kernel<IO, true, true> : ssm::sd_conv_bwd_kernel<IO, false, true>
+              : al ? ssm::sd_conv_bwd_kernel<IO, true, false> : ssm::sd_conv_bwd_kernel<IO, false, false>;
     hipLaunchKernelGGL(kern, dim3((unsigned)g.blocks), dim3(256), 0, st, static_cast<const IO *>(x_), stride, w, bias,
                        (int)dm->width, static_cast<const IO *>(st_in), lens, du, dbc, static_cast<IO *>(dx),
                        static_cast<IO *>(dst), parts, dm->seqlen, (int)row_of(dm), (int)(dm->nheads * dm->headdim),

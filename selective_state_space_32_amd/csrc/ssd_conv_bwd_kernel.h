@@ -605,10 +605,10 @@ static __global__ void __launch_bounds__(256) sd_parts_kernel(float *dbc, int64_
 // Back through silu and the convolution; thread: kSdConvV channels of `tt` tokens, kSdConvT at a time, the next ones'
 // rows requested before.  With g_t = du_t silu'(pre_t):
 //   dx_t = sum_j w[j] g_{t+3-j},   dw[j] = sum g_t x_{t-3+j},   db = sum g_t         (w[j]: four taps, oldest first)
-// so a thread forms g for three tokens past its own.  Bound: HBM (B8 L2048 of 5,248 channels bf16: 148 us, 688 MB, 4.6 TB/s;
+// so a thread forms g for three tokens past its own.  W4 as in sd_conv_kernel (a tap that is not there takes no g either).  Bound: HBM (B8 L2048 of 5,248 channels bf16: 148 us, 688 MB, 4.6 TB/s;
 // B2 L2048 of 1,664 fp32 20 us).  parts: [b * tile][5][dc] sums over the tile's tokens of dw's four
 // taps and of db.
-template <typename IO, bool AL>
+template <typename IO, bool AL, bool W4>
 __global__ void __launch_bounds__(256)
 sd_conv_bwd_kernel(const IO *__restrict__ x, int64_t xstride, const float *__restrict__ w, const float *__restrict__ bias,
                    int width, const IO *__restrict__ st_in, const int32_t *__restrict__ lens, const float *__restrict__ du,
@@ -646,7 +646,7 @@ sd_conv_bwd_kernel(const IO *__restrict__ x, int64_t xstride, const float *__res
         if (t >= 0) conv_vec<IO, AL>::load(xb + t * xstride, o);
         else if (st_in && t >= -hw) conv_vec<IO, true>::load(st_in + (b * hw + hw + t) * dc + c, o);
 #pragma unroll
-        for (int k = 0; k < kSdConvV; ++k) past[j][k] = io_f32(o[k]);
+        for (int k = 0; k < kSdConvV; ++k) past[j][k] = W4 || hw >= 3 - j ? io_f32(o[k]) : 0.0f;
     }
     for (int64_t tb = t0; tb < t1 + 3; tb += kSdConvT) {
         IO rn[kSdConvT][kSdConvV];
@@ -682,16 +682,17 @@ sd_conv_bwd_kernel(const IO *__restrict__ x, int64_t xstride, const float *__res
                     aw[3][k] = fmaf(gt, now, aw[3][k]);
                     ab[k] += gt;
                 }
-                past[0][k] = past[1][k];
-                past[1][k] = past[2][k];
-                past[2][k] = now;
+                past[0][k] = W4 || hw >= 3 ? past[1][k] : 0.0f;
+                past[1][k] = W4 || hw >= 2 ? past[2][k] : 0.0f;
+                past[2][k] = W4 || hw >= 1 ? now : 0.0f;
             }
             const int64_t to = t - 3;
             if (to >= t0 || (to < 0 && dst && to >= -hw)) {
                 IO o[kSdConvV];
 #pragma unroll
                 for (int k = 0; k < kSdConvV; ++k) {
-                    const float q = fmaf(wv[0][k], g[0][k], fmaf(wv[1][k], g[1][k], fmaf(wv[2][k], g[2][k], wv[3][k] * g[3][k])));
+                    const float g0 = W4 || hw >= 3 ? g[0][k] : 0.0f, g1 = W4 || hw >= 2 ? g[1][k] : 0.0f, g2 = W4 || hw >= 1 ? g[2][k] : 0.0f;
+                    const float q = fmaf(wv[0][k], g0, fmaf(wv[1][k], g1, fmaf(wv[2][k], g2, wv[3][k] * g[3][k])));
                     if constexpr (sizeof(IO) == 2) o[k] = f32_to_bf16(q);
                     else o[k] = q;
                 }

@@ -346,13 +346,14 @@ struct sd_tok_args {
 // u[b][t][c] = silu(bias + sum_k w[c][k] row_{t - (W-1) + k}), zero at and past a sequence's length; thread:
 // kSdConvV channels of `tt` tokens, kSdConvT at a time, the next ones' rows requested before.  A row before token 0 comes
 // from st_in (zero without it).  The thread of the first tokens also writes the W - 1 rows before token len
-// (st_out may be st_in: nothing else reads it, as tt >= 3).  Taps short of four count as zeros in front.
+// (st_out may be st_in: nothing else reads it, as tt >= 3).  W4: four taps; fewer count as zeros in front, of rows that count
+// as zeros too (what lies in a row that the convolution does not reach, an infinity times no weight, is not its).
 // Bound: vector instructions in bf16, of which the exact rounding is a third, then HBM: B8 L2048 of 5,248 channels bf16
 // 95 - 113 us (344 MB, 3.0 - 3.6 TB/s; 83 without the rounding's test), B1 L65536 of 4,096 249 - 263 us (1.07 GB, 4.1 - 4.3 TB/s; 203);
 // B2 L2048 of 1,664 fp32 12.5 us.  Workgroups behind the convolution's write the tokens' decays, as the work of a launch of
 // their own is small.
 constexpr int kSdConvT = 4;
-template <typename IO, bool AL>
+template <typename IO, bool AL, bool W4>
 __global__ void __launch_bounds__(256)
 sd_conv_kernel(const IO *__restrict__ x, int64_t xstride, const float *__restrict__ w, const float *__restrict__ bias,
                int width, const IO *st_in, IO *st_out, const int32_t *__restrict__ lens, IO *__restrict__ u, int64_t L,
@@ -397,7 +398,7 @@ sd_conv_kernel(const IO *__restrict__ x, int64_t xstride, const float *__restric
         IO o[kSdConvV];
         row(t0 - 3 + j, o);
 #pragma unroll
-        for (int i = 0; i < kSdConvV; ++i) past[j][i] = io_f32(o[i]);
+        for (int i = 0; i < kSdConvV; ++i) past[j][i] = W4 || h >= 3 - j ? io_f32(o[i]) : 0.0f;
     }
     for (int64_t t = t0; t < t1; t += kSdConvT) {
         IO now[kSdConvT][kSdConvV];
@@ -416,9 +417,9 @@ sd_conv_kernel(const IO *__restrict__ x, int64_t xstride, const float *__restric
             conv_token<IO>(wv, bv, past[0], past[1], past[2], last, o);
 #pragma unroll
             for (int e = 0; e < kSdConvV; ++e) {
-                past[0][e] = past[1][e];
-                past[1][e] = past[2][e];
-                past[2][e] = last[e];
+                past[0][e] = W4 || h >= 3 ? past[1][e] : 0.0f;
+                past[1][e] = W4 || h >= 2 ? past[2][e] : 0.0f;
+                past[2][e] = W4 || h >= 1 ? last[e] : 0.0f;
             }
             if (t + i >= len)
                 for (int e = 0; e < kSdConvV; ++e) o[e] = 0;
