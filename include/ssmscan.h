@@ -600,8 +600,7 @@ typedef struct ssm_ssd_conv_dims {
  *                    contents on entry do not matter
  * y, the states and the rows of the convolution's state are 16-byte aligned.  Outputs must not overlap inputs
  * or each other otherwise.  Products of bf16 u take u's values as they are; what is formed in between is carried
- * to 16 bits where the result leaves in bf16 and to 24 where it is kept in fp32, sums and states are fp32; with fp32
- * I/O all products are fp32.  Tokens are taken 64 at a time: a NaN or infinity in a token may reach the
+ * to 24 bits, sums and states are fp32; with fp32 I/O all products are fp32.  Tokens are taken 64 at a time: a NaN or infinity in a token may reach the
  * outputs of the 63 tokens before it, and no others before it.  nheads*headdim and 2*ngroups*dstate are at most
  * 2^22.
  * Returns SSM_OK or a negative ssm_status (nothing is launched on an error). */

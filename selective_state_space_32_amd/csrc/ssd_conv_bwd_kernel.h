@@ -84,7 +84,7 @@ sd_walk_kernel(const typename sd<E>::io *__restrict__ u_, const typename sd<E>::
         for (int k = 0; k < 2; ++k) {
             const float *wt = (ADJ ? tk.e : tk.w) + 32 * k + 8 * (lane >> 4);
             const op32<E> x = col32<E, 64>(tX, 32 * k, 16 * w, lane);
-            const formed<E, 3> f0(widen(x.lo) * ld4(wt)), f1(widen(x.hi) * ld4(wt + 4));
+            const formed<E> f0(widen(x.lo) * ld4(wt)), f1(widen(x.hi) * ld4(wt + 4));
 #pragma unroll
             for (int n0 = 0; n0 < NB; n0 += 4) {
                 op32<E> bv[4];
@@ -92,7 +92,7 @@ sd_walk_kernel(const typename sd<E>::io *__restrict__ u_, const typename sd<E>::
 #pragma unroll
                 for (int nb = 0; nb < 4; ++nb) bv[nb] = col32<E, NT>(tB, 32 * k, 16 * (n0 + nb), lane);
 #pragma unroll
-                for (int m = 0; m < formed<E, 3>::N; ++m)
+                for (int m = 0; m < formed<E>::N; ++m)
 #pragma unroll
                     for (int nb = 0; nb < 4; ++nb) {
                         f32x4_t &to = ADJ ? add[nb] : S[n0 + nb];
@@ -116,13 +116,11 @@ sd_walk_kernel(const typename sd<E>::io *__restrict__ u_, const typename sd<E>::
 // goes into leave in fp32.  For their sake too products that are not of a smaller part start from zero and are added up
 // by vector instructions: the bf16 matrix instruction cuts its addend downward to 2^-24 of its largest product, a bias
 // that sums over tokens collect (B8 L2048 H80 N64: the error of dt_bias's gradient 2.4e-6 that way).
-constexpr int kSdParts = 3;
-
 constexpr int kSdBwdThreads = 1024;
 
 // 64 x 64 of an adjoint [p][n] in fp32 from memory to LDS, as operand parts.
 template <typename E> struct state64 {
-    static constexpr int NP = formed<E, kSdParts>::N, NU = 1024 / kSdBwdThreads, RPP = kSdBwdThreads / 16;
+    static constexpr int NP = formed<E>::N, NU = 1024 / kSdBwdThreads, RPP = kSdBwdThreads / 16;
     f32x4_t r[NU];
     __device__ __forceinline__ void load(const float *m, int N, int pw, int nw) {   // N: row stride; pw x nw exist
         const int p = threadIdx.x / 16, n = threadIdx.x % 16 * 4;
@@ -138,7 +136,7 @@ template <typename E> struct state64 {
         const int p = threadIdx.x / 16, n = threadIdx.x % 16 * 4;
 #pragma unroll
         for (int i = 0; i < NU; ++i) {
-            const formed<E, kSdParts> f(r[i]);
+            const formed<E> f(r[i]);
 #pragma unroll
             for (int k = 0; k < NP; ++k) *reinterpret_cast<typename sd<E>::frag *>(&t[k][(p + RPP * i) * sd_ld<E>(64) + n]) = f.p[k];
         }
@@ -186,7 +184,7 @@ sd_bwd_kernel(const typename sd<E>::io *__restrict__ u_, const typename sd<E>::i
     using F = typename sd<E>::frag;
     constexpr bool FULL = MODE >= 1, ONE = MODE == 2;
     const int N = FULL ? NT : s.N, P = ONE ? 64 : s.P;
-    constexpr int NH = NT / 64, NP = formed<E, kSdParts>::N, LD = sd_ld<E>(64);
+    constexpr int NH = NT / 64, NP = formed<E>::N, LD = sd_ld<E>(64);
     // Two sets of an item's tiles where they fit in LDS: the next item's are staged while one is worked on, and a
     // barrier an item is enough.
     constexpr int NBUF = sd<E>::split || NT == 64 ? 2 : 1;
@@ -376,7 +374,7 @@ sd_bwd_kernel(const typename sd<E>::io *__restrict__ u_, const typename sd<E>::i
             const sd_tokens &tk = hd[now.h & 1].tk;
             const E *tY = tYs[xbuf];
             const parts_t &tD = tDs[dbuf];
-            const formed<E, kSdParts> S[4] = {formed<E, kSdParts>(rS[0]), formed<E, kSdParts>(rS[1]), formed<E, kSdParts>(rS[2]), formed<E, kSdParts>(rS[3])};
+            const formed<E> S[4] = {formed<E>(rS[0]), formed<E>(rS[1]), formed<E>(rS[2]), formed<E>(rS[3])};
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
                 op32<E> d = col32<E, 64>(tD[0], 32 * k, 16 * w, lane);
@@ -538,7 +536,7 @@ sd_bwd_kernel(const typename sd<E>::io *__restrict__ u_, const typename sd<E>::i
                             if (c16 == 0) hn.R[w][t + e] = ONE || now.pt == 0 ? r : hn.R[w][t + e] + r;
                         }
                     }
-                    const formed<E, kSdParts> g0(gk[0]), g1(gk[1]);
+                    const formed<E> g0(gk[0]), g1(gk[1]);
                     F y0[2], y1[2];
                     f32x4_t add[2] = {};
 #pragma unroll
@@ -582,7 +580,7 @@ sd_bwd_kernel(const typename sd<E>::io *__restrict__ u_, const typename sd<E>::i
         __syncthreads();
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-            const formed<E, kSdParts> f(Z[j]);
+            const formed<E> f(Z[j]);
 #pragma unroll
             for (int m = 0; m < NP; ++m)
 #pragma unroll

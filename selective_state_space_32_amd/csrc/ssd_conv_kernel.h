@@ -19,6 +19,7 @@ constexpr int kSdQ = 64;           // tokens per chunk
 constexpr int kSdThreads = 256;    // four waves; wave w owns the 16 channels 16 w .. of a 64-channel tile
 constexpr int kSdTaps = 4;         // taps of the convolution at most
 constexpr int kSdConvV = 4;        // channels per thread of the convolution's kernels
+constexpr int kSdParts = 3;        // bf16 parts of an operand that is formed in fp32
 
 // ---- operands of the matrix products --------------------------------------------------------
 //
@@ -27,8 +28,9 @@ constexpr int kSdConvV = 4;        // channels per thread of the convolution's k
 // accumulator (rows 4 (l / 16) + e, column l % 16), so an accumulator is a fragment of the product
 // that contracts over its rows without leaving its registers.  bf16: two fragments make one operand of
 // v_mfma_f32_16x16x32_bf16 (both operands order k alike); fp32: a fragment feeds four
-// v_mfma_f32_16x16x4_f32.  Operands that are formed in fp32 are split into NS bf16 parts of 8 bits each:
-// two where the result leaves in bf16 (2^-17 of a value is lost), three where it is carried in fp32.
+// v_mfma_f32_16x16x4_f32.  Operands that are formed in fp32 are split into three bf16 parts of 8 bits each, which hold
+// fp32's 24.  (Two, 16 bits, took 263 us in place of 282 for prompts of B8 L2048 H80 N64 and 766 in place of 826 for B1 L65536
+// H32 N128, but moved one output in 600 to the other side of a border between two bf16 values, 1.1e-4 of their root mean square.)
 typedef __bf16 sd_bf16x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 sd_bf16x8 __attribute__((ext_vector_type(8)));
 typedef short sd_i16x4 __attribute__((ext_vector_type(4)));
@@ -81,9 +83,9 @@ __device__ __forceinline__ f32x4_t mma(f32x4_t a0, f32x4_t a1, f32x4_t b0, f32x4
     for (int e = 0; e < 4; ++e) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a1[e], b1[e], c, 0, 0, 0);
     return c;
 }
-// A fragment formed in fp32, in NS parts (one with fp32 operands).
-template <typename E, int NS> struct formed {
-    static constexpr int N = sd<E>::split ? NS : 1;
+// A fragment formed in fp32, in parts (one with fp32 operands).
+template <typename E> struct formed {
+    static constexpr int N = sd<E>::split ? kSdParts : 1;
     typename sd<E>::frag p[N];
     __device__ __forceinline__ formed() {}
     __device__ __forceinline__ explicit formed(f32x4_t v) {
@@ -537,6 +539,17 @@ sd_combine_kernel(const float *__restrict__ tok, const float *__restrict__ first
     }
 }
 
+// M in LDS: 64 x 64 without the quarter of t < 32 <= s, which is zero and not read.  32 rows of 32, then 32 of 64 columns.
+template <typename E> struct pairs_tile {
+    static constexpr int size = 32 * (sd_ld<E>(32) + sd_ld<E>(64));
+    __device__ __forceinline__ static int at(int t, bool low) {   // low: t >= 32
+        return low ? 32 * sd_ld<E>(32) + (t - 32) * sd_ld<E>(64) : t * sd_ld<E>(32);
+    }
+    __device__ __forceinline__ static op32<E> row32(const E *m, int j, int k0, int lane) {   // rows of block j
+        return j >= 2 ? ssm::row32<E, 64>(m + 32 * sd_ld<E>(32), 16 * j - 32, k0, lane) : ssm::row32<E, 32>(m, 16 * j, k0, lane);
+    }
+};
+
 // One workgroup per (sequence, head, 64-channel tile, segment): the segment's chunks in order, the state in
 // accumulators.  from: the segments' first states [b][h][segment][P][N], or null (zero); last: [b][h][P][N].  ckpt:
 // [b][h][chunk][P][N], receives the state entering each chunk, or null.
@@ -557,7 +570,7 @@ sd_scan_kernel(const typename sd<E>::io *__restrict__ u_, const float *__restric
     constexpr int NB = NT / 16;
     const int N = FULL ? NT : s.N;
     __shared__ __attribute__((aligned(16))) E tB[64 * sd_ld<E>(NT)], tC[64 * sd_ld<E>(NT)], tX[64 * sd_ld<E>(64)];
-    __shared__ __attribute__((aligned(16))) E tM[(sd<E>::split ? 2 : 1)][64 * sd_ld<E>(64)];
+    __shared__ __attribute__((aligned(16))) E tM[formed<E>::N][pairs_tile<E>::size];
     __shared__ sd_tokens tk;
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int c16 = lane & 15, q4 = 4 * (lane >> 4);
@@ -602,7 +615,7 @@ sd_scan_kernel(const typename sd<E>::io *__restrict__ u_, const float *__restric
         f32x4_t Y[4] = {}, Gt[4] = {};
 #pragma unroll
         for (int k = 0; k < NB; k += 2) {
-            const formed<E, 2> s0(S[k]), s1(S[k + 1]);
+            const formed<E> s0(S[k]), s1(S[k + 1]);
             const F b0 = ld_row<E, NT>(tB, 16 * w, 16 * k, lane), b1 = ld_row<E, NT>(tB, 16 * w, 16 * k + 16, lane);
             F c0[4], c1[4];
 #pragma unroll
@@ -611,7 +624,7 @@ sd_scan_kernel(const typename sd<E>::io *__restrict__ u_, const float *__restric
                 c1[j] = ld_row<E, NT>(tC, 16 * j, 16 * k + 16, lane);
             }
 #pragma unroll
-            for (int m = 0; m < formed<E, 2>::N; ++m)
+            for (int m = 0; m < formed<E>::N; ++m)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) Y[j] = mma(s0.p[m], s1.p[m], c0[j], c1[j], Y[j]);
 #pragma unroll
@@ -643,9 +656,9 @@ sd_scan_kernel(const typename sd<E>::io *__restrict__ u_, const float *__restric
                     }
                 }
                 if (j < (w & ~1)) continue;   // (the products read pairs of 16 tokens s up to t's)
-                const formed<E, 2> f(m);
+                const formed<E> f(m);
 #pragma unroll
-                for (int i = 0; i < formed<E, 2>::N; ++i) *reinterpret_cast<F *>(&tM[i][t * sd_ld<E>(64) + s0]) = f.p[i];
+                for (int i = 0; i < formed<E>::N; ++i) *reinterpret_cast<F *>(&tM[i][pairs_tile<E>::at(t, j >= 2) + s0]) = f.p[i];
             }
         }
         // the state leaving the chunk
@@ -655,14 +668,14 @@ sd_scan_kernel(const typename sd<E>::io *__restrict__ u_, const float *__restric
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const float *wt = tk.w + 32 * i + 2 * q4;
-            const formed<E, 3> x0(widen(xf[i].lo) * ld4(wt)), x1(widen(xf[i].hi) * ld4(wt + 4));
+            const formed<E> x0(widen(xf[i].lo) * ld4(wt)), x1(widen(xf[i].hi) * ld4(wt + 4));
 #pragma unroll
             for (int n0 = 0; n0 < NB; n0 += 4) {
                 op32<E> bv[4];
 #pragma unroll
                 for (int nb = 0; nb < 4; ++nb) bv[nb] = col32<E, NT>(tB, 32 * i, 16 * (n0 + nb), lane);
 #pragma unroll
-                for (int m = 0; m < formed<E, 3>::N; ++m)
+                for (int m = 0; m < formed<E>::N; ++m)
 #pragma unroll
                     for (int nb = 0; nb < 4; ++nb) S[n0 + nb] = mma(bv[nb].lo, bv[nb].hi, x0.p[m], x1.p[m], S[n0 + nb]);
             }
@@ -673,9 +686,9 @@ sd_scan_kernel(const typename sd<E>::io *__restrict__ u_, const float *__restric
 #pragma unroll
         for (int i = 0; i < 2; ++i)
 #pragma unroll
-            for (int m = 0; m < formed<E, 2>::N; ++m)
+            for (int m = 0; m < formed<E>::N; ++m)
 #pragma unroll
-                for (int j = 2 * i; j < 4; ++j) Y[j] = mma(xf[i], row32<E, 64>(tM[m], 16 * j, 32 * i, lane), Y[j]);
+                for (int j = 2 * i; j < 4; ++j) Y[j] = mma(xf[i], pairs_tile<E>::row32(tM[m], j, 32 * i, lane), Y[j]);
         const int rows = (int)min((int64_t)64, len - t0);
         char *yc = reinterpret_cast<char *>(yb + t0 * s.H * s.P);
         const uint32_t yrow = (uint32_t)(s.H * s.P) * (uint32_t)sizeof(IO), yoff = (uint32_t)c16 * yrow + (uint32_t)(16 * w + q4) * (uint32_t)sizeof(IO);
