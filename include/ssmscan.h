@@ -560,7 +560,7 @@ SSMSCAN_API size_t ssm_layernorm_bwd_workspace_bytes(const ssm_dims *dims);
 /* Sizes of the state space dual layer with its convolution (ssm_ssd_conv_*). */
 typedef struct ssm_ssd_conv_dims {
     int64_t batch;      /* sequences */
-    int64_t seqlen;     /* tokens per sequence (ignored by ssm_ssd_conv_step) */
+    int64_t seqlen;     /* tokens per sequence (ssm_ssd_conv_step takes one, whatever valid number is here) */
     int64_t nheads;     /* heads H */
     int64_t headdim;    /* channels per head P: a multiple of 8 */
     int64_t ngroups;    /* groups G of B and C; H % G == 0 */
