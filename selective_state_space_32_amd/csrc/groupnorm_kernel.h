@@ -211,9 +211,9 @@ groupnorm_bwd_kernel(const IO *__restrict__ dy, const IO *__restrict__ x, const 
     if (at.row < s.M) fetch(at.row);
     int turn = 0;
     for (int64_t row = at.row; row < s.M; row += at.step, turn ^= 1) {
-        // The row is held as it was read and its elements are formed twice, before and after the sums (the empty asm keeps
-        // the compiler from holding the first ones): with what is formed in registers a SIMD has two waves in place of
-        // four to hide the reads (16384x5120 bf16, 8 groups, gate first: 262 us that way, 223 this way).
+        // The row is held as it was read and its elements are formed twice, before and after the sums.  (That the compiler
+        // may hold the first ones instead, as far as the waves that are asked for leave registers, costs nothing: with an
+        // empty asm against it 16384x5120 bf16 of 8 groups takes 195 us gate first, 194 without, 197 and 181 gate after.)
         vec_t nx[NV], nz[NV], ng[NV];
         const float m_now = m, rs_now = rs;
         float p = 0.0f, q = 0.0f;
@@ -223,11 +223,6 @@ groupnorm_bwd_kernel(const IO *__restrict__ dy, const IO *__restrict__ x, const 
             nx[j] = rx[j];
             ng[j] = rg[j];
             if (kGated) nz[j] = rz[j];
-#pragma unroll
-            for (int i = 0; i < vec_t::W; ++i) {
-                asm volatile("" : "+v"(nx[j].w[i]), "+v"(ng[j].w[i]));
-                if (kGated) asm volatile("" : "+v"(nz[j].w[i]));
-            }
             float za[kNormVec];
 #pragma unroll
             for (int k = 0; k < kNormVec; ++k) {
