@@ -52,8 +52,8 @@ int launched() {
 int group_threads(int64_t D) { return D <= 32 ? 8 : D <= 64 ? 16 : D <= 128 ? 32 : D <= 1024 ? 64 : D <= 5120 ? 256 : 512; }
 
 // Workgroups, at most: they take several rows each, so that the weights they hold are worth it; as many as the chip
-// holds at once, or nearly (16384x5120 bf16, 8 groups, gate first: forward 120 us with 1024, 102 with 1536, 109 with
-// 4096; backward 242 with 768, 223 with 1024, which fit where a thread holds up to three vectors).
+// holds at once, or nearly (16384x5120 bf16, 8 groups, gate first: forward 115 us with 1024, 102 with 1536, 111 with
+// 4096; backward 286 with 512, 218 with 768, 192 with 1024, which fit where a thread holds up to three vectors).
 constexpr int64_t kFwdGroups = 1536;
 int64_t bwd_groups(int64_t D) { return D <= 768 || (D > 1024 && D <= 2048) ? 1024 : 512; }
 

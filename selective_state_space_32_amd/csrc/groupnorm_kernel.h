@@ -10,10 +10,10 @@
 // of TPG threads, NV vectors of kNormVec each: 8 lanes for groups of 32, a wave for up to 1024, a workgroup
 // beyond.  A thread keeps its columns over all the rows that its workgroup takes, so that the weights stay
 // in registers, and so do the sums over rows behind dw and db.  Groups wider than the registers hold are
-// passed over several times.  The activation is the kernel's, not the launch's: tests of it in the loops cost
-// 16384x5120 bf16 of 8 groups, gate first, 8 us of 128, its backward 40 of 302.
-// Measured: that case 102 - 110 us (503 MB, 4.6 - 4.9 TB/s), backward 223 + 5 us (839 MB, 3.8 TB/s); 4096x1536 fp32 of
-// groups of 64, gate after, 14.6 and 23 + 4 us; 256x5120 bf16, one group, 6.0 us.
+// passed over several times.  The activation is the kernel's, not the launch's: when it became so, 16384x5120 bf16 of 8
+// groups, gate first, went from 128 to 120 us, its backward from 302 to 262.
+// Measured: that case 102 us (503 MB, 4.9 TB/s), backward 191 + 5 us (839 MB, 4.3 TB/s); 4096x1536 fp32 of
+// groups of 64, gate after, 14.4 and 23 + 4 us; 256x5120 bf16, one group, 6.0 us.
 #pragma once
 
 #include "layernorm_kernel.h"

@@ -61,8 +61,9 @@ int launched() {
 
 // Segments of a sequence, which run beside each other: a pass over the state alone finds what each of them starts
 // from.  One, unless the sequences' heads leave most of the workgroups that fit on the chip without work; at least two
-// chunks each.  (All passes, B1 L65536 H32 N128: 550 us, 4,036 as one segment; B5 L777 H20 N128: 45 and 63; B1 L512 H24
-// N64: 20 and 29.  768 to 1,536 in place of 512 changed little: 555 to 630 for the first, 69 for 67 of B2 L2048 H24 fp32.)
+// chunks each.  (All passes, B1 L65536 H32 N128: 567 us, 4,658 as one segment; B5 L777 H20 N128: 47 and 70; B1 L512 H24
+// N64: 21 and 32; B2 L2048 H24 fp32: 68 and 197.  768 to 1,536 in place of 512 are no better: 583 to 633 for the first, 65
+// to 66 for the last.)
 constexpr int64_t kSegTarget = 512;
 int64_t segments(const ssm_ssd_conv_dims *dm) {
     const int64_t items = dm->batch * dm->nheads * p_tiles(dm), most = std::max<int64_t>(chunks(dm) / 2, 1);
@@ -100,8 +101,8 @@ size_t seg_bytes(const ssm_ssd_conv_dims *dm) {
 }
 
 // Tokens per thread of the convolution: 32 (a thread reads three rows more than it has), 8 where that leaves CUs
-// with less than four waves per SIMD (B8 L2048 of 5,248 channels bf16: 113 us, 138 with 8; B1 L512 of 1,664: 7.8 us with
-// 8, 17.8 with 32; B5 L777 of 2,304: 19 and 32).
+// with less than four waves per SIMD (B8 L2048 of 5,248 channels bf16: 96 us, 127 with 8; B1 L512 of 1,664: 8.2 us with
+// 8, 17.7 with 32; B5 L777 of 2,304: 20 and 28; B2 L2048 of 1,664 fp32: 16.6 and 14.8).
 int conv_tokens(const ssm_ssd_conv_dims *dm) {
     return dm->batch * dm->seqlen * (row_of(dm) / ssm::kSdConvV) >= (int64_t)32 * 64 * 4096 ? 32 : 8;
 }
@@ -203,7 +204,7 @@ void launch_step(float *state, const void *u, const void *dt, const float *A, co
                  const ssm_ssd_conv_dims *dm, int flags, hipStream_t st) {
     const ssm::sd_shape s = shape_of(dm, flags);
     // Lanes per channel; two channels of a thread at a time, and a head's channels in several workgroups where there
-    // are few heads (one sequence of 32 heads P64 N128: 3.9 us, 6.5 with one workgroup a head)
+    // are few heads (one sequence of 32 heads P64 N128: 3.9 us, 6.6 with one workgroup a head)
     const int lanes = s.N / 4, lpr = lanes <= 2 ? 2 : lanes <= 4 ? 4 : lanes <= 8 ? 8 : lanes <= 16 ? 16 : 32;
     const int64_t heads = dm->batch * s.H, most = ceil_div(s.P, 2 * (256 / lpr));
     const int parts = (int)std::min<int64_t>(most, std::max<int64_t>(2048 / heads, 1));
@@ -226,8 +227,8 @@ void launch_conv_step(const void *x_, const float *w, const float *bias, void *s
 
 // How the backward cuts its work, and its workspace.
 // Tokens per thread of the convolution's backward: 64 (a thread goes three tokens further than its own), 16 where
-// that leaves CUs with less than four waves per SIMD (B5 L777 of 2,304 channels bf16: 19.8 us with 16, 33 with 64; B2
-// L2048 of 1,664 fp32: 19.3 and 37.7).
+// that leaves CUs with less than four waves per SIMD (B5 L777 of 2,304 channels bf16: 20 us with 16, 33 with 64; B2
+// L2048 of 1,664 fp32: 20 and 40; B8 L2048 of 5,248 bf16: 163 and 149).
 int conv_bwd_tokens(const ssm_ssd_conv_dims *dm) {
     return dm->batch * dm->seqlen * (row_of(dm) / ssm::kSdConvV) >= (int64_t)64 * 64 * 4096 ? 64 : 16;
 }
@@ -240,8 +241,9 @@ BwdPlan bwd_plan(const ssm_ssd_conv_dims *dm, bool have_checkpoints) {
     BwdPlan p;
     const int64_t per = dm->nheads / dm->ngroups, items = std::max<int64_t>(dm->batch * chunks(dm) * dm->ngroups, 1);
     // Parts of a group's heads: what takes the fewest rounds of a workgroup per CU, a workgroup's start and end
-    // counted as kStart heads (and its part of dB and dC written and read again).  B5 L777 G4 of five heads each: 125 us
-    // in one part, 144 + 15 in five, as 0 would have it (106 in one part since); 8 chose the same there.
+    // counted as kStart heads (and its part of dB and dC written and read again).  B5 L777 G4 of five heads each: 103 us
+    // in one part, 130 + 15 in five, as 0 would have it; 8 chooses as 3 does there.  (B8 L2048 H80 and B2 L2048 H24 take the
+    // same time with 0, 3 and 8.)
     constexpr int64_t kCUs = 256, kStart = 3;
     int64_t best = -1;
     for (int64_t parts = 1; parts <= per; ++parts) {

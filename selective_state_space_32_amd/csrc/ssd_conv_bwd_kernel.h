@@ -24,8 +24,8 @@ namespace ssm {
 // 64-channel tile, segment).  each: [b][h][chunk][P][N], or null.  from: [b][h][segment][P][N], or null (zero).  to: with
 // `ends` [b][h][segment][P][N], what every segment leaves, else [b][h][P][N], what the last (ADJ: first) one leaves, or null.
 // FULL as in sd_scan_kernel.
-// Bound: HBM where every chunk's state is written (B8 L2048 H80 N64 bf16, adjoints: 157 us, 506 MB, 3.2 TB/s), the chunks'
-// chain otherwise (B1 L65536 H32 N128, 16 segments: 155 us).
+// Bound: HBM where every chunk's state is written (B8 L2048 H80 N64 bf16, adjoints: 158 us, 506 MB, 3.2 TB/s), the chunks'
+// chain otherwise (B1 L65536 H32 N128, 16 segments: 144 us).
 template <typename E, int NT, bool ADJ, bool FULL>
 __global__ void __launch_bounds__(kSdThreads)
 sd_walk_kernel(const typename sd<E>::io *__restrict__ u_, const typename sd<E>::io *__restrict__ dy_,
@@ -166,13 +166,14 @@ struct sd_grad {
 // 16 from 16 w of dC, kind 1 those of dB; kinds 2 and 3 (z = 0, 1) the 16 tokens 16 w .. of the chunk as s of T, G and v, of
 // these the tokens t in blocks z and 3 - z of T and the channels 32 z .. of every 64 of v.
 // MODE 1: whole tiles (P a multiple of 64, N = NT), without the checks for less; 2: and one item per head (P = N = 64).
-// (B5 L777 H20 N128 bf16: 125 us, 154 without MODE, since then 106; B2 L2048 H24 N64 fp32: 70, 79.)
+// (MODE 2, 1 and 0: B8 L2048 H80 N64 bf16 347, 415 and 847 us, B2 L2048 H24 N64 fp32 68, 68 and 78; 1 and 0: B5 L777 H20
+// N128 bf16 103 and 123.)
 // The pairs of tokens are worked on once a head's 64 channels have their last states, 32 tokens t at a time: G, K, T and
-// what comes of them then live for a few products only (492 us for B8 L2048 H80 N64 with G K of all tokens held over a
-// head, 351 - 370 this way).  Waves of kinds in loops of their own took less than eight waves of every kind's work (559) and
-// four (683): a kind's accumulators stay in 128 registers.
-// Bound: HBM, 1.5 GB in 349 us there (4.3 TB/s; each chunk's states and adjoints are 45 % of it), with vector
-// instructions busy 52 % and LDS 36 % of the time beside it.
+// what comes of them then live for a few products only (351 us for B8 L2048 H80 N64 when this came, 492 with G K of all
+// tokens held over a head).  Waves of kinds in loops of their own were taken as quicker than eight waves of every kind's work
+// (559 there, before that) and four (683): a kind's accumulators stay in 128 registers.
+// Bound: HBM, 1.5 GB in 347 us there (4.3 TB/s; each chunk's states and adjoints are 45 % of it), with vector
+// instructions busy 56 % and LDS 39 % of the time beside it.
 template <typename E, int NT, int MODE>
 __global__ void __launch_bounds__(kSdBwdThreads) __attribute__((amdgpu_waves_per_eu(4)))
 sd_bwd_kernel(const typename sd<E>::io *__restrict__ u_, const typename sd<E>::io *__restrict__ dy_,
@@ -364,7 +365,7 @@ sd_bwd_kernel(const typename sd<E>::io *__restrict__ u_, const typename sd<E>::i
     };
     if (kind == 0) {   // through the state entering: dC^T[n][t]
         // (two blocks of tokens at a time where both halves' accumulators are held: with four they spill, B5 L777 H20 N128
-        // 126 us for 106; with two at N <= 64 the B8 case takes 529)
+        // 117 us for 103; with two at N <= 64 the B8 case takes 509 for 347, B2 L2048 H24 fp32 65 for 68)
         constexpr int kTogether = NH == 1 ? 4 : 2;
         f32x4_t acc[NH][4] = {};
         float dot = 0.0f, ys[4] = {};
@@ -603,9 +604,9 @@ static __global__ void __launch_bounds__(256) sd_parts_kernel(float *dbc, int64_
 // Back through silu and the convolution; thread: kSdConvV channels of `tt` tokens, kSdConvT at a time, the next ones'
 // rows requested before.  With g_t = du_t silu'(pre_t):
 //   dx_t = sum_j w[j] g_{t+3-j},   dw[j] = sum g_t x_{t-3+j},   db = sum g_t         (w[j]: four taps, oldest first)
-// so a thread forms g for three tokens past its own.  W4 as in sd_conv_kernel (a tap that is not there takes no g either).  Bound: HBM (B8 L2048 of 5,248 channels bf16: 148 us, 688 MB, 4.6 TB/s;
-// B2 L2048 of 1,664 fp32 20 us).  parts: [b * tile][5][dc] sums over the tile's tokens of dw's four
-// taps and of db.
+// so a thread forms g for three tokens past its own.  W4 as in sd_conv_kernel (a tap that is not there takes no g
+// either).  Bound: HBM (B8 L2048 of 5,248 channels bf16: 149 us, 688 MB, 4.6 TB/s; B2 L2048 of 1,664 fp32 20 us).
+// parts: [b * tile][5][dc] sums over the tile's tokens of dw's four taps and of db.
 template <typename IO, bool AL, bool W4>
 __global__ void __launch_bounds__(256)
 sd_conv_bwd_kernel(const IO *__restrict__ x, int64_t xstride, const float *__restrict__ w, const float *__restrict__ bias,

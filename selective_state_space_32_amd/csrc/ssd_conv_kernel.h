@@ -30,7 +30,7 @@ constexpr int kSdParts = 3;        // bf16 parts of an operand that is formed in
 // v_mfma_f32_16x16x32_bf16 (both operands order k alike); fp32: a fragment feeds four
 // v_mfma_f32_16x16x4_f32.  Operands that are formed in fp32 are split into three bf16 parts of 8 bits each, which hold
 // fp32's 24.  (Two, 16 bits, took 263 us in place of 282 for prompts of B8 L2048 H80 N64 and 766 in place of 826 for B1 L65536
-// H32 N128, but moved one output in 600 to the other side of a border between two bf16 values, 1.1e-4 of their root mean square.)
+// H32 N128, but left bf16 outputs 1.1e-4 of their root mean square from the roundings of fp32's; now 1.1e-5 to 2.7e-5.)
 typedef __bf16 sd_bf16x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 sd_bf16x8 __attribute__((ext_vector_type(8)));
 typedef short sd_i16x4 __attribute__((ext_vector_type(4)));
@@ -325,7 +325,7 @@ __device__ __forceinline__ void conv_token(const float (&w)[kSdTaps][kSdConvV], 
     if constexpr (sizeof(IO) == 2)
         if (near[0] || near[1] || near[2] || near[3]) {
 #pragma unroll 1
-            for (int e = 0; e < kSdConvV; ++e)   // (unrolled it took registers from the rest: B1 L65536 of 4096 channels 280 us for 265)
+            for (int e = 0; e < kSdConvV; ++e)   // (unrolled it takes registers from the rest: B1 L65536 of 4096 channels 263 us for 246, B8 L2048 of 5,248 103 for 96)
                 if (near[e]) {
                     double q = fma((double)w[0][e], (double)x0[e], (double)b[e]);
                     q = fma((double)w[1][e], (double)x1[e], q);
@@ -350,9 +350,9 @@ struct sd_tok_args {
 // from st_in (zero without it).  The thread of the first tokens also writes the W - 1 rows before token len
 // (st_out may be st_in: nothing else reads it, as tt >= 3).  W4: four taps; fewer count as zeros in front, of rows that count
 // as zeros too (what lies in a row that the convolution does not reach, an infinity times no weight, is not its).
-// Bound: vector instructions in bf16, of which the exact rounding is a third, then HBM: B8 L2048 of 5,248 channels bf16
-// 95 - 113 us (344 MB, 3.0 - 3.6 TB/s; 83 without the rounding's test), B1 L65536 of 4,096 249 - 263 us (1.07 GB, 4.1 - 4.3 TB/s; 203);
-// B2 L2048 of 1,664 fp32 12.5 us.  Workgroups behind the convolution's write the tokens' decays, as the work of a launch of
+// Bound: vector instructions in bf16 (a sixth of the time is the exact rounding's), then HBM: B8 L2048 of 5,248 channels bf16
+// 95 us (344 MB, 3.6 TB/s; 80 without the exact rounding), B1 L65536 of 4,096 246 us (1.07 GB, 4.4 TB/s; 203);
+// B2 L2048 of 1,664 fp32 16.5 us.  Workgroups behind the convolution's write the tokens' decays, as the work of a launch of
 // their own is small.
 constexpr int kSdConvT = 4;
 template <typename IO, bool AL, bool W4>
@@ -553,12 +553,13 @@ template <typename E> struct pairs_tile {
 // One workgroup per (sequence, head, 64-channel tile, segment): the segment's chunks in order, the state in
 // accumulators.  from: the segments' first states [b][h][segment][P][N], or null (zero); last: [b][h][P][N].  ckpt:
 // [b][h][chunk][P][N], receives the state entering each chunk, or null.
-// FULL: whole tiles (P a multiple of 64, N = NT), without the checks for less (B8 L2048 H80 N64: 195 us, 207 with them).
+// FULL: whole tiles (P a multiple of 64, N = NT), without the checks for less (B8 L2048 H80 N64: 192 us, 200 with them; B1
+// L65536 H32 N128 402 and 417; no difference where the chunks' states are written).
 // The state stays in accumulators, so HBM sees rows and y only (rows through L2 where heads share B and C).  Bound: the
-// chain of a chunk's products: the waves wait half of the time (two barriers a chunk), while vector instructions and LDS
-// are busy 40 % of it each; B8 L2048 H80 N64 bf16 169 us (rows and y, 340 MB, 2.0 TB/s; reads of C without their bank
-// conflicts took LDS to 33 % and changed nothing), with the chunks' states written 246; B1 L65536 H32 N128 in 16
-// segments 354 - 370; B2 L2048 H24 fp32 46.  Three waves a SIMD (N <= 64, bf16) is what LDS allows.
+// chain of a chunk's products: the waves wait half of the time (two barriers a chunk), while vector instructions are busy
+// 38 % of it and LDS 34 %; B8 L2048 H80 N64 bf16 186 us (rows and y, 340 MB, 1.8 TB/s; reads of C without their bank
+// conflicts relieved LDS and changed nothing), with the chunks' states written 253; B1 L65536 H32 N128 in 16
+// segments 404; B2 L2048 H24 fp32 45.  Three waves a SIMD (N <= 64, bf16) is what LDS allows.
 template <typename E, int NT, bool FULL>
 __global__ void __launch_bounds__(kSdThreads)
 __attribute__((amdgpu_waves_per_eu(sd<E>::split && NT == 64 ? 3 : 2)))
@@ -726,7 +727,7 @@ sd_scan_kernel(const typename sd<E>::io *__restrict__ u_, const float *__restric
 // ---- one token ------------------------------------------------------------------------------
 
 // The convolution of one token a sequence, its rows advanced in place; thread: kSdConvV channels of a sequence.
-// Bound: its reads' latency (256 sequences of 5,248 channels bf16: 10.6 us, 13.4 MB; one of 4,096: 3.0 us).  The prompt's
+// Bound: its reads' latency (256 sequences of 5,248 channels bf16: 10.6 us, 13.4 MB; one of 4,096: 3.1 us).  The prompt's
 // kernel took 24 us: a thread of it reads past tokens and writes the rows after its own work.
 template <typename IO, bool AL>
 __global__ void __launch_bounds__(256)
@@ -756,8 +757,8 @@ sd_conv_step_kernel(const IO *__restrict__ x, int64_t xstride, const float *__re
 }
 
 // One workgroup per (sequence, head, part of its channels): LPR lanes hold a channel's N states, four each; U channels
-// at a time.  Bound: HBM, the state read and written once (256 sequences of 80 heads P64 N64: 671 MB in 119 us, 5.6 TB/s;
-// one of 32 heads N128: 3.9 us, 6.5 with one workgroup a head).
+// at a time.  Bound: HBM, the state read and written once (256 sequences of 80 heads P64 N64: 671 MB in 127 us, 5.3 TB/s;
+// one of 32 heads N128: 3.9 us, 6.6 with one workgroup a head).
 template <typename IO, int LPR, int U>
 __global__ void __launch_bounds__(256)
 sd_step_kernel(float *__restrict__ state, const IO *__restrict__ u, const IO *__restrict__ dt, int64_t dt_stride,

@@ -1133,8 +1133,8 @@ def ssd_conv_fwd(xbc: torch.Tensor, conv_w: torch.Tensor, conv_b: Optional[torch
     """The state space dual layer with its causal convolution (ssm_ssd_conv_fwd), over whole sequences.
 
     xbc: (batch, L, H P + 2 G N) float32 or bfloat16, the projected x, B and C; dt: (batch, L, H) of the same
-    dtype; both may be parts of a wider projected row, not one row broadcast over an axis.  conv_w: (row, width), conv_b: (row,), A, D, dt_bias:
-    (H,) float32; dstate N and ngroups G.  conv_state: (batch, width-1, row), the rows before token 0; initial_state:
+    dtype; both may be parts of a wider projected row, not one row broadcast over an axis.  conv_w: (row,
+    width), conv_b: (row,), A, D, dt_bias: (H,) float32; dstate N and ngroups G.  conv_state: (batch, width-1, row), the rows before token 0; initial_state:
     (batch, H, P, N) float32; seq_lens: (batch,) int32 on the device, sequence b then has seq_lens[b] tokens and y
     is zero past them.  last_state may be initial_state and conv_state_out conv_state (advanced in place).
     Returns (y (batch, L, H, P), last_state, conv_state_out) -- the states None if neither given nor
