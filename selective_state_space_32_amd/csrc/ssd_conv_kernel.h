@@ -795,18 +795,24 @@ sd_step_kernel(float *__restrict__ state, const IO *__restrict__ u, const IO *__
         }
         // a S + in = S + ((a - 1) S + in): a decay near 1 would lose by its rounding what a slow head remembers by
         // (60,000 tokens at a memory of 20,000, the same step size every token: the state off by 1.4e-3 of its rms
-        // that way).  Below 1/2 the sum with S would lose more than a does.
-        const float d = softplus ? softplus_f32(v) : v, am1 = expm1f(ah * d);
-        const bool slow = am1 > -0.5f;
-        const float a = slow ? am1 : expf(ah * d);
+        // that way).  Below 1/2 the sum with S would lose more than a does.  (An infinite S stays what it is: the product
+        // takes the largest finite value for it.)
+        const float d = softplus ? softplus_f32(v) : v, am1 = expm1f(ah * d), a = expf(ah * d);
+        const bool slow = __builtin_amdgcn_readfirstlane(am1 > -0.5f);   // (the same in all lanes)
 #pragma unroll
         for (int i = 0; i < U; ++i) {
             const int p = p0 + i * ROWS + row;
             if (p >= P) continue;   // (a channel's lanes together)
             float o = 0.0f;
             if (n < N) {
-                const f32x4_t t = st[i] * a + Bv * (d * x[i]);
-                st[i] = slow ? st[i] + t : t;
+                const f32x4_t in = Bv * (d * x[i]);
+                if (slow) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        st[i][e] += fmaf(__builtin_amdgcn_fmed3f(st[i][e], -__FLT_MAX__, __FLT_MAX__), am1, in[e]);
+                } else {
+                    st[i] = st[i] * a + in;
+                }
                 *reinterpret_cast<f32x4_t *>(sb + (int64_t)p * N + n) = st[i];
                 o = st[i][0] * Cv[0] + st[i][1] * Cv[1] + st[i][2] * Cv[2] + st[i][3] * Cv[3];
             }

@@ -115,3 +115,29 @@ def test_prompt_then_tokens(io):
         x, w, cb, raw, A, D, bias = c.args(t)
         ssmscan.ssd_conv_step(st, cs, x, w, cb, raw, A, D, bias, dstate=16)
     close(st[0], want, STATE, "state")
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+def test_states_that_are_not_finite(io):
+    """An infinite or NaN state stays so, beside states that keep their values, in heads that forget slowly, fast, and
+    not at all; tokens one by one and as a prompt."""
+    H, P, N = 4, 8, 16
+    c = Slow(2, 3, H, P, N, io, 0.5, True, seed=5)
+    c.A = torch.tensor([-1e-4, -0.5, -4.0, 0.0], device="cuda")
+    st = torch.randn(2, H, P, N, device="cuda", generator=torch.Generator(device="cuda").manual_seed(6))
+    clean = st.clone()
+    st[0, :, 2, 3], st[1, :, 5, 7], st[1, :, 0, 0] = float("inf"), -float("inf"), float("nan")
+    bad = ~torch.isfinite(st)
+    first = st.clone()
+
+    def steps(s):
+        cs = torch.zeros(2, 3, c.x.shape[2], dtype=IO[io], device="cuda")
+        for t in range(3):
+            x, w, cb, raw, A, D, bias = c.args(t)
+            ssmscan.ssd_conv_step(s, cs, x, w, cb, raw, A, D, bias, dstate=N)
+        return s
+    one, without = steps(st), steps(clean.clone())
+    assert torch.equal(torch.isnan(one), torch.isnan(first)) and torch.equal(one[torch.isinf(first)], first[torch.isinf(first)])
+    assert torch.equal(one[~bad], without[~bad])
+    last = ssmscan.ssd_conv_fwd(*c.args(), dstate=N, initial_state=first)[1]
+    assert torch.equal(torch.isnan(last), torch.isnan(first)) and torch.equal(last[torch.isinf(first)], first[torch.isinf(first)])
